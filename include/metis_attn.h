@@ -324,6 +324,113 @@ int metis_mla_reshape_and_cache(const void* kv_c, const void* k_pe, void* kv_cac
                                 int block_size, int num_blocks, void* stream);
 
 /*
+ * The 8-bit cache.  K and V pages may be held as e4m3 codes (four exponent bits,
+ * three of mantissa, no infinity, largest value 448) with one power-of-two scale
+ * per page and KV head:
+ *
+ *   k_cache, v_cache  uint8 [num_blocks, block_size, num_kv_heads, head_dim]: codes
+ *   k_scale, v_scale  uint8 [num_blocks, num_kv_heads]: bytes b, the scale being
+ *                     2^(b - 127) (any alignment; 255 stands for NaN and is never
+ *                     written)
+ *   element = value(code) * 2^(b - 127)
+ *
+ * The four calls below write such a cache, read it back and attend over it.  Page
+ * tables, lengths, streams, errors and the handling of bad contents are those of the
+ * calls above; head_dim 64 or 128, block_size 16, 32 or 64.
+ *
+ * metis_reshape_and_cache_fp8 -- quantise one step's new key/value rows into their
+ * pages, in front of the attention call (the counterpart of
+ * metis_reshape_and_cache, addressed like a prefill chunk because a page's scale
+ * depends on all of its rows).  Sequence s has seq_lens[s] cached tokens INCLUDING
+ * its q_len = cu_q_lens[s+1] - cu_q_lens[s] new ones, whose rows are
+ * key[cu_q_lens[s] ..]; they go to positions seq_lens[s] - q_len .. seq_lens[s] - 1.
+ * For each page that new rows fall into, and each KV head and cache:
+ *
+ *   e    = the smallest exponent with  max |x| <= 448 * 2^e  over the new rows of the
+ *          page (finite values only), at least -126
+ *   page begun by this call (its first slot is a new row):  scale = 2^e
+ *   page with earlier tokens of the sequence:  scale = the larger of 2^e and the
+ *          scale it has; when it grows, the earlier tokens' codes are rounded
+ *          again: code = e4m3(value(code) * old / new)
+ *   new row: code = e4m3(x / scale), round to nearest even; NaN and infinities
+ *          are stored as NaN
+ *
+ * Slots at or beyond seq_lens[s], other pages and their scales are left as they were.
+ *
+ *   key, value     [num_tokens, num_kv_heads, head_dim], dtype
+ *   cu_q_lens      int32 [num_seqs + 1], cu_q_lens[0] = 0, non-decreasing,
+ *                  cu_q_lens[num_seqs] <= num_tokens (rows behind it are not read)
+ *   block_table, seq_lens   as for metis_paged_attn_decode
+ *   dtype          METIS_F32 or METIS_BF16
+ * A page that new rows fall into must belong to one sequence of the call (a page
+ * shared by several may only be read); otherwise its contents are unspecified.
+ * A sequence with q_len < 0 or > seq_lens[s] (METIS_STATUS_BAD_Q_LEN), with rows
+ * outside [0, num_tokens) (METIS_STATUS_BAD_OFFSETS) or longer than its table row
+ * (METIS_STATUS_SEQ_TOO_LONG) is not written, and neither is a page whose id is
+ * outside the pool (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_tokens == 0
+ * is a successful no-op.
+ */
+int metis_reshape_and_cache_fp8(const void* key, const void* value, void* k_cache, void* v_cache,
+                                uint8_t* k_scale, uint8_t* v_scale, const int32_t* cu_q_lens,
+                                const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
+                                int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                int max_blocks, int num_blocks, int dtype, void* stream);
+
+/*
+ * metis_gather_cache_fp8 -- read cached tokens back: for every sequence s and
+ * t < seq_lens[s],
+ *   k_out[row_offsets[s] + t, :, :] = the K element values of token t, and v_out alike
+ * rounded once to out_dtype (a value is exact in bf16 and fp32 unless its scale puts
+ * it outside the type's range).  Rows that no token maps to are left as they were.
+ * With row_offsets[s] a multiple of block_size, k_out and v_out are at the same time
+ * pages [num_rows / block_size, block_size, num_kv_heads, head_dim] of a bf16 or
+ * fp32 cache (page row_offsets[s] / block_size + j holds page j of sequence s), which
+ * the calls above take.
+ *
+ *   row_offsets    int32 [num_seqs]
+ *   k_out, v_out   [num_rows, num_kv_heads, head_dim], out_dtype (written)
+ *   out_dtype      METIS_F32 or METIS_BF16
+ *   max_seq_len    host-side upper bound on seq_lens; tokens beyond it are not read
+ *                  (METIS_STATUS_SEQ_TOO_LONG)
+ * Sixteen tokens whose rows are not all inside [0, num_rows) are not written
+ * (METIS_STATUS_BAD_OFFSETS); a page whose id is outside the pool reads as zeros
+ * (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_rows == 0 is a successful no-op.
+ */
+int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                           const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* row_offsets, void* k_out, void* v_out, int num_seqs, int num_rows,
+                           int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks,
+                           int out_dtype, int max_seq_len, void* stream);
+
+/*
+ * metis_paged_attn_decode_fp8 -- metis_paged_attn_decode over an 8-bit cache.  q, out
+ * and lse_out, partition_size, max_seq_len and the workspace
+ * (metis_decode_workspace_bytes) are those of that call; dtype is the type of q and
+ * out, METIS_BF16 or METIS_F32.  num_heads / num_kv_heads may be any ratio up to 8.
+ * Products are fp16 tensor-core products of exact codes with fp32 accumulation; the
+ * softmax weights carry fp16's 11 bits (bf16 q), or 22 bits as q does (fp32 q).
+ */
+int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                                int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                int max_blocks, int num_blocks, int dtype, float scale, int partition_size,
+                                int max_seq_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * metis_paged_attn_prefill_chunk_fp8 -- metis_paged_attn_prefill_chunk over an 8-bit
+ * cache: the same arguments, workspace (metis_prefill_workspace_bytes) and
+ * limits, with the scales behind the codes.
+ */
+int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,
+                                       const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                                       const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                       float* lse_out, int num_seqs, int num_tokens, int num_heads,
+                                       int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                                       int num_blocks, int dtype, float scale, int max_seq_len,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Prefix cache: page keys and lookup-or-allocate.  A new prompt reuses the KV
  * pages of an earlier prompt with the same leading tokens (vllm-metis 0.1.0
  * page, "How the model maps onto vLLM", "Caches": vLLM's cache manager runs

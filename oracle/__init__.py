@@ -21,3 +21,4 @@ from .attention import (  # noqa: F401
 )
 from .cache_write import mla_reshape_and_cache, reshape_and_cache  # noqa: F401,E402
 from .prefix_cache import block_hashes, lookup_or_allocate, mix64  # noqa: F401,E402
+from .cache_fp8 import E4M3_VALUES, dequantize, encode_e4m3, quantize_pages, scale_byte, write_cache  # noqa: F401,E402

@@ -22,6 +22,7 @@ from ._binding import (  # noqa: F401
     MetisError,
     load_library,
     metis_decode_workspace_bytes,
+    metis_gather_cache_fp8,
     metis_last_error,
     metis_merge_attn_states,
     metis_mla_decode,
@@ -29,9 +30,11 @@ from ._binding import (  # noqa: F401
     metis_mla_workspace_bytes,
     NOALLOC_SCRATCH_BYTES,
     metis_paged_attn_decode,
+    metis_paged_attn_decode_fp8,
     metis_paged_attn_decode_noalloc,
     metis_paged_attn_decode_partials,
     metis_paged_attn_prefill_chunk,
+    metis_paged_attn_prefill_chunk_fp8,
     metis_prefill_workspace_bytes,
     metis_prefix_block_hashes,
     metis_prefix_lookup,
@@ -42,6 +45,7 @@ from ._binding import (  # noqa: F401
     metis_read_status,
     metis_debug_wait_probe,
     metis_reshape_and_cache,
+    metis_reshape_and_cache_fp8,
     metis_version,
 )
 from .pipeline import DecodePipeline  # noqa: F401,E402

@@ -77,6 +77,14 @@ SIGNATURES = {
     "metis_version": (_i, []),
     "metis_reshape_and_cache": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "metis_mla_reshape_and_cache": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "metis_reshape_and_cache_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                         _vp]),
+    "metis_gather_cache_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                    _vp]),
+    "metis_paged_attn_decode_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                         _f, _i, _i, _vp, _sz, _vp]),
+    "metis_paged_attn_prefill_chunk_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                                _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "metis_prefix_block_hashes": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "metis_prefix_table_init": (_i, [_vp, _vp, _vp, _i, _vp]),
     "metis_prefix_lookup_workspace_bytes": (_sz, [_i]),
@@ -410,6 +418,179 @@ def metis_mla_reshape_and_cache(kv_c: torch.Tensor, k_pe: torch.Tensor, kv_cache
         raise ValueError("inconsistent shapes")
     _check(lib.metis_mla_reshape_and_cache(_ptr(kv_c), _ptr(k_pe), _ptr(kv_cache), _ptr(slot_mapping), N, dl, dr,
                                            bs, nb, _stream(stream)))
+
+
+def _fp8_cache(device: torch.device, k_cache, v_cache, k_scale, v_scale):
+    """Check an 8-bit cache: codes (float8_e4m3fn or uint8) [nb, bs, G, D], scale bytes (uint8) [nb, G]."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda(name, t, ndim=4)
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.uint8 codes, got {t.dtype}")
+    _cuda("k_scale", k_scale, dtype=torch.uint8, ndim=2)
+    _cuda("v_scale", v_scale, dtype=torch.uint8, ndim=2)
+    nb, bs, G, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or tuple(k_scale.shape) != (nb, G) or v_scale.shape != k_scale.shape:
+        raise ValueError("inconsistent shapes: codes [num_blocks, block_size, num_kv_heads, head_dim], scales "
+                         "[num_blocks, num_kv_heads]")
+    _one_device(device, k_cache, v_cache, k_scale, v_scale)
+    return nb, bs, G, D
+
+
+def _one_device(device: torch.device, *tensors: Optional[torch.Tensor]):
+    """The library launches on the current device: refuse tensors that live elsewhere."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device} but the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on one device: got {t.device} and {device}")
+
+
+def metis_reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                k_scale: torch.Tensor, v_scale: torch.Tensor, cu_q_lens: torch.Tensor,
+                                block_table: torch.Tensor, seq_lens: torch.Tensor, stream=None) -> None:
+    """Quantise the new rows ``key`` / ``value`` ``[T, G, D]`` (bf16 or fp32) into an 8-bit
+    cache: sequence s's rows ``cu_q_lens[s] .. cu_q_lens[s + 1]`` are its last tokens, and
+    ``seq_lens`` counts them.  Codes and scales are updated in place, asynchronously."""
+    lib = load_library()
+    _cuda("key", key, ndim=3)
+    dt = _dtype_code(key.dtype)
+    _cuda("value", value, dtype=key.dtype, ndim=3)
+    nb, bs, G, D = _fp8_cache(key.device, k_cache, v_cache, k_scale, v_scale)
+    _cuda("cu_q_lens", cu_q_lens, dtype=torch.int32, ndim=1)
+    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
+    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
+    _one_device(key.device, value, cu_q_lens, block_table, seq_lens)
+    S = seq_lens.shape[0]
+    if (value.shape != key.shape or tuple(key.shape[1:]) != (G, D) or cu_q_lens.shape[0] != S + 1
+            or block_table.shape[0] != S):
+        raise ValueError("inconsistent shapes")
+    _check(lib.metis_reshape_and_cache_fp8(
+        _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_q_lens),
+        _ptr(block_table), _ptr(seq_lens), S, key.shape[0], G, D, bs, block_table.shape[1], nb, dt, _stream(stream)))
+
+
+def metis_gather_cache_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_table: torch.Tensor, seq_lens: torch.Tensor, row_offsets: torch.Tensor, *,
+                           num_rows: Optional[int] = None, k_out: Optional[torch.Tensor] = None,
+                           v_out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                           max_seq_len: Optional[int] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read an 8-bit cache back: token t of sequence s becomes row ``row_offsets[s] + t`` of
+    ``k_out`` / ``v_out`` ``[num_rows, G, D]`` (bf16 or fp32).  Pass the outputs, or
+    ``num_rows`` to have them allocated (rows that no token maps to then hold anything).
+    ``max_seq_len=None`` reads seq_lens (a sync)."""
+    lib = load_library()
+    _cuda("k_cache", k_cache)
+    dev = k_cache.device
+    nb, bs, G, D = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
+    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
+    _cuda("row_offsets", row_offsets, dtype=torch.int32, ndim=1)
+    S = seq_lens.shape[0]
+    if block_table.shape[0] != S or row_offsets.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("pass both of k_out and v_out, or neither")
+    if k_out is None:
+        if num_rows is None:
+            raise ValueError("num_rows is needed to allocate the outputs")
+        k_out = torch.empty((num_rows, G, D), dtype=out_dtype, device=dev)
+        v_out = torch.empty_like(k_out)
+    dt = _dtype_code(k_out.dtype)
+    _cuda("k_out", k_out, ndim=3)
+    _cuda("v_out", v_out, dtype=k_out.dtype, ndim=3)
+    if tuple(k_out.shape[1:]) != (G, D) or v_out.shape != k_out.shape or num_rows not in (None, k_out.shape[0]):
+        raise ValueError("k_out and v_out must be [num_rows, num_kv_heads, head_dim]")
+    _one_device(dev, block_table, seq_lens, row_offsets, k_out, v_out)
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    _check(lib.metis_gather_cache_fp8(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+        _ptr(row_offsets), _ptr(k_out), _ptr(v_out), S, k_out.shape[0], G, D, bs, block_table.shape[1], nb, dt,
+        int(max_seq_len), _stream(stream)))
+    return k_out, v_out
+
+
+def metis_paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                scale: float, *, out: Optional[torch.Tensor] = None,
+                                lse_out: Optional[torch.Tensor] = None, partition_size: int = 0,
+                                max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                                stream=None, want_lse: bool = False) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Paged decode over an 8-bit cache (``q`` bf16 or fp32); returns ``(out, lse_out)``.
+    ``max_seq_len=None`` reads seq_lens (a sync)."""
+    lib = load_library()
+    _cuda("q", q, ndim=3)
+    dt = _dtype_code(q.dtype)
+    dev = q.device
+    nb, bs, G, Dk = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
+    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
+    S, H, D = q.shape
+    if Dk != D or block_table.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda("out", out, dtype=q.dtype, ndim=3)
+    if lse_out is None and want_lse:
+        lse_out = torch.empty((S, H), dtype=torch.float32, device=dev)
+    if lse_out is not None:
+        _cuda("lse_out", lse_out, dtype=torch.float32, ndim=2)
+    if out.shape != q.shape or (lse_out is not None and tuple(lse_out.shape) != (S, H)):
+        raise ValueError("out must have q's shape and lse_out [num_seqs, num_heads]")
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    need = metis_decode_workspace_bytes(S, H, D, max_seq_len, partition_size)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _one_device(dev, block_table, seq_lens, out, lse_out, workspace)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib.metis_paged_attn_decode_fp8(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+        _ptr(out), _ptr(lse_out), S, H, G, D, bs, block_table.shape[1], nb, dt, float(scale), int(partition_size),
+        int(max_seq_len), _ptr(workspace), ws_bytes, _stream(stream)))
+    return out, lse_out
+
+
+def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: torch.Tensor,
+                                       v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                       block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float, *,
+                                       out: Optional[torch.Tensor] = None, lse_out: Optional[torch.Tensor] = None,
+                                       max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                                       stream=None, want_lse: bool = False):
+    """Chunked prefill (+ single-token decodes) over an 8-bit cache; returns ``(out, lse_out)``."""
+    lib = load_library()
+    _cuda("q", q, ndim=3)
+    dt = _dtype_code(q.dtype)
+    dev = q.device
+    _cuda("cu_q_lens", cu_q_lens, dtype=torch.int32, ndim=1)
+    nb, bs, G, Dk = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
+    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
+    T, H, D = q.shape
+    S = seq_lens.shape[0]
+    if cu_q_lens.shape[0] != S + 1 or block_table.shape[0] != S or Dk != D:
+        raise ValueError("inconsistent shapes")
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda("out", out, dtype=q.dtype, ndim=3)
+    if lse_out is None and want_lse:
+        lse_out = torch.empty((T, H), dtype=torch.float32, device=dev)
+    if lse_out is not None:
+        _cuda("lse_out", lse_out, dtype=torch.float32, ndim=2)
+    if out.shape != q.shape or (lse_out is not None and tuple(lse_out.shape) != (T, H)):
+        raise ValueError("out must have q's shape and lse_out [num_tokens, num_heads]")
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    need = metis_prefill_workspace_bytes(S, T, H, G)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _one_device(dev, cu_q_lens, block_table, seq_lens, out, lse_out, workspace)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.metis_paged_attn_prefill_chunk_fp8(
+        _ptr(q), _ptr(cu_q_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+        _ptr(seq_lens), _ptr(out), _ptr(lse_out), S, T, H, G, D, bs, block_table.shape[1], nb, dt, float(scale),
+        int(max_seq_len), _ptr(workspace), ws_bytes, _stream(stream)))
+    return out, lse_out
 
 
 def metis_prefix_block_hashes(token_ids: torch.Tensor, cu_tokens: torch.Tensor, cu_pages: torch.Tensor,

@@ -91,6 +91,10 @@ extern "C" int metis_read_status(uint32_t* status_out, int clear) {
   if (rc) return rc;
   rc = metis::prefix_status(&bits, clear);
   if (rc) return rc;
+  rc = metis::fp8_status(&bits, clear);
+  if (rc) return rc;
+  rc = metis::decode_fp8_status(&bits, clear);
+  if (rc) return rc;
   *status_out = bits;
   return METIS_OK;
 }

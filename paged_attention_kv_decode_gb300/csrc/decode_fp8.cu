@@ -1,0 +1,678 @@
+// Decode attention over an 8-bit paged cache: e4m3 codes with one power-of-two scale per
+// page and KV head (cache_fp8.cu writes it).  For query head h over its KV head g
+//
+//   z_t = scale * 2^kb(t) * (q_h . code_K(t)),  out = sum_t softmax(z)_t 2^vb(t) code_V(t)
+//
+// with kb, vb the scale exponents of the page that holds token t.
+//
+// Memory-bound: 2 G D bytes per cached token against 4 H D operations.  The structure is
+// that of the bf16 kernel in decode.cu -- one CTA per (partition, KV head, sequence), the
+// group's query heads share each K/V byte, each warp fills a private ring with TMA tile
+// loads and keeps its own softmax state -- with what the codes change:
+//
+//   * A unit is 32 tokens (two m16 tiles): at one byte per element the 16-token units of
+//     the bf16 kernel would halve the bytes behind each softmax step.
+//   * Codes become fp16 in registers (cvt.e4m3x2 -> f16x2, exact); the products are fp16
+//     mma.sync with fp32 accumulation.  K: a 32-bit piece of ldmatrix holds four
+//     consecutive dims of a token, so dims are dealt to the k-slots in that order and the
+//     query is loaded to match.  V: ldmatrix.trans of 16-bit pairs gives {two dims} x {two
+//     tokens}; one byte permute splits it into the even and the odd dim's token pair, so
+//     an m16 tile of output rows is 8 even dims followed by 8 odd ones.
+//   * The query row is scaled by a power of two into fp16's range (its largest element in
+//     [2^14, 2^15)): exact for bf16 elements down to 2^-29 of the largest, and below that
+//     off by at most 2^-40 of it.  fp32 queries are split into two fp16 parts (22 bits).
+//   * The softmax reference is the running maximum minus 14, so that the weights use
+//     fp16's range down to 2^-28 of the largest before they lose bits (fp32 queries: two
+//     fp16 parts again).
+//   * The scales stay out of the codes: a page's K factor multiplies its scores, and each
+//     tile's P V lands in a fresh accumulator that joins O with the page's V factor, so any
+//     spread of scales between pages is held in fp32.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/metis_attn.h"
+#include "common.cuh"
+#include "decode.cuh"
+#include "fp8.cuh"
+#include "host.h"
+
+namespace metis {
+
+__device__ unsigned int g_status_decode_fp8 = 0;
+
+struct DecodeFp8Params {
+  DecodeParams d;
+  const uint8_t* k_scale;  // [num_blocks, G]
+  const uint8_t* v_scale;
+};
+
+constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
+constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
+
+template <int D>
+struct Fp8DecodeShape {
+  static constexpr int kTileBytes = kUnit8 * D;     // K or V of one unit
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kSteps = D / 16;             // 16-dim chunks of a row
+};
+
+template <int D, int NW, int STAGES>
+constexpr int fp8_decode_smem_bytes() {
+  return 1024 + NW * STAGES * (Fp8DecodeShape<D>::kStageBytes + 16 + 8);
+}
+
+// Byte offset of 16-byte chunk c of row `row` in a TMA tile of D-byte rows: 128-byte
+// swizzle for 128-byte rows, 64-byte swizzle for 64-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t tile_chunk(int row, int c) {
+  return row * D + ((c ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The part of (lo, hi) that fp16 `packed` left over, scaled by 2^11, as fp16
+__device__ __forceinline__ uint32_t pack_f16x2_rest(float lo, float hi, uint32_t packed) {
+  const float2 v = unpack_f16x2(packed);
+  return pack_f16x2((lo - v.x) * 2048.f, (hi - v.y) * 2048.f);
+}
+
+// One work item: the tokens [t0, t1) of KV head g of sequence s; arguments as for
+// decode_bf16_item (decode.cu).  scales: this warp group's [NW][STAGES] page factors.
+template <int D, typename QT, int NW, int STAGES, typename Sync>
+__device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                                const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
+                                                float4* scales, int part, int g, int s, int orow, int t0, int t1,
+                                                int warp, int lane, int tid, int& kb, Sync sync) {
+  using Shape = Fp8DecodeShape<D>;
+  constexpr int KS = Shape::kSteps;
+  constexpr bool SPLIT = sizeof(QT) == 4;  // two fp16 parts of q and P
+  const DecodeParams& p = pp.d;
+  unsigned int* const status = &g_status_decode_fp8;
+
+  // this warp's units: u0 + warp + k * NW, k < n_my
+  const int u0 = t0 / kUnit8;
+  const int n_units = (t1 - u0 * kUnit8 + kUnit8 - 1) / kUnit8;
+  const int n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
+  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
+  const bool small_pages = p.bs == 16;        // two pages per unit, else part of one
+  const int box = small_pages ? 16 : kUnit8;  // rows of a TMA box
+
+  // Lane l holds unit k = 32 * batch + l: the TMA row of its page(s) and the scale bytes
+  // (k0, v0, k1, v1).  -box (a box outside the tensor, read as zeros) marks a bad block id
+  // or a page past the range.
+  auto unit_info = [&](int k, int& c0, int& c1, uint32_t& sc) {
+    c0 = c1 = -box;
+    sc = 0x7f7f7f7fu;
+    if (k >= n_my) return;
+    const int tok = (u0 + warp + k * NW) * kUnit8;
+    const int page = tok / p.bs;
+    const int b = checked_block(bt_row, page, p.num_blocks, status);
+    if (b >= 0) {
+      c0 = b * p.bs + (tok - page * p.bs);
+      const size_t at = (size_t)b * p.G + g;
+      sc = __ldg(pp.k_scale + at) | ((uint32_t)__ldg(pp.v_scale + at) << 8);
+      sc |= sc << 16;
+    }
+    if (small_pages && tok + 16 < t1) {
+      const int b1 = checked_block(bt_row, page + 1, p.num_blocks, status);
+      sc = (sc & 0xffffu) | 0x7f7f0000u;
+      if (b1 >= 0) {
+        c1 = b1 * 16;
+        const size_t at = (size_t)b1 * p.G + g;
+        sc = (sc & 0xffffu) | ((uint32_t)__ldg(pp.k_scale + at) << 16) | ((uint32_t)__ldg(pp.v_scale + at) << 24);
+      }
+    }
+  };
+  int cur0, cur1, next0, next1;
+  uint32_t cur_sc, next_sc;
+  unit_info(lane, cur0, cur1, cur_sc);
+  unit_info(32 + lane, next0, next1, next_sc);
+  const uint64_t policy = l2_policy_evict_first();
+
+  auto issue = [&](int k) {  // called by all lanes, in order k = 0, 1, 2, ...
+    if (k > 0 && (k & 31) == 0) {
+      cur0 = next0;
+      cur1 = next1;
+      cur_sc = next_sc;
+      unit_info(k + 32 + lane, next0, next1, next_sc);
+    }
+    const int st = (kb + k) % STAGES;
+    uint8_t* base = smem + (warp * STAGES + st) * Shape::kStageBytes;
+    uint64_t* bar = &bars[warp * STAGES + st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, Shape::kStageBytes);
+    if (lane == (k & 31))
+      scales[warp * STAGES + st] = make_float4(scale_of_byte(cur_sc & 255u), scale_of_byte((cur_sc >> 8) & 255u),
+                                               scale_of_byte((cur_sc >> 16) & 255u), scale_of_byte(cur_sc >> 24));
+    const int r0 = __shfl_sync(0xffffffffu, cur0, k & 31);
+    const int r1 = __shfl_sync(0xffffffffu, cur1, k & 31);
+    __syncwarp();
+    // one box per lane: lanes 0, 1 the K page(s), lanes 2, 3 the V page(s)
+    if (lane < 4 && (small_pages || !(lane & 1)))
+      tma_load_3d(base + (lane >> 1) * Shape::kTileBytes + (lane & 1) * (16 * D), lane < 2 ? &tmK : &tmV, bar, 0, g,
+                  (lane & 1) ? r1 : r0, policy);
+  };
+
+  // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
+  // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
+  const int q4 = lane & 3, rA = lane >> 2;
+  uint32_t qf[KS][2], ql[SPLIT ? KS : 1][2];
+  float undo;  // what the row's scaling has to be undone by
+  {
+    const bool live = rA < p.r;
+    const QT* qrow = reinterpret_cast<const QT*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D + 4 * q4;
+    float x[KS][4];
+    float top = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      if (SPLIT) {
+        const float4 v = live ? *reinterpret_cast<const float4*>(qrow + kk * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[kk][0] = v.x;
+        x[kk][1] = v.y;
+        x[kk][2] = v.z;
+        x[kk][3] = v.w;
+      } else {
+        const uint2 v = live ? *reinterpret_cast<const uint2*>(qrow + kk * 16) : make_uint2(0u, 0u);
+        x[kk][0] = __uint_as_float(v.x << 16);
+        x[kk][1] = __uint_as_float(v.x & 0xffff0000u);
+        x[kk][2] = __uint_as_float(v.y << 16);
+        x[kk][3] = __uint_as_float(v.y & 0xffff0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[kk][i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // up = 2^(14 - e) for the largest element m 2^e, 1 <= m < 2, and undo = 1 / up, from the
+    // exponent field e + 127 (held above 14: a row below 2^-112 is scaled by 2^126)
+    const uint32_t field = min(max(__float_as_uint(top) >> 23, 15u), 254u);
+    const float up = __uint_as_float((268u - field) << 23);
+    undo = __uint_as_float((field - 14u) << 23);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[kk][i] *= up;
+      qf[kk][0] = pack_f16x2(x[kk][0], x[kk][1]);
+      qf[kk][1] = pack_f16x2(x[kk][2], x[kk][3]);
+      if (SPLIT) {
+        ql[kk][0] = pack_f16x2_rest(x[kk][0], x[kk][1], qf[kk][0]);
+        ql[kk][1] = pack_f16x2_rest(x[kk][2], x[kk][3], qf[kk][1]);
+      }
+    }
+  }
+  // factor of this thread's score columns, heads 2 q4 and 2 q4 + 1
+  const float f0 = p.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * q4);
+  const float f1 = p.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * q4 + 4);
+
+  uint64_t o[KS][2];  // [chunk][even, odd dim of lane / 4] x {head 2 q4, head 2 q4 + 1}
+#pragma unroll
+  for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = 0ull;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+  const int prologue = n_my < STAGES ? n_my : STAGES;
+  for (int k = 0; k < prologue; ++k) issue(k);
+
+  // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
+  const int lrow = (((lane >> 3) & 1) << 3) + (lane & 7), lchunk = lane >> 4;
+
+  int k = 0;
+  bool ok = true;
+  for (; k < n_my; ++k) {
+    const int st = (kb + k) % STAGES;
+    const bool landed = mbar_wait(&bars[warp * STAGES + st], ((kb + k) / STAGES) & 1, status);
+    if (!__all_sync(0xffffffffu, landed)) {  // leave the loop together
+      ok = false;
+      break;
+    }
+    const int tok0 = (u0 + warp + k * NW) * kUnit8;
+    const uint32_t kbase = smem_u32(smem + (warp * STAGES + st) * Shape::kStageBytes);
+    const uint32_t vbase = kbase + Shape::kTileBytes;
+    const float4 sc = scales[warp * STAGES + st];
+    // valid tokens of the two tiles (the first tile of a range may start before it)
+    int nv[2];
+    nv[0] = tok0 < t0 ? 0 : min(16, t1 - tok0);
+    nv[1] = max(0, min(16, t1 - tok0 - 16));
+
+    // S^T (16 tokens x 8 heads, twice) = K codes . q^T
+    float acc[2][4], acl[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[h][i] = acl[h][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KS; kk += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
+        ldsm_x4(kbase + tile_chunk<D>(16 * h + lrow, kk + lchunk), r0, r1, r2, r3);
+        unpack_e4m3x4(r0, a0, a2);
+        unpack_e4m3x4(r1, a1, a3);
+        mma_f16_16816(acc[h], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+        if (SPLIT) mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+        unpack_e4m3x4(r2, a0, a2);
+        unpack_e4m3x4(r3, a1, a3);
+        mma_f16_16816(acc[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
+        if (SPLIT) mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk + 1][0], ql[kk + 1][1]);
+      }
+    }
+
+    // online softmax; the thread holds tokens rA, rA + 8 of each tile, heads 2 q4, 2 q4 + 1
+    float x[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float kf = h ? sc.z : sc.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = SPLIT ? fmaf(acl[h][i], 1.f / 2048.f, acc[h][i]) : acc[h][i];
+        x[h][i] = a * (((i & 1) ? f1 : f0) * kf);
+        if (rA + ((i & 2) << 2) >= nv[h]) x[h][i] = -INFINITY;
+      }
+    }
+    const float t0m = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), 4) - kRefDown;
+    const float t1m = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), 4) - kRefDown;
+    // weights reach 2^15 before the reference moves
+    const bool grow0 = t0m > m0 + 1.f, grow1 = t1m > m1 + 1.f;
+    if (__any_sync(0xffffffffu, grow0 || grow1)) {
+      const float al0 = grow0 ? exp2_approx(m0 - t0m) : 1.f;
+      const float al1 = grow1 ? exp2_approx(m1 - t1m) : 1.f;
+      if (grow0) m0 = t0m;
+      if (grow1) m1 = t1m;
+      l0 *= al0;
+      l1 *= al1;
+      const uint64_t al = f2_pack(al0, al1);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        o[i][0] = f2_mul(o[i][0], al);
+        o[i][1] = f2_mul(o[i][1], al);
+      }
+    }
+    // P^T (tokens x heads) -> B operand (k = token, n = head) by 8x8 transposes
+    uint32_t pb[2][2], pl[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = exp2_approx(x[h][i] - ((i & 1) ? m1 : m0));
+      l0 += e[0] + e[2];
+      l1 += e[1] + e[3];
+      const uint32_t a = pack_f16x2(e[0], e[1]), b = pack_f16x2(e[2], e[3]);
+      pb[h][0] = movmatrix_trans(a);
+      pb[h][1] = movmatrix_trans(b);
+      if (SPLIT) {
+        pl[h][0] = movmatrix_trans(pack_f16x2_rest(e[0], e[1], a));
+        pl[h][1] = movmatrix_trans(pack_f16x2_rest(e[2], e[3], b));
+      }
+    }
+
+    // Rows past the range may hold anything (NaN codes included): zero them in the V^T
+    // fragments so that 0 * NaN cannot poison O.
+    const bool partial = nv[0] < 16 || nv[1] < 16;
+    uint32_t vm[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 2 * q4;
+      vm[h][0] = (t < nv[h] ? 0x0000ffffu : 0u) | (t + 1 < nv[h] ? 0xffff0000u : 0u);
+      vm[h][1] = (t + 8 < nv[h] ? 0x0000ffffu : 0u) | (t + 9 < nv[h] ? 0xffff0000u : 0u);
+    }
+    // O^T (D x 8 heads) += 2^vb * V^T codes (D x 16 tokens) . P^T, one fresh accumulator per tile
+#pragma unroll
+    for (int c = 0; c < KS; c += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[4];
+        ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, c + lchunk), r[0], r[1], r[2], r[3]);
+        const float vf = h ? sc.w : sc.y;
+        const uint64_t vf2 = f2_pack(vf, vf);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t lo = r[2 * u], hi = r[2 * u + 1];
+          if (partial) {
+            lo &= vm[h][0];
+            hi &= vm[h][1];
+          }
+          uint32_t a0, a1, a2, a3;
+          unpack_e4m3x4(__byte_perm(lo, 0, 0x3120), a0, a1);  // even, odd dims of tokens 0..7
+          unpack_e4m3x4(__byte_perm(hi, 0, 0x3120), a2, a3);  // ... of tokens 8..15
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16_16816(t, a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          if (SPLIT) {
+            float tl[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16_16816(tl, a0, a1, a2, a3, pl[h][0], pl[h][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = fmaf(tl[i], 1.f / 2048.f, t[i]);
+          }
+          o[c + u][0] = f2_fma(f2_pack(t[0], t[1]), vf2, o[c + u][0]);
+          o[c + u][1] = f2_fma(f2_pack(t[2], t[3]), vf2, o[c + u][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (k + STAGES < n_my) issue(k + STAGES);
+  }
+  if (!ok) {
+    // drain this warp's loads still in flight (bounded) before the ring is reused
+    for (int kk = k + 1; kk < n_my && kk < k + STAGES; ++kk) {
+      const int st = (kb + kk) % STAGES;
+      mbar_wait(&bars[warp * STAGES + st], ((kb + kk) / STAGES) & 1, status);
+    }
+  }
+
+  l0 = warp_sum_xor(l0, 4);
+  l1 = warp_sum_xor(l1, 4);
+  sync();  // every warp is done with its ring
+
+  float* cm = reinterpret_cast<float*>(smem);
+  float* cl = cm + NW * 8;
+  float* co = cl + NW * 8;
+  if (lane < 4) {
+    cm[warp * 8 + 2 * lane] = m0;
+    cm[warp * 8 + 2 * lane + 1] = m1;
+    cl[warp * 8 + 2 * lane] = l0;
+    cl[warp * 8 + 2 * lane + 1] = l1;
+  }
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    float* at = co + ((size_t)warp * D + c * 16 + 2 * rA) * 8 + 2 * q4;
+    *reinterpret_cast<uint64_t*>(at) = o[c][0];
+    *reinterpret_cast<uint64_t*>(at + 8) = o[c][1];
+  }
+  sync();
+  combine_and_store<QT, NW>(p, cm, cl, co, part, g, s, orow, tid);
+  kb += n_my;
+  return ok;
+}
+
+// Warps per CTA and ring depth per warp.
+constexpr int kFp8Warps = 4;
+constexpr int kFp8Stages = 3;
+
+template <int D, typename QT, int NW, int STAGES>
+__global__ void __launch_bounds__(NW * 32) decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                              const __grid_constant__ CUtensorMap tmV,
+                                                              const DecodeFp8Params pp) {
+  constexpr int STAGE_BYTES = Fp8DecodeShape<D>::kStageBytes;
+  static_assert(NW * (64 + D * 32) <= NW * STAGES * STAGE_BYTES, "combine area must fit in the ring");
+  const DecodeParams& p = pp.d;
+  pdl_wait();  // inputs are read after the previous grid in the stream has completed
+  pdl_launch_dependents();
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
+  float4* scales = reinterpret_cast<float4*>(smem + NW * STAGES * STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + NW * STAGES);
+
+  __shared__ int rank_lens[kMaxRankSeqs];
+  __shared__ int rank_found;
+  const int part = blockIdx.x, g = blockIdx.y;
+  const int s = (p.partition_size == 0 && p.S <= kMaxRankSeqs) ? seq_of_rank(p, blockIdx.z, rank_lens, &rank_found)
+                                                                : (int)blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int t0, t1;
+  if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int i = 0; i < NW * STAGES; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  int kb = 0;
+  decode_fp8_item<D, QT, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
+                                     kb, [] { __syncthreads(); });
+}
+
+// ---------------------------------------------------------------------------
+// the decodes of a mixed chunked-prefill batch, beside the chunk kernel: the scheme of
+// decode_rows_beside_kernel (decode.cu)
+// ---------------------------------------------------------------------------
+constexpr int kDec8Groups = 2;
+
+template <int D>
+constexpr int dec8_beside_smem_bytes() {
+  constexpr int need = 1024 + kDec8Groups * kFp8Warps * kFp8Stages * (Fp8DecodeShape<D>::kStageBytes + 24);
+  return need > 116 * 1024 ? need : 116 * 1024;  // never two CTAs on one SM
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
+    decode_fp8_rows_beside_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                                  const DecodeFp8Params pp, const int* n_ctas, int* next_item) {
+  constexpr int NW = kFp8Warps, STAGES = kFp8Stages, GT = NW * 32;
+  constexpr int STAGE_BYTES = Fp8DecodeShape<D>::kStageBytes;
+  static_assert(NW * (64 + D * 32) <= NW * STAGES * STAGE_BYTES, "combine area must fit in the ring");
+  const DecodeParams& p = pp.d;
+  pdl_wait();  // the schedule kernel (n_ctas, the zeroed counter) and every kernel before it completed
+  if ((int)blockIdx.x >= __ldcg(n_ctas)) return;
+  pdl_launch_dependents();  // every CTA of the grid has waited by now: the chunk kernel may launch
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ int rank_seq[kMaxRankSeqs];
+  __shared__ int lens[kMaxRankSeqs];
+  __shared__ int n_dec;
+  __shared__ int item_slot[kDec8Groups];
+  __shared__ int gave_up[kDec8Groups];  // a warp of the group gave up a wait: the group stops
+  // the batch's decodes, longest first (larger batches: in sequence order)
+  const bool ranked = p.S <= kMaxRankSeqs;
+  if (ranked) {
+    if (threadIdx.x == 0) n_dec = 0;
+    for (int i = threadIdx.x; i < p.S; i += blockDim.x)
+      lens[i] = decode_row(p, i) < 0 ? -1 : min(max(p.seq_lens[i], 0), p.cap);
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.S; c += blockDim.x) {
+      const int Lc = lens[c];
+      if (Lc < 0) continue;
+      int r = 0;
+      for (int k = 0; k < p.S; ++k) r += (lens[k] > Lc) || (lens[k] == Lc && k < c);
+      rank_seq[r] = c;
+      atomicAdd(&n_dec, 1);
+    }
+  }
+  const int grp = threadIdx.x / GT, tid = threadIdx.x - grp * GT;
+  const int warp = tid >> 5, lane = tid & 31;
+  uint8_t* gsmem = smem + grp * NW * STAGES * STAGE_BYTES;
+  float4* scales = reinterpret_cast<float4*>(smem + kDec8Groups * NW * STAGES * STAGE_BYTES) + grp * NW * STAGES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDec8Groups * NW * STAGES * (STAGE_BYTES + 16)) + grp * NW * STAGES;
+  if (tid == 0) {
+    if (grp == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    for (int i = 0; i < NW * STAGES; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+    gave_up[grp] = 0;
+  }
+  __syncthreads();
+  const int n_items = (ranked ? n_dec : p.S) * p.G;
+  auto gsync = [grp] { named_barrier_sync(1 + grp, GT); };
+  int kb = 0;  // this warp's ring position, across the group's items
+  for (;;) {
+    gsync();  // the previous item's combine is done with the ring, and the slot was read
+    if (gave_up[grp]) break;  // read after the barrier: the whole group leaves together
+    if (tid == 0) item_slot[grp] = atomicAdd(next_item, 1);
+    gsync();
+    const int it = item_slot[grp];
+    if (it >= n_items) break;
+    const int rank = it / p.G, g = it - rank * p.G;
+    const int s = ranked ? rank_seq[rank] : rank;
+    const int orow = decode_row(p, s);
+    if (orow < 0) continue;  // not a decode (unranked order only)
+    int t0, t1;
+    if (!decode_range<__nv_bfloat16>(p, 0, g, s, orow, t0, t1, tid, GT, &g_status_decode_fp8)) continue;
+    // A wait that gave up (flagged) is seen by its warp only: every warp of the group
+    // still reaches the item's barriers and the next one above, where they all stop.
+    if (!decode_fp8_item<D, __nv_bfloat16, NW, STAGES>(tmK, tmV, pp, gsmem, bars, scales, 0, g, s, orow, t0, t1, warp,
+                                                       lane, tid, kb, gsync) &&
+        lane == 0)
+      gave_up[grp] = 1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int decode_fp8_status(uint32_t* bits, int clear) {
+  unsigned int v = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_status_decode_fp8, sizeof(v));
+  if (e == cudaSuccess && clear) {
+    unsigned int z = 0;
+    e = cudaMemcpyToSymbol(g_status_decode_fp8, &z, sizeof(z));
+  }
+  if (e != cudaSuccess) return fail(METIS_E_CUDA, "reading the status word: %s", cudaGetErrorString(e));
+  *bits |= v;
+  return METIS_OK;
+}
+
+// TMA maps of the K and V codes: boxes of one KV head, a whole row, one page or (pages of
+// 32 and 64) 32 tokens of it.
+template <int D>
+static int encode_kv8_maps(const DecodeParams& p, const void* k_cache, const void* v_cache, CUtensorMap* tmK,
+                           CUtensorMap* tmV) {
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
+  const uint64_t strides[2] = {(uint64_t)D, (uint64_t)p.G * D};
+  const uint32_t box[3] = {(uint32_t)D, 1, (uint32_t)std::min(p.bs, kUnit8)};
+  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  int rc = encode_tiled(tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_cache, dims, strides, box, sw);
+  if (rc) return rc;
+  return encode_tiled(tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_cache, dims, strides, box, sw);
+}
+
+template <int D, typename QT>
+static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, dim3 grid,
+                      cudaStream_t st) {
+  CUtensorMap tmK, tmV;
+  int rc = encode_kv8_maps<D>(pp.d, k_cache, v_cache, &tmK, &tmV);
+  if (rc) return rc;
+  constexpr int smem = fp8_decode_smem_bytes<D, kFp8Warps, kFp8Stages>();
+  static int done = 0;
+  auto kern = decode_fp8_kernel<D, QT, kFp8Warps, kFp8Stages>;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
+  if (rc) return rc;
+  return launch_dependent(kern, grid, dim3(kFp8Warps * 32), (size_t)smem, st, "decode_fp8_kernel launch", tmK, tmV, pp);
+}
+
+template <int D>
+static int launch_beside8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, const int* n_ctas,
+                          int* next_item, int grid, cudaStream_t st) {
+  CUtensorMap tmK, tmV;
+  int rc = encode_kv8_maps<D>(pp.d, k_cache, v_cache, &tmK, &tmV);
+  if (rc) return rc;
+  constexpr int smem = dec8_beside_smem_bytes<D>();
+  static int done = 0;
+  auto kern = decode_fp8_rows_beside_kernel<D>;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
+  if (rc) return rc;
+  return launch_dependent(kern, dim3((unsigned)grid), dim3(kDec8Groups * kFp8Warps * 32), (size_t)smem, st,
+                          "decode_fp8_rows_beside_kernel launch", tmK, tmV, pp, n_ctas, next_item);
+}
+
+static DecodeFp8Params fp8_params(const void* q, const Fp8Cache& cache, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
+                                  int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap) {
+  DecodeFp8Params pp{};
+  DecodeParams& p = pp.d;
+  p.q = q;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.out = out;
+  p.lse_out = lse_out;
+  p.S = S;
+  p.H = H;
+  p.G = G;
+  p.D = D;
+  p.bs = bs;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.r = H / G;
+  p.scale_log2 = scale * kLog2e;
+  p.max_parts = 1;
+  p.cap = cap;
+  p.rows = rows;
+  pp.k_scale = cache.k_scale;
+  pp.v_scale = cache.v_scale;
+  return pp;
+}
+
+int launch_decode_fp8_rows_beside(const void* q, const Fp8Cache& cache, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
+                                  int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                                  const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
+  const DecodeFp8Params pp = fp8_params(q, cache, block_table, seq_lens, rows, out, lse_out, S, H, G, D, bs, max_blocks,
+                                        num_blocks, scale, cap);
+  return D == 64 ? launch_beside8<64>(pp, cache.k_cache, cache.v_cache, n_ctas, next_item, grid, st)
+                 : launch_beside8<128>(pp, cache.k_cache, cache.v_cache, n_ctas, next_item, grid, st);
+}
+
+}  // namespace metis
+
+using namespace metis;
+
+extern "C" int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                           const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                           const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                                           int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                           int max_blocks, int num_blocks, int dtype, float scale, int partition_size,
+                                           int max_seq_len, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (num_seqs < 0) return fail(METIS_E_SHAPE, "num_seqs < 0");
+  if (num_seqs == 0) return METIS_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out)
+    return fail(METIS_E_NULL, "q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens and out are required");
+  if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks <= 0 ||
+      num_blocks <= 0 || max_seq_len <= 0)
+    return fail(METIS_E_SHAPE, "sizes must be positive");
+  if (num_heads % num_kv_heads) return fail(METIS_E_SHAPE, "num_heads %% num_kv_heads != 0");
+  if (num_seqs > 65535 || num_kv_heads > 65535) return fail(METIS_E_SHAPE, "num_seqs and num_kv_heads must be <= 65535");
+  if ((long long)max_blocks * block_size > 0x7fffffffLL || (long long)num_blocks * block_size > 0x7fffffffLL)
+    return fail(METIS_E_SHAPE, "max_blocks * block_size and num_blocks * block_size must fit in int32");
+  if (head_dim != 64 && head_dim != 128) return fail(METIS_E_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(METIS_E_UNSUPPORTED, "block_size must be 16, 32 or 64");
+  if (dtype != METIS_F32 && dtype != METIS_BF16) return fail(METIS_E_UNSUPPORTED, "dtype must be METIS_F32 or METIS_BF16");
+  if (num_heads / num_kv_heads > 8) return fail(METIS_E_UNSUPPORTED, "num_heads / num_kv_heads must be <= 8");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse_out, 4))
+    return fail(METIS_E_ALIGN, "tensors must be 16-byte aligned (block_table, seq_lens, lse_out: 4-byte; scales: any)");
+  if (partition_size < 0 || (partition_size % 16))
+    return fail(METIS_E_SHAPE, "partition_size must be 0 or a positive multiple of 16");
+  if (!(scale == scale)) return fail(METIS_E_SHAPE, "scale is NaN");
+
+  const int eff_len = effective_max_len(max_seq_len, max_blocks, block_size);
+  const size_t parts = split_parts(eff_len, partition_size);
+  if (parts > 0x7fffffff) return fail(METIS_E_SHAPE, "too many partitions");
+  const size_t need = metis_decode_workspace_bytes(num_seqs, num_heads, head_dim, eff_len, partition_size);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(METIS_E_WORKSPACE, "workspace must hold %zu bytes (256-byte aligned)", need);
+
+  const Fp8Cache cache = {k_cache, v_cache, k_scale, v_scale};
+  DecodeFp8Params pp = fp8_params(q, cache, block_table, seq_lens, nullptr, out, lse_out, num_seqs, num_heads,
+                                  num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale, eff_len);
+  DecodeParams& p = pp.d;
+  p.partition_size = partition_size;
+  if (parts) {
+    const size_t units = (size_t)num_seqs * num_heads * parts;
+    p.max_parts = (int)parts;
+    p.part_out = reinterpret_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
+                                          align_up(units * head_dim * sizeof(float), 256));
+  }
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)p.max_parts, (unsigned)num_kv_heads, (unsigned)num_seqs);
+  int rc;
+  if (dtype == METIS_F32)
+    rc = head_dim == 64 ? launch_fp8<64, float>(pp, k_cache, v_cache, grid, st)
+                        : launch_fp8<128, float>(pp, k_cache, v_cache, grid, st);
+  else
+    rc = head_dim == 64 ? launch_fp8<64, __nv_bfloat16>(pp, k_cache, v_cache, grid, st)
+                        : launch_fp8<128, __nv_bfloat16>(pp, k_cache, v_cache, grid, st);
+  if (rc) return rc;
+  if (parts)
+    rc = launch_merge_ex(p.part_out, p.part_lse, seq_lens, partition_size, out, lse_out, num_seqs, num_heads, head_dim,
+                         p.max_parts, dtype, 0, st);
+  return rc;
+}

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/metis_attn.h"
 
 namespace metis {
@@ -53,6 +55,20 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Partitions a split call launches: ceil(max_seq_len / partition_size), in 64
+// bits (max_seq_len near INT_MAX must not overflow); 0 when unsplit.
+inline size_t split_parts(int max_seq_len, int partition_size) {
+  if (partition_size <= 0 || max_seq_len <= 0) return 0;
+  return (size_t)(((long long)max_seq_len + partition_size - 1) / partition_size);
+}
+
+// The longest sequence a call can read: max_seq_len, clamped to what a
+// block-table row addresses (max_blocks * block_size).  Partitions past it
+// would only ever be empty, so they are neither launched nor given scratch.
+inline int effective_max_len(int max_seq_len, int max_blocks, int block_size) {
+  return (int)std::min<long long>((long long)max_blocks * block_size, (long long)max_seq_len);
+}
+
 // Log-sum-exp merge of split partials [S, H, max_parts, D] (decode.cu); with
 // skip_single, sequences with at most one partition are left untouched.
 int launch_merge_ex(const float* part_out, const float* part_lse, const int32_t* seq_lens, int P, void* out,
@@ -81,11 +97,25 @@ int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_
                               int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
                               const int* n_ctas, int* next_item, int grid, cudaStream_t st);
 
+// The same two for an 8-bit cache (decode_fp8.cu).
+struct Fp8Cache {
+  const void* k_cache;  // e4m3 codes [num_blocks, bs, G, D]
+  const void* v_cache;
+  const uint8_t* k_scale;  // scale bytes [num_blocks, G]
+  const uint8_t* v_scale;
+};
+int launch_decode_fp8_rows_beside(const void* q, const Fp8Cache& cache, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
+                                  int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                                  const int* n_ctas, int* next_item, int grid, cudaStream_t st);
+
 // Per-translation-unit device status words.
 int decode_status(uint32_t* bits, int clear);
 int prefill_status(uint32_t* bits, int clear);
 int mla_status(uint32_t* bits, int clear);
 int cache_status(uint32_t* bits, int clear);
 int prefix_status(uint32_t* bits, int clear);
+int fp8_status(uint32_t* bits, int clear);
+int decode_fp8_status(uint32_t* bits, int clear);
 
 }  // namespace metis

@@ -55,6 +55,7 @@
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
+#include "fp8.cuh"
 #include "host.h"
 #include "tcgen05.cuh"
 
@@ -107,7 +108,9 @@ struct PrefillParams {
   int* dec_ctas;
   int* dec_next;
   int num_sms, D;
+  int kv_token_bytes;  // K and V of one cached token, every KV head
   int wait_at_exit;
+  Fp8Cache fp8;  // an 8-bit cache (k_cache NULL: bf16)
 };
 
 // Shared-memory layout (all tiles 128-byte swizzled, [64-column half][row][128 B]).
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
       cq += __shfl_xor_sync(0xffffffffu, cq, o);
     }
     if (lane == 0) {
-      const float d = (float)dt * ((float)p.G * p.D * 4.0f / kDecSmBytesPerS);   // K and V rows of every decode
+      const float d = (float)dt * ((float)p.kv_token_bytes / kDecSmBytesPerS);   // K and V rows of every decode
       const float c = (float)cq * ((float)p.H * p.D * 4.0f / kChunkSmFlopsPerS);  // QK^T and PV of every chunk query
       int k = 0;
       if (dt > 0) k = cq > 0 ? (int)ceilf(p.num_sms * (d / (d + c))) : p.num_sms;
@@ -322,7 +325,19 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag
   return it.n0 > 0;
 }
 
-template <int D>
+// Eight e4m3 codes of one row times their page's scale, as bf16 (exact: four significant
+// bits and a power of two)
+__device__ __forceinline__ uint4 codes_to_bf16x8(uint32_t w0, uint32_t w1, float scale) {
+  float a[4], b[4];
+  unpack_e4m3x4_f32(w0, a);
+  unpack_e4m3x4_f32(w1, b);
+  return make_uint4(pack_bf16x2(a[0] * scale, a[1] * scale), pack_bf16x2(a[2] * scale, a[3] * scale),
+                    pack_bf16x2(b[0] * scale, b[1] * scale), pack_bf16x2(b[2] * scale, b[3] * scale));
+}
+
+// KV8: the cache holds e4m3 codes; the producer warps convert them to bf16 tiles of the
+// same layout, and every other role is the same.
+template <int D, bool KV8>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                        const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
@@ -424,12 +439,58 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const int half_pg = npg >> 1;              // pages of this warp
     const uint64_t pol = l2_policy_evict_last();
     const int depth = is_k ? kKStages : kVStages;
-    if (lane == 0) tma_prefetch_desc(map);
+    if (!KV8 && lane == 0) tma_prefetch_desc(map);
     uint32_t t = 0, k = 0;                     // tiles issued so far, units read
     bool ok = true;
     PfUnit it;
     while (ok && next_unit(k, it) > 0) {
       const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
+      if constexpr (KV8) {
+        constexpr int CPR = D / 16, RPP = 32 / CPR;  // 16-byte pieces of a row, rows per pass
+        const uint8_t* codes = reinterpret_cast<const uint8_t*>(is_k ? p.fp8.k_cache : p.fp8.v_cache);
+        const uint8_t* bytes = is_k ? p.fp8.k_scale : p.fp8.v_scale;
+        const int piece = lane % CPR;
+        for (int j = 0; ok && j < it.n_kv; ++j, ++t) {
+          const int st = t % depth;
+          if (t >= (uint32_t)depth && !wait_all(&empty[st], ((t / depth) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* tile = ring + st * Sh::kKvBytes + (piece * 16 / 64) * Sh::kKvHalf;
+#pragma unroll 1
+          for (int r0 = part * (kKvTile / 2); r0 < (part + 1) * (kKvTile / 2); r0 += 2 * RPP) {
+            uint4 c[2];
+            float f[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int tok = j * kKvTile + r0 + u * RPP + lane / CPR;
+              c[u] = make_uint4(0u, 0u, 0u, 0u);  // rows past the end: zeros
+              f[u] = 1.f;
+              if (tok < it.L) {
+                const int page = tok / p.bs;
+                const int b = checked_block(bt_row, page, p.num_blocks, &g_status_prefill);
+                if (b >= 0) {
+                  const size_t row = (size_t)b * p.bs + (tok - page * p.bs);
+                  c[u] = __ldg(reinterpret_cast<const uint4*>(codes + (row * p.G + it.g) * D) + piece);
+                  f[u] = scale_of_byte(__ldg(bytes + (size_t)b * p.G + it.g));
+                }
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int row = r0 + u * RPP + lane / CPR;
+              const int ch = piece * 2 & 7;  // first of the two 16-byte chunks of the 128-byte row
+              uint8_t* dst = tile + row * 128;
+              *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = codes_to_bf16x8(c[u].x, c[u].y, f[u]);
+              *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) << 4)) = codes_to_bf16x8(c[u].z, c[u].w, f[u]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
+        }
+        continue;
+      }
       for (int j = 0; j < it.n_kv; ++j, ++t) {
         const int st = t % depth;
         const int lp = part * half_pg + lane;  // page index inside the tile
@@ -453,7 +514,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
                         rowc, pol);
       }
     }
-    if (*abort_flag) {
+    if (!KV8 && *abort_flag) {
       // let the loads still in flight land before the CTA's memory goes away
       for (uint32_t k = t > (uint32_t)depth ? t - depth : 0; k < t; ++k)
         mbar_wait(&full[k % depth], (k / depth) & 1, &g_status_prefill);
@@ -521,7 +582,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
         tc_fence_after_sync();
         const int tok0 = j * kKvTile;
-        if (tok0 + kKvTile > it.L) {
+        if (!KV8 && tok0 + kKvTile > it.L) {  // (the converted tiles hold zeros there)
           // rows past the sequence end may hold anything (NaN included): zero them so that P = 0 stays 0
           uint8_t* vb = sV + vst * Sh::kKvBytes;
           for (int row = (it.L - tok0) + lane; row < kKvTile; row += 32)
@@ -802,7 +863,7 @@ static size_t prefill_max_items(int num_seqs, int num_tokens, int Tq) {
 
 // The schedule kernel, then `between(p)` (the decodes of a mixed batch, or
 // nothing), then the chunk kernel.
-template <int D, typename Between>
+template <int D, bool KV8, typename Between>
 static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_cache, const void* v_cache,
                           void* workspace, size_t max_items, int sms, cudaStream_t st, Between between) {
   PrefillParams p = p0;
@@ -818,19 +879,24 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   }
   p.num_sms = sms;
   p.D = D;
+  p.kv_token_bytes = 2 * p.G * D * (KV8 ? 1 : 2);
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)p.H, (uint64_t)p.T};
   const uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)p.H * D * 2};
   const uint32_t qbox[3] = {64, 1, (uint32_t)p.Tq};
   int rc = encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  const uint64_t kdims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
-  const uint64_t kstr[2] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2};
-  const uint32_t kbox[3] = {64, 1, (uint32_t)p.bs};
-  rc = encode_tiled(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc) return rc;
-  rc = encode_tiled(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc) return rc;
+  if (KV8) {
+    tmK = tmV = tmQ;  // not used: the codes are loaded by the producers' threads
+  } else {
+    const uint64_t kdims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
+    const uint64_t kstr[2] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2};
+    const uint32_t kbox[3] = {64, 1, (uint32_t)p.bs};
+    rc = encode_tiled(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+    rc = encode_tiled(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+  }
   // a programmatic dependent of the kernel before it (e.g. the paged K/V write): its
   // launch overlaps that kernel's tail
   rc = launch_dependent(prefill_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, "prefill_schedule_kernel launch",
@@ -840,7 +906,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   if (rc) return rc;
   constexpr int smem = PfShape<D>::kSmem;
   static int done = 0;
-  auto kern = prefill_bf16_kernel<D>;
+  auto kern = prefill_bf16_kernel<D, KV8>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   // the warpgroups' register targets draw on the launch allocation: refuse to launch
@@ -873,14 +939,14 @@ extern "C" size_t metis_prefill_workspace_bytes(int num_seqs, int num_tokens, in
   return 256 + prefill_max_items(num_seqs, num_tokens, kRows / r) * sizeof(int4);
 }
 
-extern "C" int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_cache,
-                                              const void* v_cache, const int32_t* block_table,
-                                              const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
-                                              int num_tokens, int num_heads, int num_kv_heads, int head_dim,
-                                              int block_size, int max_blocks, int num_blocks, int dtype, float scale,
-                                              int max_seq_len, void* workspace, size_t workspace_bytes,
-                                              void* stream) {
-  clear_error();
+namespace metis {
+
+// Both entry points: fp8.k_cache is NULL for a bf16 cache, else k_cache and the codes are one.
+static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                         int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                         int num_blocks, int dtype, float scale, int max_seq_len, void* workspace,
+                         size_t workspace_bytes, void* stream, const Fp8Cache& fp8) {
   if (num_seqs < 0 || num_tokens < 0) return fail(METIS_E_SHAPE, "num_seqs and num_tokens must be >= 0");
   if (num_seqs == 0 || num_tokens == 0) return METIS_OK;
   if (!q || !cu_q_lens || !k_cache || !v_cache || !block_table || !seq_lens || !out)
@@ -934,6 +1000,7 @@ extern "C" int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q
   // behind it, which it allows only after its CTAs waited for the schedule -- takes
   // the remaining SMs at once and the decodes' SMs as they finish.  Head ratios
   // above 8 stay on the chunk path.
+  p.fp8 = fp8;
   p.skip_decodes = r <= 8 && num_seqs <= 65535;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -942,10 +1009,47 @@ extern "C" int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q
   sms = std::max(sms, 1);
   auto between = [&](const PrefillParams& pp) -> int {
     if (!pp.skip_decodes) return METIS_OK;
+    if (fp8.k_cache)
+      return launch_decode_fp8_rows_beside(q, fp8, block_table, seq_lens, cu_q_lens, out, lse_out, num_seqs, num_heads,
+                                           num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale, pp.cap,
+                                           pp.dec_ctas, pp.dec_next, sms, st);
     return launch_decode_rows_beside(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, out, lse_out, num_seqs,
                                      num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale,
                                      pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
   };
-  return head_dim == 128 ? launch_prefill<128>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between)
-                         : launch_prefill<64>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+  if (fp8.k_cache)
+    return head_dim == 128 ? launch_prefill<128, true>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between)
+                           : launch_prefill<64, true>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+  return head_dim == 128 ? launch_prefill<128, false>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between)
+                         : launch_prefill<64, false>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+}
+
+}  // namespace metis
+
+extern "C" int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_cache,
+                                              const void* v_cache, const int32_t* block_table,
+                                              const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                                              int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                              int block_size, int max_blocks, int num_blocks, int dtype, float scale,
+                                              int max_seq_len, void* workspace, size_t workspace_bytes,
+                                              void* stream) {
+  clear_error();
+  return prefill_chunk(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse_out, num_seqs, num_tokens,
+                       num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, dtype, scale, max_seq_len,
+                       workspace, workspace_bytes, stream, Fp8Cache{});
+}
+
+extern "C" int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,
+                                                  const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                                                  const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                                  float* lse_out, int num_seqs, int num_tokens, int num_heads,
+                                                  int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                                                  int num_blocks, int dtype, float scale, int max_seq_len,
+                                                  void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (num_seqs > 0 && num_tokens > 0 && (!k_cache || !k_scale || !v_scale))
+    return fail(METIS_E_NULL, "k_cache, k_scale and v_scale are required");
+  return prefill_chunk(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse_out, num_seqs, num_tokens,
+                       num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, dtype, scale, max_seq_len,
+                       workspace, workspace_bytes, stream, Fp8Cache{k_cache, v_cache, k_scale, v_scale});
 }

@@ -276,3 +276,91 @@ def test_prefix_lookup_empty_and_workspace(lib):
 def test_wait_probe_rejects_limits_outside_one_second(lib, limit_ns):
     assert lib.metis_debug_wait_probe(limit_ns, None) == -2   # METIS_E_SHAPE
     assert "limit_ns" in pa.metis_last_error()
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache's entry points
+# ---------------------------------------------------------------------------
+def _vp(x):
+    return None if x is None else ctypes.c_void_p(x)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(key=None), -1), (dict(ks=None), -1), (dict(cu=None), -1), (dict(bt=None), -1), (dict(sl=None), -1),
+    (dict(S=-1), -2), (dict(T=-1), -2), (dict(G=0), -2), (dict(nb=0), -2), (dict(mb=0), -2),
+    (dict(D=96), -3), (dict(D=256), -3), (dict(bs=8), -3), (dict(bs=128), -3), (dict(dt=5), -3),
+    (dict(mb=1 << 28, bs=64), -2), (dict(nb=1 << 28, bs=64), -2), (dict(G=1 << 24), -2),
+    (dict(key=FAKE + 8), -4), (dict(kc=FAKE + 8), -4), (dict(cu=FAKE + 2), -4),
+    (dict(S=0), 0), (dict(T=0), 0),
+])
+def test_reshape_and_cache_fp8_rejects(lib, kw, code):
+    a = dict(key=FAKE, value=FAKE, kc=FAKE, vc=FAKE, ks=FAKE + 1, vs=FAKE + 3, cu=FAKE, bt=FAKE, sl=FAKE, S=2, T=10,
+             G=8, D=128, bs=16, mb=4, nb=64, dt=pa.METIS_BF16)
+    a.update(kw)
+    assert lib.metis_reshape_and_cache_fp8(
+        *[_vp(a[k]) for k in ("key", "value", "kc", "vc", "ks", "vs", "cu", "bt", "sl")], a["S"], a["T"], a["G"],
+        a["D"], a["bs"], a["mb"], a["nb"], a["dt"], None) == code
+    assert (pa.metis_last_error() == "") == (code == 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kc=None), -1), (dict(vs=None), -1), (dict(ro=None), -1), (dict(ko=None), -1),
+    (dict(S=-1), -2), (dict(R=-1), -2), (dict(S=65536), -2), (dict(G=0), -2), (dict(ml=0), -2), (dict(G=1 << 18), -2),
+    (dict(D=32), -3), (dict(bs=48), -3), (dict(dt=2), -3),
+    (dict(ko=FAKE + 8), -4), (dict(ro=FAKE + 1), -4),
+    (dict(S=0), 0), (dict(R=0), 0),
+])
+def test_gather_cache_fp8_rejects(lib, kw, code):
+    a = dict(kc=FAKE, vc=FAKE, ks=FAKE + 1, vs=FAKE + 3, bt=FAKE, sl=FAKE, ro=FAKE, ko=FAKE, vo=FAKE, S=2, R=10, G=8,
+             D=128, bs=16, mb=4, nb=64, dt=pa.METIS_BF16, ml=64)
+    a.update(kw)
+    assert lib.metis_gather_cache_fp8(
+        *[_vp(a[k]) for k in ("kc", "vc", "ks", "vs", "bt", "sl", "ro", "ko", "vo")], a["S"], a["R"], a["G"], a["D"],
+        a["bs"], a["mb"], a["nb"], a["dt"], a["ml"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(ks=None), -1), (dict(vs=None), -1), (dict(out=None), -1),
+    (dict(S=-1), -2), (dict(S=65536), -2), (dict(H=0), -2), (dict(H=30), -2), (dict(ml=0), -2),
+    (dict(H=72, G=8), -3), (dict(D=96), -3), (dict(bs=8), -3), (dict(dt=9), -3),
+    (dict(q=FAKE + 4), -4), (dict(vc=FAKE + 8), -4), (dict(lse=FAKE + 2), -4),
+    (dict(P=100), -2), (dict(P=-16), -2), (dict(P=64), -5), (dict(P=64, ws=FAKE, wb=64), -5),
+    (dict(P=64, ws=FAKE + 16, wb=1 << 30), -5), (dict(scale=float("nan")), -2), (dict(S=0), 0),
+])
+def test_decode_fp8_rejects(lib, kw, code):
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE + 1, vs=FAKE + 3, bt=FAKE, sl=FAKE, out=FAKE, lse=None, S=4, H=56, G=8,
+             D=128, bs=16, mb=8, nb=64, dt=pa.METIS_BF16, scale=0.1, P=0, ml=128, ws=None, wb=0)
+    a.update(kw)
+    assert lib.metis_paged_attn_decode_fp8(
+        *[_vp(a[k]) for k in ("q", "kc", "vc", "ks", "vs", "bt", "sl", "out", "lse")], a["S"], a["H"], a["G"], a["D"],
+        a["bs"], a["mb"], a["nb"], a["dt"], a["scale"], a["P"], a["ml"], _vp(a["ws"]), a["wb"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(kc=None), -1), (dict(ks=None), -1), (dict(vs=None), -1),
+    (dict(dt=pa.METIS_F32), -3), (dict(D=96), -3), (dict(bs=8), -3), (dict(H=24), -3), (dict(H=30), -2),
+    (dict(q=FAKE + 8), -4), (dict(ws=None), -5), (dict(wb=16), -5), (dict(T=-1), -2), (dict(ml=0), -2),
+    (dict(T=0), 0), (dict(S=0), 0),
+])
+def test_prefill_fp8_rejects(lib, kw, code):
+    a = dict(q=FAKE, cu=FAKE, kc=FAKE, vc=FAKE, ks=FAKE + 1, vs=FAKE + 3, bt=FAKE, sl=FAKE, out=FAKE, lse=None, S=4,
+             T=100, H=32, G=8, D=128, bs=16, mb=8, nb=64, dt=pa.METIS_BF16, scale=0.1, ml=128, ws=FAKE, wb=1 << 20)
+    a.update(kw)
+    assert lib.metis_paged_attn_prefill_chunk_fp8(
+        *[_vp(a[k]) for k in ("q", "cu", "kc", "vc", "ks", "vs", "bt", "sl", "out", "lse")], a["S"], a["T"], a["H"],
+        a["G"], a["D"], a["bs"], a["mb"], a["nb"], a["dt"], a["scale"], a["ml"], _vp(a["ws"]), a["wb"], None) == code
+
+
+def test_binding_refuses_cpu_tensors_fp8(lib):
+    import torch
+    codes, byte = torch.zeros(2, 16, 1, 64, dtype=torch.uint8), torch.zeros(2, 1, dtype=torch.uint8)
+    bt, sl = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q = torch.zeros(1, 4, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_paged_attn_decode_fp8(q, codes, codes, byte, byte, bt, sl, 0.1, max_seq_len=1)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_gather_cache_fp8(codes, codes, byte, byte, bt, sl, sl, num_rows=1)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_reshape_and_cache_fp8(q, q, codes, codes, byte, byte, sl, bt, sl)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_paged_attn_prefill_chunk_fp8(q.bfloat16(), sl, codes, codes, byte, byte, bt, sl, 0.1)
