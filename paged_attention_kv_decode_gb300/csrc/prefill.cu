@@ -65,7 +65,7 @@ __device__ unsigned int g_status_prefill = 0;
 
 constexpr int kPfThreads = 512;   // 2 softmax groups + 4 TMA warps + MMA warp + 3 idle warps
 constexpr int kMmaWarp = 12;
-constexpr int kUnitReaders = 14;  // warps 0..13 read every unit from the unit ring
+constexpr int kUnitReaders = 14;  // warps 0..13 read every unit from the unit ring (8-bit cache: and warp 15)
 constexpr int kRegsLaunch = 65536 / kPfThreads;  // 128: the block takes the whole register file
 #ifndef PF_REGS_SOFTMAX
 #define PF_REGS_SOFTMAX 216
@@ -77,18 +77,25 @@ constexpr int kRegsProd = PF_REGS_PROD;        // warpgroup 2: K/V producers
 constexpr int kRegsMma = PF_REGS_MMA;          // warpgroup 3: UMMA issuer, query loader, idle warps
 static_assert(128 * (2 * kRegsSoftmax + kRegsProd + kRegsMma) <= kPfThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
+// 8-bit cache: the converters in the last two warpgroups need more
+constexpr int kRegsSoftmax8 = 200;
+constexpr int kRegsOther8 = 56;
+static_assert(128 * (2 * kRegsSoftmax8 + 2 * kRegsOther8) <= kPfThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
 #ifndef METIS_PF_K_STAGES
 #define METIS_PF_K_STAGES 3
 #define METIS_PF_V_STAGES 2
 #endif
 constexpr int kKStages = METIS_PF_K_STAGES;  // K ring depth
 constexpr int kVStages = METIS_PF_V_STAGES;  // V ring depth
+constexpr int kV8Stages = 2;      // 8-bit cache: staged e4m3 V tiles
 constexpr int kKvTile = 128;      // tokens per K/V tile
 constexpr int kRows = 128;        // query rows per tile
 constexpr int kTmemCols = 512;    // S0 | S1 | O0 | O1
 constexpr int kSortMax = 2048;    // schedule: heaviest-first sort up to this many items
 
 struct PrefillParams {
+  const void* q;
   const int32_t* cu_q_lens;
   const int32_t* block_table;
   const int32_t* seq_lens;
@@ -114,21 +121,43 @@ struct PrefillParams {
 };
 
 // Shared-memory layout (all tiles 128-byte swizzled, [64-column half][row][128 B]).
-template <int D>
+template <int D, bool KV8>
 struct PfShape {
   static constexpr int kHalves = D / 64;
   static constexpr int kQHalf = kRows * 128;                   // 128 query rows x 64 bf16
   static constexpr int kQBytes = kHalves * kQHalf;             // one query tile
   static constexpr int kKvHalf = kKvTile * 128;                // 128 tokens x 64 bf16
   static constexpr int kKvBytes = kHalves * kKvHalf;
+  // 8-bit cache: K tiles stay e4m3 (rows of D bytes), a query tile is its two e4m3 parts
+  // (the same bytes as bf16), V tiles are converted from staged e4m3 tiles
+  static constexpr int kQPart = kRows * D;
+  static constexpr int kKBytes = KV8 ? kKvTile * D : kKvBytes;
   static constexpr int kQ = 0;                                 // 2 query tiles
   static constexpr int kK = kQ + 2 * kQBytes;                  // kKStages stages
-  static constexpr int kV = kK + kKStages * kKvBytes;          // kVStages stages
-  static constexpr int kTiles = kV + kVStages * kKvBytes;      // 224 KB at head_dim 128
+  static constexpr int kV = kK + kKStages * kKBytes;           // kVStages stages
+  static constexpr int kStage = kV + kVStages * kKvBytes;      // kV8Stages staged e4m3 tiles of V
+  static constexpr int kTiles = kStage + (KV8 ? kV8Stages * kKvTile * D : 0);  // bf16: 224 KB at head_dim 128
   // + 1 KB: the barriers live in the alignment slack (below the aligned base when it
   // is at least 256 B, else just past the tiles).  At least 120 KB so that one CTA
   // (all 512 TMEM columns) is resident per SM.
   static constexpr int kSmem = (kTiles + 1024) > 120 * 1024 ? (kTiles + 1024) : 120 * 1024;
+};
+
+// 8-bit cache, roles of the warps beside the softmax groups, the UMMA issuer (12) and the
+// unit fetcher (14): warp 8 loads K tiles and stages V tiles (TMA); warps 9..11 convert
+// staged V tiles to bf16; warps 9..11, 13 and 15 split a unit's query rows.
+constexpr int kV8Converters = 3;
+constexpr int kQ8Splitters = 5;
+constexpr int kKScaleSlots = 4;  // tiles whose K factors are kept
+
+struct PfFp8Shared {
+  uint64_t stage_full[kV8Stages];   // staged V tile landed
+  uint64_t stage_empty[kV8Stages];  // every converter has read it
+  uint64_t undo_full[2];            // row factors of a unit written
+  uint64_t ks_full[kKScaleSlots];   // K factors of a tile written
+  float ks[kKScaleSlots][8];        // per 16 tokens of a K tile: its page's scale
+  float vs[kV8Stages][8];           // ... of a staged V tile
+  float undo[2][2][kRows];          // [unit parity][query tile][row]: what undoes the row's scaling
 };
 
 // mbarrier layout (indices into the barrier area) and arrival counts
@@ -138,10 +167,12 @@ struct PfBar {
                        kPvDone = kPFull + 2, kDrain = kPvDone + 2, kQFree = kDrain + 1, kUnitFull = kQFree + 1,
                        kUnitEmpty = kUnitFull + 2, kCount = kUnitEmpty + 2;
   // full barriers: one arrival per producer warp of the ring; p_full: 128 softmax threads
-  __host__ __device__ static constexpr int arrivals(int i) {
+  __host__ __device__ static constexpr int arrivals(int i, bool kv8) {
     return (i >= kPFull && i < kPFull + 2) ? 128
-           : ((i >= kKFull && i < kKFull + kKStages) || (i >= kVFull && i < kVFull + kVStages)) ? 2
-           : (i >= kUnitEmpty && i < kUnitEmpty + 2) ? kUnitReaders
+           : (i >= kKFull && i < kKFull + kKStages) ? (kv8 ? 1 : 2)
+           : (i >= kVFull && i < kVFull + kVStages) ? (kv8 ? kV8Converters : 2)
+           : (i == kQFull && kv8) ? kQ8Splitters
+           : (i >= kUnitEmpty && i < kUnitEmpty + 2) ? kUnitReaders + (kv8 ? 1 : 0)
                                                       : 1;
   }
 };
@@ -335,15 +366,17 @@ __device__ __forceinline__ uint4 codes_to_bf16x8(uint32_t w0, uint32_t w1, float
                     pack_bf16x2(b[0] * scale, b[1] * scale), pack_bf16x2(b[2] * scale, b[3] * scale));
 }
 
-// KV8: the cache holds e4m3 codes; the producer warps convert them to bf16 tiles of the
-// same layout, and every other role is the same.
+// KV8: the cache holds e4m3 codes.  K tiles feed the tensor cores as they are, against the
+// query rows split into two e4m3 parts; V tiles are converted to bf16 on the way; a K page's
+// scale joins the softmax factor of its 16 tokens.
 template <int D, bool KV8>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                        const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
                                                                        const PrefillParams p) {
-  using Sh = PfShape<D>;
+  using Sh = PfShape<D, KV8>;
   constexpr int HALVES = Sh::kHalves;
+  constexpr int kStages8 = kV8Stages;
   if (!p.wait_at_exit) pdl_wait();  // the schedule kernel's items are complete and visible
   extern __shared__ uint8_t smem_raw[];
   const uint32_t slack = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -368,6 +401,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + PfBar::kCount + 1);
   volatile int* unit_slot = reinterpret_cast<volatile int*>(bars + PfBar::kCount + 2);  // [2]
   __shared__ PfUnit unit_info[2];  // the published unit, derived once by the fetcher
+  __shared__ PfFp8Shared x8;       // (8-bit cache only)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = __ldcg(p.item_count) * p.G;
@@ -378,7 +412,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
 
   if (threadIdx.x == 0) {
     // full barriers: one arrival per producer warp of the ring; p_full: 128 softmax threads
-    for (int i = 0; i < PfBar::kCount; ++i) mbar_init(&bars[i], PfBar::arrivals(i));
+    for (int i = 0; i < PfBar::kCount; ++i) mbar_init(&bars[i], PfBar::arrivals(i, KV8));
+    if constexpr (KV8) {
+      for (int i = 0; i < kV8Stages; ++i) {
+        mbar_init(&x8.stage_full[i], 1);
+        mbar_init(&x8.stage_empty[i], kV8Converters);
+      }
+      for (int i = 0; i < 2; ++i) mbar_init(&x8.undo_full[i], kQ8Splitters);
+      for (int i = 0; i < kKScaleSlots; ++i) mbar_init(&x8.ks_full[i], 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -425,7 +467,209 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   // Ring positions run on across units: K/V tile t (counted over every unit this
   // CTA has processed) sits in K stage t % kKStages and V stage t % kVStages, and each
   // barrier's phase is the number of its earlier completions.
-  if (warp >= 8 && warp < kMmaWarp) {
+  if (KV8 && warp == 8) {
+    // ------------------------------------------------------------ 8-bit cache: TMA producer
+    regs_dec<kRegsOther8>();
+    const int npg = kKvTile / p.bs;            // pages per K/V tile (2, 4 or 8)
+    const int reps = p.bs >> 4;                // 16-token groups per page
+    const uint64_t pol = l2_policy_evict_last();
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    uint32_t t = 0, k = 0;                     // tiles issued so far, units read
+    bool ok = true;
+    PfUnit it;
+    while (ok && next_unit(k, it) > 0) {
+      const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
+      // page `lane` of tile j: its TMA row (a bad id reads a box out of bounds: zeros) and scales
+      auto page_of = [&](int j, int& rowc, float& fk, float& fv) -> bool {
+        const int pg = j * npg + lane;
+        rowc = -p.bs;
+        fk = fv = 1.f;
+        if (lane >= npg || pg >= it.n_pages) return false;
+        const int b = checked_block(bt_row, pg, p.num_blocks, &g_status_prefill);
+        if (b >= 0) {
+          rowc = b * p.bs;
+          fk = scale_of_byte(__ldg(p.fp8.k_scale + (size_t)b * p.G + it.g));
+          fv = scale_of_byte(__ldg(p.fp8.v_scale + (size_t)b * p.G + it.g));
+        }
+        return true;
+      };
+      int rowc = 0;
+      float fk = 1.f, fv = 1.f;
+      bool live = page_of(0, rowc, fk, fv);
+      for (int j = 0; j < it.n_kv; ++j, ++t) {
+        int next_row = 0;
+        float next_k = 1.f, next_v = 1.f;
+        bool next_live = false;
+        if (j + 1 < it.n_kv) next_live = page_of(j + 1, next_row, next_k, next_v);  // in flight during the waits
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)) * p.bs * D;
+        const int st = t % kKStages, sv = t % kStages8;
+        // K_{t-3} consumed: also every softmax group is past tile t - 4, whose factors sit in this slot
+        if (t >= (uint32_t)kKStages && !wait_all(&k_empty[st], ((t / kKStages) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        if (lane < npg)
+          for (int u = 0; u < reps; ++u) x8.ks[t % kKScaleSlots][lane * reps + u] = fk;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&x8.ks_full[t % kKScaleSlots]);
+          mbar_arrive_expect_tx(&k_full[st], bytes);
+        }
+        __syncwarp();
+        if (live) tma_load_3d(sK + st * Sh::kKBytes + lane * p.bs * D, &tmK, &k_full[st], 0, it.g, rowc, pol);
+        if (t >= (uint32_t)kStages8 && !wait_all(&x8.stage_empty[sv], ((t / kStages8) - 1) & 1)) {
+          ok = false;
+          ++t;  // K of this tile is in flight
+          break;
+        }
+        if (lane < npg)
+          for (int u = 0; u < reps; ++u) x8.vs[sv][lane * reps + u] = fv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&x8.stage_full[sv], bytes);
+        __syncwarp();
+        if (live)
+          tma_load_3d(smem + Sh::kStage + sv * kKvTile * D + lane * p.bs * D, &tmV, &x8.stage_full[sv], 0, it.g, rowc,
+                      pol);
+        rowc = next_row;
+        fk = next_k;
+        fv = next_v;
+        live = next_live;
+      }
+    }
+    if (*abort_flag) {
+      // let the loads still in flight land before the CTA's memory goes away (the limit of
+      // each wait bounds the one on a V tile that was not issued)
+      for (uint32_t i = t > (uint32_t)kKStages ? t - kKStages : 0; i < t; ++i)
+        mbar_wait(&k_full[i % kKStages], (i / kKStages) & 1, &g_status_prefill);
+      for (uint32_t i = t > (uint32_t)kStages8 ? t - kStages8 : 0; i < t; ++i)
+        mbar_wait(&x8.stage_full[i % kStages8], (i / kStages8) & 1, &g_status_prefill);
+    }
+  } else if (KV8 && (warp < kMmaWarp ? warp > 8 : (warp == 13 || warp == 15))) {
+    // ------------------------------------------------------------ 8-bit cache: converters
+    // Per unit: the query rows as two e4m3 parts, q 2^n = hi + lo (n from the row's largest
+    // element, which lands in [2^7, 2^8): exact for bf16 elements down to 2^-8 of it, off by
+    // at most 2^-10 beside 2^7 below that), so that S = (hi + lo) K^T runs on the codes
+    // themselves at twice the bf16 rate, twice.  Warps 9..11 then convert the unit's V tiles.
+    regs_dec<kRegsOther8>();
+    const int cw = warp - 9;                                     // converter of V tiles (0..2), or none
+    const int share = warp == 13 ? 3 : warp == 15 ? 4 : cw;      // of the query rows
+    constexpr int LPR = D / 8, RPP = 32 / LPR;                   // query split: lanes per row, rows per pass
+    constexpr int kBatch = 4;
+    const int tq_log = 31 - __clz(p.Tq);
+    uint32_t t = 0, k = 0;
+    bool ok = true;
+    PfUnit it;
+    while (ok && next_unit(k, it) > 0) {
+      const uint32_t n = k - 1;
+      const int passes = (it.n1 > 0 ? 2 : 1) * kRows / RPP;
+      const int part = lane % LPR;
+      auto load_q = [&](int pass) -> uint4 {
+        const int rr = pass * RPP + lane / LPR, w = rr / kRows, row = rr % kRows;
+        const int hh = row >> tq_log, qi = (2 * it.pair + w) * p.Tq + (row & (p.Tq - 1));
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (pass < passes && qi < it.q_len && it.q0 + qi < p.T)
+          v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                   ((size_t)(it.q0 + qi) * p.H + it.g * p.r + hh) * D) + part);
+        return v;
+      };
+      uint4 v[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) v[u] = load_q(share + u * kQ8Splitters);
+      // the previous unit's query tiles stay until its last QK has completed
+      if (n > 0 && !wait_all(q_free, (n - 1) & 1)) {
+        ok = false;
+        break;
+      }
+#pragma unroll 1
+      for (int p0 = share; p0 < passes; p0 += kBatch * kQ8Splitters) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int pass = p0 + u * kQ8Splitters;
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          v[u] = load_q(pass + kBatch * kQ8Splitters);
+          uint32_t top = 0;  // bf16 magnitudes order like their bits
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max_u16x2(top, x[e] & 0x7fff7fffu);
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top = max(top >> 16, top & 0xffffu);
+          const uint32_t field = max(top >> 7, 8u);  // exponent field of the largest element
+          const float up = __uint_as_float((261u - min(field, 254u)) << 23);
+          const uint64_t up2 = f2_pack(up, up);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint16_t h[2], l[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              const uint32_t w2 = x[2 * e + a];
+              float x0, x1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(w2 << 16), __uint_as_float(w2 & 0xffff0000u)), up2), x0, x1);
+              const __half2 y = __floats2half2_rn(x0, x1);
+              h[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&y));
+              const uint32_t back = f16x2_of_e4m3x2(h[a]);
+              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&back));  // exact
+              l[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
+            }
+            hi[e] = h[0] | ((uint32_t)h[1] << 16);
+            lo[e] = l[0] | ((uint32_t)l[1] << 16);
+          }
+          if (pass < passes) {
+            const int rr = pass * RPP + lane / LPR, w = rr / kRows, row = rr % kRows;
+            const int swz = D == 128 ? (row & 7) : ((row >> 1) & 3);
+            uint8_t* dst = sQ + w * Sh::kQBytes + row * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + Sh::kQPart) = make_uint2(lo[0], lo[1]);
+            // a row with an infinity or NaN gets scores of NaN
+            if (part == 0)
+              x8.undo[n & 1][w][row] = __uint_as_float(field >= 255u ? 0x7fc00000u : (field - 7u) << 23);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&x8.undo_full[n & 1]);
+        mbar_arrive(q_full);
+      }
+      if (warp > kMmaWarp) continue;
+      constexpr int CPR = D / 16, RPC = 32 / CPR;   // V: 16-byte pieces of a row, rows per pass
+      const int piece = lane % CPR;
+      const int flip = D == 128 ? piece >> 2 : 0;   // the two halves' lanes write opposite chunks at a time
+      for (int j = 0; j < it.n_kv; ++j, ++t) {
+        const int sv = t % kStages8, st = t % kVStages;
+        if (!wait_all(&x8.stage_full[sv], (t / kStages8) & 1) ||
+            (t >= (uint32_t)kVStages && !wait_all(&v_empty[st], ((t / kVStages) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(smem + Sh::kStage + sv * kKvTile * D) + lane;
+        uint8_t* tile = sV + st * Sh::kKvBytes + (piece * 16 / 64) * Sh::kKvHalf;
+        const int live_rows = it.L - j * kKvTile;   // rows past the sequence end become zeros
+#pragma unroll 2
+        for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
+          const int row = i * RPC + lane / CPR;
+          uint4 c = src[i * 32];
+          const float f = x8.vs[sv][row >> 4];
+          if (row >= live_rows) c = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 a = codes_to_bf16x8(c.x, c.y, f), b = codes_to_bf16x8(c.z, c.w, f);
+          const int ch = (piece * 2 & 7) + flip;
+          uint8_t* dst = tile + row * 128;
+          *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = flip ? b : a;
+          *reinterpret_cast<uint4*>(dst + (((ch ^ 1) ^ (row & 7)) << 4)) = flip ? a : b;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&x8.stage_empty[sv]);
+          mbar_arrive(&v_full[st]);
+        }
+      }
+    }
+  } else if (warp >= 8 && warp < kMmaWarp) {
     // ------------------------------------------------------------ K/V producers
     regs_dec<kRegsProd>();
     const int pw = warp - 8;
@@ -439,58 +683,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const int half_pg = npg >> 1;              // pages of this warp
     const uint64_t pol = l2_policy_evict_last();
     const int depth = is_k ? kKStages : kVStages;
-    if (!KV8 && lane == 0) tma_prefetch_desc(map);
+    if (lane == 0) tma_prefetch_desc(map);
     uint32_t t = 0, k = 0;                     // tiles issued so far, units read
     bool ok = true;
     PfUnit it;
     while (ok && next_unit(k, it) > 0) {
       const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
-      if constexpr (KV8) {
-        constexpr int CPR = D / 16, RPP = 32 / CPR;  // 16-byte pieces of a row, rows per pass
-        const uint8_t* codes = reinterpret_cast<const uint8_t*>(is_k ? p.fp8.k_cache : p.fp8.v_cache);
-        const uint8_t* bytes = is_k ? p.fp8.k_scale : p.fp8.v_scale;
-        const int piece = lane % CPR;
-        for (int j = 0; ok && j < it.n_kv; ++j, ++t) {
-          const int st = t % depth;
-          if (t >= (uint32_t)depth && !wait_all(&empty[st], ((t / depth) - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t* tile = ring + st * Sh::kKvBytes + (piece * 16 / 64) * Sh::kKvHalf;
-#pragma unroll 1
-          for (int r0 = part * (kKvTile / 2); r0 < (part + 1) * (kKvTile / 2); r0 += 2 * RPP) {
-            uint4 c[2];
-            float f[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int tok = j * kKvTile + r0 + u * RPP + lane / CPR;
-              c[u] = make_uint4(0u, 0u, 0u, 0u);  // rows past the end: zeros
-              f[u] = 1.f;
-              if (tok < it.L) {
-                const int page = tok / p.bs;
-                const int b = checked_block(bt_row, page, p.num_blocks, &g_status_prefill);
-                if (b >= 0) {
-                  const size_t row = (size_t)b * p.bs + (tok - page * p.bs);
-                  c[u] = __ldg(reinterpret_cast<const uint4*>(codes + (row * p.G + it.g) * D) + piece);
-                  f[u] = scale_of_byte(__ldg(bytes + (size_t)b * p.G + it.g));
-                }
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int row = r0 + u * RPP + lane / CPR;
-              const int ch = piece * 2 & 7;  // first of the two 16-byte chunks of the 128-byte row
-              uint8_t* dst = tile + row * 128;
-              *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = codes_to_bf16x8(c[u].x, c[u].y, f[u]);
-              *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) << 4)) = codes_to_bf16x8(c[u].z, c[u].w, f[u]);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[st]);
-        }
-        continue;
-      }
       for (int j = 0; j < it.n_kv; ++j, ++t) {
         const int st = t % depth;
         const int lp = part * half_pg + lane;  // page index inside the tile
@@ -514,26 +712,37 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
                         rowc, pol);
       }
     }
-    if (!KV8 && *abort_flag) {
+    if (*abort_flag) {
       // let the loads still in flight land before the CTA's memory goes away
       for (uint32_t k = t > (uint32_t)depth ? t - depth : 0; k < t; ++k)
         mbar_wait(&full[k % depth], (k / depth) & 1, &g_status_prefill);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ UMMA issuer
-    regs_dec<kRegsMma>();
+    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     constexpr uint32_t kIdQK = umma_idesc_bf16_f32(kRows, kKvTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_bf16_f32(kRows, D, false, true);
     bool issued = false;
     auto qk = [&](int w, uint32_t t) {  // S_w = Q_w K_t^T
       if (lane == 0) {
         const uint32_t qbase = smem_u32(sQ + w * Sh::kQBytes);
-        const uint32_t kbase = smem_u32(sK + (t % kKStages) * Sh::kKvBytes);
+        const uint32_t kbase = smem_u32(sK + (t % kKStages) * Sh::kKBytes);
+        if constexpr (KV8) {  // (hi + lo) codes^T: rows of D bytes, 32 dims per instruction
+          constexpr uint32_t kId8 = umma_idesc_e4m3_f32(kRows, kKvTile);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t within = (kk & 3) * 32;
-          umma_bf16(tmem + w * kKvTile, umma_desc_sw128(qbase + (kk >> 2) * Sh::kQHalf + within, 16, 1024),
-                    umma_desc_sw128(kbase + (kk >> 2) * Sh::kKvHalf + within, 16, 1024), kIdQK, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+            const uint32_t qa = qbase + (kk / (D / 32)) * Sh::kQPart + (kk % (D / 32)) * 32;
+            const uint32_t ka = kbase + (kk % (D / 32)) * 32;
+            umma_e4m3(tmem + w * kKvTile, D == 128 ? umma_desc_sw128(qa, 16, 1024) : umma_desc_sw64(qa, 512),
+                      D == 128 ? umma_desc_sw128(ka, 16, 1024) : umma_desc_sw64(ka, 512), kId8, kk > 0 ? 1u : 0u);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t within = (kk & 3) * 32;
+            umma_bf16(tmem + w * kKvTile, umma_desc_sw128(qbase + (kk >> 2) * Sh::kQHalf + within, 16, 1024),
+                      umma_desc_sw128(kbase + (kk >> 2) * Sh::kKvHalf + within, 16, 1024), kIdQK, kk > 0 ? 1u : 0u);
+          }
         }
         umma_commit(&s_full[w]);
       }
@@ -637,9 +846,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       __syncwarp();
       mbar_wait(drain, 0, &g_status_prefill);
     }
-  } else if (warp == kMmaWarp + 1) {
+  } else if (!KV8 && warp == kMmaWarp + 1) {
     // ------------------------------------------------------------ query loader
-    regs_dec<kRegsMma>();
+    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     if (lane == 0) tma_prefetch_desc(&tmQ);
     uint32_t n_units = 0, k = 0;
     PfUnit it;
@@ -668,7 +877,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // the other warps through the two-slot unit ring; -1 ends the walk.  Unit k is
     // claimed only once every warp has taken unit k - 1: one unit of lookahead, so
     // that at the end of the list no CTA holds small units that an idle CTA could run.
-    regs_dec<kRegsMma>();
+    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     uint32_t k = 0;
     for (;;) {
       const int slot = k & 1;
@@ -692,10 +901,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if (u < 0) break;
     }
   } else if (warp > kMmaWarp) {
-    regs_dec<kRegsMma>();  // idle: give the registers to the softmax groups
+    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();  // idle: give the registers to the softmax groups
   } else {
     // ------------------------------------------------------------ softmax groups
-    regs_inc<kRegsSoftmax>();
+    regs_inc<KV8 ? kRegsSoftmax8 : kRegsSoftmax>();
     const int w = warp >> 2;                    // query tile of this group
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -707,11 +916,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // leaves every exponent equal to the max to fp32 precision (uniform weights)
     const float asl2 = fmaxf(fabsf(sl2), 1e-30f);
     uint32_t ns = 0, npv = 0, k = 0;            // s_full phases consumed, PVs of this group, units read
+    [[maybe_unused]] uint32_t t_base = 0;       // K/V tiles of the units before (8-bit cache)
     bool ok = true;
     PfUnit it;
     while (ok && next_unit(k, it) > 0) {
       const int nkv = w ? it.n1 : it.n0;
+      [[maybe_unused]] const uint32_t t0 = t_base;
+      t_base += it.n_kv;
       if (nkv == 0) continue;                   // no second query tile in this unit
+      [[maybe_unused]] float row_factor = 0.f;  // |sl2| without the query row's scaling
+      if constexpr (KV8) {
+        if (!wait_all(&x8.undo_full[(k - 1) & 1], ((k - 1) >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        row_factor = asl2 * x8.undo[(k - 1) & 1][w][row];
+      }
       const int L = it.L, q_len = it.q_len;
       const int hh = row / p.Tq;
       const int qi0 = (2 * it.pair + w) * p.Tq;
@@ -747,11 +967,33 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           for (int c = 0; c < kKvTile; ++c)
             sv[c] = c < vis ? __float_as_uint(__uint_as_float(sv[c]) * sgn) : 0xff800000u;
         }
+        [[maybe_unused]] float fac[8];  // 8-bit cache: log2 units per unit of S, for each 16 tokens
+        float m_new;
+        if constexpr (KV8) {
+          // (the wait orders this thread after the factors' writer; it has completed by now)
+          const uint32_t slot = (t0 + j) % kKScaleSlots;
+          if (!wait_all(&x8.ks_full[slot], ((t0 + j) / kKScaleSlots) & 1)) {
+            ok = false;
+            break;
+          }
+          float top = m_run;
 #pragma unroll
-        for (int c = 0; c < kKvTile; c += 2)
-          mx[(c >> 1) & 7] = max3f(mx[(c >> 1) & 7], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-        const float mxa = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-        const float m_new = fmaxf(m_run, mxa == -INFINITY ? -INFINITY : mxa * asl2);
+          for (int i = 0; i < 8; ++i) {
+            // > 0, so that a hidden key's -inf stays -inf; NaN passes
+            fac[i] = max_nan(x8.ks[slot][i] * row_factor, 1.17549435e-38f);
+            float g = mx[i];
+#pragma unroll
+            for (int c = 16 * i; c < 16 * i + 16; c += 2) g = max3f(g, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            top = fmaxf(top, g * fac[i]);
+          }
+          m_new = top;
+        } else {
+#pragma unroll
+          for (int c = 0; c < kKvTile; c += 2)
+            mx[(c >> 1) & 7] = max3f(mx[(c >> 1) & 7], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+          const float mxa = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          m_new = fmaxf(m_run, mxa == -INFINITY ? -INFINITY : mxa * asl2);
+        }
         const bool grow = m_new > m_run + 8.0f;   // rescale only when the max grew past 2^8
         float alpha = 1.f;
         if (grow) {
@@ -782,7 +1024,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < kKvTile; c += 2) {
           float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), asl2_2, neg_m2), x0, x1);
+          const uint64_t f2 = KV8 ? f2_pack(fac[KV8 ? c >> 4 : 0], fac[KV8 ? c >> 4 : 0]) : asl2_2;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), f2, neg_m2), x0, x1);
           const float e0 = exp2_approx(x0);
           const float e1 = exp2_approx(x1);
           ls2[(c >> 1) & 3] = f2_add(ls2[(c >> 1) & 3], f2_pack(e0, e1));
@@ -886,17 +1129,17 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   const uint32_t qbox[3] = {64, 1, (uint32_t)p.Tq};
   int rc = encode_tiled(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  if (KV8) {
-    tmK = tmV = tmQ;  // not used: the codes are loaded by the producers' threads
-  } else {
-    const uint64_t kdims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
-    const uint64_t kstr[2] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2};
-    const uint32_t kbox[3] = {64, 1, (uint32_t)p.bs};
-    rc = encode_tiled(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (rc) return rc;
-    rc = encode_tiled(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (rc) return rc;
-  }
+  const uint64_t kdims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
+  constexpr uint64_t kElem = KV8 ? 1 : 2;
+  const uint64_t kstr[2] = {D * kElem, (uint64_t)p.G * D * kElem};
+  const uint32_t kbox[3] = {KV8 ? D : 64, 1, (uint32_t)p.bs};
+  const CUtensorMapDataType kind = KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle k_sw = KV8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  rc = encode_tiled(&tmK, kind, 3, k_cache, kdims, kstr, kbox, k_sw);
+  if (rc) return rc;
+  // staged V codes are read back row by row: plain rows
+  rc = encode_tiled(&tmV, kind, 3, v_cache, kdims, kstr, kbox, KV8 ? CU_TENSOR_MAP_SWIZZLE_NONE : k_sw);
+  if (rc) return rc;
   // a programmatic dependent of the kernel before it (e.g. the paged K/V write): its
   // launch overlaps that kernel's tail
   rc = launch_dependent(prefill_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, "prefill_schedule_kernel launch",
@@ -904,7 +1147,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   if (rc) return rc;
   rc = between(p);
   if (rc) return rc;
-  constexpr int smem = PfShape<D>::kSmem;
+  constexpr int smem = PfShape<D, KV8>::kSmem;
   static int done = 0;
   auto kern = prefill_bf16_kernel<D, KV8>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
@@ -975,6 +1218,7 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   if (max_items * num_kv_heads > 0x7fffffffull) return fail(METIS_E_SHAPE, "too many query tiles");
 
   PrefillParams p{};
+  p.q = q;
   p.cu_q_lens = cu_q_lens;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
