@@ -143,21 +143,20 @@ struct PfShape {
   static constexpr int kSmem = (kTiles + 1024) > 120 * 1024 ? (kTiles + 1024) : 120 * 1024;
 };
 
-// 8-bit cache, roles of the warps beside the softmax groups, the UMMA issuer (12) and the
-// unit fetcher (14): warp 8 loads K tiles and stages V tiles (TMA); warps 9..11 convert
-// staged V tiles to bf16; warps 9..11, 13 and 15 split a unit's query rows.
-constexpr int kV8Converters = 3;
-constexpr int kQ8Splitters = 5;
+// 8-bit cache, roles of the warps that differ: warp 8 loads K tiles and stages V tiles
+// (TMA), warps 9..11 and 15 convert staged V tiles to bf16 (none on the UMMA issuer's
+// scheduler: one there cost 4 %), warp 13 loads the bf16 query rows and the softmax groups
+// split them.
+constexpr int kV8Converters = 4;
 constexpr int kKScaleSlots = 4;  // tiles whose K factors are kept
 
 struct PfFp8Shared {
   uint64_t stage_full[kV8Stages];   // staged V tile landed
   uint64_t stage_empty[kV8Stages];  // every converter has read it
-  uint64_t undo_full[2];            // row factors of a unit written
-  uint64_t ks_full[kKScaleSlots];   // K factors of a tile written
-  float ks[kKScaleSlots][8];        // per 16 tokens of a K tile: its page's scale
+  uint64_t q_raw[2];                // bf16 rows of a query tile landed
+  uint64_t q_full[2];               // ... split into their two e4m3 parts (4 warps)
+  float4 ks[kKScaleSlots][2];       // per 16 tokens of a K tile: its page's scale
   float vs[kV8Stages][8];           // ... of a staged V tile
-  float undo[2][2][kRows];          // [unit parity][query tile][row]: what undoes the row's scaling
 };
 
 // mbarrier layout (indices into the barrier area) and arrival counts
@@ -171,7 +170,6 @@ struct PfBar {
     return (i >= kPFull && i < kPFull + 2) ? 128
            : (i >= kKFull && i < kKFull + kKStages) ? (kv8 ? 1 : 2)
            : (i >= kVFull && i < kVFull + kVStages) ? (kv8 ? kV8Converters : 2)
-           : (i == kQFull && kv8) ? kQ8Splitters
            : (i >= kUnitEmpty && i < kUnitEmpty + 2) ? kUnitReaders + (kv8 ? 1 : 0)
                                                       : 1;
   }
@@ -214,6 +212,10 @@ constexpr int kSchedThreads = 1024;
 // with 7 TFLOP/s per SM the mixed batch above ends its decodes and chunks together).
 constexpr float kDecSmBytesPerS = 75e9f;
 constexpr float kChunkSmFlopsPerS = 7.0e12f;
+// The same two over an 8-bit cache: 226 MB of decodes on 11 SMs took 475 us, and the chunks
+// alone run at 0.94 PFLOP/s.
+constexpr float kDec8SmBytesPerS = 43e9f;
+constexpr float kChunk8SmFlopsPerS = 5.8e12f;
 
 __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const PrefillParams p, int4* items,
                                                                           int* count, int max_items) {
@@ -268,15 +270,17 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
   if (p.dec_ctas && warp == kSchedThreads / 32 - 1) {
     // SMs for the decodes beside the chunks: decodes on k SMs and chunks on the
     // other N - k finish together when k / N = d / (d + c), with d and c the SM time
-    // each kind needs alone (rates of one SM: kDecSmBytesPerS, kChunkSmFlopsPerS)
+    // each kind needs alone (rates of one SM: kDecSmBytesPerS, kChunkSmFlopsPerS): K and V
+    // rows of every decode, QK^T and PV of every chunk query
     long long dt = red[0][lane], cq = red[1][lane];
     for (int o = 16; o > 0; o >>= 1) {
       dt += __shfl_xor_sync(0xffffffffu, dt, o);
       cq += __shfl_xor_sync(0xffffffffu, cq, o);
     }
     if (lane == 0) {
-      const float d = (float)dt * ((float)p.kv_token_bytes / kDecSmBytesPerS);   // K and V rows of every decode
-      const float c = (float)cq * ((float)p.H * p.D * 4.0f / kChunkSmFlopsPerS);  // QK^T and PV of every chunk query
+      const bool kv8 = p.fp8.k_cache != nullptr;
+      const float d = (float)dt * ((float)p.kv_token_bytes / (kv8 ? kDec8SmBytesPerS : kDecSmBytesPerS));  // K, V rows
+      const float c = (float)cq * ((float)p.H * p.D * 4.0f / (kv8 ? kChunk8SmFlopsPerS : kChunkSmFlopsPerS));
       int k = 0;
       if (dt > 0) k = cq > 0 ? (int)ceilf(p.num_sms * (d / (d + c))) : p.num_sms;
       *p.dec_ctas = min(max(k, dt > 0 ? 1 : 0), p.num_sms);
@@ -366,6 +370,58 @@ __device__ __forceinline__ uint4 codes_to_bf16x8(uint32_t w0, uint32_t w1, float
                     pack_bf16x2(b[0] * scale, b[1] * scale), pack_bf16x2(b[2] * scale, b[3] * scale));
 }
 
+// 8-bit cache: the query row `row` of a 128-row bf16 tile as two e4m3 parts, q up = hi + lo, so
+// that S = (hi + lo) codes^T runs on the codes themselves at twice the bf16 rate, twice.  up
+// is a power of two that brings the row's largest element into [2^7, 2^8): the parts are
+// exact for elements down to 2^-8 of it and off by at most 2^-10 (of 2^7) below that.
+// In place, one thread per row: the row's bytes of hi go over its first 128-byte half and
+// those of lo over the second (head_dim 64: both into its one 128 bytes).  Returns 1 / up,
+// or NaN for a row with an infinity or NaN (its scores are NaN).
+template <int D>
+__device__ __forceinline__ float split_query_row(uint8_t* tile, int row) {
+  constexpr int kChunks = D / 8;  // 16-byte chunks of the bf16 row
+  uint8_t* at = tile + row * 128;
+  uint4 v[kChunks];
+  uint32_t top = 0;               // bf16 magnitudes order like their bits
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    v[c] = *reinterpret_cast<const uint4*>(at + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4));
+    top = max_u16x2(max_u16x2(top, v[c].x & 0x7fff7fffu), v[c].y & 0x7fff7fffu);
+    top = max_u16x2(max_u16x2(top, v[c].z & 0x7fff7fffu), v[c].w & 0x7fff7fffu);
+  }
+  top = max(top >> 16, top & 0xffffu);
+  const uint32_t field = max(top >> 7, 8u);  // exponent field of the largest element
+  const float up = __uint_as_float((261u - min(field, 254u)) << 23);
+  const uint64_t up2 = f2_pack(up, up);
+#pragma unroll
+  for (int c = 0; c < kChunks; c += 2) {
+    uint32_t hi[4], lo[4];
+    const uint32_t x[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint16_t h[2], l[2];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const uint32_t w2 = x[2 * e + a];
+        float x0, x1;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(w2 << 16), __uint_as_float(w2 & 0xffff0000u)), up2), x0, x1);
+        const __half2 y = __floats2half2_rn(x0, x1);
+        h[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&y));
+        const uint32_t back = f16x2_of_e4m3x2(h[a]);
+        const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&back));  // exact
+        l[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
+      }
+      hi[e] = h[0] | ((uint32_t)h[1] << 16);
+      lo[e] = l[0] | ((uint32_t)l[1] << 16);
+    }
+    const int o = c / 2;  // output chunk of the row
+    *reinterpret_cast<uint4*>(at + ((o ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    uint8_t* lo_at = D == 128 ? at + kRows * D + ((o ^ (row & 7)) << 4) : at + (((4 + o) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  return __uint_as_float(field >= 255u ? 0x7fc00000u : (field - 7u) << 23);
+}
+
 // KV8: the cache holds e4m3 codes.  K tiles feed the tensor cores as they are, against the
 // query rows split into two e4m3 parts; V tiles are converted to bf16 on the way; a K page's
 // scale joins the softmax factor of its 16 tokens.
@@ -418,8 +474,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         mbar_init(&x8.stage_full[i], 1);
         mbar_init(&x8.stage_empty[i], kV8Converters);
       }
-      for (int i = 0; i < 2; ++i) mbar_init(&x8.undo_full[i], kQ8Splitters);
-      for (int i = 0; i < kKScaleSlots; ++i) mbar_init(&x8.ks_full[i], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&x8.q_raw[i], 1);
+        mbar_init(&x8.q_full[i], 4);
+      }
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -512,12 +570,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           break;
         }
         if (lane < npg)
-          for (int u = 0; u < reps; ++u) x8.ks[t % kKScaleSlots][lane * reps + u] = fk;
+          for (int u = 0; u < reps; ++u)
+            reinterpret_cast<float*>(x8.ks[t % kKScaleSlots])[lane * reps + u] = fk;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&x8.ks_full[t % kKScaleSlots]);
-          mbar_arrive_expect_tx(&k_full[st], bytes);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
         __syncwarp();
         if (live) tma_load_3d(sK + st * Sh::kKBytes + lane * p.bs * D, &tmK, &k_full[st], 0, it.g, rowc, pol);
         if (t >= (uint32_t)kStages8 && !wait_all(&x8.stage_empty[sv], ((t / kStages8) - 1) & 1)) {
@@ -547,95 +603,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       for (uint32_t i = t > (uint32_t)kStages8 ? t - kStages8 : 0; i < t; ++i)
         mbar_wait(&x8.stage_full[i % kStages8], (i / kStages8) & 1, &g_status_prefill);
     }
-  } else if (KV8 && (warp < kMmaWarp ? warp > 8 : (warp == 13 || warp == 15))) {
-    // ------------------------------------------------------------ 8-bit cache: converters
-    // Per unit: the query rows as two e4m3 parts, q 2^n = hi + lo (n from the row's largest
-    // element, which lands in [2^7, 2^8): exact for bf16 elements down to 2^-8 of it, off by
-    // at most 2^-10 beside 2^7 below that), so that S = (hi + lo) K^T runs on the codes
-    // themselves at twice the bf16 rate, twice.  Warps 9..11 then convert the unit's V tiles.
+  } else if (KV8 && ((warp > 8 && warp < kMmaWarp) || warp == 15)) {
+    // ------------------------------------------------------------ 8-bit cache: V converters
     regs_dec<kRegsOther8>();
-    const int cw = warp - 9;                                     // converter of V tiles (0..2), or none
-    const int share = warp == 13 ? 3 : warp == 15 ? 4 : cw;      // of the query rows
-    constexpr int LPR = D / 8, RPP = 32 / LPR;                   // query split: lanes per row, rows per pass
-    constexpr int kBatch = 4;
-    const int tq_log = 31 - __clz(p.Tq);
+    const int cw = warp == 15 ? 3 : warp - 9;
     uint32_t t = 0, k = 0;
     bool ok = true;
     PfUnit it;
     while (ok && next_unit(k, it) > 0) {
-      const uint32_t n = k - 1;
-      const int passes = (it.n1 > 0 ? 2 : 1) * kRows / RPP;
-      const int part = lane % LPR;
-      auto load_q = [&](int pass) -> uint4 {
-        const int rr = pass * RPP + lane / LPR, w = rr / kRows, row = rr % kRows;
-        const int hh = row >> tq_log, qi = (2 * it.pair + w) * p.Tq + (row & (p.Tq - 1));
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (pass < passes && qi < it.q_len && it.q0 + qi < p.T)
-          v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                   ((size_t)(it.q0 + qi) * p.H + it.g * p.r + hh) * D) + part);
-        return v;
-      };
-      uint4 v[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) v[u] = load_q(share + u * kQ8Splitters);
-      // the previous unit's query tiles stay until its last QK has completed
-      if (n > 0 && !wait_all(q_free, (n - 1) & 1)) {
-        ok = false;
-        break;
-      }
-#pragma unroll 1
-      for (int p0 = share; p0 < passes; p0 += kBatch * kQ8Splitters) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int pass = p0 + u * kQ8Splitters;
-          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          v[u] = load_q(pass + kBatch * kQ8Splitters);
-          uint32_t top = 0;  // bf16 magnitudes order like their bits
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max_u16x2(top, x[e] & 0x7fff7fffu);
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
-          top = max(top >> 16, top & 0xffffu);
-          const uint32_t field = max(top >> 7, 8u);  // exponent field of the largest element
-          const float up = __uint_as_float((261u - min(field, 254u)) << 23);
-          const uint64_t up2 = f2_pack(up, up);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint16_t h[2], l[2];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              const uint32_t w2 = x[2 * e + a];
-              float x0, x1;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(w2 << 16), __uint_as_float(w2 & 0xffff0000u)), up2), x0, x1);
-              const __half2 y = __floats2half2_rn(x0, x1);
-              h[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&y));
-              const uint32_t back = f16x2_of_e4m3x2(h[a]);
-              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&back));  // exact
-              l[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
-            }
-            hi[e] = h[0] | ((uint32_t)h[1] << 16);
-            lo[e] = l[0] | ((uint32_t)l[1] << 16);
-          }
-          if (pass < passes) {
-            const int rr = pass * RPP + lane / LPR, w = rr / kRows, row = rr % kRows;
-            const int swz = D == 128 ? (row & 7) : ((row >> 1) & 3);
-            uint8_t* dst = sQ + w * Sh::kQBytes + row * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + Sh::kQPart) = make_uint2(lo[0], lo[1]);
-            // a row with an infinity or NaN gets scores of NaN
-            if (part == 0)
-              x8.undo[n & 1][w][row] = __uint_as_float(field >= 255u ? 0x7fc00000u : (field - 7u) << 23);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&x8.undo_full[n & 1]);
-        mbar_arrive(q_full);
-      }
-      if (warp > kMmaWarp) continue;
       constexpr int CPR = D / 16, RPC = 32 / CPR;   // V: 16-byte pieces of a row, rows per pass
       const int piece = lane % CPR;
       const int flip = D == 128 ? piece >> 2 : 0;   // the two halves' lanes write opposite chunks at a time
@@ -649,7 +624,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         const uint4* src = reinterpret_cast<const uint4*>(smem + Sh::kStage + sv * kKvTile * D) + lane;
         uint8_t* tile = sV + st * Sh::kKvBytes + (piece * 16 / 64) * Sh::kKvHalf;
         const int live_rows = it.L - j * kKvTile;   // rows past the sequence end become zeros
-#pragma unroll 2
+#pragma unroll 1
         for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
           const int row = i * RPC + lane / CPR;
           uint4 c = src[i * 32];
@@ -717,6 +692,111 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       for (uint32_t k = t > (uint32_t)depth ? t - depth : 0; k < t; ++k)
         mbar_wait(&full[k % depth], (k / depth) & 1, &g_status_prefill);
     }
+  } else if (KV8 && warp == kMmaWarp) {
+    // ------------------------------------------------------------ 8-bit cache: UMMA issuer
+    // The same order of products as below, PV0_j, QK0_{j+1}, PV1_j, QK1_{j+1}.  Everything
+    // the instructions' operands come from is kept uniform over the warp (values from
+    // shared memory by shuffle, outcomes of waits by vote, ring positions counted instead
+    // of divided), so that descriptors are built on the uniform datapath.
+    regs_dec<kRegsOther8>();
+    constexpr uint32_t kIdQK = umma_idesc_e4m3_f32(kRows, kKvTile);
+    constexpr uint32_t kIdPV = umma_idesc_bf16_f32(kRows, D, false, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
+    const uint32_t k_at = __shfl_sync(0xffffffffu, smem_u32(sK), 0);
+    const uint32_t v_at = __shfl_sync(0xffffffffu, smem_u32(sV), 0);
+    uint32_t k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;   // next K and V tile: ring stage, phase parity
+    uint32_t p_ph[2] = {0u, 0u}, u = 0, n_two = 0;     // p_full parities; units; units with two query tiles
+    bool ok = true, issued = false;
+    auto qk = [&](int w) {  // S_w = (hi_w + lo_w) codes^T of the K tile in stage k_st, 32 dims per instruction
+      const uint32_t a = q_at + w * Sh::kQBytes, b = k_at + k_st * Sh::kKBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+          const uint32_t qa = a + (kk / (D / 32)) * (D == 128 ? Sh::kQPart : 64) + (kk % (D / 32)) * 32;
+          const uint32_t ka = b + (kk % (D / 32)) * 32;
+          umma_e4m3(tm + w * kKvTile, umma_desc_sw128(qa, 16, 1024),
+                    D == 128 ? umma_desc_sw128(ka, 16, 1024) : umma_desc_sw64(ka, 512), kIdQK, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[w]);
+      }
+    };
+    auto pv = [&](int w, uint32_t add) {  // O_w (+)= P_w V of the V tile in stage v_st, P_w over S_w's first columns
+      const uint32_t b = v_at + v_st * Sh::kKvBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kKvTile / 16; ++kk)
+          umma_bf16_tmem_a(tm + 2 * kKvTile + w * D, tm + w * kKvTile + kk * 8,
+                           umma_desc_sw128(b + kk * 2048, Sh::kKvHalf, 1024), kIdPV, kk > 0 ? 1u : add);
+        umma_commit(&pv_done[w]);
+      }
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+    };
+    for (;; ++u) {
+      const int slot = u & 1;
+      if (!(ok = wait_all(&unit_full[slot], (u >> 1) & 1))) break;
+      const int index = __shfl_sync(0xffffffffu, unit_slot[slot], 0);
+      const int n0 = __shfl_sync(0xffffffffu, unit_info[slot].n0, 0);
+      const int n1 = __shfl_sync(0xffffffffu, unit_info[slot].n1, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[slot]);  // release: the reads above are done
+      if (index < 0) break;
+      const int n_kv = max(n0, n1);
+      if (!(ok = wait_all(&x8.q_full[0], u & 1) && wait_all(&k_full[k_st], k_ph))) break;
+      tc_fence_after_sync();
+      issued = true;
+      qk(0);
+      if (n1 > 0) {
+        if (!(ok = wait_all(&x8.q_full[1], n_two & 1))) break;
+        ++n_two;
+        tc_fence_after_sync();
+        qk(1);
+      }
+      commit(&k_empty[k_st]);
+      if (n_kv == 1) commit(q_free);  // the unit's last QK is issued
+      if (++k_st == kKStages) k_st = 0, k_ph ^= 1;
+      for (int j = 0; j < n_kv; ++j) {
+        if (!(ok = wait_all(&v_full[v_st], v_ph))) break;
+        const bool more = j + 1 < n_kv;
+        bool k_ready = false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int nw = w ? n1 : n0;
+          if (j < nw) {
+            if (!(ok = wait_all(&p_full[w], p_ph[w]))) break;
+            p_ph[w] ^= 1;
+            tc_fence_after_sync();
+            pv(w, j > 0 ? 1u : 0u);
+            // the V stage is free once the last PV of this tile has run
+            if (w == 1 || n1 <= j) commit(&v_empty[v_st]);
+          }
+          if (j + 1 < nw) {
+            if (!k_ready) {  // K_{t+1} is waited for only after PV0_t is on its way
+              if (!(ok = wait_all(&k_full[k_st], k_ph))) break;
+              tc_fence_after_sync();
+              k_ready = true;
+            }
+            qk(w);
+          }
+        }
+        if (!ok) break;
+        if (more) {
+          commit(&k_empty[k_st]);
+          if (j + 2 == n_kv) commit(q_free);  // the unit's last QK is issued
+          if (++k_st == kKStages) k_st = 0, k_ph ^= 1;
+        }
+        if (++v_st == kVStages) v_st = 0, v_ph ^= 1;
+      }
+      if (!ok) break;
+    }
+    if (!ok && issued) {
+      // wait (bounded) for every UMMA this warp issued before TMEM is freed
+      commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, &g_status_prefill);
+    }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ UMMA issuer
     regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
@@ -727,22 +807,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if (lane == 0) {
         const uint32_t qbase = smem_u32(sQ + w * Sh::kQBytes);
         const uint32_t kbase = smem_u32(sK + (t % kKStages) * Sh::kKBytes);
-        if constexpr (KV8) {  // (hi + lo) codes^T: rows of D bytes, 32 dims per instruction
-          constexpr uint32_t kId8 = umma_idesc_e4m3_f32(kRows, kKvTile);
 #pragma unroll
-          for (int kk = 0; kk < 2 * (D / 32); ++kk) {
-            const uint32_t qa = qbase + (kk / (D / 32)) * Sh::kQPart + (kk % (D / 32)) * 32;
-            const uint32_t ka = kbase + (kk % (D / 32)) * 32;
-            umma_e4m3(tmem + w * kKvTile, D == 128 ? umma_desc_sw128(qa, 16, 1024) : umma_desc_sw64(qa, 512),
-                      D == 128 ? umma_desc_sw128(ka, 16, 1024) : umma_desc_sw64(ka, 512), kId8, kk > 0 ? 1u : 0u);
-          }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t within = (kk & 3) * 32;
-            umma_bf16(tmem + w * kKvTile, umma_desc_sw128(qbase + (kk >> 2) * Sh::kQHalf + within, 16, 1024),
-                      umma_desc_sw128(kbase + (kk >> 2) * Sh::kKvHalf + within, 16, 1024), kIdQK, kk > 0 ? 1u : 0u);
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t within = (kk & 3) * 32;
+          umma_bf16(tmem + w * kKvTile, umma_desc_sw128(qbase + (kk >> 2) * Sh::kQHalf + within, 16, 1024),
+                    umma_desc_sw128(kbase + (kk >> 2) * Sh::kKvHalf + within, 16, 1024), kIdQK, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[w]);
       }
@@ -791,7 +860,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
         tc_fence_after_sync();
         const int tok0 = j * kKvTile;
-        if (!KV8 && tok0 + kKvTile > it.L) {  // (the converted tiles hold zeros there)
+        if (tok0 + kKvTile > it.L) {
           // rows past the sequence end may hold anything (NaN included): zero them so that P = 0 stays 0
           uint8_t* vb = sV + vst * Sh::kKvBytes;
           for (int row = (it.L - tok0) + lane; row < kKvTile; row += 32)
@@ -846,31 +915,36 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       __syncwarp();
       mbar_wait(drain, 0, &g_status_prefill);
     }
-  } else if (!KV8 && warp == kMmaWarp + 1) {
+  } else if (warp == kMmaWarp + 1) {
     // ------------------------------------------------------------ query loader
     regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     if (lane == 0) tma_prefetch_desc(&tmQ);
-    uint32_t n_units = 0, k = 0;
+    uint32_t n_units = 0, n_two = 0, k = 0;
     PfUnit it;
     while (next_unit(k, it) > 0) {
       // the previous unit's query tiles stay until its last QK has completed
       if (n_units > 0 && !wait_all(q_free, (n_units - 1) & 1)) break;
+      const int ntiles = it.n1 > 0 ? 2 : 1;
       if (lane == 0) {
-        const int ntiles = it.n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(ntiles * Sh::kQBytes));
+        if (!KV8) mbar_arrive_expect_tx(q_full, (uint32_t)(ntiles * Sh::kQBytes));
         const uint64_t pol = l2_policy_evict_first();
         for (int w = 0; w < ntiles; ++w) {
+          if (KV8) mbar_arrive_expect_tx(&x8.q_raw[w], (uint32_t)Sh::kQBytes);
           const int qi0 = (2 * it.pair + w) * p.Tq;
           for (int hh = 0; hh < p.r; ++hh)
             for (int h = 0; h < HALVES; ++h)
-              tma_load_3d(sQ + w * Sh::kQBytes + h * Sh::kQHalf + hh * p.Tq * 128, &tmQ, q_full, h * 64,
-                          it.g * p.r + hh, it.q0 + qi0, pol);
+              tma_load_3d(sQ + w * Sh::kQBytes + h * Sh::kQHalf + hh * p.Tq * 128, &tmQ, KV8 ? &x8.q_raw[w] : q_full,
+                          h * 64, it.g * p.r + hh, it.q0 + qi0, pol);
         }
       }
       __syncwarp();
       ++n_units;
+      n_two += ntiles - 1;
     }
-    if (*abort_flag && n_units > 0) mbar_wait(q_full, (n_units - 1) & 1, &g_status_prefill);
+    if (*abort_flag && n_units > 0) {
+      mbar_wait(KV8 ? &x8.q_raw[0] : q_full, (n_units - 1) & 1, &g_status_prefill);
+      if (KV8 && n_two > 0) mbar_wait(&x8.q_raw[1], (n_two - 1) & 1, &g_status_prefill);
+    }
   } else if (warp == kMmaWarp + 2) {
     // ------------------------------------------------------------ unit fetcher
     // claims units from the global list, heaviest first, and publishes them to
@@ -916,21 +990,44 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // leaves every exponent equal to the max to fp32 precision (uniform weights)
     const float asl2 = fmaxf(fabsf(sl2), 1e-30f);
     uint32_t ns = 0, npv = 0, k = 0;            // s_full phases consumed, PVs of this group, units read
-    [[maybe_unused]] uint32_t t_base = 0;       // K/V tiles of the units before (8-bit cache)
     bool ok = true;
     PfUnit it;
-    while (ok && next_unit(k, it) > 0) {
+    // 8-bit cache: a unit is taken, and its query rows are split, before the unit in front
+    // of it is written out, so that the tensor cores have the next QK meanwhile.
+    [[maybe_unused]] uint32_t t_base = 0, n_split = 0;  // K/V tiles of the units before, query tiles split
+    [[maybe_unused]] float row_factor = 0.f, next_factor = 0.f;  // |sl2| without the query row's scaling
+    [[maybe_unused]] bool have = false;
+    [[maybe_unused]] PfUnit next;
+    [[maybe_unused]] auto advance = [&]() {
+      have = next_unit(k, next) > 0;
+      if (!have || (w ? next.n1 : next.n0) == 0) return;
+      if (!wait_all(&x8.q_raw[w], n_split & 1)) {
+        ok = false;
+        return;
+      }
+      ++n_split;
+      next_factor = asl2 * split_query_row<D>(sQ + w * Sh::kQBytes, row);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x8.q_full[w]);
+    };
+    if constexpr (KV8) advance();
+    auto take = [&]() -> bool {
+      if constexpr (KV8) {
+        it = next;
+        row_factor = next_factor;
+        return have;
+      } else {
+        return next_unit(k, it) > 0;
+      }
+    };
+    while (ok && take()) {
       const int nkv = w ? it.n1 : it.n0;
       [[maybe_unused]] const uint32_t t0 = t_base;
       t_base += it.n_kv;
-      if (nkv == 0) continue;                   // no second query tile in this unit
-      [[maybe_unused]] float row_factor = 0.f;  // |sl2| without the query row's scaling
-      if constexpr (KV8) {
-        if (!wait_all(&x8.undo_full[(k - 1) & 1], ((k - 1) >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        row_factor = asl2 * x8.undo[(k - 1) & 1][w][row];
+      if (nkv == 0) {                           // no second query tile in this unit
+        if constexpr (KV8) advance();
+        continue;
       }
       const int L = it.L, q_len = it.q_len;
       const int hh = row / p.Tq;
@@ -970,22 +1067,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         [[maybe_unused]] float fac[8];  // 8-bit cache: log2 units per unit of S, for each 16 tokens
         float m_new;
         if constexpr (KV8) {
-          // (the wait orders this thread after the factors' writer; it has completed by now)
-          const uint32_t slot = (t0 + j) % kKScaleSlots;
-          if (!wait_all(&x8.ks_full[slot], ((t0 + j) / kKScaleSlots) & 1)) {
-            ok = false;
-            break;
+          // (written before the K tile's barrier, which the UMMA issuer waited for before S)
+          const float4 f0 = x8.ks[(t0 + j) % kKScaleSlots][0], f1 = x8.ks[(t0 + j) % kKScaleSlots][1];
+          const float ks[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fac[i] = ks[i] * row_factor;
+          if (!lean) {
+            // > 0, so that a hidden key's -inf stays -inf; NaN passes
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fac[i] = max_nan(fac[i], 1.17549435e-38f);
           }
           float top = m_run;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            // > 0, so that a hidden key's -inf stays -inf; NaN passes
-            fac[i] = max_nan(x8.ks[slot][i] * row_factor, 1.17549435e-38f);
             float g = mx[i];
 #pragma unroll
             for (int c = 16 * i; c < 16 * i + 16; c += 2) g = max3f(g, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            top = fmaxf(top, g * fac[i]);
+            mx[i] = g * fac[i];
           }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) top = max3f(top, mx[i], mx[i + 1]);
           m_new = top;
         } else {
 #pragma unroll
@@ -1042,6 +1143,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
+      if constexpr (KV8) {
+        advance();
+        if (!ok) break;
+      }
       npv += nkv;
       if (!wait_all(&pv_done[w], (npv - 1) & 1)) {
         ok = false;
