@@ -41,7 +41,8 @@ static void load_encode() {
 }
 
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
-                 const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+                 const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                 CUtensorMapL2promotion promotion) {
   std::call_once(g_encode_once, load_encode);
   if (!g_encode) return fail(METIS_E_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(g_encode_err));
   cuuint64_t d[5];
@@ -55,7 +56,7 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const vo
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
   CUresult r = g_encode(map, dtype, rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(METIS_E_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   return METIS_OK;
 }

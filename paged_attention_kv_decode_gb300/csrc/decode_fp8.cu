@@ -385,41 +385,56 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
   return ok;
 }
 
-// Warps per CTA and ring depth per warp.
-constexpr int kFp8Warps = 4;
-constexpr int kFp8Stages = 3;
+// Warps per CTA, ring depth per warp and CTAs per SM that the registers allow.  Measured on a
+// GB300 (32/8 heads, head_dim 128, pages of 16):
+//   unsplit        4 warps, 3 stages, two CTAs per SM: 64 sequences of 512..4096 tokens in
+//                  55.6 us; 4 warps, 2 stages, three CTAs 64.6 us (fewer bytes in flight
+//                  once the long sequences are alone), one warp 118 us
+//   many partitions  one warp and 2 stages, twelve CTAs per SM: nothing to combine, and a
+//                  partition's start-up (block ids, scales, query) hides behind eleven others:
+//                  8 sequences of 32-128 K in 512-token partitions 245 us, 4 warps 361 us
+//   few partitions  4 warps, 2 stages, three CTAs per SM: 29 sequences up to 6,000 tokens in
+//                  1,024-token partitions, 28/4 heads, 28 us; two CTAs 34 us, one warp 45 us
+template <int NW_, int STAGES_, int MIN_CTAS_>
+struct Fp8Plan {
+  static constexpr int NW = NW_, STAGES = STAGES_, MIN_CTAS = MIN_CTAS_;
+};
+using Fp8Unsplit = Fp8Plan<4, 3, 2>;
+using Fp8ManyParts = Fp8Plan<1, 2, 12>;
+using Fp8FewParts = Fp8Plan<4, 2, 3>;
 
-template <int D, typename QT, int NW, int STAGES>
-__global__ void __launch_bounds__(NW * 32) decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK,
+template <int D, typename QT, typename Plan>
+__global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
                                                               const DecodeFp8Params pp) {
+  constexpr int NW = Plan::NW, STAGES = Plan::STAGES;
   constexpr int STAGE_BYTES = Fp8DecodeShape<D>::kStageBytes;
   static_assert(NW * (64 + D * 32) <= NW * STAGES * STAGE_BYTES, "combine area must fit in the ring");
   const DecodeParams& p = pp.d;
-  pdl_wait();  // inputs are read after the previous grid in the stream has completed
-  pdl_launch_dependents();
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
   float4* scales = reinterpret_cast<float4*>(smem + NW * STAGES * STAGE_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(scales + NW * STAGES);
-
-  __shared__ int rank_lens[kMaxRankSeqs];
-  __shared__ int rank_found;
-  const int part = blockIdx.x, g = blockIdx.y;
-  const int s = (p.partition_size == 0 && p.S <= kMaxRankSeqs) ? seq_of_rank(p, blockIdx.z, rank_lens, &rank_found)
-                                                                : (int)blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int t0, t1;
-  if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
-
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     for (int i = 0; i < NW * STAGES; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
-  __syncthreads();
+  pdl_wait();  // inputs are read after the previous grid in the stream has completed
+  pdl_launch_dependents();
+
+  __shared__ int rank_lens[kMaxRankSeqs];
+  __shared__ int rank_found;
+  // KV heads vary fastest: the CTAs that read one page's rows (all heads of a token lie side
+  // by side) run at about the same time
+  const int part = blockIdx.x / p.G, g = blockIdx.x - part * p.G;
+  const int s = (p.partition_size == 0 && p.S <= kMaxRankSeqs) ? seq_of_rank(p, blockIdx.y, rank_lens, &rank_found)
+                                                                : (int)blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int t0, t1;
+  if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
+  __syncthreads();  // the barriers are initialised
   int kb = 0;
   decode_fp8_item<D, QT, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
                                      kb, [] { __syncthreads(); });
@@ -430,6 +445,7 @@ __global__ void __launch_bounds__(NW * 32) decode_fp8_kernel(const __grid_consta
 // decode_rows_beside_kernel (decode.cu)
 // ---------------------------------------------------------------------------
 constexpr int kDec8Groups = 2;
+constexpr int kFp8Warps = 4, kFp8Stages = 3;  // per group
 
 template <int D>
 constexpr int dec8_beside_smem_bytes() {
@@ -537,23 +553,38 @@ static int encode_kv8_maps(const DecodeParams& p, const void* k_cache, const voi
   const uint64_t strides[2] = {(uint64_t)D, (uint64_t)p.G * D};
   const uint32_t box[3] = {(uint32_t)D, 1, (uint32_t)std::min(p.bs, kUnit8)};
   const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  int rc = encode_tiled(tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_cache, dims, strides, box, sw);
+  // a row is 64 or 128 bytes: promoting its fetches to 256 would bring the next head's along,
+  // whose own fetch may come too late to use it (2 % slower)
+  const CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  int rc = encode_tiled(tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_cache, dims, strides, box, sw, promo);
   if (rc) return rc;
-  return encode_tiled(tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_cache, dims, strides, box, sw);
+  return encode_tiled(tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_cache, dims, strides, box, sw, promo);
 }
 
-template <int D, typename QT>
-static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, dim3 grid,
-                      cudaStream_t st) {
+template <int D, typename QT, typename Plan>
+static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st) {
   CUtensorMap tmK, tmV;
   int rc = encode_kv8_maps<D>(pp.d, k_cache, v_cache, &tmK, &tmV);
   if (rc) return rc;
-  constexpr int smem = fp8_decode_smem_bytes<D, kFp8Warps, kFp8Stages>();
+  constexpr int smem = fp8_decode_smem_bytes<D, Plan::NW, Plan::STAGES>();
   static int done = 0;
-  auto kern = decode_fp8_kernel<D, QT, kFp8Warps, kFp8Stages>;
+  auto kern = decode_fp8_kernel<D, QT, Plan>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
-  return launch_dependent(kern, grid, dim3(kFp8Warps * 32), (size_t)smem, st, "decode_fp8_kernel launch", tmK, tmV, pp);
+  const dim3 grid((unsigned)pp.d.max_parts * (unsigned)pp.d.G, (unsigned)pp.d.S);
+  return launch_dependent(kern, grid, dim3(Plan::NW * 32), (size_t)smem, st, "decode_fp8_kernel launch", tmK, tmV, pp);
+}
+
+// Partitions a launch may hold before one warp each is enough to fill the GPU: twelve on
+// each of 152 SMs, twice over (seq_lens are not known here: the bound counts max_seq_len).
+constexpr long long kManyParts = 2 * 12 * 152;
+
+template <int D, typename QT>
+static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st) {
+  const DecodeParams& p = pp.d;
+  if (p.partition_size == 0) return launch_fp8<D, QT, Fp8Unsplit>(pp, k_cache, v_cache, st);
+  if ((long long)p.max_parts * p.G * p.S >= kManyParts) return launch_fp8<D, QT, Fp8ManyParts>(pp, k_cache, v_cache, st);
+  return launch_fp8<D, QT, Fp8FewParts>(pp, k_cache, v_cache, st);
 }
 
 template <int D>
@@ -644,7 +675,7 @@ extern "C" int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, c
 
   const int eff_len = effective_max_len(max_seq_len, max_blocks, block_size);
   const size_t parts = split_parts(eff_len, partition_size);
-  if (parts > 0x7fffffff) return fail(METIS_E_SHAPE, "too many partitions");
+  if (parts > 0x7fffffff / (size_t)num_kv_heads) return fail(METIS_E_SHAPE, "too many partitions");
   const size_t need = metis_decode_workspace_bytes(num_seqs, num_heads, head_dim, eff_len, partition_size);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return fail(METIS_E_WORKSPACE, "workspace must hold %zu bytes (256-byte aligned)", need);
@@ -662,14 +693,13 @@ extern "C" int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, c
                                           align_up(units * head_dim * sizeof(float), 256));
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)p.max_parts, (unsigned)num_kv_heads, (unsigned)num_seqs);
   int rc;
   if (dtype == METIS_F32)
-    rc = head_dim == 64 ? launch_fp8<64, float>(pp, k_cache, v_cache, grid, st)
-                        : launch_fp8<128, float>(pp, k_cache, v_cache, grid, st);
+    rc = head_dim == 64 ? launch_fp8<64, float>(pp, k_cache, v_cache, st)
+                        : launch_fp8<128, float>(pp, k_cache, v_cache, st);
   else
-    rc = head_dim == 64 ? launch_fp8<64, __nv_bfloat16>(pp, k_cache, v_cache, grid, st)
-                        : launch_fp8<128, __nv_bfloat16>(pp, k_cache, v_cache, grid, st);
+    rc = head_dim == 64 ? launch_fp8<64, __nv_bfloat16>(pp, k_cache, v_cache, st)
+                        : launch_fp8<128, __nv_bfloat16>(pp, k_cache, v_cache, st);
   if (rc) return rc;
   if (parts)
     rc = launch_merge_ex(p.part_out, p.part_lse, seq_lens, partition_size, out, lse_out, num_seqs, num_heads, head_dim,

@@ -24,7 +24,8 @@ int check_launch(const char* what);
 // strides of dims 1..rank-1.  Returns METIS_OK or an error code.
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,
                  const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                 CUtensorMapSwizzle swizzle);
+                 CUtensorMapSwizzle swizzle,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Launch `kernel` as a programmatic dependent of the previous kernel in the
 // stream: it may start launching while that kernel still runs, so it must

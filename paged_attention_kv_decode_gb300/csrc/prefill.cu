@@ -88,7 +88,7 @@ static_assert(128 * (2 * kRegsSoftmax8 + 2 * kRegsOther8) <= kPfThreads * kRegsL
 #endif
 constexpr int kKStages = METIS_PF_K_STAGES;  // K ring depth
 constexpr int kVStages = METIS_PF_V_STAGES;  // V ring depth
-constexpr int kV8Stages = 2;      // 8-bit cache: staged e4m3 V tiles
+constexpr int kV8Stages = 3;      // 8-bit cache: staged e4m3 V tiles
 constexpr int kKvTile = 128;      // tokens per K/V tile
 constexpr int kRows = 128;        // query rows per tile
 constexpr int kTmemCols = 512;    // S0 | S1 | O0 | O1
