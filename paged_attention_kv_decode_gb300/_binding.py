@@ -420,29 +420,81 @@ def metis_mla_reshape_and_cache(kv_c: torch.Tensor, k_pe: torch.Tensor, kv_cache
                                            bs, nb, _stream(stream)))
 
 
-def _fp8_cache(device: torch.device, k_cache, v_cache, k_scale, v_scale):
-    """Check an 8-bit cache: codes (float8_e4m3fn or uint8) [nb, bs, G, D], scale bytes (uint8) [nb, G]."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda(name, t, ndim=4)
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.uint8 codes, got {t.dtype}")
-    _cuda("k_scale", k_scale, dtype=torch.uint8, ndim=2)
-    _cuda("v_scale", v_scale, dtype=torch.uint8, ndim=2)
-    nb, bs, G, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or tuple(k_scale.shape) != (nb, G) or v_scale.shape != k_scale.shape:
-        raise ValueError("inconsistent shapes: codes [num_blocks, block_size, num_kv_heads, head_dim], scales "
-                         "[num_blocks, num_kv_heads]")
-    _one_device(device, k_cache, v_cache, k_scale, v_scale)
-    return nb, bs, G, D
+# The 8-bit cache's calls are short on the GPU (a few microseconds for a small step), so
+# their checks are written for few Python operations: plain ints for pointers and devices.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (absent from builds without CUDA)
 
 
-def _one_device(device: torch.device, *tensors: Optional[torch.Tensor]):
-    """The library launches on the current device: refuse tensors that live elsewhere."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device} but the current device is cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on one device: got {t.device} and {device}")
+def _stream_of(device: int, stream) -> int:
+    if stream is None:
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory of a call on `stream`: torch's allocator reuses freed memory in the order of one stream,
+    so the outputs and workspace of a call on another stream come from that one's pool."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_of(like.get_device(), stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _on(device: int, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
+    """Check a tensor's device, dtype, shape and layout; returns its address."""
+    try:
+        if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.get_device() != device:
+        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not cuda:{device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"inconsistent shapes: {name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device_of(name: str, t: torch.Tensor, ndim: int) -> int:
+    """The index of a CUDA tensor's device, which has to be the current one (the library launches there)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _fp8_cache(dev: int, k_cache, v_cache, k_scale, v_scale):
+    """Check an 8-bit cache: codes (float8_e4m3fn or uint8) [nb, bs, G, D], scale bytes (uint8) [nb, G].
+    Returns its sizes and the four addresses."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [num_blocks, block_size, num_kv_heads, head_dim]")
+    dt = k_cache.dtype
+    if dt is not torch.float8_e4m3fn and dt is not torch.uint8:
+        raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.uint8 codes, got {dt}")
+    shape = k_cache.shape
+    nb, bs, G, D = shape
+    return (nb, bs, G, D), (_on(dev, "k_cache", k_cache, dt, shape), _on(dev, "v_cache", v_cache, dt, shape),
+                            _on(dev, "k_scale", k_scale, torch.uint8, (nb, G)),
+                            _on(dev, "v_scale", v_scale, torch.uint8, (nb, G)))
+
+
+def _table(dev: int, block_table, num_seqs: int):
+    """Check a block table of num_seqs rows; returns its width and address."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [num_seqs, max_blocks]")
+    width = block_table.shape[1]
+    return width, _on(dev, "block_table", block_table, torch.int32, (num_seqs, width))
 
 
 def metis_reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -451,22 +503,20 @@ def metis_reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, k_cache:
     """Quantise the new rows ``key`` / ``value`` ``[T, G, D]`` (bf16 or fp32) into an 8-bit
     cache: sequence s's rows ``cu_q_lens[s] .. cu_q_lens[s + 1]`` are its last tokens, and
     ``seq_lens`` counts them.  Codes and scales are updated in place, asynchronously."""
-    lib = load_library()
-    _cuda("key", key, ndim=3)
-    dt = _dtype_code(key.dtype)
-    _cuda("value", value, dtype=key.dtype, ndim=3)
-    nb, bs, G, D = _fp8_cache(key.device, k_cache, v_cache, k_scale, v_scale)
-    _cuda("cu_q_lens", cu_q_lens, dtype=torch.int32, ndim=1)
-    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
-    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
-    _one_device(key.device, value, cu_q_lens, block_table, seq_lens)
-    S = seq_lens.shape[0]
-    if (value.shape != key.shape or tuple(key.shape[1:]) != (G, D) or cu_q_lens.shape[0] != S + 1
-            or block_table.shape[0] != S):
-        raise ValueError("inconsistent shapes")
-    _check(lib.metis_reshape_and_cache_fp8(
-        _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(cu_q_lens),
-        _ptr(block_table), _ptr(seq_lens), S, key.shape[0], G, D, bs, block_table.shape[1], nb, dt, _stream(stream)))
+    lib = _lib or load_library()
+    dev = _device_of("key", key, 3)
+    code = _dtype_code(key.dtype)
+    (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    T = key.shape[0]
+    rows = (T, G, D)
+    S = seq_lens.numel()
+    width, table = _table(dev, block_table, S)
+    rc = lib.metis_reshape_and_cache_fp8(
+        _on(dev, "key", key, key.dtype, rows), _on(dev, "value", value, key.dtype, rows), *cache,
+        _on(dev, "cu_q_lens", cu_q_lens, torch.int32, (S + 1,)), table,
+        _on(dev, "seq_lens", seq_lens, torch.int32, (S,)), S, T, G, D, bs, width, nb, code, _stream_of(dev, stream))
+    if rc:
+        _check(rc)
 
 
 def metis_gather_cache_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -478,36 +528,64 @@ def metis_gather_cache_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale
     ``k_out`` / ``v_out`` ``[num_rows, G, D]`` (bf16 or fp32).  Pass the outputs, or
     ``num_rows`` to have them allocated (rows that no token maps to then hold anything).
     ``max_seq_len=None`` reads seq_lens (a sync)."""
-    lib = load_library()
-    _cuda("k_cache", k_cache)
-    dev = k_cache.device
-    nb, bs, G, D = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
-    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
-    _cuda("row_offsets", row_offsets, dtype=torch.int32, ndim=1)
-    S = seq_lens.shape[0]
-    if block_table.shape[0] != S or row_offsets.shape[0] != S:
-        raise ValueError("inconsistent shapes")
+    lib = _lib or load_library()
+    dev = _device_of("k_cache", k_cache, 4)
+    (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    S = seq_lens.numel()
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    offsets = _on(dev, "row_offsets", row_offsets, torch.int32, (S,))
     if (k_out is None) != (v_out is None):
         raise ValueError("pass both of k_out and v_out, or neither")
     if k_out is None:
         if num_rows is None:
             raise ValueError("num_rows is needed to allocate the outputs")
-        k_out = torch.empty((num_rows, G, D), dtype=out_dtype, device=dev)
-        v_out = torch.empty_like(k_out)
-    dt = _dtype_code(k_out.dtype)
-    _cuda("k_out", k_out, ndim=3)
-    _cuda("v_out", v_out, dtype=k_out.dtype, ndim=3)
-    if tuple(k_out.shape[1:]) != (G, D) or v_out.shape != k_out.shape or num_rows not in (None, k_out.shape[0]):
-        raise ValueError("k_out and v_out must be [num_rows, num_kv_heads, head_dim]")
-    _one_device(dev, block_table, seq_lens, row_offsets, k_out, v_out)
+        code = _dtype_code(out_dtype)
+        k_out = _empty((num_rows, G, D), out_dtype, k_cache, stream)
+        v_out = _empty((num_rows, G, D), out_dtype, k_cache, stream)
+        k_at, v_at = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        if num_rows is None:
+            num_rows = k_out.shape[0]
+        code = _dtype_code(k_out.dtype)
+        k_at = _on(dev, "k_out", k_out, k_out.dtype, (num_rows, G, D))
+        v_at = _on(dev, "v_out", v_out, k_out.dtype, (num_rows, G, D))
     if max_seq_len is None:
         max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
-    _check(lib.metis_gather_cache_fp8(
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
-        _ptr(row_offsets), _ptr(k_out), _ptr(v_out), S, k_out.shape[0], G, D, bs, block_table.shape[1], nb, dt,
-        int(max_seq_len), _stream(stream)))
+    rc = lib.metis_gather_cache_fp8(*cache, table, lens, offsets, k_at, v_at, S, num_rows, G, D, bs, width, nb, code,
+                                    int(max_seq_len), _stream_of(dev, stream))
+    if rc:
+        _check(rc)
     return k_out, v_out
+
+
+def _attention_outputs(dev: int, q: torch.Tensor, out, lse_out, want_lse: bool, stream):
+    """Allocate or check out (like q) and lse_out (fp32 [rows, heads]); returns both and their addresses."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+        o_at = out.data_ptr()
+    else:
+        o_at = _on(dev, "out", out, q.dtype, q.shape)
+    if lse_out is not None:
+        l_at = _on(dev, "lse_out", lse_out, torch.float32, q.shape[:2])
+    elif want_lse:
+        lse_out = _empty(q.shape[:2], torch.float32, q, stream)
+        l_at = lse_out.data_ptr()
+    else:
+        l_at = None
+    return out, o_at, lse_out, l_at
+
+
+def _workspace(dev: int, q: torch.Tensor, workspace, need: int, stream):
+    """The caller's workspace, or one of `need` bytes; returns it with its address and size."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _empty(need, torch.uint8, q, stream)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def metis_paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -518,36 +596,24 @@ def metis_paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 stream=None, want_lse: bool = False) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Paged decode over an 8-bit cache (``q`` bf16 or fp32); returns ``(out, lse_out)``.
     ``max_seq_len=None`` reads seq_lens (a sync)."""
-    lib = load_library()
-    _cuda("q", q, ndim=3)
-    dt = _dtype_code(q.dtype)
-    dev = q.device
-    nb, bs, G, Dk = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
-    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
-    S, H, D = q.shape
-    if Dk != D or block_table.shape[0] != S or seq_lens.shape[0] != S:
-        raise ValueError("inconsistent shapes")
-    if out is None:
-        out = torch.empty_like(q)
-    _cuda("out", out, dtype=q.dtype, ndim=3)
-    if lse_out is None and want_lse:
-        lse_out = torch.empty((S, H), dtype=torch.float32, device=dev)
-    if lse_out is not None:
-        _cuda("lse_out", lse_out, dtype=torch.float32, ndim=2)
-    if out.shape != q.shape or (lse_out is not None and tuple(lse_out.shape) != (S, H)):
-        raise ValueError("out must have q's shape and lse_out [num_seqs, num_heads]")
+    lib = _lib or load_library()
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    S, H = q.shape[0], q.shape[1]
+    q_at = _on(dev, "q", q, q.dtype, (S, H, D))
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
     if max_seq_len is None:
         max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
-    need = metis_decode_workspace_bytes(S, H, D, max_seq_len, partition_size)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _one_device(dev, block_table, seq_lens, out, lse_out, workspace)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib.metis_paged_attn_decode_fp8(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
-        _ptr(out), _ptr(lse_out), S, H, G, D, bs, block_table.shape[1], nb, dt, float(scale), int(partition_size),
-        int(max_seq_len), _ptr(workspace), ws_bytes, _stream(stream)))
+    need = metis_decode_workspace_bytes(S, H, D, max_seq_len, partition_size) if partition_size else 0
+    workspace, w_at, w_bytes = _workspace(dev, q, workspace, need, stream)
+    rc = lib.metis_paged_attn_decode_fp8(q_at, *cache, table, lens, o_at, l_at, S, H, G, D, bs, width, nb, code,
+                                         float(scale), int(partition_size), int(max_seq_len), w_at, w_bytes,
+                                         _stream_of(dev, stream))
+    if rc:
+        _check(rc)
     return out, lse_out
 
 
@@ -558,38 +624,26 @@ def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor,
                                        max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
                                        stream=None, want_lse: bool = False):
     """Chunked prefill (+ single-token decodes) over an 8-bit cache; returns ``(out, lse_out)``."""
-    lib = load_library()
-    _cuda("q", q, ndim=3)
-    dt = _dtype_code(q.dtype)
-    dev = q.device
-    _cuda("cu_q_lens", cu_q_lens, dtype=torch.int32, ndim=1)
-    nb, bs, G, Dk = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    _cuda("block_table", block_table, dtype=torch.int32, ndim=2)
-    _cuda("seq_lens", seq_lens, dtype=torch.int32, ndim=1)
-    T, H, D = q.shape
-    S = seq_lens.shape[0]
-    if cu_q_lens.shape[0] != S + 1 or block_table.shape[0] != S or Dk != D:
-        raise ValueError("inconsistent shapes")
-    if out is None:
-        out = torch.empty_like(q)
-    _cuda("out", out, dtype=q.dtype, ndim=3)
-    if lse_out is None and want_lse:
-        lse_out = torch.empty((T, H), dtype=torch.float32, device=dev)
-    if lse_out is not None:
-        _cuda("lse_out", lse_out, dtype=torch.float32, ndim=2)
-    if out.shape != q.shape or (lse_out is not None and tuple(lse_out.shape) != (T, H)):
-        raise ValueError("out must have q's shape and lse_out [num_tokens, num_heads]")
+    lib = _lib or load_library()
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    T, H = q.shape[0], q.shape[1]
+    q_at = _on(dev, "q", q, q.dtype, (T, H, D))
+    S = seq_lens.numel()
+    cu = _on(dev, "cu_q_lens", cu_q_lens, torch.int32, (S + 1,))
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
     if max_seq_len is None:
         max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
-    need = metis_prefill_workspace_bytes(S, T, H, G)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _one_device(dev, cu_q_lens, block_table, seq_lens, out, lse_out, workspace)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib.metis_paged_attn_prefill_chunk_fp8(
-        _ptr(q), _ptr(cu_q_lens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-        _ptr(seq_lens), _ptr(out), _ptr(lse_out), S, T, H, G, D, bs, block_table.shape[1], nb, dt, float(scale),
-        int(max_seq_len), _ptr(workspace), ws_bytes, _stream(stream)))
+    need = metis_prefill_workspace_bytes(S, T, H, G) if workspace is None else 0
+    workspace, w_at, w_bytes = _workspace(dev, q, workspace, max(need, 256), stream)
+    rc = lib.metis_paged_attn_prefill_chunk_fp8(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width, nb,
+                                                code, float(scale), int(max_seq_len), w_at, w_bytes,
+                                                _stream_of(dev, stream))
+    if rc:
+        _check(rc)
     return out, lse_out
 
 
