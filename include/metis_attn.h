@@ -392,9 +392,8 @@ int metis_reshape_and_cache_fp8(const void* key, const void* value, void* k_cach
  *   out_dtype      METIS_F32 or METIS_BF16
  *   max_seq_len    host-side upper bound on seq_lens; tokens beyond it are not read
  *                  (METIS_STATUS_SEQ_TOO_LONG)
- * Sixteen tokens whose rows are not all inside [0, num_rows) are not written
- * (METIS_STATUS_BAD_OFFSETS); a page whose id is outside the pool reads as zeros
- * (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_rows == 0 is a successful no-op.
+ * A row outside [0, num_rows) is not written (METIS_STATUS_BAD_OFFSETS); a page whose
+ * id is outside the pool reads as zeros (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_rows == 0 is a successful no-op.
  */
 int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                            const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,

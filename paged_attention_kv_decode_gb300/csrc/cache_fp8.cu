@@ -40,32 +40,127 @@ struct WriteFp8Params {
   const int32_t* cu_q_lens;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  int S, T, G, bs, max_blocks, num_blocks;
+  int S, T, G, bs, bs_log, max_blocks, num_blocks;
 };
 
 constexpr int kWriteWarps = 8;
 
-// Index of the sequence that item i belongs to: the largest s with off(s) <= i, by a
-// 32-way search of the warp.  All lanes return it.
-__device__ __forceinline__ int seq_of_item(const WriteFp8Params& p, int i, int lane) {
+// The sequence that item i belongs to, the largest s with off(s) <= i, with its row range
+// and length; every lane returns them.  A 128-way search of the warp, four probes per lane
+// in flight; up to 127 sequences take one round of loads, which brings the lengths along.
+struct ItemSeq {
+  int s, r0, r1, L;
+};
+
+__device__ __forceinline__ ItemSeq seq_of_item(const WriteFp8Params& p, int i, int lane) {
+  ItemSeq it;
+  int cu[4];
   int lo = 0, n = p.S;
+  if (n < 128) {
+    int len[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = k * 32 + lane;
+      cu[k] = at <= n ? __ldg(p.cu_q_lens + at) : 0;
+      len[k] = at < n ? __ldg(p.seq_lens + at) : 0;
+    }
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = k * 32 + lane;
+      c += __popc(__ballot_sync(0xffffffffu, at < n && (max(cu[k], 0) >> p.bs_log) + 2ll * at <= i));
+    }
+    it.s = max(c, 1) - 1;
+    const int k0 = it.s >> 5, k1 = (it.s + 1) >> 5;  // uniform over the warp
+    it.r0 = __shfl_sync(0xffffffffu, k0 == 0 ? cu[0] : k0 == 1 ? cu[1] : k0 == 2 ? cu[2] : cu[3], it.s & 31);
+    it.r1 = __shfl_sync(0xffffffffu, k1 == 0 ? cu[0] : k1 == 1 ? cu[1] : k1 == 2 ? cu[2] : cu[3], (it.s + 1) & 31);
+    it.L = __shfl_sync(0xffffffffu, k0 == 0 ? len[0] : k0 == 1 ? len[1] : k0 == 2 ? len[2] : len[3], it.s & 31);
+    return it;
+  }
   while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int s = lo + lane * step;
-    const bool le = lane * step < n && max(__ldg(p.cu_q_lens + s), 0) / p.bs + 2ll * s <= i;
-    const int c = max(__popc(__ballot_sync(0xffffffffu, le)), 1);
+    const int step = (n + 127) / 128;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = (k * 32 + lane) * step;
+      cu[k] = at < n ? __ldg(p.cu_q_lens + lo + at) : 0;
+    }
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = (k * 32 + lane) * step;
+      c += __popc(__ballot_sync(0xffffffffu, at < n && (max(cu[k], 0) >> p.bs_log) + 2ll * (lo + at) <= i));
+    }
+    c = max(c, 1);
     lo += (c - 1) * step;
     n = min(step, n - (c - 1) * step);
   }
-  return lo;
+  it.s = lo;
+  it.r0 = __ldg(p.cu_q_lens + lo);
+  it.r1 = __ldg(p.cu_q_lens + lo + 1);
+  it.L = __ldg(p.seq_lens + lo);
+  return it;
+}
+
+// The largest finite |x| of a 16-byte piece's values, 0 without one; *odd: the piece holds
+// an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ float piece_amax(const uint4& v, bool* odd);
+
+template <>
+__device__ __forceinline__ float piece_amax<__nv_bfloat16>(const uint4& v, bool* odd) {
+  // bf16 magnitudes order like their bits; 0x7f80 and above are not finite
+  const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+  m = max(m & 0xffffu, m >> 16);
+  if (m >= 0x7f80u) {
+    *odd = true;
+    m = 0;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+      if (h < 0x7f80u) m = max(m, h);
+    }
+  }
+  return __uint_as_float(m << 16);
+}
+
+template <>
+__device__ __forceinline__ float piece_amax<float>(const uint4& v, bool* odd) {
+  const uint32_t w[4] = {v.x & 0x7fffffffu, v.y & 0x7fffffffu, v.z & 0x7fffffffu, v.w & 0x7fffffffu};
+  uint32_t m = max(max(w[0], w[1]), max(w[2], w[3]));
+  if (m >= 0x7f800000u) {
+    *odd = true;
+    m = 0;
+    for (int e = 0; e < 4; ++e)
+      if (w[e] < 0x7f800000u) m = max(m, w[e]);
+  }
+  return __uint_as_float(m);
+}
+
+// Four values times inv as codes; odd: infinities become NaN first (0 * x + x keeps the rest)
+__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv, bool odd) {
+  if (odd) {
+    a = fmaf(a, 0.f, a);
+    b = fmaf(b, 0.f, b);
+    c = fmaf(c, 0.f, c);
+    d = fmaf(d, 0.f, d);
+  }
+  const uint64_t inv2 = f2_pack(inv, inv);
+  float x0, x1, x2, x3;
+  f2_unpack(f2_mul(f2_pack(a, b), inv2), x0, x1);
+  f2_unpack(f2_mul(f2_pack(c, d), inv2), x2, x3);
+  return pack_e4m3x4(x0, x1, x2, x3);
 }
 
 // One warp: 16 slots of a page x one head of K or V.  Lanes hold 16-byte pieces of the
 // new rows (8 bf16 or 4 fp32), several rows per load, all loads issued before the first
 // use; the rows stay in registers between the maximum and the rounding, so each input is
 // read once.  Pages of 32 or 64 slots take 2 or 4 warps that share their maximum.
+// The grid is a few waves of short CTAs, so CTAs per SM (registers) decide: 8,240 rows of
+// 8 x 128 bf16 take 12.2 us with five on an SM, 13.3 us with four or three, 15.8 us with two;
+// fp32 rows of 8 x 128, twice the registers, 18 us with three and 26 us with five.  Eight
+// slots per warp instead of 16 are no faster (13.2 us).
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteWarps * 32) write_fp8_kernel(const WriteFp8Params p) {
+__global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5) write_fp8_kernel(const WriteFp8Params p) {
   constexpr int VEC = 16 / (int)sizeof(T);  // elements per lane and load
   constexpr int LPR = D / VEC;              // lanes per row
   constexpr int RPL = 32 / LPR;             // rows per load
@@ -74,13 +169,13 @@ __global__ void __launch_bounds__(kWriteWarps * 32) write_fp8_kernel(const Write
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int subs = p.bs / 16;                                         // warps per page, head and cache
-  const int combo = (blockIdx.y * (blockDim.x >> 5) + warp) / subs;   // head * 2 + cache
-  const int sub = warp & (subs - 1);                                  // (a block holds whole combos)
+  const int subs = p.bs >> 4;                                                       // warps per page, head and cache
+  const int combo = (int)((blockIdx.y * (blockDim.x >> 5) + warp) >> (p.bs_log - 4));  // head * 2 + cache
+  const int sub = warp & (subs - 1);                                                // (a block holds whole combos)
 
   const int i = blockIdx.x;
-  const int s = seq_of_item(p, i, lane);
-  const int r0 = p.cu_q_lens[s], q = p.cu_q_lens[s + 1] - r0, L = p.seq_lens[s];
+  const ItemSeq it = seq_of_item(p, i, lane);
+  const int s = it.s, r0 = it.r0, q = it.r1 - r0, L = it.L;
   if (q == 0) return;
   if (q < 0 || r0 < 0 || r0 > p.T - q || q > L || L > p.max_blocks * p.bs) {
     if (threadIdx.x == 0)
@@ -89,51 +184,37 @@ __global__ void __launch_bounds__(kWriteWarps * 32) write_fp8_kernel(const Write
     return;
   }
   const int first = L - q;                         // earlier tokens of the sequence
-  const int j = i - (r0 / p.bs + 2 * s);           // page of this sequence's new rows
-  if (j < 0 || ((long long)(first / p.bs) + j) * p.bs >= L) return;
-  const int page = first / p.bs + j;
+  const int page0 = first >> p.bs_log;
+  const int j = i - ((r0 >> p.bs_log) + 2 * s);    // page of this sequence's new rows
+  if (j < 0 || ((long long)page0 + j) * p.bs >= L) return;
+  const int page = page0 + j;
   const int base = page * p.bs;
-  const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
-  if (b < 0) return;
   const int kept = max(first - base, 0);           // slots [0, kept): earlier tokens
   const int end = min(L - base, p.bs);             // slots [kept, end): new rows
   const bool live = combo < 2 * p.G;
   const int g = combo >> 1, which = combo & 1;
-  uint8_t* const byte_at = (which ? p.scale[1] : p.scale[0]) + (size_t)b * p.G + g;
-  const uint32_t before = live && kept > 0 ? min((uint32_t)*byte_at, 254u) : 0u;
 
+  // the rows are on their way before the page's block id is known
   const int col = (lane % LPR) * VEC;
   const int slot0 = sub * 16 + lane / LPR;
-  const T* src = reinterpret_cast<const T*>(which ? p.src[1] : p.src[0]) + ((size_t)(r0 + base - first) * p.G + g) * D + col;
+  const size_t row_len = (size_t)p.G * D;
+  const T* src = reinterpret_cast<const T*>(which ? p.src[1] : p.src[0]) +
+                 ((long long)(r0 + base - first + slot0) * p.G + g) * D + col;
   uint4 raw[NL];
 #pragma unroll
   for (int k = 0; k < NL; ++k) {
     const int slot = slot0 + k * RPL;
-    raw[k] = live && slot >= kept && slot < end
-                 ? __ldg(reinterpret_cast<const uint4*>(src + (long long)slot * p.G * D))
-                 : make_uint4(0u, 0u, 0u, 0u);
+    raw[k] = live && slot >= kept && slot < end ? __ldg(reinterpret_cast<const uint4*>(src + k * RPL * row_len))
+                                                : make_uint4(0u, 0u, 0u, 0u);
   }
-  auto value = [&](int k, int e) -> float {  // element e of piece k
-    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-    if (sizeof(T) == 4) return __uint_as_float(w[e & 3]);
-    return __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-  };
-  float amax = 0.f;  // fmaxf drops NaN
+  const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
+  if (b < 0) return;
+  uint8_t* const byte_at = (which ? p.scale[1] : p.scale[0]) + (size_t)b * p.G + g;
+  const uint32_t before = live && kept > 0 ? min((uint32_t)*byte_at, 254u) : 0u;
+  bool odd = false;
+  float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < NL; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(value(k, e)));
-  const bool odd = amax == INFINITY;  // this lane holds an infinity: it counts as NaN
-  if (odd) {
-    amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < NL; ++k)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float a = fabsf(value(k, e));
-        if (a < INFINITY) amax = fmaxf(amax, a);
-      }
-  }
+  for (int k = 0; k < NL; ++k) amax = fmaxf(amax, piece_amax<T>(raw[k], &odd));
   amax = warp_max_xor(amax, 1);
   if (subs > 1) {
     if (lane == 0) part_max[warp] = amax;
@@ -146,26 +227,24 @@ __global__ void __launch_bounds__(kWriteWarps * 32) write_fp8_kernel(const Write
 
   uint8_t* const codes = (which ? p.cache[1] : p.cache[0]) + ((size_t)b * p.bs * p.G + g) * D;
   const float inv = scale_of_byte(254u - byte);  // 2^(127 - byte)
+  uint8_t* dst = codes + slot0 * row_len + col;
 #pragma unroll
   for (int k = 0; k < NL; ++k) {
     const int slot = slot0 + k * RPL;
-    if (slot < kept || slot >= end) continue;
-    uint32_t out[VEC / 4];
-#pragma unroll
-    for (int e = 0; e < VEC; e += 4) {
-      float y[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        y[u] = value(k, e + u) * inv;
-        if (odd) y[u] = fmaf(y[u], 0.f, y[u]);  // infinity -> NaN, anything else stays
+    const uint4 v = raw[k];
+    if (slot >= kept && slot < end) {
+      if (sizeof(T) == 2) {
+        uint2 out;
+        out.x = quantize4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                          __uint_as_float(v.y & 0xffff0000u), inv, odd);
+        out.y = quantize4(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u), __uint_as_float(v.w << 16),
+                          __uint_as_float(v.w & 0xffff0000u), inv, odd);
+        *reinterpret_cast<uint2*>(dst + k * RPL * row_len) = out;
+      } else {
+        *reinterpret_cast<uint32_t*>(dst + k * RPL * row_len) =
+            quantize4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w), inv, odd);
       }
-      out[e / 4] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
     }
-    uint8_t* dst = codes + (size_t)slot * p.G * D + col;
-    if (VEC == 8)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[VEC / 8]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = out[0];
   }
 
   // the scale grew: round the earlier codes at the new one
@@ -199,77 +278,110 @@ struct GatherFp8Params {
   const int32_t* seq_lens;
   const int32_t* row_offsets;
   void* out[2];
-  int S, G, D, bs, max_blocks, num_blocks, cap;
+  int S, G, D, bs, bs_log, max_blocks, num_blocks, cap;
+  int tile;  // tokens per CTA
   long long num_rows;
 };
 
 constexpr int kGatherThreads = 256;
-constexpr int kGatherTile = 16;  // tokens per CTA: one page's worth, so one block id
+constexpr int kGatherBatch = 4;        // rows of K and of V that a thread has in flight
+constexpr int kGatherTileBatches = 2;  // such batches per CTA (one or two are alike, four leave small batches few CTAs)
 
+// One store of values: eight codes to bf16, four to fp32 (16 bytes either way)
 template <typename T>
-__device__ __forceinline__ void store16(T* dst, const uint4& c, float scale);
+struct GatherVec;
 
 template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* dst, const uint4& c, float scale) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float v[4];
-    unpack_e4m3x4_f32(w[u], v);
-    o[2 * u] = pack_bf16x2(v[0] * scale, v[1] * scale);
-    o[2 * u + 1] = pack_bf16x2(v[2] * scale, v[3] * scale);
+struct GatherVec<__nv_bfloat16> {
+  using Codes = uint2;
+  static constexpr int N = 8;
+  __device__ static __forceinline__ Codes zero() { return make_uint2(0u, 0u); }
+  __device__ static __forceinline__ uint4 values(const Codes& c, float scale) {
+    float a[4], b[4];
+    unpack_e4m3x4_f32(c.x, a);
+    unpack_e4m3x4_f32(c.y, b);
+    return make_uint4(pack_bf16x2(a[0] * scale, a[1] * scale), pack_bf16x2(a[2] * scale, a[3] * scale),
+                      pack_bf16x2(b[0] * scale, b[1] * scale), pack_bf16x2(b[2] * scale, b[3] * scale));
   }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-}
+};
 
 template <>
-__device__ __forceinline__ void store16<float>(float* dst, const uint4& c, float scale) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float v[4];
-    unpack_e4m3x4_f32(w[u], v);
-    reinterpret_cast<float4*>(dst)[u] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+struct GatherVec<float> {
+  using Codes = uint32_t;
+  static constexpr int N = 4;
+  __device__ static __forceinline__ Codes zero() { return 0u; }
+  __device__ static __forceinline__ uint4 values(const Codes& c, float scale) {
+    float a[4];
+    unpack_e4m3x4_f32(c, a);
+    return make_uint4(__float_as_uint(a[0] * scale), __float_as_uint(a[1] * scale), __float_as_uint(a[2] * scale),
+                      __float_as_uint(a[3] * scale));
   }
-}
+};
 
-// One CTA: 16 tokens of one sequence (inside one page), every head of K and V.  A thread
-// takes 16-byte pieces of codes and writes 16 values.
+// One CTA: `tile` tokens of one sequence, every head of K and V.  A thread keeps one column
+// of 16 bytes of output and walks the rows, kGatherBatch of K and of V in flight, so that
+// loads and stores of a warp are whole runs of a row.  HBM-bound: 64 sequences of 512..4096
+// tokens of 8 x 128 to bf16 in 137 us (6,650 GB/s, the measured copy rate), to fp32 in 233 us;
+// with 16 codes per thread and two 16-byte stores side by side the bf16 case took 151 us.
 template <typename T>
 __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherFp8Params p) {
+  using Vec = GatherVec<T>;
+  using Codes = typename Vec::Codes;
   pdl_wait();
   pdl_launch_dependents();
   const int s = blockIdx.y;
-  const int tok0 = blockIdx.x * kGatherTile;
+  const long long tile0 = (long long)blockIdx.x * p.tile;
   int L = p.seq_lens[s];
   if (L > p.cap) {
-    if (threadIdx.x == 0 && tok0 == 0) atomicOr(&g_status_fp8, METIS_STATUS_SEQ_TOO_LONG);
+    if (threadIdx.x == 0 && tile0 == 0) atomicOr(&g_status_fp8, METIS_STATUS_SEQ_TOO_LONG);
     L = p.cap;
   }
-  if (tok0 >= L) return;
-  const int n = min(L - tok0, kGatherTile);
-  const long long row0 = (long long)p.row_offsets[s] + tok0;
-  if (row0 < 0 || row0 + n > p.num_rows) {
-    if (threadIdx.x == 0) atomicOr(&g_status_fp8, METIS_STATUS_BAD_OFFSETS);
-    return;
-  }
-  const int page = tok0 / p.bs;
-  const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
-  const int pieces = p.G * p.D / 16;  // per token row
-  const size_t src0 = b < 0 ? 0 : ((size_t)b * p.bs + (tok0 - page * p.bs)) * p.G * p.D;
-  for (int c = threadIdx.x; c < n * pieces; c += kGatherThreads) {
-    const int g = (c % pieces) * 16 / p.D;
+  if (tile0 >= L) return;
+  const int tok0 = (int)tile0;
+  const int n = min(L - tok0, p.tile);
+  const long long first_row = (long long)p.row_offsets[s] + tok0;
+  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
+  const int cols = p.G * p.D / Vec::N;                  // stores per row
+  const int lanes = min(cols, kGatherThreads);          // threads across a row
+  const int rows = kGatherThreads / lanes;              // rows at a time
+  const int ty = threadIdx.x / lanes;
+  if (ty >= rows) return;
+  for (int col = threadIdx.x - ty * lanes; col < cols; col += lanes) {
+    const int g = col * Vec::N / p.D;
+    for (int r0 = ty; r0 < n; r0 += rows * kGatherBatch) {
+      Codes c[2][kGatherBatch];
+      uint32_t byte[2][kGatherBatch];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      float scale = 0.f;
-      if (b >= 0) {
-        v = __ldg(reinterpret_cast<const uint4*>(p.cache[w] + src0) + c);
-        scale = scale_of_byte(__ldg(p.scale[w] + (size_t)b * p.G + g));
+      for (int u = 0; u < kGatherBatch; ++u) {
+        const int r = r0 + u * rows;
+        c[0][u] = c[1][u] = Vec::zero();                // a page with a bad id reads as zeros
+        byte[0][u] = byte[1][u] = 127;
+        if (r < n) {
+          const int tok = tok0 + r, page = tok >> p.bs_log;
+          const int b = checked_block(bt_row, page, p.num_blocks, &g_status_fp8);
+          if (b >= 0) {
+            const size_t row = ((size_t)b << p.bs_log) + (tok & (p.bs - 1));
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              c[w][u] = __ldg(reinterpret_cast<const Codes*>(p.cache[w] + row * p.G * p.D) + col);
+              byte[w][u] = __ldg(p.scale[w] + (size_t)b * p.G + g);
+            }
+          }
+        }
       }
-      store16<T>(reinterpret_cast<T*>(p.out[w]) + (size_t)row0 * p.G * p.D + (size_t)c * 16, v, scale);
+#pragma unroll
+      for (int u = 0; u < kGatherBatch; ++u) {
+        const int r = r0 + u * rows;
+        if (r >= n) break;
+        const long long row = first_row + r;
+        if (row < 0 || row >= p.num_rows) {             // rows outside the outputs are not written
+          if (col == 0) atomicOr(&g_status_fp8, METIS_STATUS_BAD_OFFSETS);
+          continue;
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          reinterpret_cast<uint4*>(p.out[w])[(size_t)row * cols + col] = Vec::values(c[w][u], scale_of_byte(byte[w][u]));
+      }
     }
   }
 }
@@ -333,6 +445,7 @@ extern "C" int metis_reshape_and_cache_fp8(const void* key, const void* value, v
   p.T = num_tokens;
   p.G = num_kv_heads;
   p.bs = block_size;
+  p.bs_log = block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
   p.max_blocks = max_blocks;
   p.num_blocks = num_blocks;
   auto kern = dtype == METIS_F32 ? (head_dim == 64 ? write_fp8_kernel<float, 64> : write_fp8_kernel<float, 128>)
@@ -385,7 +498,11 @@ extern "C" int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, 
   p.num_blocks = num_blocks;
   p.cap = (int)std::min<long long>((long long)max_blocks * block_size, (long long)max_seq_len);
   p.num_rows = num_rows;
-  const dim3 grid((unsigned)((p.cap - 1) / kGatherTile + 1), (unsigned)num_seqs);
+  p.bs_log = block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
+  // two batches per thread: fewer tokens for wide rows, at least 16
+  const int cols = num_kv_heads * head_dim / (out_dtype == METIS_BF16 ? 8 : 4);
+  p.tile = std::max(16, kGatherTileBatches * kGatherBatch * (kGatherThreads / std::min(cols, kGatherThreads)));
+  const dim3 grid((unsigned)((p.cap - 1) / p.tile + 1), (unsigned)num_seqs);
   return launch_dependent(out_dtype == METIS_BF16 ? gather_fp8_kernel<__nv_bfloat16> : gather_fp8_kernel<float>, grid,
                           dim3(kGatherThreads), 0, reinterpret_cast<cudaStream_t>(stream), "gather_fp8_kernel launch",
                           p);

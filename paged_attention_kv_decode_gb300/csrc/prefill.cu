@@ -212,10 +212,10 @@ constexpr int kSchedThreads = 1024;
 // with 7 TFLOP/s per SM the mixed batch above ends its decodes and chunks together).
 constexpr float kDecSmBytesPerS = 75e9f;
 constexpr float kChunkSmFlopsPerS = 7.0e12f;
-// The same two over an 8-bit cache: 226 MB of decodes on 11 SMs took 475 us, and the chunks
-// alone run at 0.94 PFLOP/s.
+// The same two over an 8-bit cache (rates between 40 and 46 GB/s change the mixed batch above by
+// 1 %; 58 GB/s, which leaves the decodes too few SMs, costs 15 %)
 constexpr float kDec8SmBytesPerS = 43e9f;
-constexpr float kChunk8SmFlopsPerS = 5.8e12f;
+constexpr float kChunk8SmFlopsPerS = 7.0e12f;
 
 __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const PrefillParams p, int4* items,
                                                                           int* count, int max_items) {

@@ -303,13 +303,13 @@ def test_gather_bad_contents():
     ref = np.concatenate([c.rows(s, n, "k") for s, n in enumerate(c.lens)])
     ref[40 + 16:40 + 32] = 0.0
     assert np.array_equal(k.double().cpu().numpy(), ref)
-    # rows past the end, and before the start: those groups of 16 tokens are left alone
+    # rows past the end, and before the start, are not written
     out = [torch.full((60, 2, 64), 7.0, device=DEV) for _ in range(2)]
     pa.metis_gather_cache_fp8(*c.dev, c.bt, c.sl, i32([20, -4, 1 << 30]), k_out=out[0], v_out=out[1], max_seq_len=64)
     assert pa.metis_read_status(clear=True) == pa.STATUS_BAD_OFFSETS
     ref = np.full((60, 2, 64), 7.0)
-    ref[12:28] = c.rows(1, 32, "v")[16:]
-    ref[20:60] = c.rows(0, 40, "v")
+    ref[0:29] = c.rows(1, 33, "v")[4:]
+    ref[29:60] = c.rows(0, 40, "v")[9:]
     got = out[1].double().cpu().numpy()
     # rows 20 .. 28 belong to two sequences here
     assert np.array_equal(got[:20], ref[:20]) and np.array_equal(got[29:], ref[29:])
