@@ -101,52 +101,64 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
   const bool small_pages = p.bs == 16;        // two pages per unit, else part of one
   const int box = small_pages ? 16 : kUnit8;  // rows of a TMA box
 
-  // Lane l holds unit k = 32 * batch + l: the TMA row of its page(s) and the scale bytes
-  // (k0, v0, k1, v1).  -box (a box outside the tensor, read as zeros) marks a bad block id
-  // or a page past the range.
-  auto unit_info = [&](int k, int& c0, int& c1, uint32_t& sc) {
-    c0 = c1 = -box;
-    sc = 0x7f7f7f7fu;
+  // Lane l holds unit k = 32 * window + l of the current window: the TMA row of its page(s)
+  // and the scale bytes (k0, v0, k1, v1); and the block ids of the next window's unit.
+  // -box (a box outside the tensor, read as zeros) stands for a bad block id or a page past
+  // the range.  Ids, then loads of K and V, then scales and query: the item's first bytes
+  // wait for one lookup only.
+  auto load_ids = [&](int k, int& b0, int& b1) {  // -1: no such page (no id is flagged here)
+    b0 = b1 = -1;
     if (k >= n_my) return;
     const int tok = (u0 + warp + k * NW) * kUnit8;
-    const int page = tok / p.bs;
-    const int b = checked_block(bt_row, page, p.num_blocks, status);
-    if (b >= 0) {
-      c0 = b * p.bs + (tok - page * p.bs);
-      const size_t at = (size_t)b * p.G + g;
+    b0 = __ldg(bt_row + tok / p.bs);
+    if (small_pages && tok + 16 < t1) b1 = __ldg(bt_row + tok / 16 + 1);
+  };
+  auto check = [&](int b, bool wanted) {  // a bad id (flagged) becomes -1
+    if (b >= 0 && b < p.num_blocks) return b;
+    if (wanted) atomicOr(status, METIS_STATUS_BAD_BLOCK_ID);
+    return -1;
+  };
+  auto load_scales = [&](int b0, int b1) -> uint32_t {
+    uint32_t sc = 0x7f7f7f7fu;
+    if (b0 >= 0) {
+      const size_t at = (size_t)b0 * p.G + g;
       sc = __ldg(pp.k_scale + at) | ((uint32_t)__ldg(pp.v_scale + at) << 8);
       sc |= sc << 16;
     }
-    if (small_pages && tok + 16 < t1) {
-      const int b1 = checked_block(bt_row, page + 1, p.num_blocks, status);
+    if (small_pages) {
       sc = (sc & 0xffffu) | 0x7f7f0000u;
       if (b1 >= 0) {
-        c1 = b1 * 16;
         const size_t at = (size_t)b1 * p.G + g;
         sc = (sc & 0xffffu) | ((uint32_t)__ldg(pp.k_scale + at) << 16) | ((uint32_t)__ldg(pp.v_scale + at) << 24);
       }
     }
+    return sc;
   };
-  int cur0, cur1, next0, next1;
-  uint32_t cur_sc, next_sc;
-  unit_info(lane, cur0, cur1, cur_sc);
-  unit_info(32 + lane, next0, next1, next_sc);
+  int cur0, cur1, id0, id1;  // TMA rows of the current window, ids of the next one
+  uint32_t cur_sc = 0, next_sc = 0;
+  auto rows_of = [&](int k, int b0, int b1) {  // current window := unit k with these (checked) ids
+    const int tok = (u0 + warp + k * NW) * kUnit8;
+    cur0 = b0 < 0 ? -box : b0 * p.bs + tok % p.bs;
+    cur1 = b1 < 0 ? -box : b1 * 16;
+  };
+  auto checked = [&](int k, int& b0, int& b1) {
+    const int tok = (u0 + warp + k * NW) * kUnit8;
+    b0 = check(b0, k < n_my);
+    b1 = check(b1, k < n_my && small_pages && tok + 16 < t1);
+  };
   const uint64_t policy = l2_policy_evict_first();
 
-  auto issue = [&](int k) {  // called by all lanes, in order k = 0, 1, 2, ...
+  // K and V of unit k (called by all lanes, in order k = 0, 1, 2, ...)
+  auto issue = [&](int k) {
     if (k > 0 && (k & 31) == 0) {
-      cur0 = next0;
-      cur1 = next1;
+      rows_of(k + lane, id0, id1);  // (checked with their scales, half a window ago)
       cur_sc = next_sc;
-      unit_info(k + 32 + lane, next0, next1, next_sc);
+      load_ids(k + 32 + lane, id0, id1);
     }
     const int st = (kb + k) % STAGES;
     uint8_t* base = smem + (warp * STAGES + st) * Shape::kStageBytes;
     uint64_t* bar = &bars[warp * STAGES + st];
     if (lane == 0) mbar_arrive_expect_tx(bar, Shape::kStageBytes);
-    if (lane == (k & 31))
-      scales[warp * STAGES + st] = make_float4(scale_of_byte(cur_sc & 255u), scale_of_byte((cur_sc >> 8) & 255u),
-                                               scale_of_byte((cur_sc >> 16) & 255u), scale_of_byte(cur_sc >> 24));
     const int r0 = __shfl_sync(0xffffffffu, cur0, k & 31);
     const int r1 = __shfl_sync(0xffffffffu, cur1, k & 31);
     __syncwarp();
@@ -155,6 +167,27 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       tma_load_3d(base + (lane >> 1) * Shape::kTileBytes + (lane & 1) * (16 * D), lane < 2 ? &tmK : &tmV, bar, 0, g,
                   (lane & 1) ? r1 : r0, policy);
   };
+  // its page factors (after the loads: they wait for the scale bytes)
+  auto put_scales = [&](int k) {
+    if (lane == (k & 31))
+      scales[warp * STAGES + (kb + k) % STAGES] =
+          make_float4(scale_of_byte(cur_sc & 255u), scale_of_byte((cur_sc >> 8) & 255u),
+                      scale_of_byte((cur_sc >> 16) & 255u), scale_of_byte(cur_sc >> 24));
+    if ((k & 31) == 16) {  // the next window's ids are here by now
+      checked(k + 16 + lane, id0, id1);
+      next_sc = load_scales(id0, id1);
+    }
+  };
+  const int prologue = n_my < STAGES ? n_my : STAGES;
+  {
+    int b0, b1;
+    load_ids(lane, b0, b1);
+    load_ids(32 + lane, id0, id1);
+    checked(lane, b0, b1);
+    rows_of(lane, b0, b1);
+    for (int k = 0; k < prologue; ++k) issue(k);
+    cur_sc = load_scales(b0, b1);
+  }
 
   // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
   // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
@@ -212,8 +245,7 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
   for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = 0ull;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  const int prologue = n_my < STAGES ? n_my : STAGES;
-  for (int k = 0; k < prologue; ++k) issue(k);
+  for (int k = 0; k < prologue; ++k) put_scales(k);
 
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (((lane >> 3) & 1) << 3) + (lane & 7), lchunk = lane >> 4;
@@ -227,6 +259,7 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       ok = false;
       break;
     }
+    __syncwarp();  // the unit's page factors, written by one lane
     const int tok0 = (u0 + warp + k * NW) * kUnit8;
     const uint32_t kbase = smem_u32(smem + (warp * STAGES + st) * Shape::kStageBytes);
     const uint32_t vbase = kbase + Shape::kTileBytes;
@@ -350,7 +383,10 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       }
     }
     __syncwarp();
-    if (k + STAGES < n_my) issue(k + STAGES);
+    if (k + STAGES < n_my) {
+      issue(k + STAGES);
+      put_scales(k + STAGES);
+    }
   }
   if (!ok) {
     // drain this warp's loads still in flight (bounded) before the ring is reused
