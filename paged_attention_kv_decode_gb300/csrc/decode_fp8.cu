@@ -13,20 +13,21 @@
 //   * A unit is 32 tokens (two m16 tiles): at one byte per element the 16-token units of
 //     the bf16 kernel would halve the bytes behind each softmax step.
 //   * Codes become fp16 in registers (cvt.e4m3x2 -> f16x2, exact); the products are fp16
-//     mma.sync with fp32 accumulation.  K: a 32-bit piece of ldmatrix holds four
+//     mma.sync with fp32 accumulation (an e4m3 mma.sync runs as the same conversions and fp16
+//     products, of more operands: 13 % slower).  K: a 32-bit piece of ldmatrix holds four
 //     consecutive dims of a token, so dims are dealt to the k-slots in that order and the
 //     query is loaded to match.  V: ldmatrix.trans of 16-bit pairs gives {two dims} x {two
-//     tokens}; one byte permute splits it into the even and the odd dim's token pair, so
-//     an m16 tile of output rows is 8 even dims followed by 8 odd ones.
+//     tokens}; one byte permute splits it into the even and the odd dim's token pair, so an
+//     m16 tile of output rows is 8 even dims followed by 8 odd ones.
 //   * The query row is scaled by a power of two into fp16's range (its largest element in
 //     [2^14, 2^15)): exact for bf16 elements down to 2^-29 of the largest, and below that
 //     off by at most 2^-40 of it.  fp32 queries are split into two fp16 parts (22 bits).
-//   * The softmax reference is the running maximum minus 14, so that the weights use
-//     fp16's range down to 2^-28 of the largest before they lose bits (fp32 queries: two
-//     fp16 parts again).
-//   * The scales stay out of the codes: a page's K factor multiplies its scores, and each
-//     tile's P V lands in a fresh accumulator that joins O with the page's V factor, so any
-//     spread of scales between pages is held in fp32.
+//   * bf16 queries: a token's weight takes V's page scale along, 2^(z + vb - M), so that P V
+//     accumulates straight into O; its reference M, the running maximum of z + vb minus 14,
+//     leaves fp16 the range down to 2^-38 of the largest.  The sum of weights has a reference
+//     of its own, m, of z alone: any spread of scales between pages is held.
+//   * fp32 queries: weights are two fp16 parts too, and each tile's P V lands in a fresh
+//     accumulator that joins O with the page's factor.
 #include <math.h>
 
 #include <algorithm>
@@ -49,6 +50,7 @@ struct DecodeFp8Params {
 
 constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
 constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
+constexpr float kSlack = 16.f;   // bf16 queries: the sums' reference moves when it is exceeded by 2^16
 
 template <int D>
 struct Fp8DecodeShape {
@@ -59,7 +61,7 @@ struct Fp8DecodeShape {
 
 template <int D, int NW, int STAGES>
 constexpr int fp8_decode_smem_bytes() {
-  return 1024 + NW * STAGES * (Fp8DecodeShape<D>::kStageBytes + 16 + 8);
+  return 1024 + NW * STAGES * (Fp8DecodeShape<D>::kStageBytes + 8 + 8);
 }
 
 // Byte offset of 16-byte chunk c of row `row` in a TMA tile of D-byte rows: 128-byte
@@ -69,151 +71,428 @@ __device__ __forceinline__ uint32_t tile_chunk(int row, int c) {
   return row * D + ((c ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4);
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // The part of (lo, hi) that fp16 `packed` left over, scaled by 2^11, as fp16
 __device__ __forceinline__ uint32_t pack_f16x2_rest(float lo, float hi, uint32_t packed) {
   const float2 v = unpack_f16x2(packed);
   return pack_f16x2((lo - v.x) * 2048.f, (hi - v.y) * 2048.f);
 }
 
-// One work item: the tokens [t0, t1) of KV head g of sequence s; arguments as for
-// decode_bf16_item (decode.cu).  scales: this warp group's [NW][STAGES] page factors.
-template <int D, typename QT, int NW, int STAGES, typename Sync>
-__device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                                const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
-                                                float4* scales, int part, int g, int s, int orow, int t0, int t1,
-                                                int warp, int lane, int tid, int& kb, Sync sync) {
+// A warp's units of one work item, the tokens [t0, t1) of KV head g of sequence s, and the
+// loads of their K and V into the warp's ring.
+// Lane l holds unit k = 32 * window + l of the current window: the TMA row of its page(s)
+// and the scale bytes (k0, v0, k1, v1); and the block ids of the next window's unit.
+// -box (a box outside the tensor, read as zeros) stands for a bad block id or a page past
+// the range.  Ids, then loads of K and V, then scales (and the caller's query): the item's
+// first bytes wait for one lookup only.
+template <int D, int NW, int STAGES>
+struct Fp8Units {
   using Shape = Fp8DecodeShape<D>;
-  constexpr int KS = Shape::kSteps;
-  constexpr bool SPLIT = sizeof(QT) == 4;  // two fp16 parts of q and P
-  const DecodeParams& p = pp.d;
-  unsigned int* const status = &g_status_decode_fp8;
+  const CUtensorMap *tmK, *tmV;
+  const DecodeFp8Params& pp;
+  const int32_t* bt_row;
+  uint8_t* ring;      // this warp's stages
+  uint64_t* bars;
+  uint32_t* scales;   // scale bytes of the unit in each stage
+  int g, t1, warp, lane, u0, n_my, kb, box;
+  bool small_pages;   // two pages per unit, else part of one
+  int cur0, cur1, id0, id1;  // TMA rows of the current window, ids of the next one
+  uint32_t cur_sc, next_sc;
+  uint64_t policy;
 
-  // this warp's units: u0 + warp + k * NW, k < n_my
-  const int u0 = t0 / kUnit8;
-  const int n_units = (t1 - u0 * kUnit8 + kUnit8 - 1) / kUnit8;
-  const int n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
-  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
-  const bool small_pages = p.bs == 16;        // two pages per unit, else part of one
-  const int box = small_pages ? 16 : kUnit8;  // rows of a TMA box
+  __device__ __forceinline__ Fp8Units(const CUtensorMap& tmK_, const CUtensorMap& tmV_, const DecodeFp8Params& pp_,
+                                      uint8_t* smem, uint64_t* bars_, uint32_t* scales_, int g_, int s, int t0, int t1_,
+                                      int warp_, int lane_, int kb_)
+      : tmK(&tmK_), tmV(&tmV_), pp(pp_), bt_row(pp_.d.block_table + (size_t)s * pp_.d.max_blocks),
+        ring(smem + warp_ * STAGES * Shape::kStageBytes), bars(bars_ + warp_ * STAGES),
+        scales(scales_ + warp_ * STAGES), g(g_), t1(t1_), warp(warp_), lane(lane_), kb(kb_) {
+    // this warp's units: u0 + warp + k * NW, k < n_my
+    u0 = t0 / kUnit8;
+    const int n_units = (t1 - u0 * kUnit8 + kUnit8 - 1) / kUnit8;
+    n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
+    small_pages = pp.d.bs == 16;
+    box = small_pages ? 16 : kUnit8;
+    policy = l2_policy_evict_first();
+    int b0, b1;
+    load_ids(lane, b0, b1);
+    load_ids(32 + lane, id0, id1);
+    check_ids(lane, b0, b1);
+    set_rows(lane, b0, b1);
+    cur_sc = next_sc = 0;
+    for (int k = 0; k < prologue(); ++k) issue(k);
+    cur_sc = load_scales(b0, b1);
+  }
 
-  // Lane l holds unit k = 32 * window + l of the current window: the TMA row of its page(s)
-  // and the scale bytes (k0, v0, k1, v1); and the block ids of the next window's unit.
-  // -box (a box outside the tensor, read as zeros) stands for a bad block id or a page past
-  // the range.  Ids, then loads of K and V, then scales and query: the item's first bytes
-  // wait for one lookup only.
-  auto load_ids = [&](int k, int& b0, int& b1) {  // -1: no such page (no id is flagged here)
+  __device__ __forceinline__ int prologue() const { return n_my < STAGES ? n_my : STAGES; }
+  __device__ __forceinline__ int first_token(int k) const { return (u0 + warp + k * NW) * kUnit8; }
+  __device__ __forceinline__ int stage(int k) const { return (kb + k) % STAGES; }
+  __device__ __forceinline__ uint32_t tile(int k) const { return smem_u32(ring + stage(k) * Shape::kStageBytes); }
+
+  // Wait for unit k (all lanes).  False: the wait gave up.
+  __device__ __forceinline__ bool wait(int k) {
+    const bool landed = mbar_wait(&bars[stage(k)], ((kb + k) / STAGES) & 1, &g_status_decode_fp8);
+    const bool ok = __all_sync(0xffffffffu, landed);
+    __syncwarp();  // the unit's scale bytes, written by one lane
+    return ok;
+  }
+
+  // Unit k is consumed: load the one that takes its stage.
+  __device__ __forceinline__ void release(int k) {
+    __syncwarp();
+    if (k + STAGES < n_my) {
+      issue(k + STAGES);
+      put_scales(k + STAGES);
+    }
+  }
+
+  // A wait for unit k gave up: drain the loads still in flight (bounded) before the ring is reused.
+  __device__ __forceinline__ void drain(int k) {
+    for (int kk = k + 1; kk < n_my && kk < k + STAGES; ++kk)
+      mbar_wait(&bars[stage(kk)], ((kb + kk) / STAGES) & 1, &g_status_decode_fp8);
+  }
+
+  __device__ __forceinline__ void load_ids(int k, int& b0, int& b1) const {  // -1: no such page
     b0 = b1 = -1;
     if (k >= n_my) return;
-    const int tok = (u0 + warp + k * NW) * kUnit8;
-    b0 = __ldg(bt_row + tok / p.bs);
+    const int tok = first_token(k);
+    b0 = __ldg(bt_row + tok / pp.d.bs);
     if (small_pages && tok + 16 < t1) b1 = __ldg(bt_row + tok / 16 + 1);
-  };
-  auto check = [&](int b, bool wanted) {  // a bad id (flagged) becomes -1
-    if (b >= 0 && b < p.num_blocks) return b;
-    if (wanted) atomicOr(status, METIS_STATUS_BAD_BLOCK_ID);
+  }
+
+  __device__ __forceinline__ int check_id(int b, bool wanted) const {  // a bad id (flagged) becomes -1
+    if (b >= 0 && b < pp.d.num_blocks) return b;
+    if (wanted) atomicOr(&g_status_decode_fp8, METIS_STATUS_BAD_BLOCK_ID);
     return -1;
-  };
-  auto load_scales = [&](int b0, int b1) -> uint32_t {
-    uint32_t sc = 0x7f7f7f7fu;
+  }
+
+  __device__ __forceinline__ void check_ids(int k, int& b0, int& b1) const {
+    b0 = check_id(b0, k < n_my);
+    b1 = check_id(b1, k < n_my && small_pages && first_token(k) + 16 < t1);
+  }
+
+  __device__ __forceinline__ void set_rows(int k, int b0, int b1) {  // of the (checked) ids of unit k
+    cur0 = b0 < 0 ? -box : b0 * pp.d.bs + first_token(k) % pp.d.bs;
+    cur1 = b1 < 0 ? -box : b1 * 16;
+  }
+
+  // (k0, v0, k1, v1); a bad page has scale 1, the second page of a unit that has one the first's
+  __device__ __forceinline__ uint32_t load_scales(int b0, int b1) const {
+    uint32_t sc = 0x7f7fu;
     if (b0 >= 0) {
-      const size_t at = (size_t)b0 * p.G + g;
+      const size_t at = (size_t)b0 * pp.d.G + g;
       sc = __ldg(pp.k_scale + at) | ((uint32_t)__ldg(pp.v_scale + at) << 8);
-      sc |= sc << 16;
     }
-    if (small_pages) {
-      sc = (sc & 0xffffu) | 0x7f7f0000u;
-      if (b1 >= 0) {
-        const size_t at = (size_t)b1 * p.G + g;
-        sc = (sc & 0xffffu) | ((uint32_t)__ldg(pp.k_scale + at) << 16) | ((uint32_t)__ldg(pp.v_scale + at) << 24);
-      }
+    sc |= sc << 16;
+    if (small_pages && b1 >= 0) {
+      const size_t at = (size_t)b1 * pp.d.G + g;
+      sc = (sc & 0xffffu) | ((uint32_t)__ldg(pp.k_scale + at) << 16) | ((uint32_t)__ldg(pp.v_scale + at) << 24);
     }
     return sc;
-  };
-  int cur0, cur1, id0, id1;  // TMA rows of the current window, ids of the next one
-  uint32_t cur_sc = 0, next_sc = 0;
-  auto rows_of = [&](int k, int b0, int b1) {  // current window := unit k with these (checked) ids
-    const int tok = (u0 + warp + k * NW) * kUnit8;
-    cur0 = b0 < 0 ? -box : b0 * p.bs + tok % p.bs;
-    cur1 = b1 < 0 ? -box : b1 * 16;
-  };
-  auto checked = [&](int k, int& b0, int& b1) {
-    const int tok = (u0 + warp + k * NW) * kUnit8;
-    b0 = check(b0, k < n_my);
-    b1 = check(b1, k < n_my && small_pages && tok + 16 < t1);
-  };
-  const uint64_t policy = l2_policy_evict_first();
+  }
 
   // K and V of unit k (called by all lanes, in order k = 0, 1, 2, ...)
-  auto issue = [&](int k) {
+  __device__ __forceinline__ void issue(int k) {
     if (k > 0 && (k & 31) == 0) {
-      rows_of(k + lane, id0, id1);  // (checked with their scales, half a window ago)
+      set_rows(k + lane, id0, id1);  // (checked with their scales, half a window ago)
       cur_sc = next_sc;
       load_ids(k + 32 + lane, id0, id1);
     }
-    const int st = (kb + k) % STAGES;
-    uint8_t* base = smem + (warp * STAGES + st) * Shape::kStageBytes;
-    uint64_t* bar = &bars[warp * STAGES + st];
+    uint8_t* base = ring + stage(k) * Shape::kStageBytes;
+    uint64_t* bar = &bars[stage(k)];
     if (lane == 0) mbar_arrive_expect_tx(bar, Shape::kStageBytes);
     const int r0 = __shfl_sync(0xffffffffu, cur0, k & 31);
     const int r1 = __shfl_sync(0xffffffffu, cur1, k & 31);
     __syncwarp();
     // one box per lane: lanes 0, 1 the K page(s), lanes 2, 3 the V page(s)
     if (lane < 4 && (small_pages || !(lane & 1)))
-      tma_load_3d(base + (lane >> 1) * Shape::kTileBytes + (lane & 1) * (16 * D), lane < 2 ? &tmK : &tmV, bar, 0, g,
+      tma_load_3d(base + (lane >> 1) * Shape::kTileBytes + (lane & 1) * (16 * D), lane < 2 ? tmK : tmV, bar, 0, g,
                   (lane & 1) ? r1 : r0, policy);
-  };
-  // its page factors (after the loads: they wait for the scale bytes)
-  auto put_scales = [&](int k) {
-    if (lane == (k & 31))
-      scales[warp * STAGES + (kb + k) % STAGES] =
-          make_float4(scale_of_byte(cur_sc & 255u), scale_of_byte((cur_sc >> 8) & 255u),
-                      scale_of_byte((cur_sc >> 16) & 255u), scale_of_byte(cur_sc >> 24));
+  }
+
+  // its scale bytes (after its loads: they wait for the lookup)
+  __device__ __forceinline__ void put_scales(int k) {
+    if (lane == (k & 31)) scales[stage(k)] = cur_sc;
     if ((k & 31) == 16) {  // the next window's ids are here by now
-      checked(k + 16 + lane, id0, id1);
+      check_ids(k + 16 + lane, id0, id1);
       next_sc = load_scales(id0, id1);
     }
-  };
-  const int prologue = n_my < STAGES ? n_my : STAGES;
-  {
-    int b0, b1;
-    load_ids(lane, b0, b1);
-    load_ids(32 + lane, id0, id1);
-    checked(lane, b0, b1);
-    rows_of(lane, b0, b1);
-    for (int k = 0; k < prologue; ++k) issue(k);
-    cur_sc = load_scales(b0, b1);
   }
+};
+
+// The warps' softmax states meet in the ring's memory (every warp is done with it after the
+// first sync) and become the item's result.  o[c]: dims d0(c), d1(c) of the lane for
+// heads 2 q4, 2 q4 + 1, unnormalised relative to 2^m0, 2^m1.
+template <int D, typename QT, int NW, typename Sync, typename Dims>
+__device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem, const uint64_t (*o)[2], float m0,
+                                            float m1, float l0, float l1, int part, int g, int s, int orow, int warp,
+                                            int lane, int tid, Sync sync, Dims dims) {
+  constexpr int KS = Fp8DecodeShape<D>::kSteps;
+  l0 = warp_sum_xor(l0, 4);
+  l1 = warp_sum_xor(l1, 4);
+  sync();  // every warp is done with its ring
+  float* cm = reinterpret_cast<float*>(smem);
+  float* cl = cm + NW * 8;
+  float* co = cl + NW * 8;
+  if (lane < 4) {
+    cm[warp * 8 + 2 * lane] = m0;
+    cm[warp * 8 + 2 * lane + 1] = m1;
+    cl[warp * 8 + 2 * lane] = l0;
+    cl[warp * 8 + 2 * lane + 1] = l1;
+  }
+#pragma unroll
+  for (int c = 0; c < KS; ++c)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint64_t*>(co + ((size_t)warp * D + dims(c, i)) * 8 + 2 * (lane & 3)) = o[c][i];
+  sync();
+  combine_and_store<QT, NW>(p, cm, cl, co, part, g, s, orow, tid);
+}
+
+// ---------------------------------------------------------------------------
+// bf16 queries
+// ---------------------------------------------------------------------------
+// One work item; arguments as for decode_bf16_item (decode.cu).  scales: the group's
+// [NW][STAGES] scale bytes.
+template <int D, int NW, int STAGES, typename Sync>
+__device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                                     const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
+                                                     uint32_t* scales, int part, int g, int s, int orow, int t0, int t1,
+                                                     int warp, int lane, int tid, int& kb, Sync sync) {
+  constexpr int KS = Fp8DecodeShape<D>::kSteps;
+  const DecodeParams& p = pp.d;
+  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, scales, g, s, t0, t1, warp, lane, kb);
 
   // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
   // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
   const int q4 = lane & 3, rA = lane >> 2;
-  uint32_t qf[KS][2], ql[SPLIT ? KS : 1][2];
+  uint32_t qf[KS][2];
   float undo;  // what the row's scaling has to be undone by
   {
     const bool live = rA < p.r;
-    const QT* qrow = reinterpret_cast<const QT*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D + 4 * q4;
+    const __nv_bfloat16* qrow =
+        reinterpret_cast<const __nv_bfloat16*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D + 4 * q4;
+    uint2 v[KS];
+    uint32_t top = 0;  // bf16 magnitudes order like their bits
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      v[kk] = live ? *reinterpret_cast<const uint2*>(qrow + kk * 16) : make_uint2(0u, 0u);
+      top = max_u16x2(max_u16x2(top, v[kk].x & 0x7fff7fffu), v[kk].y & 0x7fff7fffu);
+    }
+    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top >> 16, top & 0xffffu);
+    // up = 2^(14 - e) for the largest element m 2^e, 1 <= m < 2, and undo = 1 / up, from the
+    // exponent field e + 127 (held above 14: a row below 2^-112 is scaled by 2^126)
+    const uint32_t field = min(max(top >> 7, 15u), 254u);
+    const float up = __uint_as_float((268u - field) << 23);
+    undo = __uint_as_float((field - 14u) << 23);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      qf[kk][0] = pack_f16x2(__uint_as_float(v[kk].x << 16) * up, __uint_as_float(v[kk].x & 0xffff0000u) * up);
+      qf[kk][1] = pack_f16x2(__uint_as_float(v[kk].y << 16) * up, __uint_as_float(v[kk].y & 0xffff0000u) * up);
+    }
+  }
+  // factor of this thread's score columns, heads 2 q4 and 2 q4 + 1
+  const float f0 = p.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * q4);
+  const float f1 = p.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * q4 + 4);
+
+  float o[KS][4];  // [chunk][even, odd dim of lane / 4] x {head 2 q4, head 2 q4 + 1}, relative to 2^M0, 2^M1
+#pragma unroll
+  for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float M0 = -INFINITY, M1 = -INFINITY;                      // references of O: z + V's page exponent
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references of the sums: z
+
+  for (int k = 0; k < units.prologue(); ++k) units.put_scales(k);
+
+  // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
+  const int lrow = (lane & 8) + (lane & 7), lchunk = lane >> 4;
+
+  int k = 0;
+  bool ok = true;
+  for (; k < units.n_my; ++k) {
+    if (!units.wait(k)) {  // leave the loop together
+      ok = false;
+      break;
+    }
+    const int tok0 = units.first_token(k);
+    const uint32_t kbase = units.tile(k);
+    const uint32_t vbase = kbase + Fp8DecodeShape<D>::kTileBytes;
+    const uint32_t sc = units.scales[units.stage(k)];
+    const float vb[2] = {exponent_of_byte((sc >> 8) & 255u), exponent_of_byte(sc >> 24)};
+
+    // S^T (16 tokens x 8 heads, twice) = K codes . q^T
+    float x[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KS; kk += 2)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
+        ldsm_x4(kbase + tile_chunk<D>(16 * h + lrow, kk + lchunk), r0, r1, r2, r3);
+        unpack_e4m3x4(r0, a0, a2);
+        unpack_e4m3x4(r1, a1, a3);
+        mma_f16_16816(x[h], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+        unpack_e4m3x4(r2, a0, a2);
+        unpack_e4m3x4(r3, a1, a3);
+        mma_f16_16816(x[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
+      }
+
+    // y = z + vb in log2 units (z: the scaled score); the thread holds tokens rA, rA + 8 of
+    // each tile, heads 2 q4, 2 q4 + 1
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float ks = scale_of_byte((h ? sc >> 16 : sc) & 255u), a = f0 * ks, b = f1 * ks;
+      x[h][0] = fmaf(x[h][0], a, vb[h]);
+      x[h][1] = fmaf(x[h][1], b, vb[h]);
+      x[h][2] = fmaf(x[h][2], a, vb[h]);
+      x[h][3] = fmaf(x[h][3], b, vb[h]);
+    }
+    // valid tokens of the two tiles (the first tile of a range may start before it)
+    const int nv0 = tok0 < t0 ? 0 : min(16, t1 - tok0), nv1 = max(0, min(16, t1 - tok0 - 16));
+    const bool partial = nv0 < 16 || nv1 < 16;
+    if (partial) {
+      if (rA >= nv0) x[0][0] = x[0][1] = -INFINITY;
+      if (rA + 8 >= nv0) x[0][2] = x[0][3] = -INFINITY;
+      if (rA >= nv1) x[1][0] = x[1][1] = -INFINITY;
+      if (rA + 8 >= nv1) x[1][2] = x[1][3] = -INFINITY;
+    }
+    const float y0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), 4);
+    const float y1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), 4);
+    // the sums' reference: at least the unit's largest z, above it by at most the exponents'
+    // spread (where that is large, from the scores themselves)
+    const bool apart = fabsf(vb[0] - vb[1]) > 32.f;
+    const float vb_min = fminf(vb[0], vb[1]);
+    float z0 = y0 - vb_min, z1 = y1 - vb_min;
+    if (apart) {
+      z0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]) - vb[0], fmaxf(x[1][0], x[1][2]) - vb[1]), 4);
+      z1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]) - vb[0], fmaxf(x[1][1], x[1][3]) - vb[1]), 4);
+    }
+    // references move rarely: weights reach 2^15 before O's does
+    const bool grow0 = y0 - kRefDown > M0 + 1.f || z0 > m0 + kSlack, grow1 = y1 - kRefDown > M1 + 1.f || z1 > m1 + kSlack;
+    if (__any_sync(0xffffffffu, grow0 || grow1)) {
+      const float N0 = fmaxf(M0, y0 - kRefDown), N1 = fmaxf(M1, y1 - kRefDown);
+      const float n0 = fmaxf(m0, z0), n1 = fmaxf(m1, z1);
+      const float al0 = exp2_approx(M0 - N0), al1 = exp2_approx(M1 - N1);
+      l0 *= exp2_approx(m0 - n0);
+      l1 *= exp2_approx(m1 - n1);
+      M0 = N0;
+      M1 = N1;
+      m0 = n0;
+      m1 = n1;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        o[i][0] *= al0;
+        o[i][1] *= al1;
+        o[i][2] *= al0;
+        o[i][3] *= al1;
+      }
+    }
+    // P^T (tokens x heads) -> B operand (k = token, n = head) by 8x8 transposes
+    uint32_t pb[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float e0 = exp2_approx(x[h][0] - M0), e1 = exp2_approx(x[h][1] - M1);
+      const float e2 = exp2_approx(x[h][2] - M0), e3 = exp2_approx(x[h][3] - M1);
+      pb[h][0] = movmatrix_trans(pack_f16x2(e0, e1));
+      pb[h][1] = movmatrix_trans(pack_f16x2(e2, e3));
+      // sums of 2^(z - m): the weights without V's exponent
+      if (!apart) {
+        l0 = fmaf(e0 + e2, exp2_approx(M0 - vb[h] - m0), l0);
+        l1 = fmaf(e1 + e3, exp2_approx(M1 - vb[h] - m1), l1);
+      } else {
+        l0 += exp2_approx(x[h][0] - vb[h] - m0) + exp2_approx(x[h][2] - vb[h] - m0);
+        l1 += exp2_approx(x[h][1] - vb[h] - m1) + exp2_approx(x[h][3] - vb[h] - m1);
+      }
+    }
+
+    // O^T (D x 8 heads) += V^T codes (D x 32 tokens) . P^T
+    auto pv = [&](const uint32_t (&mask)[2][2], bool masked) {
+#pragma unroll
+      for (int c = 0; c < KS; c += 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[4];
+          ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, c + lchunk), r[0], r[1], r[2], r[3]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t lo = r[2 * u], hi = r[2 * u + 1];
+            if (masked) {
+              lo &= mask[h][0];
+              hi &= mask[h][1];
+            }
+            uint32_t a0, a1, a2, a3;
+            unpack_e4m3x4(__byte_perm(lo, 0, 0x3120), a0, a1);  // even, odd dims of tokens 0..7
+            unpack_e4m3x4(__byte_perm(hi, 0, 0x3120), a2, a3);  // ... of tokens 8..15
+            mma_f16_16816(o[c + u], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          }
+        }
+    };
+    if (!partial) {
+      const uint32_t none[2][2] = {{0u, 0u}, {0u, 0u}};
+      pv(none, false);
+    } else {
+      // Rows past the range may hold anything (NaN codes included): zero them in the V^T
+      // fragments so that 0 * NaN cannot poison O.
+      uint32_t mask[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = 2 * q4, nv = h ? nv1 : nv0;
+        mask[h][0] = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
+        mask[h][1] = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
+      }
+      pv(mask, true);
+    }
+    units.release(k);
+  }
+  if (!ok) units.drain(k);
+
+  // O relative to the sums' references (a warp without units: nothing)
+  const float b0 = m0 == -INFINITY ? 0.f : exp2_approx(M0 - m0), b1 = m1 == -INFINITY ? 0.f : exp2_approx(M1 - m1);
+  uint64_t o2[KS][2];
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    o2[c][0] = f2_pack(o[c][0] * b0, o[c][1] * b1);
+    o2[c][1] = f2_pack(o[c][2] * b0, o[c][3] * b1);
+  }
+  combine_fp8<D, __nv_bfloat16, NW>(p, smem, o2, m0, m1, l0, l1, part, g, s, orow, warp, lane, tid, sync,
+                                    [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  kb += units.n_my;
+  return ok;
+}
+
+// ---------------------------------------------------------------------------
+// fp32 queries
+// ---------------------------------------------------------------------------
+// The same item for fp32 q and out: two fp16 parts of q and of the weights, and fresh
+// accumulators per tile.
+template <int D, int NW, int STAGES, typename Sync>
+__device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                                    const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
+                                                    uint32_t* scales, int part, int g, int s, int orow, int t0, int t1,
+                                                    int warp, int lane, int tid, int& kb, Sync sync) {
+  constexpr int KS = Fp8DecodeShape<D>::kSteps;
+  const DecodeParams& p = pp.d;
+  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, scales, g, s, t0, t1, warp, lane, kb);
+
+  // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
+  // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
+  const int q4 = lane & 3, rA = lane >> 2;
+  uint32_t qf[KS][2], ql[KS][2];
+  float undo;  // what the row's scaling has to be undone by
+  {
+    const bool live = rA < p.r;
+    const float* qrow = reinterpret_cast<const float*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D + 4 * q4;
     float x[KS][4];
     float top = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
-      if (SPLIT) {
-        const float4 v = live ? *reinterpret_cast<const float4*>(qrow + kk * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[kk][0] = v.x;
-        x[kk][1] = v.y;
-        x[kk][2] = v.z;
-        x[kk][3] = v.w;
-      } else {
-        const uint2 v = live ? *reinterpret_cast<const uint2*>(qrow + kk * 16) : make_uint2(0u, 0u);
-        x[kk][0] = __uint_as_float(v.x << 16);
-        x[kk][1] = __uint_as_float(v.x & 0xffff0000u);
-        x[kk][2] = __uint_as_float(v.y << 16);
-        x[kk][3] = __uint_as_float(v.y & 0xffff0000u);
-      }
+      const float4 v = live ? *reinterpret_cast<const float4*>(qrow + kk * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[kk][0] = v.x;
+      x[kk][1] = v.y;
+      x[kk][2] = v.z;
+      x[kk][3] = v.w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[kk][i]));
     }
@@ -230,10 +509,8 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       for (int i = 0; i < 4; ++i) x[kk][i] *= up;
       qf[kk][0] = pack_f16x2(x[kk][0], x[kk][1]);
       qf[kk][1] = pack_f16x2(x[kk][2], x[kk][3]);
-      if (SPLIT) {
-        ql[kk][0] = pack_f16x2_rest(x[kk][0], x[kk][1], qf[kk][0]);
-        ql[kk][1] = pack_f16x2_rest(x[kk][2], x[kk][3], qf[kk][1]);
-      }
+      ql[kk][0] = pack_f16x2_rest(x[kk][0], x[kk][1], qf[kk][0]);
+      ql[kk][1] = pack_f16x2_rest(x[kk][2], x[kk][3], qf[kk][1]);
     }
   }
   // factor of this thread's score columns, heads 2 q4 and 2 q4 + 1
@@ -245,25 +522,22 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
   for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = 0ull;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  for (int k = 0; k < prologue; ++k) put_scales(k);
+  for (int k = 0; k < units.prologue(); ++k) units.put_scales(k);
 
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (((lane >> 3) & 1) << 3) + (lane & 7), lchunk = lane >> 4;
 
   int k = 0;
   bool ok = true;
-  for (; k < n_my; ++k) {
-    const int st = (kb + k) % STAGES;
-    const bool landed = mbar_wait(&bars[warp * STAGES + st], ((kb + k) / STAGES) & 1, status);
-    if (!__all_sync(0xffffffffu, landed)) {  // leave the loop together
+  for (; k < units.n_my; ++k) {
+    if (!units.wait(k)) {  // leave the loop together
       ok = false;
       break;
     }
-    __syncwarp();  // the unit's page factors, written by one lane
-    const int tok0 = (u0 + warp + k * NW) * kUnit8;
-    const uint32_t kbase = smem_u32(smem + (warp * STAGES + st) * Shape::kStageBytes);
-    const uint32_t vbase = kbase + Shape::kTileBytes;
-    const float4 sc = scales[warp * STAGES + st];
+    const int tok0 = units.first_token(k);
+    const uint32_t kbase = units.tile(k);
+    const uint32_t vbase = kbase + Fp8DecodeShape<D>::kTileBytes;
+    const uint32_t sc = units.scales[units.stage(k)];
     // valid tokens of the two tiles (the first tile of a range may start before it)
     int nv[2];
     nv[0] = tok0 < t0 ? 0 : min(16, t1 - tok0);
@@ -284,11 +558,11 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
         unpack_e4m3x4(r0, a0, a2);
         unpack_e4m3x4(r1, a1, a3);
         mma_f16_16816(acc[h], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
-        if (SPLIT) mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+        mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
         unpack_e4m3x4(r2, a0, a2);
         unpack_e4m3x4(r3, a1, a3);
         mma_f16_16816(acc[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
-        if (SPLIT) mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk + 1][0], ql[kk + 1][1]);
+        mma_f16_16816(acl[h], a0, a1, a2, a3, ql[kk + 1][0], ql[kk + 1][1]);
       }
     }
 
@@ -296,10 +570,10 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
     float x[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float kf = h ? sc.z : sc.x;
+      const float kf = scale_of_byte((h ? sc >> 16 : sc) & 255u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = SPLIT ? fmaf(acl[h][i], 1.f / 2048.f, acc[h][i]) : acc[h][i];
+        const float a = fmaf(acl[h][i], 1.f / 2048.f, acc[h][i]);
         x[h][i] = a * (((i & 1) ? f1 : f0) * kf);
         if (rA + ((i & 2) << 2) >= nv[h]) x[h][i] = -INFINITY;
       }
@@ -334,10 +608,8 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       const uint32_t a = pack_f16x2(e[0], e[1]), b = pack_f16x2(e[2], e[3]);
       pb[h][0] = movmatrix_trans(a);
       pb[h][1] = movmatrix_trans(b);
-      if (SPLIT) {
-        pl[h][0] = movmatrix_trans(pack_f16x2_rest(e[0], e[1], a));
-        pl[h][1] = movmatrix_trans(pack_f16x2_rest(e[2], e[3], b));
-      }
+      pl[h][0] = movmatrix_trans(pack_f16x2_rest(e[0], e[1], a));
+      pl[h][1] = movmatrix_trans(pack_f16x2_rest(e[2], e[3], b));
     }
 
     // Rows past the range may hold anything (NaN codes included): zero them in the V^T
@@ -357,7 +629,7 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
       for (int h = 0; h < 2; ++h) {
         uint32_t r[4];
         ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, c + lchunk), r[0], r[1], r[2], r[3]);
-        const float vf = h ? sc.w : sc.y;
+        const float vf = scale_of_byte((h ? sc >> 24 : sc >> 8) & 255u);
         const uint64_t vf2 = f2_pack(vf, vf);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -371,53 +643,21 @@ __device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CU
           unpack_e4m3x4(__byte_perm(hi, 0, 0x3120), a2, a3);  // ... of tokens 8..15
           float t[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16_16816(t, a0, a1, a2, a3, pb[h][0], pb[h][1]);
-          if (SPLIT) {
-            float tl[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(tl, a0, a1, a2, a3, pl[h][0], pl[h][1]);
+          float tl[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16_16816(tl, a0, a1, a2, a3, pl[h][0], pl[h][1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = fmaf(tl[i], 1.f / 2048.f, t[i]);
-          }
+          for (int i = 0; i < 4; ++i) t[i] = fmaf(tl[i], 1.f / 2048.f, t[i]);
           o[c + u][0] = f2_fma(f2_pack(t[0], t[1]), vf2, o[c + u][0]);
           o[c + u][1] = f2_fma(f2_pack(t[2], t[3]), vf2, o[c + u][1]);
         }
       }
     }
-    __syncwarp();
-    if (k + STAGES < n_my) {
-      issue(k + STAGES);
-      put_scales(k + STAGES);
-    }
+    units.release(k);
   }
-  if (!ok) {
-    // drain this warp's loads still in flight (bounded) before the ring is reused
-    for (int kk = k + 1; kk < n_my && kk < k + STAGES; ++kk) {
-      const int st = (kb + kk) % STAGES;
-      mbar_wait(&bars[warp * STAGES + st], ((kb + kk) / STAGES) & 1, status);
-    }
-  }
-
-  l0 = warp_sum_xor(l0, 4);
-  l1 = warp_sum_xor(l1, 4);
-  sync();  // every warp is done with its ring
-
-  float* cm = reinterpret_cast<float*>(smem);
-  float* cl = cm + NW * 8;
-  float* co = cl + NW * 8;
-  if (lane < 4) {
-    cm[warp * 8 + 2 * lane] = m0;
-    cm[warp * 8 + 2 * lane + 1] = m1;
-    cl[warp * 8 + 2 * lane] = l0;
-    cl[warp * 8 + 2 * lane + 1] = l1;
-  }
-#pragma unroll
-  for (int c = 0; c < KS; ++c) {
-    float* at = co + ((size_t)warp * D + c * 16 + 2 * rA) * 8 + 2 * q4;
-    *reinterpret_cast<uint64_t*>(at) = o[c][0];
-    *reinterpret_cast<uint64_t*>(at + 8) = o[c][1];
-  }
-  sync();
-  combine_and_store<QT, NW>(p, cm, cl, co, part, g, s, orow, tid);
-  kb += n_my;
+  if (!ok) units.drain(k);
+  combine_fp8<D, float, NW>(p, smem, o, m0, m1, l0, l1, part, g, s, orow, warp, lane, tid, sync,
+                            [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  kb += units.n_my;
   return ok;
 }
 
@@ -449,8 +689,8 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
   const DecodeParams& p = pp.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
-  float4* scales = reinterpret_cast<float4*>(smem + NW * STAGES * STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + NW * STAGES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NW * STAGES * STAGE_BYTES);
+  uint32_t* scales = reinterpret_cast<uint32_t*>(bars + NW * STAGES);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -472,8 +712,13 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
   if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
   __syncthreads();  // the barriers are initialised
   int kb = 0;
-  decode_fp8_item<D, QT, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
-                                     kb, [] { __syncthreads(); });
+  auto sync = [] { __syncthreads(); };
+  if constexpr (sizeof(QT) == 4)
+    decode_fp8_item_f32<D, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
+                                       kb, sync);
+  else
+    decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane,
+                                        threadIdx.x, kb, sync);
 }
 
 // ---------------------------------------------------------------------------
@@ -488,7 +733,7 @@ constexpr int kFp8Warps = 6, kFp8Stages = 2;  // per group
 
 template <int D>
 constexpr int dec8_beside_smem_bytes() {
-  constexpr int need = 1024 + kDec8Groups * kFp8Warps * kFp8Stages * (Fp8DecodeShape<D>::kStageBytes + 24);
+  constexpr int need = 1024 + kDec8Groups * kFp8Warps * kFp8Stages * (Fp8DecodeShape<D>::kStageBytes + 16);
   return need > 116 * 1024 ? need : 116 * 1024;  // never two CTAs on one SM
 }
 
@@ -530,8 +775,9 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
   const int grp = threadIdx.x / GT, tid = threadIdx.x - grp * GT;
   const int warp = tid >> 5, lane = tid & 31;
   uint8_t* gsmem = smem + grp * NW * STAGES * STAGE_BYTES;
-  float4* scales = reinterpret_cast<float4*>(smem + kDec8Groups * NW * STAGES * STAGE_BYTES) + grp * NW * STAGES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDec8Groups * NW * STAGES * (STAGE_BYTES + 16)) + grp * NW * STAGES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDec8Groups * NW * STAGES * STAGE_BYTES) + grp * NW * STAGES;
+  uint32_t* scales =
+      reinterpret_cast<uint32_t*>(smem + kDec8Groups * NW * STAGES * (STAGE_BYTES + 8)) + grp * NW * STAGES;
   if (tid == 0) {
     if (grp == 0) {
       tma_prefetch_desc(&tmK);
@@ -560,8 +806,8 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
     if (!decode_range<__nv_bfloat16>(p, 0, g, s, orow, t0, t1, tid, GT, &g_status_decode_fp8)) continue;
     // A wait that gave up (flagged) is seen by its warp only: every warp of the group
     // still reaches the item's barriers and the next one above, where they all stop.
-    if (!decode_fp8_item<D, __nv_bfloat16, NW, STAGES>(tmK, tmV, pp, gsmem, bars, scales, 0, g, s, orow, t0, t1, warp,
-                                                       lane, tid, kb, gsync) &&
+    if (!decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, gsmem, bars, scales, 0, g, s, orow, t0, t1, warp, lane, tid,
+                                             kb, gsync) &&
         lane == 0)
       gave_up[grp] = 1;
   }

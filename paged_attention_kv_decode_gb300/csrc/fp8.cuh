@@ -14,6 +14,11 @@ __device__ __forceinline__ float scale_of_byte(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
 }
 
+// Its exponent, b - 127 (NaN for 255)
+__device__ __forceinline__ float exponent_of_byte(uint32_t b) {
+  return b == 255 ? __uint_as_float(0x7fc00000u) : (float)((int)b - 127);
+}
+
 // The exponent byte of the smallest 2^k with amax <= 448 * 2^k, at least 1 (2^-126).
 // amax is finite and >= 0: with amax = m * 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8, that
 // is k = e - 8, or e - 7 when m > 1.75.
@@ -80,6 +85,34 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// A pair of fp16 pairs as two e4m3 parts, x = hi + lo up to lo's rounding (|x| at most 448).
+// Results: the codes of (a lo, a hi, b lo, b hi), low byte first.
+__device__ __forceinline__ void split_e4m3x2x2(uint32_t a, uint32_t b, uint32_t& hi, uint32_t& lo) {
+  const uint16_t ha = e4m3x2_of_f16x2(a), hb = e4m3x2_of_f16x2(b);
+  const uint32_t ba = f16x2_of_e4m3x2(ha), bb = f16x2_of_e4m3x2(hb);
+  // exact: x and its code lie within a factor of two or in the subnormals of one grid
+  const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&ba));
+  const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bb));
+  hi = ha | ((uint32_t)hb << 16);
+  lo = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&ra)) |
+       ((uint32_t)e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rb)) << 16);
+}
+
+// Two floats to fp16 (round to nearest even)
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four bf16 values times `up` (a power of two) as two e4m3 parts
+__device__ __forceinline__ void split_e4m3x4(const uint2& v, float up, uint32_t& hi, uint32_t& lo) {
+  const uint64_t up2 = f2_pack(up, up);
+  float x0, x1, x2, x3;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)), up2), x0, x1);
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)), up2), x2, x3);
+  split_e4m3x2x2(pack_f16x2(x0, x1), pack_f16x2(x2, x3), hi, lo);
 }
 
 // D(16x8, f32) += A(16x16, fp16, row) * B(16x8, fp16, col)

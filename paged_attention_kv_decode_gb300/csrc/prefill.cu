@@ -392,28 +392,13 @@ __device__ __forceinline__ float split_query_row(uint8_t* tile, int row) {
   top = max(top >> 16, top & 0xffffu);
   const uint32_t field = max(top >> 7, 8u);  // exponent field of the largest element
   const float up = __uint_as_float((261u - min(field, 254u)) << 23);
-  const uint64_t up2 = f2_pack(up, up);
 #pragma unroll
   for (int c = 0; c < kChunks; c += 2) {
     uint32_t hi[4], lo[4];
-    const uint32_t x[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint16_t h[2], l[2];
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const uint32_t w2 = x[2 * e + a];
-        float x0, x1;
-        f2_unpack(f2_mul(f2_pack(__uint_as_float(w2 << 16), __uint_as_float(w2 & 0xffff0000u)), up2), x0, x1);
-        const __half2 y = __floats2half2_rn(x0, x1);
-        h[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&y));
-        const uint32_t back = f16x2_of_e4m3x2(h[a]);
-        const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&back));  // exact
-        l[a] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
-      }
-      hi[e] = h[0] | ((uint32_t)h[1] << 16);
-      lo[e] = l[0] | ((uint32_t)l[1] << 16);
-    }
+    split_e4m3x4(make_uint2(v[c].x, v[c].y), up, hi[0], lo[0]);
+    split_e4m3x4(make_uint2(v[c].z, v[c].w), up, hi[1], lo[1]);
+    split_e4m3x4(make_uint2(v[c + 1].x, v[c + 1].y), up, hi[2], lo[2]);
+    split_e4m3x4(make_uint2(v[c + 1].z, v[c + 1].w), up, hi[3], lo[3]);
     const int o = c / 2;  // output chunk of the row
     *reinterpret_cast<uint4*>(at + ((o ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     uint8_t* lo_at = D == 128 ? at + kRows * D + ((o ^ (row & 7)) << 4) : at + (((4 + o) ^ (row & 7)) << 4);

@@ -4,14 +4,19 @@ bit, decode and chunked prefill against softmax attention in float64 over the sa
 Tolerances of the attention outputs (derived, not tuned).  With w the exact softmax
 weights of a row and A = sum_t w_t |v_t| per output column:
 
-* scores are fp32 sums of exact products.  A sum of D products, added 16 at a time in
+* scores are fp32 sums of exact products.  A sum of D products, added 16 or 32 at a time in
   the tensor core with at most one unit of 2^-23 of the partial sums lost per addition,
   is off by at most 24 * 2^-23 < 2^-18 of sum |q k|; the multiplication by the scales, the
-  subtraction of the maximum and ex2.approx add less than 2^-21 (1 + sum |q k| scale).  So
-  ds = 2^-18 * T + 2^-20 bounds the error of a score, T = scale * max_t sum_d |q_d k_td|, and
-  a weight is off by a factor within 1 +- 2 ds (numerator and denominator): 2 ds A.
-* each weight is rounded once for the P V product: fp16 2^-11, bf16 2^-8 (half a step,
-  relative; smaller for the fp32 path's two fp16 parts, 2^-21): that times A.
+  subtraction of the maximum and ex2.approx add less than 2^-21 (1 + sum |q k| scale).
+  Prefill chunks take the query as two e4m3 parts at one power of two, the row's largest
+  element in [2^7, 2^8): an element is off by at most half of e4m3's smallest step, 2^-10,
+  that is 2^-17 of the largest.  So ds = 2^-18 T + 2^-20 (+ 2^-17 U for prefill) bounds the
+  error of a score, T = |scale| max_t sum_d |q_d k_td|, U = |scale| max_d |q_d| max_t sum_d |k_td|,
+  and a weight is off by a factor within 1 +- 2 ds (numerator and denominator): 2 ds A.
+* each weight is rounded once for the P V product: bf16 2^-8 (half a step, relative; chunks),
+  fp16 2^-11 (decode, bf16 queries), two fp16 parts 2^-21 (fp32): that times A.  fp16 weights
+  are also off by up to 2^-25 where the largest w 2^vb (vb: V's page exponent) of the
+  tokens is 2^14 or more: at most B = 2^-39 max(w 2^vb) sum_t |code_t|.
 * the accumulation of P V and the merges: less than 2^-16 A for the lengths here.
 * the result is rounded once: 2^-8 |o| for bf16.
 
@@ -99,9 +104,13 @@ class Cache:
         return oracle.E4M3_VALUES[codes[page, t % self.bs]] * (2.0 ** (b[page].astype(np.float64) - 127))[:, :, None]
 
 
-def attention(cache, q, rows, scale, p_step):
+STEP = {BF16: 2.0 ** -11, F32: 2.0 ** -21}  # decode's rounding of a weight
+CHUNK_STEP = 2.0 ** -8                      # prefill's
+
+
+def attention(cache, q, rows, scale, p_step, parts=False):
     """q [R, H, D] float64; rows[i] = (sequence, visible tokens).  Returns out, its bound
-    without the final rounding, lse and its bound."""
+    without the final rounding, lse and its bound.  parts: queries as two e4m3 parts."""
     R, H, D = q.shape
     r = H // cache.G
     out, tol = np.zeros((R, H, D)), np.zeros((R, H, D))
@@ -111,8 +120,11 @@ def attention(cache, q, rows, scale, p_step):
         if n == 0:
             continue
         if s not in kept:
-            kept = {s: (cache.rows(s, cache.lens[s], "k"), cache.rows(s, cache.lens[s], "v"))}
-        k, v = (x[:n] for x in kept[s])
+            L = cache.lens[s]
+            t = np.arange(L)
+            kept = {s: (cache.rows(s, L, "k"), cache.rows(s, L, "v"),
+                        2.0 ** (cache.vs[cache.table[s, t // cache.bs]].astype(np.float64) - 127))}
+        k, v, unit = (x[:n] for x in kept[s])
         for h in range(H):
             g = h // r
             z = scale * (k[:, g] @ q[i, h])
@@ -122,7 +134,10 @@ def attention(cache, q, rows, scale, p_step):
             out[i, h] = w @ v[:, g]
             lse[i, h] = m + np.log(e.sum())
             ds = 2.0 ** -18 * abs(scale) * (np.abs(k[:, g]) @ np.abs(q[i, h])).max() + 2.0 ** -20
-            tol[i, h] = (2 * ds + p_step + 2.0 ** -16) * (w @ np.abs(v[:, g]))
+            if parts:
+                ds += 2.0 ** -17 * abs(scale) * np.abs(q[i, h]).max() * np.abs(k[:, g]).sum(axis=1).max()
+            B = 2.0 ** -39 * (w * unit[:, g]).max() * (np.abs(v[:, g]) / unit[:, g, None]).sum(axis=0)
+            tol[i, h] = (2 * ds + p_step + 2.0 ** -16) * (w @ np.abs(v[:, g])) + B
             ltol[i, h] = ds + 2.0 ** -21 * abs(lse[i, h])
     return out, tol, lse, ltol
 
@@ -333,7 +348,7 @@ def decode_case(rng, lens, r, G, D, bs, dtype, scale=None, spread=2.0, partition
     out, lse = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, c.sl, scale, partition_size=partition,
                                               max_seq_len=max_len, workspace=workspace, want_lse=True)
     ref, tol, rl, lt = attention(c, q.double().numpy(), list(enumerate(lens)), scale,
-                                 2.0 ** -11 if dtype == BF16 else 2.0 ** -21)
+                                 STEP[dtype])
     check(out, ref, tol, dtype, "out")
     check_lse(lse, rl, lt)
     assert pa.metis_read_status() == 0
@@ -363,6 +378,27 @@ def test_decode_scales_of_any_spread(dtype, bs):
     decode_case(np.random.default_rng(4), [400, 90, 33], 4, 2, 128, bs, dtype, scale=2.0 ** -30, spread=30.0)
 
 
+@pytest.mark.parametrize("partition", [0, 512])
+def test_decode_long_flat_tail_beside_one_large_weight(partition):
+    """One token 2^18 times as heavy as each of 6,000 others: their sum still counts."""
+    rng = np.random.default_rng(14)
+    n, D, bs = 6000, 64, 16
+    c = Cache(rng, [n], 1, D, bs, spread=0.0)
+    t = np.arange(n)
+    page = c.table[0, t // bs]
+    c.k[page, t % bs, 0] = 0
+    c.k[page[0], 0, 0] = oracle.encode_e4m3(np.full(D, 1.0))
+    c.ks[:] = 127
+    c.put()
+    q = torch.full((1, 4, D), 18.0 * np.log(2) / D).to(BF16)
+    for dtype in (BF16, F32):
+        out, lse = pa.metis_paged_attn_decode_fp8(gpu(q, dtype), *c.dev, c.bt, c.sl, 1.0, partition_size=partition,
+                                                  want_lse=True)
+        ref, tol, rl, lt = attention(c, q.double().numpy(), [(0, n)], 1.0, STEP[dtype])
+        check(out, ref, tol, dtype, "out")
+        check_lse(lse, rl, lt)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_decode_softmax_scales(scale):
     decode_case(np.random.default_rng(5), [300, 1, 40], 4, 2, 64, 16, BF16, scale=scale, spread=0.5)
@@ -384,7 +420,7 @@ def test_decode_query_of_any_size():
             one.__dict__.update(c.__dict__)
             one.table, one.lens = c.table[s:s + 1], lens[s:s + 1]
             ref, tol, rl, lt = attention(one, qt[s:s + 1].double().numpy(), [(0, lens[s])], scale,
-                                         2.0 ** -11 if dtype == BF16 else 2.0 ** -21)
+                                         STEP[dtype])
             check(out, ref, tol, dtype, "out")
             check_lse(lse, rl, lt)
 
@@ -414,7 +450,7 @@ def test_decode_bad_contents():
     assert pa.metis_read_status(clear=True) == pa.STATUS_BAD_BLOCK_ID
     b = c.table[0, 2]
     c.k[b], c.v[b], c.ks[b], c.vs[b] = 0, 0, 127, 127  # the page reads as zeros
-    ref, tol, _, _ = attention(c, q.double().numpy(), list(enumerate(lens)), 0.125, 2.0 ** -11)
+    ref, tol, _, _ = attention(c, q.double().numpy(), list(enumerate(lens)), 0.125, STEP[BF16])
     check(out, ref, tol, BF16, "out")
     # longer than the table row: clamped to it
     out, _ = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, i32([999, 40]), 0.125, max_seq_len=1000,
@@ -435,7 +471,7 @@ def prefill_case(rng, spans, r, G, D, bs, scale=None, spread=2.0):
     pa.metis_read_status(clear=True)
     out, lse = pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32(cu), *c.dev, c.bt, c.sl, scale, want_lse=True)
     rows = [(s, n - m + i + 1) for s, (n, m) in enumerate(spans) for i in range(m)]
-    ref, tol, rl, lt = attention(c, q.double().numpy(), rows, scale, 2.0 ** -8)
+    ref, tol, rl, lt = attention(c, q.double().numpy(), rows, scale, CHUNK_STEP, parts=True)
     check(out, ref, tol, BF16, "out")
     check_lse(lse, rl, lt)
     assert pa.metis_read_status() == 0
@@ -501,12 +537,12 @@ def test_steps_of_a_serving_loop():
         c.v, c.vs = oracle.write_cache(kv[1], c.v, c.vs, cu, c.table, done)
         c.lens = [int(n) for n in done]
         rows = [(s, int(done[s]) - m + i + 1) for s, m in enumerate(step) for i in range(m)]
-        ref, tol, rl, lt = attention(c, q.double().numpy(), rows, scale, 2.0 ** -8)
+        ref, tol, rl, lt = attention(c, q.double().numpy(), rows, scale, CHUNK_STEP, parts=True)
         check(out, ref, tol, BF16, "prefill")
         check_lse(lse, rl, lt)
         if max(step) == 1:
             o2, _ = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, sl, scale, max_seq_len=160, partition_size=32)
-            ref, tol, _, _ = attention(c, q.double().numpy(), list(enumerate(c.lens)), scale, 2.0 ** -11)
+            ref, tol, _, _ = attention(c, q.double().numpy(), list(enumerate(c.lens)), scale, STEP[BF16])
             check(o2, ref, tol, BF16, "decode")
     # read back as pages of a bf16 cache, and attend over those
     pages = [-(-n // bs) for n in c.lens]
@@ -517,6 +553,7 @@ def test_steps_of_a_serving_loop():
     for s in range(S):
         bt[s, :pages[s]] = np.arange(first[s], first[s + 1])
     o3, _ = pa.metis_paged_attn_decode(gpu(q), k.view(-1, bs, G, D), v.view(-1, bs, G, D), i32(bt), i32(c.lens), scale)
+    # (that kernel's weights are bf16: 2^-8)
     ref, tol, _, _ = attention(c, q.double().numpy(), list(enumerate(c.lens)), scale, 2.0 ** -8)
     check(o3, ref, tol, BF16, "bf16 decode over the pages read back")
 
@@ -556,7 +593,7 @@ def test_graph_of_a_decode_step_replayed():
         c.k, c.ks = oracle.write_cache(kv[0], c.k, c.ks, [0, 1, 2, 3], c.table, lens)
         c.v, c.vs = oracle.write_cache(kv[1], c.v, c.vs, [0, 1, 2, 3], c.table, lens)
         c.lens = [int(n) for n in lens]
-        ref, tol, _, _ = attention(c, qh.double().numpy(), list(enumerate(c.lens)), 0.125, 2.0 ** -11)
+        ref, tol, _, _ = attention(c, qh.double().numpy(), list(enumerate(c.lens)), 0.125, STEP[BF16])
         check(out, ref, tol, BF16, "out")
         for s in range(3):
             assert np.array_equal(v[s * cap:s * cap + c.lens[s]].double().cpu().numpy(), c.rows(s, c.lens[s], "v"))
@@ -602,10 +639,10 @@ def test_offsets_past_32_bits():
     assert np.array_equal(k.double().cpu().numpy(), c.rows(0, n, "k"))
     assert np.array_equal(v.double().cpu().numpy(), c.rows(0, n, "v"))
     out, _ = pa.metis_paged_attn_decode_fp8(gpu(q[-1:]), *dev, i32(table), i32([n]), 0.09)
-    ref, tol, _, _ = attention(c, q[-1:].double().numpy(), [(0, n)], 0.09, 2.0 ** -11)
+    ref, tol, _, _ = attention(c, q[-1:].double().numpy(), [(0, n)], 0.09, STEP[BF16])
     check(out, ref, tol, BF16, "decode")
     out, _ = pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32([0, n]), *dev, i32(table), i32([n]), 0.09)
-    ref, tol, _, _ = attention(c, q.double().numpy(), [(0, i + 1) for i in range(n)], 0.09, 2.0 ** -8)
+    ref, tol, _, _ = attention(c, q.double().numpy(), [(0, i + 1) for i in range(n)], 0.09, CHUNK_STEP, parts=True)
     check(out, ref, tol, BF16, "prefill")
 
 
