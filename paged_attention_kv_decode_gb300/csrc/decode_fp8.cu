@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
@@ -61,7 +62,7 @@ struct Fp8DecodeShape {
 
 template <int D, int NW, int STAGES>
 constexpr int fp8_decode_smem_bytes() {
-  return 1024 + NW * STAGES * (Fp8DecodeShape<D>::kStageBytes + 8 + 8);
+  return 1024 + NW * STAGES * (Fp8DecodeShape<D>::kStageBytes + 8);
 }
 
 // Byte offset of 16-byte chunk c of row `row` in a TMA tile of D-byte rows: 128-byte
@@ -92,23 +93,27 @@ struct Fp8Units {
   const int32_t* bt_row;
   uint8_t* ring;      // this warp's stages
   uint64_t* bars;
-  uint32_t* scales;   // scale bytes of the unit in each stage
-  int g, t1, warp, lane, u0, n_my, kb, box;
+  int g, t1, warp, lane, u0, n_my, box;
+  int st;             // stage of the unit to consume, which the unit STAGES later takes
+  uint32_t phase;     // ... and the parity of its barrier
   bool small_pages;   // two pages per unit, else part of one
-  int cur0, cur1, id0, id1;  // TMA rows of the current window, ids of the next one
-  uint32_t cur_sc, next_sc;
+  int cur0, cur1, id0, id1;  // TMA rows of the window being issued, ids of the next one
+  uint32_t cur_sc, next_sc;  // scale bytes alike
+  uint32_t use_sc;           // scale bytes of the window being consumed
   uint64_t policy;
 
   __device__ __forceinline__ Fp8Units(const CUtensorMap& tmK_, const CUtensorMap& tmV_, const DecodeFp8Params& pp_,
-                                      uint8_t* smem, uint64_t* bars_, uint32_t* scales_, int g_, int s, int t0, int t1_,
-                                      int warp_, int lane_, int kb_)
+                                      uint8_t* smem, uint64_t* bars_, int g_, int s, int t0, int t1_, int warp_,
+                                      int lane_, int kb)
       : tmK(&tmK_), tmV(&tmV_), pp(pp_), bt_row(pp_.d.block_table + (size_t)s * pp_.d.max_blocks),
-        ring(smem + warp_ * STAGES * Shape::kStageBytes), bars(bars_ + warp_ * STAGES),
-        scales(scales_ + warp_ * STAGES), g(g_), t1(t1_), warp(warp_), lane(lane_), kb(kb_) {
+        ring(smem + warp_ * STAGES * Shape::kStageBytes), bars(bars_ + warp_ * STAGES), g(g_), t1(t1_), warp(warp_),
+        lane(lane_) {
     // this warp's units: u0 + warp + k * NW, k < n_my
     u0 = t0 / kUnit8;
     const int n_units = (t1 - u0 * kUnit8 + kUnit8 - 1) / kUnit8;
     n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
+    st = kb % STAGES;
+    phase = (kb / STAGES) & 1;
     small_pages = pp.d.bs == 16;
     box = small_pages ? 16 : kUnit8;
     policy = l2_policy_evict_first();
@@ -117,37 +122,57 @@ struct Fp8Units {
     load_ids(32 + lane, id0, id1);
     check_ids(lane, b0, b1);
     set_rows(lane, b0, b1);
-    cur_sc = next_sc = 0;
-    for (int k = 0; k < prologue(); ++k) issue(k);
-    cur_sc = load_scales(b0, b1);
+    for (int k = 0; k < STAGES && k < n_my; ++k) load(k, (st + k) % STAGES);
+    next_sc = 0;
+    cur_sc = use_sc = load_scales(b0, b1);
   }
 
-  __device__ __forceinline__ int prologue() const { return n_my < STAGES ? n_my : STAGES; }
   __device__ __forceinline__ int first_token(int k) const { return (u0 + warp + k * NW) * kUnit8; }
-  __device__ __forceinline__ int stage(int k) const { return (kb + k) % STAGES; }
-  __device__ __forceinline__ uint32_t tile(int k) const { return smem_u32(ring + stage(k) * Shape::kStageBytes); }
+  __device__ __forceinline__ uint32_t tile() const { return smem_u32(ring + st * Shape::kStageBytes); }
 
-  // Wait for unit k (all lanes).  False: the wait gave up.
-  __device__ __forceinline__ bool wait(int k) {
-    const bool landed = mbar_wait(&bars[stage(k)], ((kb + k) / STAGES) & 1, &g_status_decode_fp8);
-    const bool ok = __all_sync(0xffffffffu, landed);
-    __syncwarp();  // the unit's scale bytes, written by one lane
-    return ok;
+  // Scale bytes (k0, v0, k1, v1) of unit k, the next to be consumed (all lanes)
+  __device__ __forceinline__ uint32_t scales(int k) {
+    // the window being issued is STAGES units ahead: still the same one where a window begins
+    if ((k & 31) == 0) use_sc = cur_sc;
+    return __shfl_sync(0xffffffffu, use_sc, k & 31);
+  }
+
+  // Wait for the next unit (all lanes).  False: the wait gave up.
+  __device__ __forceinline__ bool wait() {
+    return __all_sync(0xffffffffu, mbar_wait(&bars[st], phase, &g_status_decode_fp8));
   }
 
   // Unit k is consumed: load the one that takes its stage.
   __device__ __forceinline__ void release(int k) {
     __syncwarp();
-    if (k + STAGES < n_my) {
-      issue(k + STAGES);
-      put_scales(k + STAGES);
+    const int n = k + STAGES;
+    if (n < n_my) {
+      if ((n & 31) == 0) {
+        set_rows(n + lane, id0, id1);  // (checked with their scales, half a window ago)
+        cur_sc = next_sc;
+        load_ids(n + 32 + lane, id0, id1);
+      }
+      load(n, st);
+      if ((n & 31) == 16) {            // the next window's ids are here by now
+        check_ids(n + 16 + lane, id0, id1);
+        next_sc = load_scales(id0, id1);
+      }
+    }
+    if (++st == STAGES) {
+      st = 0;
+      phase ^= 1;
     }
   }
 
-  // A wait for unit k gave up: drain the loads still in flight (bounded) before the ring is reused.
+  // The wait for unit k gave up: drain the loads still in flight (bounded) before the ring is reused.
   __device__ __forceinline__ void drain(int k) {
-    for (int kk = k + 1; kk < n_my && kk < k + STAGES; ++kk)
-      mbar_wait(&bars[stage(kk)], ((kb + kk) / STAGES) & 1, &g_status_decode_fp8);
+    for (int n = k + 1; n < n_my && n < k + STAGES; ++n) {
+      if (++st == STAGES) {
+        st = 0;
+        phase ^= 1;
+      }
+      mbar_wait(&bars[st], phase, &g_status_decode_fp8);
+    }
   }
 
   __device__ __forceinline__ void load_ids(int k, int& b0, int& b1) const {  // -1: no such page
@@ -189,15 +214,10 @@ struct Fp8Units {
     return sc;
   }
 
-  // K and V of unit k (called by all lanes, in order k = 0, 1, 2, ...)
-  __device__ __forceinline__ void issue(int k) {
-    if (k > 0 && (k & 31) == 0) {
-      set_rows(k + lane, id0, id1);  // (checked with their scales, half a window ago)
-      cur_sc = next_sc;
-      load_ids(k + 32 + lane, id0, id1);
-    }
-    uint8_t* base = ring + stage(k) * Shape::kStageBytes;
-    uint64_t* bar = &bars[stage(k)];
+  // K and V of unit k of the current window into a stage (all lanes)
+  __device__ __forceinline__ void load(int k, int stage) {
+    uint8_t* base = ring + stage * Shape::kStageBytes;
+    uint64_t* bar = &bars[stage];
     if (lane == 0) mbar_arrive_expect_tx(bar, Shape::kStageBytes);
     const int r0 = __shfl_sync(0xffffffffu, cur0, k & 31);
     const int r1 = __shfl_sync(0xffffffffu, cur1, k & 31);
@@ -206,15 +226,6 @@ struct Fp8Units {
     if (lane < 4 && (small_pages || !(lane & 1)))
       tma_load_3d(base + (lane >> 1) * Shape::kTileBytes + (lane & 1) * (16 * D), lane < 2 ? tmK : tmV, bar, 0, g,
                   (lane & 1) ? r1 : r0, policy);
-  }
-
-  // its scale bytes (after its loads: they wait for the lookup)
-  __device__ __forceinline__ void put_scales(int k) {
-    if (lane == (k & 31)) scales[stage(k)] = cur_sc;
-    if ((k & 31) == 16) {  // the next window's ids are here by now
-      check_ids(k + 16 + lane, id0, id1);
-      next_sc = load_scales(id0, id1);
-    }
   }
 };
 
@@ -250,16 +261,15 @@ __device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem
 // ---------------------------------------------------------------------------
 // bf16 queries
 // ---------------------------------------------------------------------------
-// One work item; arguments as for decode_bf16_item (decode.cu).  scales: the group's
-// [NW][STAGES] scale bytes.
+// One work item; arguments as for decode_bf16_item (decode.cu).
 template <int D, int NW, int STAGES, typename Sync>
 __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                                      const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
-                                                     uint32_t* scales, int part, int g, int s, int orow, int t0, int t1,
-                                                     int warp, int lane, int tid, int& kb, Sync sync) {
+                                                     int part, int g, int s, int orow, int t0, int t1, int warp,
+                                                     int lane, int tid, int& kb, Sync sync) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   const DecodeParams& p = pp.d;
-  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, scales, g, s, t0, t1, warp, lane, kb);
+  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, g, s, t0, t1, warp, lane, kb);
 
   // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
   // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
@@ -301,30 +311,23 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
   float M0 = -INFINITY, M1 = -INFINITY;                      // references of O: z + V's page exponent
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references of the sums: z
 
-  for (int k = 0; k < units.prologue(); ++k) units.put_scales(k);
-
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (lane & 8) + (lane & 7), lchunk = lane >> 4;
 
-  int k = 0;
-  bool ok = true;
-  for (; k < units.n_my; ++k) {
-    if (!units.wait(k)) {  // leave the loop together
-      ok = false;
-      break;
-    }
-    const int tok0 = units.first_token(k);
-    const uint32_t kbase = units.tile(k);
+  // One unit.  ODD: tiles that are partly outside the range, or pages whose V scales are far
+  // apart; everything else runs without a branch but the one of moving references.
+  auto consume = [&](auto odd_unit, int tok0, uint32_t sc) {
+    constexpr bool ODD = decltype(odd_unit)::value;
+    const uint32_t kbase = units.tile();
     const uint32_t vbase = kbase + Fp8DecodeShape<D>::kTileBytes;
-    const uint32_t sc = units.scales[units.stage(k)];
     const float vb[2] = {exponent_of_byte((sc >> 8) & 255u), exponent_of_byte(sc >> 24)};
 
-    // S^T (16 tokens x 8 heads, twice) = K codes . q^T
-    float x[2][4];
+    // S^T (16 tokens x 8 heads, twice) = K codes . q^T, in two chains per tile
+    float x[2][4], x2[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[h][i] = 0.f;
+      for (int i = 0; i < 4; ++i) x[h][i] = x2[h][i] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; kk += 2)
 #pragma unroll
@@ -336,42 +339,64 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
         mma_f16_16816(x[h], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
         unpack_e4m3x4(r2, a0, a2);
         unpack_e4m3x4(r3, a1, a3);
-        mma_f16_16816(x[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
+        mma_f16_16816(x2[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
       }
+    // V's pieces, on their way during the softmax
+    uint32_t v[KS / 2][2][4];
+#pragma unroll
+    for (int c = 0; c < KS / 2; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, 2 * c + lchunk), v[c][h][0], v[c][h][1], v[c][h][2],
+                      v[c][h][3]);
 
     // y = z + vb in log2 units (z: the scaled score); the thread holds tokens rA, rA + 8 of
     // each tile, heads 2 q4, 2 q4 + 1
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float ks = scale_of_byte((h ? sc >> 16 : sc) & 255u), a = f0 * ks, b = f1 * ks;
-      x[h][0] = fmaf(x[h][0], a, vb[h]);
-      x[h][1] = fmaf(x[h][1], b, vb[h]);
-      x[h][2] = fmaf(x[h][2], a, vb[h]);
-      x[h][3] = fmaf(x[h][3], b, vb[h]);
+      x[h][0] = fmaf(x[h][0] + x2[h][0], a, vb[h]);
+      x[h][1] = fmaf(x[h][1] + x2[h][1], b, vb[h]);
+      x[h][2] = fmaf(x[h][2] + x2[h][2], a, vb[h]);
+      x[h][3] = fmaf(x[h][3] + x2[h][3], b, vb[h]);
     }
-    // valid tokens of the two tiles (the first tile of a range may start before it)
-    const int nv0 = tok0 < t0 ? 0 : min(16, t1 - tok0), nv1 = max(0, min(16, t1 - tok0 - 16));
-    const bool partial = nv0 < 16 || nv1 < 16;
-    if (partial) {
-      if (rA >= nv0) x[0][0] = x[0][1] = -INFINITY;
-      if (rA + 8 >= nv0) x[0][2] = x[0][3] = -INFINITY;
-      if (rA >= nv1) x[1][0] = x[1][1] = -INFINITY;
-      if (rA + 8 >= nv1) x[1][2] = x[1][3] = -INFINITY;
+    if (ODD) {
+      // valid tokens of the two tiles (the first tile of a range may start before it)
+      const int t = 2 * q4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int nv = h ? min(16, t1 - tok0 - 16) : tok0 < t0 ? 0 : min(16, t1 - tok0);
+        if (rA >= nv) x[h][0] = x[h][1] = -INFINITY;
+        if (rA + 8 >= nv) x[h][2] = x[h][3] = -INFINITY;
+        // Rows past the range may hold anything (NaN codes included): zero them in the V^T
+        // fragments so that 0 * NaN cannot poison O.
+        const uint32_t lo = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
+        const uint32_t hi = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int c = 0; c < KS / 2; ++c) {
+          v[c][h][0] &= lo;
+          v[c][h][1] &= hi;
+          v[c][h][2] &= lo;
+          v[c][h][3] &= hi;
+        }
+      }
     }
     const float y0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), 4);
     const float y1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), 4);
     // the sums' reference: at least the unit's largest z, above it by at most the exponents'
-    // spread (where that is large, from the scores themselves)
-    const bool apart = fabsf(vb[0] - vb[1]) > 32.f;
-    const float vb_min = fminf(vb[0], vb[1]);
-    float z0 = y0 - vb_min, z1 = y1 - vb_min;
-    if (apart) {
+    // spread (ODD: from the scores themselves)
+    float z0, z1;
+    if (ODD) {
       z0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]) - vb[0], fmaxf(x[1][0], x[1][2]) - vb[1]), 4);
       z1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]) - vb[0], fmaxf(x[1][1], x[1][3]) - vb[1]), 4);
+    } else {
+      const float vb_min = fminf(vb[0], vb[1]);
+      z0 = y0 - vb_min;
+      z1 = y1 - vb_min;
     }
     // references move rarely: weights reach 2^15 before O's does
-    const bool grow0 = y0 - kRefDown > M0 + 1.f || z0 > m0 + kSlack, grow1 = y1 - kRefDown > M1 + 1.f || z1 > m1 + kSlack;
-    if (__any_sync(0xffffffffu, grow0 || grow1)) {
+    const bool grow = y0 - kRefDown > M0 + 1.f || z0 > m0 + kSlack || y1 - kRefDown > M1 + 1.f || z1 > m1 + kSlack;
+    if (__any_sync(0xffffffffu, grow)) {
       const float N0 = fmaxf(M0, y0 - kRefDown), N1 = fmaxf(M1, y1 - kRefDown);
       const float n0 = fmaxf(m0, z0), n1 = fmaxf(m1, z1);
       const float al0 = exp2_approx(M0 - N0), al1 = exp2_approx(M1 - N1);
@@ -398,52 +423,43 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
       pb[h][0] = movmatrix_trans(pack_f16x2(e0, e1));
       pb[h][1] = movmatrix_trans(pack_f16x2(e2, e3));
       // sums of 2^(z - m): the weights without V's exponent
-      if (!apart) {
-        l0 = fmaf(e0 + e2, exp2_approx(M0 - vb[h] - m0), l0);
-        l1 = fmaf(e1 + e3, exp2_approx(M1 - vb[h] - m1), l1);
-      } else {
+      if (ODD) {
         l0 += exp2_approx(x[h][0] - vb[h] - m0) + exp2_approx(x[h][2] - vb[h] - m0);
         l1 += exp2_approx(x[h][1] - vb[h] - m1) + exp2_approx(x[h][3] - vb[h] - m1);
+      } else {
+        l0 = fmaf(e0 + e2, exp2_approx(M0 - vb[h] - m0), l0);
+        l1 = fmaf(e1 + e3, exp2_approx(M1 - vb[h] - m1), l1);
       }
     }
-
     // O^T (D x 8 heads) += V^T codes (D x 32 tokens) . P^T
-    auto pv = [&](const uint32_t (&mask)[2][2], bool masked) {
 #pragma unroll
-      for (int c = 0; c < KS; c += 2)
+    for (int c = 0; c < KS / 2; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[4];
-          ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, c + lchunk), r[0], r[1], r[2], r[3]);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t lo = r[2 * u], hi = r[2 * u + 1];
-            if (masked) {
-              lo &= mask[h][0];
-              hi &= mask[h][1];
-            }
-            uint32_t a0, a1, a2, a3;
-            unpack_e4m3x4(__byte_perm(lo, 0, 0x3120), a0, a1);  // even, odd dims of tokens 0..7
-            unpack_e4m3x4(__byte_perm(hi, 0, 0x3120), a2, a3);  // ... of tokens 8..15
-            mma_f16_16816(o[c + u], a0, a1, a2, a3, pb[h][0], pb[h][1]);
-          }
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a0, a1, a2, a3;
+          unpack_e4m3x4(__byte_perm(v[c][h][2 * u], 0, 0x3120), a0, a1);      // even, odd dims of tokens 0..7
+          unpack_e4m3x4(__byte_perm(v[c][h][2 * u + 1], 0, 0x3120), a2, a3);  // ... of tokens 8..15
+          mma_f16_16816(o[2 * c + u], a0, a1, a2, a3, pb[h][0], pb[h][1]);
         }
-    };
-    if (!partial) {
-      const uint32_t none[2][2] = {{0u, 0u}, {0u, 0u}};
-      pv(none, false);
-    } else {
-      // Rows past the range may hold anything (NaN codes included): zero them in the V^T
-      // fragments so that 0 * NaN cannot poison O.
-      uint32_t mask[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = 2 * q4, nv = h ? nv1 : nv0;
-        mask[h][0] = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
-        mask[h][1] = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
-      }
-      pv(mask, true);
+  };
+
+  int k = 0;
+  bool ok = true;
+  for (; k < units.n_my; ++k) {
+    const uint32_t sc = units.scales(k);
+    const int tok0 = units.first_token(k);
+    if (!units.wait()) {  // leave the loop together
+      ok = false;
+      break;
     }
+    const int apart = (int)((sc >> 8) & 255u) - (int)(sc >> 24);
+    const bool nan_scale = ((sc >> 8) & 255u) == 255u || (sc >> 24) == 255u;
+    if (tok0 < t0 || tok0 + kUnit8 > t1 || abs(apart) > 32 || nan_scale)
+      consume(std::true_type{}, tok0, sc);
+    else
+      consume(std::false_type{}, tok0, sc);
     units.release(k);
   }
   if (!ok) units.drain(k);
@@ -470,11 +486,11 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
 template <int D, int NW, int STAGES, typename Sync>
 __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                                     const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
-                                                    uint32_t* scales, int part, int g, int s, int orow, int t0, int t1,
-                                                    int warp, int lane, int tid, int& kb, Sync sync) {
+                                                    int part, int g, int s, int orow, int t0, int t1, int warp, int lane,
+                                                    int tid, int& kb, Sync sync) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   const DecodeParams& p = pp.d;
-  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, scales, g, s, t0, t1, warp, lane, kb);
+  Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, g, s, t0, t1, warp, lane, kb);
 
   // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4; chunk kk's slots
   // are dims 16 kk + 4 (lane % 4) + {0, 1} and + {2, 3}
@@ -522,7 +538,6 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
   for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = 0ull;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  for (int k = 0; k < units.prologue(); ++k) units.put_scales(k);
 
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (((lane >> 3) & 1) << 3) + (lane & 7), lchunk = lane >> 4;
@@ -530,14 +545,14 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
   int k = 0;
   bool ok = true;
   for (; k < units.n_my; ++k) {
-    if (!units.wait(k)) {  // leave the loop together
+    const uint32_t sc = units.scales(k);
+    if (!units.wait()) {  // leave the loop together
       ok = false;
       break;
     }
     const int tok0 = units.first_token(k);
-    const uint32_t kbase = units.tile(k);
+    const uint32_t kbase = units.tile();
     const uint32_t vbase = kbase + Fp8DecodeShape<D>::kTileBytes;
-    const uint32_t sc = units.scales[units.stage(k)];
     // valid tokens of the two tiles (the first tile of a range may start before it)
     int nv[2];
     nv[0] = tok0 < t0 ? 0 : min(16, t1 - tok0);
@@ -690,7 +705,6 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NW * STAGES * STAGE_BYTES);
-  uint32_t* scales = reinterpret_cast<uint32_t*>(bars + NW * STAGES);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -714,10 +728,10 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
   int kb = 0;
   auto sync = [] { __syncthreads(); };
   if constexpr (sizeof(QT) == 4)
-    decode_fp8_item_f32<D, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
+    decode_fp8_item_f32<D, NW, STAGES>(tmK, tmV, pp, smem, bars, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
                                        kb, sync);
   else
-    decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, smem, bars, scales, part, g, s, s, t0, t1, warp, lane,
+    decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, smem, bars, part, g, s, s, t0, t1, warp, lane,
                                         threadIdx.x, kb, sync);
 }
 
@@ -733,7 +747,7 @@ constexpr int kFp8Warps = 6, kFp8Stages = 2;  // per group
 
 template <int D>
 constexpr int dec8_beside_smem_bytes() {
-  constexpr int need = 1024 + kDec8Groups * kFp8Warps * kFp8Stages * (Fp8DecodeShape<D>::kStageBytes + 16);
+  constexpr int need = 1024 + kDec8Groups * kFp8Warps * kFp8Stages * (Fp8DecodeShape<D>::kStageBytes + 8);
   return need > 116 * 1024 ? need : 116 * 1024;  // never two CTAs on one SM
 }
 
@@ -776,8 +790,6 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
   const int warp = tid >> 5, lane = tid & 31;
   uint8_t* gsmem = smem + grp * NW * STAGES * STAGE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDec8Groups * NW * STAGES * STAGE_BYTES) + grp * NW * STAGES;
-  uint32_t* scales =
-      reinterpret_cast<uint32_t*>(smem + kDec8Groups * NW * STAGES * (STAGE_BYTES + 8)) + grp * NW * STAGES;
   if (tid == 0) {
     if (grp == 0) {
       tma_prefetch_desc(&tmK);
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
     if (!decode_range<__nv_bfloat16>(p, 0, g, s, orow, t0, t1, tid, GT, &g_status_decode_fp8)) continue;
     // A wait that gave up (flagged) is seen by its warp only: every warp of the group
     // still reaches the item's barriers and the next one above, where they all stop.
-    if (!decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, gsmem, bars, scales, 0, g, s, orow, t0, t1, warp, lane, tid,
+    if (!decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, gsmem, bars, 0, g, s, orow, t0, t1, warp, lane, tid,
                                              kb, gsync) &&
         lane == 0)
       gave_up[grp] = 1;
