@@ -677,20 +677,28 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 }
 
 // Warps per CTA, ring depth per warp and CTAs per SM that the registers allow.  Measured on a
-// GB300 (32/8 heads, head_dim 128, pages of 16):
-//   unsplit        4 warps, 3 stages, two CTAs per SM: 64 sequences of 512..4096 tokens in
-//                  55.6 us; 4 warps, 2 stages, three CTAs 64.6 us (fewer bytes in flight
-//                  once the long sequences are alone), one warp 118 us
+// GB300 (head_dim 128, pages of 16, bf16 queries; items: (sequence, KV head) pairs):
+//   unsplit        4 warps, 3 stages, two CTAs per SM: 64 sequences of 512..4096 tokens, 32/8
+//                  heads, in 53.6 us; 2 stages and three CTAs 60.9 us (fewer bytes in flight
+//                  once the long sequences are alone), 8 warps and one CTA 68 us.
+//                  head_dim 64 (half the bytes per unit): 8 warps, 2 stages, two CTAs: the same
+//                  batch in 33.6 us, 4 warps and 3 stages 43.9 us
+//   few items      up to one per SM: 8 warps, 3 stages: 8 such sequences in 23.6 us, 4 warps
+//                  31.8 us; 29 sequences up to 6,000 tokens, 28/4 heads, 32.9 and 43.6 us
 //   many partitions  one warp and 2 stages, twelve CTAs per SM: nothing to combine, and a
 //                  partition's start-up (block ids, scales, query) hides behind eleven others:
-//                  8 sequences of 32-128 K in 512-token partitions 245 us, 4 warps 361 us
-//   few partitions  4 warps, 2 stages, three CTAs per SM: 29 sequences up to 6,000 tokens in
-//                  1,024-token partitions, 28/4 heads, 28 us; two CTAs 34 us, one warp 45 us
+//                  8 sequences of 32-128 K in 512-token partitions 248 us, 4 warps and 3
+//                  stages 361 us before other steps
+//   few partitions  4 warps, 2 stages, three CTAs per SM: the 29 sequences in 1,024-token
+//                  partitions 26.8 us; 3 stages and two CTAs 32.5 us, 8 warps 39.7 us
 template <int NW_, int STAGES_, int MIN_CTAS_>
 struct Fp8Plan {
   static constexpr int NW = NW_, STAGES = STAGES_, MIN_CTAS = MIN_CTAS_;
 };
-using Fp8Unsplit = Fp8Plan<4, 3, 2>;
+template <int D>
+using Fp8Unsplit = std::conditional_t<D == 128, Fp8Plan<4, 3, 2>, Fp8Plan<8, 2, 2>>;
+template <int D>
+using Fp8FewItems = std::conditional_t<D == 128, Fp8Plan<8, 3, 1>, Fp8Plan<8, 2, 2>>;
 using Fp8ManyParts = Fp8Plan<1, 2, 12>;
 using Fp8FewParts = Fp8Plan<4, 2, 3>;
 
@@ -872,15 +880,21 @@ static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void
   return launch_dependent(kern, grid, dim3(Plan::NW * 32), (size_t)smem, st, "decode_fp8_kernel launch", tmK, tmV, pp);
 }
 
-// Partitions a launch may hold before one warp each is enough to fill the GPU: twelve on
-// each of 152 SMs, twice over (seq_lens are not known here: the bound counts max_seq_len).
-constexpr long long kManyParts = 2 * 12 * 152;
-
+// The plan by the number of items or partitions against the GPU's SMs (seq_lens are not
+// known here: partitions count max_seq_len).  Many partitions: twelve on each SM, twice over.
 template <int D, typename QT>
 static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st) {
   const DecodeParams& p = pp.d;
-  if (p.partition_size == 0) return launch_fp8<D, QT, Fp8Unsplit>(pp, k_cache, v_cache, st);
-  if ((long long)p.max_parts * p.G * p.S >= kManyParts) return launch_fp8<D, QT, Fp8ManyParts>(pp, k_cache, v_cache, st);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(METIS_E_CUDA, "querying the SM count: %s", cudaGetErrorString(e));
+  const long long items = (long long)p.G * p.S;
+  if (p.partition_size == 0) {
+    if (items <= sms) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
+    return launch_fp8<D, QT, Fp8Unsplit<D>>(pp, k_cache, v_cache, st);
+  }
+  if (p.max_parts * items >= 24ll * sms) return launch_fp8<D, QT, Fp8ManyParts>(pp, k_cache, v_cache, st);
   return launch_fp8<D, QT, Fp8FewParts>(pp, k_cache, v_cache, st);
 }
 
