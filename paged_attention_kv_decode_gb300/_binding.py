@@ -489,6 +489,12 @@ def _fp8_cache(dev: int, k_cache, v_cache, k_scale, v_scale):
                             _on(dev, "v_scale", v_scale, torch.uint8, (nb, G)))
 
 
+def _num_seqs(seq_lens) -> int:
+    if not isinstance(seq_lens, torch.Tensor):
+        raise TypeError("seq_lens must be a torch.Tensor")
+    return seq_lens.numel()
+
+
 def _table(dev: int, block_table, num_seqs: int):
     """Check a block table of num_seqs rows; returns its width and address."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -509,7 +515,7 @@ def metis_reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, k_cache:
     (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
     T = key.shape[0]
     rows = (T, G, D)
-    S = seq_lens.numel()
+    S = _num_seqs(seq_lens)
     width, table = _table(dev, block_table, S)
     rc = lib.metis_reshape_and_cache_fp8(
         _on(dev, "key", key, key.dtype, rows), _on(dev, "value", value, key.dtype, rows), *cache,
@@ -531,7 +537,7 @@ def metis_gather_cache_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale
     lib = _lib or load_library()
     dev = _device_of("k_cache", k_cache, 4)
     (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
-    S = seq_lens.numel()
+    S = _num_seqs(seq_lens)
     width, table = _table(dev, block_table, S)
     lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
     offsets = _on(dev, "row_offsets", row_offsets, torch.int32, (S,))
@@ -630,7 +636,7 @@ def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor,
     (nb, bs, G, D), cache = _fp8_cache(dev, k_cache, v_cache, k_scale, v_scale)
     T, H = q.shape[0], q.shape[1]
     q_at = _on(dev, "q", q, q.dtype, (T, H, D))
-    S = seq_lens.numel()
+    S = _num_seqs(seq_lens)
     cu = _on(dev, "cu_q_lens", cu_q_lens, torch.int32, (S + 1,))
     width, table = _table(dev, block_table, S)
     lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
   const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
   if (b < 0) return;
   uint8_t* const byte_at = (which ? p.scale[1] : p.scale[0]) + (size_t)b * p.G + g;
-  const uint32_t before = live && kept > 0 ? min((uint32_t)*byte_at, 254u) : 0u;
+  const uint32_t before = live && kept > 0 ? min(ld_byte(byte_at), 254u) : 0u;
   bool odd = false;
   float amax = 0.f;
 #pragma unroll
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
     const int top = min(kept, sub * 16 + 16);
     for (int slot = sub * 16 + lane / CPR; slot < top; slot += 32 / CPR) {
       uint4* at = reinterpret_cast<uint4*>(codes + (size_t)slot * p.G * D) + lane % CPR;
-      const uint4 c = *at;
+      const uint4 c = ld_codes(at);
       uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
             const size_t row = ((size_t)b << p.bs_log) + (tok & (p.bs - 1));
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              c[w][u] = __ldg(reinterpret_cast<const Codes*>(p.cache[w] + row * p.G * p.D) + col);
-              byte[w][u] = __ldg(p.scale[w] + (size_t)b * p.G + g);
+              c[w][u] = ld_codes(reinterpret_cast<const Codes*>(p.cache[w] + row * p.G * p.D) + col);
+              byte[w][u] = ld_byte(p.scale[w] + (size_t)b * p.G + g);
             }
           }
         }

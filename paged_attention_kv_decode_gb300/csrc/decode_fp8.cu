@@ -204,12 +204,12 @@ struct Fp8Units {
     uint32_t sc = 0x7f7fu;
     if (b0 >= 0) {
       const size_t at = (size_t)b0 * pp.d.G + g;
-      sc = __ldg(pp.k_scale + at) | ((uint32_t)__ldg(pp.v_scale + at) << 8);
+      sc = ld_byte(pp.k_scale + at) | (ld_byte(pp.v_scale + at) << 8);
     }
     sc |= sc << 16;
     if (small_pages && b1 >= 0) {
       const size_t at = (size_t)b1 * pp.d.G + g;
-      sc = (sc & 0xffffu) | ((uint32_t)__ldg(pp.k_scale + at) << 16) | ((uint32_t)__ldg(pp.v_scale + at) << 24);
+      sc = (sc & 0xffffu) | (ld_byte(pp.k_scale + at) << 16) | (ld_byte(pp.v_scale + at) << 24);
     }
     return sc;
   }

@@ -9,6 +9,16 @@
 
 namespace metis {
 
+// A byte, or 16 bytes, of the cache.  The kernel in front may be the one that wrote them, and
+// this one may have been launched while it ran (pdl_wait comes between): they are read from
+// L2, past an L1 line or the read-only path that still holds what was there before.
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) { return __ldcg(p); }
+
+template <typename T>
+__device__ __forceinline__ T ld_codes(const T* p) {
+  return __ldcg(p);
+}
+
 // 2^(b - 127): b = 0 is the subnormal 2^-127, b = 255 (never written) is NaN
 __device__ __forceinline__ float scale_of_byte(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);

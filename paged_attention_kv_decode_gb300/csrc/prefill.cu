@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         const int b = checked_block(bt_row, pg, p.num_blocks, &g_status_prefill);
         if (b >= 0) {
           rowc = b * p.bs;
-          fk = scale_of_byte(__ldg(p.fp8.k_scale + (size_t)b * p.G + it.g));
-          fv = scale_of_byte(__ldg(p.fp8.v_scale + (size_t)b * p.G + it.g));
+          fk = scale_of_byte(ld_byte(p.fp8.k_scale + (size_t)b * p.G + it.g));
+          fv = scale_of_byte(ld_byte(p.fp8.v_scale + (size_t)b * p.G + it.g));
         }
         return true;
       };

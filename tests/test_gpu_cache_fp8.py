@@ -368,7 +368,24 @@ def test_decode_parity(r, G, D, bs, dtype, partition):
 def test_decode_unranked_batch():
     """More sequences than the longest-first ranking takes."""
     rng = np.random.default_rng(2)
-    decode_case(rng, list(rng.integers(0, 90, 150)), 2, 1, 64, 16, BF16)
+    decode_case(rng, list(rng.integers(0, 90, 200)), 2, 1, 64, 16, BF16)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32), (64, F32)])
+@pytest.mark.parametrize("partition", [0, 16, 256])
+def test_decode_more_items_than_sms(D, dtype, partition):
+    """The plans for large batches: several warps per item, and (many partitions) one."""
+    rng = np.random.default_rng(D + partition)
+    lens = [0, 1, 1100] + [int(n) for n in rng.integers(1, 400, 20)]
+    decode_case(rng, lens, 2, 8, D, 16, dtype, partition=partition)
+
+
+def test_decode_windows_of_32_units():
+    """Sequences whose warps walk several windows of block ids (one warp: 32 units of 32 tokens each)."""
+    rng = np.random.default_rng(15)
+    for bs in (16, 64):
+        decode_case(rng, [9000, 8192, 8191, 1], 1, 1, 64, bs, BF16)
+        decode_case(rng, [5000, 4100], 2, 1, 128, bs, BF16, partition=4096)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -484,6 +501,30 @@ def test_prefill_parity(r, G, D, bs):
     rng = np.random.default_rng(r + G + D + bs)
     prefill_case(rng, [(1, 1), (130, 130), (0, 0), (300, 1), (129, 2), (260, 64), (64, 33), (17, 17), (400, 129)], r, G,
                  D, bs)
+
+
+@pytest.mark.parametrize("r,G,D,bs", [(4, 8, 128, 16), (16, 8, 64, 32), (1, 8, 128, 64)])
+def test_prefill_more_units_than_sms(r, G, D, bs):
+    """Every SM walks several units, some with one query tile and some with two; rows sampled."""
+    rng = np.random.default_rng(r + D)
+    spans = [(int(n) + int(q), int(q)) for n, q in zip(rng.integers(0, 500, 12), rng.integers(60, 420, 12))]
+    spans += [(300, 1), (5, 5), (33, 1)]
+    lens = [n for n, _ in spans]
+    c = Cache(rng, lens, G, D, bs)
+    cu = np.concatenate([[0], np.cumsum([q for _, q in spans])])
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), G * r, D))).to(BF16)
+    pa.metis_read_status(clear=True)
+    call = lambda: pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32(cu), *c.dev, c.bt, c.sl, 0.1, want_lse=True)
+    out, lse = call()
+    rows = [(s, n - m + i + 1) for s, (n, m) in enumerate(spans) for i in range(m)]
+    at = np.sort(rng.choice(len(rows), 40, replace=False))
+    ref, tol, rl, lt = attention(c, q[torch.from_numpy(at)].double().numpy(), [rows[i] for i in at], 0.1, CHUNK_STEP,
+                                 parts=True)
+    check(out[torch.from_numpy(at).to(DEV)], ref, tol, BF16, "out")
+    check_lse(lse[torch.from_numpy(at).to(DEV)], rl, lt)
+    again, _ = call()  # the units land on other SMs: the same bits
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    assert pa.metis_read_status() == 0
 
 
 def test_prefill_chunks_only_and_decodes_only():
@@ -616,6 +657,27 @@ def test_graph_of_a_decode_step_replayed():
         torch.cuda.synchronize()
         # sequence 2 skips tokens: only its newest row is written, the rest is what the pool held
         verify()
+
+
+def test_calls_on_another_stream_own_their_memory():
+    """Outputs and workspaces allocated by a call for `stream` are not reused by the current stream's work."""
+    rng = np.random.default_rng(34)
+    c = Cache(rng, [700, 300], 2, 64, 16)
+    q = gpu(torch.from_numpy(rng.standard_normal((2, 8, 64))).to(BF16))
+    ref, _ = pa.metis_paged_attn_decode_fp8(q, *c.dev, c.bt, c.sl, 0.125, partition_size=64, max_seq_len=700)
+    kref, _ = pa.metis_gather_cache_fp8(*c.dev, c.bt, c.sl, i32([0, 700]), num_rows=1000)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        outs = []
+        for _ in range(8):
+            o, _ = pa.metis_paged_attn_decode_fp8(q, *c.dev, c.bt, c.sl, 0.125, partition_size=64, max_seq_len=700,
+                                                  stream=stream)
+            k, _ = pa.metis_gather_cache_fp8(*c.dev, c.bt, c.sl, i32([0, 700]), num_rows=1000, stream=stream)
+            outs.append((o, k))
+            torch.full((1 << 20,), 3.0, device=DEV)  # current-stream work that takes freed memory
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref) and torch.equal(k, kref) for o, k in outs)
 
 
 def test_offsets_past_32_bits():
