@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
   const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
   if (b < 0) return;
   uint8_t* const byte_at = (which ? p.scale[1] : p.scale[0]) + (size_t)b * p.G + g;
-  const uint32_t before = live && kept > 0 ? min(ld_byte(byte_at), 254u) : 0u;
+  uint32_t before = 0;  // the scale byte of the earlier tokens, if any
+  if (live && kept > 0) before = ld_byte(byte_at);
   bool odd = false;
   float amax = 0.f;
 #pragma unroll
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
     for (int w = 0; w < subs; ++w) amax = fmaxf(amax, part_max[(warp & ~(subs - 1)) + w]);
   }
   if (!live) return;
+  before = min(before, 254u);
   const uint32_t byte = max(byte_of_amax(amax), before);
   if (sub == 0 && lane == 0) *byte_at = (uint8_t)byte;
 

@@ -9,14 +9,15 @@
 
 namespace metis {
 
-// A byte, or 16 bytes, of the cache.  The kernel in front may be the one that wrote them, and
-// this one may have been launched while it ran (pdl_wait comes between): they are read from
-// L2, past an L1 line or the read-only path that still holds what was there before.
-__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) { return __ldcg(p); }
+// A byte, or a piece of codes, of the cache.  The kernel in front may be the one that wrote
+// them, and this one may have been launched while it ran: after pdl_wait an ordinary load
+// sees what it wrote, one through the read-only path (__ldg, for data that nothing writes
+// while the kernel runs) need not.
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) { return *p; }
 
 template <typename T>
 __device__ __forceinline__ T ld_codes(const T* p) {
-  return __ldcg(p);
+  return *p;
 }
 
 // 2^(b - 127): b = 0 is the subnormal 2^-127, b = 255 (never written) is NaN
