@@ -104,7 +104,7 @@ def load_tc_peaks():
 
 def source_hash() -> str:
     h = hashlib.sha256()
-    for f in ("decode.cu", "common.cuh"):
+    for f in ("decode.cu", "decode.cuh", "common.cuh"):
         with open(os.path.join(ROOT, "paged_attention_kv_decode_gb300", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
