@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
@@ -101,54 +102,49 @@ __device__ __forceinline__ ItemSeq seq_of_item(const WriteFp8Params& p, int i, i
   return it;
 }
 
-// The largest finite |x| of a 16-byte piece's values, 0 without one; *odd: the piece holds
-// an infinity or NaN.
+// Magnitudes of a lane's values: they order like their bits, for bf16 two to a word.
 template <typename T>
-__device__ __forceinline__ float piece_amax(const uint4& v, bool* odd);
+struct WriteVals;
 
 template <>
-__device__ __forceinline__ float piece_amax<__nv_bfloat16>(const uint4& v, bool* odd) {
-  // bf16 magnitudes order like their bits; 0x7f80 and above are not finite
-  const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
-  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
-  m = max(m & 0xffffu, m >> 16);
-  if (m >= 0x7f80u) {
-    *odd = true;
-    m = 0;
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-      if (h < 0x7f80u) m = max(m, h);
+struct WriteVals<__nv_bfloat16> {
+  __device__ static __forceinline__ uint32_t larger(uint32_t m, const uint4& v) {
+    m = max_u16x2(max_u16x2(m, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+    return max_u16x2(max_u16x2(m, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+  }
+  __device__ static __forceinline__ uint32_t bits(uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
+  static constexpr int N = 8;
+  __device__ static __forceinline__ void get(const uint4& v, float* x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  return __uint_as_float(m << 16);
-}
+};
 
 template <>
-__device__ __forceinline__ float piece_amax<float>(const uint4& v, bool* odd) {
-  const uint32_t w[4] = {v.x & 0x7fffffffu, v.y & 0x7fffffffu, v.z & 0x7fffffffu, v.w & 0x7fffffffu};
-  uint32_t m = max(max(w[0], w[1]), max(w[2], w[3]));
-  if (m >= 0x7f800000u) {
-    *odd = true;
-    m = 0;
-    for (int e = 0; e < 4; ++e)
-      if (w[e] < 0x7f800000u) m = max(m, w[e]);
+struct WriteVals<float> {
+  __device__ static __forceinline__ uint32_t larger(uint32_t m, const uint4& v) {
+    return max(max(max(m, v.x & 0x7fffffffu), v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
   }
-  return __uint_as_float(m);
-}
+  __device__ static __forceinline__ uint32_t bits(uint32_t m) { return m; }
+  static constexpr int N = 4;
+  __device__ static __forceinline__ void get(const uint4& v, float* x) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+};
 
-// Four values times inv as codes; odd: infinities become NaN first (0 * x + x keeps the rest)
-__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv, bool odd) {
-  if (odd) {
-    a = fmaf(a, 0.f, a);
-    b = fmaf(b, 0.f, b);
-    c = fmaf(c, 0.f, c);
-    d = fmaf(d, 0.f, d);
-  }
-  const uint64_t inv2 = f2_pack(inv, inv);
-  float x0, x1, x2, x3;
-  f2_unpack(f2_mul(f2_pack(a, b), inv2), x0, x1);
-  f2_unpack(f2_mul(f2_pack(c, d), inv2), x2, x3);
-  return pack_e4m3x4(x0, x1, x2, x3);
+// Four values times the pair inv2 as codes
+__device__ __forceinline__ uint32_t quantize4(const float* x, uint64_t inv2) {
+  float y0, y1, y2, y3;
+  f2_unpack(f2_mul(f2_pack(x[0], x[1]), inv2), y0, y1);
+  f2_unpack(f2_mul(f2_pack(x[2], x[3]), inv2), y2, y3);
+  return pack_e4m3x4(y0, y1, y2, y3);
 }
 
 // One warp: 16 slots of a page x one head of K or V.  Lanes hold 16-byte pieces of the
@@ -156,9 +152,9 @@ __device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d
 // use; the rows stay in registers between the maximum and the rounding, so each input is
 // read once.  Pages of 32 or 64 slots take 2 or 4 warps that share their maximum.
 // The grid is a few waves of short CTAs, so CTAs per SM (registers) decide: 8,240 rows of
-// 8 x 128 bf16 take 12.2 us with five on an SM, 13.3 us with four or three, 15.8 us with two;
-// fp32 rows of 8 x 128, twice the registers, 18 us with three and 26 us with five.  Eight
-// slots per warp instead of 16 are no faster (13.2 us).
+// 8 x 128 bf16 take 11.0 us with five or four on an SM, 11.3 us with three, 11.4 us with six;
+// fp32 rows of 8 x 128, twice the registers, 15.4 us with three, 16.0 us with two, 23.9 us
+// with five.  Eight slots per warp instead of 16 were 8 % slower.
 template <typename T, int D>
 __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5) write_fp8_kernel(const WriteFp8Params p) {
   constexpr int VEC = 16 / (int)sizeof(T);  // elements per lane and load
@@ -201,21 +197,34 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
   const T* src = reinterpret_cast<const T*>(which ? p.src[1] : p.src[0]) +
                  ((long long)(r0 + base - first + slot0) * p.G + g) * D + col;
   uint4 raw[NL];
+  const unsigned rows = live ? (unsigned)max(end - kept, 0) : 0u;
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int slot = slot0 + k * RPL;
-    raw[k] = live && slot >= kept && slot < end ? __ldg(reinterpret_cast<const uint4*>(src + k * RPL * row_len))
-                                                : make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int k = 0; k < NL; ++k, src += RPL * row_len)
+    raw[k] = (unsigned)(slot0 + k * RPL - kept) < rows ? ld_codes(reinterpret_cast<const uint4*>(src))
+                                                       : make_uint4(0u, 0u, 0u, 0u);
   const int b = checked_block(p.block_table + (size_t)s * p.max_blocks, page, p.num_blocks, &g_status_fp8);
   if (b < 0) return;
   uint8_t* const byte_at = (which ? p.scale[1] : p.scale[0]) + (size_t)b * p.G + g;
   uint32_t before = 0;  // the scale byte of the earlier tokens, if any
   if (live && kept > 0) before = ld_byte(byte_at);
-  bool odd = false;
-  float amax = 0.f;
+  // the largest finite magnitude; infinities and NaN (rare) are stored as NaN and do not count
+  using Vals = WriteVals<T>;
+  uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < NL; ++k) amax = fmaxf(amax, piece_amax<T>(raw[k], &odd));
+  for (int k = 0; k < NL; ++k) top = Vals::larger(top, raw[k]);
+  float amax = __uint_as_float(Vals::bits(top));
+  const bool odd = __any_sync(0xffffffffu, !(amax < INFINITY));
+  if (odd) {
+    amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < NL; ++k) {
+      float x[VEC];
+      Vals::get(raw[k], x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (fabsf(x[e]) < INFINITY) amax = fmaxf(amax, fabsf(x[e]));
+    }
+  }
   amax = warp_max_xor(amax, 1);
   if (subs > 1) {
     if (lane == 0) part_max[warp] = amax;
@@ -229,25 +238,29 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) * D == 512 ? 3 : 5
 
   uint8_t* const codes = (which ? p.cache[1] : p.cache[0]) + ((size_t)b * p.bs * p.G + g) * D;
   const float inv = scale_of_byte(254u - byte);  // 2^(127 - byte)
+  const uint64_t inv2 = f2_pack(inv, inv);
   uint8_t* dst = codes + slot0 * row_len + col;
+  auto put = [&](auto with_odd) {
 #pragma unroll
-  for (int k = 0; k < NL; ++k) {
-    const int slot = slot0 + k * RPL;
-    const uint4 v = raw[k];
-    if (slot >= kept && slot < end) {
-      if (sizeof(T) == 2) {
-        uint2 out;
-        out.x = quantize4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                          __uint_as_float(v.y & 0xffff0000u), inv, odd);
-        out.y = quantize4(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u), __uint_as_float(v.w << 16),
-                          __uint_as_float(v.w & 0xffff0000u), inv, odd);
-        *reinterpret_cast<uint2*>(dst + k * RPL * row_len) = out;
-      } else {
-        *reinterpret_cast<uint32_t*>(dst + k * RPL * row_len) =
-            quantize4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w), inv, odd);
+    for (int k = 0; k < NL; ++k, dst += RPL * row_len) {
+      float x[VEC];
+      Vals::get(raw[k], x);
+      if (decltype(with_odd)::value) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = fmaf(x[e], 0.f, x[e]);  // infinity -> NaN, anything else stays
+      }
+      if ((unsigned)(slot0 + k * RPL - kept) < (unsigned)(end - kept)) {
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(quantize4(x, inv2), quantize4(x + 4, inv2));
+        else
+          *reinterpret_cast<uint32_t*>(dst) = quantize4(x, inv2);
       }
     }
-  }
+  };
+  if (!odd)
+    put(std::false_type{});
+  else
+    put(std::true_type{});
 
   // the scale grew: round the earlier codes at the new one
   if (kept > 0 && byte > before) {

@@ -9,7 +9,7 @@
 
 namespace metis {
 
-// A byte, or a piece of codes, of the cache.  The kernel in front may be the one that wrote
+// A byte, a piece of codes or of rows.  The kernel in front may be the one that wrote
 // them, and this one may have been launched while it ran: after pdl_wait an ordinary load
 // sees what it wrote, one through the read-only path (__ldg, for data that nothing writes
 // while the kernel runs) need not.
