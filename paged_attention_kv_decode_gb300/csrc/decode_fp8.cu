@@ -314,8 +314,10 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (lane & 8) + (lane & 7), lchunk = lane >> 4;
 
-  // One unit.  ODD: tiles that are partly outside the range, or pages whose V scales are far
-  // apart; everything else runs without a branch but the one of moving references.
+  // One unit.  ODD: tiles that are partly outside the range, or pages whose V scale is 2^32
+  // below the largest so far (against a reference with that one's exponent their weights
+  // may be below fp32's range: their sum is taken from the scores); everything else runs
+  // without a branch but the one of moving references.
   auto consume = [&](auto odd_unit, int tok0, uint32_t sc) {
     constexpr bool ODD = decltype(odd_unit)::value;
     const uint32_t kbase = units.tile();
@@ -446,6 +448,7 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
   };
 
   int k = 0;
+  int v_top = 0;  // the largest V scale byte so far
   bool ok = true;
   for (; k < units.n_my; ++k) {
     const uint32_t sc = units.scales(k);
@@ -454,9 +457,9 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
       ok = false;
       break;
     }
-    const int apart = (int)((sc >> 8) & 255u) - (int)(sc >> 24);
-    const bool nan_scale = ((sc >> 8) & 255u) == 255u || (sc >> 24) == 255u;
-    if (tok0 < t0 || tok0 + kUnit8 > t1 || abs(apart) > 32 || nan_scale)
+    const int vb0 = (sc >> 8) & 255u, vb1 = sc >> 24;
+    v_top = max(v_top, max(vb0, vb1));
+    if (tok0 < t0 || tok0 + kUnit8 > t1 || v_top - min(vb0, vb1) > 32 || v_top == 255)
       consume(std::true_type{}, tok0, sc);
     else
       consume(std::false_type{}, tok0, sc);

@@ -416,6 +416,35 @@ def test_decode_long_flat_tail_beside_one_large_weight(partition):
         check_lse(lse, rl, lt)
 
 
+@pytest.mark.parametrize("big", [127, 200])
+@pytest.mark.parametrize("partition", [0, 512, 8192])
+def test_decode_many_pages_of_zero_values_beside_one_of_large_ones(partition, big):
+    """8,000 tokens whose V is zero (scale 2^-126) and whose weight is e^-11 of the first one's
+    take part in the sum, whatever the scale of the page in front of, between or behind them."""
+    rng = np.random.default_rng(big)
+    n, D, bs = 8000, 128, 16
+    for first in (0, 300, 499):
+        c = Cache(rng, [n], 1, D, bs, spread=0.0)
+        t = np.arange(n)
+        page = c.table[0, t // bs]
+        c.k[page, t % bs, 0] = 0
+        c.k[page[first * bs], 0, 0, 0] = oracle.encode_e4m3(np.full(1, 11.0))[0]
+        c.ks[:] = 127
+        others = np.delete(c.table[0, :n // bs], first)
+        c.v[others] = 0
+        c.vs[others] = 1
+        c.vs[page[first * bs]] = big
+        c.put()
+        q = torch.zeros((1, 4, D)).to(BF16)
+        q[:, :, 0] = 1.0
+        for dtype in (BF16, F32):
+            out, lse = pa.metis_paged_attn_decode_fp8(gpu(q, dtype), *c.dev, c.bt, c.sl, 1.0, partition_size=partition,
+                                                      want_lse=True)
+            ref, tol, rl, lt = attention(c, q.double().numpy(), [(0, n)], 1.0, STEP[dtype])
+            check(out, ref, tol, dtype, "out")
+            check_lse(lse, rl, lt)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_decode_softmax_scales(scale):
     decode_case(np.random.default_rng(5), [300, 1, 40], 4, 2, 64, 16, BF16, scale=scale, spread=0.5)
