@@ -149,6 +149,9 @@ struct PfShape {
 // split them.
 constexpr int kV8Converters = 4;
 constexpr int kKScaleSlots = 4;  // tiles whose K factors are kept
+// Units whose NaN notes are kept.  Unit k is published once every warp has taken unit k - 1,
+// which a softmax group does after it has written out unit k - 3: its notes may be cleared.
+constexpr int kNanUnits = 3;
 
 struct PfFp8Shared {
   uint64_t stage_full[kV8Stages];   // staged V tile landed
@@ -157,7 +160,40 @@ struct PfFp8Shared {
   uint64_t q_full[2];               // ... split into their two e4m3 parts (4 warps)
   float4 ks[kKScaleSlots][2];       // per 16 tokens of a K tile: its page's scale
   float vs[kV8Stages][8];           // ... of a staged V tile
+  // NaN in V rows that only some of a unit's query rows see: kept out of the V tile, where
+  // 0 * NaN would reach every row, and put into the output columns of the rows that see them
+  int nan_any[kNanUnits];
+  uint16_t nan_first[kNanUnits][128];  // per column: the first such token behind the unit's first query
 };
+
+// The converters' rare case: one row's 16 codes from column `col` on, or their scale, hold
+// NaN; the codes become zeros (returned) and their columns are noted.
+__device__ __forceinline__ uint4 note_nan_codes(uint4 c, bool scale_nan, uint16_t* first, int* any, uint16_t rel) {
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b)
+      if (scale_nan || ((w[i] >> (8 * b)) & 0x7fu) == 0x7fu) {
+        w[i] &= ~(0xffu << (8 * b));
+        uint16_t* at = first + 4 * i + b;
+        uint16_t seen = *reinterpret_cast<volatile uint16_t*>(at);
+        while (rel < seen) {  // each turn that another lane wins lowers `seen`
+          const uint16_t was = atomicCAS(at, seen, rel);
+          if (was == seen) break;
+          seen = was;
+        }
+      }
+  }
+  *reinterpret_cast<volatile int*>(any) = 1;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Any NaN (0x7f, 0xff) among 16 codes
+__device__ __forceinline__ bool any_nan_code(const uint4& c) {
+  return ((((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) != 0;
+}
 
 // mbarrier layout (indices into the barrier area) and arrival counts
 struct PfBar {
@@ -525,6 +561,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     PfUnit it;
     while (ok && next_unit(k, it) > 0) {
       const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
+      {
+        const int slot = (k - 1) % kNanUnits;  // (the converters see it cleared by the unit's first V tile)
+        uint32_t* first = reinterpret_cast<uint32_t*>(x8.nan_first[slot]);
+        for (int i = lane; i < 64; i += 32) first[i] = 0xffffffffu;
+        if (lane == 0) x8.nan_any[slot] = 0;
+        __syncwarp();
+      }
       // page `lane` of tile j: its TMA row (a bad id reads a box out of bounds: zeros) and scales
       auto page_of = [&](int j, int& rowc, float& fk, float& fv) -> bool {
         const int pg = j * npg + lane;
@@ -599,6 +642,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       constexpr int CPR = D / 16, RPC = 32 / CPR;   // V: 16-byte pieces of a row, rows per pass
       const int piece = lane % CPR;
       const int flip = D == 128 ? piece >> 2 : 0;   // the two halves' lanes write opposite chunks at a time
+      const int p_min = it.L - it.q_len + 2 * it.pair * p.Tq;  // position of the unit's first query token
+      const int nan_slot = (k - 1) % kNanUnits;
       for (int j = 0; j < it.n_kv; ++j, ++t) {
         const int sv = t % kStages8, st = t % kVStages;
         if (!wait_all(&x8.stage_full[sv], (t / kStages8) & 1) ||
@@ -608,18 +653,37 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
         const uint4* src = reinterpret_cast<const uint4*>(smem + Sh::kStage + sv * kKvTile * D) + lane;
         uint8_t* tile = sV + st * Sh::kKvBytes + (piece * 16 / 64) * Sh::kKvHalf;
-        const int live_rows = it.L - j * kKvTile;   // rows past the sequence end become zeros
-#pragma unroll 1
-        for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
-          const int row = i * RPC + lane / CPR;
-          uint4 c = src[i * 32];
-          const float f = x8.vs[sv][row >> 4];
-          if (row >= live_rows) c = make_uint4(0u, 0u, 0u, 0u);
+        auto put = [&](int row, const uint4& c, float f) {
           const uint4 a = codes_to_bf16x8(c.x, c.y, f), b = codes_to_bf16x8(c.z, c.w, f);
           const int ch = (piece * 2 & 7) + flip;
           uint8_t* dst = tile + row * 128;
           *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = flip ? b : a;
           *reinterpret_cast<uint4*>(dst + (((ch ^ 1) ^ (row & 7)) << 4)) = flip ? a : b;
+        };
+        const int seen_rows = p_min + 1 - j * kKvTile;  // rows that every query row of the unit sees
+        if (seen_rows >= kKvTile) {
+#pragma unroll 1
+          for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
+            const int row = i * RPC + lane / CPR;
+            put(row, src[i * 32], x8.vs[sv][row >> 4]);
+          }
+        } else {
+          const int live_rows = it.L - j * kKvTile;     // rows past the sequence end become zeros
+#pragma unroll 1
+          for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
+            const int row = i * RPC + lane / CPR;
+            uint4 c = src[i * 32];
+            float f = x8.vs[sv][row >> 4];
+            if (row >= live_rows) {
+              c = make_uint4(0u, 0u, 0u, 0u);
+              f = 1.f;
+            } else if (row >= seen_rows && (any_nan_code(c) || f != f)) {
+              c = note_nan_codes(c, f != f, x8.nan_first[nan_slot] + piece * 16, &x8.nan_any[nan_slot],
+                                 (uint16_t)(row - seen_rows + 1));
+              f = f != f ? 1.f : f;
+            }
+            put(row, c, f);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -981,6 +1045,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // of it is written out, so that the tensor cores have the next QK meanwhile.
     [[maybe_unused]] uint32_t t_base = 0, n_split = 0;  // K/V tiles of the units before, query tiles split
     [[maybe_unused]] float row_factor = 0.f, next_factor = 0.f;  // |sl2| without the query row's scaling
+    [[maybe_unused]] int nan_slot = 0;                           // of the unit in hand
     [[maybe_unused]] bool have = false;
     [[maybe_unused]] PfUnit next;
     [[maybe_unused]] auto advance = [&]() {
@@ -1001,6 +1066,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if constexpr (KV8) {
         it = next;
         row_factor = next_factor;
+        nan_slot = (k - 1) % kNanUnits;
         return have;
       } else {
         return next_unit(k, it) > 0;
@@ -1058,9 +1124,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 8; ++i) fac[i] = ks[i] * row_factor;
           if (!lean) {
-            // > 0, so that a hidden key's -inf stays -inf; NaN passes
+            // > 0, so that a hidden key's -inf stays -inf; NaN passes for keys that are seen
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fac[i] = max_nan(fac[i], 1.17549435e-38f);
+            for (int i = 0; i < 8; ++i) fac[i] = 16 * i < vis ? max_nan(fac[i], 1.17549435e-38f) : 1.f;
           }
           float top = m_run;
 #pragma unroll
@@ -1156,6 +1222,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
             v.w = pack_bf16x2(__uint_as_float(ov[i + 6]) * inv, __uint_as_float(ov[i + 7]) * inv);
             *reinterpret_cast<uint4*>(orow + c * 32 + i) = v;
           }
+        }
+      }
+      if constexpr (KV8) {
+        if (*reinterpret_cast<volatile int*>(&x8.nan_any[nan_slot]) && row_valid) {
+          const int rel = p_row - (L - q_len + 2 * it.pair * p.Tq);
+#pragma unroll 1
+          for (int d = 0; d < D; ++d)
+            if (x8.nan_first[nan_slot][d] <= rel) orow[d] = __ushort_as_bfloat16(0x7fff);
         }
       }
       if (row_valid && p.lse_out) p.lse_out[(size_t)(it.q0 + qi) * p.H + head] = (m_run + log2f(l_run)) * kLn2;

@@ -580,6 +580,47 @@ def test_prefill_nan_code_of_a_live_token_reaches_the_output():
     assert torch.isfinite(o[40:, :, :11]).all() and torch.isfinite(o[40:, :, 12:]).all()
 
 
+@pytest.mark.parametrize("r,D,bs", [(4, 128, 16), (1, 64, 32), (8, 64, 16), (2, 128, 64)])
+def test_prefill_nan_of_a_token_reaches_only_the_rows_that_see_it(r, D, bs):
+    """NaN codes in K and V, and pages whose scale is NaN, of tokens that earlier rows of the same
+    chunk must not see: NaN appears in the rows at and behind them alone, of V in its column alone."""
+    rng = np.random.default_rng(r * 10 + D)
+    spans = [(400, 300), (170, 170), (333, 130), (90, 1), (260, 5)]
+    lens, q_lens = [n for n, _ in spans], [n for _, n in spans]
+    G = 2
+    c = Cache(rng, lens, G, D, bs)
+
+    def at(s, t):
+        return c.table[s, t // bs], t % bs
+
+    v_nans = [(0, 101, 0, 3), (0, 130, 0, 3), (0, 140, 1, 60), (0, 377, 0, 7), (0, 399, 1, 0), (1, 5, 1, 33), (1, 6, 1, 33),
+              (1, 127, 0, 63), (1, 128, 0, 62), (2, 250, 1, 1), (2, 20, 1, 40), (4, 258, 0, 9)]
+    for s, t, g, d in v_nans:
+        c.v[(*at(s, t), g, d)] = rng.choice([0x7F, 0xFF])
+    c.k[(*at(1, 150), 1, 4)] = 0x7F
+    c.ks[at(2, 320)[0], 0] = 255
+    c.vs[at(0, 384)[0], 1] = 255
+    c.put()
+    # the reference's view of a NaN scale: every code of the page is NaN
+    c.k[at(2, 320)[0], :, 0], c.ks[at(2, 320)[0], 0] = 0x7F, 127
+    c.v[at(0, 384)[0], :, 1], c.vs[at(0, 384)[0], 1] = 0x7F, 127
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), G * r, D))).to(BF16)
+    out, lse = pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32(cu), *c.dev, c.bt, c.sl, D ** -0.5, want_lse=True)
+    rows = [(s, n - m + i + 1) for s, (n, m) in enumerate(spans) for i in range(m)]
+    with np.errstate(invalid="ignore"):
+        ref, tol, rl, lt = attention(c, q.double().numpy(), rows, D ** -0.5, CHUNK_STEP, parts=True)
+    o = out.double().cpu().numpy()
+    np.testing.assert_array_equal(np.isnan(o), np.isnan(ref))
+    # B of the bound counts every V code a row sees: its NaN columns do not matter, those beside them do
+    good = ~np.isnan(ref)
+    assert good.mean() > 0.5 and (~good).any()
+    assert (np.abs(o - ref)[good] <= (tol + 2.0 ** -8 * np.abs(ref))[good]).all()
+    ln = lse.double().cpu().numpy()
+    np.testing.assert_array_equal(np.isnan(ln), np.isnan(rl))
+    assert (np.abs(ln - rl)[~np.isnan(rl)] <= (lt + 2.0 ** -21 * np.abs(rl))[~np.isnan(rl)]).all()
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
