@@ -393,7 +393,9 @@ int metis_reshape_and_cache_fp8(const void* key, const void* value, void* k_cach
  *   max_seq_len    host-side upper bound on seq_lens; tokens beyond it are not read
  *                  (METIS_STATUS_SEQ_TOO_LONG)
  * A row outside [0, num_rows) is not written (METIS_STATUS_BAD_OFFSETS); a page whose
- * id is outside the pool reads as zeros (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_rows == 0 is a successful no-op.
+ * id is outside the pool reads as zeros (METIS_STATUS_BAD_BLOCK_ID).  Sequences whose
+ * rows overlap leave either's values.  num_seqs == 0 or num_rows == 0 is a successful
+ * no-op.
  */
 int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                            const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
@@ -419,7 +421,12 @@ int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* 
 /*
  * metis_paged_attn_prefill_chunk_fp8 -- metis_paged_attn_prefill_chunk over an 8-bit
  * cache: the same arguments, workspace (metis_prefill_workspace_bytes) and
- * limits, with the scales behind the codes.
+ * limits, with the scales behind the codes; dtype METIS_BF16.  A chunk's query rows
+ * enter the products as two e4m3 parts at one power of two each: elements down to 2^-8
+ * of the row's largest are exact, smaller ones are off by at most 2^-17 of it.  V
+ * enters as bf16, scale included (exact), with softmax weights in bf16.  NaN in V reaches
+ * the rows that see its token, in its column.  Sequences with one query and a head ratio
+ * up to 8 are computed as metis_paged_attn_decode_fp8 computes them.
  */
 int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,
                                        const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
