@@ -1058,6 +1058,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // of it is written out, so that the tensor cores have the next QK meanwhile.
     [[maybe_unused]] uint32_t t_base = 0, n_split = 0;  // K/V tiles of the units before, query tiles split
     [[maybe_unused]] float row_factor = 0.f, next_factor = 0.f;  // |sl2| without the query row's scaling
+    [[maybe_unused]] int nan_slot = 0;                           // of the unit in hand
     [[maybe_unused]] bool have = false;
     [[maybe_unused]] PfUnit next;
     [[maybe_unused]] auto advance = [&]() {
@@ -1078,6 +1079,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if constexpr (KV8) {
         it = next;
         row_factor = next_factor;
+        nan_slot = (k - 1) % kNanUnits;
         return have;
       } else {
         return next_unit(k, it) > 0;
@@ -1236,7 +1238,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
       }
       if constexpr (KV8) {
-        const uint32_t nan_slot = (k - 2) % kNanUnits;  // (unit k - 1, the next, is taken already)
         if (*reinterpret_cast<volatile int*>(&x8.nan_any[nan_slot]) && row_valid) {
           const int rel = p_row - (L - q_len + 2 * it.pair * p.Tq);
 #pragma unroll 1
