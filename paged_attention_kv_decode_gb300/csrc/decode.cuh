@@ -90,8 +90,9 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, float 
 // Merge the per-warp online-softmax states held in shared memory (cm, cl:
 // [NW][8] running max in log2 units and running sum; co: [NW][D][8] unnormalised
 // accumulators) and write the CTA's result: the final output row or a
-// split-KV partial.
-template <typename OutT, int NW>
+// split-KV partial.  NAN_LSE_AS_INF: a partial whose lse is NaN says +inf, which the
+// merge turns into NaN (it passes a NaN over).
+template <typename OutT, int NW, bool NAN_LSE_AS_INF = false>
 __device__ __forceinline__ void combine_and_store(const DecodeParams& p, const float* cm, const float* cl,
                                                   const float* co, int part, int g, int s, int orow, int tid) {
   const int D = p.D;
@@ -121,7 +122,8 @@ __device__ __forceinline__ void combine_and_store(const DecodeParams& p, const f
     if (p.partition_size > 0) {
       float* dst = p.part_out + (((size_t)s * p.H + head) * p.max_parts + part) * D + d;
       *reinterpret_cast<float4*>(dst) = make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
-      if (d == 0) p.part_lse[((size_t)s * p.H + head) * p.max_parts + part] = lse;
+      if (d == 0)
+        p.part_lse[((size_t)s * p.H + head) * p.max_parts + part] = NAN_LSE_AS_INF && lse != lse ? INFINITY : lse;
     } else {
       OutT* dst = reinterpret_cast<OutT*>(p.out) + ((size_t)orow * p.H + head) * D + d;
       store4<OutT>(dst, a0 * inv, a1 * inv, a2 * inv, a3 * inv);

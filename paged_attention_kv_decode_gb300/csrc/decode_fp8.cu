@@ -239,6 +239,10 @@ __device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   l0 = warp_sum_xor(l0, 4);
   l1 = warp_sum_xor(l1, 4);
+  // scores of NaN have left the sum NaN, but not the reference (no comparison with them
+  // holds): any finite one makes the state count
+  if (l0 != l0) m0 = 0.f;
+  if (l1 != l1) m1 = 0.f;
   sync();  // every warp is done with its ring
   float* cm = reinterpret_cast<float*>(smem);
   float* cl = cm + NW * 8;
@@ -255,7 +259,7 @@ __device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem
     for (int i = 0; i < 2; ++i)
       *reinterpret_cast<uint64_t*>(co + ((size_t)warp * D + dims(c, i)) * 8 + 2 * (lane & 3)) = o[c][i];
   sync();
-  combine_and_store<QT, NW>(p, cm, cl, co, part, g, s, orow, tid);
+  combine_and_store<QT, NW, true>(p, cm, cl, co, part, g, s, orow, tid);
 }
 
 // ---------------------------------------------------------------------------
@@ -374,12 +378,14 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
         // fragments so that 0 * NaN cannot poison O.
         const uint32_t lo = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
         const uint32_t hi = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
+        // a scale of NaN: so is every code
+        const uint32_t nan = ((h ? sc >> 24 : sc >> 8) & 255u) == 255u ? 0x7f7f7f7fu : 0u;
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
-          v[c][h][0] &= lo;
-          v[c][h][1] &= hi;
-          v[c][h][2] &= lo;
-          v[c][h][3] &= hi;
+          v[c][h][0] = (v[c][h][0] | nan) & lo;
+          v[c][h][1] = (v[c][h][1] | nan) & hi;
+          v[c][h][2] = (v[c][h][2] | nan) & lo;
+          v[c][h][3] = (v[c][h][3] | nan) & hi;
         }
       }
     }

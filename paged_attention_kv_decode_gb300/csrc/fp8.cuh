@@ -25,10 +25,8 @@ __device__ __forceinline__ float scale_of_byte(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
 }
 
-// Its exponent, b - 127 (NaN for 255)
-__device__ __forceinline__ float exponent_of_byte(uint32_t b) {
-  return b == 255 ? __uint_as_float(0x7fc00000u) : (float)((int)b - 127);
-}
+// Its exponent (finite for 255 too, which the caller has to treat apart)
+__device__ __forceinline__ float exponent_of_byte(uint32_t b) { return (float)((int)b - 127); }
 
 // The exponent byte of the smallest 2^k with amax <= 448 * 2^k, at least 1 (2^-126).
 // amax is finite and >= 0: with amax = m * 2^e, 1 <= m < 2, and 448 = 1.75 * 2^8, that

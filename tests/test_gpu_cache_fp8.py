@@ -484,6 +484,43 @@ def test_decode_nan_code_of_a_live_token_reaches_the_output():
     assert torch.isnan(o[1, :, 11]).all() and torch.isfinite(o[1, :, :11]).all() and torch.isfinite(o[1, :, 12:]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("partition", [0, 16, 64, 512])
+def test_decode_nan_wherever_it_stands(partition, dtype):
+    """NaN codes in K and V, pages whose scale is NaN, whole units of NaN scores and a NaN query reach
+    the outputs of the heads (and, of V's codes, the columns) that use them, and no others."""
+    rng = np.random.default_rng(partition)
+    lens, G, r, D, bs = [200, 70, 333, 16, 300, 129], 2, 3, 128, 16
+    c = Cache(rng, lens, G, D, bs)
+    c.k[c.table[0, 4:8], :, 0, 5] = 0x7F        # two whole units of one warp
+    c.v[c.table[1, 3], 7, 1, 99] = 0xFF
+    c.ks[c.table[2, 20], 1] = 255               # the last, partial page
+    c.vs[c.table[4, 9], 0] = 255
+    c.k[c.table[5, 8], 0, 1, 0] = 0x7F          # the last token
+    c.put()
+    c.k[c.table[2, 20], :, 1], c.ks[c.table[2, 20], 1] = 0x7F, 127  # the reference's view of a NaN scale
+    c.v[c.table[4, 9], :, 0], c.vs[c.table[4, 9], 0] = 0x7F, 127
+    q = torch.from_numpy(rng.standard_normal((len(lens), G * r, D))).to(dtype)
+    q[3, 4, 17] = float("nan")
+    out, lse = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, c.sl, D ** -0.5, partition_size=partition,
+                                              want_lse=True)
+    with np.errstate(invalid="ignore"):
+        ref, tol, rl, lt = attention(c, q.double().numpy(), list(enumerate(lens)), D ** -0.5, STEP[dtype])
+    o, ln = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    np.testing.assert_array_equal(np.isnan(o), np.isnan(ref))
+    np.testing.assert_array_equal(np.isnan(ln), np.isnan(rl))
+    good = ~np.isnan(ref)
+    assert (np.abs(o - ref)[good] <= (tol + (2.0 ** -8 if dtype == BF16 else 2.0 ** -23) * np.abs(ref))[good]).all()
+    assert (np.abs(ln - rl)[~np.isnan(rl)] <= lt[~np.isnan(rl)]).all()
+    if dtype == BF16 and partition == 0:  # the same rows as decodes of a chunked call (ratio 3 has no chunks)
+        q4 = torch.cat([q.view(-1, G, r, D), q.view(-1, G, r, D)[:, :, :1]], 2).reshape(-1, G * 4, D)
+        out4, lse4 = pa.metis_paged_attn_prefill_chunk_fp8(gpu(q4), i32(np.arange(len(lens) + 1)), *c.dev, c.bt, c.sl,
+                                                           D ** -0.5, want_lse=True)
+        o4 = out4.double().cpu().numpy().reshape(-1, G, 4, D)[:, :, :3].reshape(o.shape)
+        np.testing.assert_array_equal(np.isnan(o4), np.isnan(ref))
+        assert (np.abs(o4 - ref)[good] <= (tol + 2.0 ** -8 * np.abs(ref))[good]).all()
+
+
 def test_decode_bad_contents():
     rng = np.random.default_rng(8)
     lens = [70, 40]
