@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "../../include/metis_attn.h"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 #include "fp8.cuh"
@@ -51,6 +52,7 @@ struct DecodeFp8Params {
 
 constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
 constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
+constexpr int kMaxJoin = 8;      // partitions of an item that a cluster takes
 constexpr float kSlack = 16.f;   // bf16 queries: the sums' reference moves when it is exceeded by 2^16
 
 template <int D>
@@ -230,12 +232,12 @@ struct Fp8Units {
 };
 
 // The warps' softmax states meet in the ring's memory (every warp is done with it after the
-// first sync) and become the item's result.  o[c]: dims d0(c), d1(c) of the lane for
-// heads 2 q4, 2 q4 + 1, unnormalised relative to 2^m0, 2^m1.
-template <int D, typename QT, int NW, typename Sync, typename Dims>
-__device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem, const uint64_t (*o)[2], float m0,
-                                            float m1, float l0, float l1, int part, int g, int s, int orow, int warp,
-                                            int lane, int tid, Sync sync, Dims dims) {
+// first sync) and become the item's result through store(cm, cl, co) (combine_and_store's
+// arguments).  o[c]: dims d0(c), d1(c) of the lane for heads 2 q4, 2 q4 + 1, unnormalised
+// relative to 2^m0, 2^m1.
+template <int D, int NW, typename Sync, typename Store, typename Dims>
+__device__ __forceinline__ void combine_fp8(uint8_t* smem, const uint64_t (*o)[2], float m0, float m1, float l0,
+                                            float l1, int warp, int lane, Sync sync, Store store, Dims dims) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   l0 = warp_sum_xor(l0, 4);
   l1 = warp_sum_xor(l1, 4);
@@ -259,18 +261,18 @@ __device__ __forceinline__ void combine_fp8(const DecodeParams& p, uint8_t* smem
     for (int i = 0; i < 2; ++i)
       *reinterpret_cast<uint64_t*>(co + ((size_t)warp * D + dims(c, i)) * 8 + 2 * (lane & 3)) = o[c][i];
   sync();
-  combine_and_store<QT, NW, true>(p, cm, cl, co, part, g, s, orow, tid);
+  store(cm, cl, co);
 }
 
 // ---------------------------------------------------------------------------
 // bf16 queries
 // ---------------------------------------------------------------------------
-// One work item; arguments as for decode_bf16_item (decode.cu).
-template <int D, int NW, int STAGES, typename Sync>
+// One work item; arguments as for decode_bf16_item (decode.cu), store as for combine_fp8.
+template <int D, int NW, int STAGES, typename Sync, typename Store>
 __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                                     const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
-                                                     int part, int g, int s, int orow, int t0, int t1, int warp,
-                                                     int lane, int tid, int& kb, Sync sync) {
+                                                     const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars, int g,
+                                                     int s, int orow, int t0, int t1, int warp, int lane, int& kb,
+                                                     Sync sync, Store store) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   const DecodeParams& p = pp.d;
   Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, g, s, t0, t1, warp, lane, kb);
@@ -481,8 +483,8 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
     o2[c][0] = f2_pack(o[c][0] * b0, o[c][1] * b1);
     o2[c][1] = f2_pack(o[c][2] * b0, o[c][3] * b1);
   }
-  combine_fp8<D, __nv_bfloat16, NW>(p, smem, o2, m0, m1, l0, l1, part, g, s, orow, warp, lane, tid, sync,
-                                    [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  combine_fp8<D, NW>(smem, o2, m0, m1, l0, l1, warp, lane, sync, store,
+                     [rA](int c, int i) { return c * 16 + 2 * rA + i; });
   kb += units.n_my;
   return ok;
 }
@@ -492,11 +494,11 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
 // ---------------------------------------------------------------------------
 // The same item for fp32 q and out: two fp16 parts of q and of the weights, and fresh
 // accumulators per tile.
-template <int D, int NW, int STAGES, typename Sync>
+template <int D, int NW, int STAGES, typename Sync, typename Store>
 __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                                    const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars,
-                                                    int part, int g, int s, int orow, int t0, int t1, int warp, int lane,
-                                                    int tid, int& kb, Sync sync) {
+                                                    const DecodeFp8Params& pp, uint8_t* smem, uint64_t* bars, int g,
+                                                    int s, int orow, int t0, int t1, int warp, int lane, int& kb,
+                                                    Sync sync, Store store) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   const DecodeParams& p = pp.d;
   Fp8Units<D, NW, STAGES> units(tmK, tmV, pp, smem, bars, g, s, t0, t1, warp, lane, kb);
@@ -679,8 +681,8 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
     units.release(k);
   }
   if (!ok) units.drain(k);
-  combine_fp8<D, float, NW>(p, smem, o, m0, m1, l0, l1, part, g, s, orow, warp, lane, tid, sync,
-                            [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  combine_fp8<D, NW>(smem, o, m0, m1, l0, l1, warp, lane, sync, store,
+                     [rA](int c, int i) { return c * 16 + 2 * rA + i; });
   kb += units.n_my;
   return ok;
 }
@@ -697,9 +699,17 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 //   many partitions  one warp and 2 stages, twelve CTAs per SM: nothing to combine, and a
 //                  partition's start-up (block ids, scales, query) hides behind eleven others:
 //                  8 sequences of 32-128 K in 512-token partitions 248 us, 4 warps and 3
-//                  stages 361 us before other steps
-//   few partitions  4 warps, 2 stages, three CTAs per SM: the 29 sequences in 1,024-token
-//                  partitions 26.8 us; 3 stages and two CTAs 32.5 us, 8 warps 39.7 us
+//                  stages 361 us before other steps; 16 sequences of 4,096 tokens in as many
+//                  30.1 us, 4 warps 37.7 us
+//   few partitions  4 warps, 2 stages, three CTAs per SM: 29 sequences up to 6,000 tokens, 28/4
+//                  heads, in 1,024-token partitions 26.8 us; 3 stages and two CTAs 32.5 us, 8
+//                  warps 39.7 us, one warp 40.9 us
+//   a CTA per SM at most, up to 8 partitions  joined in a cluster instead of by a merge kernel:
+//                  one sequence of 4,096 tokens in 512-token partitions 8.5 us, 10.6 us with the
+//                  merge (but 16 sequences 41.7 us, 37.7 with it: a cluster's CTAs hold their
+//                  slots until the last one is done).  Partitions of 1,024 tokens and more, half
+//                  the SMs at most: 8 warps, 4,096-token ones 24.2 us, 4 warps 32.3 us; over more
+//                  SMs clusters of whole-SM CTAs do not all fit at a time (16.2 us for 10.4)
 template <int NW_, int STAGES_, int MIN_CTAS_>
 struct Fp8Plan {
   static constexpr int NW = NW_, STAGES = STAGES_, MIN_CTAS = MIN_CTAS_;
@@ -710,8 +720,63 @@ template <int D>
 using Fp8FewItems = std::conditional_t<D == 128, Fp8Plan<8, 3, 1>, Fp8Plan<8, 2, 2>>;
 using Fp8ManyParts = Fp8Plan<1, 2, 12>;
 using Fp8FewParts = Fp8Plan<4, 2, 3>;
+using Fp8JoinLong = Fp8Plan<8, 2, 1>;
 
-template <int D, typename QT, typename Plan>
+template <int D, int NW, int STAGES, typename QT, typename Sync, typename Store>
+__device__ __forceinline__ bool decode_fp8_item(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeFp8Params& pp,
+                                                uint8_t* smem, uint64_t* bars, int g, int s, int orow, int t0, int t1,
+                                                int warp, int lane, int& kb, Sync sync, Store store) {
+  if constexpr (sizeof(QT) == 4)
+    return decode_fp8_item_f32<D, NW, STAGES>(tmK, tmV, pp, smem, bars, g, s, orow, t0, t1, warp, lane, kb, sync, store);
+  else
+    return decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, smem, bars, g, s, orow, t0, t1, warp, lane, kb, sync, store);
+}
+
+// A (sequence, KV head)'s partitions are one cluster: their results, normalised rows o
+// [r][D] and their lse, are in their CTAs' shared memory at the same addresses, and every
+// CTA writes a share of the merged rows, in the order of the partitions.  out = sum of
+// o_i 2^(x_i - M) over sum of 2^(x_i - M), x_i the lse in log2 units, M the largest.
+template <int D, typename QT, int NT>
+__device__ __forceinline__ void join_partitions(const DecodeParams& p, const float* o, const float* lse, int n, int g,
+                                                int s) {
+  const int parts = p.max_parts, part = blockIdx.y;
+  for (int idx = part * NT + threadIdx.x; idx < p.r * (D / 4); idx += parts * NT) {
+    const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+    float x[kMaxJoin];
+    float4 v[kMaxJoin];
+#pragma unroll
+    for (int i = 0; i < kMaxJoin; ++i) {
+      x[i] = -INFINITY;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        x[i] = ld_cluster_f32(dsmem_map(smem_u32(lse + h), i)) * kLog2e;
+        v[i] = ld_cluster_f32x4(dsmem_map(smem_u32(o + h * D + d), i));
+      }
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMaxJoin; ++i) M = fmaxf(M, x[i]);
+    float W = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxJoin; ++i) {
+      if (x[i] == -INFINITY) continue;
+      const float w = exp2_approx(x[i] - M);  // (NaN of a partition stays)
+      W += w;
+      a0 = fmaf(w, v[i].x, a0);
+      a1 = fmaf(w, v[i].y, a1);
+      a2 = fmaf(w, v[i].z, a2);
+      a3 = fmaf(w, v[i].w, a3);
+    }
+    const bool empty = n == 0;
+    const float inv = empty ? 0.f : 1.f / W;
+    const size_t row = (size_t)s * p.H + g * p.r + h;
+    store4<QT>(reinterpret_cast<QT*>(p.out) + row * D + d, a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+    if (d == 0 && p.lse_out) p.lse_out[row] = empty ? -INFINITY : (M + log2f(W)) * kLn2;
+  }
+}
+
+// JOIN: the partitions of an item are a cluster along y, else one grid row of all of them.
+template <int D, typename QT, typename Plan, bool JOIN>
 __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
                                                               const DecodeFp8Params pp) {
@@ -731,25 +796,56 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
   pdl_wait();  // inputs are read after the previous grid in the stream has completed
   pdl_launch_dependents();
 
-  __shared__ int rank_lens[kMaxRankSeqs];
-  __shared__ int rank_found;
-  // KV heads vary fastest: the CTAs that read one page's rows (all heads of a token lie side
-  // by side) run at about the same time
-  const int part = blockIdx.x / p.G, g = blockIdx.x - part * p.G;
-  const int s = (p.partition_size == 0 && p.S <= kMaxRankSeqs) ? seq_of_rank(p, blockIdx.y, rank_lens, &rank_found)
-                                                                : (int)blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int t0, t1;
-  if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
-  __syncthreads();  // the barriers are initialised
   int kb = 0;
   auto sync = [] { __syncthreads(); };
-  if constexpr (sizeof(QT) == 4)
-    decode_fp8_item_f32<D, NW, STAGES>(tmK, tmV, pp, smem, bars, part, g, s, s, t0, t1, warp, lane, threadIdx.x,
-                                       kb, sync);
-  else
-    decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, smem, bars, part, g, s, s, t0, t1, warp, lane,
-                                        threadIdx.x, kb, sync);
+  if constexpr (JOIN) {
+    // behind the area of the warps' states (combine_fp8)
+    float* jo = reinterpret_cast<float*>(smem + NW * (64 + D * 32));
+    float* jl = jo + 8 * D;
+    static_assert(NW * (64 + D * 32) + 8 * D * 4 + 32 <= NW * STAGES * STAGE_BYTES, "the partial must fit in the ring");
+    const int g = blockIdx.x, part = blockIdx.y, s = blockIdx.z, P = p.partition_size;
+    int L = p.seq_lens[s];
+    if (L > p.cap) {
+      if (threadIdx.x == 0 && part == 0) atomicOr(&g_status_decode_fp8, METIS_STATUS_SEQ_TOO_LONG);
+      L = p.cap;
+    }
+    L = max(L, 0);
+    const int n = L / P + (L % P != 0);  // partitions with tokens
+    __syncthreads();                     // the barriers are initialised
+    if (part < n)
+      decode_fp8_item<D, NW, STAGES, QT>(
+          tmK, tmV, pp, smem, bars, g, s, s, part * P, min(L, part * P + P), warp, lane, kb, sync,
+          [&](const float* cm, const float* cl, const float* co) {
+            DecodeParams local{};  // one item's partial, in shared memory
+            local.D = D;
+            local.r = local.H = p.r;
+            local.partition_size = P;
+            local.max_parts = 1;
+            local.part_out = jo;
+            local.part_lse = jl;
+            combine_and_store<QT, NW>(local, cm, cl, co, 0, 0, 0, 0, threadIdx.x);
+          });
+    __syncwarp();
+    cluster_sync_all();
+    join_partitions<D, QT, NW * 32>(p, jo, jl, n, g, s);
+    cluster_sync_all();  // nobody leaves while its partial may be read
+  } else {
+    __shared__ int rank_lens[kMaxRankSeqs];
+    __shared__ int rank_found;
+    // KV heads vary fastest: the CTAs that read one page's rows (all heads of a token lie side
+    // by side) run at about the same time
+    const int part = blockIdx.x / p.G, g = blockIdx.x - part * p.G;
+    const int s = (p.partition_size == 0 && p.S <= kMaxRankSeqs) ? seq_of_rank(p, blockIdx.y, rank_lens, &rank_found)
+                                                                  : (int)blockIdx.y;
+    int t0, t1;
+    if (!decode_range<QT>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode_fp8)) return;
+    __syncthreads();  // the barriers are initialised
+    decode_fp8_item<D, NW, STAGES, QT>(tmK, tmV, pp, smem, bars, g, s, s, t0, t1, warp, lane, kb, sync,
+                                       [&](const float* cm, const float* cl, const float* co) {
+                                         combine_and_store<QT, NW, true>(p, cm, cl, co, part, g, s, s, threadIdx.x);
+                                       });
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -835,8 +931,10 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
     if (!decode_range<__nv_bfloat16>(p, 0, g, s, orow, t0, t1, tid, GT, &g_status_decode_fp8)) continue;
     // A wait that gave up (flagged) is seen by its warp only: every warp of the group
     // still reaches the item's barriers and the next one above, where they all stop.
-    if (!decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, gsmem, bars, 0, g, s, orow, t0, t1, warp, lane, tid,
-                                             kb, gsync) &&
+    if (!decode_fp8_item_bf16<D, NW, STAGES>(tmK, tmV, pp, gsmem, bars, g, s, orow, t0, t1, warp, lane, kb, gsync,
+                                             [&](const float* cm, const float* cl, const float* co) {
+                                               combine_and_store<__nv_bfloat16, NW>(p, cm, cl, co, 0, g, s, orow, tid);
+                                             }) &&
         lane == 0)
       gave_up[grp] = 1;
   }
@@ -875,24 +973,29 @@ static int encode_kv8_maps(const DecodeParams& p, const void* k_cache, const voi
   return encode_tiled(tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_cache, dims, strides, box, sw, promo);
 }
 
-template <int D, typename QT, typename Plan>
+template <int D, typename QT, typename Plan, bool JOIN = false>
 static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st) {
   CUtensorMap tmK, tmV;
   int rc = encode_kv8_maps<D>(pp.d, k_cache, v_cache, &tmK, &tmV);
   if (rc) return rc;
   constexpr int smem = fp8_decode_smem_bytes<D, Plan::NW, Plan::STAGES>();
   static int done = 0;
-  auto kern = decode_fp8_kernel<D, QT, Plan>;
+  auto kern = decode_fp8_kernel<D, QT, Plan, JOIN>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
-  const dim3 grid((unsigned)pp.d.max_parts * (unsigned)pp.d.G, (unsigned)pp.d.S);
-  return launch_dependent(kern, grid, dim3(Plan::NW * 32), (size_t)smem, st, "decode_fp8_kernel launch", tmK, tmV, pp);
+  const unsigned parts = (unsigned)pp.d.max_parts, G = (unsigned)pp.d.G, S = (unsigned)pp.d.S;
+  if (JOIN)
+    return launch_dependent_cluster(kern, dim3(G, parts, S), dim3(1, parts, 1), dim3(Plan::NW * 32), (size_t)smem, st,
+                                    "decode_fp8_kernel launch", tmK, tmV, pp);
+  return launch_dependent(kern, dim3(parts * G, S), dim3(Plan::NW * 32), (size_t)smem, st, "decode_fp8_kernel launch",
+                          tmK, tmV, pp);
 }
 
 // The plan by the number of items or partitions against the GPU's SMs (seq_lens are not
-// known here: partitions count max_seq_len).  Many partitions: twelve on each SM, twice over.
+// known here: partitions count max_seq_len).  *joined: the partitions need no merge.
 template <int D, typename QT>
-static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st) {
+static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st,
+                      bool* joined) {
   const DecodeParams& p = pp.d;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -903,7 +1006,15 @@ static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void
     if (items <= sms) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
     return launch_fp8<D, QT, Fp8Unsplit<D>>(pp, k_cache, v_cache, st);
   }
-  if (p.max_parts * items >= 24ll * sms) return launch_fp8<D, QT, Fp8ManyParts>(pp, k_cache, v_cache, st);
+  const long long ctas = p.max_parts * items;
+  *joined = p.max_parts <= kMaxJoin && ctas <= sms;
+  if (*joined && p.partition_size >= 1024 && 2 * ctas <= sms)
+    return launch_fp8<D, QT, Fp8JoinLong, true>(pp, k_cache, v_cache, st);
+  if (*joined) return launch_fp8<D, QT, Fp8FewParts, true>(pp, k_cache, v_cache, st);
+  // one warp per partition: where twelve on each SM are filled twice over, and for short ones as
+  // soon as the four-warp CTAs would not be on the GPU all at once (three per SM, head_dim 64 four)
+  if (ctas >= 24ll * sms || (p.partition_size <= 512 && ctas > (D == 64 ? 4ll : 3ll) * sms))
+    return launch_fp8<D, QT, Fp8ManyParts>(pp, k_cache, v_cache, st);
   return launch_fp8<D, QT, Fp8FewParts>(pp, k_cache, v_cache, st);
 }
 
@@ -1014,14 +1125,15 @@ extern "C" int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, c
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int rc;
+  bool joined = false;
   if (dtype == METIS_F32)
-    rc = head_dim == 64 ? launch_fp8<64, float>(pp, k_cache, v_cache, st)
-                        : launch_fp8<128, float>(pp, k_cache, v_cache, st);
+    rc = head_dim == 64 ? launch_fp8<64, float>(pp, k_cache, v_cache, st, &joined)
+                        : launch_fp8<128, float>(pp, k_cache, v_cache, st, &joined);
   else
-    rc = head_dim == 64 ? launch_fp8<64, __nv_bfloat16>(pp, k_cache, v_cache, st)
-                        : launch_fp8<128, __nv_bfloat16>(pp, k_cache, v_cache, st);
+    rc = head_dim == 64 ? launch_fp8<64, __nv_bfloat16>(pp, k_cache, v_cache, st, &joined)
+                        : launch_fp8<128, __nv_bfloat16>(pp, k_cache, v_cache, st, &joined);
   if (rc) return rc;
-  if (parts)
+  if (parts && !joined)
     rc = launch_merge_ex(p.part_out, p.part_lse, seq_lens, partition_size, out, lse_out, num_seqs, num_heads, head_dim,
                          p.max_parts, dtype, 0, st);
   return rc;

@@ -31,22 +31,33 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const vo
 // stream: it may start launching while that kernel still runs, so it must
 // execute pdl_wait() (common.cuh) before touching anything the previous kernel
 // writes.  Returns METIS_OK or METIS_E_CUDA.
+// The _cluster form launches clusters of the given shape.
 template <typename... KArgs, typename... Args>
-int launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const char* what,
-                     Args... args) {
+int launch_dependent_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 cluster, dim3 block, size_t smem,
+                             cudaStream_t st, const char* what, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) return fail(METIS_E_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return METIS_OK;
+}
+
+template <typename... KArgs, typename... Args>
+int launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const char* what,
+                     Args... args) {
+  return launch_dependent_cluster(kernel, grid, dim3(1, 1, 1), block, smem, st, what, args...);
 }
 
 // Raise a kernel's dynamic shared memory limit once per device.

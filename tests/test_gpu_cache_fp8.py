@@ -380,6 +380,33 @@ def test_decode_more_items_than_sms(D, dtype, partition):
     decode_case(rng, lens, 2, 8, D, 16, dtype, partition=partition)
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32), (64, F32)])
+@pytest.mark.parametrize("partition", [16, 80, 1024])
+def test_decode_few_partitions_joined_in_one_launch(D, dtype, partition):
+    """Up to eight partitions of few items: none, one, a part of one, all of them, and a bound on the
+    lengths that leaves the last ones empty."""
+    rng = np.random.default_rng(partition + D)
+    P = partition
+    for lens, parts in (([0, 1, P - 1, P, P + 1], 2), ([2 * P + 5, 0, 5 * P - 1], 8), ([7 * P + 3], 8), ([P // 2, 3], 1)):
+        for r in (1, 3, 8):
+            decode_case(rng, lens, r, 2, D, 16, dtype, partition=P, max_len=parts * P)
+
+
+def test_decode_joined_partitions_of_a_sequence_past_the_bound():
+    rng = np.random.default_rng(77)
+    lens, D = [300, 90], 64
+    c = Cache(rng, lens, 1, D, 16)
+    q = torch.from_numpy(rng.standard_normal((2, 4, D))).to(BF16)
+    pa.metis_read_status(clear=True)
+    out, lse = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, c.sl, 0.125, partition_size=64, max_seq_len=256,
+                                              want_lse=True)
+    assert pa.metis_read_status(clear=True) == pa.STATUS_SEQ_TOO_LONG  # the first 256 tokens are read
+    c.lens = [256, 90]
+    ref, tol, rl, lt = attention(c, q.double().numpy(), [(0, 256), (1, 90)], 0.125, STEP[BF16])
+    check(out, ref, tol, BF16, "out")
+    check_lse(lse, rl, lt)
+
+
 def test_decode_windows_of_32_units():
     """Sequences whose warps walk several windows of block ids (one warp: 32 units of 32 tokens each)."""
     rng = np.random.default_rng(15)
