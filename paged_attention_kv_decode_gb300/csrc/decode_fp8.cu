@@ -52,7 +52,8 @@ struct DecodeFp8Params {
 
 constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
 constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
-constexpr int kMaxJoin = 8;      // partitions of an item that a cluster takes
+constexpr int kMaxJoin = 8;          // partitions of an item that a cluster takes
+constexpr int kMinJoinTokens = 128;  // ... in a call that asked for none: tokens in each at least
 constexpr float kSlack = 16.f;   // bf16 queries: the sums' reference moves when it is exceeded by 2^16
 
 template <int D>
@@ -694,8 +695,8 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 //                  once the long sequences are alone), 8 warps and one CTA 68 us.
 //                  head_dim 64 (half the bytes per unit): 8 warps, 2 stages, two CTAs: the same
 //                  batch in 33.6 us, 4 warps and 3 stages 43.9 us
-//   few items      up to one per SM: 8 warps, 3 stages: 8 such sequences in 23.6 us, 4 warps
-//                  31.8 us; 29 sequences up to 6,000 tokens, 28/4 heads, 32.9 and 43.6 us
+//   few items      up to one per SM: 8 warps, 3 stages: 29 sequences up to 6,000 tokens, 28/4
+//                  heads, in 32.9 us, 4 warps 43.6 us
 //   many partitions  one warp and 2 stages, twelve CTAs per SM: nothing to combine, and a
 //                  partition's start-up (block ids, scales, query) hides behind eleven others:
 //                  8 sequences of 32-128 K in 512-token partitions 248 us, 4 warps and 3
@@ -705,11 +706,14 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 //                  heads, in 1,024-token partitions 26.8 us; 3 stages and two CTAs 32.5 us, 8
 //                  warps 39.7 us, one warp 40.9 us
 //   a CTA per SM at most, up to 8 partitions  joined in a cluster instead of by a merge kernel:
-//                  one sequence of 4,096 tokens in 512-token partitions 8.5 us, 10.6 us with the
+//                  one sequence of 4,096 tokens in 512-token partitions 8.5 us, 10.7 us with the
 //                  merge (but 16 sequences 41.7 us, 37.7 with it: a cluster's CTAs hold their
-//                  slots until the last one is done).  Partitions of 1,024 tokens and more, half
-//                  the SMs at most: 8 warps, 4,096-token ones 24.2 us, 4 warps 32.3 us; over more
-//                  SMs clusters of whole-SM CTAs do not all fit at a time (16.2 us for 10.4)
+//                  slots until the last one is done).  No merge, no workspace: an unsplit call
+//                  whose items leave SMs idle is split the same way, one sequence of 16,384
+//                  tokens 15.7 us (one CTA per item 73.9), eight of 512..4,096 15.8 us (23.8).
+//                  Partitions of 1,024 tokens and more: 8 warps, 4,096-token ones 24.2 us, 4
+//                  warps 32.3 us; not for clusters of more than four over more than half the
+//                  SMs, which do not all fit at a time (2 x 4,096: 16.2 us for 10.4)
 template <int NW_, int STAGES_, int MIN_CTAS_>
 struct Fp8Plan {
   static constexpr int NW = NW_, STAGES = STAGES_, MIN_CTAS = MIN_CTAS_;
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
     __syncthreads();                     // the barriers are initialised
     if (part < n)
       decode_fp8_item<D, NW, STAGES, QT>(
-          tmK, tmV, pp, smem, bars, g, s, s, part * P, min(L, part * P + P), warp, lane, kb, sync,
+          tmK, tmV, pp, smem, bars, g, s, s, part * P, part * P + min(L - part * P, P), warp, lane, kb, sync,
           [&](const float* cm, const float* cl, const float* co) {
             DecodeParams local{};  // one item's partial, in shared memory
             local.D = D;
@@ -996,21 +1000,26 @@ static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void
 template <int D, typename QT>
 static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void* v_cache, cudaStream_t st,
                       bool* joined) {
-  const DecodeParams& p = pp.d;
+  DecodeFp8Params split = pp;
+  DecodeParams& p = split.d;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(METIS_E_CUDA, "querying the SM count: %s", cudaGetErrorString(e));
   const long long items = (long long)p.G * p.S;
   if (p.partition_size == 0) {
-    if (items <= sms) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
-    return launch_fp8<D, QT, Fp8Unsplit<D>>(pp, k_cache, v_cache, st);
+    if (items > sms) return launch_fp8<D, QT, Fp8Unsplit<D>>(pp, k_cache, v_cache, st);
+    // SMs to spare: partitions all the same (no workspace: they are joined), of whole units
+    const int parts = (int)std::min<long long>({kMaxJoin, sms / items, p.cap / kMinJoinTokens});
+    if (parts < 2) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
+    p.partition_size = (int)((((long long)p.cap + parts - 1) / parts + kUnit8 - 1) / kUnit8 * kUnit8);
+    p.max_parts = (int)(((long long)p.cap + p.partition_size - 1) / p.partition_size);
   }
   const long long ctas = p.max_parts * items;
   *joined = p.max_parts <= kMaxJoin && ctas <= sms;
-  if (*joined && p.partition_size >= 1024 && 2 * ctas <= sms)
-    return launch_fp8<D, QT, Fp8JoinLong, true>(pp, k_cache, v_cache, st);
-  if (*joined) return launch_fp8<D, QT, Fp8FewParts, true>(pp, k_cache, v_cache, st);
+  if (*joined && p.partition_size >= 1024 && (2 * ctas <= sms || p.max_parts <= kMaxJoin / 2))
+    return launch_fp8<D, QT, Fp8JoinLong, true>(split, k_cache, v_cache, st);
+  if (*joined) return launch_fp8<D, QT, Fp8FewParts, true>(split, k_cache, v_cache, st);
   // one warp per partition: where twelve on each SM are filled twice over, and for short ones as
   // soon as the four-warp CTAs would not be on the GPU all at once (three per SM, head_dim 64 four)
   if (ctas >= 24ll * sms || (p.partition_size <= 512 && ctas > (D == 64 ? 4ll : 3ll) * sms))

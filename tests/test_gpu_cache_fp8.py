@@ -381,6 +381,16 @@ def test_decode_more_items_than_sms(D, dtype, partition):
 
 
 @pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32), (64, F32)])
+@pytest.mark.parametrize("S", [1, 3, 12])
+def test_decode_unsplit_with_sms_to_spare(D, dtype, S):
+    """8 to 96 items: several CTAs for each of them (lengths far below the bound, and above them all), or one."""
+    rng = np.random.default_rng(S + D)
+    for lens, max_len in (([2100] + [257] * (S - 1), None), ([700, 0, 1][:S] + [31] * (S - 3), 5000),
+                          ([127, 255, 256][:S] + [100] * (S - 3), None)):
+        decode_case(rng, lens, 2, 8, D, 32, dtype, max_len=max_len)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, BF16), (128, F32), (64, F32)])
 @pytest.mark.parametrize("partition", [16, 80, 1024])
 def test_decode_few_partitions_joined_in_one_launch(D, dtype, partition):
     """Up to eight partitions of few items: none, one, a part of one, all of them, and a bound on the
