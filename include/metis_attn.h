@@ -420,8 +420,11 @@ int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* 
 
 /*
  * metis_paged_attn_prefill_chunk_fp8 -- metis_paged_attn_prefill_chunk over an 8-bit
- * cache: the same arguments, workspace (metis_prefill_workspace_bytes) and
- * limits, with the scales behind the codes; dtype METIS_BF16.  A chunk's query rows
+ * cache: the same arguments and limits, with the scales behind the codes; dtype
+ * METIS_BF16.  The workspace holds at least metis_prefill_workspace_bytes(...); with the
+ * metis_prefill_fp8_workspace_bytes(...) bytes of the call's own sizes (more, where its
+ * chunks may leave SMs idle) the chunks' work is also split over long sequences' keys.
+ * A chunk's query rows
  * enter the products as two e4m3 parts at one power of two each: elements down to 2^-8
  * of the row's largest are exact, smaller ones are off by at most 2^-17 of it.  V
  * enters as bf16, scale included (exact), with softmax weights in bf16.  NaN in V reaches
@@ -435,6 +438,9 @@ int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, 
                                        int num_kv_heads, int head_dim, int block_size, int max_blocks,
                                        int num_blocks, int dtype, float scale, int max_seq_len,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+size_t metis_prefill_fp8_workspace_bytes(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                         int head_dim, int max_seq_len);
 
 /*
  * Prefix cache: page keys and lookup-or-allocate.  A new prompt reuses the KV

@@ -35,6 +35,7 @@ from ._binding import (  # noqa: F401
     metis_paged_attn_decode_partials,
     metis_paged_attn_prefill_chunk,
     metis_paged_attn_prefill_chunk_fp8,
+    metis_prefill_fp8_workspace_bytes,
     metis_prefill_workspace_bytes,
     metis_prefix_block_hashes,
     metis_prefix_lookup,

@@ -69,6 +69,7 @@ SIGNATURES = {
     "metis_paged_attn_prefill_chunk": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                                             _i, _f, _i, _vp, _sz, _vp]),
     "metis_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "metis_prefill_fp8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "metis_mla_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp, _sz, _vp]),
     "metis_mla_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "metis_merge_attn_states": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
@@ -623,6 +624,14 @@ def metis_paged_attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     return out, lse_out
 
 
+def metis_prefill_fp8_workspace_bytes(num_seqs: int, num_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                      max_seq_len: int) -> int:
+    """Workspace with which :func:`metis_paged_attn_prefill_chunk_fp8` may split few chunks over long
+    sequences' keys (:func:`metis_prefill_workspace_bytes` is what it needs at least)."""
+    return int(load_library().metis_prefill_fp8_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                                                max_seq_len))
+
+
 def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: torch.Tensor,
                                        v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                                        block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float, *,
@@ -643,7 +652,7 @@ def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor,
     out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
     if max_seq_len is None:
         max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
-    need = metis_prefill_workspace_bytes(S, T, H, G) if workspace is None else 0
+    need = metis_prefill_fp8_workspace_bytes(S, T, H, G, D, max_seq_len) if workspace is None else 0
     workspace, w_at, w_bytes = _workspace(dev, q, workspace, max(need, 256), stream)
     rc = lib.metis_paged_attn_prefill_chunk_fp8(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width, nb,
                                                 code, float(scale), int(max_seq_len), w_at, w_bytes,

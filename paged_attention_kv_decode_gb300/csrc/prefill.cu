@@ -65,6 +65,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
@@ -106,6 +107,14 @@ constexpr int kKvTile = 128;      // tokens per K/V tile
 constexpr int kRows = 128;        // query rows per tile
 constexpr int kTmemCols = 512;    // S0 | S1 | O0 | O1
 constexpr int kSortMax = 2048;    // schedule: heaviest-first sort up to this many items
+// 8-bit cache, few chunks: parts of a unit at most, K/V tiles of each at least, and of the whole
+// unit.  A part costs some 3 us (its start, its rows written, read and merged) and a tile 1.5:
+// 512 queries behind 1,024 tokens (9 tiles and more) take 37 us in parts and 34 whole, behind
+// 2,048 43.7 and 47.7, behind 8,192 84.6 and 126.9, behind 32,768 264 and 476; 256 behind 16,384
+// 85 and 232.
+constexpr int kMaxSplits = 8;
+constexpr int kMinPartTiles = 4;
+constexpr int kMinSplitTiles = 13;
 
 struct PrefillParams {
   const void* q;
@@ -131,6 +140,12 @@ struct PrefillParams {
   int kv_token_bytes;  // K and V of one cached token, every KV head
   int wait_at_exit;
   Fp8Cache fp8;  // an 8-bit cache (k_cache NULL: bf16)
+  // 8-bit cache, splits != NULL: units that leave SMs idle are split over their keys.  The
+  // schedule kernel writes how often (*splits) and zeroes the counters of finished parts.
+  int* splits;
+  int* parts_done;  // [item, KV head][query tile][warp]
+  float* part_lse;  // [unit][query tile][row], log2 units
+  float* part_out;  // [unit][query tile][head_dim / 4][row][4], normalised
 };
 
 // Shared-memory layout (all tiles 128-byte swizzled, [64-column half][row][128 B]).
@@ -177,6 +192,7 @@ struct PfFp8Shared {
   // 0 * NaN would reach every row, and put into the output columns of the rows that see them
   int nan_any[kNanUnits];
   uint16_t nan_first[kNanUnits][128];  // per column: the first such token behind the unit's first query
+  int tag[kNanUnits];                  // the unit's PfUnit8::tag
 };
 
 // The converters' rare case: one row's 16 codes from column `col` on, or their scale, hold
@@ -302,6 +318,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
   // and combined by the last warp (no sequences there unless S > 992): off the path
   // of the listing and the sort.
   __shared__ long long red[2][kSchedThreads / 32];
+  __shared__ int dec_share;
   static_assert(kSchedThreads == 32 * 32, "one warp combines the warp sums");
   const int lane = tid & 31, warp = tid >> 5;
   if (p.dec_ctas) {
@@ -332,11 +349,19 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
       const float c = (float)cq * ((float)p.H * p.D * 4.0f / (kv8 ? kChunk8SmFlopsPerS : kChunkSmFlopsPerS));
       int k = 0;
       if (dt > 0) k = cq > 0 ? (int)ceilf(p.num_sms * (d / (d + c))) : p.num_sms;
-      *p.dec_ctas = min(max(k, dt > 0 ? 1 : 0), p.num_sms);
+      *p.dec_ctas = dec_share = min(max(k, dt > 0 ? 1 : 0), p.num_sms);
       *p.dec_next = 0;
     }
   }
   const int total = min(all, max_items);
+  if (p.splits) {
+    __syncthreads();  // the decodes' share is known
+    const int units = total * p.G, sms = p.num_sms - (p.dec_ctas ? dec_share : 0);
+    const int n = units > 0 ? min(kMaxSplits, sms / units) : 1;
+    if (tid == 0) *p.splits = max(n, 1);
+    if (n > 1)
+      for (int i = tid; i < units * 2 * (kRows / 32); i += kSchedThreads) p.parts_done[i] = 0;
+  }
   const bool sort = total <= kSortMax;
   for (int s = s0; s < s1; ++s) {
     int L = L_first, q_len = q_first;
@@ -394,6 +419,16 @@ struct PfUnit {
   int s, pair, g, L, q_len, n0, n1, n_kv, q0, n_pages;
 };
 
+// 8-bit cache: a unit may be one of `parts` parts of the pair's K/V tiles, [j0, j0 + n_kv).
+struct PfUnit8 : PfUnit {
+  int j0;
+  int tag;  // 0: all of them, else (item, KV head) << 8 | parts << 4 | part
+};
+
+// The unit's first K/V tile
+__device__ __forceinline__ int pf_first(const PfUnit&) { return 0; }
+__device__ __forceinline__ int pf_first(const PfUnit8& it) { return it.j0; }
+
 __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag, PfUnit& it) {
   const int item_idx = u / p.G;
   it.g = u - item_idx * p.G;
@@ -407,6 +442,30 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag
   it.q0 = p.cu_q_lens[it.s];
   it.n_pages = (it.L + p.bs - 1) / p.bs;
   return it.n0 > 0;
+}
+
+// Unit u of whole * splits; the parts in order of their keys, so that every CTA counts the
+// same ones.  A part begins where every query row of the pair sees keys: its running
+// maximum is finite from its first tile on.
+__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole, int splits, bool flag, PfUnit8& it) {
+  const int part = u / whole;
+  u -= part * whole;
+  it.j0 = it.tag = 0;
+  if (!pf_unit(p, u, flag && part == 0, it)) return false;
+  if (splits > 1 && it.n_kv < kMinSplitTiles) return part == 0;
+  if (splits > 1) {
+    const int len = max((it.n_kv + splits - 1) / splits, kMinPartTiles);
+    const int last = (it.L - it.q_len + 2 * it.pair * p.Tq) / kKvTile;  // the latest first tile
+    const int parts = min(splits, last / len + 1);
+    if (part >= parts) return false;
+    if (parts > 1) it.tag = u << 8 | parts << 4 | part;
+    it.j0 = part * len;
+    const int end = part == parts - 1 ? it.n_kv : it.j0 + len;
+    it.n0 = min(it.n0, end) - it.j0;
+    if (it.n1 > 0) it.n1 = min(it.n1, end) - it.j0;
+    it.n_kv = max(it.n0, it.n1);
+  }
+  return true;
 }
 
 // Eight e4m3 codes of one row times their page's scale, as bf16 (exact: four significant
@@ -456,10 +515,83 @@ __device__ __forceinline__ float split_query_row(uint8_t* tile, int row) {
   return __uint_as_float(field >= 255u ? 0x7fc00000u : (field - 7u) << 23);
 }
 
+// A part's result for row `row` of query tile w, for join_parts: normalised, rows side by side.
+template <int D>
+__device__ __forceinline__ void write_part(const PrefillParams& p, int tag, int whole, int w, int row,
+                                           uint32_t o_tmem, float inv, float lse2, bool nan_any,
+                                           const uint16_t* nan_first, int rel) {
+  const size_t tile = (size_t)((tag & 15) * whole + (tag >> 8)) * 2 + w;
+  float4* out = reinterpret_cast<float4*>(p.part_out) + tile * (D / 4) * kRows + row;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t ov[32];
+    tmem_ld32(o_tmem + c * 32, ov);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+      out[(c * 8 + i / 4) * kRows] = make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
+                                                 __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
+  }
+  if (nan_any) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d)
+      if (nan_first[d] <= rel) reinterpret_cast<float*>(out + (d / 4) * kRows)[d % 4] = __uint_as_float(0x7fc00000u);
+  }
+  p.part_lse[tile * kRows + row] = lse2;
+}
+
+// The warp that finishes its 32 rows of a unit last merges their parts, in the order of the
+// keys: out = sum of o_i 2^(x_i - M) over sum of 2^(x_i - M).
+template <int D>
+__device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int whole, int w, int row, int lane,
+                                           __nv_bfloat16* orow, float* lse) {
+  const int parts = (tag >> 4) & 15;
+  __threadfence();  // the part is visible before it is counted
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicAdd(p.parts_done + ((size_t)(tag >> 8) * 2 + w) * (kRows / 32) + row / 32, 1);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before != parts - 1) return;
+  __threadfence();
+  if (orow == nullptr) return;
+  const size_t tile = (size_t)(tag >> 8) * 2 + w, next = (size_t)whole * 2;
+  float x[kMaxSplits], M = -INFINITY, W = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) {
+    x[i] = i < parts ? __ldcg(p.part_lse + (tile + i * next) * kRows + row) : -INFINITY;
+    M = fmaxf(M, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) {
+    x[i] = i < parts ? exp2_approx(x[i] - M) : 0.f;
+    W += x[i];
+  }
+  const float inv = 1.f / W;
+  const float4* src = reinterpret_cast<const float4*>(p.part_out) + tile * (D / 4) * kRows + row;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i)
+      if (i < parts) {
+        const float4* at = src + i * next * (D / 4) * kRows + (size_t)(2 * c) * kRows;
+        const float4 u = __ldcg(at), v = __ldcg(at + kRows);
+        a = make_float4(fmaf(x[i], u.x, a.x), fmaf(x[i], u.y, a.y), fmaf(x[i], u.z, a.z), fmaf(x[i], u.w, a.w));
+        b = make_float4(fmaf(x[i], v.x, b.x), fmaf(x[i], v.y, b.y), fmaf(x[i], v.z, b.z), fmaf(x[i], v.w, b.w));
+      }
+    *reinterpret_cast<uint4*>(orow + c * 8) =
+        make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
+                   pack_bf16x2(b.x * inv, b.y * inv), pack_bf16x2(b.z * inv, b.w * inv));
+  }
+  if (lse) *lse = (M + log2f(W)) * kLn2;
+}
+
 // KV8: the cache holds e4m3 codes.  K tiles feed the tensor cores as they are, against the
 // query rows split into two e4m3 parts; V tiles are converted to bf16 on the way; a K page's
 // scale joins the softmax factor of its 16 tokens.
-template <int D, bool KV8>
+// SPLIT (8-bit cache): units may be parts of a pair's keys.  An instantiation of its own: the
+// registers and the code of the parts cost whole units 2-3 %.
+template <int D, bool KV8, bool SPLIT>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                        const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
@@ -467,6 +599,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   using Sh = PfShape<D, KV8>;
   constexpr int HALVES = Sh::kHalves;
   constexpr int kStages8 = kV8Stages;
+  static_assert(KV8 || !SPLIT, "parts of units: 8-bit cache only");
+  using Unit = std::conditional_t<SPLIT, PfUnit8, PfUnit>;
   if (!p.wait_at_exit) pdl_wait();  // the schedule kernel's items are complete and visible
   extern __shared__ uint8_t smem_raw[];
   const uint32_t slack = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -490,11 +624,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PfBar::kCount);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + PfBar::kCount + 1);
   volatile int* unit_slot = reinterpret_cast<volatile int*>(bars + PfBar::kCount + 2);  // [2]
-  __shared__ PfUnit unit_info[2];  // the published unit, derived once by the fetcher
+  __shared__ Unit unit_info[2];  // the published unit, derived once by the fetcher
   __shared__ PfFp8Shared x8;       // (8-bit cache only)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = __ldcg(p.item_count) * p.G;
+  const int whole = __ldcg(p.item_count) * p.G;
+  const int splits = SPLIT ? __ldcg(p.splits) : 1;
+  const int units = whole * splits;
   if ((int)blockIdx.x >= units) {
     if (p.wait_at_exit) pdl_wait();  // complete only after the decode grid in front of this one
     return;
@@ -545,7 +681,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   // The k-th unit of this CTA, from the unit ring: 1 = a unit, 0 = no more, -1 = aborted.
   // The fetcher publishes the unit's derived fields with it, so that no role waits on
   // global loads at a unit boundary.
-  auto next_unit = [&](uint32_t& k, PfUnit& it) -> int {
+  auto next_unit = [&](uint32_t& k, Unit& it) -> int {
     const int slot = k & 1;
     if (!wait_all(&unit_full[slot], (k >> 1) & 1)) return -1;
     const int u = unit_slot[slot];
@@ -571,7 +707,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     }
     uint32_t t = 0, k = 0;                     // tiles issued so far, units read
     bool ok = true;
-    PfUnit it;
+    Unit it;
     while (ok && next_unit(k, it) > 0) {
       const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
       {
@@ -579,11 +715,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         uint32_t* first = reinterpret_cast<uint32_t*>(x8.nan_first[slot]);
         for (int i = lane; i < 64; i += 32) first[i] = 0xffffffffu;
         if (lane == 0) x8.nan_any[slot] = 0;
+        if constexpr (SPLIT)
+          if (lane == 0) x8.tag[slot] = it.tag;
         __syncwarp();
       }
       // page `lane` of tile j: its TMA row (a bad id reads a box out of bounds: zeros) and scales
       auto page_of = [&](int j, int& rowc, float& fk, float& fv) -> bool {
-        const int pg = j * npg + lane;
+        const int pg = (pf_first(it) + j) * npg + lane;
         rowc = -p.bs;
         fk = fv = 1.f;
         if (lane >= npg || pg >= it.n_pages) return false;
@@ -650,7 +788,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const int cw = warp == 15 ? 3 : warp - 9;
     uint32_t t = 0, k = 0;
     bool ok = true;
-    PfUnit it;
+    Unit it;
     while (ok && next_unit(k, it) > 0) {
       constexpr int CPR = D / 16, RPC = 32 / CPR;   // V: 16-byte pieces of a row, rows per pass
       const int piece = lane % CPR;
@@ -673,7 +811,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) = flip ? b : a;
           *reinterpret_cast<uint4*>(dst + (((ch ^ 1) ^ (row & 7)) << 4)) = flip ? a : b;
         };
-        const int seen_rows = p_min + 1 - j * kKvTile;  // rows that every query row of the unit sees
+        const int seen_rows = p_min + 1 - (pf_first(it) + j) * kKvTile;  // rows that every query row of the unit sees
         if (seen_rows >= kKvTile) {
 #pragma unroll 1
           for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
@@ -681,7 +819,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
             put(row, src[i * 32], x8.vs[sv][row >> 4]);
           }
         } else {
-          const int live_rows = it.L - j * kKvTile;     // rows past the sequence end become zeros
+          const int live_rows = it.L - (pf_first(it) + j) * kKvTile;  // rows past the sequence end become zeros
 #pragma unroll 1
           for (int i = cw; i < kKvTile / RPC; i += kV8Converters) {
             const int row = i * RPC + lane / CPR;
@@ -723,7 +861,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     if (lane == 0) tma_prefetch_desc(map);
     uint32_t t = 0, k = 0;                     // tiles issued so far, units read
     bool ok = true;
-    PfUnit it;
+    Unit it;
     while (ok && next_unit(k, it) > 0) {
       const int32_t* bt_row = p.block_table + (size_t)it.s * p.max_blocks;
       for (int j = 0; j < it.n_kv; ++j, ++t) {
@@ -892,7 +1030,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     uint32_t t_base = 0, n_units = 0, np[2] = {0u, 0u};  // tiles, units, p_full phases consumed
     uint32_t k = 0;
     bool ok = true;
-    PfUnit it;
+    Unit it;
     while (ok) {
       const int r = next_unit(k, it);
       if (r <= 0) {
@@ -982,7 +1120,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     if (lane == 0) tma_prefetch_desc(&tmQ);
     uint32_t n_units = 0, n_two = 0, k = 0;
-    PfUnit it;
+    Unit it;
     while (next_unit(k, it) > 0) {
       // the previous unit's query tiles stay until its last QK has completed
       if (n_units > 0 && !wait_all(q_free, (n_units - 1) & 1)) break;
@@ -1018,12 +1156,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     for (;;) {
       const int slot = k & 1;
       if (k >= 1 && !wait_all(&unit_empty[(k - 1) & 1], ((k - 1) >> 1) & 1)) break;
+      // parts: about as many as CTAs.  One that claims a second while it runs its first takes it
+      // from a CTA that starts a little later (2 x 256 queries beside 32 decodes: 147 or 173 us)
+      if (SPLIT && k >= 1 && !wait_all(q_free, (k - 1) & 1)) break;
       int u = 0;
       if (lane == 0) u = atomicAdd(p.unit_head, 1);
       u = __shfl_sync(0xffffffffu, u, 0);
-      PfUnit it;
+      Unit it;
       if (u < units) {
-        if (!pf_unit(p, u, lane == 0, it)) continue;   // nothing to compute (length errors flagged here)
+        bool some;                                     // nothing to compute (length errors flagged here)
+        if constexpr (SPLIT)
+          some = pf_unit(p, u, whole, splits, lane == 0, it);
+        else
+          some = pf_unit(p, u, lane == 0, it);
+        if (!some) continue;
       } else {
         u = -1;
       }
@@ -1053,14 +1199,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const float asl2 = fmaxf(fabsf(sl2), 1e-30f);
     uint32_t ns = 0, npv = 0, k = 0;            // s_full phases consumed, PVs of this group, units read
     bool ok = true;
-    PfUnit it;
+    Unit it;
     // 8-bit cache: a unit is taken, and its query rows are split, before the unit in front
     // of it is written out, so that the tensor cores have the next QK meanwhile.
     [[maybe_unused]] uint32_t t_base = 0, n_split = 0;  // K/V tiles of the units before, query tiles split
     [[maybe_unused]] float row_factor = 0.f, next_factor = 0.f;  // |sl2| without the query row's scaling
     [[maybe_unused]] int nan_slot = 0;                           // of the unit in hand
     [[maybe_unused]] bool have = false;
-    [[maybe_unused]] PfUnit next;
+    [[maybe_unused]] Unit next;
     [[maybe_unused]] auto advance = [&]() {
       have = next_unit(k, next) > 0;
       if (!have || (w ? next.n1 : next.n0) == 0) return;
@@ -1093,7 +1239,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         if constexpr (KV8) advance();
         continue;
       }
-      const int L = it.L, q_len = it.q_len;
+      const int L = it.L - pf_first(it) * kKvTile, q_len = it.q_len;  // positions from the unit's first key on
       const int hh = row / p.Tq;
       const int qi0 = (2 * it.pair + w) * p.Tq;
       const int qi = qi0 + (row - hh * p.Tq);
@@ -1220,6 +1366,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       const float inv = 1.0f / l_run;
       const int head = it.g * p.r + hh;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)(it.q0 + qi) * p.H + head) * D;
+      if constexpr (SPLIT) {
+        const int tag = *reinterpret_cast<volatile int*>(&x8.tag[nan_slot]);
+        if (tag) {
+          const int whole = __ldcg(p.item_count) * p.G;
+          write_part<D>(p, tag, whole, w, row, o_tmem, inv, m_run + log2f(l_run), x8.nan_any[nan_slot] != 0,
+                        x8.nan_first[nan_slot], p_row - (L - q_len + 2 * it.pair * p.Tq));
+          tc_fence_before_sync();  // O_w may be overwritten
+          join_parts<D>(p, tag, whole, w, row, lane, row_valid ? orow : nullptr,
+                        row_valid && p.lse_out ? p.lse_out + (size_t)(it.q0 + qi) * p.H + head : nullptr);
+          continue;
+        }
+      }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
@@ -1281,9 +1439,20 @@ static size_t prefill_max_items(int num_seqs, int num_tokens, int Tq) {
   return (size_t)(num_tokens + 2 * Tq - 1) / (2 * Tq) + (size_t)num_seqs;
 }
 
+// 8-bit cache: memory for parts of units, behind the item list: counters, lse and rows of as
+// many units as SMs.  None where the chunks' pairs (one sequence's, if all are) fill more
+// than half of the SMs, or the sequences are short.
+static size_t prefill_split_offset(size_t max_items) { return align_up(256 + max_items * sizeof(int4), 256); }
+
+static size_t prefill_split_bytes(int num_tokens, int Tq, int G, int D, int cap, int sms) {
+  const long long pairs = std::max(1, num_tokens / (2 * Tq));
+  if (2 * pairs * G > sms || cap <= (kMinSplitTiles - 1) * kKvTile) return 0;
+  return align_up((size_t)sms * 2 * (kRows / 32) * sizeof(int), 256) + (size_t)sms * 2 * kRows * (1 + D) * sizeof(float);
+}
+
 // The schedule kernel, then `between(p)` (the decodes of a mixed batch, or
 // nothing), then the chunk kernel.
-template <int D, bool KV8, typename Between>
+template <int D, bool KV8, bool SPLIT, typename Between>
 static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_cache, const void* v_cache,
                           void* workspace, size_t max_items, int sms, cudaStream_t st, Between between) {
   PrefillParams p = p0;
@@ -1296,6 +1465,15 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
     p.dec_ctas = count + 2;
     p.dec_next = count + 3;
     p.wait_at_exit = 1;
+  }
+  if (SPLIT) {
+    char* at = reinterpret_cast<char*>(workspace) + prefill_split_offset(max_items);
+    p.splits = count + 4;
+    p.parts_done = reinterpret_cast<int*>(at);
+    at += align_up((size_t)sms * 2 * (kRows / 32) * sizeof(int), 256);
+    p.part_lse = reinterpret_cast<float*>(at);
+    at += (size_t)sms * 2 * kRows * sizeof(float);
+    p.part_out = reinterpret_cast<float*>(at);
   }
   p.num_sms = sms;
   p.D = D;
@@ -1326,7 +1504,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   if (rc) return rc;
   constexpr int smem = PfShape<D, KV8>::kSmem;
   static int done = 0;
-  auto kern = prefill_bf16_kernel<D, KV8>;
+  auto kern = prefill_bf16_kernel<D, KV8, SPLIT>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   // the warpgroups' register targets draw on the launch allocation: refuse to launch
@@ -1343,7 +1521,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   }
   // persistent: at most one CTA per SM, each taking units from the list as it goes
   // (beside the decodes: the CTAs past the SMs they keep start as their CTAs finish)
-  const size_t grid = std::min<size_t>(max_items * p.G, (size_t)std::max(sms, 1));
+  const size_t grid = SPLIT ? (size_t)sms : std::min<size_t>(max_items * p.G, (size_t)std::max(sms, 1));
   return launch_dependent(kern, dim3((unsigned)grid), dim3(kPfThreads), smem, st, "prefill_bf16_kernel launch", tmQ,
                           tmK, tmV, p);
 }
@@ -1357,6 +1535,21 @@ extern "C" size_t metis_prefill_workspace_bytes(int num_seqs, int num_tokens, in
   const int r = num_heads / num_kv_heads;
   if (r > kRows) return 0;
   return 256 + prefill_max_items(num_seqs, num_tokens, kRows / r) * sizeof(int4);
+}
+
+extern "C" size_t metis_prefill_fp8_workspace_bytes(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                                    int head_dim, int max_seq_len) {
+  const size_t need = metis_prefill_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads);
+  if (!need || (head_dim != 64 && head_dim != 128) || max_seq_len <= 0) return need;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return need;
+  }
+  const int Tq = kRows / (num_heads / num_kv_heads);
+  const size_t split = prefill_split_bytes(num_tokens, Tq, num_kv_heads, head_dim, max_seq_len, sms);
+  return split ? prefill_split_offset(prefill_max_items(num_seqs, num_tokens, Tq)) + split : need;
 }
 
 namespace metis {
@@ -1438,11 +1631,19 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
                                      num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale,
                                      pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
   };
-  if (fp8.k_cache)
-    return head_dim == 128 ? launch_prefill<128, true>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between)
-                           : launch_prefill<64, true>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
-  return head_dim == 128 ? launch_prefill<128, false>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between)
-                         : launch_prefill<64, false>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+  auto launch = [&](auto dim, auto kv8, auto split) {
+    return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value>(
+        p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (!fp8.k_cache) return head_dim == 128 ? launch(D128{}, No{}, No{}) : launch(D64{}, No{}, No{});
+  const size_t parts = prefill_split_bytes(num_tokens, p.Tq, num_kv_heads, head_dim, p.cap, sms);
+  if (parts > 0 && workspace_bytes >= prefill_split_offset(max_items) + parts)
+    return head_dim == 128 ? launch(D128{}, Yes{}, Yes{}) : launch(D64{}, Yes{}, Yes{});
+  return head_dim == 128 ? launch(D128{}, Yes{}, No{}) : launch(D64{}, Yes{}, No{});
 }
 
 }  // namespace metis

@@ -167,6 +167,16 @@ def test_prefill_workspace_bytes(lib):
     assert pa.metis_prefill_workspace_bytes(0, 100, 32, 8) == 0
 
 
+def test_prefill_fp8_workspace_bytes(lib):
+    # never less than what every call needs; the same where nothing can be split (a GPU's worth of chunks, short sequences)
+    for args in ((4, 100, 32, 8), (1, 512, 32, 8), (0, 100, 32, 8), (3, 9, 30, 8)):
+        least = pa.metis_prefill_workspace_bytes(*args)
+        assert pa.metis_prefill_fp8_workspace_bytes(*args, 128, 100000) >= least
+        assert pa.metis_prefill_fp8_workspace_bytes(*args, 128, 1000) == least
+    assert pa.metis_prefill_fp8_workspace_bytes(9, 100000, 32, 8, 128, 100000) == pa.metis_prefill_workspace_bytes(
+        9, 100000, 32, 8)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), -1), (dict(kv=None), -1), (dict(dl=256), -3), (dict(dr=32), -3), (dict(H=100), -3),
     (dict(bs=8), -3), (dict(P=48), -2), (dict(q=FAKE + 4), -4), (dict(ws=None), -5), (dict(ws_bytes=8), -5),

@@ -630,6 +630,35 @@ def test_prefill_more_units_than_sms(r, G, D, bs):
     assert pa.metis_read_status() == 0
 
 
+@pytest.mark.parametrize("r,G,D,bs", [(4, 2, 128, 16), (1, 1, 64, 32), (8, 1, 64, 16), (2, 3, 128, 64), (16, 2, 128, 16)])
+def test_prefill_few_chunks_split_over_their_keys(r, G, D, bs):
+    """Chunks that leave most SMs idle, behind prefixes that end at, before and behind a tile's and a
+    part's edge, beside short ones and decodes."""
+    rng = np.random.default_rng(r + D)
+    for spans in ([(3000, 70)], [(1025, 1024)], [(2560, 128), (90, 1), (700, 33)], [(1024 + 17, 17), (513, 2), (40, 40)],
+                  [(4500, 3), (1300, 1), (0, 0), (5, 2)]):
+        prefill_case(rng, spans, r, G, D, bs)
+
+
+def test_prefill_split_and_whole_agree_and_repeat():
+    """The same call with and without the memory for parts, and twice with it."""
+    rng = np.random.default_rng(31)
+    c = Cache(rng, [2900, 64, 1500], 2, 128, 16)
+    q_lens = [100, 1, 300]
+    cu = i32(np.concatenate([[0], np.cumsum(q_lens)]))
+    q = gpu(torch.from_numpy(rng.standard_normal((401, 8, 128))).to(BF16))
+    small, full = pa.metis_prefill_workspace_bytes(3, 401, 8, 2), pa.metis_prefill_fp8_workspace_bytes(3, 401, 8, 2, 128, 2900)
+    assert full > small
+    outs = [pa.metis_paged_attn_prefill_chunk_fp8(
+        q, cu, *c.dev, c.bt, c.sl, 0.088, max_seq_len=2900, want_lse=True,
+        workspace=torch.full((n,), 0xAB, dtype=torch.uint8, device=DEV)) for n in (small, full, full)]
+    assert torch.equal(outs[1][0].view(torch.int16), outs[2][0].view(torch.int16)) and torch.equal(outs[1][1], outs[2][1])
+    a, b = outs[0][0].double(), outs[1][0].double()
+    # each is within its bound of the exact row, 2^-7 of a weighted mean of |v| (at most 2^2 * 4.5 here) and a rounding
+    assert ((a - b).abs() <= 2 * (2.0 ** -7 * 18 + 2.0 ** -8 * a.abs())).all()
+    assert (outs[0][1] - outs[1][1]).abs().max() <= 1e-3
+
+
 def test_prefill_chunks_only_and_decodes_only():
     rng = np.random.default_rng(20)
     prefill_case(rng, [(520, 257), (3, 3)], 4, 2, 128, 16)
@@ -659,7 +688,7 @@ def test_prefill_nan_of_a_token_reaches_only_the_rows_that_see_it(r, D, bs):
     """NaN codes in K and V, and pages whose scale is NaN, of tokens that earlier rows of the same
     chunk must not see: NaN appears in the rows at and behind them alone, of V in its column alone."""
     rng = np.random.default_rng(r * 10 + D)
-    spans = [(400, 300), (170, 170), (333, 130), (90, 1), (260, 5)]
+    spans = [(400, 300), (170, 170), (333, 130), (90, 1), (260, 5), (2100, 60)]
     lens, q_lens = [n for n, _ in spans], [n for _, n in spans]
     G = 2
     c = Cache(rng, lens, G, D, bs)
@@ -668,7 +697,7 @@ def test_prefill_nan_of_a_token_reaches_only_the_rows_that_see_it(r, D, bs):
         return c.table[s, t // bs], t % bs
 
     v_nans = [(0, 101, 0, 3), (0, 130, 0, 3), (0, 140, 1, 60), (0, 377, 0, 7), (0, 399, 1, 0), (1, 5, 1, 33), (1, 6, 1, 33),
-              (1, 127, 0, 63), (1, 128, 0, 62), (2, 250, 1, 1), (2, 20, 1, 40), (4, 258, 0, 9)]
+              (1, 127, 0, 63), (1, 128, 0, 62), (2, 250, 1, 1), (2, 20, 1, 40), (4, 258, 0, 9), (5, 700, 0, 11), (5, 2041, 1, 12), (5, 2099, 0, 0), (5, 2048, 0, 8)]
     for s, t, g, d in v_nans:
         c.v[(*at(s, t), g, d)] = rng.choice([0x7F, 0xFF])
     c.k[(*at(1, 150), 1, 4)] = 0x7F
