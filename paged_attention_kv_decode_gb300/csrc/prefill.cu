@@ -61,7 +61,8 @@
 // (bf16 kernel 460 us); 16 chunks of 512 behind up to 4,096 tokens 258 us (247).  On the way
 // there: K converted to bf16 as well 2,154 us for the first; codes into the UMMAs and V
 // converted by three warps 528 us; the issuer's operands uniform over its warp, queries
-// split by the softmax threads and a fourth converter 431 us.
+// split by the softmax threads and a fourth converter 431 us.  Few chunks: units are split
+// over their keys (SPLIT, at kMaxSplits).
 #include <math.h>
 
 #include <algorithm>
