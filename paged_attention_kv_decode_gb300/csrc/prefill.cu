@@ -57,7 +57,7 @@
 // page's scale joins the softmax factor of its 16 tokens.  V's codes are staged by TMA and
 // become bf16 rows, scale included (exact), by four warps; P stays bf16.  What bounds it is
 // what bounds the bf16 kernel, the UMMA issuer's waits for P (and here for converted V
-// tiles): 2,048 queries over 16,384 tokens, 32/8 heads of 128, take 430 us = 1,200 TFLOP/s
+// tiles): 2,048 queries over 16,384 tokens, 32/8 heads of 128, take 420 us = 1,230 TFLOP/s
 // (bf16 kernel 460 us); 16 chunks of 512 behind up to 4,096 tokens 258 us (247).  On the way
 // there: K converted to bf16 as well 2,154 us for the first; codes into the UMMAs and V
 // converted by three warps 528 us; the issuer's operands uniform over its warp, queries
@@ -109,10 +109,10 @@ constexpr int kRows = 128;        // query rows per tile
 constexpr int kTmemCols = 512;    // S0 | S1 | O0 | O1
 constexpr int kSortMax = 2048;    // schedule: heaviest-first sort up to this many items
 // 8-bit cache, few chunks: parts of a unit at most, K/V tiles of each at least, and of the whole
-// unit.  A part costs some 3 us (its start, its rows written, read and merged) and a tile 1.5:
-// 512 queries behind 1,024 tokens (9 tiles and more) take 37 us in parts and 34 whole, behind
-// 2,048 43.7 and 47.7, behind 8,192 84.6 and 126.9, behind 32,768 264 and 476; 256 behind 16,384
-// 85 and 232.
+// unit (a tile takes 1.5 us).  64 units, 512 queries at 32/8 heads: behind 1,024 tokens (9 tiles
+// and more) 37 us in parts and 34 whole, behind 2,048 43.7 and 47.7, behind 8,192 84.6 and 126.9,
+// behind 32,768 264 and 476.  32 units behind 16,384: 85 and 232.  192, 40 of them behind a whole
+// round, behind 8,192: 196 and 257.
 constexpr int kMaxSplits = 8;
 constexpr int kMinPartTiles = 4;
 constexpr int kMinSplitTiles = 13;
@@ -141,12 +141,14 @@ struct PrefillParams {
   int kv_token_bytes;  // K and V of one cached token, every KV head
   int wait_at_exit;
   Fp8Cache fp8;  // an 8-bit cache (k_cache NULL: bf16)
-  // 8-bit cache, splits != NULL: units that leave SMs idle are split over their keys.  The
-  // schedule kernel writes how often (*splits) and zeroes the counters of finished parts.
-  int* splits;
-  int* parts_done;  // [item, KV head][query tile][warp]
-  float* part_lse;  // [unit][query tile][row], log2 units
-  float* part_out;  // [unit][query tile][head_dim / 4][row][4], normalised
+  // 8-bit cache, splits != NULL: the units of a last round that leaves SMs idle are split
+  // over their keys.  The schedule kernel writes {how often, how many units stay whole} and
+  // zeroes the counters of finished parts.
+  int2* splits;
+  int max_parts;    // memory for this many parts
+  int* parts_done;  // [split unit][query tile][warp]
+  float* part_lse;  // [part][query tile][row], log2 units
+  float* part_out;  // [part][query tile][head_dim / 4][row][4], normalised
 };
 
 // Shared-memory layout (all tiles 128-byte swizzled, [64-column half][row][128 B]).
@@ -283,6 +285,26 @@ constexpr float kChunkSmFlopsPerS = 7.0e12f;
 constexpr float kDec8SmBytesPerS = 43e9f;
 constexpr float kChunk8SmFlopsPerS = 7.0e12f;
 
+// How often to split each unit of the last round, units % sms of them on `sms` SMs with up to
+// `tiles` K/V tiles each: the least time, in tiles.  Parts cost two on top in a round of their
+// own and nine for each round that begins behind another (the next unit is claimed, and its
+// queries fetched, when the last one's QK is done).
+__host__ __device__ inline int pf_splits(long long units, int sms, int tiles, int max_parts) {
+  const int rest = (int)(units % sms);
+  if (tiles < kMinSplitTiles || rest == 0) return 1;
+  int best = 1, cost = tiles;
+  for (int n = 2; n <= kMaxSplits && rest * n <= max_parts; ++n) {
+    const int len = (tiles + n - 1) / n, rounds = (rest * n + sms - 1) / sms;
+    if (len < kMinPartTiles) break;
+    const int c = rounds * len + 2 + 9 * (rounds - 1) + (units > rest ? 9 : 0);
+    if (c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
 __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const PrefillParams p, int4* items,
                                                                           int* count, int max_items) {
   __shared__ int warp_sums[32];
@@ -319,7 +341,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
   // and combined by the last warp (no sequences there unless S > 992): off the path
   // of the listing and the sort.
   __shared__ long long red[2][kSchedThreads / 32];
-  __shared__ int dec_share;
+  __shared__ int dec_share, longest;
   static_assert(kSchedThreads == 32 * 32, "one warp combines the warp sums");
   const int lane = tid & 31, warp = tid >> 5;
   if (p.dec_ctas) {
@@ -355,15 +377,11 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
     }
   }
   const int total = min(all, max_items);
-  if (p.splits) {
-    __syncthreads();  // the decodes' share is known
-    const int units = total * p.G, sms = p.num_sms - (p.dec_ctas ? dec_share : 0);
-    const int n = units > 0 ? min(kMaxSplits, sms / units) : 1;
-    if (tid == 0) *p.splits = max(n, 1);
-    if (n > 1)
-      for (int i = tid; i < units * 2 * (kRows / 32); i += kSchedThreads) p.parts_done[i] = 0;
-  }
   const bool sort = total <= kSortMax;
+  if (p.splits) {
+    if (tid == 0) longest = 0;
+    __syncthreads();
+  }
   for (int s = s0; s < s1; ++s) {
     int L = L_first, q_len = q_first;
     bool routed = routed_first;
@@ -376,6 +394,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
       if (pos >= total) break;
       const int work = pf_kv_tiles(L, q_len, 2 * t, p.Tq) + pf_kv_tiles(L, q_len, 2 * t + 1, p.Tq);
       const int4 it = make_int4(s, t, work, 0);
+      if (p.splits) atomicMax(&longest, pf_kv_tiles(L, q_len, 2 * t, p.Tq));
       if (sort)
         buf[pos] = it;
       else
@@ -405,6 +424,14 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
       if (live && sub == 0) items[rank] = me;
     }
   }
+  if (p.splits) {
+    __syncthreads();  // the decodes' share and the longest unit are known
+    const int units = total * p.G, sms = max(p.num_sms - (p.dec_ctas ? dec_share : 0), 1);
+    const int rest = units % sms, n = pf_splits(units, sms, longest, p.max_parts);
+    if (tid == 0) *p.splits = make_int2(n, n > 1 ? units - rest : units);
+    if (n > 1)
+      for (int i = tid; i < rest * 2 * (kRows / 32); i += kSchedThreads) p.parts_done[i] = 0;
+  }
   if (tid == 0) {
     *count = total;
     *p.unit_head = 0;
@@ -423,7 +450,7 @@ struct PfUnit {
 // 8-bit cache: a unit may be one of `parts` parts of the pair's K/V tiles, [j0, j0 + n_kv).
 struct PfUnit8 : PfUnit {
   int j0;
-  int tag;  // 0: all of them, else (item, KV head) << 8 | parts << 4 | part
+  int tag;  // 0: all of them, else index among the split units << 8 | parts << 4 | part
 };
 
 // The unit's first K/V tile
@@ -445,21 +472,24 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag
   return it.n0 > 0;
 }
 
-// Unit u of whole * splits; the parts in order of their keys, so that every CTA counts the
-// same ones.  A part begins where every query row of the pair sees keys: its running
-// maximum is finite from its first tile on.
-__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole, int splits, bool flag, PfUnit8& it) {
-  const int part = u / whole;
-  u -= part * whole;
+// Unit u: `whole` units in one piece, then the parts of `rest` others.  A part begins where
+// every query row of the pair sees keys: its running maximum is finite from its first tile on.
+__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole, int rest, int splits, bool flag,
+                                        PfUnit8& it) {
+  int part = 0;
+  if (u >= whole) {
+    part = (u - whole) / rest;
+    u -= part * rest;
+  }
   it.j0 = it.tag = 0;
   if (!pf_unit(p, u, flag && part == 0, it)) return false;
-  if (splits > 1 && it.n_kv < kMinSplitTiles) return part == 0;
-  if (splits > 1) {
+  if (u >= whole && it.n_kv < kMinSplitTiles) return part == 0;
+  if (u >= whole) {
     const int len = max((it.n_kv + splits - 1) / splits, kMinPartTiles);
     const int last = (it.L - it.q_len + 2 * it.pair * p.Tq) / kKvTile;  // the latest first tile
     const int parts = min(splits, last / len + 1);
     if (part >= parts) return false;
-    if (parts > 1) it.tag = u << 8 | parts << 4 | part;
+    if (parts > 1) it.tag = (u - whole) << 8 | parts << 4 | part;
     it.j0 = part * len;
     const int end = part == parts - 1 ? it.n_kv : it.j0 + len;
     it.n0 = min(it.n0, end) - it.j0;
@@ -518,10 +548,10 @@ __device__ __forceinline__ float split_query_row(uint8_t* tile, int row) {
 
 // A part's result for row `row` of query tile w, for join_parts: normalised, rows side by side.
 template <int D>
-__device__ __forceinline__ void write_part(const PrefillParams& p, int tag, int whole, int w, int row,
+__device__ __forceinline__ void write_part(const PrefillParams& p, int tag, int rest, int w, int row,
                                            uint32_t o_tmem, float inv, float lse2, bool nan_any,
                                            const uint16_t* nan_first, int rel) {
-  const size_t tile = (size_t)((tag & 15) * whole + (tag >> 8)) * 2 + w;
+  const size_t tile = (size_t)((tag & 15) * rest + (tag >> 8)) * 2 + w;
   float4* out = reinterpret_cast<float4*>(p.part_out) + tile * (D / 4) * kRows + row;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
@@ -544,7 +574,7 @@ __device__ __forceinline__ void write_part(const PrefillParams& p, int tag, int 
 // The warp that finishes its 32 rows of a unit last merges their parts, in the order of the
 // keys: out = sum of o_i 2^(x_i - M) over sum of 2^(x_i - M).
 template <int D>
-__device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int whole, int w, int row, int lane,
+__device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int rest, int w, int row, int lane,
                                            __nv_bfloat16* orow, float* lse) {
   const int parts = (tag >> 4) & 15;
   __threadfence();  // the part is visible before it is counted
@@ -555,7 +585,7 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
   if (before != parts - 1) return;
   __threadfence();
   if (orow == nullptr) return;
-  const size_t tile = (size_t)(tag >> 8) * 2 + w, next = (size_t)whole * 2;
+  const size_t tile = (size_t)(tag >> 8) * 2 + w, next = (size_t)rest * 2;
   float x[kMaxSplits], M = -INFINITY, W = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxSplits; ++i) {
@@ -629,9 +659,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   __shared__ PfFp8Shared x8;       // (8-bit cache only)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int whole = __ldcg(p.item_count) * p.G;
-  const int splits = SPLIT ? __ldcg(p.splits) : 1;
-  const int units = whole * splits;
+  int units = __ldcg(p.item_count) * p.G;
+  [[maybe_unused]] int2 splits = make_int2(1, units);  // parts of each unit that is split, units that are not
+  [[maybe_unused]] const int rest = SPLIT ? units - (splits = __ldcg(p.splits)).y : 0;
+  if (SPLIT) units = splits.y + rest * splits.x;
   if ((int)blockIdx.x >= units) {
     if (p.wait_at_exit) pdl_wait();  // complete only after the decode grid in front of this one
     return;
@@ -1167,7 +1198,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if (u < units) {
         bool some;                                     // nothing to compute (length errors flagged here)
         if constexpr (SPLIT)
-          some = pf_unit(p, u, whole, splits, lane == 0, it);
+          some = pf_unit(p, u, splits.y, rest, splits.x, lane == 0, it);
         else
           some = pf_unit(p, u, lane == 0, it);
         if (!some) continue;
@@ -1370,11 +1401,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if constexpr (SPLIT) {
         const int tag = *reinterpret_cast<volatile int*>(&x8.tag[nan_slot]);
         if (tag) {
-          const int whole = __ldcg(p.item_count) * p.G;
-          write_part<D>(p, tag, whole, w, row, o_tmem, inv, m_run + log2f(l_run), x8.nan_any[nan_slot] != 0,
+          const int rest = __ldcg(p.item_count) * p.G - __ldcg(p.splits).y;
+          write_part<D>(p, tag, rest, w, row, o_tmem, inv, m_run + log2f(l_run), x8.nan_any[nan_slot] != 0,
                         x8.nan_first[nan_slot], p_row - (L - q_len + 2 * it.pair * p.Tq));
           tc_fence_before_sync();  // O_w may be overwritten
-          join_parts<D>(p, tag, whole, w, row, lane, row_valid ? orow : nullptr,
+          join_parts<D>(p, tag, rest, w, row, lane, row_valid ? orow : nullptr,
                         row_valid && p.lse_out ? p.lse_out + (size_t)(it.q0 + qi) * p.H + head : nullptr);
           continue;
         }
@@ -1440,15 +1471,20 @@ static size_t prefill_max_items(int num_seqs, int num_tokens, int Tq) {
   return (size_t)(num_tokens + 2 * Tq - 1) / (2 * Tq) + (size_t)num_seqs;
 }
 
-// 8-bit cache: memory for parts of units, behind the item list: counters, lse and rows of as
-// many units as SMs.  None where the chunks' pairs (one sequence's, if all are) fill more
-// than half of the SMs, or the sequences are short.
+// 8-bit cache: memory for parts of units, behind the item list: counters, lse and rows.
 static size_t prefill_split_offset(size_t max_items) { return align_up(256 + max_items * sizeof(int4), 256); }
 
-static size_t prefill_split_bytes(int num_tokens, int Tq, int G, int D, int cap, int sms) {
-  const long long pairs = std::max(1, num_tokens / (2 * Tq));
-  if (2 * pairs * G > sms || cap <= (kMinSplitTiles - 1) * kKvTile) return 0;
-  return align_up((size_t)sms * 2 * (kRows / 32) * sizeof(int), 256) + (size_t)sms * 2 * kRows * (1 + D) * sizeof(float);
+static size_t prefill_split_bytes(int parts, int D) {
+  return align_up((size_t)parts * 2 * (kRows / 32) * sizeof(int), 256) + (size_t)parts * 2 * kRows * (1 + D) * sizeof(float);
+}
+
+// ... for how many parts.  None where the chunks' units (all of one sequence, as far as the
+// host knows) fill two rounds of the SMs, would not be split, or the sequences are short.
+static int prefill_max_parts(int num_tokens, int Tq, int G, int cap, int sms) {
+  const long long units = (long long)std::max(1, num_tokens / (2 * Tq)) * G;
+  if (units >= 2 * sms) return 0;
+  const int parts = 2 * units <= sms ? sms : 4 * sms;
+  return pf_splits(units, sms, (cap - 1) / kKvTile + 1, parts) > 1 ? parts : 0;
 }
 
 // The schedule kernel, then `between(p)` (the decodes of a mixed batch, or
@@ -1469,11 +1505,11 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   }
   if (SPLIT) {
     char* at = reinterpret_cast<char*>(workspace) + prefill_split_offset(max_items);
-    p.splits = count + 4;
+    p.splits = reinterpret_cast<int2*>(count + 4);
     p.parts_done = reinterpret_cast<int*>(at);
-    at += align_up((size_t)sms * 2 * (kRows / 32) * sizeof(int), 256);
+    at += align_up((size_t)p.max_parts * 2 * (kRows / 32) * sizeof(int), 256);
     p.part_lse = reinterpret_cast<float*>(at);
-    at += (size_t)sms * 2 * kRows * sizeof(float);
+    at += (size_t)p.max_parts * 2 * kRows * sizeof(float);
     p.part_out = reinterpret_cast<float*>(at);
   }
   p.num_sms = sms;
@@ -1549,8 +1585,9 @@ extern "C" size_t metis_prefill_fp8_workspace_bytes(int num_seqs, int num_tokens
     return need;
   }
   const int Tq = kRows / (num_heads / num_kv_heads);
-  const size_t split = prefill_split_bytes(num_tokens, Tq, num_kv_heads, head_dim, max_seq_len, sms);
-  return split ? prefill_split_offset(prefill_max_items(num_seqs, num_tokens, Tq)) + split : need;
+  const int parts = prefill_max_parts(num_tokens, Tq, num_kv_heads, max_seq_len, sms);
+  if (!parts) return need;
+  return prefill_split_offset(prefill_max_items(num_seqs, num_tokens, Tq)) + prefill_split_bytes(parts, head_dim);
 }
 
 namespace metis {
@@ -1641,8 +1678,9 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   using Yes = std::true_type;
   using No = std::false_type;
   if (!fp8.k_cache) return head_dim == 128 ? launch(D128{}, No{}, No{}) : launch(D64{}, No{}, No{});
-  const size_t parts = prefill_split_bytes(num_tokens, p.Tq, num_kv_heads, head_dim, p.cap, sms);
-  if (parts > 0 && workspace_bytes >= prefill_split_offset(max_items) + parts)
+  p.max_parts = prefill_max_parts(num_tokens, p.Tq, num_kv_heads, p.cap, sms);
+  if (p.max_parts > 0 &&
+      workspace_bytes >= prefill_split_offset(max_items) + prefill_split_bytes(p.max_parts, head_dim))
     return head_dim == 128 ? launch(D128{}, Yes{}, Yes{}) : launch(D64{}, Yes{}, Yes{});
   return head_dim == 128 ? launch(D128{}, Yes{}, No{}) : launch(D64{}, Yes{}, No{});
 }

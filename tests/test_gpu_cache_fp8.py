@@ -640,6 +640,33 @@ def test_prefill_few_chunks_split_over_their_keys(r, G, D, bs):
         prefill_case(rng, spans, r, G, D, bs)
 
 
+@pytest.mark.parametrize("r,G,D,bs,spans", [
+    (8, 8, 64, 16, [(2900, 800)]),                            # 200 units: a round of whole ones, 48 in parts
+    (4, 8, 128, 32, [(3700, 640)]),                           # 80 units: parts in two rounds
+    (4, 8, 128, 16, [(2500, 900), (2300, 500), (90, 60), (700, 1), (40, 1)]),
+])
+def test_prefill_last_round_split_over_its_keys(r, G, D, bs, spans):
+    rng = np.random.default_rng(D + bs)
+    lens = [n for n, _ in spans]
+    c = Cache(rng, lens, G, D, bs)
+    cu = np.concatenate([[0], np.cumsum([q for _, q in spans])])
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), G * r, D))).to(BF16)
+    pa.metis_read_status(clear=True)
+    call = lambda: pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32(cu), *c.dev, c.bt, c.sl, D ** -0.5, want_lse=True)
+    out, lse = call()
+    rows = [(s, n - m + i + 1) for s, (n, m) in enumerate(spans) for i in range(m)]
+    at = np.sort(rng.choice(len(rows), 40, replace=False))
+    ref, tol, rl, lt = attention(c, q[torch.from_numpy(at)].double().numpy(), [rows[i] for i in at], D ** -0.5,
+                                 CHUNK_STEP, parts=True)
+    check(out[torch.from_numpy(at).to(DEV)], ref, tol, BF16, "out")
+    check_lse(lse[torch.from_numpy(at).to(DEV)], rl, lt)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    for _ in range(3):  # the parts land on other SMs: the same bits
+        again, lse2 = call()
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+    assert pa.metis_read_status() == 0
+
+
 def test_prefill_split_and_whole_agree_and_repeat():
     """The same call with and without the memory for parts, and twice with it."""
     rng = np.random.default_rng(31)
