@@ -880,6 +880,42 @@ def test_calls_on_another_stream_own_their_memory():
         assert all(torch.equal(o, ref) and torch.equal(k, kref) for o, k in outs)
 
 
+def test_two_streams_at_once():
+    """Split prefill, joined and merged decode and the write on two streams, each with its own tensors:
+    the bits of the same calls one after another."""
+    rng = np.random.default_rng(50)
+    cases = []
+    for lens, q_lens in (([2600, 300, 70], [200, 1, 70]), ([1900, 2300, 5], [64, 130, 1])):
+        c = Cache(rng, lens, 2, 128, 16)
+        T = sum(q_lens)
+        q = gpu(torch.from_numpy(rng.standard_normal((T, 8, 128))).to(BF16))
+        kv = [gpu(torch.from_numpy(rng.standard_normal((T, 2, 128))).to(BF16)) for _ in range(2)]
+        cases.append((c, q, kv, i32(np.concatenate([[0], np.cumsum(q_lens)]))))
+
+    def steps(c, q, kv, cu, dev, stream):
+        pa.metis_reshape_and_cache_fp8(*kv, *dev, cu, c.bt, c.sl, stream=stream)
+        outs = [pa.metis_paged_attn_prefill_chunk_fp8(q, cu, *dev, c.bt, c.sl, 0.09, max_seq_len=2600, stream=stream)[0]]
+        for partition in (0, 64, 512):
+            outs.append(pa.metis_paged_attn_decode_fp8(q[:3], *dev, c.bt, c.sl, 0.09, partition_size=partition,
+                                                       max_seq_len=2600, stream=stream)[0])
+        return outs
+
+    alone = []
+    for case in cases:
+        dev = [x.clone() for x in case[0].dev]
+        alone.append((steps(*case, dev, None), dev))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        dev = [[x.clone() for x in case[0].dev] for case in cases]
+        torch.cuda.synchronize()
+        outs = [steps(*case, d, st) for case, d, st in zip(cases, dev, streams)]
+        torch.cuda.synchronize()
+        for got, d, (ref, ref_dev) in zip(outs, dev, alone):
+            assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, ref))
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(d, ref_dev))
+
+
 def test_offsets_past_32_bits():
     """Pages at the end of pools of more than 2^32 bytes."""
     bs, G, D, r = 64, 8, 128, 4
