@@ -410,6 +410,8 @@ int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, const uint8
  * out, METIS_BF16 or METIS_F32.  num_heads / num_kv_heads may be any ratio up to 8.
  * Products are fp16 tensor-core products of exact codes with fp32 accumulation; the
  * softmax weights carry fp16's 11 bits (bf16 q), or 22 bits as q does (fp32 q).
+ * Sequences that would leave SMs idle are split further and joined in the same launch
+ * (also with partition_size 0, and without scratch).
  */
 int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
                                 const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,

@@ -710,7 +710,9 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 //                  merge (but 16 sequences 41.7 us, 37.7 with it: a cluster's CTAs hold their
 //                  slots until the last one is done).  No merge, no workspace: an unsplit call
 //                  whose items leave SMs idle is split the same way, one sequence of 16,384
-//                  tokens 15.7 us (one CTA per item 73.9), eight of 512..4,096 15.8 us (23.8).
+//                  tokens 15.7 us (one CTA per item 73.9), eight of 512..4,096 16.5 us (23.8);
+//                  by its own length: with a bound of 128 K on 2,048 tokens 7.5 us, in parts of
+//                  the bound 14.8.
 //                  Partitions of 1,024 tokens and more: 8 warps, 4,096-token ones 24.2 us, 4
 //                  warps 32.3 us; not for clusters of more than four over more than half the
 //                  SMs, which do not all fit at a time (2 x 4,096: 16.2 us for 10.4)
@@ -808,14 +810,17 @@ __global__ void __launch_bounds__(Plan::NW * 32, Plan::MIN_CTAS) decode_fp8_kern
     float* jo = reinterpret_cast<float*>(smem + NW * (64 + D * 32));
     float* jl = jo + 8 * D;
     static_assert(NW * (64 + D * 32) + 8 * D * 4 + 32 <= NW * STAGES * STAGE_BYTES, "the partial must fit in the ring");
-    const int g = blockIdx.x, part = blockIdx.y, s = blockIdx.z, P = p.partition_size;
+    const int g = blockIdx.x, part = blockIdx.y, s = blockIdx.z;
     int L = p.seq_lens[s];
     if (L > p.cap) {
       if (threadIdx.x == 0 && part == 0) atomicOr(&g_status_decode_fp8, METIS_STATUS_SEQ_TOO_LONG);
       L = p.cap;
     }
     L = max(L, 0);
-    const int n = L / P + (L % P != 0);  // partitions with tokens
+    int P = p.partition_size;
+    if (P == 0)  // an unsplit call: the sequence, not its bound, in equal parts of whole units
+      P = max(kMinJoinTokens, (int)(((unsigned)L + kUnit8 * p.max_parts - 1) / (kUnit8 * p.max_parts) * kUnit8));
+    const int n = L / P + (L % P != 0);  // partitions with tokens, at most max_parts
     __syncthreads();                     // the barriers are initialised
     if (part < n)
       decode_fp8_item<D, NW, STAGES, QT>(
@@ -1002,6 +1007,7 @@ static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void
                       bool* joined) {
   DecodeFp8Params split = pp;
   DecodeParams& p = split.d;
+  int tokens = p.partition_size;  // of a partition, at most
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1009,15 +1015,14 @@ static int launch_fp8(const DecodeFp8Params& pp, const void* k_cache, const void
   const long long items = (long long)p.G * p.S;
   if (p.partition_size == 0) {
     if (items > sms) return launch_fp8<D, QT, Fp8Unsplit<D>>(pp, k_cache, v_cache, st);
-    // SMs to spare: partitions all the same (no workspace: they are joined), of whole units
-    const int parts = (int)std::min<long long>({kMaxJoin, sms / items, p.cap / kMinJoinTokens});
-    if (parts < 2) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
-    p.partition_size = (int)((((long long)p.cap + parts - 1) / parts + kUnit8 - 1) / kUnit8 * kUnit8);
-    p.max_parts = (int)(((long long)p.cap + p.partition_size - 1) / p.partition_size);
+    // SMs to spare: partitions all the same (no workspace: they are joined)
+    p.max_parts = (int)std::min<long long>({kMaxJoin, sms / items, p.cap / kMinJoinTokens});
+    if (p.max_parts < 2) return launch_fp8<D, QT, Fp8FewItems<D>>(pp, k_cache, v_cache, st);
+    tokens = p.cap / p.max_parts;
   }
   const long long ctas = p.max_parts * items;
   *joined = p.max_parts <= kMaxJoin && ctas <= sms;
-  if (*joined && p.partition_size >= 1024 && (2 * ctas <= sms || p.max_parts <= kMaxJoin / 2))
+  if (*joined && tokens >= 1024 && (2 * ctas <= sms || p.max_parts <= kMaxJoin / 2))
     return launch_fp8<D, QT, Fp8JoinLong, true>(split, k_cache, v_cache, st);
   if (*joined) return launch_fp8<D, QT, Fp8FewParts, true>(split, k_cache, v_cache, st);
   // one warp per partition: where twelve on each SM are filled twice over, and for short ones as
