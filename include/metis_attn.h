@@ -409,7 +409,9 @@ int metis_gather_cache_fp8(const void* k_cache, const void* v_cache, const uint8
  * (metis_decode_workspace_bytes) are those of that call; dtype is the type of q and
  * out, METIS_BF16 or METIS_F32.  num_heads / num_kv_heads may be any ratio up to 8.
  * Products are fp16 tensor-core products of exact codes with fp32 accumulation; the
- * softmax weights carry fp16's 11 bits (bf16 q), or 22 bits as q does (fp32 q).
+ * softmax weights carry fp16's 11 bits (bf16 q), or 22 bits as q does (fp32 q); a weight
+ * below 2^-27 (bf16 q) or 2^-50 (fp32 q) of its row's largest may be lost, whatever the
+ * scales of the pages (as long as V's are within 2^80 of one another).
  * Sequences that would leave SMs idle are split further and joined in the same launch
  * (also with partition_size 0, and without scratch).
  */

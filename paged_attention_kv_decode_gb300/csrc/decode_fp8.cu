@@ -21,11 +21,15 @@
 //     m16 tile of output rows is 8 even dims followed by 8 odd ones.
 //   * The query row is scaled by a power of two into fp16's range (its largest element in
 //     [2^14, 2^15)): exact for bf16 elements down to 2^-29 of the largest, and below that
-//     off by at most 2^-40 of it.  fp32 queries are split into two fp16 parts (22 bits).
+//     off by at most 2^-39 of it.  fp32 queries are split into two fp16 parts (22 bits).
 //   * bf16 queries: a token's weight takes V's page scale along, 2^(z + vb - M), so that P V
 //     accumulates straight into O; its reference M, the running maximum of z + vb minus 14,
-//     leaves fp16 the range down to 2^-38 of the largest.  The sum of weights has a reference
-//     of its own, m, of z alone: any spread of scales between pages is held.
+//     leaves fp16 the range down to 2^-38 of the largest.  M follows the pages' scales, not the
+//     values that the weights meet: a page 2^kWide below the largest one so far would lose
+//     weights that count in columns where the large page holds zeros.  Its weights are of z
+//     alone, each tile against its own maximum, and its products join O in fp32 with the page's
+//     factor.  So a weight is off by at most 2^-11 of itself or 2^-27 of the largest one.  The
+//     sum of weights has a reference of its own, m, of z alone.
 //   * fp32 queries: weights are two fp16 parts too, and each tile's P V lands in a fresh
 //     accumulator that joins O with the page's factor.
 #include <math.h>
@@ -54,6 +58,7 @@ constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
 constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
 constexpr int kMaxJoin = 8;          // partitions of an item that a cluster takes
 constexpr int kMinJoinTokens = 128;  // ... in a call that asked for none: tokens in each at least
+constexpr int kWide = 12;        // bf16 queries: a V scale this far (log2) below the largest so far stays out of the weights
 constexpr float kSlack = 16.f;   // bf16 queries: the sums' reference moves when it is exceeded by 2^16
 
 template <int D>
@@ -321,10 +326,10 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
   // ldmatrix rows and chunks: matrices 0, 1 = token rows 0..7, 8..15 of a chunk, 2, 3 of the next
   const int lrow = (lane & 8) + (lane & 7), lchunk = lane >> 4;
 
-  // One unit.  ODD: tiles that are partly outside the range, or pages whose V scale is 2^32
-  // below the largest so far (against a reference with that one's exponent their weights
-  // may be below fp32's range: their sum is taken from the scores); everything else runs
-  // without a branch but the one of moving references.
+  // One unit.  ODD: tiles that are partly outside the range, or pages whose V scale is more
+  // than 2^kWide below the largest so far: weights of the scores alone, each tile's against its
+  // own maximum, and fresh accumulators that join O with the page's factor.  Everything else
+  // runs without a branch but the one of moving references.
   auto consume = [&](auto odd_unit, int tok0, uint32_t sc) {
     constexpr bool ODD = decltype(odd_unit)::value;
     const uint32_t kbase = units.tile();
@@ -350,25 +355,31 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
         unpack_e4m3x4(r3, a1, a3);
         mma_f16_16816(x2[h], a0, a1, a2, a3, qf[kk + 1][0], qf[kk + 1][1]);
       }
-    // V's pieces, on their way during the softmax
+    // V's pieces, on their way during the softmax (ODD: loaded where they are used, to hold fewer registers)
     uint32_t v[KS / 2][2][4];
+    auto load_v = [&](int c, int h) {
+      ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, 2 * c + lchunk), v[c][h][0], v[c][h][1], v[c][h][2],
+                    v[c][h][3]);
+    };
+    if (!ODD) {
 #pragma unroll
-    for (int c = 0; c < KS / 2; ++c)
+      for (int c = 0; c < KS / 2; ++c)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, 2 * c + lchunk), v[c][h][0], v[c][h][1], v[c][h][2],
-                      v[c][h][3]);
+        for (int h = 0; h < 2; ++h) load_v(c, h);
+    }
 
-    // y = z + vb in log2 units (z: the scaled score); the thread holds tokens rA, rA + 8 of
-    // each tile, heads 2 q4, 2 q4 + 1
+    // y = z + vb in log2 units (z: the scaled score; ODD: z itself); the thread holds tokens
+    // rA, rA + 8 of each tile, heads 2 q4, 2 q4 + 1
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float ks = scale_of_byte((h ? sc >> 16 : sc) & 255u), a = f0 * ks, b = f1 * ks;
-      x[h][0] = fmaf(x[h][0] + x2[h][0], a, vb[h]);
-      x[h][1] = fmaf(x[h][1] + x2[h][1], b, vb[h]);
-      x[h][2] = fmaf(x[h][2] + x2[h][2], a, vb[h]);
-      x[h][3] = fmaf(x[h][3] + x2[h][3], b, vb[h]);
+      const float e = ODD ? 0.f : vb[h];
+      x[h][0] = fmaf(x[h][0] + x2[h][0], a, e);
+      x[h][1] = fmaf(x[h][1] + x2[h][1], b, e);
+      x[h][2] = fmaf(x[h][2] + x2[h][2], a, e);
+      x[h][3] = fmaf(x[h][3] + x2[h][3], b, e);
     }
+    [[maybe_unused]] uint32_t v_lo[2], v_hi[2], v_nan[2];  // ODD: which of V's codes count
     if (ODD) {
       // valid tokens of the two tiles (the first tile of a range may start before it)
       const int t = 2 * q4;
@@ -379,28 +390,29 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
         if (rA + 8 >= nv) x[h][2] = x[h][3] = -INFINITY;
         // Rows past the range may hold anything (NaN codes included): zero them in the V^T
         // fragments so that 0 * NaN cannot poison O.
-        const uint32_t lo = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
-        const uint32_t hi = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
+        v_lo[h] = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
+        v_hi[h] = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
         // a scale of NaN: so is every code
-        const uint32_t nan = ((h ? sc >> 24 : sc >> 8) & 255u) == 255u ? 0x7f7f7f7fu : 0u;
-#pragma unroll
-        for (int c = 0; c < KS / 2; ++c) {
-          v[c][h][0] = (v[c][h][0] | nan) & lo;
-          v[c][h][1] = (v[c][h][1] | nan) & hi;
-          v[c][h][2] = (v[c][h][2] | nan) & lo;
-          v[c][h][3] = (v[c][h][3] | nan) & hi;
-        }
+        v_nan[h] = ((h ? sc >> 24 : sc >> 8) & 255u) == 255u ? 0x7f7f7f7fu : 0u;
       }
     }
-    const float y0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), 4);
-    const float y1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), 4);
-    // the sums' reference: at least the unit's largest z, above it by at most the exponents'
-    // spread (ODD: from the scores themselves)
-    float z0, z1;
+    // y: the unit's largest z + vb; z: the sums' reference, at least the unit's largest z and
+    // above it by at most the exponents' spread (ODD: that z itself, from the tiles' own, zt)
+    float y0, y1, z0, z1;
+    [[maybe_unused]] float zt0[2], zt1[2];
     if (ODD) {
-      z0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]) - vb[0], fmaxf(x[1][0], x[1][2]) - vb[1]), 4);
-      z1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]) - vb[0], fmaxf(x[1][1], x[1][3]) - vb[1]), 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        zt0[h] = warp_max_xor(fmaxf(x[h][0], x[h][2]), 4);
+        zt1[h] = warp_max_xor(fmaxf(x[h][1], x[h][3]), 4);
+      }
+      y0 = fmaxf(zt0[0] + vb[0], zt0[1] + vb[1]);
+      y1 = fmaxf(zt1[0] + vb[0], zt1[1] + vb[1]);
+      z0 = fmaxf(zt0[0], zt0[1]);
+      z1 = fmaxf(zt1[0], zt1[1]);
     } else {
+      y0 = warp_max_xor(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), 4);
+      y1 = warp_max_xor(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), 4);
       const float vb_min = fminf(vb[0], vb[1]);
       z0 = y0 - vb_min;
       z1 = y1 - vb_min;
@@ -427,16 +439,22 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
     }
     // P^T (tokens x heads) -> B operand (k = token, n = head) by 8x8 transposes
     uint32_t pb[2][2];
+    [[maybe_unused]] float f0t[2], f1t[2];  // ODD: what brings a tile's products to O's reference
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float e0 = exp2_approx(x[h][0] - M0), e1 = exp2_approx(x[h][1] - M1);
-      const float e2 = exp2_approx(x[h][2] - M0), e3 = exp2_approx(x[h][3] - M1);
+      // (a tile without a score, or with NaN alone: any finite reference)
+      const bool none0 = ODD && zt0[h] == -INFINITY, none1 = ODD && zt1[h] == -INFINITY;
+      const float r0 = !ODD ? M0 : none0 ? 0.f : zt0[h] - kRefDown, r1 = !ODD ? M1 : none1 ? 0.f : zt1[h] - kRefDown;
+      const float e0 = exp2_approx(x[h][0] - r0), e1 = exp2_approx(x[h][1] - r1);
+      const float e2 = exp2_approx(x[h][2] - r0), e3 = exp2_approx(x[h][3] - r1);
       pb[h][0] = movmatrix_trans(pack_f16x2(e0, e1));
       pb[h][1] = movmatrix_trans(pack_f16x2(e2, e3));
       // sums of 2^(z - m): the weights without V's exponent
       if (ODD) {
-        l0 += exp2_approx(x[h][0] - vb[h] - m0) + exp2_approx(x[h][2] - vb[h] - m0);
-        l1 += exp2_approx(x[h][1] - vb[h] - m1) + exp2_approx(x[h][3] - vb[h] - m1);
+        f0t[h] = none0 ? 1.f : exp2_approx(r0 + vb[h] - M0);  // at most 2
+        f1t[h] = none1 ? 1.f : exp2_approx(r1 + vb[h] - M1);
+        l0 = fmaf(e0 + e2, none0 ? 1.f : exp2_approx(r0 - m0), l0);
+        l1 = fmaf(e1 + e3, none1 ? 1.f : exp2_approx(r1 - m1), l1);
       } else {
         l0 = fmaf(e0 + e2, exp2_approx(M0 - vb[h] - m0), l0);
         l1 = fmaf(e1 + e3, exp2_approx(M1 - vb[h] - m1), l1);
@@ -446,14 +464,30 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
 #pragma unroll
     for (int c = 0; c < KS / 2; ++c)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (ODD) {
+          load_v(c, h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[c][h][i] = (v[c][h][i] | v_nan[h]) & (i & 1 ? v_hi[h] : v_lo[h]);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t a0, a1, a2, a3;
           unpack_e4m3x4(__byte_perm(v[c][h][2 * u], 0, 0x3120), a0, a1);      // even, odd dims of tokens 0..7
           unpack_e4m3x4(__byte_perm(v[c][h][2 * u + 1], 0, 0x3120), a2, a3);  // ... of tokens 8..15
-          mma_f16_16816(o[2 * c + u], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          if (ODD) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16_16816(t, a0, a1, a2, a3, pb[h][0], pb[h][1]);
+            float* const acc = o[2 * c + u];
+            acc[0] = fmaf(t[0], f0t[h], acc[0]);
+            acc[1] = fmaf(t[1], f1t[h], acc[1]);
+            acc[2] = fmaf(t[2], f0t[h], acc[2]);
+            acc[3] = fmaf(t[3], f1t[h], acc[3]);
+          } else {
+            mma_f16_16816(o[2 * c + u], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          }
         }
+      }
   };
 
   int k = 0;
@@ -468,7 +502,7 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
     }
     const int vb0 = (sc >> 8) & 255u, vb1 = sc >> 24;
     v_top = max(v_top, max(vb0, vb1));
-    if (tok0 < t0 || tok0 + kUnit8 > t1 || v_top - min(vb0, vb1) > 32 || v_top == 255)
+    if (tok0 < t0 || tok0 + kUnit8 > t1 || v_top - min(vb0, vb1) > kWide || v_top == 255)
       consume(std::true_type{}, tok0, sc);
     else
       consume(std::false_type{}, tok0, sc);

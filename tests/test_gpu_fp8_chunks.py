@@ -1,0 +1,70 @@
+"""Chunked prefill over the 8-bit cache: softmax scales of either sign and zero, query rows of any
+size, and the split over keys held to each row's own bound."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_attention_kv_decode_gb300 as pa
+from test_gpu_cache_fp8 import BF16, CHUNK_STEP, DEV, Cache, attention, check, check_lse, gpu, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def run(c, q, q_lens, scale, **kw):
+    cu = i32(np.concatenate([[0], np.cumsum(q_lens)]))
+    return pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), cu, *c.dev, c.bt, c.sl, scale, want_lse=True, **kw)
+
+
+def rows_of(lens, q_lens):
+    return [(s, n - m + i + 1) for s, (n, m) in enumerate(zip(lens, q_lens)) for i in range(m)]
+
+
+@pytest.mark.parametrize("r,D,bs", [(4, 128, 16), (8, 64, 64), (16, 128, 32)])
+@pytest.mark.parametrize("scale", [0.0, -0.05, -0.3, 0.7])
+def test_chunk_softmax_scales(scale, r, D, bs):
+    """Masked, whole and split tiles; a prefix long enough to be split over its keys."""
+    rng = np.random.default_rng(r + D)
+    lens, q_lens = [200, 70, 2100, 33], [150, 70, 40, 5]
+    c = Cache(rng, lens, 1, D, bs, spread=0.5)
+    q = torch.from_numpy(rng.standard_normal((sum(q_lens), r, D))).to(BF16)
+    out, lse = run(c, q, q_lens, scale)
+    ref, tol, rl, lt = attention(c, q.double().numpy(), rows_of(lens, q_lens), scale, CHUNK_STEP, parts=True)
+    check(out, ref, tol, BF16, "out")
+    check_lse(lse, rl, lt)
+
+
+@pytest.mark.parametrize("size,scale", [(1e30, 1e-31), (1e-30, 1e29), (0.0, 1.0), (1.0, 0.01), (1e30, 0.0), (1e30, -1e-31)])
+def test_chunk_query_rows_of_any_size(size, scale):
+    """The power of two that brings a row into e4m3's range is undone; a scale of zero weighs every
+    visible token alike, whatever the scores."""
+    rng = np.random.default_rng(6)
+    lens, q_lens = [180, 40], [130, 40]
+    c = Cache(rng, lens, 2, 128, 16, spread=0.0)
+    q = rng.standard_normal((170, 8, 128)) * size
+    q[100, 2, 5] = 4096.0 * size  # one large element beside small ones
+    q[7] = 0.0
+    q = torch.from_numpy(q).to(BF16)
+    out, lse = run(c, q, q_lens, scale)
+    ref, tol, rl, lt = attention(c, q.double().numpy(), rows_of(lens, q_lens), scale, CHUNK_STEP, parts=True)
+    check(out, ref, tol, BF16, "out")
+    check_lse(lse, rl, lt)
+
+
+def test_chunk_split_and_whole_within_each_rows_own_bound():
+    """The same call with and without the memory for parts, every element against its own bound."""
+    rng = np.random.default_rng(31)
+    lens, q_lens = [2900, 64, 1500], [100, 1, 300]
+    c = Cache(rng, lens, 2, 128, 16)
+    q = torch.from_numpy(rng.standard_normal((401, 8, 128))).to(BF16)
+    at = np.sort(np.concatenate([rng.choice(401, 40, replace=False), [100]]))
+    rows = rows_of(lens, q_lens)
+    ref, tol, rl, lt = attention(c, q[torch.from_numpy(at)].double().numpy(), [rows[i] for i in at], 0.088, CHUNK_STEP,
+                                 parts=True)
+    dev_at = torch.from_numpy(at).to(DEV)
+    for n in (pa.metis_prefill_workspace_bytes(3, 401, 8, 2),
+              pa.metis_prefill_fp8_workspace_bytes(3, 401, 8, 2, 128, 2900)):
+        out, lse = run(c, q, q_lens, 0.088, max_seq_len=2900,
+                       workspace=torch.full((n,), 0xAB, dtype=torch.uint8, device=DEV))
+        check(out[dev_at], ref, tol, BF16, "out")
+        check_lse(lse[dev_at], rl, lt)
