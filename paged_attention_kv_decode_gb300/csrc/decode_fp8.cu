@@ -56,6 +56,7 @@ struct DecodeFp8Params {
 
 constexpr int kUnit8 = 32;       // tokens per pipeline unit (two m16 tiles)
 constexpr float kRefDown = 14.f; // softmax reference below the running maximum, log2 units
+constexpr float kUndoRefDown = 1.f / 16384.f;  // 2^-kRefDown
 constexpr int kMaxJoin = 8;          // partitions of an item that a cluster takes
 constexpr int kMinJoinTokens = 128;  // ... in a call that asked for none: tokens in each at least
 constexpr int kWide = 12;        // bf16 queries: a V scale this far (log2) below the largest so far stays out of the weights
@@ -237,12 +238,22 @@ struct Fp8Units {
   }
 };
 
+// A sum l relative to 2^m (m = -infinity: of nothing) brought into [1, 2)
+__device__ __forceinline__ void normalise_sum(float& l, float& m) {
+  const int field = (int)((__float_as_uint(l) >> 23) & 255u);
+  if (field == 0 || field == 255) return;  // zero or NaN
+  l *= __uint_as_float((uint32_t)(254 - field) << 23);
+  m += (float)(field - 127);
+}
+
 // The warps' softmax states meet in the ring's memory (every warp is done with it after the
 // first sync) and become the item's result through store(cm, cl, co) (combine_and_store's
-// arguments).  o[c]: dims d0(c), d1(c) of the lane for heads 2 q4, 2 q4 + 1, unnormalised
-// relative to 2^m0, 2^m1.
-template <int D, int NW, typename Sync, typename Store, typename Dims>
-__device__ __forceinline__ void combine_fp8(uint8_t* smem, const uint64_t (*o)[2], float m0, float m1, float l0,
+// arguments).  o(c, i): dim dims(c, i) of the lane for heads 2 q4, 2 q4 + 1, unnormalised
+// relative to 2^R0, 2^R1; the sums l0, l1 to 2^m0, 2^m1.  A state leaves with its sum in
+// [1, 2) and o against the same power of two, so that no o is larger than the largest |v|
+// by more than a factor of two: values up to 2^124 pass the sums over warps.
+template <int D, int NW, typename O, typename Sync, typename Store, typename Dims>
+__device__ __forceinline__ void combine_fp8(uint8_t* smem, O o, float R0, float R1, float m0, float m1, float l0,
                                             float l1, int warp, int lane, Sync sync, Store store, Dims dims) {
   constexpr int KS = Fp8DecodeShape<D>::kSteps;
   l0 = warp_sum_xor(l0, 4);
@@ -251,6 +262,13 @@ __device__ __forceinline__ void combine_fp8(uint8_t* smem, const uint64_t (*o)[2
   // holds): any finite one makes the state count
   if (l0 != l0) m0 = 0.f;
   if (l1 != l1) m1 = 0.f;
+  normalise_sum(l0, m0);
+  normalise_sum(l1, m1);
+  // 2^(R - m) in two factors: R follows V's scale, and the power itself may be out of range
+  const float d0 = m0 == -INFINITY ? 0.f : R0 - m0, d1 = m1 == -INFINITY ? 0.f : R1 - m1;
+  const float h0 = fminf(fmaxf(d0, -100.f), 100.f), h1 = fminf(fmaxf(d1, -100.f), 100.f);
+  const uint64_t near = f2_pack(exp2_approx(h0), exp2_approx(h1));
+  const uint64_t far = f2_pack(exp2_approx(d0 - h0), exp2_approx(d1 - h1));
   sync();  // every warp is done with its ring
   float* cm = reinterpret_cast<float*>(smem);
   float* cl = cm + NW * 8;
@@ -265,7 +283,8 @@ __device__ __forceinline__ void combine_fp8(uint8_t* smem, const uint64_t (*o)[2
   for (int c = 0; c < KS; ++c)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint64_t*>(co + ((size_t)warp * D + dims(c, i)) * 8 + 2 * (lane & 3)) = o[c][i];
+      *reinterpret_cast<uint64_t*>(co + ((size_t)warp * D + dims(c, i)) * 8 + 2 * (lane & 3)) =
+          f2_mul(f2_mul(o(c, i), near), far);
   sync();
   store(cm, cl, co);
 }
@@ -510,16 +529,8 @@ __device__ __forceinline__ bool decode_fp8_item_bf16(const CUtensorMap& tmK, con
   }
   if (!ok) units.drain(k);
 
-  // O relative to the sums' references (a warp without units: nothing)
-  const float b0 = m0 == -INFINITY ? 0.f : exp2_approx(M0 - m0), b1 = m1 == -INFINITY ? 0.f : exp2_approx(M1 - m1);
-  uint64_t o2[KS][2];
-#pragma unroll
-  for (int c = 0; c < KS; ++c) {
-    o2[c][0] = f2_pack(o[c][0] * b0, o[c][1] * b1);
-    o2[c][1] = f2_pack(o[c][2] * b0, o[c][3] * b1);
-  }
-  combine_fp8<D, NW>(smem, o2, m0, m1, l0, l1, warp, lane, sync, store,
-                     [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  combine_fp8<D, NW>(smem, [&](int c, int i) { return f2_pack(o[c][2 * i], o[c][2 * i + 1]); }, M0, M1, m0, m1, l0, l1,
+                     warp, lane, sync, store, [rA](int c, int i) { return c * 16 + 2 * rA + i; });
   kb += units.n_my;
   return ok;
 }
@@ -690,7 +701,8 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
       for (int h = 0; h < 2; ++h) {
         uint32_t r[4];
         ldsm_x4_trans(vbase + tile_chunk<D>(16 * h + lrow, c + lchunk), r[0], r[1], r[2], r[3]);
-        const float vf = scale_of_byte((h ? sc >> 24 : sc >> 8) & 255u);
+        // 2^vb without the weights' 2^kRefDown: O stays within fp32's range wherever a value does
+        const float vf = scale_of_byte((h ? sc >> 24 : sc >> 8) & 255u) * kUndoRefDown;
         const uint64_t vf2 = f2_pack(vf, vf);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -716,8 +728,8 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
     units.release(k);
   }
   if (!ok) units.drain(k);
-  combine_fp8<D, NW>(smem, o, m0, m1, l0, l1, warp, lane, sync, store,
-                     [rA](int c, int i) { return c * 16 + 2 * rA + i; });
+  combine_fp8<D, NW>(smem, [&](int c, int i) { return o[c][i]; }, m0 + kRefDown, m1 + kRefDown, m0, m1, l0, l1, warp,
+                     lane, sync, store, [rA](int c, int i) { return c * 16 + 2 * rA + i; });
   kb += units.n_my;
   return ok;
 }

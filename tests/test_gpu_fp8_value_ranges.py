@@ -131,3 +131,28 @@ def test_small_pages_beside_a_large_one_in_a_mixed_batch(gap, where):
         ref, tol, rl, lt = exact(c, q[at].double().numpy(), rows, D ** -0.5, BF16 if m == 1 else "chunk")
         check(out[at], ref, tol, BF16, f"sequence {s}")
         check_lse(lse[at], rl, lt)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [2.0 ** 119, 2.0 ** 100, 2.0 ** -100, 2.0 ** -113])
+def test_decode_values_near_the_ends_of_the_range(size, dtype):
+    """V of one size throughout: no sum on the way overflows, and no factor is flushed to zero
+    (results of 2^-113 are still normal numbers of both types)."""
+    rng = np.random.default_rng(3)
+    lens, D = [100, 300, 1], 128
+    c = Cache(rng, lens, 1, D, 16, spread=0.0, poisoned=False)
+    c.v, c.vs = oracle.quantize_pages(rng.standard_normal((c.nb, 16, 1, D)) * size)
+    c.put()
+    q = torch.from_numpy(rng.standard_normal((3, 4, D))).to(dtype)
+    ref, tol, rl, lt = exact(c, q.double().numpy(), list(enumerate(lens)), 0.1, dtype)
+    for partition in (0, 16, 64):
+        out, lse = pa.metis_paged_attn_decode_fp8(gpu(q), *c.dev, c.bt, c.sl, 0.1, partition_size=partition,
+                                                  want_lse=True)
+        check(out, ref, tol, dtype, f"out, partitions of {partition}")
+        check_lse(lse, rl, lt)
+        # (an output of nothing but zeros would pass the comparison's absolute part at 2^-113)
+        assert np.abs(out.double().cpu().numpy()).max() >= 0.5 * np.abs(ref).max()
+    if dtype == BF16:  # single-token rows of a chunked call
+        out, lse = pa.metis_paged_attn_prefill_chunk_fp8(gpu(q), i32([0, 1, 2, 3]), *c.dev, c.bt, c.sl, 0.1, want_lse=True)
+        check(out, ref, tol, dtype, "single-token rows")
+        assert np.abs(out.double().cpu().numpy()).max() >= 0.5 * np.abs(ref).max()
