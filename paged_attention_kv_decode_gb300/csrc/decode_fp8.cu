@@ -972,6 +972,7 @@ __global__ void __launch_bounds__(kDec8Groups * kFp8Warps * 32, 1)
   auto gsync = [grp] { named_barrier_sync(1 + grp, GT); };
   int kb = 0;  // this warp's ring position, across the group's items
   for (;;) {
+    fence_proxy_async_smem();  // the combine's stores into the ring come before the next item's loads of the same bytes
     gsync();  // the previous item's combine is done with the ring, and the slot was read
     if (gave_up[grp]) break;  // read after the barrier: the whole group leaves together
     if (tid == 0) item_slot[grp] = atomicAdd(next_item, 1);

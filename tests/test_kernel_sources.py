@@ -1,0 +1,23 @@
+"""Rules of ordering that no run shows reliably, held to the kernels' sources."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_attention_kv_decode_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())  # without comments
+
+
+@pytest.mark.parametrize("name,kernel", [("decode.cu", "decode_rows_beside_kernel"),
+                                         ("decode_fp8.cu", "decode_fp8_rows_beside_kernel")])
+def test_persistent_decodes_fence_the_ring_between_items(name, kernel):
+    """The combine step's ordinary stores and the next item's TMA loads write the same shared memory:
+    every thread orders its stores before accesses of the async proxy, in front of the barrier."""
+    body = re.search(r"\n\s+" + kernel + r"\(.*?\n}\n", source(name), re.S).group(0)
+    loop = body[body.index("for (;;)"):]
+    assert "combine_and_store" in loop or "decode_bf16_item" in loop
+    assert loop.index("fence_proxy_async_smem();") < loop.index("gsync();")
