@@ -62,8 +62,8 @@ __device__ __forceinline__ ItemSeq seq_of_item(const WriteFp8Params& p, int i, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = k * 32 + lane;
-      cu[k] = at <= n ? __ldg(p.cu_q_lens + at) : 0;
-      len[k] = at < n ? __ldg(p.seq_lens + at) : 0;
+      cu[k] = at <= n ? p.cu_q_lens[at] : 0;
+      len[k] = at < n ? p.seq_lens[at] : 0;
     }
     int c = 0;
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ ItemSeq seq_of_item(const WriteFp8Params& p, int i, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = (k * 32 + lane) * step;
-      cu[k] = at < n ? __ldg(p.cu_q_lens + lo + at) : 0;
+      cu[k] = at < n ? p.cu_q_lens[lo + at] : 0;
     }
     int c = 0;
 #pragma unroll
@@ -96,9 +96,9 @@ __device__ __forceinline__ ItemSeq seq_of_item(const WriteFp8Params& p, int i, i
     n = min(step, n - (c - 1) * step);
   }
   it.s = lo;
-  it.r0 = __ldg(p.cu_q_lens + lo);
-  it.r1 = __ldg(p.cu_q_lens + lo + 1);
-  it.L = __ldg(p.seq_lens + lo);
+  it.r0 = p.cu_q_lens[lo];
+  it.r1 = p.cu_q_lens[lo + 1];
+  it.L = p.seq_lens[lo];
   return it;
 }
 

@@ -44,7 +44,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // Programmatic dependent launch.  pdl_launch_dependents(): the next kernel in
 // the stream may start launching once every CTA of this grid has executed it
 // (or exited).  pdl_wait(): block until the previous grid in the stream has
-// completed and its memory is visible (a no-op without such a dependency).
+// completed and its memory is visible (a no-op without such a dependency).  What that
+// grid may have written -- caches, index arrays, partials -- is read with ordinary loads
+// behind the wait: the read-only path (__ldg, ld.global.nc) is for data that nothing writes
+// while the kernel runs, and it runs from before the wait.
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -171,11 +174,12 @@ __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// 32-byte read-only global load (8 words; the address 32-byte aligned)
-__device__ __forceinline__ void ld_global_nc_v8(const void* ptr, uint32_t* v) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+// 32-byte global load (8 words; the address 32-byte aligned)
+__device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t* v) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(ptr));
+               : "l"(ptr)
+               : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -325,7 +329,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int* 
 // Physical block of a sequence's logical page, validated against the pool.
 // Returns -1 (and flags the status word) for an id outside [0, num_blocks).
 __device__ __forceinline__ int checked_block(const int32_t* row, int page, int num_blocks, unsigned int* status) {
-  int b = __ldg(row + page);
+  int b = row[page];
   if (b < 0 || b >= num_blocks) {
     atomicOr(status, METIS_STATUS_BAD_BLOCK_ID);
     return -1;

@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kDecGroups * kBf16Warps * 32, 1)
 constexpr int kF32Warps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kF32Warps * 32) decode_f32_kernel(const float* __restrict__ k_cache,
-                                                                     const float* __restrict__ v_cache,
+__global__ void __launch_bounds__(kF32Warps * 32) decode_f32_kernel(const float* k_cache,
+                                                                     const float* v_cache,
                                                                      const DecodeParams p) {
   constexpr int DPL = D / 32;  // dims per lane
   pdl_launch_dependents();
@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kF32Warps * 32) decode_f32_kernel(const float*
         const size_t off = ((size_t)b * p.bs + (t - page * p.bs)) * row_stride + (size_t)g * D + lane * DPL;
 #pragma unroll
         for (int i = 0; i < DPL; ++i) {
-          kv[u][i] = __ldg(k_cache + off + i);
-          vv[u][i] = __ldg(v_cache + off + i);
+          kv[u][i] = k_cache[off + i];
+          vv[u][i] = v_cache[off + i];
         }
       } else {
 #pragma unroll
@@ -512,10 +512,10 @@ constexpr int kMergeUnroll = 4;
 constexpr int kMergeCache = 2048;   // partitions whose weights are cached (beyond: recomputed per row)
 
 template <typename OutT>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const float* __restrict__ part_out,
-                                                                 const float* __restrict__ part_lse,
-                                                                 const int32_t* __restrict__ seq_lens, int P,
-                                                                 OutT* __restrict__ out, float* __restrict__ lse_out,
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const float* part_out,
+                                                                 const float* part_lse,
+                                                                 const int32_t* seq_lens, int P,
+                                                                 OutT* out, float* lse_out,
                                                                  int H, int D, int max_parts, int skip_single) {
   constexpr int NT = kMergeWarps * 32;
   constexpr int NJ = kMergeMaxD / 128;   // float4 columns per lane
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const float* __
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const int c = lane + 32 * j;
-          v[k][j] = (w[k] != 0.f && c < nq) ? __ldg(prow + (size_t)i * nq + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[k][j] = (w[k] != 0.f && c < nq) ? prow[(size_t)i * nq + c] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
 #pragma unroll
@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const float* __
 // The merge of row sh = (sequence, head) over its n partitions by one warp: lanes
 // share the lse reductions and own float4 columns lane, lane + 32, ...
 template <typename OutT>
-__device__ __forceinline__ void merge_row(const float* __restrict__ part_out, const float* __restrict__ part_lse,
-                                          OutT* __restrict__ out, float* __restrict__ lse_out, size_t sh, int n,
+__device__ __forceinline__ void merge_row(const float* part_out, const float* part_lse,
+                                          OutT* out, float* lse_out, size_t sh, int n,
                                           int D, int max_parts, int lane) {
   const float* lrow = part_lse + sh * max_parts;
   float M = -INFINITY;
@@ -658,7 +658,7 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ part_out, co
 #pragma unroll
         for (int j = 0; j < kMergeMaxD / 128; ++j) {
           const int c = lane + 32 * j;
-          v[k][j] = (w[k] != 0.f && c < nq) ? __ldg(prow + (size_t)i * nq + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[k][j] = (w[k] != 0.f && c < nq) ? prow[(size_t)i * nq + c] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
 #pragma unroll
@@ -684,11 +684,11 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ part_out, co
 
 // One warp per (sequence, head) when there are few partitions.
 template <typename OutT>
-__global__ void __launch_bounds__(kMergeThreads) merge_warp_kernel(const float* __restrict__ part_out,
-                                                                   const float* __restrict__ part_lse,
-                                                                   const int32_t* __restrict__ seq_lens, int P,
-                                                                   OutT* __restrict__ out,
-                                                                   float* __restrict__ lse_out, int S, int H, int D,
+__global__ void __launch_bounds__(kMergeThreads) merge_warp_kernel(const float* part_out,
+                                                                   const float* part_lse,
+                                                                   const int32_t* seq_lens, int P,
+                                                                   OutT* out,
+                                                                   float* lse_out, int S, int H, int D,
                                                                    int max_parts, int skip_single) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();  // the partials of the kernel before this one are complete and visible
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_warp_kernel(const float* 
 constexpr int kMergeListThreads = 512;  // 128 registers a thread: the row merge needs ~94
 template <typename OutT>
 __global__ void __launch_bounds__(kMergeListThreads, 1) merge_split_rows_kernel(
-    const float* __restrict__ part_out, const float* __restrict__ part_lse, const int32_t* __restrict__ seq_lens,
-    int P, OutT* __restrict__ out, float* __restrict__ lse_out, int S, int H, int D, int max_parts) {
+    const float* part_out, const float* part_lse, const int32_t* seq_lens,
+    int P, OutT* out, float* lse_out, int S, int H, int D, int max_parts) {
   __shared__ int warp_sums[32];
   __shared__ int list_s[kMergeListThreads];
   __shared__ int list_n[kMergeListThreads];

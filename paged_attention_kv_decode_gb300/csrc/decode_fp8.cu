@@ -188,8 +188,8 @@ struct Fp8Units {
     b0 = b1 = -1;
     if (k >= n_my) return;
     const int tok = first_token(k);
-    b0 = __ldg(bt_row + tok / pp.d.bs);
-    if (small_pages && tok + 16 < t1) b1 = __ldg(bt_row + tok / 16 + 1);
+    b0 = bt_row[tok / pp.d.bs];
+    if (small_pages && tok + 16 < t1) b1 = bt_row[tok / 16 + 1];
   }
 
   __device__ __forceinline__ int check_id(int b, bool wanted) const {  // a bad id (flagged) becomes -1

@@ -9,10 +9,7 @@
 
 namespace metis {
 
-// A byte, a piece of codes or of rows.  The kernel in front may be the one that wrote
-// them, and this one may have been launched while it ran: after pdl_wait an ordinary load
-// sees what it wrote, one through the read-only path (__ldg, for data that nothing writes
-// while the kernel runs) need not.
+// A byte, a piece of codes or of rows: ordinary loads (see pdl_wait)
 __device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) { return *p; }
 
 template <typename T>

@@ -364,7 +364,7 @@ __device__ __forceinline__ int mla_rank_inline(const MlaParams& p, int* scratch,
         int bid[kMaxPages];
 #pragma unroll
         for (int i = 0; i < kMaxPages; ++i)
-          bid[i] = i < n_pg ? __ldg(p.block_table + (size_t)sq * p.max_blocks + pg0 + i) : -1;
+          bid[i] = i < n_pg ? p.block_table[(size_t)sq * p.max_blocks + pg0 + i] : -1;
 #pragma unroll
         for (int i = 0; i < kMaxPages; ++i)
           if (bid[i] >= 0 && bid[i] < p.num_blocks)
@@ -575,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (row_valid)
-            ld_global_nc_v8(src + 32 * rank + c0 / 4 + 2 * i, v + 8 * i);
+            ld_global_v8(src + 32 * rank + c0 / 4 + 2 * i, v + 8 * i);
           else
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[8 * i + k] = 0u;
@@ -583,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const uint4 x4 = row_valid ? __ldg(src + 32 * rank + c0 / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 x4 = row_valid ? src[32 * rank + c0 / 4 + i] : make_uint4(0u, 0u, 0u, 0u);
           v[4 * i] = x4.x, v[4 * i + 1] = x4.y, v[4 * i + 2] = x4.z, v[4 * i + 3] = x4.w;
         }
       }
@@ -592,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMlaThreads, 1)
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint4 x4 = row_valid ? __ldg(src + kMlaDv / 8 + 4 * rank + c) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 x4 = row_valid ? src[kMlaDv / 8 + 4 * rank + c] : make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(sQr + hr * 64 + ((c ^ ((hr >> 1) & 3)) << 4)) = x4;
     }
     fence_proxy_async_smem();  // the score UMMA reads the rope tile through the async proxy

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kLocalWarps * 32)
 constexpr int kChainThreads = 64;
 constexpr int kChainBatch = 8;
 __global__ void __launch_bounds__(kChainThreads)
-    prefix_chain_kernel(const int32_t* __restrict__ cu_pages, int S, int total, uint64_t* keys) {
+    prefix_chain_kernel(const int32_t* cu_pages, int S, int total, uint64_t* keys) {
   pdl_wait();
   const int s = blockIdx.x * kChainThreads + threadIdx.x;
   if (s >= S) return;
@@ -212,8 +212,8 @@ constexpr int kLookupThreads = 256;
 // turns the counts into exclusive offsets, saves the clamped stack depth for the
 // allocation pass and pops the pages taken
 __global__ void __launch_bounds__(kLookupThreads)
-    prefix_mark_kernel(int n, const int32_t* __restrict__ slot_of, const int32_t* table_pages,
-                       const int32_t* claim, uint8_t* __restrict__ owner, int32_t* cta_count, int32_t* done,
+    prefix_mark_kernel(int n, const int32_t* slot_of, const int32_t* table_pages,
+                       const int32_t* claim, uint8_t* owner, int32_t* cta_count, int32_t* done,
                        int32_t* free_count, int free_capacity, int32_t* fc_saved) {
   pdl_wait();
   pdl_launch_dependents();
@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kLookupThreads)
 
 // grid, one thread per key: an owner takes stack page (depth - 1 - rank)
 __global__ void __launch_bounds__(kLookupThreads)
-    prefix_alloc_kernel(int n, const int32_t* __restrict__ slot_of, const uint8_t* __restrict__ owner,
-                        const int32_t* __restrict__ cta_offset, const int32_t* __restrict__ fc_saved,
-                        int32_t* table_pages, int32_t* claim, const int32_t* __restrict__ free_stack,
+    prefix_alloc_kernel(int n, const int32_t* slot_of, const uint8_t* owner,
+                        const int32_t* cta_offset, const int32_t* fc_saved,
+                        int32_t* table_pages, int32_t* claim, const int32_t* free_stack,
                         int32_t* refcount, int num_pages) {
   pdl_wait();
   pdl_launch_dependents();
@@ -299,9 +299,9 @@ __global__ void __launch_bounds__(kLookupThreads)
 
 // grid, one thread per key: its page and whether it was a hit
 __global__ void __launch_bounds__(kLookupThreads)
-    prefix_resolve_kernel(int n, const int32_t* __restrict__ slot_of, const int32_t* table_pages,
-                          const uint8_t* __restrict__ owner, int32_t* refcount, int num_pages,
-                          int32_t* __restrict__ pages_out, uint8_t* __restrict__ hits_out) {
+    prefix_resolve_kernel(int n, const int32_t* slot_of, const int32_t* table_pages,
+                          const uint8_t* owner, int32_t* refcount, int num_pages,
+                          int32_t* pages_out, uint8_t* hits_out) {
   pdl_wait();
   pdl_launch_dependents();
   const int i = blockIdx.x * kLookupThreads + threadIdx.x;

@@ -21,3 +21,17 @@ def test_persistent_decodes_fence_the_ring_between_items(name, kernel):
     loop = body[body.index("for (;;)"):]
     assert "combine_and_store" in loop or "decode_bf16_item" in loop
     assert loop.index("fence_proxy_async_smem();") < loop.index("gsync();")
+
+
+READ_ONLY = re.compile(r"__ldg\s*\(|\.nc\.|__restrict__")
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))))
+def test_dependent_kernels_read_with_ordinary_loads(name):
+    """A kernel that may start while the one in front runs (it calls pdl_wait) reads nothing through the
+    read-only path, which the compiler may also take for `const __restrict__` parameters: caches, index
+    arrays and partials may be what the kernel in front writes."""
+    text = source(name)
+    if name in ("cache_write.cu", "prefix_cache.cu"):  # some of their kernels are launched behind complete ones only
+        text = "\n".join(k for k in re.findall(r"__global__.*?\n}\n", text, re.S) if "pdl_wait" in k)
+    assert not READ_ONLY.search(text), READ_ONLY.search(text).group(0)
