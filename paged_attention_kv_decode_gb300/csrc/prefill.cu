@@ -244,12 +244,13 @@ struct PfBar {
 };
 static_assert((PfBar::kCount + 4) * 8 <= 256, "prefill barrier area");
 
-// Effective (sequence length, query count) after clamping to what can be read.
+// Effective (sequence length, query count) after clamping to what can be read.  `flag`: report
+// what had to be clamped (the schedule kernel, which sees every sequence once).
 __device__ __forceinline__ void pf_lengths(const PrefillParams& p, int s, int& L, int& q_len, bool flag) {
   L = p.seq_lens[s];
   q_len = p.cu_q_lens[s + 1] - p.cu_q_lens[s];
   if (L > p.cap) {
-    if (flag) atomicOr(&g_status_prefill, METIS_STATUS_SEQ_TOO_LONG);
+    if (flag && q_len != 0) atomicOr(&g_status_prefill, METIS_STATUS_SEQ_TOO_LONG);
     L = p.cap;
   }
   if (L < 0) L = 0;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
   for (int s = s0; s < s1; ++s) {
     int L, q_len;
     const bool routed = p.skip_decodes && p.cu_q_lens[s + 1] - p.cu_q_lens[s] == 1;
-    pf_lengths(p, s, L, q_len, routed);  // a routed decode's content errors are flagged here
+    pf_lengths(p, s, L, q_len, true);
     if (s == s0) {
       L_first = L;
       q_first = q_len;
@@ -457,13 +458,13 @@ struct PfUnit8 : PfUnit {
 __device__ __forceinline__ int pf_first(const PfUnit&) { return 0; }
 __device__ __forceinline__ int pf_first(const PfUnit8& it) { return it.j0; }
 
-__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag, PfUnit& it) {
+__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, PfUnit& it) {
   const int item_idx = u / p.G;
   it.g = u - item_idx * p.G;
   const int4 v = __ldcg(p.items + item_idx);  // written by this call's schedule kernel: read from L2
   it.s = v.x;
   it.pair = v.y;
-  pf_lengths(p, it.s, it.L, it.q_len, flag && it.g == 0);
+  pf_lengths(p, it.s, it.L, it.q_len, false);
   it.n0 = pf_kv_tiles(it.L, it.q_len, 2 * it.pair, p.Tq);      // K/V tiles of query tile 0
   it.n1 = pf_kv_tiles(it.L, it.q_len, 2 * it.pair + 1, p.Tq);  // ... of query tile 1 (0: no second tile)
   it.n_kv = max(it.n0, it.n1);
@@ -474,15 +475,14 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, bool flag
 
 // Unit u: `whole` units in one piece, then the parts of `rest` others.  A part begins where
 // every query row of the pair sees keys: its running maximum is finite from its first tile on.
-__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole, int rest, int splits, bool flag,
-                                        PfUnit8& it) {
+__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole, int rest, int splits, PfUnit8& it) {
   int part = 0;
   if (u >= whole) {
     part = (u - whole) / rest;
     u -= part * rest;
   }
   it.j0 = it.tag = 0;
-  if (!pf_unit(p, u, flag && part == 0, it)) return false;
+  if (!pf_unit(p, u, it)) return false;
   if (u >= whole && it.n_kv < kMinSplitTiles) return part == 0;
   if (u >= whole) {
     const int len = max((it.n_kv + splits - 1) / splits, kMinPartTiles);
@@ -1196,11 +1196,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       u = __shfl_sync(0xffffffffu, u, 0);
       Unit it;
       if (u < units) {
-        bool some;                                     // nothing to compute (length errors flagged here)
+        bool some;  // false: nothing to compute
         if constexpr (SPLIT)
-          some = pf_unit(p, u, splits.y, rest, splits.x, lane == 0, it);
+          some = pf_unit(p, u, splits.y, rest, splits.x, it);
         else
-          some = pf_unit(p, u, lane == 0, it);
+          some = pf_unit(p, u, it);
         if (!some) continue;
       } else {
         u = -1;
