@@ -70,7 +70,8 @@ extern "C" {
 #define METIS_STATUS_BAD_Q_LEN     8u  /* prefill: q_len > seq_len or a negative q_len */
 #define METIS_STATUS_TABLE_FULL   16u  /* prefix lookup: a key found no free table slot */
 #define METIS_STATUS_OUT_OF_PAGES 32u  /* prefix lookup: a new key found the free stack empty */
-#define METIS_STATUS_BAD_OFFSETS  64u  /* page keys: cu_pages asks for a page past its sequence's tokens */
+#define METIS_STATUS_BAD_OFFSETS  64u  /* an offset outside the call's rows; page keys: cu_pages asks for a
+                                          page past its sequence's tokens */
 
 /*
  * metis_paged_attn_decode -- one query token per sequence over its pages
@@ -191,7 +192,7 @@ size_t metis_decode_workspace_bytes(int num_seqs, int num_heads, int head_dim,
  *   q          [num_tokens, num_heads, head_dim] bf16; the sequences' query
  *              rows back to back, sequence s at rows cu_q_lens[s] ..
  *   cu_q_lens  int32 [num_seqs + 1], cu_q_lens[0] = 0, non-decreasing,
- *              cu_q_lens[num_seqs] = num_tokens
+ *              cu_q_lens[num_seqs] <= num_tokens
  *   k_cache, v_cache, block_table, seq_lens   as for metis_paged_attn_decode
  *   out        [num_tokens, num_heads, head_dim] bf16 (written)
  *   lse_out    fp32 [num_tokens, num_heads] or NULL
@@ -202,8 +203,11 @@ size_t metis_decode_workspace_bytes(int num_seqs, int num_heads, int head_dim,
  * Supported: dtype METIS_BF16 (tensor cores: bf16 operands, fp32 accumulation);
  * head_dim 64 or 128; block_size 16, 32 or 64; num_heads / num_kv_heads in
  * {1, 2, 4, 8, 16}.  A q_len larger than the sequence length is clamped to it
- * (status bit METIS_STATUS_BAD_Q_LEN).  num_seqs == 0 or num_tokens == 0 is a
- * successful no-op.
+ * (status bit METIS_STATUS_BAD_Q_LEN); a sequence with q_len < 0 has no rows (the
+ * same bit).  A sequence with an offset outside [0, num_tokens] is left out
+ * (METIS_STATUS_BAD_OFFSETS), and rows of out and lse_out that belong to no
+ * sequence are left as they were.  Offsets that decrease may leave other rows of
+ * the call unwritten too.  num_seqs == 0 or num_tokens == 0 is a successful no-op.
  */
 int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q_lens,
                                    const void* k_cache, const void* v_cache,
@@ -367,8 +371,9 @@ int metis_mla_reshape_and_cache(const void* kv_c, const void* k_pe, void* kv_cac
  * A sequence with q_len < 0 or > seq_lens[s] (METIS_STATUS_BAD_Q_LEN), with rows
  * outside [0, num_tokens) (METIS_STATUS_BAD_OFFSETS) or longer than its table row
  * (METIS_STATUS_SEQ_TOO_LONG) is not written, and neither is a page whose id is
- * outside the pool (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 or num_tokens == 0
- * is a successful no-op.
+ * outside the pool (METIS_STATUS_BAD_BLOCK_ID).  Offsets that decrease may leave other
+ * pages of the call unwritten too.  num_seqs == 0 or num_tokens == 0 is a successful
+ * no-op.
  */
 int metis_reshape_and_cache_fp8(const void* key, const void* value, void* k_cache, void* v_cache,
                                 uint8_t* k_scale, uint8_t* v_scale, const int32_t* cu_q_lens,

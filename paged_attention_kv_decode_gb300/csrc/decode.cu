@@ -828,9 +828,25 @@ static int launch_bf16(const DecodeParams& p, const void* k_cache, const void* v
                           p);
 }
 
-static DecodeParams rows_params(const void* q, const int32_t* block_table, const int32_t* seq_lens,
-                                const int32_t* rows, void* out, float* lse_out, int S, int H, int G, int D, int bs,
-                                int max_blocks, int num_blocks, float scale, int cap) {
+template <int D>
+static int launch_beside(const DecodeParams& p, const void* k_cache, const void* v_cache, const int* n_ctas,
+                         int* next_item, int grid, cudaStream_t st) {
+  CUtensorMap tmK, tmV;
+  int rc = encode_kv_maps<D>(p, k_cache, v_cache, &tmK, &tmV);
+  if (rc) return rc;
+  constexpr int smem = dec_beside_smem_bytes<D>();
+  static int done = 0;
+  auto kern = decode_rows_beside_kernel<D>;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
+  if (rc) return rc;
+  return launch_dependent(kern, dim3((unsigned)grid), dim3(kDecGroups * kBf16Warps * 32), (size_t)smem, st,
+                          "decode_rows_beside_kernel launch", tmK, tmV, p, n_ctas, next_item);
+}
+
+int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
+                              int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                              const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
   DecodeParams p;
   p.q = q;
   p.block_table = block_table;
@@ -852,42 +868,7 @@ static DecodeParams rows_params(const void* q, const int32_t* block_table, const
   p.max_parts = 1;
   p.cap = cap;
   p.rows = rows;
-  return p;
-}
-
-// The single-token sequences of a chunked-prefill batch, through the decode
-// kernel (unsplit, longest first): rows = the batch's cu_q_lens.  The caller has
-// validated the shapes (bf16, head_dim 64 or 128, head ratio 1, 2, 4 or 8).
-int launch_decode_rows(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                       const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H, int G,
-                       int D, int bs, int max_blocks, int num_blocks, float scale, int cap, cudaStream_t st) {
-  const DecodeParams p =
-      rows_params(q, block_table, seq_lens, rows, out, lse_out, S, H, G, D, bs, max_blocks, num_blocks, scale, cap);
-  const dim3 grid(1u, (unsigned)G, (unsigned)S);
-  return D == 64 ? launch_bf16<64>(p, k_cache, v_cache, grid, st) : launch_bf16<128>(p, k_cache, v_cache, grid, st);
-}
-
-template <int D>
-static int launch_beside(const DecodeParams& p, const void* k_cache, const void* v_cache, const int* n_ctas,
-                         int* next_item, int grid, cudaStream_t st) {
-  CUtensorMap tmK, tmV;
-  int rc = encode_kv_maps<D>(p, k_cache, v_cache, &tmK, &tmV);
-  if (rc) return rc;
-  constexpr int smem = dec_beside_smem_bytes<D>();
-  static int done = 0;
-  auto kern = decode_rows_beside_kernel<D>;
-  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
-  if (rc) return rc;
-  return launch_dependent(kern, dim3((unsigned)grid), dim3(kDecGroups * kBf16Warps * 32), (size_t)smem, st,
-                          "decode_rows_beside_kernel launch", tmK, tmV, p, n_ctas, next_item);
-}
-
-int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                              const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
-                              int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
-                              const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
-  const DecodeParams p =
-      rows_params(q, block_table, seq_lens, rows, out, lse_out, S, H, G, D, bs, max_blocks, num_blocks, scale, cap);
+  p.T = T;
   return D == 64 ? launch_beside<64>(p, k_cache, v_cache, n_ctas, next_item, grid, st)
                  : launch_beside<128>(p, k_cache, v_cache, n_ctas, next_item, grid, st);
 }

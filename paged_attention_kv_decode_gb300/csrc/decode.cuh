@@ -23,17 +23,22 @@ struct DecodeParams {
   int max_parts;
   int cap;  // tokens readable per sequence: min(max_blocks * bs, max_seq_len)
   // Decodes of a chunked-prefill batch (NULL otherwise): the batch's cu_q_lens.
-  // Sequence s is handled only if rows[s + 1] - rows[s] == 1; its query, output
-  // and lse row is rows[s] of the packed [T, H, D] tensors.
+  // Sequence s is handled only if rows[s + 1] - rows[s] == 1 and that row exists; its
+  // query, output and lse row is rows[s] of the packed [T, H, D] tensors.
   const int32_t* rows;
+  int T;
 };
 
-// Output (and query) row of sequence s; -1 when the call skips it (a sequence
-// with more than one query token in a mixed batch).
+// The sequence's single query row in a mixed batch of T packed rows; -1: it has several,
+// none, or one outside them.
+__device__ __forceinline__ int single_row(const int32_t* rows, int T, int s) {
+  const int r0 = rows[s];
+  return r0 >= 0 && r0 < T && rows[s + 1] == r0 + 1 ? r0 : -1;
+}
+
+// Output (and query) row of sequence s; -1 when the call skips it (single_row).
 __device__ __forceinline__ int decode_row(const DecodeParams& p, int s) {
-  if (!p.rows) return s;
-  const int r0 = p.rows[s];
-  return p.rows[s + 1] - r0 == 1 ? r0 : -1;
+  return p.rows ? single_row(p.rows, p.T, s) : s;
 }
 
 // Token range of this CTA, after clamping the sequence length.  Returns

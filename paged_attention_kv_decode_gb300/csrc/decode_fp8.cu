@@ -1122,11 +1122,12 @@ static DecodeFp8Params fp8_params(const void* q, const Fp8Cache& cache, const in
 }
 
 int launch_decode_fp8_rows_beside(const void* q, const Fp8Cache& cache, const int32_t* block_table,
-                                  const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
-                                  int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                                  const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
+                                  int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
                                   const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
-  const DecodeFp8Params pp = fp8_params(q, cache, block_table, seq_lens, rows, out, lse_out, S, H, G, D, bs, max_blocks,
-                                        num_blocks, scale, cap);
+  DecodeFp8Params pp = fp8_params(q, cache, block_table, seq_lens, rows, out, lse_out, S, H, G, D, bs, max_blocks,
+                                  num_blocks, scale, cap);
+  pp.d.T = T;
   return D == 64 ? launch_beside8<64>(pp, cache.k_cache, cache.v_cache, n_ctas, next_item, grid, st)
                  : launch_beside8<128>(pp, cache.k_cache, cache.v_cache, n_ctas, next_item, grid, st);
 }

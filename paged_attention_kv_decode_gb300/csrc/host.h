@@ -93,23 +93,18 @@ int launch_merge_split_rows(const float* part_out, const float* part_lse, const 
                             float* lse_out, int S, int H, int D, int max_parts, int out_dtype, int sms,
                             cudaStream_t st);
 
-// The single-token sequences of a chunked-prefill batch through the bf16 decode
-// kernel (decode.cu); rows = the batch's cu_q_lens.  Other sequences are skipped.
-int launch_decode_rows(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                       const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H, int G,
-                       int D, int bs, int max_blocks, int num_blocks, float scale, int cap, cudaStream_t st);
-
-// The same, persistent, beside the chunk kernel: one CTA per SM in a grid of `grid`
-// CTAs, of which the first *n_ctas (device value, written by the prefill schedule
-// kernel before this grid reads it) take (sequence, KV head) items from the
-// counter *next_item (zeroed by that kernel); the others exit at once.  Every CTA
-// lets the next grid launch only after waiting for the previous one.
+// The single-token sequences of a chunked-prefill batch of T packed rows, persistent,
+// beside the chunk kernel (decode.cu); rows = the batch's cu_q_lens.  One CTA per SM in a
+// grid of `grid` CTAs, of which the first *n_ctas (device value, written by the prefill
+// schedule kernel before this grid reads it) take (sequence, KV head) items from the counter
+// *next_item (zeroed by that kernel); the others exit at once.  Every CTA lets the next grid
+// launch only after waiting for the previous one.
 int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                              const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
-                              int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                              const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
+                              int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
                               const int* n_ctas, int* next_item, int grid, cudaStream_t st);
 
-// The same two for an 8-bit cache (decode_fp8.cu).
+// The same for an 8-bit cache (decode_fp8.cu).
 struct Fp8Cache {
   const void* k_cache;  // e4m3 codes [num_blocks, bs, G, D]
   const void* v_cache;
@@ -117,8 +112,8 @@ struct Fp8Cache {
   const uint8_t* v_scale;
 };
 int launch_decode_fp8_rows_beside(const void* q, const Fp8Cache& cache, const int32_t* block_table,
-                                  const int32_t* seq_lens, const int32_t* rows, void* out, float* lse_out, int S, int H,
-                                  int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
+                                  const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
+                                  int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
                                   const int* n_ctas, int* next_item, int grid, cudaStream_t st);
 
 // Per-translation-unit device status words.

@@ -70,6 +70,7 @@
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
+#include "decode.cuh"
 #include "fp8.cuh"
 #include "host.h"
 #include "tcgen05.cuh"
@@ -248,7 +249,13 @@ static_assert((PfBar::kCount + 4) * 8 <= 256, "prefill barrier area");
 // what had to be clamped (the schedule kernel, which sees every sequence once).
 __device__ __forceinline__ void pf_lengths(const PrefillParams& p, int s, int& L, int& q_len, bool flag) {
   L = p.seq_lens[s];
-  q_len = p.cu_q_lens[s + 1] - p.cu_q_lens[s];
+  const int r0 = p.cu_q_lens[s], r1 = p.cu_q_lens[s + 1];
+  if (r0 < 0 || r1 < 0 || r0 > p.T || r1 > p.T) {  // rows outside the batch's: the sequence is left out
+    if (flag) atomicOr(&g_status_prefill, METIS_STATUS_BAD_OFFSETS);
+    L = q_len = 0;
+    return;
+  }
+  q_len = r1 - r0;
   if (L > p.cap) {
     if (flag && q_len != 0) atomicOr(&g_status_prefill, METIS_STATUS_SEQ_TOO_LONG);
     L = p.cap;
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
   bool routed_first = false;
   for (int s = s0; s < s1; ++s) {
     int L, q_len;
-    const bool routed = p.skip_decodes && p.cu_q_lens[s + 1] - p.cu_q_lens[s] == 1;
+    const bool routed = p.skip_decodes && single_row(p.cu_q_lens, p.T, s) >= 0;
     pf_lengths(p, s, L, q_len, true);
     if (s == s0) {
       L_first = L;
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
       *p.dec_next = 0;
     }
   }
-  const int total = min(all, max_items);
+  const int total = min(max(all, 0), max_items);
   const bool sort = total <= kSortMax;
   if (p.splits) {
     if (tid == 0) longest = 0;
@@ -388,11 +395,11 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
     bool routed = routed_first;
     if (s != s0) {
       pf_lengths(p, s, L, q_len, false);
-      routed = p.skip_decodes && p.cu_q_lens[s + 1] - p.cu_q_lens[s] == 1;
+      routed = p.skip_decodes && single_row(p.cu_q_lens, p.T, s) >= 0;
     }
     const int np = routed ? 0 : (q_len + pair_tokens - 1) / pair_tokens;
     for (int t = 0; t < np; ++t, ++pos) {
-      if (pos >= total) break;
+      if ((unsigned)pos >= (unsigned)total) break;  // (offsets that decrease may list more than fits)
       const int work = pf_kv_tiles(L, q_len, 2 * t, p.Tq) + pf_kv_tiles(L, q_len, 2 * t + 1, p.Tq);
       const int4 it = make_int4(s, t, work, 0);
       if (p.splits) atomicMax(&longest, pf_kv_tiles(L, q_len, 2 * t, p.Tq));
@@ -1662,12 +1669,12 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   auto between = [&](const PrefillParams& pp) -> int {
     if (!pp.skip_decodes) return METIS_OK;
     if (fp8.k_cache)
-      return launch_decode_fp8_rows_beside(q, fp8, block_table, seq_lens, cu_q_lens, out, lse_out, num_seqs, num_heads,
-                                           num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale, pp.cap,
-                                           pp.dec_ctas, pp.dec_next, sms, st);
-    return launch_decode_rows_beside(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, out, lse_out, num_seqs,
-                                     num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, scale,
-                                     pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
+      return launch_decode_fp8_rows_beside(q, fp8, block_table, seq_lens, cu_q_lens, num_tokens, out, lse_out, num_seqs,
+                                           num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                           scale, pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
+    return launch_decode_rows_beside(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, num_tokens, out, lse_out,
+                                     num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                     scale, pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
   };
   auto launch = [&](auto dim, auto kv8, auto split) {
     return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value>(

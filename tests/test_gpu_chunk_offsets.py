@@ -68,3 +68,37 @@ def test_query_counts_that_do_not_fit_are_reported(batch):
     # a length past the bound counts only where there are queries
     assert batch.run([0, 20, 21, 21, 61], [90, 40, 500, 70])[2] == 0
     assert batch.run([0, 20, 21, 24, 64], [90, 40, 500, 70])[2] & pa.STATUS_SEQ_TOO_LONG
+
+
+@pytest.mark.parametrize("cu,out_of_it", [
+    ([0, 20, 21, 24, 65], [3]),                    # a chunk past the last row
+    ([0, 20, 21, 24, (1 << 31) - 1], [3]),
+    ([0, 20, 21, 30, 1 << 20], [3]),
+    ([64, 65, 65, 65, 65], [0, 1, 2, 3]),          # a single row past it
+    ([(1 << 31) - 1, -(1 << 31), 1, 4, 44], [0, 1]),
+    ([-1, 0, 1, 4, 44], [0]),                      # a single row in front of the first
+    ([-30, 20, 21, 24, 64], [0]),
+    ([-(1 << 31), 20, 21, 24, 64], [0]),
+    ([0, 20, 1 << 30, 24, 64], [1, 2]),
+])
+def test_rows_outside_the_batch_are_left_out(batch, cu, out_of_it):
+    got = batch.run(cu)
+    assert got[2] == pa.STATUS_BAD_OFFSETS
+    # the other sequences, each alone in a call of its own
+    written = np.zeros(batch.rows, bool)
+    for s in range(4):
+        if s in out_of_it:
+            continue
+        alone = [cu[s]] * (s + 1) + [cu[s + 1]] * (4 - s)
+        ref = batch.run(alone)
+        assert ref[2] == 0
+        rows = slice(cu[s], cu[s + 1])
+        written[rows] = True
+        assert np.abs((got[0][rows].float() - ref[0][rows].float()).cpu().numpy()).max(initial=0.0) <= 0.05
+        assert np.abs((got[1][rows] - ref[1][rows]).cpu().numpy()).max(initial=0.0) <= 1e-3
+    assert untouched(got, torch.from_numpy(np.flatnonzero(~written)).to(DEV))
+
+
+def test_rows_behind_the_last_sequence_stay(batch):
+    got = batch.run([0, 20, 21, 24, 50])
+    assert got[2] == 0 and untouched(got, slice(50, 64)) and not untouched(got, slice(49, 50))
