@@ -1232,10 +1232,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const uint32_t s_tmem = lane_base + w * kKvTile;
     const uint32_t o_tmem = lane_base + 2 * kKvTile + w * D;
     const float sl2 = p.scale_log2;
-    const float sgn = sl2 < 0.f ? -1.f : 1.f;   // max of sl2 * s = |sl2| * max(sgn * s)
-    // |sl2| > 0 keeps -inf (hidden key) * |sl2| = -inf; a zero scale becomes 1e-30, which
-    // leaves every exponent equal to the max to fp32 precision (uniform weights)
-    const float asl2 = fmaxf(fabsf(sl2), 1e-30f);
+    // max of sl2 * s = |sl2| * max(sgn * s); a zero scale makes every visible score zero (uniform weights)
+    const float sgn = sl2 < 0.f ? -1.f : sl2 > 0.f ? 1.f : 0.f;
+    // > 0, so that a hidden key's -inf stays -inf (8-bit cache: the tile's factors are held above zero)
+    const float asl2 = sl2 != 0.f ? fabsf(sl2) : KV8 ? 0.f : 1.f;
     uint32_t ns = 0, npv = 0, k = 0;            // s_full phases consumed, PVs of this group, units read
     bool ok = true;
     Unit it;
