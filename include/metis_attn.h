@@ -436,8 +436,10 @@ int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* 
  * A chunk's query rows
  * enter the products as two e4m3 parts at one power of two each: elements down to 2^-8
  * of the row's largest are exact, smaller ones are off by at most 2^-17 of it.  V
- * enters as bf16, scale included (exact), with softmax weights in bf16.  NaN in V reaches
- * the rows that see its token, in its column.  Sequences with one query and a head ratio
+ * enters as bf16, scale included (exact for scales of 2^-124 and more; values past bf16's
+ * range as its largest), with softmax weights in bf16 of up to 2^8: sums of V values above
+ * 2^119 may overflow to infinity.  NaN in V reaches
+ * the rows that see its token, in its column, as no value of an unseen token does.  Sequences with one query and a head ratio
  * up to 8 are computed as metis_paged_attn_decode_fp8 computes them.
  */
 int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,

@@ -219,6 +219,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Two floats to bf16 (round to nearest even), infinities and values beyond the bf16 range
+// saturated to its largest (NaN stays); `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Two floats to fp16 (round to nearest even), finite values beyond the fp16 range
 // saturated to +-65504; `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {

@@ -507,13 +507,14 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, int whole
 }
 
 // Eight e4m3 codes of one row times their page's scale, as bf16 (exact: four significant
-// bits and a power of two)
+// bits and a power of two).  Values past bf16's range become its largest: an infinity of a
+// token that a row must not see would reach it as 0 * infinity.
 __device__ __forceinline__ uint4 codes_to_bf16x8(uint32_t w0, uint32_t w1, float scale) {
   float a[4], b[4];
   unpack_e4m3x4_f32(w0, a);
   unpack_e4m3x4_f32(w1, b);
-  return make_uint4(pack_bf16x2(a[0] * scale, a[1] * scale), pack_bf16x2(a[2] * scale, a[3] * scale),
-                    pack_bf16x2(b[0] * scale, b[1] * scale), pack_bf16x2(b[2] * scale, b[3] * scale));
+  return make_uint4(pack_bf16x2_sat(a[0] * scale, a[1] * scale), pack_bf16x2_sat(a[2] * scale, a[3] * scale),
+                    pack_bf16x2_sat(b[0] * scale, b[1] * scale), pack_bf16x2_sat(b[2] * scale, b[3] * scale));
 }
 
 // 8-bit cache: the query row `row` of a 128-row bf16 tile as two e4m3 parts, q up = hi + lo, so

@@ -7,6 +7,7 @@ import torch
 import oracle
 import paged_attention_kv_decode_gb300 as pa
 from test_gpu_cache_fp8 import BF16, CHUNK_STEP, DEV, Cache, attention, check, check_lse, gpu, i32
+from test_gpu_fp8_value_ranges import exact
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,33 @@ def test_chunk_split_and_whole_within_each_rows_own_bound():
                        workspace=torch.full((n,), 0xAB, dtype=torch.uint8, device=DEV))
         check(out[dev_at], ref, tol, BF16, "out")
         check_lse(lse[dev_at], rl, lt)
+
+
+@pytest.mark.parametrize("r,D,bs", [(4, 128, 16), (1, 64, 32), (8, 64, 64)])
+def test_chunk_lowest_value_of_an_unseen_token_stays_out(r, D, bs):
+    """V rows hold the type's lowest and largest value (2^128 once rounded to a code): rows of the same
+    chunk that do not see them are what they are without them."""
+    rng = np.random.default_rng(r + D)
+    lens, q_lens = [200, 150], [170, 150]
+    c = Cache(rng, lens, 1, D, bs, spread=0.0, poisoned=False)
+    rows = [torch.from_numpy(rng.standard_normal((350, 1, D))).to(BF16) for _ in range(2)]
+    extreme = ((0, 150, 5, torch.finfo(BF16).min), (0, 151, 9, torch.finfo(BF16).max), (1, 20, 7, torch.finfo(BF16).min),
+               (1, 149, 0, torch.finfo(BF16).max))
+    for s, t, d, x in extreme:
+        rows[1][200 * s + t, 0, d] = x
+    pa.metis_reshape_and_cache_fp8(gpu(rows[0]), gpu(rows[1]), *c.dev, i32([0, 200, 350]), c.bt, c.sl)
+    c.k, c.ks = oracle.write_cache(rows[0], c.k, c.ks, [0, 200, 350], c.table, lens)
+    c.v, c.vs = oracle.write_cache(rows[1], c.v, c.vs, [0, 200, 350], c.table, lens)
+    q = torch.from_numpy(rng.standard_normal((320, r, D))).to(BF16)
+    out, lse = run(c, q, q_lens, D ** -0.5)
+    visible = rows_of(lens, q_lens)
+    ref, tol, rl, lt = exact(c, q.double().numpy(), visible, D ** -0.5, "chunk")
+    check_lse(lse, rl, lt)
+    sees = np.zeros((320, D), bool)
+    for s, t, d, _ in extreme:
+        sees[[i for i, (seq, n) in enumerate(visible) if seq == s and n > t], d] = True
+    sees = np.broadcast_to(sees[:, None], ref.shape)
+    got = out.double().cpu().numpy()
+    assert not np.isnan(got).any()
+    check(torch.from_numpy(np.where(sees, 0.0, got)), np.where(sees, 0.0, ref), tol, BF16, "columns that see none")
+    assert sees.any() and (np.abs(ref[sees]) > 1e30).all() and (np.sign(got[sees]) == np.sign(ref[sees])).all()
