@@ -41,6 +41,13 @@ __device__ __forceinline__ int decode_row(const DecodeParams& p, int s) {
   return p.rows ? single_row(p.rows, p.T, s) : s;
 }
 
+// Tokens [t0, t1) of partition `part` (of P tokens each) of a sequence of L; t1 <= t0: none.
+// (t0 + P may pass 2^31.)
+__host__ __device__ __forceinline__ void partition_tokens(int L, int P, int part, int& t0, int& t1) {
+  t0 = part * P;
+  t1 = L - t0 > P ? t0 + P : L;
+}
+
 // Token range of this CTA, after clamping the sequence length.  Returns
 // false when the CTA has nothing to do (after writing what an empty
 // partition or sequence must leave behind).
@@ -57,8 +64,7 @@ __device__ __forceinline__ bool decode_range(const DecodeParams& p, int part, in
   }
   if (L < 0) L = 0;
   if (p.partition_size > 0) {
-    t0 = part * p.partition_size;
-    t1 = min(L, t0 + p.partition_size);
+    partition_tokens(L, p.partition_size, part, t0, t1);
   } else {
     t0 = 0;
     t1 = L;
