@@ -55,10 +55,12 @@
 // softmax threads split their query row, scaled by a power of two, into two e4m3 parts,
 // S = (hi + lo) codes^T, so that QK costs what it costs in bf16 at half of K's bytes.  A K
 // page's scale joins the softmax factor of its 16 tokens.  V's codes are staged by TMA and
-// become bf16 rows, scale included (exact), by four warps; P stays bf16.  What bounds it is
-// what bounds the bf16 kernel, the UMMA issuer's waits for P (and here for converted V
-// tiles): 2,048 queries over 16,384 tokens, 32/8 heads of 128, take 420 us = 1,230 TFLOP/s
-// (bf16 kernel 460 us); 16 chunks of 512 behind up to 4,096 tokens 258 us (247).  On the way
+// become bf16 rows, scale included (exact), by four warps; P stays bf16.  2,048 queries over
+// 16,384 tokens, 32/8 heads of 128, take 420-435 us = 1,185-1,230 TFLOP/s (bf16 kernel 460 us);
+// 16 chunks of 512 behind up to 4,096 tokens 258 us (247).  What bounds it: a K/V-tile pair
+// takes 2,930 cycles, of which the tensor work is 2,054, and shared memory's port is busy for
+// 2,176 (QK's and PV's operands, V's conversion, the TMA writes); the rest are the hand-offs
+// between softmax, converters and issuer (without V's conversion 3 % less).  On the way
 // there: K converted to bf16 as well 2,154 us for the first; codes into the UMMAs and V
 // converted by three warps 528 us; the issuer's operands uniform over its warp, queries
 // split by the softmax threads and a fourth converter 431 us.  Few chunks: units are split
@@ -119,7 +121,6 @@ constexpr int kMinPartTiles = 4;
 constexpr int kMinSplitTiles = 13;
 
 struct PrefillParams {
-  const void* q;
   const int32_t* cu_q_lens;
   const int32_t* block_table;
   const int32_t* seq_lens;
@@ -1039,7 +1040,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ UMMA issuer
-    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
+    regs_dec<kRegsMma>();
     constexpr uint32_t kIdQK = umma_idesc_bf16_f32(kRows, kKvTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_bf16_f32(kRows, D, false, true);
     bool issued = false;
@@ -1223,7 +1224,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if (u < 0) break;
     }
   } else if (warp > kMmaWarp) {
-    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();  // idle: give the registers to the softmax groups
+    regs_dec<kRegsMma>();  // idle: give the registers to the softmax groups
   } else {
     // ------------------------------------------------------------ softmax groups
     regs_inc<KV8 ? kRegsSoftmax8 : kRegsSoftmax>();
@@ -1634,7 +1635,6 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   if (max_items * num_kv_heads > 0x7fffffffull) return fail(METIS_E_SHAPE, "too many query tiles");
 
   PrefillParams p{};
-  p.q = q;
   p.cu_q_lens = cu_q_lens;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
