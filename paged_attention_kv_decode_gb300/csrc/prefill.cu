@@ -641,7 +641,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   constexpr int kStages8 = kV8Stages;
   static_assert(KV8 || !SPLIT, "parts of units: 8-bit cache only");
   using Unit = std::conditional_t<SPLIT, PfUnit8, PfUnit>;
-  if (!p.wait_at_exit) pdl_wait();  // the schedule kernel's items are complete and visible
+  // The schedule kernel's items, and what the kernels in front of it wrote (tables, scale bytes),
+  // are complete: waited for here, or by every CTA of the decode grid in front before it let this
+  // grid launch (the warps that read more than the items then fence, below).
+  if (!p.wait_at_exit) pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t slack = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + slack;
@@ -696,6 +699,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
+  } else if (warp >= 8 && p.wait_at_exit) {
+    __threadfence();  // nothing here waited: lines that an earlier kernel left in this SM's L1 are dropped
   }
   tc_fence_before_sync();
   __syncthreads();

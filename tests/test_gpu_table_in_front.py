@@ -75,3 +75,45 @@ def test_lookup_then_each_call_replayed():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
     assert sorted(bt.view(-1).tolist()) == sorted(set(bt.view(-1).tolist()))
     assert pa.metis_read_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["fp8", "bf16"])
+def test_chunks_beside_decodes_see_what_the_write_in_front_left(fp8):
+    """A mixed step again and again over the same pages: its rows, their pages' scales and the table all
+    change, and the outputs are those of the same call on a GPU at rest."""
+    rng = np.random.default_rng(2)
+    bs, G, r, D = 16, 2, 4, 128
+    lens, q_lens = [300, 40, 90, 200, 130], [250, 1, 60, 1, 130]
+    c = Cache(rng, lens, G, D, bs, spread=0.0, poisoned=False)
+    cu, T = i32(np.concatenate([[0], np.cumsum(q_lens)])), sum(q_lens)
+    slots_host = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, q_lens)])
+    owner = np.repeat(np.arange(5), q_lens)
+    q = gpu(torch.from_numpy(rng.standard_normal((T, G * r, D))).to(BF16))
+    kv = [gpu(torch.from_numpy(rng.standard_normal((T, G, D))).to(BF16)) for _ in range(2)]
+    tables = [c.table, c.table.copy()]
+    for s, n in enumerate(lens):  # the second table: a sequence's pages in another order
+        k = -(-n // bs)
+        tables[1][s, :k] = tables[1][s, :k][::-1]
+    tables = [i32(t) for t in tables]
+    bt = tables[0].clone()
+    cache = [x.clone() for x in c.dev] if fp8 else [torch.zeros(c.nb, bs, G, D, dtype=BF16, device=DEV) for _ in range(2)]
+    slots = [torch.from_numpy(t.cpu().numpy()[owner, slots_host // bs].astype(np.int64) * bs + slots_host % bs).to(DEV)
+             for t in tables]
+    pa.metis_read_status(clear=True)
+    for step in range(24):
+        which = step & 1
+        bt.copy_(tables[which])
+        size = 2.0 ** (step % 7 - 3)
+        rows = [x * size for x in kv]
+        if fp8:
+            pa.metis_reshape_and_cache_fp8(*rows, *cache, cu, bt, c.sl)
+            call = lambda: pa.metis_paged_attn_prefill_chunk_fp8(q, cu, *cache, bt, c.sl, 0.1, max_seq_len=300)[0]
+        else:
+            pa.metis_reshape_and_cache(*rows, *cache, slots[which])
+            call = lambda: pa.metis_paged_attn_prefill_chunk(q, cu, *cache, bt, c.sl, 0.1, max_seq_len=300)[0]
+        out = call()
+        torch.cuda.synchronize()
+        again = call()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)), step
+    assert pa.metis_read_status(clear=True) == 0

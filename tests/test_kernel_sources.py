@@ -35,3 +35,13 @@ def test_dependent_kernels_read_with_ordinary_loads(name):
     if name in ("cache_write.cu", "prefix_cache.cu"):  # some of their kernels are launched behind complete ones only
         text = "\n".join(k for k in re.findall(r"__global__.*?\n}\n", text, re.S) if "pdl_wait" in k)
     assert not READ_ONLY.search(text), READ_ONLY.search(text).group(0)
+
+
+def test_the_chunk_kernel_waits_or_fences_before_it_reads():
+    """Beside decodes the chunk kernel's launch, not a wait of its own, orders it behind the kernels that
+    write its tables and scales."""
+    body = re.search(r"prefill_bf16_kernel\(.*?\n}\n", source("prefill.cu"), re.S).group(0)
+    head = body[:body.index("__syncthreads();")]
+    assert "if (!p.wait_at_exit) pdl_wait();" in head
+    # the warps from 8 on (producers, converters, unit fetcher), but for the one that allocates TMEM
+    assert re.search(r"else if \(warp >= 8 && p\.wait_at_exit\) {\s+__threadfence\(\);", head)
