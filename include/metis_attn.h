@@ -432,14 +432,14 @@ int metis_paged_attn_decode_fp8(const void* q, const void* k_cache, const void* 
  * cache: the same arguments and limits, with the scales behind the codes; dtype
  * METIS_BF16.  The workspace holds at least metis_prefill_workspace_bytes(...); with the
  * metis_prefill_fp8_workspace_bytes(...) bytes of the call's own sizes (more, where its
- * chunks may leave SMs idle) the chunks' work is also split over long sequences' keys.
- * A chunk's query rows
- * enter the products as two e4m3 parts at one power of two each: elements down to 2^-8
+ * chunks may leave SMs idle: up to 4 parts per SM of 2 x 128 rows, 80 MB on 152 SMs at
+ * head_dim 128, 40 MB at 64) the chunks' work is also split over long sequences' keys.
+ * A chunk's query rows enter the products as two e4m3 parts at one power of two each: elements down to 2^-8
  * of the row's largest are exact, smaller ones are off by at most 2^-17 of it.  V
  * enters as bf16, scale included (exact for scales of 2^-124 and more; values past bf16's
  * range as its largest), with softmax weights in bf16 of up to 2^8: sums of V values above
- * 2^119 may overflow to infinity.  NaN in V reaches
- * the rows that see its token, in its column, as no value of an unseen token does.  Sequences with one query and a head ratio
+ * 2^119 may overflow to infinity.  NaN in V reaches the rows that see its token, in its
+ * column; no value of an unseen token reaches a row.  Sequences with one query and a head ratio
  * up to 8 are computed as metis_paged_attn_decode_fp8 computes them.
  */
 int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,

@@ -737,7 +737,7 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 // Warps per CTA, ring depth per warp and CTAs per SM that the registers allow.  Measured on a
 // GB300 (head_dim 128, pages of 16, bf16 queries; items: (sequence, KV head) pairs):
 //   unsplit        4 warps, 3 stages, two CTAs per SM: 64 sequences of 512..4096 tokens, 32/8
-//                  heads, in 53.6 us; 2 stages and three CTAs 60.9 us (fewer bytes in flight
+//                  heads, in 53.6 us (54-56 by box); 2 stages and three CTAs 60.9 us (fewer bytes in flight
 //                  once the long sequences are alone), 8 warps and one CTA 68 us.
 //                  head_dim 64 (half the bytes per unit): 8 warps, 2 stages, two CTAs: the same
 //                  batch in 33.6 us, 4 warps and 3 stages 43.9 us
