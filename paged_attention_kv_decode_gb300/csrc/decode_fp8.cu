@@ -59,7 +59,9 @@ constexpr float kRefDown = 14.f; // softmax reference below the running maximum,
 constexpr float kUndoRefDown = 1.f / 16384.f;  // 2^-kRefDown
 constexpr int kMaxJoin = 8;          // partitions of an item that a cluster takes
 constexpr int kMinJoinTokens = 128;  // ... in a call that asked for none: tokens in each at least
-constexpr int kWide = 12;        // bf16 queries: a V scale this far (log2) below the largest so far stays out of the weights
+// bf16 queries: a page whose V scale is further than this (log2) below the largest so far keeps it
+// out of its weights, which costs a weight 2^-(39 - kWide) of the largest at most
+constexpr int kWide = 12;
 constexpr float kSlack = 16.f;   // bf16 queries: the sums' reference moves when it is exceeded by 2^16
 
 template <int D>
@@ -737,8 +739,8 @@ __device__ __forceinline__ bool decode_fp8_item_f32(const CUtensorMap& tmK, cons
 // Warps per CTA, ring depth per warp and CTAs per SM that the registers allow.  Measured on a
 // GB300 (head_dim 128, pages of 16, bf16 queries; items: (sequence, KV head) pairs):
 //   unsplit        4 warps, 3 stages, two CTAs per SM: 64 sequences of 512..4096 tokens, 32/8
-//                  heads, in 53.6 us (54-56 by box); 2 stages and three CTAs 60.9 us (fewer bytes in flight
-//                  once the long sequences are alone), 8 warps and one CTA 68 us.
+//                  heads, in 53.6 us (54-56 from box to box); 2 stages and three CTAs 60.9 us (fewer
+//                  bytes in flight once the long sequences are alone), 8 warps and one CTA 68 us.
 //                  head_dim 64 (half the bytes per unit): 8 warps, 2 stages, two CTAs: the same
 //                  batch in 33.6 us, 4 warps and 3 stages 43.9 us
 //   few items      up to one per SM: 8 warps, 3 stages: 29 sequences up to 6,000 tokens, 28/4
