@@ -72,6 +72,7 @@ extern "C" {
 #define METIS_STATUS_OUT_OF_PAGES 32u  /* prefix lookup: a new key found the free stack empty */
 #define METIS_STATUS_BAD_OFFSETS  64u  /* an offset outside the call's rows; page keys: cu_pages asks for a
                                           page past its sequence's tokens */
+#define METIS_STATUS_BAD_POSITION 128u /* norm and rotation: a position outside the table's rows */
 
 /*
  * metis_paged_attn_decode -- one query token per sequence over its pages
@@ -326,6 +327,92 @@ int metis_reshape_and_cache(const void* key, const void* value, void* k_cache, v
 int metis_mla_reshape_and_cache(const void* kv_c, const void* k_pe, void* kv_cache,
                                 const int64_t* slot_mapping, int num_tokens, int d_latent, int d_rope,
                                 int block_size, int num_blocks, void* stream);
+
+/*
+ * metis_plan_step -- the index arrays of a step, built on the GPU from the requests'
+ * lengths: what the calls above take as block_table, seq_lens, cu_q_lens and slot_mapping
+ * (the scheduler's block table and lengths of the vllm-metal article, section 4, with the
+ * pages of vLLM's cache manager, vllm-metis 0.1.0 page, "Caches").  Sequence s has
+ * L0 = cached_lens[s] cached tokens and gets n = q_lens[s] new ones:
+ *
+ *   held    = held_blocks[s] (at least ceil(L0 / block_size), which it is without the
+ *             array; at most max_blocks): the pages that its table row already names
+ *   pages   held .. ceil((L0 + n) / block_size) - 1 are new (none if n == 0).  New pages
+ *           are dealt out sequence by sequence and in a sequence's order, the k-th of the
+ *           call being free_stack[*free_count - 1 - k], as metis_prefix_lookup takes them;
+ *           block_table gets the entry, refcount[page] = 1
+ *   cu_q_lens[s + 1] = cu_q_lens[s] + n, cu_q_lens[0] = 0
+ *   row cu_q_lens[s] + i, i < n:  positions = L0 + i,
+ *           slot_mapping = block_table[s][position / block_size] * block_size
+ *                          + position % block_size
+ *   seq_lens[s] = L0 + n;  held_blocks_out[s] = the pages its row names now
+ *   *free_count_out = *free_count less the pages taken
+ *   rows behind the last sequence's, up to num_tokens: slot -1, position 0 (padding)
+ *
+ *   q_lens, cached_lens, held_blocks   int32 [num_seqs] (held_blocks may be NULL)
+ *   block_table   int32 [num_seqs, max_blocks], only new entries are written
+ *   free_stack    int32 [free_capacity], the top at the end;  free_count  int32 [1], read
+ *                 clamped to [0, free_capacity]
+ *   refcount      int32 [num_blocks] or NULL
+ *   seq_lens, held_blocks_out (or NULL), cu_q_lens [num_seqs + 1], positions [num_tokens]
+ *                 int32;  slot_mapping int64 [num_tokens]
+ * seq_lens may be cached_lens, held_blocks_out may be held_blocks and free_count_out may be
+ * free_count (a captured step then advances by itself); other arrays must not overlap.
+ * Contents that the device flags: a negative length counts as 0 (METIS_STATUS_BAD_Q_LEN);
+ * tokens whose row would be num_tokens or more are not planned: they count in no output
+ * (METIS_STATUS_BAD_OFFSETS); tokens past the table row get slot -1
+ * (METIS_STATUS_SEQ_TOO_LONG); with the stack empty a new page's entry and its slots are -1
+ * (METIS_STATUS_OUT_OF_PAGES); so are those of an entry, held or from the stack, outside
+ * [0, num_blocks) (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 is a successful no-op.
+ */
+int metis_plan_step(const int32_t* q_lens, const int32_t* cached_lens, const int32_t* held_blocks,
+                    int32_t* block_table, const int32_t* free_stack, int free_capacity,
+                    const int32_t* free_count, int32_t* refcount, int32_t* seq_lens,
+                    int32_t* held_blocks_out, int32_t* free_count_out, int32_t* cu_q_lens,
+                    int64_t* slot_mapping, int32_t* positions, int num_seqs, int num_tokens,
+                    int block_size, int max_blocks, int num_blocks, void* stream);
+
+/*
+ * metis_qk_norm_rope -- queries and keys of a step's new rows normalised per head and
+ * rotated by their positions, in one pass:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight     over head_dim (weight NULL: y = x)
+ *   for the pairs (a, b) of the first rotary_dim dims and pair index i < rotary_dim / 2:
+ *     out_a = y_a cos_i - y_b sin_i,  out_b = y_b cos_i + y_a sin_i
+ *   (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved != 0
+ *
+ * in fp32, rounded once.  Dims from rotary_dim on are not rotated; 0 rotates none.
+ *
+ *   q, k         [num_tokens, num_heads or num_kv_heads, head_dim], dtype; a token's heads
+ *                are dense, tokens are q_stride / k_stride elements apart (multiples of 16
+ *                bytes), so that q and k may lie side by side in a projection's output
+ *   q_weight, k_weight   [head_dim], dtype, or NULL
+ *   cos_sin      fp32 [max_position, rotary_dim]: cos_i, then sin_i, of each position
+ *   positions    int32 [num_tokens]; outside [0, max_position) the table's row reads as
+ *                zeros (METIS_STATUS_BAD_POSITION)
+ *   q_out, k_out [num_tokens, heads, head_dim] dense; may be q / k where those are dense,
+ *                and must not overlap them otherwise
+ * Supported: dtype METIS_F32 or METIS_BF16; head_dim 64 or 128; rotary_dim a multiple of
+ * 16 up to head_dim; eps >= 0.  num_tokens == 0 is a successful no-op.
+ *
+ * metis_qk_norm_rope_and_cache -- the same, with the keys written into their pages and the
+ * values beside them: what metis_reshape_and_cache(k_out, v, ...) would do, without the
+ * keys' way through memory.  v is [num_tokens, num_kv_heads, head_dim] with v_stride; the
+ * caches, slot_mapping (negative: the row's key and value are not written, its query is
+ * computed all the same) and errors are those of that call.
+ */
+int metis_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                       const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
+                       int num_tokens, int num_heads, int num_kv_heads, int head_dim, int64_t q_stride,
+                       int64_t k_stride, int rotary_dim, int max_position, int interleaved, float eps,
+                       int dtype, void* stream);
+int metis_qk_norm_rope_and_cache(const void* q, const void* k, const void* v, const void* q_weight,
+                                 const void* k_weight, const float* cos_sin, const int32_t* positions,
+                                 void* q_out, void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                 int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int rotary_dim,
+                                 int max_position, int interleaved, float eps, int block_size,
+                                 int num_blocks, int dtype, void* stream);
 
 /*
  * The 8-bit cache.  K and V pages may be held as e4m3 codes (four exponent bits,

@@ -14,12 +14,14 @@ from ._binding import (  # noqa: F401
     SIGNATURES,
     STATUS_BAD_BLOCK_ID,
     STATUS_BAD_OFFSETS,
+    STATUS_BAD_POSITION,
     STATUS_BAD_Q_LEN,
     STATUS_OUT_OF_PAGES,
     STATUS_SEQ_TOO_LONG,
     STATUS_TABLE_FULL,
     STATUS_WAIT_TIMEOUT,
     MetisError,
+    StepPlan,
     load_library,
     metis_decode_workspace_bytes,
     metis_gather_cache_fp8,
@@ -37,11 +39,15 @@ from ._binding import (  # noqa: F401
     metis_paged_attn_prefill_chunk_fp8,
     metis_prefill_fp8_workspace_bytes,
     metis_prefill_workspace_bytes,
+    metis_plan_step,
     metis_prefix_block_hashes,
     metis_prefix_lookup,
     metis_prefix_lookup_workspace_bytes,
     metis_prefix_table_init,
+    metis_qk_norm_rope,
+    metis_qk_norm_rope_and_cache,
     prefix_table_alloc,
+    rope_table,
     split_workspace_views,
     metis_read_status,
     metis_debug_wait_probe,

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -30,6 +30,7 @@ STATUS_BAD_Q_LEN = 8
 STATUS_TABLE_FULL = 16
 STATUS_OUT_OF_PAGES = 32
 STATUS_BAD_OFFSETS = 64
+STATUS_BAD_POSITION = 128
 
 _ERRORS = {
     -1: "METIS_E_NULL",
@@ -56,6 +57,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
+_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes); mirrors include/metis_attn.h
 SIGNATURES = {
@@ -86,6 +88,12 @@ SIGNATURES = {
                                          _f, _i, _i, _vp, _sz, _vp]),
     "metis_paged_attn_prefill_chunk_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                                 _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "metis_plan_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                             _vp]),
+    "metis_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i64, _i64, _i, _i, _i, _f, _i,
+                                _vp]),
+    "metis_qk_norm_rope_and_cache": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i64,
+                                          _i64, _i64, _i, _i, _i, _f, _i, _i, _i, _vp]),
     "metis_prefix_block_hashes": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "metis_prefix_table_init": (_i, [_vp, _vp, _vp, _i, _vp]),
     "metis_prefix_lookup_workspace_bytes": (_sz, [_i]),
@@ -660,6 +668,164 @@ def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor,
     if rc:
         _check(rc)
     return out, lse_out
+
+
+class StepPlan(NamedTuple):
+    """What :func:`metis_plan_step` builds: int32 ``seq_lens`` ``[S]``, ``cu_q_lens`` ``[S + 1]`` and
+    ``positions`` ``[T]``, int64 ``slot_mapping`` ``[T]``, and int32 ``held_blocks`` ``[S]`` (None unless
+    wanted) and ``free_count`` ``[1]``."""
+
+    seq_lens: torch.Tensor
+    cu_q_lens: torch.Tensor
+    positions: torch.Tensor
+    slot_mapping: torch.Tensor
+    held_blocks: Optional[torch.Tensor]
+    free_count: torch.Tensor
+
+
+def metis_plan_step(q_lens: torch.Tensor, cached_lens: torch.Tensor, block_table: torch.Tensor,
+                    free_stack: torch.Tensor, free_count: torch.Tensor, *, block_size: int, num_tokens: int,
+                    num_blocks: int, held_blocks: Optional[torch.Tensor] = None,
+                    refcount: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None,
+                    cu_q_lens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    slot_mapping: Optional[torch.Tensor] = None, held_blocks_out: Optional[torch.Tensor] = None,
+                    free_count_out: Optional[torch.Tensor] = None, stream=None) -> StepPlan:
+    """The index arrays of a step of ``q_lens`` new tokens behind ``cached_lens`` cached ones (int32 ``[S]``):
+    new pages come from the top of ``free_stack`` (``free_count`` int32 ``[1]``) and are entered into
+    ``block_table`` (int32 ``[S, max_blocks]``, in place) and ``refcount`` (int32 ``[num_blocks]``).
+    ``num_tokens`` is the number of rows of the step's tensors: rows behind the new tokens' are padding.
+    Outputs may be passed in; ``seq_lens``, ``held_blocks_out`` and ``free_count_out`` may be the inputs
+    they follow, which a captured step then advances.  Asynchronous."""
+    lib = _lib or load_library()
+    dev = _device_of("q_lens", q_lens, 1)
+    S = q_lens.shape[0]
+    T = int(num_tokens)
+    i32 = torch.int32
+    width, table = _table(dev, block_table, S)
+
+    def output(name, t, dtype, shape):
+        if t is None:
+            t = _empty(shape, dtype, q_lens, stream)
+            return t, t.data_ptr()
+        return t, _on(dev, name, t, dtype, shape)
+
+    if T < 0:
+        raise ValueError("num_tokens must be >= 0")
+    seq_lens, seq_at = output("seq_lens", seq_lens, i32, (S,))
+    cu_q_lens, cu_at = output("cu_q_lens", cu_q_lens, i32, (S + 1,))
+    positions, pos_at = output("positions", positions, i32, (T,))
+    slot_mapping, slot_at = output("slot_mapping", slot_mapping, torch.int64, (T,))
+    free_count_out, left_at = output("free_count_out", free_count_out, i32, (1,))
+    if held_blocks is not None and held_blocks_out is None:
+        held_blocks_out = _empty((S,), i32, q_lens, stream)
+    held_at = None if held_blocks is None else _on(dev, "held_blocks", held_blocks, i32, (S,))
+    held_out_at = None if held_blocks_out is None else _on(dev, "held_blocks_out", held_blocks_out, i32, (S,))
+    if not isinstance(free_stack, torch.Tensor) or free_stack.dim() != 1:
+        raise ValueError("free_stack must be a tensor [free_capacity]")
+    capacity = free_stack.shape[0]
+    rc = lib.metis_plan_step(
+        _on(dev, "q_lens", q_lens, i32, (S,)), _on(dev, "cached_lens", cached_lens, i32, (S,)), held_at, table,
+        _on(dev, "free_stack", free_stack, i32, (capacity,)), capacity, _on(dev, "free_count", free_count, i32, (1,)),
+        None if refcount is None else _on(dev, "refcount", refcount, i32, (num_blocks,)), seq_at, held_out_at, left_at,
+        cu_at, slot_at, pos_at, S, T, int(block_size), width, int(num_blocks), _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return StepPlan(seq_lens, cu_q_lens, positions, slot_mapping, held_blocks_out, free_count_out)
+
+
+def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The table of angles for :func:`metis_qk_norm_rope`: fp32 ``[max_position, rotary_dim]``, position p's
+    row holding the cosines, then the sines, of p * base^(-2 i / rotary_dim), computed in 64 bits."""
+    turn = torch.arange(max_position, dtype=torch.float64)[:, None]
+    turn = turn * float(base) ** (-2.0 * torch.arange(rotary_dim // 2, dtype=torch.float64) / rotary_dim)
+    return torch.cat([turn.cos(), turn.sin()], 1).to(torch.float32).to(device)
+
+
+def _token_rows(dev: int, name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> Tuple[int, int]:
+    """Check rows [T, heads, D] whose tokens may lie apart; returns their address and token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    T, heads, D = shape
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        return _on(dev, name, t, dtype, shape), heads * D  # raises
+    tokens, head, dim = t.stride()
+    if T <= 1:
+        tokens = heads * D  # (the stride of a dimension of one says nothing)
+    if (dim != 1 and D > 1) or (head != D and heads > 1) or tokens < heads * D:
+        raise ValueError(f"{name}: a token's heads must be contiguous, and tokens must not overlap")
+    return t.data_ptr(), tokens
+
+
+def _norm_rope(q, k, q_weight, k_weight, cos_sin, positions):
+    """The checks that both calls share: device, dtype code, sizes and addresses."""
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    T, H, D = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [num_tokens, num_kv_heads, head_dim]")
+    G = k.shape[1]
+    q_at, q_stride = _token_rows(dev, "q", q, q.dtype, (T, H, D))
+    k_at, k_stride = _token_rows(dev, "k", k, q.dtype, (T, G, D))
+    qw = None if q_weight is None else _on(dev, "q_weight", q_weight, q.dtype, (D,))
+    kw = None if k_weight is None else _on(dev, "k_weight", k_weight, q.dtype, (D,))
+    table = pos = None
+    rows = R = 0
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a tensor [max_position, rotary_dim]")
+        rows, R = cos_sin.shape
+        table = _on(dev, "cos_sin", cos_sin, torch.float32, (rows, R))
+        pos = _on(dev, "positions", positions, torch.int32, (T,))
+    return dev, code, (T, H, G, D), (q_at, k_at, qw, kw, table, pos), (q_stride, k_stride), (R, rows)
+
+
+def metis_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.Tensor],
+                       positions: Optional[torch.Tensor], *, q_weight: Optional[torch.Tensor] = None,
+                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                       q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``q`` ``[T, H, D]`` and ``k`` ``[T, G, D]`` (bf16 or fp32; views into a projection's output will do)
+    normalised per head (a weight given) and rotated by ``positions`` (int32 ``[T]``; ``cos_sin`` None: not
+    rotated); returns ``(q_out, k_out)``, which may be ``q`` and ``k`` where those are contiguous."""
+    lib = _lib or load_library()
+    dev, code, (T, H, G, D), (q_at, k_at, qw, kw, table, pos), strides, (R, rows) = _norm_rope(
+        q, k, q_weight, k_weight, cos_sin, positions)
+    if q_out is None:
+        q_out = _empty((T, H, D), q.dtype, q, stream)
+    if k_out is None:
+        k_out = _empty((T, G, D), q.dtype, q, stream)
+    rc = lib.metis_qk_norm_rope(q_at, k_at, qw, kw, table, pos, _on(dev, "q_out", q_out, q.dtype, (T, H, D)),
+                                _on(dev, "k_out", k_out, q.dtype, (T, G, D)), T, H, G, D, *strides, R, rows,
+                                int(bool(interleaved)), float(eps), code, _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return q_out, k_out
+
+
+def metis_qk_norm_rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: Optional[torch.Tensor],
+                                 positions: Optional[torch.Tensor], k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 slot_mapping: torch.Tensor, *, q_weight: Optional[torch.Tensor] = None,
+                                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                                 q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`metis_qk_norm_rope`, the keys and ``v`` ``[T, G, D]`` going into the caches ``[nb, bs, G, D]`` at
+    ``slot_mapping`` (int64 ``[T]``, negative = padding), in place; returns ``q_out``."""
+    lib = _lib or load_library()
+    dev, code, (T, H, G, D), (q_at, k_at, qw, kw, table, pos), (q_stride, k_stride), (R, rows) = _norm_rope(
+        q, k, q_weight, k_weight, cos_sin, positions)
+    v_at, v_stride = _token_rows(dev, "v", v, q.dtype, (T, G, D))
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [num_blocks, block_size, num_kv_heads, head_dim]")
+    nb, bs = k_cache.shape[:2]
+    if q_out is None:
+        q_out = _empty((T, H, D), q.dtype, q, stream)
+    rc = lib.metis_qk_norm_rope_and_cache(
+        q_at, k_at, v_at, qw, kw, table, pos, _on(dev, "q_out", q_out, q.dtype, (T, H, D)),
+        _on(dev, "k_cache", k_cache, q.dtype, (nb, bs, G, D)), _on(dev, "v_cache", v_cache, q.dtype, (nb, bs, G, D)),
+        _on(dev, "slot_mapping", slot_mapping, torch.int64, (T,)), T, H, G, D, q_stride, k_stride, v_stride, R, rows,
+        int(bool(interleaved)), float(eps), bs, nb, code, _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return q_out
 
 
 def metis_prefix_block_hashes(token_ids: torch.Tensor, cu_tokens: torch.Tensor, cu_pages: torch.Tensor,

@@ -33,228 +33,17 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/metis_attn.h"
 #include "common.cuh"
 #include "decode.cuh"
+#include "decode_items.cuh"
 #include "host.h"
 
 namespace metis {
 
 __device__ unsigned int g_status_decode = 0;
-
-// ---------------------------------------------------------------------------
-// bf16 decode: TMA page units + mma.sync
-// ---------------------------------------------------------------------------
-constexpr int kUnit = 16;              // tokens per pipeline unit (one m16 tile)
-constexpr int kBoxBytes = kUnit * 128; // one 16-token x 64-dim bf16 box, 128-byte rows
-
-template <int D>
-struct Bf16DecodeShape {
-  static constexpr int kHalves = D / 64;
-  static constexpr int kStageBytes = 2 * kHalves * kBoxBytes;  // K halves, then V halves
-  static constexpr int kSteps = D / 16;                        // QK k-steps == PV m-tiles
-};
-
-template <int D, int NW, int STAGES>
-constexpr int bf16_decode_smem_bytes() {
-  return 1024 + NW * STAGES * Bf16DecodeShape<D>::kStageBytes + NW * STAGES * 8;
-}
-
-// One work item of the bf16 decode: the tokens [t0, t1) of KV head g of sequence s
-// (query / output row orow), run by NW warps (warp 0 .. NW - 1 of the caller's
-// group; tid = the thread's index in the group) over their NW x STAGES TMA ring at
-// smem with its barriers at bars.  kb: this warp's ring position before the item
-// (ring stages and barrier phases run on across the items of a persistent group),
-// advanced past the item's units.  sync(): a barrier over the group's threads.
-// The combine step reuses the ring: the caller syncs the group before the next
-// item's loads.  Returns false when a wait gave up.
-template <int D, int NW, int STAGES, typename Sync>
-__device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeParams& p,
-                                                 uint8_t* smem, uint64_t* bars, int part, int g, int s, int orow,
-                                                 int t0, int t1, int warp, int lane, int tid, int& kb, Sync sync) {
-  using Shape = Bf16DecodeShape<D>;
-  constexpr int HALVES = Shape::kHalves;
-  constexpr int STAGE_BYTES = Shape::kStageBytes;
-  constexpr int KS = Shape::kSteps;
-
-  // this warp's units: u0 + warp + k * NW, k < n_my
-  const int u0 = t0 / kUnit;
-  const int n_units = (t1 - u0 * kUnit + kUnit - 1) / kUnit;
-  const int n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
-  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
-
-  // Lane l holds the TMA row coordinate (block * bs + slot) of unit k = 32 * batch + l;
-  // -kUnit (a box entirely outside the tensor, read as zeros) marks a bad block id.
-  auto row_coord = [&](int k) -> int {
-    if (k >= n_my) return -kUnit;
-    const int tok = (u0 + warp + k * NW) * kUnit;
-    const int page = tok / p.bs;
-    const int b = checked_block(bt_row, page, p.num_blocks, &g_status_decode);
-    return b < 0 ? -kUnit : b * p.bs + (tok - page * p.bs);
-  };
-  int win_cur = row_coord(lane);
-  int win_next = row_coord(32 + lane);
-  const uint64_t policy = l2_policy_evict_first();
-
-  auto issue = [&](int k) {  // called by all lanes, in order k = 0, 1, 2, ...
-    if (k > 0 && (k & 31) == 0) {
-      win_cur = win_next;
-      win_next = row_coord(k + 32 + lane);
-    }
-    const int row = __shfl_sync(0xffffffffu, win_cur, k & 31);
-    const int st = (kb + k) % STAGES;
-    uint8_t* base = smem + (warp * STAGES + st) * STAGE_BYTES;
-    uint64_t* bar = &bars[warp * STAGES + st];
-    if (lane == 0) mbar_arrive_expect_tx(bar, STAGE_BYTES);
-    __syncwarp();
-    // one box per lane: a single thread issues TMA instructions far slower than several
-    if (lane < 2 * HALVES) {
-      const int h = lane % HALVES;
-      tma_load_3d(base + lane * kBoxBytes, lane < HALVES ? &tmK : &tmV, bar, h * 64, g, row, policy);
-    }
-  };
-
-  // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4, dims 2*(lane%4) (+1, +8, +9)
-  const int q4 = lane & 3, rA = lane >> 2;
-  uint32_t qf[KS][2];
-  {
-    const bool live = rA < p.r;
-    const __nv_bfloat16* qrow =
-        reinterpret_cast<const __nv_bfloat16*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D;
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      qf[kk][0] = live ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 2 * q4) : 0u;
-      qf[kk][1] = live ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 8 + 2 * q4) : 0u;
-    }
-  }
-
-  float o[KS][4];
-#pragma unroll
-  for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2*q4 and 2*q4+1
-  const float sl2 = p.scale_log2;
-
-  const int prologue = n_my < STAGES ? n_my : STAGES;
-  for (int k = 0; k < prologue; ++k) issue(k);
-
-  int k = 0;
-  bool ok = true;
-  for (; k < n_my; ++k) {
-    const int st = (kb + k) % STAGES;
-    const bool landed = mbar_wait(&bars[warp * STAGES + st], ((kb + k) / STAGES) & 1, &g_status_decode);
-    if (!__all_sync(0xffffffffu, landed)) {  // leave the loop together
-      ok = false;
-      break;
-    }
-    const int tok0 = (u0 + warp + k * NW) * kUnit;
-    const int nv = min(kUnit, t1 - tok0);  // valid tokens in this unit, >= 1
-    const uint32_t kbase = smem_u32(smem + (warp * STAGES + st) * STAGE_BYTES);
-    const uint32_t vbase = kbase + HALVES * kBoxBytes;
-
-    // S^T (16 tokens x 8 heads) = K (16 x D) . q^T (D x 8), in two independent
-    // accumulation chains (even / odd k-steps) to halve the dependent-MMA latency
-    float sacc[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      float sacc2[4] = {0.f, 0.f, 0.f, 0.f};
-      const int j = lane >> 3;
-      const int row = ((j & 1) << 3) + (lane & 7);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        const int c = kk * 2 + (j >> 1);
-        const uint32_t addr = kbase + (c >> 3) * kBoxBytes + row * 128 + ((((c & 7) ^ (row & 7))) << 4);
-        uint32_t a0, a1, a2, a3;
-        ldsm_x4(addr, a0, a1, a2, a3);
-        mma_bf16_16816((kk & 1) ? sacc2 : sacc, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sacc[i] += sacc2[i];
-    }
-
-    // online softmax over this unit; the thread holds tokens rA, rA+8 of heads 2*q4, 2*q4+1
-    float s0 = sacc[0] * sl2, s1 = sacc[1] * sl2, s2 = sacc[2] * sl2, s3 = sacc[3] * sl2;
-    if (rA >= nv) s0 = s1 = -INFINITY;
-    if (rA + 8 >= nv) s2 = s3 = -INFINITY;
-    const float mn0 = fmaxf(m0, warp_max_xor(fmaxf(s0, s2), 4));
-    const float mn1 = fmaxf(m1, warp_max_xor(fmaxf(s1, s3), 4));
-    const float al0 = exp2_approx(m0 - mn0), al1 = exp2_approx(m1 - mn1);
-    const float p0 = exp2_approx(s0 - mn0), p1 = exp2_approx(s1 - mn1);
-    const float p2 = exp2_approx(s2 - mn0), p3 = exp2_approx(s3 - mn1);
-    l0 = l0 * al0 + (p0 + p2);
-    l1 = l1 * al1 + (p1 + p3);
-    m0 = mn0;
-    m1 = mn1;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      o[i][0] *= al0;
-      o[i][1] *= al1;
-      o[i][2] *= al0;
-      o[i][3] *= al1;
-    }
-    // P^T (tokens x heads) -> B operand (k = token, n = head) by 8x8 transposes
-    const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p0, p1));
-    const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p2, p3));
-
-    // Rows past the last valid token may hold anything (NaN included): zero
-    // them in the V^T fragments so that 0 * garbage cannot poison O.
-    uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-    if (nv < kUnit) {
-      const int t = 2 * q4;
-      mlo = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
-      mhi = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
-    }
-    // O^T (D x 8 heads) += V^T (D x 16 tokens) . P^T (16 tokens x 8 heads)
-    {
-      const int j = lane >> 3;
-      const int row = ((j >> 1) << 3) + (lane & 7);
-#pragma unroll
-      for (int mt = 0; mt < KS; ++mt) {
-        const int c = mt * 2 + (j & 1);
-        const uint32_t addr = vbase + (c >> 3) * kBoxBytes + row * 128 + ((((c & 7) ^ (row & 7))) << 4);
-        uint32_t a0, a1, a2, a3;
-        ldsm_x4_trans(addr, a0, a1, a2, a3);
-        mma_bf16_16816(o[mt], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
-      }
-    }
-    __syncwarp();
-    if (k + STAGES < n_my) issue(k + STAGES);
-  }
-  if (!ok) {
-    // drain this warp's loads still in flight (bounded) before the ring is reused
-    for (int kk = k + 1; kk < n_my && kk < k + STAGES; ++kk) {
-      const int st = (kb + kk) % STAGES;
-      mbar_wait(&bars[warp * STAGES + st], ((kb + kk) / STAGES) & 1, &g_status_decode);
-    }
-  }
-
-  l0 = warp_sum_xor(l0, 4);
-  l1 = warp_sum_xor(l1, 4);
-  sync();  // every warp is done with its ring
-
-  float* cm = reinterpret_cast<float*>(smem);
-  float* cl = cm + NW * 8;
-  float* co = cl + NW * 8;
-  if (lane < 4) {
-    cm[warp * 8 + 2 * lane] = m0;
-    cm[warp * 8 + 2 * lane + 1] = m1;
-    cl[warp * 8 + 2 * lane] = l0;
-    cl[warp * 8 + 2 * lane + 1] = l1;
-  }
-#pragma unroll
-  for (int mt = 0; mt < KS; ++mt) {
-    const int d0 = mt * 16 + rA;
-    float* c0 = co + ((size_t)warp * D + d0) * 8 + 2 * q4;
-    float* c1 = c0 + 8 * 8;
-    c0[0] = o[mt][0];
-    c0[1] = o[mt][1];
-    c1[0] = o[mt][2];
-    c1[1] = o[mt][3];
-  }
-  sync();
-  combine_and_store<__nv_bfloat16, NW>(p, cm, cl, co, part, g, s, orow, tid);
-  kb += n_my;
-  return ok;
-}
 
 template <int D, int NW, int STAGES>
 __global__ void __launch_bounds__(NW * 32) decode_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -293,19 +82,12 @@ __global__ void __launch_bounds__(NW * 32) decode_bf16_kernel(const __grid_const
   }
   __syncthreads();
   int kb = 0;
-  decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, smem, bars, part, g, s, orow, t0, t1, warp, lane, threadIdx.x, kb,
-                                  [] { __syncthreads(); });
+  decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, smem, bars, g, s, orow, RangeSpan{t0, t1}, warp, lane, kb,
+                                  &g_status_decode, [] { __syncthreads(); },
+                                  [&](const float* cm, const float* cl, const float* co) {
+                                    combine_and_store<__nv_bfloat16, NW>(p, cm, cl, co, part, g, s, orow, threadIdx.x);
+                                  });
 }
-
-// bf16 decode configuration: warps per CTA and ring depth per warp.
-#ifndef METIS_DECODE_WARPS
-#define METIS_DECODE_WARPS 4
-#endif
-#ifndef METIS_DECODE_STAGES
-#define METIS_DECODE_STAGES 3
-#endif
-constexpr int kBf16Warps = METIS_DECODE_WARPS;
-constexpr int kBf16Stages = METIS_DECODE_STAGES;
 
 // ---------------------------------------------------------------------------
 // the decodes of a mixed chunked-prefill batch, beside the chunk kernel
@@ -324,10 +106,11 @@ constexpr int dec_beside_smem_bytes() {
   return need > 116 * 1024 ? need : 116 * 1024;  // never two CTAs on one SM
 }
 
-template <int D>
+// WINDOW: a query sees the last `window` and the first `sinks` tokens of its sequence.
+template <int D, bool WINDOW>
 __global__ void __launch_bounds__(kDecGroups * kBf16Warps * 32, 1)
     decode_rows_beside_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                              const DecodeParams p, const int* n_ctas, int* next_item) {
+                              const DecodeParams p, const int* n_ctas, int* next_item, int window, int sinks) {
   constexpr int NW = kBf16Warps, STAGES = kBf16Stages, GT = NW * 32;
   constexpr int STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
   static_assert(NW * (64 + D * 32) <= NW * STAGES * STAGE_BYTES, "combine area must fit in the ring");
@@ -391,109 +174,35 @@ __global__ void __launch_bounds__(kDecGroups * kBf16Warps * 32, 1)
     if (!decode_range<__nv_bfloat16>(p, 0, g, s, orow, t0, t1, tid, GT, &g_status_decode)) continue;
     // A wait that gave up (flagged) is seen by its warp only: every warp of the group
     // still reaches the item's barriers and the next one above, where they all stop.
-    if (!decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, gsmem, bars, 0, g, s, orow, t0, t1, warp, lane, tid, kb, gsync) &&
-        lane == 0)
-      gave_up[grp] = 1;
+    auto item = [&](const auto& span) {
+      return decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, gsmem, bars, g, s, orow, span, warp, lane, kb,
+                                             &g_status_decode, gsync,
+                                             [&](const float* cm, const float* cl, const float* co) {
+                                               combine_and_store<__nv_bfloat16, NW>(p, cm, cl, co, 0, g, s, orow, tid);
+                                             });
+    };
+    bool fine;
+    if constexpr (WINDOW)
+      fine = item(window_span(t1, window, sinks));
+    else
+      fine = item(RangeSpan{t0, t1});
+    if (!fine && lane == 0) gave_up[grp] = 1;
   }
 }
 
 // ---------------------------------------------------------------------------
 // fp32 decode on FMA units
 // ---------------------------------------------------------------------------
-constexpr int kF32Warps = 8;
-
 template <int D>
 __global__ void __launch_bounds__(kF32Warps * 32) decode_f32_kernel(const float* k_cache,
                                                                      const float* v_cache,
                                                                      const DecodeParams p) {
-  constexpr int DPL = D / 32;  // dims per lane
   pdl_launch_dependents();
   pdl_wait();  // inputs are read after the previous grid in the stream has completed
-  __shared__ float cm[kF32Warps * 8], cl[kF32Warps * 8];
-  __shared__ float co[kF32Warps * D * 8];
-
   const int part = blockIdx.x, g = blockIdx.y, s = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int t0, t1;
   if (!decode_range<float>(p, part, g, s, s, t0, t1, threadIdx.x, blockDim.x, &g_status_decode)) return;
-
-  const float* q = reinterpret_cast<const float*>(p.q) + ((size_t)s * p.H + (size_t)g * p.r) * D;
-  float qv[8][DPL];
-#pragma unroll
-  for (int h = 0; h < 8; ++h)
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) qv[h][i] = h < p.r ? q[h * D + lane * DPL + i] * p.scale_log2 : 0.f;
-
-  float m[8], l[8], o[8][DPL];
-#pragma unroll
-  for (int h = 0; h < 8; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) o[h][i] = 0.f;
-  }
-  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
-  const size_t row_stride = (size_t)p.G * D;
-  // The warp's tokens t0 + warp, + kF32Warps, ... in groups of kF32Batch: the block ids
-  // and K/V rows of a group are loaded together, then folded in one at a time in token
-  // order (the same order as without grouping).
-  constexpr int kF32Batch = D == 64 ? 8 : 4;
-  for (int tb = t0 + warp; tb < t1; tb += kF32Batch * kF32Warps) {
-    float kv[kF32Batch][DPL], vv[kF32Batch][DPL];
-#pragma unroll
-    for (int u = 0; u < kF32Batch; ++u) {
-      const int t = tb + u * kF32Warps;
-      int b = -1, page = 0;
-      if (t < t1) {
-        page = t / p.bs;
-        b = checked_block(bt_row, page, p.num_blocks, &g_status_decode);
-      }
-      if (b >= 0) {
-        const size_t off = ((size_t)b * p.bs + (t - page * p.bs)) * row_stride + (size_t)g * D + lane * DPL;
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) {
-          kv[u][i] = k_cache[off + i];
-          vv[u][i] = v_cache[off + i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) kv[u][i] = vv[u][i] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kF32Batch; ++u) {
-      if (tb + u * kF32Warps >= t1) break;
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        if (h < p.r) {
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < DPL; ++i) dot = fmaf(qv[h][i], kv[u][i], dot);
-          dot = warp_sum_xor(dot, 1);
-          const float mn = fmaxf(m[h], dot);
-          const float al = exp2_approx(m[h] - mn);
-          const float pr = exp2_approx(dot - mn);
-          l[h] = l[h] * al + pr;
-#pragma unroll
-          for (int i = 0; i < DPL; ++i) o[h][i] = fmaf(pr, vv[u][i], o[h][i] * al);
-          m[h] = mn;
-        }
-      }
-    }
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      cm[warp * 8 + h] = m[h];
-      cl[warp * 8 + h] = l[h];
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < 8; ++h)
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) co[((size_t)warp * D + lane * DPL + i) * 8 + h] = o[h][i];
-  __syncthreads();
-  combine_and_store<float, kF32Warps>(p, cm, cl, co, part, g, s, s, threadIdx.x);
+  decode_f32_item<D>(k_cache, v_cache, p, part, g, s, RangeSpan{t0, t1}, &g_status_decode);
 }
 
 // ---------------------------------------------------------------------------
@@ -800,20 +509,6 @@ static int launch_merge(const float* part_out, const float* part_lse, const int3
   return launch_merge_ex(part_out, part_lse, seq_lens, P, out, lse_out, S, H, D, max_parts, out_dtype, 0, st);
 }
 
-// TMA maps of the K and V caches: 16-token x 64-dim boxes of one KV head.
-template <int D>
-static int encode_kv_maps(const DecodeParams& p, const void* k_cache, const void* v_cache, CUtensorMap* tmK,
-                          CUtensorMap* tmV) {
-  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.num_blocks * p.bs};
-  const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2};
-  const uint32_t box[3] = {64, 1, (uint32_t)kUnit};
-  int rc = encode_tiled(tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, dims, strides, box,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc) return rc;
-  return encode_tiled(tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int D>
 static int launch_bf16(const DecodeParams& p, const void* k_cache, const void* v_cache, dim3 grid, cudaStream_t st) {
   CUtensorMap tmK, tmV;
@@ -828,25 +523,25 @@ static int launch_bf16(const DecodeParams& p, const void* k_cache, const void* v
                           p);
 }
 
-template <int D>
+template <int D, bool WINDOW>
 static int launch_beside(const DecodeParams& p, const void* k_cache, const void* v_cache, const int* n_ctas,
-                         int* next_item, int grid, cudaStream_t st) {
+                         int* next_item, int window, int sinks, int grid, cudaStream_t st) {
   CUtensorMap tmK, tmV;
   int rc = encode_kv_maps<D>(p, k_cache, v_cache, &tmK, &tmV);
   if (rc) return rc;
   constexpr int smem = dec_beside_smem_bytes<D>();
   static int done = 0;
-  auto kern = decode_rows_beside_kernel<D>;
+  auto kern = decode_rows_beside_kernel<D, WINDOW>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   return launch_dependent(kern, dim3((unsigned)grid), dim3(kDecGroups * kBf16Warps * 32), (size_t)smem, st,
-                          "decode_rows_beside_kernel launch", tmK, tmV, p, n_ctas, next_item);
+                          "decode_rows_beside_kernel launch", tmK, tmV, p, n_ctas, next_item, window, sinks);
 }
 
 int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                               const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
                               int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
-                              const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
+                              int window, int sinks, const int* n_ctas, int* next_item, int grid, cudaStream_t st) {
   DecodeParams p;
   p.q = q;
   p.block_table = block_table;
@@ -869,8 +564,14 @@ int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_
   p.cap = cap;
   p.rows = rows;
   p.T = T;
-  return D == 64 ? launch_beside<64>(p, k_cache, v_cache, n_ctas, next_item, grid, st)
-                 : launch_beside<128>(p, k_cache, v_cache, n_ctas, next_item, grid, st);
+  auto launch = [&](auto dim, auto windowed) {
+    return launch_beside<decltype(dim)::value, decltype(windowed)::value>(p, k_cache, v_cache, n_ctas, next_item,
+                                                                          window, sinks, grid, st);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (window) return D == 64 ? launch(D64{}, std::true_type{}) : launch(D128{}, std::true_type{});
+  return D == 64 ? launch(D64{}, std::false_type{}) : launch(D128{}, std::false_type{});
 }
 
 }  // namespace metis

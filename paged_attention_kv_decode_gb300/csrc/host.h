@@ -98,11 +98,12 @@ int launch_merge_split_rows(const float* part_out, const float* part_lse, const 
 // grid of `grid` CTAs, of which the first *n_ctas (device value, written by the prefill
 // schedule kernel before this grid reads it) take (sequence, KV head) items from the counter
 // *next_item (zeroed by that kernel); the others exit at once.  Every CTA lets the next grid
-// launch only after waiting for the previous one.
+// launch only after waiting for the previous one.  window > 0: a query sees the last `window` and the
+// first `sinks` tokens of its sequence.
 int launch_decode_rows_beside(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                               const int32_t* seq_lens, const int32_t* rows, int T, void* out, float* lse_out, int S,
                               int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
-                              const int* n_ctas, int* next_item, int grid, cudaStream_t st);
+                              int window, int sinks, const int* n_ctas, int* next_item, int grid, cudaStream_t st);
 
 // The same for an 8-bit cache (decode_fp8.cu).
 struct Fp8Cache {
@@ -124,5 +125,7 @@ int cache_status(uint32_t* bits, int clear);
 int prefix_status(uint32_t* bits, int clear);
 int fp8_status(uint32_t* bits, int clear);
 int decode_fp8_status(uint32_t* bits, int clear);
+int plan_status(uint32_t* bits, int clear);
+int rope_status(uint32_t* bits, int clear);
 
 }  // namespace metis

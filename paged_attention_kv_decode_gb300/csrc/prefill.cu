@@ -1682,7 +1682,7 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
                                            scale, pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
     return launch_decode_rows_beside(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, num_tokens, out, lse_out,
                                      num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
-                                     scale, pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
+                                     scale, pp.cap, 0, 0, pp.dec_ctas, pp.dec_next, sms, st);
   };
   auto launch = [&](auto dim, auto kv8, auto split) {
     return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value>(

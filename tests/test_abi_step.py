@@ -1,0 +1,87 @@
+"""Refusals of the step-planning and norm/rotation calls, on the host (no GPU; nothing is launched)."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_attention_kv_decode_gb300 as pa
+from test_abi import FAKE, lib  # noqa: F401
+
+vp = lambda x: None if x is None else ctypes.c_void_p(x)
+
+
+def plan(lib, **kw):
+    a = dict(q=FAKE, cached=FAKE, held=None, bt=FAKE, stack=FAKE, cap=8, count=FAKE, refs=None, sl=FAKE, ho=None,
+             left=FAKE, cu=FAKE, slots=FAKE, pos=FAKE, S=4, T=16, bs=16, mb=8, nb=64)
+    a.update(kw)
+    return lib.metis_plan_step(vp(a["q"]), vp(a["cached"]), vp(a["held"]), vp(a["bt"]), vp(a["stack"]), a["cap"],
+                               vp(a["count"]), vp(a["refs"]), vp(a["sl"]), vp(a["ho"]), vp(a["left"]), vp(a["cu"]),
+                               vp(a["slots"]), vp(a["pos"]), a["S"], a["T"], a["bs"], a["mb"], a["nb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(bt=None), -1), (dict(stack=None), -1), (dict(count=None), -1), (dict(cu=None), -1),
+    (dict(slots=None), -1), (dict(left=None), -1), (dict(S=-1), -2), (dict(T=-1), -2), (dict(bs=0), -2), (dict(mb=0), -2),
+    (dict(nb=0), -2), (dict(cap=-1), -2), (dict(mb=1 << 28, bs=16), -2), (dict(slots=FAKE + 4), -4),
+    (dict(held=FAKE + 2), -4), (dict(refs=FAKE + 1), -4), (dict(bt=FAKE + 2), -4),
+])
+def test_plan_rejects(lib, kw, code):  # noqa: F811
+    assert plan(lib, **kw) == code
+    assert pa.metis_last_error() != ""
+
+
+def test_plan_of_no_sequences_is_a_no_op(lib):  # noqa: F811
+    assert plan(lib, S=0) == 0
+
+
+def rope(lib, cache=True, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, qw=FAKE, kw=FAKE, cs=FAKE, pos=FAKE, qo=FAKE + 4096, kc=FAKE, vc=FAKE, slots=FAKE, n=4,
+             H=8, G=2, D=128, qs=1024, ks=256, vs=256, R=128, P=100, il=0, eps=1e-6, bs=16, nb=64, dt=pa.METIS_BF16)
+    a.update(kw)
+    head = (vp(a["q"]), vp(a["k"]))
+    mid = (vp(a["qw"]), vp(a["kw"]), vp(a["cs"]), vp(a["pos"]), vp(a["qo"]), vp(a["kc"]))
+    size = (a["n"], a["H"], a["G"], a["D"], a["qs"], a["ks"])
+    tail = (a["R"], a["P"], a["il"], a["eps"])
+    if cache:
+        return lib.metis_qk_norm_rope_and_cache(*head, vp(a["v"]), *mid, vp(a["vc"]), vp(a["slots"]), *size, a["vs"], *tail,
+                                                a["bs"], a["nb"], a["dt"], None)
+    return lib.metis_qk_norm_rope(*head, *mid, *size, *tail, a["dt"], None)
+
+
+@pytest.mark.parametrize("cache", [True, False])
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(k=None), -1), (dict(cs=None), -1), (dict(pos=None), -1), (dict(qo=None), -1), (dict(n=-1), -2),
+    (dict(H=0), -2), (dict(P=0), -2), (dict(D=96), -3), (dict(R=24), -3), (dict(R=144), -3), (dict(dt=3), -3),
+    (dict(eps=-1.0), -2), (dict(eps=float("nan")), -2), (dict(qs=1020), -2), (dict(qs=1028), -4), (dict(ks=8), -2),
+    (dict(q=FAKE + 8), -4), (dict(qw=FAKE + 2), -4), (dict(pos=FAKE + 1), -4), (dict(qo=FAKE, qs=2048), -2),
+])
+def test_norm_rope_rejects(lib, cache, kw, code):  # noqa: F811
+    assert rope(lib, cache, **kw) == code
+    assert pa.metis_last_error() != ""
+
+
+@pytest.mark.parametrize("kw,code", [(dict(v=None), -1), (dict(slots=None), -1), (dict(vc=None), -1), (dict(bs=0), -2),
+                                     (dict(nb=0), -2), (dict(vs=8), -2), (dict(slots=FAKE + 4), -4)])
+def test_norm_rope_and_cache_rejects(lib, kw, code):  # noqa: F811
+    assert rope(lib, True, **kw) == code
+
+
+def test_norm_rope_of_no_rows_is_a_no_op(lib):  # noqa: F811
+    assert rope(lib, True, n=0) == 0 and rope(lib, False, n=0) == 0
+
+
+def test_binding_refuses_cpu_tensors(lib):  # noqa: F811
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_plan_step(i, i, i.view(1, 2), i, i[:1], block_size=16, num_tokens=2, num_blocks=4)
+    x = torch.zeros(2, 1, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.metis_qk_norm_rope(x, x, None, None)
+
+
+def test_rope_table_on_the_host():
+    t = pa.rope_table(100, 16, base=500.0, device="cpu")
+    assert t.shape == (100, 16) and t.dtype == torch.float32
+    angle = 99 * 500.0 ** (-2 * 5 / 16)
+    assert abs(t[99, 5].item() - torch.tensor(angle, dtype=torch.float64).cos().item()) <= 2 ** -24
+    assert abs(t[99, 13].item() - torch.tensor(angle, dtype=torch.float64).sin().item()) <= 2 ** -24
