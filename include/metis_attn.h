@@ -223,6 +223,38 @@ int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q_lens,
 size_t metis_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_heads, int num_kv_heads);
 
 /*
+ * Attention with a sliding window and a few first tokens that stay visible: of the keys
+ * t <= p that a query at position p has before it (its own among them), it sees those with
+ * t > p - window or t < sinks.
+ *
+ * metis_paged_attn_decode_window -- metis_paged_attn_decode with a window: the query of
+ * sequence s sees its last `window` and its first `sinks` tokens.  Pages that hold none of
+ * them are not read and need not exist: their table entries may be anything (pages given
+ * back, -1), and so may other tokens' slots of the pages that are read.  An item that would
+ * leave SMs idle is shared by a cluster of CTAs and joined in the same launch: no
+ * partition_size, no workspace.  Arguments otherwise as there; num_heads / num_kv_heads may
+ * be any ratio up to 8; window >= 1, sinks >= 0 (either may exceed the length).
+ *
+ * metis_paged_attn_prefill_chunk_window -- metis_paged_attn_prefill_chunk with a window:
+ * each query row sees its own window, and single-token sequences are decoded as by the call
+ * above.  Pages without a token that a query of the call sees are not read.  A value of a
+ * token that a row does not see (NaN and infinities included) does not reach it.  Arguments,
+ * limits and workspace (metis_prefill_workspace_bytes) as there.
+ */
+int metis_paged_attn_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                   float* lse_out, int num_seqs, int num_heads, int num_kv_heads,
+                                   int head_dim, int block_size, int max_blocks, int num_blocks, int dtype,
+                                   float scale, int window, int sinks, int max_seq_len, void* stream);
+int metis_paged_attn_prefill_chunk_window(const void* q, const int32_t* cu_q_lens, const void* k_cache,
+                                          const void* v_cache, const int32_t* block_table,
+                                          const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                                          int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int max_blocks, int num_blocks, int dtype,
+                                          float scale, int window, int sinks, int max_seq_len,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * metis_mla_decode -- multi-head latent attention decode over a paged latent
  * cache (the MLA kernel of the vllm-metal article, section 3, fed by the block
  * table and sequence lengths of section 4).

@@ -24,3 +24,4 @@ from .prefix_cache import block_hashes, lookup_or_allocate, mix64  # noqa: F401,
 from .cache_fp8 import E4M3_VALUES, dequantize, encode_e4m3, quantize_pages, scale_byte, write_cache  # noqa: F401,E402
 from .norm_rope import norm_rope  # noqa: F401,E402
 from .step_plan import plan_step  # noqa: F401,E402
+from .window import paged_window, paged_window_decode, window_tokens  # noqa: F401,E402

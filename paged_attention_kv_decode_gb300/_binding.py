@@ -88,6 +88,10 @@ SIGNATURES = {
                                          _f, _i, _i, _vp, _sz, _vp]),
     "metis_paged_attn_prefill_chunk_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                                 _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "metis_paged_attn_decode_window": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i,
+                                            _i, _i, _vp]),
+    "metis_paged_attn_prefill_chunk_window": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                                                   _i, _i, _f, _i, _i, _i, _vp, _sz, _vp]),
     "metis_plan_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                              _vp]),
     "metis_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i64, _i64, _i, _i, _i, _f, _i,
@@ -665,6 +669,72 @@ def metis_paged_attn_prefill_chunk_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor,
     rc = lib.metis_paged_attn_prefill_chunk_fp8(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width, nb,
                                                 code, float(scale), int(max_seq_len), w_at, w_bytes,
                                                 _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return out, lse_out
+
+
+def _paged_cache(dev: int, q: torch.Tensor, k_cache, v_cache):
+    """Check a cache of q's type [nb, bs, G, D]; returns its sizes and the two addresses."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [num_blocks, block_size, num_kv_heads, head_dim]")
+    shape = k_cache.shape
+    return tuple(shape), (_on(dev, "k_cache", k_cache, q.dtype, shape), _on(dev, "v_cache", v_cache, q.dtype, shape))
+
+
+def metis_paged_attn_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float, window: int,
+                                   sinks: int = 0, *, out: Optional[torch.Tensor] = None,
+                                   lse_out: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+                                   stream=None, want_lse: bool = False) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Paged decode over each sequence's last ``window`` and first ``sinks`` tokens (bf16 or fp32); returns
+    ``(out, lse_out)``.  ``max_seq_len=None`` reads seq_lens (a sync)."""
+    lib = _lib or load_library()
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    (nb, bs, G, D), cache = _paged_cache(dev, q, k_cache, v_cache)
+    S, H = q.shape[0], q.shape[1]
+    q_at = _on(dev, "q", q, q.dtype, (S, H, D))
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    rc = lib.metis_paged_attn_decode_window(q_at, *cache, table, lens, o_at, l_at, S, H, G, D, bs, width, nb, code,
+                                            float(scale), int(window), int(sinks), int(max_seq_len),
+                                            _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return out, lse_out
+
+
+def metis_paged_attn_prefill_chunk_window(q: torch.Tensor, cu_q_lens: torch.Tensor, k_cache: torch.Tensor,
+                                          v_cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                          scale: float, window: int, sinks: int = 0, *,
+                                          out: Optional[torch.Tensor] = None, lse_out: Optional[torch.Tensor] = None,
+                                          max_seq_len: Optional[int] = None,
+                                          workspace: Optional[torch.Tensor] = None, stream=None,
+                                          want_lse: bool = False):
+    """Chunked prefill (+ single-token decodes) in which a query sees the last ``window`` tokens up to its
+    own and the first ``sinks``; returns ``(out, lse_out)``."""
+    lib = _lib or load_library()
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    (nb, bs, G, D), cache = _paged_cache(dev, q, k_cache, v_cache)
+    T, H = q.shape[0], q.shape[1]
+    q_at = _on(dev, "q", q, q.dtype, (T, H, D))
+    S = _num_seqs(seq_lens)
+    cu = _on(dev, "cu_q_lens", cu_q_lens, torch.int32, (S + 1,))
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    need = metis_prefill_workspace_bytes(S, T, H, G) if workspace is None else 0
+    workspace, w_at, w_bytes = _workspace(dev, q, workspace, max(need, 256), stream)
+    rc = lib.metis_paged_attn_prefill_chunk_window(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width,
+                                                   nb, code, float(scale), int(window), int(sinks), int(max_seq_len),
+                                                   w_at, w_bytes, _stream_of(dev, stream))
     if rc:
         _check(rc)
     return out, lse_out

@@ -49,8 +49,10 @@ struct RangeSpan {
     return (t1 - t0 / kUnit * kUnit + kUnit - 1) / kUnit;
   }
   __host__ __device__ __forceinline__ int token(int i) const { return (t0 / kUnit + i) * kUnit; }  // first of unit i
-  __host__ __device__ __forceinline__ int count() const { return t1 - t0; }
-  __host__ __device__ __forceinline__ int nth(int i) const { return t0 + i; }
+  // the tokens one by one: nth(begin()) .. nth(end() - 1)
+  __host__ __device__ __forceinline__ int begin() const { return t0; }
+  __host__ __device__ __forceinline__ int end() const { return t1; }
+  __host__ __device__ __forceinline__ int nth(int i) const { return i; }
 };
 
 // The tokens [0, h0) and [h1, t1): a sequence's first ones and its recent ones.  Only units with such
@@ -67,7 +69,8 @@ struct WindowSpan {
     return (i < low_units ? i : i + skip) * kUnit;
   }
   __host__ __device__ __forceinline__ bool hidden(int t) const { return t >= h0 && t < h1; }
-  __host__ __device__ __forceinline__ int count() const { return h0 + t1 - h1; }
+  __host__ __device__ __forceinline__ int begin() const { return 0; }
+  __host__ __device__ __forceinline__ int end() const { return h0 + t1 - h1; }
   __host__ __device__ __forceinline__ int nth(int i) const { return i < h0 ? i : i - h0 + h1; }
   // part `part` of `parts` equal ones (whole units); false: it is empty
   __host__ __device__ __forceinline__ bool take(int part, int parts) {
@@ -303,6 +306,107 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
 }
 
 // ---------------------------------------------------------------------------
+// joining the parts of an item
+// ---------------------------------------------------------------------------
+constexpr int kMaxParts = 8;  // of an item: the CTAs of a cluster
+
+// One row's running result: a sum of o_i 2^(x_i - M) and of 2^(x_i - M), x_i the lse of part i in log2
+// units and o_i its normalised values.
+struct JoinedRow {
+  float M = -INFINITY, W = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  __device__ __forceinline__ void add(float x, const float4& v) {
+    if (x == -INFINITY) return;  // an empty part: its values may be anything
+    const float top = fmaxf(M, x), keep = exp2_approx(M - top), w = exp2_approx(x - top);  // (NaN stays, in W)
+    M = top;
+    W = fmaf(W, keep, w);
+    a0 = fmaf(a0, keep, w * v.x);
+    a1 = fmaf(a1, keep, w * v.y);
+    a2 = fmaf(a2, keep, w * v.z);
+    a3 = fmaf(a3, keep, w * v.w);
+  }
+};
+
+// What else joins a row: nothing.
+struct NoParts {
+  __device__ __forceinline__ void add(JoinedRow&, int, int) const {}
+};
+
+// The item's `n` parts that hold tokens, rows o [r][D] and their lse (natural log) in the shared memory
+// of the CTAs 0 .. n - 1 of this cluster, and `more` (add(row, h, d) joins what it holds for dims
+// d .. d + 3 of query head h of the group).  Each of the cluster's `parts` CTAs writes a share of the rows.
+template <int D, typename OutT, int NT, typename More>
+__device__ __forceinline__ void join_parts_of_item(const DecodeParams& p, const float* o, const float* lse, int part,
+                                                   int parts, int n, int g, int orow, const More& more) {
+  for (int idx = part * NT + threadIdx.x; idx < p.r * (D / 4); idx += parts * NT) {
+    const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+    JoinedRow row;
+    float x[kMaxParts];
+    float4 v[kMaxParts];
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+      x[i] = -INFINITY;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        x[i] = ld_cluster_f32(dsmem_map(smem_u32(lse + h), i)) * kLog2e;
+        v[i] = ld_cluster_f32x4(dsmem_map(smem_u32(o + h * D + d), i));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) row.add(x[i], v[i]);
+    more.add(row, h, d);
+    const bool empty = row.W == 0.f;  // no part, or none with a token
+    const float inv = empty ? 0.f : 1.f / row.W;
+    const size_t at = (size_t)orow * p.H + g * p.r + h;
+    store4<OutT>(reinterpret_cast<OutT*>(p.out) + at * D + d, row.a0 * inv, row.a1 * inv, row.a2 * inv, row.a3 * inv);
+    if (d == 0 && p.lse_out) p.lse_out[at] = empty ? -INFINITY : (row.M + log2f(row.W)) * kLn2;
+  }
+}
+
+// One of `parts` CTAs (a cluster along y where there are several) that share an item of one
+// (sequence, KV head): its part of the units of `span`, then the join.  `has`: the sequence has
+// tokens in the span.  The ring holds the partial: o, then the lse, behind the warps' states.
+template <int D, int NW, int STAGES, typename More>
+__device__ __forceinline__ void decode_joined_item(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                                   const DecodeParams& p, uint8_t* smem, uint64_t* bars, int g, int s,
+                                                   int part, int parts, bool has, WindowSpan span,
+                                                   unsigned int* status, const More& more) {
+  constexpr int STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
+  static_assert(NW * (64 + D * 32) + 8 * D * 4 + 32 <= NW * STAGES * STAGE_BYTES, "the partial must fit in the ring");
+  float* jo = reinterpret_cast<float*>(smem + NW * (64 + D * 32));
+  float* jl = jo + 8 * D;
+  int n = 0, kb = 0;
+  if (has) {
+    const int len = (span.n + parts - 1) / parts;
+    n = (span.n + len - 1) / len;  // parts with units
+    if (span.take(part, parts))
+      decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, smem, bars, g, s, s, span, threadIdx.x >> 5, threadIdx.x & 31, kb,
+                                      status, [] { __syncthreads(); },
+                                      [&](const float* cm, const float* cl, const float* co) {
+                                        DecodeParams local{};  // one item's partial, in shared memory
+                                        local.D = D;
+                                        local.r = local.H = p.r;
+                                        local.partition_size = 1;
+                                        local.max_parts = 1;
+                                        local.part_out = jo;
+                                        local.part_lse = jl;
+                                        combine_and_store<__nv_bfloat16, NW>(local, cm, cl, co, 0, 0, 0, 0,
+                                                                             threadIdx.x);
+                                      });
+  }
+  if (parts > 1) {
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  join_parts_of_item<D, __nv_bfloat16, NW * 32>(p, jo, jl, part, parts, n, g, s, more);
+  if (parts > 1) {
+    __syncwarp();
+    cluster_sync_all();  // nobody leaves while its partial may be read
+  }
+}
+
+// ---------------------------------------------------------------------------
 // fp32 decode on FMA units
 // ---------------------------------------------------------------------------
 constexpr int kF32Warps = 8;
@@ -337,14 +441,14 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
   // and K/V rows of a group are loaded together, then folded in one at a time in token
   // order (the same order as without grouping).
   constexpr int kF32Batch = D == 64 ? 8 : 4;
-  const int n = span.count();
-  for (int ib = warp; ib < n; ib += kF32Batch * kF32Warps) {
+  const int end = span.end();
+  for (int ib = span.begin() + warp; ib < end; ib += kF32Batch * kF32Warps) {
     float kv[kF32Batch][DPL], vv[kF32Batch][DPL];
 #pragma unroll
     for (int u = 0; u < kF32Batch; ++u) {
       const int i = ib + u * kF32Warps;
       int b = -1, page = 0, t = 0;
-      if (i < n) {
+      if (i < end) {
         t = span.nth(i);
         page = t / p.bs;
         b = checked_block(bt_row, page, p.num_blocks, status);
@@ -363,7 +467,7 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
     }
 #pragma unroll
     for (int u = 0; u < kF32Batch; ++u) {
-      if (ib + u * kF32Warps >= n) break;
+      if (ib + u * kF32Warps >= end) break;
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
         if (h < p.r) {

@@ -117,6 +117,24 @@ int launch_decode_fp8_rows_beside(const void* q, const Fp8Cache& cache, const in
                                   int H, int G, int D, int bs, int max_blocks, int num_blocks, float scale, int cap,
                                   const int* n_ctas, int* next_item, int grid, cudaStream_t st);
 
+// The sizes that a bf16 or fp32 decode takes (head ratios up to 8).  Returns METIS_OK or an error code.
+inline int check_decode_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                              int max_blocks, int num_blocks, int max_seq_len, float scale) {
+  if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks <= 0 || num_blocks <= 0 ||
+      max_seq_len <= 0)
+    return fail(METIS_E_SHAPE, "sizes must be positive");
+  if (num_heads % num_kv_heads) return fail(METIS_E_SHAPE, "num_heads %% num_kv_heads != 0");
+  if (num_seqs > 65535 || num_kv_heads > 65535) return fail(METIS_E_SHAPE, "num_seqs and num_kv_heads must be <= 65535");
+  if ((long long)max_blocks * block_size > 0x7fffffffLL || (long long)num_blocks * block_size > 0x7fffffffLL)
+    return fail(METIS_E_SHAPE, "max_blocks * block_size and num_blocks * block_size must fit in int32");
+  if (head_dim != 64 && head_dim != 128) return fail(METIS_E_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(METIS_E_UNSUPPORTED, "block_size must be 16, 32 or 64");
+  if (num_heads / num_kv_heads > 8) return fail(METIS_E_UNSUPPORTED, "num_heads / num_kv_heads must be <= 8");
+  if (!(scale == scale)) return fail(METIS_E_SHAPE, "scale is NaN");
+  return METIS_OK;
+}
+
 // Per-translation-unit device status words.
 int decode_status(uint32_t* bits, int clear);
 int prefill_status(uint32_t* bits, int clear);
@@ -127,5 +145,6 @@ int fp8_status(uint32_t* bits, int clear);
 int decode_fp8_status(uint32_t* bits, int clear);
 int plan_status(uint32_t* bits, int clear);
 int rope_status(uint32_t* bits, int clear);
+int window_status(uint32_t* bits, int clear);
 
 }  // namespace metis

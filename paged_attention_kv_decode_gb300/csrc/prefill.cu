@@ -144,6 +144,9 @@ struct PrefillParams {
   int num_sms, D;
   int kv_token_bytes;  // K and V of one cached token, every KV head
   int wait_at_exit;
+  // window > 0: a query at position p sees the keys t <= p with t > p - window or t < sinks
+  int window, sinks;
+  const void *q, *k_cache, *v_cache;  // (window only: the rows behind the tensor maps)
   Fp8Cache fp8;  // an 8-bit cache (k_cache NULL: bf16)
   // 8-bit cache, splits != NULL: the units of a last round that leaves SMs idle are split
   // over their keys.  The schedule kernel writes {how often, how many units stay whole} and
@@ -231,6 +234,17 @@ __device__ __forceinline__ bool any_nan_code(const uint4& c) {
            ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) != 0;
 }
 
+// Windows: V rows that hold an infinity or NaN and that only some of a unit's query rows see.  They
+// are kept out of the V tile, where 0 * NaN would reach every row; the rows that see them add them
+// in the epilogue.  A bit for each of the 2 x `span` tokens that may be such (span: the unit's query
+// tokens): first those that leave the window of some of them, then those behind the first query.
+constexpr int kOddWords = 4 * kRows / 32;  // span <= 2 x 128
+struct PfWindowShared {
+  uint64_t v_ready[kVStages];  // the tile's rows that not every query sees have been looked at
+  uint32_t odd[2][kOddWords];  // of the unit in hand and the one before
+  int any_odd[2];
+};
+
 // mbarrier layout (indices into the barrier area) and arrival counts
 struct PfBar {
   static constexpr int kQFull = 0, kKFull = 1, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages,
@@ -238,11 +252,12 @@ struct PfBar {
                        kPvDone = kPFull + 2, kDrain = kPvDone + 2, kQFree = kDrain + 1, kUnitFull = kQFree + 1,
                        kUnitEmpty = kUnitFull + 2, kCount = kUnitEmpty + 2;
   // full barriers: one arrival per producer warp of the ring; p_full: 128 softmax threads
-  __host__ __device__ static constexpr int arrivals(int i, bool kv8) {
+  __host__ __device__ static constexpr int arrivals(int i, bool kv8, bool window) {
     return (i >= kPFull && i < kPFull + 2) ? 128
            : (i >= kKFull && i < kKFull + kKStages) ? (kv8 ? 1 : 2)
            : (i >= kVFull && i < kVFull + kVStages) ? (kv8 ? kV8Converters : 2)
-           : (i >= kUnitEmpty && i < kUnitEmpty + 2) ? kUnitReaders + (kv8 ? 1 : 0)
+           : (i >= kVEmpty && i < kVEmpty + kVStages) ? (window ? 2 : 1)
+           : (i >= kUnitEmpty && i < kUnitEmpty + 2) ? kUnitReaders + (kv8 || window ? 1 : 0)
                                                       : 1;
   }
 };
@@ -276,6 +291,26 @@ __device__ __forceinline__ int pf_kv_tiles(int L, int q_len, int tile, int Tq) {
   if (qi0 >= q_len) return 0;
   const int p_max = L - q_len + min(q_len - 1, qi0 + Tq - 1);
   return (p_max + kKvTile) / kKvTile;
+}
+
+// Windows: of the keys before `oldest` the queries of a query-tile pair see the first `sinks` only: the
+// first `low` K/V tiles, and `skip` tiles behind them hold nothing that is seen.
+struct PfSpan {
+  int oldest, low, skip;
+};
+__device__ __forceinline__ PfSpan pf_span(const PrefillParams& p, int L, int q_len, int pair) {
+  PfSpan w;
+  w.oldest = max(L - q_len + 2 * pair * p.Tq - p.window + 1, 0);
+  const int ns = min(p.sinks, w.oldest), recent = w.oldest / kKvTile;
+  w.low = min(ns / kKvTile + (ns % kKvTile != 0), recent);
+  w.skip = recent - w.low;
+  return w;
+}
+
+// Keys seen by the q_len last queries of L tokens, summed, when each sees `most` at most.
+__device__ __forceinline__ long long pf_pairs(int L, int q_len, long long most) {
+  const long long free = min(max(most - (L - q_len), 0ll), (long long)q_len);  // queries that see all before them
+  return free * (L - q_len) + free * (free + 1) / 2 + (q_len - free) * most;
 }
 
 // ---------------------------------------------------------------------------
@@ -343,9 +378,10 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
     }
     if (!routed) {
       local += (q_len + pair_tokens - 1) / pair_tokens;
-      chunk_qk += (long long)q_len * (L - q_len) + (long long)q_len * (q_len + 1) / 2;
+      chunk_qk += p.window ? pf_pairs(L, q_len, (long long)p.window + p.sinks)
+                           : (long long)q_len * (L - q_len) + (long long)q_len * (q_len + 1) / 2;
     } else {
-      dec_tok += L;
+      dec_tok += p.window ? min((long long)L, (long long)p.window + p.sinks) : L;
     }
   }
   // The decodes' share of SMs, from warp sums published before the scan's barriers
@@ -403,7 +439,8 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
     const int np = routed ? 0 : (q_len + pair_tokens - 1) / pair_tokens;
     for (int t = 0; t < np; ++t, ++pos) {
       if ((unsigned)pos >= (unsigned)total) break;  // (offsets that decrease may list more than fits)
-      const int work = pf_kv_tiles(L, q_len, 2 * t, p.Tq) + pf_kv_tiles(L, q_len, 2 * t + 1, p.Tq);
+      int work = pf_kv_tiles(L, q_len, 2 * t, p.Tq) + pf_kv_tiles(L, q_len, 2 * t + 1, p.Tq);
+      if (p.window) work -= ((2 * t + 1) * p.Tq < q_len ? 2 : 1) * pf_span(p, L, q_len, t).skip;
       const int4 it = make_int4(s, t, work, 0);
       if (p.splits) atomicMax(&longest, pf_kv_tiles(L, q_len, 2 * t, p.Tq));
       if (sort)
@@ -464,6 +501,15 @@ struct PfUnit8 : PfUnit {
   int tag;  // 0: all of them, else index among the split units << 8 | parts << 4 | part
 };
 
+// Windows: n0, n1 and n_kv count the visited tiles.
+struct PfUnitW : PfUnit {
+  PfSpan w;
+};
+
+// The K/V tile that the unit visits j-th
+__device__ __forceinline__ int pf_tile(const PfUnit&, int j) { return j; }
+__device__ __forceinline__ int pf_tile(const PfUnitW& it, int j) { return j < it.w.low ? j : j + it.w.skip; }
+
 // The unit's first K/V tile
 __device__ __forceinline__ int pf_first(const PfUnit&) { return 0; }
 __device__ __forceinline__ int pf_first(const PfUnit8& it) { return it.j0; }
@@ -481,6 +527,89 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, PfUnit& i
   it.q0 = p.cu_q_lens[it.s];
   it.n_pages = (it.L + p.bs - 1) / p.bs;
   return it.n0 > 0;
+}
+
+__device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, PfUnitW& it) {
+  PfUnit& plain = it;
+  if (!pf_unit(p, u, plain)) return false;
+  it.w = pf_span(p, it.L, it.q_len, it.pair);
+  it.n0 -= it.w.skip;  // (the tile of the first query's oldest key comes before its own)
+  if (it.n1 > 0) it.n1 -= it.w.skip;
+  it.n_kv = max(it.n0, it.n1);
+  return true;
+}
+
+// Positions of a unit's first and last query
+__device__ __forceinline__ int pf_first_query(const PrefillParams& p, const PfUnit& it) {
+  return it.L - it.q_len + 2 * it.pair * p.Tq;
+}
+__device__ __forceinline__ int pf_last_query(const PrefillParams& p, const PfUnit& it) {
+  return it.L - it.q_len + min(it.q_len, (2 * it.pair + 2) * p.Tq) - 1;
+}
+
+// Windows: does the K/V tile at token tok0 hold tokens that some query of the unit does not see?
+__device__ __forceinline__ bool pf_partial(const PrefillParams& p, const PfUnitW& it, int tok0) {
+  return tok0 + kKvTile - 1 > pf_first_query(p, it) ||
+         (tok0 <= pf_last_query(p, it) - p.window && tok0 + kKvTile > p.sinks);
+}
+
+// Any infinity or NaN among eight bf16
+__device__ __forceinline__ bool any_nonfinite_bf16(const uint4& v) {
+  return ((((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+           ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
+}
+
+// Windows, the rare case: V rows with an infinity or NaN that were kept out of the unit's V tiles.
+// Every row of the warp that sees such a token adds weight * V to its O in TMEM (its sum of weights
+// has the weight already).  q: the thread's query row (NULL: none).
+template <int D>
+__device__ __forceinline__ void add_odd_tokens(const PrefillParams& p, const PfUnitW& it, const uint32_t* odd,
+                                            uint32_t o_tmem, const __nv_bfloat16* q, int p_row, float m_run) {
+  const int p_first = pf_first_query(p, it), span = 2 * p.Tq;
+  __threadfence();  // beside decodes nothing has waited: lines that an earlier kernel left in this SM's L1 are dropped
+#pragma unroll 1
+  for (int i = 0; i < 2 * span; ++i) {
+    if (!((*reinterpret_cast<const volatile uint32_t*>(odd + i / 32) >> (i % 32)) & 1u)) continue;
+    const int t = i < span ? i + p_first - p.window + 1 : i - span + p_first + 1;
+    const bool sees = q && t <= p_row && (t > p_row - p.window || t < p.sinks);
+    const int page = t / p.bs;
+    const int b = checked_block(p.block_table + (size_t)it.s * p.max_blocks, page, p.num_blocks, &g_status_prefill);
+    const size_t row = (((size_t)max(b, 0) * p.bs + (t - page * p.bs)) * p.G + it.g) * D;
+    float weight = 0.f;
+    if (sees) {
+      const uint4* a = reinterpret_cast<const uint4*>(q);
+      const uint4* k = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k_cache) + row);
+      float s = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = a[c], y = k[c];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+          s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+        }
+      }
+      weight = exp2_approx(s * p.scale_log2 - m_run);
+    }
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.v_cache) + row);
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t ov[16];
+      tmem_ld16(o_tmem + c * 16, ov);
+      tmem_ld_wait();
+      if (sees) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = v[c * 8 + e];
+          ov[2 * e] = __float_as_uint(fmaf(weight, __uint_as_float(w << 16), __uint_as_float(ov[2 * e])));
+          ov[2 * e + 1] = __float_as_uint(fmaf(weight, __uint_as_float(w & 0xffff0000u), __uint_as_float(ov[2 * e + 1])));
+        }
+      }
+      tmem_st16(o_tmem + c * 16, ov);
+      tmem_st_wait();
+    }
+  }
 }
 
 // Unit u: `whole` units in one piece, then the parts of `rest` others.  A part begins where
@@ -633,7 +762,10 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
 // scale joins the softmax factor of its 16 tokens.
 // SPLIT (8-bit cache): units may be parts of a pair's keys.  An instantiation of its own: the
 // registers and the code of the parts cost whole units 2-3 %.
-template <int D, bool KV8, bool SPLIT>
+// WINDOW (bf16 cache): a query sees the last `window` and the first `sinks` keys before it.  Only tiles with
+// such keys are visited.  Their hidden keys are masked per row as later ones are; the row may see nothing in its
+// first tiles.  Warp 15 looks at the V rows that not every query of the unit sees (PfWindowShared).
+template <int D, bool KV8, bool SPLIT, bool WINDOW>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                        const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
@@ -642,7 +774,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   constexpr int HALVES = Sh::kHalves;
   constexpr int kStages8 = kV8Stages;
   static_assert(KV8 || !SPLIT, "parts of units: 8-bit cache only");
-  using Unit = std::conditional_t<SPLIT, PfUnit8, PfUnit>;
+  static_assert(!(WINDOW && KV8), "windows: bf16 cache only");
+  using Unit = std::conditional_t<SPLIT, PfUnit8, std::conditional_t<WINDOW, PfUnitW, PfUnit>>;
   // The schedule kernel's items, and what the kernels in front of it wrote (tables, scale bytes),
   // are complete: waited for here, or by every CTA of the decode grid in front before it let this
   // grid launch (the warps that read more than the items then fence, below).
@@ -671,6 +804,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   volatile int* unit_slot = reinterpret_cast<volatile int*>(bars + PfBar::kCount + 2);  // [2]
   __shared__ Unit unit_info[2];  // the published unit, derived once by the fetcher
   __shared__ PfFp8Shared x8;       // (8-bit cache only)
+  __shared__ PfWindowShared xw;    // (windows only)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int units = __ldcg(p.item_count) * p.G;
@@ -684,7 +818,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
 
   if (threadIdx.x == 0) {
     // full barriers: one arrival per producer warp of the ring; p_full: 128 softmax threads
-    for (int i = 0; i < PfBar::kCount; ++i) mbar_init(&bars[i], PfBar::arrivals(i, KV8));
+    for (int i = 0; i < PfBar::kCount; ++i) mbar_init(&bars[i], PfBar::arrivals(i, KV8, WINDOW));
+    if constexpr (WINDOW) {
+      for (int i = 0; i < kVStages; ++i) mbar_init(&xw.v_ready[i], 1);
+    }
     if constexpr (KV8) {
       for (int i = 0; i < kV8Stages; ++i) {
         mbar_init(&x8.stage_full[i], 1);
@@ -915,8 +1052,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       for (int j = 0; j < it.n_kv; ++j, ++t) {
         const int st = t % depth;
         const int lp = part * half_pg + lane;  // page index inside the tile
-        const int pg = j * npg + lp;
-        const bool live = lane < half_pg && pg < it.n_pages;
+        const int pg = pf_tile(it, j) * npg + lp;
+        bool live = lane < half_pg && pg < it.n_pages;
+        if constexpr (WINDOW)  // a page that no query of the unit sees may have been given back
+          live = live && (pg * p.bs < p.sinks || pg * p.bs + p.bs > it.w.oldest);
         int rowc = 0;
         if (live) {
           const int b = checked_block(bt_row, pg, p.num_blocks, &g_status_prefill);
@@ -1076,6 +1215,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       }
     };
     uint32_t t_base = 0, n_units = 0, np[2] = {0u, 0u};  // tiles, units, p_full phases consumed
+    [[maybe_unused]] uint32_t looked = 0;  // per V stage, v_ready's parity
     uint32_t k = 0;
     bool ok = true;
     Unit it;
@@ -1107,8 +1247,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           break;
         }
         tc_fence_after_sync();
-        const int tok0 = j * kKvTile;
-        if (tok0 + kKvTile > it.L) {
+        const int tok0 = pf_tile(it, j) * kKvTile;
+        if constexpr (WINDOW) {
+          if (pf_partial(p, it, tok0)) {
+            if (!wait_all(&xw.v_ready[vst], (looked >> vst) & 1)) {
+              ok = false;
+              break;
+            }
+            looked ^= 1u << vst;
+          }
+        } else if (tok0 + kKvTile > it.L) {
           // rows past the sequence end may hold anything (NaN included): zero them so that P = 0 stays 0
           uint8_t* vb = sV + vst * Sh::kKvBytes;
           for (int row = (it.L - tok0) + lane; row < kKvTile; row += 32)
@@ -1230,6 +1378,68 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       ++k;
       if (u < 0) break;
     }
+  } else if (WINDOW && warp > kMmaWarp) {
+    // ------------------------------------------------------------ windows: V rows that not every query sees
+    // Rows that none sees may hold anything: zeros, so that P = 0 stays 0 (also those behind the sequence's
+    // end, and pages that were not loaded).  Rows that some see become zeros when they hold an infinity or
+    // NaN, and are noted.
+    regs_dec<kRegsMma>();
+    uint32_t t = 0, k = 0;
+    bool ok = true;
+    Unit it;
+    if constexpr (WINDOW) {
+      while (ok && next_unit(k, it) > 0) {
+        const int slot = (k - 1) & 1;  // every softmax group has written out the unit before the last one
+        if (lane < kOddWords) xw.odd[slot][lane] = 0u;
+        if (lane == 0) xw.any_odd[slot] = 0;
+        __syncwarp();
+        const int p_first = pf_first_query(p, it), p_last = pf_last_query(p, it);
+        for (int j = 0; j < it.n_kv; ++j, ++t) {
+          const int tok0 = pf_tile(it, j) * kKvTile, st = t % kVStages;
+          // (every tile is waited for and given back: a wait tells a phase from the next one only)
+          if (!wait_all(&v_full[st], (t / kVStages) & 1)) {
+            ok = false;
+            break;
+          }
+          if (!pf_partial(p, it, tok0)) {
+            if (lane == 0) mbar_arrive(&v_empty[st]);
+            continue;
+          }
+          constexpr int CPR = D / 8, RPS = 32 / CPR;  // 16-byte pieces of a row, rows per step
+          const int piece = lane % CPR;
+          uint8_t* tile = sV + st * Sh::kKvBytes + (piece / 8) * Sh::kKvHalf + (piece % 8) * 16;
+          // tokens [sinks, p_last - window] and those behind p_first, as rows of the tile
+          int a0 = max(p.sinks - tok0, 0), a1 = min(p_last - p.window + 1 - tok0, kKvTile);
+          if (a1 <= a0) a0 = a1 = 0;
+          const int b0 = min(max(p_first + 1 - tok0, a1), kKvTile);
+          for (int part = 0; part < 2; ++part) {
+            const int r0 = part ? b0 : a0, r1 = part ? kKvTile : a1;
+#pragma unroll 4
+            for (int row0 = r0; row0 < r1; row0 += RPS) {
+              const int row = row0 + lane / CPR, tok = tok0 + row;
+              const bool in = row < r1;
+              uint4* at = reinterpret_cast<uint4*>(tile + (in ? row : r0) * 128);
+              const bool seen = tok <= p_last && (tok > p_first - p.window || tok < p.sinks);
+              const bool odd = seen && any_nonfinite_bf16(*at);
+              const uint32_t votes = __ballot_sync(0xffffffffu, in && odd);
+              const bool row_odd = (votes >> (lane / CPR * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << CPR) - 1u);
+              if (in && (!seen || row_odd)) *at = make_uint4(0u, 0u, 0u, 0u);
+              if (in && row_odd && piece == 0) {
+                const int i = tok > p_first ? 2 * p.Tq + tok - p_first - 1 : tok - (p_first - p.window + 1);
+                atomicOr(&xw.odd[slot][i / 32], 1u << (i % 32));
+                *reinterpret_cast<volatile int*>(&xw.any_odd[slot]) = 1;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&xw.v_ready[st]);
+            mbar_arrive(&v_empty[st]);
+          }
+        }
+      }
+    }
   } else if (warp > kMmaWarp) {
     regs_dec<kRegsMma>();  // idle: give the registers to the softmax groups
   } else {
@@ -1303,10 +1513,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
         ++ns;
         tc_fence_after_sync();
-        const int tok0 = j * kKvTile;
+        const int tok0 = pf_tile(it, j) * kKvTile;
         // Visible keys of this row in this tile form a prefix: t <= p_row.
         const int vis = tok0 + kKvTile - 1 > p_min ? min(max(p_row - tok0 + 1, 0), kKvTile) : kKvTile;
-        const bool lean = vis == kKvTile && sgn > 0.f;   // the common case: no mask, positive scale
+        // (windows: but for the keys [hole, hole + hole_len))
+        [[maybe_unused]] int hole = 0, hole_len = 0;
+        if constexpr (WINDOW) {
+          hole = min(max(p.sinks - tok0, 0), kKvTile);
+          hole_len = max(min(p_row - p.window + 1 - tok0, kKvTile) - hole, 0);
+        }
+        const bool lean = vis == kKvTile && sgn > 0.f && hole_len == 0;   // the common case: no mask, positive scale
         // the row's 128 scores, read once
         uint32_t sv[kKvTile];
 #pragma unroll
@@ -1319,8 +1535,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           // fold the mask (a select: NaN-safe) and a negative scale's sign into the
           // scores once, so that one code path serves every tile
 #pragma unroll
-          for (int c = 0; c < kKvTile; ++c)
-            sv[c] = c < vis ? __float_as_uint(__uint_as_float(sv[c]) * sgn) : 0xff800000u;
+          for (int c = 0; c < kKvTile; ++c) {
+            bool seen = c < vis;
+            if constexpr (WINDOW) seen = seen && (unsigned)(c - hole) >= (unsigned)hole_len;
+            sv[c] = seen ? __float_as_uint(__uint_as_float(sv[c]) * sgn) : 0xff800000u;
+          }
         }
         [[maybe_unused]] float fac[8];  // 8-bit cache: log2 units per unit of S, for each 16 tokens
         float m_new;
@@ -1374,7 +1593,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         l_run *= alpha;
         // P = exp2(s * |sl2| - m) as bf16 pairs (even token in the low half), packed in
         // place into sv[0, 64) and stored over the first 64 columns of S_w
-        const float neg_m = -m_run;
+        const float neg_m = WINDOW && m_run == -INFINITY ? 0.f : -m_run;  // (windows: no key seen yet)
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};   // row sums, as packed pairs
         const uint64_t asl2_2 = f2_pack(asl2, asl2), neg_m2 = f2_pack(neg_m, neg_m);
         // per pair: one packed FMA, two exponentials, one packed add, one bf16x2 convert
@@ -1425,6 +1644,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
                         row_valid && p.lse_out ? p.lse_out + (size_t)(it.q0 + qi) * p.H + head : nullptr);
           continue;
         }
+      }
+      if constexpr (WINDOW) {
+        const int slot = (k - 1) & 1;
+        if (*reinterpret_cast<volatile int*>(&xw.any_odd[slot]))
+          add_odd_tokens<D>(p, it, xw.odd[slot], o_tmem,
+                            row_valid ? reinterpret_cast<const __nv_bfloat16*>(p.q) + ((size_t)(it.q0 + qi) * p.H + head) * D
+                                      : nullptr,
+                            p_row, m_run);
       }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1505,7 +1732,7 @@ static int prefill_max_parts(int num_tokens, int Tq, int G, int cap, int sms) {
 
 // The schedule kernel, then `between(p)` (the decodes of a mixed batch, or
 // nothing), then the chunk kernel.
-template <int D, bool KV8, bool SPLIT, typename Between>
+template <int D, bool KV8, bool SPLIT, bool WINDOW, typename Between>
 static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_cache, const void* v_cache,
                           void* workspace, size_t max_items, int sms, cudaStream_t st, Between between) {
   PrefillParams p = p0;
@@ -1557,7 +1784,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   if (rc) return rc;
   constexpr int smem = PfShape<D, KV8>::kSmem;
   static int done = 0;
-  auto kern = prefill_bf16_kernel<D, KV8, SPLIT>;
+  auto kern = prefill_bf16_kernel<D, KV8, SPLIT, WINDOW>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   // the warpgroups' register targets draw on the launch allocation: refuse to launch
@@ -1613,7 +1840,7 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
                          const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
                          int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks,
                          int num_blocks, int dtype, float scale, int max_seq_len, void* workspace,
-                         size_t workspace_bytes, void* stream, const Fp8Cache& fp8) {
+                         size_t workspace_bytes, void* stream, const Fp8Cache& fp8, int window = 0, int sinks = 0) {
   if (num_seqs < 0 || num_tokens < 0) return fail(METIS_E_SHAPE, "num_seqs and num_tokens must be >= 0");
   if (num_seqs == 0 || num_tokens == 0) return METIS_OK;
   if (!q || !cu_q_lens || !k_cache || !v_cache || !block_table || !seq_lens || !out)
@@ -1658,6 +1885,11 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   p.num_blocks = num_blocks;
   p.cap = (int)std::min<long long>((long long)max_blocks * block_size, (long long)max_seq_len);
   p.scale_log2 = scale * kLog2e;
+  p.window = window;
+  p.sinks = sinks;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Single-token sequences (the decodes of a mixed batch) go through the decode
   // kernel, which streams their K/V at the memory rate (a 128-row query tile would
@@ -1682,22 +1914,23 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
                                            scale, pp.cap, pp.dec_ctas, pp.dec_next, sms, st);
     return launch_decode_rows_beside(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, num_tokens, out, lse_out,
                                      num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
-                                     scale, pp.cap, 0, 0, pp.dec_ctas, pp.dec_next, sms, st);
+                                     scale, pp.cap, window, sinks, pp.dec_ctas, pp.dec_next, sms, st);
   };
-  auto launch = [&](auto dim, auto kv8, auto split) {
-    return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value>(
-        p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+  auto launch = [&](auto dim, auto kv8, auto split, auto windowed) {
+    return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value,
+                          decltype(windowed)::value>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
   using Yes = std::true_type;
   using No = std::false_type;
-  if (!fp8.k_cache) return head_dim == 128 ? launch(D128{}, No{}, No{}) : launch(D64{}, No{}, No{});
+  if (window) return head_dim == 128 ? launch(D128{}, No{}, No{}, Yes{}) : launch(D64{}, No{}, No{}, Yes{});
+  if (!fp8.k_cache) return head_dim == 128 ? launch(D128{}, No{}, No{}, No{}) : launch(D64{}, No{}, No{}, No{});
   p.max_parts = prefill_max_parts(num_tokens, p.Tq, num_kv_heads, p.cap, sms);
   if (p.max_parts > 0 &&
       workspace_bytes >= prefill_split_offset(max_items) + prefill_split_bytes(p.max_parts, head_dim))
-    return head_dim == 128 ? launch(D128{}, Yes{}, Yes{}) : launch(D64{}, Yes{}, Yes{});
-  return head_dim == 128 ? launch(D128{}, Yes{}, No{}) : launch(D64{}, Yes{}, No{});
+    return head_dim == 128 ? launch(D128{}, Yes{}, Yes{}, No{}) : launch(D64{}, Yes{}, Yes{}, No{});
+  return head_dim == 128 ? launch(D128{}, Yes{}, No{}, No{}) : launch(D64{}, Yes{}, No{}, No{});
 }
 
 }  // namespace metis
@@ -1713,6 +1946,21 @@ extern "C" int metis_paged_attn_prefill_chunk(const void* q, const int32_t* cu_q
   return prefill_chunk(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse_out, num_seqs, num_tokens,
                        num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, dtype, scale, max_seq_len,
                        workspace, workspace_bytes, stream, Fp8Cache{});
+}
+
+extern "C" int metis_paged_attn_prefill_chunk_window(const void* q, const int32_t* cu_q_lens, const void* k_cache,
+                                                     const void* v_cache, const int32_t* block_table,
+                                                     const int32_t* seq_lens, void* out, float* lse_out, int num_seqs,
+                                                     int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                                     int block_size, int max_blocks, int num_blocks, int dtype,
+                                                     float scale, int window, int sinks, int max_seq_len,
+                                                     void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (num_seqs > 0 && num_tokens > 0 && (window <= 0 || sinks < 0))
+    return fail(METIS_E_SHAPE, "window must be positive and sinks >= 0");
+  return prefill_chunk(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse_out, num_seqs, num_tokens,
+                       num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, dtype, scale, max_seq_len,
+                       workspace, workspace_bytes, stream, Fp8Cache{}, window, sinks);
 }
 
 extern "C" int metis_paged_attn_prefill_chunk_fp8(const void* q, const int32_t* cu_q_lens, const void* k_cache,

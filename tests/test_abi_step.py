@@ -85,3 +85,32 @@ def test_rope_table_on_the_host():
     angle = 99 * 500.0 ** (-2 * 5 / 16)
     assert abs(t[99, 5].item() - torch.tensor(angle, dtype=torch.float64).cos().item()) <= 2 ** -24
     assert abs(t[99, 13].item() - torch.tensor(angle, dtype=torch.float64).sin().item()) <= 2 ** -24
+
+
+def window(lib, prefill, **kw):
+    a = dict(q=FAKE, cu=FAKE, k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, out=FAKE, lse=None, S=4, T=8, H=32, G=8, D=128, bs=16, mb=8,
+             nb=64, dt=pa.METIS_BF16, scale=0.1, W=100, K=4, max_len=128, ws=FAKE, ws_bytes=1 << 20)
+    a.update(kw)
+    tail = (a["H"], a["G"], a["D"], a["bs"], a["mb"], a["nb"], a["dt"], a["scale"], a["W"], a["K"], a["max_len"])
+    ptrs = (vp(a["k"]), vp(a["v"]), vp(a["bt"]), vp(a["sl"]), vp(a["out"]), vp(a["lse"]), a["S"])
+    if prefill:
+        return lib.metis_paged_attn_prefill_chunk_window(vp(a["q"]), vp(a["cu"]), *ptrs, a["T"], *tail, vp(a["ws"]),
+                                                         a["ws_bytes"], None)
+    return lib.metis_paged_attn_decode_window(vp(a["q"]), *ptrs, *tail, None)
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(bt=None), -1), (dict(out=None), -1), (dict(S=-1), -2), (dict(W=0), -2), (dict(W=-5), -2),
+    (dict(K=-1), -2), (dict(H=30), -2), (dict(D=96), -3), (dict(bs=8), -3), (dict(dt=7), -3), (dict(q=FAKE + 2), -4),
+    (dict(sl=FAKE + 1), -4), (dict(scale=float("nan")), -2), (dict(mb=1 << 28, bs=64), -2), (dict(max_len=0), -2),
+])
+def test_window_rejects(lib, prefill, kw, code):  # noqa: F811
+    assert window(lib, prefill, **kw) == code
+    assert pa.metis_last_error() != ""
+
+
+def test_window_limits_of_each_call(lib):  # noqa: F811
+    assert window(lib, False, H=72, G=8) == -3 and window(lib, False, S=70000) == -2
+    assert window(lib, True, H=24, G=8) == -3 and window(lib, True, ws=None) == -5 and window(lib, True, dt=pa.METIS_F32) == -3
+    assert window(lib, False, S=0) == 0 and window(lib, True, S=0) == 0 and window(lib, True, T=0) == 0
