@@ -255,6 +255,43 @@ int metis_paged_attn_prefill_chunk_window(const void* q, const int32_t* cu_q_len
                                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * metis_paged_attn_decode_shared -- metis_paged_attn_decode for a batch whose sequences
+ * share their first tokens in groups (prefix caching gives requests behind one system
+ * prompt or document the same pages): each group's shared tokens are read and computed
+ * once for all of its members, on the tensor cores, and joined with every sequence's
+ * attention over its own tokens.  The result is that of metis_paged_attn_decode over all
+ * of them.
+ *
+ *   cu_group_seqs  int32 [num_groups + 1], non-decreasing, within [0, num_seqs]: group g's
+ *                  members are the sequences cu_group_seqs[g] .. cu_group_seqs[g + 1] - 1;
+ *                  sequences outside every group share nothing
+ *   prefix_lens    int32 [num_groups]: the first prefix_lens[g] tokens of the group's
+ *                  members have the same K and V (of whole pages or not); 0 shares nothing.
+ *                  They are read through the table row of the group's first member with as
+ *                  many tokens.  A member with fewer (an empty, padded row) is decoded by
+ *                  itself
+ *   workspace      >= metis_shared_workspace_bytes(...) bytes, 256-byte aligned, no
+ *                  initialisation needed
+ * Supported: dtype METIS_BF16; num_heads / num_kv_heads in {1, 2, 4, 8}; the rest as there.
+ * prefix_lens < 0 (METIS_STATUS_BAD_Q_LEN) or beyond max_seq_len or a table row
+ * (METIS_STATUS_SEQ_TOO_LONG): the group shares nothing.  A group with an offset outside
+ * [0, num_seqs] or offsets that decrease set METIS_STATUS_BAD_OFFSETS; with the latter the
+ * shared tokens of the call's sequences may be left out.
+ */
+int metis_paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu_group_seqs, const int32_t* prefix_lens, void* out,
+                                   float* lse_out, int num_seqs, int num_groups, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int max_blocks,
+                                   int num_blocks, int dtype, float scale, int max_seq_len,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace metis_paged_attn_decode_shared needs on the current device (0 for
+ * invalid sizes, or without a device). */
+size_t metis_shared_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                    int num_groups);
+
+/*
  * metis_mla_decode -- multi-head latent attention decode over a paged latent
  * cache (the MLA kernel of the vllm-metal article, section 3, fed by the block
  * table and sequence lengths of section 4).

@@ -92,6 +92,9 @@ SIGNATURES = {
                                             _i, _i, _vp]),
     "metis_paged_attn_prefill_chunk_window": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                                    _i, _i, _f, _i, _i, _i, _vp, _sz, _vp]),
+    "metis_paged_attn_decode_shared": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                                             _i, _i, _f, _i, _vp, _sz, _vp]),
+    "metis_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "metis_plan_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                              _vp]),
     "metis_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i64, _i64, _i, _i, _i, _f, _i,
@@ -735,6 +738,46 @@ def metis_paged_attn_prefill_chunk_window(q: torch.Tensor, cu_q_lens: torch.Tens
     rc = lib.metis_paged_attn_prefill_chunk_window(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width,
                                                    nb, code, float(scale), int(window), int(sinks), int(max_seq_len),
                                                    w_at, w_bytes, _stream_of(dev, stream))
+    if rc:
+        _check(rc)
+    return out, lse_out
+
+
+def metis_shared_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                 num_groups: int) -> int:
+    return int(load_library().metis_shared_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_groups))
+
+
+def metis_paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_table: torch.Tensor, seq_lens: torch.Tensor, cu_group_seqs: torch.Tensor,
+                                   prefix_lens: torch.Tensor, scale: float, *, out: Optional[torch.Tensor] = None,
+                                   lse_out: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+                                   workspace: Optional[torch.Tensor] = None, stream=None,
+                                   want_lse: bool = False) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Paged decode (bf16) of sequences whose groups, sequences ``cu_group_seqs[g] .. cu_group_seqs[g + 1]``
+    (int32 ``[num_groups + 1]``), share their first ``prefix_lens[g]`` tokens: those are computed once per
+    group; returns ``(out, lse_out)``.  ``max_seq_len=None`` reads seq_lens (a sync)."""
+    lib = _lib or load_library()
+    dev = _device_of("q", q, 3)
+    code = _dtype_code(q.dtype)
+    (nb, bs, G, D), cache = _paged_cache(dev, q, k_cache, v_cache)
+    S, H = q.shape[0], q.shape[1]
+    q_at = _on(dev, "q", q, q.dtype, (S, H, D))
+    width, table = _table(dev, block_table, S)
+    lens = _on(dev, "seq_lens", seq_lens, torch.int32, (S,))
+    if not isinstance(prefix_lens, torch.Tensor):
+        raise TypeError("prefix_lens must be a torch.Tensor")
+    groups = prefix_lens.numel()
+    shared = _on(dev, "prefix_lens", prefix_lens, torch.int32, (groups,))
+    cu = _on(dev, "cu_group_seqs", cu_group_seqs, torch.int32, (groups + 1,))
+    out, o_at, lse_out, l_at = _attention_outputs(dev, q, out, lse_out, want_lse, stream)
+    if max_seq_len is None:
+        max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
+    need = lib.metis_shared_workspace_bytes(S, H, G, D, groups) if workspace is None else 0
+    workspace, w_at, w_bytes = _workspace(dev, q, workspace, max(need, 256), stream)
+    rc = lib.metis_paged_attn_decode_shared(q_at, *cache, table, lens, cu, shared, o_at, l_at, S, groups, H, G, D, bs,
+                                            width, nb, code, float(scale), int(max_seq_len), w_at, w_bytes,
+                                            _stream_of(dev, stream))
     if rc:
         _check(rc)
     return out, lse_out

@@ -102,6 +102,8 @@ extern "C" int metis_read_status(uint32_t* status_out, int clear) {
   if (rc) return rc;
   rc = metis::window_status(&bits, clear);
   if (rc) return rc;
+  rc = metis::shared_status(&bits, clear);
+  if (rc) return rc;
   *status_out = bits;
   return METIS_OK;
 }

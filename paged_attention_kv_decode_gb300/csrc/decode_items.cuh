@@ -328,11 +328,12 @@ struct JoinedRow {
 
 // What else joins a row: nothing.
 struct NoParts {
+  __device__ __forceinline__ void prepare() {}
   __device__ __forceinline__ void add(JoinedRow&, int, int) const {}
 };
 
 // The item's `n` parts that hold tokens, rows o [r][D] and their lse (natural log) in the shared memory
-// of the CTAs 0 .. n - 1 of this cluster, and `more` (add(row, h, d) joins what it holds for dims
+// of the CTAs 0 .. n - 1 of this cluster, and `more` (prepared; add(row, h, d) joins what it holds for dims
 // d .. d + 3 of query head h of the group).  Each of the cluster's `parts` CTAs writes a share of the rows.
 template <int D, typename OutT, int NT, typename More>
 __device__ __forceinline__ void join_parts_of_item(const DecodeParams& p, const float* o, const float* lse, int part,
@@ -369,7 +370,7 @@ template <int D, int NW, int STAGES, typename More>
 __device__ __forceinline__ void decode_joined_item(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                                    const DecodeParams& p, uint8_t* smem, uint64_t* bars, int g, int s,
                                                    int part, int parts, bool has, WindowSpan span,
-                                                   unsigned int* status, const More& more) {
+                                                   unsigned int* status, More more) {
   constexpr int STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
   static_assert(NW * (64 + D * 32) + 8 * D * 4 + 32 <= NW * STAGES * STAGE_BYTES, "the partial must fit in the ring");
   float* jo = reinterpret_cast<float*>(smem + NW * (64 + D * 32));
@@ -399,6 +400,7 @@ __device__ __forceinline__ void decode_joined_item(const CUtensorMap& tmK, const
   } else {
     __syncthreads();
   }
+  more.prepare();
   join_parts_of_item<D, __nv_bfloat16, NW * 32>(p, jo, jl, part, parts, n, g, s, more);
   if (parts > 1) {
     __syncwarp();
@@ -504,6 +506,16 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// CTAs that share an item of up to `tokens` tokens: as many as the SMs take at once (kItemCtasPerSm each), with at
+// least kMinPartTokens each
+constexpr int kItemCtasPerSm = 2;
+constexpr int kMinPartTokens = 128;
+
+inline int item_parts(long long items, int tokens, int sms) {
+  const long long fit = items > 0 ? kItemCtasPerSm * (long long)sms / items : 1;
+  return (int)std::max<long long>(1, std::min<long long>({kMaxParts, fit, tokens / kMinPartTokens}));
+}
+
 // TMA maps of the K and V caches: 16-token x 64-dim boxes of one KV head.
 template <int D>
 inline int encode_kv_maps(const DecodeParams& p, const void* k_cache, const void* v_cache, CUtensorMap* tmK,

@@ -120,15 +120,6 @@ static int launch_window(const WindowParams& wp, const void* k_cache, const void
                           tmK, tmV, wp);
 }
 
-// CTAs that share an item: as many as the SMs take at once (kCtasPerSm each), with at least kMinPartTokens each
-constexpr int kCtasPerSm = 2;
-constexpr int kMinPartTokens = 128;
-
-static int window_parts(long long items, int tokens, int sms) {
-  const long long fit = items > 0 ? kCtasPerSm * (long long)sms / items : 1;
-  return (int)std::max<long long>(1, std::min<long long>({kMaxParts, fit, tokens / kMinPartTokens}));
-}
-
 }  // namespace metis
 
 using namespace metis;
@@ -186,7 +177,7 @@ extern "C" int metis_paged_attn_decode_window(const void* q, const void* k_cache
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(METIS_E_CUDA, "querying the SM count: %s", cudaGetErrorString(e));
   const int seen = (int)std::min<long long>((long long)window + sinks, p.cap);
-  const int parts = window_parts((long long)num_kv_heads * num_seqs, seen, sms);
+  const int parts = item_parts((long long)num_kv_heads * num_seqs, seen, sms);
   auto launch = [&](auto dim, auto join) {
     return launch_window<decltype(dim)::value, decltype(join)::value>(wp, k_cache, v_cache, parts, st);
   };

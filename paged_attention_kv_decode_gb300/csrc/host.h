@@ -135,6 +135,25 @@ inline int check_decode_sizes(int num_seqs, int num_heads, int num_kv_heads, int
   return METIS_OK;
 }
 
+// Decodes whose sequences share their first tokens in groups (shared_prefix.cu): the call's arguments,
+struct SharedArgs {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_table, *seq_lens, *cu_group_seqs, *prefix_lens;
+  void* out;
+  float* lse_out;
+  int S, num_groups, H, G, D, bs, max_blocks, num_blocks, cap;
+  float scale;
+};
+// what the kernel over the shared prefixes leaves for the one over the sequences' own tokens,
+struct SharedPlan {
+  int2 total;     // K/V tiles of all units, CTAs that share them
+  int2 unused;
+  int4 group[1];  // [num_groups]: tiles before the group, of a unit, units before the group, units per KV head
+};
+// and the launch of the first (prefill.cu), `sms` CTAs: a part is [2][128] rows.
+int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, float* part_lse, float* part_out, int sms,
+                         cudaStream_t st);
+
 // Per-translation-unit device status words.
 int decode_status(uint32_t* bits, int clear);
 int prefill_status(uint32_t* bits, int clear);
@@ -146,5 +165,6 @@ int decode_fp8_status(uint32_t* bits, int clear);
 int plan_status(uint32_t* bits, int clear);
 int rope_status(uint32_t* bits, int clear);
 int window_status(uint32_t* bits, int clear);
+int shared_status(uint32_t* bits, int clear);
 
 }  // namespace metis

@@ -121,6 +121,7 @@ constexpr int kSortMax = 2048;    // schedule: heaviest-first sort up to this ma
 constexpr int kMaxSplits = 8;
 constexpr int kMinPartTiles = 4;
 constexpr int kMinSplitTiles = 13;
+constexpr int kMinShare = 4;      // shared prefixes: K/V tiles of a CTA at least
 
 struct PrefillParams {
   const int32_t* cu_q_lens;
@@ -155,7 +156,12 @@ struct PrefillParams {
   int max_parts;    // memory for this many parts
   int* parts_done;  // [split unit][query tile][warp]
   float* part_lse;  // [part][query tile][row], log2 units
-  float* part_out;  // [part][query tile][head_dim / 4][row][4], normalised
+  float* part_out;  // [part][query tile][head_dim / 4][row][4], normalised (shared prefixes: [head_dim])
+  // Shared prefixes: the groups (cu_q_lens: their first sequences), their shared tokens, and what the
+  // kernel behind this one needs to find a row's parts.
+  const int32_t* prefix_lens;
+  SharedPlan* plan;
+  int num_groups;
 };
 
 // Shared-memory layout (all tiles 128-byte swizzled, [64-column half][row][128 B]).
@@ -262,6 +268,43 @@ struct PfBar {
   }
 };
 static_assert((PfBar::kCount + 4) * 8 <= 256, "prefill barrier area");
+
+// Shared prefixes.  A group's members are the query rows of its prefix: q_len members, L shared tokens, no
+// causal mask, the pages those of the first member that is at least as long.  A unit is (group, KV head,
+// pair of query tiles); all units' K/V tiles in a row are cut into equal shares, one per CTA, and
+// what a CTA computes of a unit is a part, number (index of the unit) + (index of the CTA): both
+// grow along the row, and one of them from each part to the next.
+struct PfGroup {
+  int q0, n;           // first member, members
+  int leader, tokens;  // the sequence whose pages are read, shared tokens
+  int tiles, units;    // K/V tiles of a unit, units (0: nothing shared)
+};
+
+// *bad: status bits; *decreases: the group's offsets do.
+__device__ __forceinline__ PfGroup pf_group(const PrefillParams& p, int g, unsigned* bad, bool* decreases) {
+  PfGroup v{};
+  const int a = p.cu_q_lens[g], b = p.cu_q_lens[g + 1], tokens = p.prefix_lens[g];
+  *decreases = a > b;
+  if (a < 0 || b > p.S || a > b) {
+    *bad |= METIS_STATUS_BAD_OFFSETS;
+    return v;
+  }
+  if (tokens < 0) *bad |= METIS_STATUS_BAD_Q_LEN;
+  if (tokens <= 0 || tokens > p.cap) {
+    if (tokens > p.cap && b > a) *bad |= METIS_STATUS_SEQ_TOO_LONG;
+    return v;
+  }
+  int s = a;
+  while (s < b && p.seq_lens[s] < tokens) ++s;
+  if (s == b) return v;
+  v.q0 = a;
+  v.n = b - a;
+  v.leader = s;
+  v.tokens = tokens;
+  v.tiles = (tokens - 1) / kKvTile + 1;
+  v.units = ((v.n - 1) / (2 * p.Tq) + 1) * p.G;
+  return v;
+}
 
 // Effective (sequence length, query count) after clamping to what can be read.  `flag`: report
 // what had to be clamped (the schedule kernel, which sees every sequence once).
@@ -506,9 +549,16 @@ struct PfUnitW : PfUnit {
   PfSpan w;
 };
 
+// Shared prefixes: tiles [j0, j0 + n_kv) of the unit, part number `part`.
+struct PfUnitS : PfUnit {
+  int j0, part;
+};
+
 // The K/V tile that the unit visits j-th
 __device__ __forceinline__ int pf_tile(const PfUnit&, int j) { return j; }
 __device__ __forceinline__ int pf_tile(const PfUnitW& it, int j) { return j < it.w.low ? j : j + it.w.skip; }
+
+__device__ __forceinline__ int pf_tile(const PfUnitS& it, int j) { return it.j0 + j; }
 
 // The unit's first K/V tile
 __device__ __forceinline__ int pf_first(const PfUnit&) { return 0; }
@@ -757,6 +807,69 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
   if (lse) *lse = (M + log2f(W)) * kLn2;
 }
 
+// Shared prefixes: this CTA's share [begin, end) of all units' K/V tiles in a row, the group in which it
+// begins, and the tiles and units of the groups before that one.  Called by the whole block; the first CTA
+// leaves the plan for the kernel behind.
+struct PfShare {
+  int begin, end, group, x, unit;
+};
+
+__device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
+  __shared__ int warp_sums[kPfThreads / 32];
+  __shared__ PfShare mine;
+  const int tid = threadIdx.x;
+  int x = 0, unit = 0;  // of the groups before this round's
+  PfGroup v{};
+  int my_x = 0, my_unit = 0;
+  bool disorder = false;
+  auto round = [&](int g0, bool first) {
+    unsigned bad = 0;
+    bool decreases = false;
+    v = g0 + tid < p.num_groups ? pf_group(p, g0 + tid, &bad, &decreases) : PfGroup{};
+    disorder |= __syncthreads_or(decreases);
+    int sum;
+    my_unit = unit + block_exclusive_scan<kPfThreads>(v.units, warp_sums, &sum);
+    unit += sum;
+    __syncthreads();  // the sums were read
+    my_x = x + block_exclusive_scan<kPfThreads>(v.units * v.tiles, warp_sums, &sum);
+    x += sum;
+    __syncthreads();
+    if (first && blockIdx.x == 0 && g0 + tid < p.num_groups) {
+      p.plan->group[g0 + tid] = make_int4(my_x, v.units ? v.tiles : 0, my_unit, v.units / p.G);
+      if (bad) atomicOr(&g_status_prefill, bad);
+    }
+  };
+  for (int g0 = 0; g0 < p.num_groups; g0 += kPfThreads) round(g0, true);
+  // Groups that overlap (offsets that decrease somewhere) could have more units than there is room for
+  const int total = disorder ? 0 : x, ctas = min((int)gridDim.x, max(total / kMinShare, 1));
+  if (blockIdx.x == 0 && tid == 0) p.plan->total = make_int2(total, ctas);
+  PfShare s{};
+  s.begin = (int)((long long)min((int)blockIdx.x, ctas) * total / ctas);
+  s.end = (int)((long long)min((int)blockIdx.x + 1, ctas) * total / ctas);
+  if (s.begin == s.end) return s;
+  auto find = [&](int g0) {  // the group with tile s.begin is this thread's
+    if (my_x <= s.begin && s.begin - my_x < v.units * v.tiles) {
+      mine.group = g0 + tid;
+      mine.x = my_x;
+      mine.unit = my_unit;
+    }
+  };
+  if (p.num_groups <= kPfThreads) {
+    find(0);
+  } else {
+    x = unit = 0;
+    for (int g0 = 0; g0 < p.num_groups; g0 += kPfThreads) {
+      round(g0, false);
+      find(g0);
+    }
+  }
+  __syncthreads();
+  s.group = mine.group;
+  s.x = mine.x;
+  s.unit = mine.unit;
+  return s;
+}
+
 // KV8: the cache holds e4m3 codes.  K tiles feed the tensor cores as they are, against the
 // query rows split into two e4m3 parts; V tiles are converted to bf16 on the way; a K page's
 // scale joins the softmax factor of its 16 tokens.
@@ -765,7 +878,9 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
 // WINDOW (bf16 cache): a query sees the last `window` and the first `sinks` keys before it.  Only tiles with
 // such keys are visited.  Their hidden keys are masked per row as later ones are; the row may see nothing in its
 // first tiles.  Warp 15 looks at the V rows that not every query of the unit sees (PfWindowShared).
-template <int D, bool KV8, bool SPLIT, bool WINDOW>
+// SHARED (bf16 cache): prefixes that groups of decodes share (PfGroup).  The units come from the groups
+// directly, without a schedule kernel, and every result is a part for the kernel behind this one.
+template <int D, bool KV8, bool SPLIT, bool WINDOW, bool SHARED>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                        const __grid_constant__ CUtensorMap tmK,
                                                                        const __grid_constant__ CUtensorMap tmV,
@@ -775,11 +890,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   constexpr int kStages8 = kV8Stages;
   static_assert(KV8 || !SPLIT, "parts of units: 8-bit cache only");
   static_assert(!(WINDOW && KV8), "windows: bf16 cache only");
-  using Unit = std::conditional_t<SPLIT, PfUnit8, std::conditional_t<WINDOW, PfUnitW, PfUnit>>;
+  static_assert(!(SHARED && (WINDOW || KV8)), "shared prefixes: bf16 cache only");
+  using Unit = std::conditional_t<SPLIT, PfUnit8, std::conditional_t<WINDOW, PfUnitW, std::conditional_t<SHARED, PfUnitS, PfUnit>>>;
   // The schedule kernel's items, and what the kernels in front of it wrote (tables, scale bytes),
   // are complete: waited for here, or by every CTA of the decode grid in front before it let this
   // grid launch (the warps that read more than the items then fence, below).
   if (!p.wait_at_exit) pdl_wait();
+  if (SHARED) pdl_launch_dependents();  // every CTA has waited: the decodes may start on SMs that are free
   extern __shared__ uint8_t smem_raw[];
   const uint32_t slack = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + slack;
@@ -807,7 +924,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   __shared__ PfWindowShared xw;    // (windows only)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int units = __ldcg(p.item_count) * p.G;
+  [[maybe_unused]] PfShare share{};  // shared prefixes
+  int units;
+  if constexpr (SHARED) {
+    share = pf_share(p);
+    units = share.end > share.begin ? gridDim.x : 0;
+  } else {
+    units = __ldcg(p.item_count) * p.G;
+  }
   [[maybe_unused]] int2 splits = make_int2(1, units);  // parts of each unit that is split, units that are not
   [[maybe_unused]] const int rest = SPLIT ? units - (splits = __ldcg(p.splits)).y : 0;
   if (SPLIT) units = splits.y + rest * splits.x;
@@ -1349,6 +1473,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // that at the end of the list no CTA holds small units that an idle CTA could run.
     regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
     uint32_t k = 0;
+    [[maybe_unused]] int at = share.begin, group = share.group;
+    [[maybe_unused]] PfGroup now{};
+    if constexpr (SHARED) {
+      unsigned bad = 0;
+      bool decreases;
+      now = pf_group(p, group, &bad, &decreases);
+    }
     for (;;) {
       const int slot = k & 1;
       if (k >= 1 && !wait_all(&unit_empty[(k - 1) & 1], ((k - 1) >> 1) & 1)) break;
@@ -1356,10 +1487,38 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       // from a CTA that starts a little later (2 x 256 queries beside 32 decodes: 147 or 173 us)
       if (SPLIT && k >= 1 && !wait_all(q_free, (k - 1) & 1)) break;
       int u = 0;
-      if (lane == 0) u = atomicAdd(p.unit_head, 1);
-      u = __shfl_sync(0xffffffffu, u, 0);
       Unit it;
-      if (u < units) {
+      if constexpr (SHARED) {
+        if (at < share.end) {
+          while (at - share.x >= now.units * now.tiles && group + 1 < p.num_groups) {
+            share.x += now.units * now.tiles;
+            share.unit += now.units;
+            unsigned bad = 0;
+            bool decreases;
+            now = pf_group(p, ++group, &bad, &decreases);
+          }
+          const int pairs = now.units / p.G, unit = (at - share.x) / now.tiles;
+          it.s = now.leader;
+          it.g = unit / pairs;
+          it.pair = unit - it.g * pairs;
+          it.L = now.tokens;
+          it.q_len = now.n;
+          it.q0 = now.q0;
+          it.n_pages = (now.tokens - 1) / p.bs + 1;
+          it.j0 = (at - share.x) - unit * now.tiles;
+          it.n_kv = it.n0 = min(now.tiles - it.j0, share.end - at);
+          it.n1 = (2 * it.pair + 1) * p.Tq < now.n ? it.n0 : 0;
+          it.part = share.unit + unit + blockIdx.x;
+          at += it.n_kv;
+        } else {
+          u = -1;
+        }
+      } else {
+        if (lane == 0) u = atomicAdd(p.unit_head, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+      }
+      if constexpr (SHARED) {
+      } else if (u < units) {
         bool some;  // false: nothing to compute
         if constexpr (SPLIT)
           some = pf_unit(p, u, splits.y, rest, splits.x, it);
@@ -1502,9 +1661,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       const int qi0 = (2 * it.pair + w) * p.Tq;
       const int qi = qi0 + (row - hh * p.Tq);
       const bool row_valid = qi < q_len;
-      const int p_min = L - q_len + qi0;        // position of the tile's first query token
-      const int p_max = L - q_len + min(q_len - 1, qi0 + p.Tq - 1);
-      const int p_row = row_valid ? (L - q_len + qi) : p_max;
+      // position of the tile's first query token (shared prefixes: every row sees every key)
+      const int p_min = SHARED ? L - 1 : L - q_len + qi0;
+      const int p_max = SHARED ? L - 1 : L - q_len + min(q_len - 1, qi0 + p.Tq - 1);
+      const int p_row = row_valid && !SHARED ? (L - q_len + qi) : p_max;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nkv; ++j) {
         if (!wait_all(&s_full[w], ns & 1)) {
@@ -1645,6 +1805,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           continue;
         }
       }
+      if constexpr (SHARED) {
+        const size_t at = ((size_t)it.part * 2 + w) * kRows + row;
+        float* to = p.part_out + at * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tmem + c * 32, ov);
+          tmem_ld_wait();
+          if (row_valid) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * inv);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global_v8(to + c * 32 + i, ov + i);
+          }
+        }
+        if (row_valid) p.part_lse[at] = m_run + log2f(l_run);
+      }
       if constexpr (WINDOW) {
         const int slot = (k - 1) & 1;
         if (*reinterpret_cast<volatile int*>(&xw.any_odd[slot]))
@@ -1654,7 +1831,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
                             p_row, m_run);
       }
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < (SHARED ? 0 : D / 32); ++c) {
         uint32_t ov[32];
         tmem_ld32(o_tmem + c * 32, ov);
         tmem_ld_wait();
@@ -1732,7 +1909,7 @@ static int prefill_max_parts(int num_tokens, int Tq, int G, int cap, int sms) {
 
 // The schedule kernel, then `between(p)` (the decodes of a mixed batch, or
 // nothing), then the chunk kernel.
-template <int D, bool KV8, bool SPLIT, bool WINDOW, typename Between>
+template <int D, bool KV8, bool SPLIT, bool WINDOW, bool SHARED, typename Between>
 static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_cache, const void* v_cache,
                           void* workspace, size_t max_items, int sms, cudaStream_t st, Between between) {
   PrefillParams p = p0;
@@ -1741,7 +1918,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   p.items = items;
   p.item_count = count;
   p.unit_head = count + 1;
-  if (p.skip_decodes) {
+  if (p.skip_decodes && !SHARED) {
     p.dec_ctas = count + 2;
     p.dec_next = count + 3;
     p.wait_at_exit = 1;
@@ -1777,14 +1954,16 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   if (rc) return rc;
   // a programmatic dependent of the kernel before it (e.g. the paged K/V write): its
   // launch overlaps that kernel's tail
-  rc = launch_dependent(prefill_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, "prefill_schedule_kernel launch",
-                        p, items, count, (int)max_items);
-  if (rc) return rc;
+  if (!SHARED) {
+    rc = launch_dependent(prefill_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, "prefill_schedule_kernel launch",
+                          p, items, count, (int)max_items);
+    if (rc) return rc;
+  }
   rc = between(p);
   if (rc) return rc;
   constexpr int smem = PfShape<D, KV8>::kSmem;
   static int done = 0;
-  auto kern = prefill_bf16_kernel<D, KV8, SPLIT, WINDOW>;
+  auto kern = prefill_bf16_kernel<D, KV8, SPLIT, WINDOW, SHARED>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   // the warpgroups' register targets draw on the launch allocation: refuse to launch
@@ -1801,7 +1980,7 @@ static int launch_prefill(const PrefillParams& p0, const void* q, const void* k_
   }
   // persistent: at most one CTA per SM, each taking units from the list as it goes
   // (beside the decodes: the CTAs past the SMs they keep start as their CTAs finish)
-  const size_t grid = SPLIT ? (size_t)sms : std::min<size_t>(max_items * p.G, (size_t)std::max(sms, 1));
+  const size_t grid = SPLIT || SHARED ? (size_t)sms : std::min<size_t>(max_items * p.G, (size_t)std::max(sms, 1));
   return launch_dependent(kern, dim3((unsigned)grid), dim3(kPfThreads), smem, st, "prefill_bf16_kernel launch", tmQ,
                           tmK, tmV, p);
 }
@@ -1918,7 +2097,7 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
   };
   auto launch = [&](auto dim, auto kv8, auto split, auto windowed) {
     return launch_prefill<decltype(dim)::value, decltype(kv8)::value, decltype(split)::value,
-                          decltype(windowed)::value>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
+                          decltype(windowed)::value, false>(p, q, k_cache, v_cache, workspace, max_items, sms, st, between);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
@@ -1931,6 +2110,37 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
       workspace_bytes >= prefill_split_offset(max_items) + prefill_split_bytes(p.max_parts, head_dim))
     return head_dim == 128 ? launch(D128{}, Yes{}, Yes{}, No{}) : launch(D64{}, Yes{}, Yes{}, No{});
   return head_dim == 128 ? launch(D128{}, Yes{}, No{}, No{}) : launch(D64{}, Yes{}, No{}, No{});
+}
+
+}  // namespace metis
+
+namespace metis {
+
+// The parts of the shared prefixes of a batch of decodes (shared_prefix.cu).
+int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, float* part_lse, float* part_out, int sms,
+                         cudaStream_t st) {
+  PrefillParams p{};
+  p.cu_q_lens = a.cu_group_seqs;
+  p.prefix_lens = a.prefix_lens;
+  p.num_groups = a.num_groups;
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.S = p.T = a.S;
+  p.H = a.H;
+  p.G = a.G;
+  p.r = a.H / a.G;
+  p.Tq = kRows / p.r;
+  p.bs = a.bs;
+  p.max_blocks = a.max_blocks;
+  p.num_blocks = a.num_blocks;
+  p.cap = a.cap;
+  p.scale_log2 = a.scale * kLog2e;
+  p.plan = plan;
+  p.part_lse = part_lse;
+  p.part_out = part_out;
+  auto none = [](const PrefillParams&) { return METIS_OK; };
+  return a.D == 128 ? launch_prefill<128, false, false, false, true>(p, a.q, a.k_cache, a.v_cache, part_out, 0, sms, st, none)
+                    : launch_prefill<64, false, false, false, true>(p, a.q, a.k_cache, a.v_cache, part_out, 0, sms, st, none);
 }
 
 }  // namespace metis

@@ -114,3 +114,29 @@ def test_window_limits_of_each_call(lib):  # noqa: F811
     assert window(lib, False, H=72, G=8) == -3 and window(lib, False, S=70000) == -2
     assert window(lib, True, H=24, G=8) == -3 and window(lib, True, ws=None) == -5 and window(lib, True, dt=pa.METIS_F32) == -3
     assert window(lib, False, S=0) == 0 and window(lib, True, S=0) == 0 and window(lib, True, T=0) == 0
+
+
+def shared(lib, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, cu=FAKE, pl=FAKE, out=FAKE, lse=None, S=4, n=2, H=32, G=8, D=128,
+             bs=16, mb=8, nb=64, dt=pa.METIS_BF16, scale=0.1, max_len=128, ws=FAKE, ws_bytes=1 << 20)
+    a.update(kw)
+    return lib.metis_paged_attn_decode_shared(
+        *(vp(a[x]) for x in ("q", "k", "v", "bt", "sl", "cu", "pl", "out", "lse")),
+        *(a[x] for x in ("S", "n", "H", "G", "D", "bs", "mb", "nb", "dt", "scale", "max_len")), vp(a["ws"]), a["ws_bytes"],
+        None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(cu=None), -1), (dict(pl=None), -1), (dict(out=None), -1), (dict(S=-1), -2), (dict(n=-1), -2),
+    (dict(H=30), -2), (dict(H=24), -3), (dict(H=128), -3), (dict(D=96), -3), (dict(bs=8), -3), (dict(dt=pa.METIS_F32), -3),
+    (dict(q=FAKE + 2), -4), (dict(cu=FAKE + 2), -4), (dict(scale=float("nan")), -2), (dict(S=70000), -2),
+    (dict(mb=1 << 26, nb=1 << 26, max_len=1 << 30, S=4000, n=4000), -2),  # more tiles than fit in int32
+])
+def test_shared_rejects(lib, kw, code):  # noqa: F811
+    assert shared(lib, **kw) == code
+    assert pa.metis_last_error() != ""
+
+
+def test_shared_of_no_sequences_and_workspace(lib):  # noqa: F811
+    assert shared(lib, S=0) == 0
+    assert pa.metis_shared_workspace_bytes(0, 8, 2, 64, 1) == 0 and pa.metis_shared_workspace_bytes(4, 9, 2, 64, 1) == 0
