@@ -511,6 +511,10 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 constexpr int kItemCtasPerSm = 2;
 constexpr int kMinPartTokens = 128;
 
+// Many items: a warp each, nine CTAs on an SM instead of two of four warps.  The bytes in flight are the
+// same, and an item's start (its lengths, block ids, first loads) hides behind eight others.
+inline bool one_warp_items(long long items, int sms) { return items >= 18ll * sms; }
+
 inline int item_parts(long long items, int tokens, int sms) {
   const long long fit = items > 0 ? kItemCtasPerSm * (long long)sms / items : 1;
   return (int)std::max<long long>(1, std::min<long long>({kMaxParts, fit, tokens / kMinPartTokens}));

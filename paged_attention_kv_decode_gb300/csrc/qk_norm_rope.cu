@@ -9,10 +9,11 @@
 // kernels fed by the scheduler's block table", vllm-metal article, sections 3 and 4; the write is
 // the one of cache_write.cu).  Everything between load and store is fp32: one rounding.
 //
-// Bound by HBM: each row is read once and written once.  One CTA per token, its warps share the
-// token's heads: a row of head_dim elements is 8 to 32 lanes with 16 bytes each, so a warp's
-// angles and weights stay in registers over all of its rows, up to kRows of which are in flight.
-// The partner of a pair is in the same lane (interleaved) or half of rotary_dim away: a shuffle.
+// Bound by HBM: each row is read once and written once.  A warp takes a token, or where there are few
+// tokens a share of a token's heads: a row of head_dim elements is 8 to 32 lanes with 16 bytes each, so the
+// token's angles and the weights stay in registers over all of the warp's rows, kRows loads of which are in
+// flight per lane.  The partner of a pair is in the same lane (interleaved) or half of rotary_dim away: a
+// shuffle.
 #include <algorithm>
 
 #include "../../include/metis_attn.h"
@@ -23,8 +24,9 @@ namespace metis {
 
 __device__ unsigned int g_status_rope = 0;
 
-constexpr int kRopeThreads = 256;
-constexpr int kRows = 3;  // rows a thread has in flight
+constexpr int kRopeWarps = 4;
+constexpr int kRows = 4;  // rows a lane has in flight
+constexpr int kRopeFill = 28;  // warps for each SM, below which tokens are shared by several
 
 struct RopeParams {
   const void* q;
@@ -44,16 +46,15 @@ struct RopeParams {
   int H, G, R, max_position;
 };
 
+// 16 bytes of a row as pairs of fp32, and back
 template <typename T>
 struct RopeVec;
 template <>
 struct RopeVec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void unpack(const uint4& v, uint64_t* x) {
+    x[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   static __device__ __forceinline__ uint4 pack(const float* x) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -62,13 +63,10 @@ struct RopeVec<float> {
 template <>
 struct RopeVec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+  static __device__ __forceinline__ void unpack(const uint4& v, uint64_t* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   static __device__ __forceinline__ uint4 pack(const float* x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -84,162 +82,215 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// x[] of the row's lane -> x / sqrt(mean(x^2) + eps) * w.  Squares that leave fp32's range are taken
-// of x times a power of two, which also goes to eps: exact, and rare.
-template <int D, int N, int LANES>
-__device__ __forceinline__ void normalise(float* x, const float* w, float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = row_sum<LANES>(ss);
-  const float up = !(ss < 1.3e36f) ? 8.271806e-25f /* 2^-80 */ : ss + eps < 1e-30f ? 1.2089258e24f /* 2^80 */ : 1.f;
-  if (__any_sync(0xffffffffu, up != 1.f)) {
-    ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] *= up;
-      ss = fmaf(x[i], x[i], ss);
-    }
-    ss = row_sum<LANES>(ss);
-    eps = eps * up * up;
-  }
-  const float f = 1.0f / sqrtf(fmaf(ss, 1.0f / D, eps));
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = x[i] * f * w[i];
-}
+// How a warp's rows are worked on: lane `at` of a row of LANES lanes holds its elements at * N .. + N - 1.
+struct RopeLane {
+  int at, sub, mate;   // sub: the lane's row among the warp's; mate: the lane that holds the partners
+  bool turned, inter;  // the lane's elements are rotated; their partners are in the lane itself
+};
 
-// The rows of one token: rows 0 .. H - 1 are queries, then G keys, then (v given) G values.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p, const int interleaved) {
+// The rows [lo, hi) of one kind (queries or keys) of a token: out = f (x a + x' b), x' the partner of x, with
+// a = weight cos and b = +-weight' sin (weight' the partner's), f = 1 / sqrt(mean(x^2) + eps) or 1.
+template <typename T, int D, typename Source, typename Target>
+__device__ __forceinline__ void turn_rows(const RopeParams& p, const RopeLane& me, const float* turn,
+                                          const void* weight, int lo, int hi, Source source, Target target) {
   using Vec = RopeVec<T>;
-  constexpr int N = Vec::kN, LANES = D / N, PER_WARP = 32 / LANES;
-  constexpr int STEP = kRopeThreads / LANES;  // rows of the CTA at a time
-  pdl_launch_dependents();
-  pdl_wait();  // rows, positions and slots may be what the kernel in front writes
-  const long long n = blockIdx.x;
-  const int lane = threadIdx.x & 31, at = lane % LANES;  // this thread's elements: at * N ..
-  const int first = (threadIdx.x >> 5) * PER_WARP + lane / LANES;
-  const int rows = p.H + (p.v ? 2 : 1) * p.G;
-
-  auto source = [&](int row) -> const uint4* {
-    const T* base;
-    if (row < p.H)
-      base = reinterpret_cast<const T*>(p.q) + n * p.q_stride + (long long)row * D;
-    else if (row < p.H + p.G)
-      base = reinterpret_cast<const T*>(p.k) + n * p.k_stride + (long long)(row - p.H) * D;
-    else
-      base = reinterpret_cast<const T*>(p.v) + n * p.v_stride + (long long)(row - p.H - p.G) * D;
-    return reinterpret_cast<const uint4*>(base) + at;
-  };
+  constexpr int N = Vec::kN, LANES = D / N, STEP = 32 / LANES;
   uint4 raw[kRows];
   auto load = [&](int row0) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       raw[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (row0 + j * STEP < rows) raw[j] = *source(row0 + j * STEP);
+      const int row = row0 + j * STEP + me.sub;
+      if (row < hi) raw[j] = *source(row);
     }
   };
-  load(first);
-
-  // angles of this lane's elements: element e belongs to pair e / 2 (interleaved) or e mod R / 2
-  float c[N], s[N];
-  long long slot = n;
+  load(lo);
+  // the factors of this lane's elements: element e belongs to pair e / 2 (interleaved) or e mod R / 2
+  float a[N], b[N];
   {
-    const int half = p.R / 2;
-    int pos = 0;
-    if (p.R > 0) pos = p.positions[n];
-    if (p.slots) slot = p.slots[n];
-    const bool known = pos >= 0 && pos < p.max_position;
-    if (p.R > 0 && !known && threadIdx.x == 0) atomicOr(&g_status_rope, METIS_STATUS_BAD_POSITION);
-    const float* turn = p.cos_sin + (long long)pos * p.R;
-    const int e0 = at * N;
+    const int e0 = me.at * N, half = p.R / 2;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
+      a[i] = 1.f;
+      b[i] = 0.f;
     }
-    if (e0 < p.R) {
-      if (!known) {  // reads as zeros
+    if (me.turned) {
+      if (turn == nullptr) {  // a position outside the table: its row reads as zeros
 #pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = s[i] = 0.f;
-      } else if (interleaved) {
+        for (int i = 0; i < N; ++i) a[i] = 0.f;
+      } else if (me.inter) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          c[i] = turn[(e0 + i) / 2];
-          s[i] = turn[half + (e0 + i) / 2];
-          if (!(i & 1)) s[i] = -s[i];
+          a[i] = turn[(e0 + i) / 2];
+          b[i] = (i & 1) ? turn[half + (e0 + i) / 2] : -turn[half + (e0 + i) / 2];
         }
       } else {
         const bool low = e0 < half;
         const float4* t4 = reinterpret_cast<const float4*>(turn + (low ? e0 : e0 - half));
+        const float sign = low ? -1.f : 1.f;
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-          const float4 a = t4[i / 4], b = t4[half / 4 + i / 4];
-          const float sign = low ? -1.f : 1.f;
-          c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
-          s[i] = sign * b.x, s[i + 1] = sign * b.y, s[i + 2] = sign * b.z, s[i + 3] = sign * b.w;
+          const float4 c = t4[i / 4], s = t4[half / 4 + i / 4];
+          a[i] = c.x, a[i + 1] = c.y, a[i + 2] = c.z, a[i + 3] = c.w;
+          b[i] = sign * s.x, b[i + 1] = sign * s.y, b[i + 2] = sign * s.z, b[i + 3] = sign * s.w;
         }
       }
     }
+    if (weight != nullptr) {
+      const uint4* w4 = reinterpret_cast<const uint4*>(weight);
+      uint64_t w2[N / 2], m2[N / 2];
+      Vec::unpack(w4[me.at], w2);
+      Vec::unpack(w4[me.mate % LANES], m2);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        float w0, w1, m0, m1;
+        f2_unpack(w2[i], w0, w1);
+        f2_unpack(m2[i], m0, m1);
+        a[2 * i] *= w0;
+        a[2 * i + 1] *= w1;
+        b[2 * i] *= me.inter ? m1 : m0;
+        b[2 * i + 1] *= me.inter ? m0 : m1;
+      }
+    }
   }
-  const int half_lanes = p.R / (2 * N);
-  // the lane that holds this lane's partners (interleaved, or not rotated: itself)
-  const int mate = interleaved || at * N >= p.R ? lane : at < half_lanes ? lane + half_lanes : lane - half_lanes;
-  uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
-  if (p.q_weight) qw = reinterpret_cast<const uint4*>(p.q_weight)[at];
-  if (p.k_weight) kw = reinterpret_cast<const uint4*>(p.k_weight)[at];
-  if (p.slots && slot >= p.total_slots) {
-    if (threadIdx.x == 0) atomicOr(&g_status_rope, METIS_STATUS_BAD_BLOCK_ID);
-    slot = -1;
+  uint64_t a2[N / 2], b2[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    a2[i] = f2_pack(a[2 * i], a[2 * i + 1]);
+    b2[i] = f2_pack(b[2 * i], b[2 * i + 1]);
   }
-
-  const int warp_first = (threadIdx.x >> 5) * PER_WARP;
-  for (int row0 = first, w0 = warp_first; w0 < rows; row0 += kRows * STEP, w0 += kRows * STEP) {
-    if (w0 != warp_first) load(row0);
+  for (int row0 = lo; row0 < hi; row0 += kRows * STEP) {
+    if (row0 != lo) load(row0);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (w0 + j * STEP >= rows) break;  // (uniform over the warp)
-      const int row = row0 + j * STEP;
-      uint4 out = raw[j];
-      const bool is_q = row < p.H, is_v = row >= p.H + p.G;
-      if (w0 + j * STEP < p.H + p.G) {  // a warp with a query or a key: all lanes take part in the shuffles
-        float x[N];
-        Vec::unpack(raw[j], x);
-        const bool norm_q = p.q_weight != nullptr, norm_k = p.k_weight != nullptr;
-        if (norm_q || norm_k) {
-          float y[N], w[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) y[i] = x[i];
-          Vec::unpack(is_q ? qw : kw, w);
-          normalise<D, N, LANES>(y, w, p.eps);
-          if (is_q ? norm_q : norm_k) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = y[i];
-          }
+      if (row0 + j * STEP >= hi) break;  // (uniform over the warp)
+      uint64_t x[N / 2], m[N / 2];
+      Vec::unpack(raw[j], x);
+      uint4 other = make_uint4(0u, 0u, 0u, 0u);  // (not rotated: b is zero, and 0 * infinity is not)
+      if (p.R > 0) {
+        uint4 got = raw[j];
+        if (!me.inter) {  // (uniform)
+          got.x = __shfl_sync(0xffffffffu, raw[j].x, me.mate);
+          got.y = __shfl_sync(0xffffffffu, raw[j].y, me.mate);
+          got.z = __shfl_sync(0xffffffffu, raw[j].z, me.mate);
+          got.w = __shfl_sync(0xffffffffu, raw[j].w, me.mate);
         }
-        if (p.R > 0) {
-          float z[N];
-          if (interleaved) {
+        if (me.turned) other = got;
+      }
+      Vec::unpack(other, m);
+      if (me.inter) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = x[i ^ 1];
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = __shfl_sync(0xffffffffu, x[i], mate);
-          }
-          if (at * N < p.R) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = fmaf(x[i], c[i], z[i] * s[i]);
-          }
+        for (int i = 0; i < N / 2; ++i) {
+          float m0, m1;
+          f2_unpack(m[i], m0, m1);
+          m[i] = f2_pack(m1, m0);
         }
-        if (!is_v) out = Vec::pack(x);
       }
-      if (row >= rows) continue;
-      if (is_q) {
-        reinterpret_cast<uint4*>(p.q_out)[(n * p.H + row) * LANES + at] = out;
-      } else if (slot >= 0) {
-        uint4* to = reinterpret_cast<uint4*>(is_v ? p.v_out : p.k_out);
-        to[(slot * p.G + (row - p.H - (is_v ? p.G : 0))) * LANES + at] = out;
+      float f = 1.f;
+      if (weight != nullptr) {
+        auto squares = [&]() {
+          uint64_t s2 = f2_mul(x[0], x[0]);
+#pragma unroll
+          for (int i = 1; i < N / 2; ++i) s2 = f2_fma(x[i], x[i], s2);
+          float s0, s1;
+          f2_unpack(s2, s0, s1);
+          return row_sum<LANES>(s0 + s1);
+        };
+        float ss = squares(), eps = p.eps;
+        // Squares that leave fp32's range are taken of x times a power of two, which eps takes along: exact, and rare.
+        const float up = !(ss < 1.3e36f) ? 8.271806e-25f /* 2^-80 */ : ss + eps < 1e-30f ? 1.2089258e24f /* 2^80 */ : 1.f;
+        if (__any_sync(0xffffffffu, up != 1.f)) {
+          const uint64_t up2 = f2_pack(up, up);
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            x[i] = f2_mul(x[i], up2);
+            m[i] = f2_mul(m[i], up2);
+          }
+          ss = squares();
+          eps = eps * up * up;
+        }
+        f = rsqrtf(fmaf(ss, 1.0f / D, eps));
       }
+      const uint64_t f2 = f2_pack(f, f);
+      float y[N];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const uint64_t v = f2_mul(f2_fma(m[i], b2[i], f2_mul(x[i], a2[i])), f2);
+        f2_unpack(v, y[2 * i], y[2 * i + 1]);
+      }
+      const int row = row0 + j * STEP + me.sub;
+      if (row < hi) target(row, Vec::pack(y));
+    }
+  }
+}
+
+// The rows of a token: 0 .. H - 1 are queries, then G keys, then (v given) G values.  `share` warps take
+// `chunk` of them each.
+template <typename T, int D>
+__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeParams p, const int interleaved,
+                                                                       const int num_tokens, const int share,
+                                                                       const int chunk) {
+  constexpr int N = RopeVec<T>::kN, LANES = D / N, STEP = 32 / LANES;  // STEP: rows of the warp at a time
+  pdl_launch_dependents();
+  pdl_wait();  // rows, positions and slots may be what the kernel in front writes
+  const long long item = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const long long n = item / share;
+  if (n >= num_tokens) return;
+  const int lane = threadIdx.x & 31;
+  const int lo = (int)(item - n * share) * chunk, hi = min(p.H + (p.v ? 2 : 1) * p.G, lo + chunk);
+
+  long long slot = n;
+  if (p.slots && hi > p.H) {
+    slot = p.slots[n];
+    if (slot >= p.total_slots) {
+      if (lane == 0) atomicOr(&g_status_rope, METIS_STATUS_BAD_BLOCK_ID);
+      slot = -1;
+    }
+  }
+  const float* turn = nullptr;
+  if (p.R > 0 && lo < p.H + p.G) {
+    const int pos = p.positions[n];
+    if (pos >= 0 && pos < p.max_position)
+      turn = p.cos_sin + (long long)pos * p.R;
+    else if (lane == 0)
+      atomicOr(&g_status_rope, METIS_STATUS_BAD_POSITION);
+  }
+  RopeLane me;
+  me.at = lane % LANES;
+  me.sub = lane / LANES;
+  me.turned = me.at * N < p.R;
+  me.inter = interleaved != 0;
+  const int half_lanes = p.R / (2 * N);
+  me.mate = interleaved || !me.turned ? lane : me.at < half_lanes ? lane + half_lanes : lane - half_lanes;
+
+  if (lo < p.H) {
+    const T* from = reinterpret_cast<const T*>(p.q) + n * p.q_stride;
+    uint4* to = reinterpret_cast<uint4*>(p.q_out) + n * p.H * LANES + me.at;
+    turn_rows<T, D>(p, me, turn, p.q_weight, lo, min(hi, p.H),
+                    [&](int row) { return reinterpret_cast<const uint4*>(from + row * D) + me.at; },
+                    [&](int row, const uint4& v) { to[row * LANES] = v; });
+  }
+  if (slot < 0) return;  // a padding row: neither its key nor its value is written
+  if (hi > p.H && lo < p.H + p.G) {
+    const T* from = reinterpret_cast<const T*>(p.k) + n * p.k_stride;
+    uint4* to = reinterpret_cast<uint4*>(p.k_out) + slot * p.G * LANES + me.at;
+    turn_rows<T, D>(p, me, turn, p.k_weight, max(lo - p.H, 0), min(hi - p.H, p.G),
+                    [&](int row) { return reinterpret_cast<const uint4*>(from + row * D) + me.at; },
+                    [&](int row, const uint4& v) { to[row * LANES] = v; });
+  }
+  if (hi > p.H + p.G) {
+    const T* from = reinterpret_cast<const T*>(p.v) + n * p.v_stride;
+    uint4* to = reinterpret_cast<uint4*>(p.v_out) + slot * p.G * LANES + me.at;
+    const int last = hi - p.H - p.G;
+    for (int row0 = max(lo - p.H - p.G, 0); row0 < last; row0 += kRows * STEP) {
+      uint4 raw[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (row0 + j * STEP + me.sub < last)
+          raw[j] = reinterpret_cast<const uint4*>(from + (row0 + j * STEP + me.sub) * D)[me.at];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (row0 + j * STEP + me.sub < last) to[(row0 + j * STEP + me.sub) * LANES] = raw[j];
     }
   }
 }
@@ -283,9 +334,21 @@ static int norm_rope(const RopeParams& p, int num_tokens, int head_dim, int inte
       !aligned(p.k_weight, 16) || !aligned(p.cos_sin, 16) || !aligned(p.q_out, 16) || !aligned(p.k_out, 16) ||
       !aligned(p.v_out, 16) || !aligned(p.positions, 4) || !aligned(p.slots, 8))
     return fail(METIS_E_ALIGN, "tensors must be 16-byte aligned (positions: 4-byte, slot_mapping: 8-byte)");
-  const dim3 grid((unsigned)num_tokens), block(kRopeThreads);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(METIS_E_CUDA, "querying the SM count: %s", cudaGetErrorString(e));
+  // a token's rows, as often as a warp holds some at a time; few tokens: shared by as many warps as fill the GPU
+  const int step = 32 / (int)(head_dim / vec);
+  const long long rows = (long long)p.H + (pages ? 2 : 1) * (long long)p.G, steps = (rows + step - 1) / step;
+  const long long want = std::max<long long>(1, std::min<long long>(steps, (long long)kRopeFill * sms / num_tokens));
+  const long long chunk = (steps + want - 1) / want * step, share = (rows + chunk - 1) / chunk;
+  if (rows * head_dim > 0x7fffffffLL) return fail(METIS_E_SHAPE, "too many heads");
+  const long long ctas = (share * num_tokens + kRopeWarps - 1) / kRopeWarps;
+  if (ctas > 0x7fffffffLL) return fail(METIS_E_SHAPE, "too many rows");
   auto launch = [&](auto kern) {
-    return launch_dependent(kern, grid, block, 0, st, "qk_norm_rope_kernel launch", p, interleaved ? 1 : 0);
+    return launch_dependent(kern, dim3((unsigned)ctas), dim3(kRopeWarps * 32), 0, st, "qk_norm_rope_kernel launch", p,
+                            interleaved ? 1 : 0, num_tokens, (int)share, (int)chunk);
   };
   if (dtype == METIS_F32)
     return head_dim == 64 ? launch(qk_norm_rope_kernel<float, 64>) : launch(qk_norm_rope_kernel<float, 128>);

@@ -82,7 +82,7 @@ struct PrefixParts {
   }
 
   __device__ __forceinline__ void add(JoinedRow& row, int h, int d) const {
-    constexpr int kBatch = 4;  // loads in flight
+    constexpr int kBatch = 8;  // loads in flight
     for (int k = 0; k < count; k += kBatch) {
       float x[kBatch];
       float4 v[kBatch];
@@ -102,11 +102,11 @@ struct PrefixParts {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kBf16Warps * 32) decode_shared_kernel(const __grid_constant__ CUtensorMap tmK,
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 32) decode_shared_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                         const __grid_constant__ CUtensorMap tmV,
                                                                         const SharedParams sp) {
-  constexpr int NW = kBf16Warps, STAGES = kBf16Stages, STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
+  constexpr int STAGES = kBf16Stages, STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
   const DecodeParams& p = sp.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
@@ -185,18 +185,18 @@ static size_t shared_bytes(int num_seqs, int num_heads, int num_kv_heads, int he
   return shared_plan_bytes(num_groups) + shared_lse_bytes(parts) * (1 + (size_t)head_dim);
 }
 
-template <int D>
+template <int D, int NW>
 static int launch_shared(const SharedParams& sp, const SharedArgs& a, int parts, cudaStream_t st) {
   CUtensorMap tmK, tmV;
   int rc = encode_kv_maps<D>(sp.d, a.k_cache, a.v_cache, &tmK, &tmV);
   if (rc) return rc;
-  constexpr int smem = bf16_decode_smem_bytes<D, kBf16Warps, kBf16Stages>();
+  constexpr int smem = bf16_decode_smem_bytes<D, NW, kBf16Stages>();
   static int done = 0;
-  auto kern = decode_shared_kernel<D>;
+  auto kern = decode_shared_kernel<D, NW>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
   return launch_dependent_cluster(kern, dim3((unsigned)a.G, (unsigned)parts, (unsigned)a.S),
-                                  dim3(1, (unsigned)parts, 1), dim3(kBf16Warps * 32), (size_t)smem, st,
+                                  dim3(1, (unsigned)parts, 1), dim3(NW * 32), (size_t)smem, st,
                                   "decode_shared_kernel launch", tmK, tmV, sp);
 }
 
@@ -295,6 +295,10 @@ extern "C" int metis_paged_attn_decode_shared(const void* q, const void* k_cache
   sp.part_out = part_out;
   sp.num_groups = num_groups;
   sp.Tq = kSharedRows / r;
-  const int parts = item_parts((long long)num_kv_heads * num_seqs, a.cap, sms);
-  return head_dim == 64 ? launch_shared<64>(sp, a, parts, st) : launch_shared<128>(sp, a, parts, st);
+  const long long items = (long long)num_kv_heads * num_seqs;
+  const int parts = item_parts(items, a.cap, sms);
+  if (one_warp_items(items, sms))
+    return head_dim == 64 ? launch_shared<64, 1>(sp, a, 1, st) : launch_shared<128, 1>(sp, a, 1, st);
+  return head_dim == 64 ? launch_shared<64, kBf16Warps>(sp, a, parts, st)
+                        : launch_shared<128, kBf16Warps>(sp, a, parts, st);
 }

@@ -13,11 +13,12 @@
 // so that a captured decode loop advances without the host (lengths, page counts and the stack's
 // depth may be updated in place).
 //
-// Bound by latency: a step of 64 tokens moves 2 KB, 400,000 rows 5 MB.  One cluster of up to
-// kMaxCluster CTAs: every CTA scans all lengths itself (4,096 sequences at a time, four per thread; two
-// scans, tokens and then pages), the cluster's barrier separates the reads of those lengths from
-// their update, and the CTAs share the rows.  Every page's first row also writes its table entry
-// and reference count, so pages need no pass of their own.
+// Bound by latency: a step of 64 tokens moves 2 KB, 400,000 rows 5 MB.  Every CTA of a cluster scans all
+// lengths itself (four sequences per thread and round; two scans, tokens and then pages), the cluster's
+// barrier separates the reads of those lengths from their update, and the CTAs share the pages and rows.  A
+// small step is one CTA of 256 threads: its barriers are the time.  Many rows would keep the cluster's eight
+// SMs busy with finding each row's sequence: a second kernel fills them, on every SM, from the offsets,
+// lengths and table that the first one wrote.
 #include <algorithm>
 
 #include "../../include/metis_attn.h"
@@ -29,11 +30,14 @@ namespace metis {
 
 __device__ unsigned int g_status_plan = 0;
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanPer = 4;                            // sequences per thread and scan
-constexpr int kPlanSeqs = kPlanThreads * kPlanPer;     // sequences per scan
-constexpr int kPlanTile = 128;                         // rows a warp takes at a time
+constexpr int kPlanPer = 4;          // sequences per thread and round
+constexpr int kPlanTile = 128;       // rows a warp takes at a time
 constexpr int kMaxCluster = 8;
+constexpr int kPlanSmall = 256;      // threads of a small step's one CTA: up to kPlanSmall * kPlanPer sequences,
+constexpr int kPlanSmallRows = 2048; // and rows
+constexpr int kPlanWide = 1024;
+constexpr int kPlanOwnRows = 8192;   // more rows are left to the second kernel
+constexpr int kRowWarps = 4;
 
 struct PlanParams {
   const int32_t* q_lens;
@@ -52,16 +56,18 @@ struct PlanParams {
   int S, T, bs, max_blocks, num_blocks, free_capacity;
 };
 
-// What a CTA keeps of each sequence of the current scan
+// What a CTA keeps of the sequences of the current round
+template <int NT>
 struct PlanSeqs {
-  int cu[kPlanSeqs + 1];  // first row
-  int before[kPlanSeqs];  // cached tokens
-  int held[kPlanSeqs];    // pages in its table row
-  int rank[kPlanSeqs];    // (first new page's place in the order of taking) - held
+  int cu[NT * kPlanPer + 1];  // first row
+  int before[NT * kPlanPer];  // cached tokens
+  int held[NT * kPlanPer];    // pages in its table row
+  int page[NT * kPlanPer];    // its first new page, in the order of taking
 };
 
 // Exclusive prefix of one value per thread, sums held at `top` (the sums of a batch may pass it:
 // min(a + b, top) adds up in any order); *total: of all.
+template <int NT>
 __device__ __forceinline__ int plan_scan(int v, int top, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto add = [top](int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)top); };
@@ -79,27 +85,39 @@ __device__ __forceinline__ int plan_scan(int v, int top, int* warp_sums, int* to
   __syncthreads();  // the last scan's sums were read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) warp_sums[lane] = inclusive(warp_sums[lane]);
-  __syncthreads();
-  *total = warp_sums[kPlanThreads / 32 - 1];
-  return warp > 0 ? add(left, warp_sums[warp - 1]) : left;
+  // every warp sums the warps for itself: one barrier less
+  const int sums = inclusive(lane < NT / 32 ? warp_sums[lane] : 0);
+  *total = __shfl_sync(0xffffffffu, sums, NT / 32 - 1);
+  const int front = __shfl_sync(0xffffffffu, sums, max(warp - 1, 0));
+  return warp > 0 ? add(left, front) : left;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParams p) {
+// The last of v[lo .. hi] at or below x (v[lo] is)
+__device__ __forceinline__ int plan_find(const int* v, int lo, int hi, int x) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int NT, bool ROWS>
+__global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
+  constexpr int SEQS = NT * kPlanPer;
   extern __shared__ uint8_t plan_smem[];
-  PlanSeqs& seqs = *reinterpret_cast<PlanSeqs*>(plan_smem);
-  __shared__ int warp_sums[kPlanThreads / 32];
-  static_assert(kPlanThreads == 32 * 32, "one warp scans the warp sums");
+  PlanSeqs<NT>& seqs = *reinterpret_cast<PlanSeqs<NT>*>(plan_smem);
+  __shared__ int warp_sums[NT / 32];
   pdl_launch_dependents();
   pdl_wait();  // lengths, table and stack may be what the kernel in front writes
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int ctas = gridDim.x, cta = blockIdx.x;  // the grid is one cluster
+  const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;  // the grid is one cluster
   const int depth = min(max(*p.free_count, 0), p.free_capacity);
-  const int all_warps = ctas * (kPlanThreads / 32), my_warp = cta * (kPlanThreads / 32) + (tid >> 5);
 
-  int rows = 0, taken = 0;  // by the scans before this one
-  for (int base = 0; base < p.S; base += kPlanSeqs) {
-    const int n_seqs = min(p.S - base, kPlanSeqs);
+  int rows = 0, taken = 0;  // by the rounds before this one
+  for (int base = 0; base < p.S; base += SEQS) {
+    const int n_seqs = min(p.S - base, SEQS);
     int n[kPlanPer], before[kPlanPer], held[kPlanPer];
     int sum = 0;
     unsigned bad = 0;
@@ -111,16 +129,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
         n[i] = p.q_lens[base + s];
         before[i] = p.cached_lens[base + s];
         if (p.held_blocks) held[i] = p.held_blocks[base + s];
-        if (n[i] < 0 || before[i] < 0) bad |= METIS_STATUS_BAD_Q_LEN;
-        n[i] = max(n[i], 0);
-        before[i] = max(before[i], 0);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+      if (n[i] < 0 || before[i] < 0) bad |= METIS_STATUS_BAD_Q_LEN;
+      n[i] = max(n[i], 0);
+      before[i] = max(before[i], 0);
       sum = (int)min((unsigned)sum + (unsigned)n[i], (unsigned)p.T);
     }
     int total;
     const int left = p.T - rows;  // rows that the call still has
-    const int first = plan_scan(min(sum, left), left, warp_sums, &total);
-    int at = first, pages = 0, take[kPlanPer];
+    int at = plan_scan<NT>(min(sum, left), left, warp_sums, &total), pages = 0, take[kPlanPer];
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
       const int s = tid * kPlanPer + i;
@@ -143,12 +163,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
       at += n[i];
     }
     int total_pages;
-    int rank = taken + plan_scan(pages, 0x7fffffff, warp_sums, &total_pages);
+    int first = taken + plan_scan<NT>(pages, 0x7fffffff, warp_sums, &total_pages);
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
       const int s = tid * kPlanPer + i;
-      if (s < n_seqs) seqs.rank[s] = rank - held[i];
-      rank += take[i];
+      if (s < n_seqs) seqs.page[s] = first;
+      first += take[i];
     }
     if (tid == 0) seqs.cu[n_seqs] = rows + total;
     if (tid == 0 && taken + total_pages > depth) bad |= METIS_STATUS_OUT_OF_PAGES;
@@ -166,46 +186,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
         p.seq_lens[base + s] = (int)min((unsigned)before[i] + (unsigned)n[i], 0x7fffffffu);
         if (p.held_out) p.held_out[base + s] = held[i] + take[i];
         p.cu_q_lens[base + s] = seqs.cu[s];
+        if (!ROWS && n[i] > 0) {  // entries that the row names already and its new tokens use
+          const int last = min((before[i] + n[i] - 1) / p.bs, held[i] - 1);
+          for (int page = before[i] / p.bs; page <= last; ++page)
+            checked_block(p.block_table + (size_t)(base + s) * p.max_blocks, page, p.num_blocks, &g_status_plan);
+        }
       }
+    }
+    // per new page
+    for (int k = taken + cta * NT + tid; k < taken + total_pages; k += ctas * NT) {
+      const int s = plan_find(seqs.page, 0, n_seqs - 1, k);
+      int block = -1;
+      if (k < depth) block = checked_block(p.free_stack, depth - 1 - k, p.num_blocks, &g_status_plan);
+      p.block_table[(size_t)(base + s) * p.max_blocks + seqs.held[s] + (k - seqs.page[s])] = block;
+      if (p.refcount && block >= 0) p.refcount[block] = 1;
     }
     // per row
     const int end = rows + total;
-    for (long long tile = (long long)rows + (long long)my_warp * kPlanTile; tile < end;
-         tile += (long long)all_warps * kPlanTile) {
-      int s = -1;
-#pragma unroll 1
-      for (int j = 0; j < kPlanTile; j += 32) {
-        const long long row_ll = tile + j + lane;
-        if (row_ll >= end) break;
-        const int row = (int)row_ll;
-        // the last sequence that begins at or before the row: a few steps on, else by halves
-        int lo = max(s, 0), hi = n_seqs - 1;
-        if (s >= 0)
-          for (int step = 0; step < 4 && lo < hi; ++step) {
-            if (seqs.cu[lo + 1] > row) hi = lo;
-            else ++lo;
-          }
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (seqs.cu[mid] <= row) lo = mid;
-          else hi = mid - 1;
-        }
-        s = lo;
+    if constexpr (ROWS) {
+      for (int row = rows + cta * NT + tid; row < end; row += ctas * NT) {
+        const int s = plan_find(seqs.cu, 0, n_seqs - 1, row);
         const unsigned pos = (unsigned)seqs.before[s] + (unsigned)(row - seqs.cu[s]);
         const unsigned page = pos / (unsigned)p.bs, off = pos - page * (unsigned)p.bs;
         int block = -1;
-        if (page < (unsigned)p.max_blocks) {
-          int32_t* entry = p.block_table + (size_t)(base + s) * p.max_blocks + page;
-          if ((int)page < seqs.held[s]) {
-            block = checked_block(entry, 0, p.num_blocks, &g_status_plan);
-          } else {
-            const int k = seqs.rank[s] + (int)page;  // in the order of taking
-            if (k < depth) block = checked_block(p.free_stack, depth - 1 - k, p.num_blocks, &g_status_plan);
-            if (off == 0) {  // the page's first row
-              *entry = block;
-              if (p.refcount && block >= 0) p.refcount[block] = 1;
-            }
-          }
+        if ((int)page < seqs.held[s]) {
+          block = checked_block(p.block_table + (size_t)(base + s) * p.max_blocks, (int)page, p.num_blocks, &g_status_plan);
+        } else if (page < (unsigned)p.max_blocks) {
+          const int k = seqs.page[s] + (int)page - seqs.held[s];
+          if (k < depth) block = checked_block(p.free_stack, depth - 1 - k, p.num_blocks, &g_status_plan);
         }
         p.slot_mapping[row] = block < 0 ? -1 : (int64_t)block * p.bs + off;
         p.positions[row] = (int)min(pos, 0x7fffffffu);
@@ -213,16 +221,73 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanParam
     }
     rows += total;
     taken += total_pages;
-    __syncthreads();  // the next scan overwrites the sequences
+    __syncthreads();  // the next round overwrites the sequences
   }
-  // rows behind the last sequence's: padding
-  for (long long row = (long long)rows + cta * kPlanThreads + tid; row < p.T; row += (long long)ctas * kPlanThreads) {
-    p.slot_mapping[row] = -1;
-    p.positions[row] = 0;
+  if constexpr (ROWS) {  // rows behind the last sequence's: padding
+    for (int row = rows + cta * NT + tid; row < p.T; row += ctas * NT) {
+      p.slot_mapping[row] = -1;
+      p.positions[row] = 0;
+    }
   }
   if (cta == 0 && tid == 0) {
     p.cu_q_lens[p.S] = rows;
     *p.free_count_out = max(depth - taken, 0);  // every CTA read the depth before the first barrier
+  }
+}
+
+// The rows of a step from its offsets, lengths and table.  A warp finds the sequence of its tile's first
+// row by thirty-two probes at a time; the offsets of the 32 sequences from there on, one per lane, then
+// place every row by shuffles.  (Shorter sequences: by halves, in memory.)
+__global__ void __launch_bounds__(kRowWarps * 32) plan_rows_kernel(const PlanParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long tile = ((long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * kPlanTile;
+  if (tile >= p.T) return;
+  const int* cu = p.cu_q_lens;
+  int lo = 0, n = p.S;  // the last of cu[0 .. S - 1] at or below the tile's first row
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = min(lane * step, n - 1);
+    const int before = __popc(__ballot_sync(0xffffffffu, lane * step < n && cu[lo + at] <= (int)tile));
+    lo += (before - 1) * step;  // (cu[0] = 0: the first probe counts)
+    n = min(step, n - (before - 1) * step);
+  }
+  const int rows = cu[p.S];
+  const int edge = cu[min(lo + 1 + lane, p.S)];  // where the sequences from lo + 1 on begin
+  const bool near = __shfl_sync(0xffffffffu, edge, 31) > min((int)tile + kPlanTile, rows) - 1;
+  constexpr int J = kPlanTile / 32;
+  int s[J], from[J], pos[J], block[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int row = (int)min(tile + j * 32 + lane, (long long)p.T - 1);
+    int k = 0;  // sequences from lo + 1 on that begin at or before the row
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (__shfl_sync(0xffffffffu, edge, k + o - 1) <= row) k += o;
+    s[j] = min(lo + k, p.S - 1);
+    if (!near) s[j] = plan_find(cu, lo, p.S - 1, row);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    from[j] = cu[s[j] + 1];
+    pos[j] = p.seq_lens[s[j]];
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const long long row = tile + j * 32 + lane;
+    pos[j] -= from[j] - (int)row;
+    const int page = pos[j] / p.bs;
+    block[j] = -1;
+    if (row < rows && page >= 0 && page < p.max_blocks) block[j] = p.block_table[(size_t)s[j] * p.max_blocks + page];
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const long long row = tile + j * 32 + lane;
+    if (row >= p.T) continue;
+    const bool fine = block[j] >= 0 && block[j] < p.num_blocks;  // (else flagged by the kernel in front)
+    p.slot_mapping[row] = fine ? (int64_t)block[j] * p.bs + pos[j] % p.bs : -1;
+    p.positions[row] = row < rows ? pos[j] : 0;
   }
 }
 
@@ -285,11 +350,24 @@ extern "C" int metis_plan_step(const int32_t* q_lens, const int32_t* cached_lens
   p.max_blocks = max_blocks;
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
-  static int done = 0;
-  const int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(plan_step_kernel), (int)sizeof(PlanSeqs), &done);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (num_seqs <= kPlanSmall * kPlanPer && num_tokens <= kPlanSmallRows)
+    return launch_dependent(plan_step_kernel<kPlanSmall, true>, dim3(1), dim3(kPlanSmall), sizeof(PlanSeqs<kPlanSmall>), st,
+                            "plan_step_kernel launch", p);
+  // (positions within int32: the second kernel counts them back from the lengths)
+  const bool own_rows = num_tokens <= kPlanOwnRows || (long long)max_blocks * block_size > 0x7fffffffLL - num_tokens;
+  auto launch = [&](auto kern, int ctas, int* done) {
+    const int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), (int)sizeof(PlanSeqs<kPlanWide>), done);
+    if (rc) return rc;
+    return launch_dependent_cluster(kern, dim3((unsigned)ctas), dim3((unsigned)ctas), dim3(kPlanWide),
+                                    sizeof(PlanSeqs<kPlanWide>), st, "plan_step_kernel launch", p);
+  };
+  static int done_rows = 0, done = 0;
+  if (own_rows)
+    return launch(plan_step_kernel<kPlanWide, true>,
+                  (int)std::min<long long>(kMaxCluster, 1 + num_tokens / (2 * kPlanWide)), &done_rows);
+  const int rc = launch(plan_step_kernel<kPlanWide, false>, kMaxCluster, &done);
   if (rc) return rc;
-  // a CTA for every two tiles of its warps' rows
-  const int ctas = std::min(kMaxCluster, 1 + (num_tokens - 1) / (2 * kPlanThreads / 32 * kPlanTile));
-  return launch_dependent_cluster(plan_step_kernel, dim3(std::max(ctas, 1)), dim3(std::max(ctas, 1)), dim3(kPlanThreads),
-                                  sizeof(PlanSeqs), reinterpret_cast<cudaStream_t>(stream), "plan_step_kernel launch", p);
+  const unsigned ctas = (unsigned)((num_tokens - 1) / (kRowWarps * kPlanTile) + 1);
+  return launch_dependent(plan_rows_kernel, dim3(ctas), dim3(kRowWarps * 32), 0, st, "plan_rows_kernel launch", p);
 }
