@@ -97,6 +97,11 @@ constexpr int kRegsProd = PF_REGS_PROD;        // warpgroup 2: K/V producers
 constexpr int kRegsMma = PF_REGS_MMA;          // warpgroup 3: UMMA issuer, query loader, idle warps
 static_assert(128 * (2 * kRegsSoftmax + kRegsProd + kRegsMma) <= kPfThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
+// windows, shared prefixes: the issuer's uniform loop needs a few more
+constexpr int kRegsSoftmaxU = 208;
+constexpr int kRegsMmaU = 56;
+static_assert(128 * (2 * kRegsSoftmaxU + kRegsProd + kRegsMmaU) <= kPfThreads * kRegsLaunch,
+              "register split exceeds the launch allocation");
 // 8-bit cache: the converters in the last two warpgroups need more
 constexpr int kRegsSoftmax8 = 200;
 constexpr int kRegsOther8 = 56;
@@ -336,17 +341,18 @@ __device__ __forceinline__ int pf_kv_tiles(int L, int q_len, int tile, int Tq) {
   return (p_max + kKvTile) / kKvTile;
 }
 
-// Windows: of the keys before `oldest` the queries of a query-tile pair see the first `sinks` only: the
-// first `low` K/V tiles, and `skip` tiles behind them hold nothing that is seen.
+// Windows: what the queries of a query-tile pair see of a sequence, in whole pages: the pages of the first
+// tokens, then those from the first query's oldest key on.  Their tokens in a row are the unit's keys; its
+// K/V tiles, lengths and positions count along that row, in which the pages in between do not exist.
 struct PfSpan {
-  int oldest, low, skip;
+  int low, skip;  // pages of first tokens, pages left out behind them (none left out: low = skip = 0)
+  int sinks;      // the row's first tokens that every query sees
 };
 __device__ __forceinline__ PfSpan pf_span(const PrefillParams& p, int L, int q_len, int pair) {
-  PfSpan w;
-  w.oldest = max(L - q_len + 2 * pair * p.Tq - p.window + 1, 0);
-  const int ns = min(p.sinks, w.oldest), recent = w.oldest / kKvTile;
-  w.low = min(ns / kKvTile + (ns % kKvTile != 0), recent);
-  w.skip = recent - w.low;
+  const int oldest = max(L - q_len + 2 * pair * p.Tq - p.window + 1, 0);
+  const int ns = min(p.sinks, oldest), low = ns / p.bs + (ns % p.bs != 0), recent = oldest / p.bs;
+  PfSpan w{0, 0, p.sinks};
+  if (low < recent) w = PfSpan{low, recent - low, ns};
   return w;
 }
 
@@ -483,7 +489,10 @@ __global__ void __launch_bounds__(kSchedThreads) prefill_schedule_kernel(const P
     for (int t = 0; t < np; ++t, ++pos) {
       if ((unsigned)pos >= (unsigned)total) break;  // (offsets that decrease may list more than fits)
       int work = pf_kv_tiles(L, q_len, 2 * t, p.Tq) + pf_kv_tiles(L, q_len, 2 * t + 1, p.Tq);
-      if (p.window) work -= ((2 * t + 1) * p.Tq < q_len ? 2 : 1) * pf_span(p, L, q_len, t).skip;
+      if (p.window) {
+        const int row = L - pf_span(p, L, q_len, t).skip * p.bs;
+        work = pf_kv_tiles(row, q_len, 2 * t, p.Tq) + pf_kv_tiles(row, q_len, 2 * t + 1, p.Tq);
+      }
       const int4 it = make_int4(s, t, work, 0);
       if (p.splits) atomicMax(&longest, pf_kv_tiles(L, q_len, 2 * t, p.Tq));
       if (sort)
@@ -544,9 +553,10 @@ struct PfUnit8 : PfUnit {
   int tag;  // 0: all of them, else index among the split units << 8 | parts << 4 | part
 };
 
-// Windows: n0, n1 and n_kv count the visited tiles.
+// Windows: L, n_pages and the tiles are those of the unit's row of keys.
 struct PfUnitW : PfUnit {
   PfSpan w;
+  int a0, a1, b0;  // tiles [a0, a1) and from b0 on hold keys that some query of the unit does not see
 };
 
 // Shared prefixes: tiles [j0, j0 + n_kv) of the unit, part number `part`.
@@ -556,7 +566,6 @@ struct PfUnitS : PfUnit {
 
 // The K/V tile that the unit visits j-th
 __device__ __forceinline__ int pf_tile(const PfUnit&, int j) { return j; }
-__device__ __forceinline__ int pf_tile(const PfUnitW& it, int j) { return j < it.w.low ? j : j + it.w.skip; }
 
 __device__ __forceinline__ int pf_tile(const PfUnitS& it, int j) { return it.j0 + j; }
 
@@ -583,9 +592,16 @@ __device__ __forceinline__ bool pf_unit(const PrefillParams& p, int u, PfUnitW& 
   PfUnit& plain = it;
   if (!pf_unit(p, u, plain)) return false;
   it.w = pf_span(p, it.L, it.q_len, it.pair);
-  it.n0 -= it.w.skip;  // (the tile of the first query's oldest key comes before its own)
-  if (it.n1 > 0) it.n1 -= it.w.skip;
+  it.L -= it.w.skip * p.bs;
+  it.n_pages -= it.w.skip;
+  it.n0 = pf_kv_tiles(it.L, it.q_len, 2 * it.pair, p.Tq);
+  it.n1 = pf_kv_tiles(it.L, it.q_len, 2 * it.pair + 1, p.Tq);
   it.n_kv = max(it.n0, it.n1);
+  const int first = it.L - it.q_len + 2 * it.pair * p.Tq;
+  const int last = it.L - it.q_len + min(it.q_len, (2 * it.pair + 2) * p.Tq) - 1;
+  it.a0 = it.w.sinks / kKvTile;
+  it.a1 = last >= p.window ? (last - p.window) / kKvTile + 1 : 0;
+  it.b0 = (first + 1) / kKvTile;
   return true;
 }
 
@@ -597,11 +613,8 @@ __device__ __forceinline__ int pf_last_query(const PrefillParams& p, const PfUni
   return it.L - it.q_len + min(it.q_len, (2 * it.pair + 2) * p.Tq) - 1;
 }
 
-// Windows: does the K/V tile at token tok0 hold tokens that some query of the unit does not see?
-__device__ __forceinline__ bool pf_partial(const PrefillParams& p, const PfUnitW& it, int tok0) {
-  return tok0 + kKvTile - 1 > pf_first_query(p, it) ||
-         (tok0 <= pf_last_query(p, it) - p.window && tok0 + kKvTile > p.sinks);
-}
+// Windows: does the unit's K/V tile j hold keys that some of its queries do not see?
+__device__ __forceinline__ bool pf_partial(const PfUnitW& it, int j) { return (j >= it.a0 && j < it.a1) || j >= it.b0; }
 
 // Any infinity or NaN among eight bf16
 __device__ __forceinline__ bool any_nonfinite_bf16(const uint4& v) {
@@ -621,9 +634,10 @@ __device__ __forceinline__ void add_odd_tokens(const PrefillParams& p, const PfU
   for (int i = 0; i < 2 * span; ++i) {
     if (!((*reinterpret_cast<const volatile uint32_t*>(odd + i / 32) >> (i % 32)) & 1u)) continue;
     const int t = i < span ? i + p_first - p.window + 1 : i - span + p_first + 1;
-    const bool sees = q && t <= p_row && (t > p_row - p.window || t < p.sinks);
+    const bool sees = q && t <= p_row && (t > p_row - p.window || t < it.w.sinks);
     const int page = t / p.bs;
-    const int b = checked_block(p.block_table + (size_t)it.s * p.max_blocks, page, p.num_blocks, &g_status_prefill);
+    const int b = checked_block(p.block_table + (size_t)it.s * p.max_blocks, page < it.w.low ? page : page + it.w.skip,
+                                p.num_blocks, &g_status_prefill);
     const size_t row = (((size_t)max(b, 0) * p.bs + (t - page * p.bs)) * p.G + it.g) * D;
     float weight = 0.f;
     if (sees) {
@@ -812,6 +826,7 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
 // leaves the plan for the kernel behind.
 struct PfShare {
   int begin, end, group, x, unit;
+  PfGroup now;  // the group
 };
 
 __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
@@ -852,6 +867,7 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
       mine.group = g0 + tid;
       mine.x = my_x;
       mine.unit = my_unit;
+      mine.now = v;
     }
   };
   if (p.num_groups <= kPfThreads) {
@@ -867,6 +883,7 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
   s.group = mine.group;
   s.x = mine.x;
   s.unit = mine.unit;
+  s.now = mine.now;
   return s;
 }
 
@@ -888,6 +905,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   using Sh = PfShape<D, KV8>;
   constexpr int HALVES = Sh::kHalves;
   constexpr int kStages8 = kV8Stages;
+  constexpr int kOther = KV8 ? kRegsOther8 : WINDOW || SHARED ? kRegsMmaU : kRegsMma;  // registers of the last warpgroup
   static_assert(KV8 || !SPLIT, "parts of units: 8-bit cache only");
   static_assert(!(WINDOW && KV8), "windows: bf16 cache only");
   static_assert(!(SHARED && (WINDOW || KV8)), "shared prefixes: bf16 cache only");
@@ -1176,10 +1194,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       for (int j = 0; j < it.n_kv; ++j, ++t) {
         const int st = t % depth;
         const int lp = part * half_pg + lane;  // page index inside the tile
-        const int pg = pf_tile(it, j) * npg + lp;
-        bool live = lane < half_pg && pg < it.n_pages;
-        if constexpr (WINDOW)  // a page that no query of the unit sees may have been given back
-          live = live && (pg * p.bs < p.sinks || pg * p.bs + p.bs > it.w.oldest);
+        int pg = pf_tile(it, j) * npg + lp;
+        const bool live = lane < half_pg && pg < it.n_pages;
+        if constexpr (WINDOW) pg += pg < it.w.low ? 0 : it.w.skip;
         int rowc = 0;
         if (live) {
           const int b = checked_block(bt_row, pg, p.num_blocks, &g_status_prefill);
@@ -1203,14 +1220,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       for (uint32_t k = t > (uint32_t)depth ? t - depth : 0; k < t; ++k)
         mbar_wait(&full[k % depth], (k / depth) & 1, &g_status_prefill);
     }
-  } else if (KV8 && warp == kMmaWarp) {
-    // ------------------------------------------------------------ 8-bit cache: UMMA issuer
+  } else if ((KV8 || WINDOW || SHARED) && warp == kMmaWarp) {
+    // ------------------------------------------------------------ UMMA issuer (8-bit cache, windows, shared prefixes)
     // The same order of products as below, PV0_j, QK0_{j+1}, PV1_j, QK1_{j+1}.  Everything
     // the instructions' operands come from is kept uniform over the warp (values from
     // shared memory by shuffle, outcomes of waits by vote, ring positions counted instead
     // of divided), so that descriptors are built on the uniform datapath.
-    regs_dec<kRegsOther8>();
-    constexpr uint32_t kIdQK = umma_idesc_e4m3_f32(kRows, kKvTile);
+    regs_dec<kOther>();
+    constexpr uint32_t kIdQK = KV8 ? umma_idesc_e4m3_f32(kRows, kKvTile) : umma_idesc_bf16_f32(kRows, kKvTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_bf16_f32(kRows, D, false, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t q_at = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
@@ -1218,16 +1235,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const uint32_t v_at = __shfl_sync(0xffffffffu, smem_u32(sV), 0);
     uint32_t k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;   // next K and V tile: ring stage, phase parity
     uint32_t p_ph[2] = {0u, 0u}, u = 0, n_two = 0;     // p_full parities; units; units with two query tiles
+    [[maybe_unused]] uint32_t looked = 0;              // windows: per V stage, v_ready's parity
     bool ok = true, issued = false;
-    auto qk = [&](int w) {  // S_w = (hi_w + lo_w) codes^T of the K tile in stage k_st, 32 dims per instruction
+    auto qk = [&](int w) {  // S_w = Q_w K^T of the K tile in stage k_st (8-bit: (hi_w + lo_w) codes^T, 32 dims per instruction)
       const uint32_t a = q_at + w * Sh::kQBytes, b = k_at + k_st * Sh::kKBytes;
       if (elect_one()) {
+        if constexpr (KV8) {
 #pragma unroll
-        for (int kk = 0; kk < 2 * (D / 32); ++kk) {
-          const uint32_t qa = a + (kk / (D / 32)) * (D == 128 ? Sh::kQPart : 64) + (kk % (D / 32)) * 32;
-          const uint32_t ka = b + (kk % (D / 32)) * 32;
-          umma_e4m3(tm + w * kKvTile, umma_desc_sw128(qa, 16, 1024),
-                    D == 128 ? umma_desc_sw128(ka, 16, 1024) : umma_desc_sw64(ka, 512), kIdQK, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+            const uint32_t qa = a + (kk / (D / 32)) * (D == 128 ? Sh::kQPart : 64) + (kk % (D / 32)) * 32;
+            const uint32_t ka = b + (kk % (D / 32)) * 32;
+            umma_e4m3(tm + w * kKvTile, umma_desc_sw128(qa, 16, 1024),
+                      D == 128 ? umma_desc_sw128(ka, 16, 1024) : umma_desc_sw64(ka, 512), kIdQK, kk > 0 ? 1u : 0u);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t within = (kk & 3) * 32;
+            umma_bf16(tm + w * kKvTile, umma_desc_sw128(a + (kk >> 2) * Sh::kQHalf + within, 16, 1024),
+                      umma_desc_sw128(b + (kk >> 2) * Sh::kKvHalf + within, 16, 1024), kIdQK, kk > 0 ? 1u : 0u);
+          }
         }
         umma_commit(&s_full[w]);
       }
@@ -1251,18 +1278,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       const int index = __shfl_sync(0xffffffffu, unit_slot[slot], 0);
       const int n0 = __shfl_sync(0xffffffffu, unit_info[slot].n0, 0);
       const int n1 = __shfl_sync(0xffffffffu, unit_info[slot].n1, 0);
+      [[maybe_unused]] int a0 = 0, a1 = 0, b0 = 0, live = 0;
+      if constexpr (WINDOW) {  // the tiles that pf_partial tells
+        a0 = __shfl_sync(0xffffffffu, unit_info[slot].a0, 0);
+        a1 = __shfl_sync(0xffffffffu, unit_info[slot].a1, 0);
+        b0 = __shfl_sync(0xffffffffu, unit_info[slot].b0, 0);
+      }
+      if constexpr (SHARED)  // keys from the part's first tile on
+        live = __shfl_sync(0xffffffffu, unit_info[slot].L - unit_info[slot].j0 * kKvTile, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&unit_empty[slot]);  // release: the reads above are done
       if (index < 0) break;
       const int n_kv = max(n0, n1);
-      if (!(ok = wait_all(&x8.q_full[0], u & 1) && wait_all(&k_full[k_st], k_ph))) break;
+      if (!(ok = wait_all(KV8 ? &x8.q_full[0] : q_full, u & 1) && wait_all(&k_full[k_st], k_ph))) break;
       tc_fence_after_sync();
       issued = true;
       qk(0);
       if (n1 > 0) {
-        if (!(ok = wait_all(&x8.q_full[1], n_two & 1))) break;
-        ++n_two;
-        tc_fence_after_sync();
+        if constexpr (KV8) {
+          if (!(ok = wait_all(&x8.q_full[1], n_two & 1))) break;
+          ++n_two;
+          tc_fence_after_sync();
+        }
         qk(1);
       }
       commit(&k_empty[k_st]);
@@ -1270,6 +1307,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       if (++k_st == kKStages) k_st = 0, k_ph ^= 1;
       for (int j = 0; j < n_kv; ++j) {
         if (!(ok = wait_all(&v_full[v_st], v_ph))) break;
+        if constexpr (WINDOW) {
+          if ((j >= a0 && j < a1) || j >= b0) {
+            if (!(ok = wait_all(&xw.v_ready[v_st], (looked >> v_st) & 1))) break;
+            looked ^= 1u << v_st;
+          }
+        }
+        if constexpr (SHARED) {
+          if (live < (j + 1) * kKvTile) {
+            // rows past the prefix may hold anything (NaN included): zero them so that P = 0 stays 0
+            uint8_t* vb = sV + v_st * Sh::kKvBytes;
+            for (int row = live - j * kKvTile + lane; row < kKvTile; row += 32)
+              for (int h = 0; h < HALVES; ++h) {
+                uint4* d = reinterpret_cast<uint4*>(vb + h * Sh::kKvHalf + row * 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         const bool more = j + 1 < n_kv;
         bool k_ready = false;
 #pragma unroll
@@ -1310,7 +1367,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ UMMA issuer
-    regs_dec<kRegsMma>();
+    regs_dec<kOther>();
     constexpr uint32_t kIdQK = umma_idesc_bf16_f32(kRows, kKvTile, false, false);
     constexpr uint32_t kIdPV = umma_idesc_bf16_f32(kRows, D, false, true);
     bool issued = false;
@@ -1339,7 +1396,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       }
     };
     uint32_t t_base = 0, n_units = 0, np[2] = {0u, 0u};  // tiles, units, p_full phases consumed
-    [[maybe_unused]] uint32_t looked = 0;  // per V stage, v_ready's parity
     uint32_t k = 0;
     bool ok = true;
     Unit it;
@@ -1371,16 +1427,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           break;
         }
         tc_fence_after_sync();
-        const int tok0 = pf_tile(it, j) * kKvTile;
-        if constexpr (WINDOW) {
-          if (pf_partial(p, it, tok0)) {
-            if (!wait_all(&xw.v_ready[vst], (looked >> vst) & 1)) {
-              ok = false;
-              break;
-            }
-            looked ^= 1u << vst;
-          }
-        } else if (tok0 + kKvTile > it.L) {
+        const int tok0 = j * kKvTile;
+        if (tok0 + kKvTile > it.L) {
           // rows past the sequence end may hold anything (NaN included): zero them so that P = 0 stays 0
           uint8_t* vb = sV + vst * Sh::kKvBytes;
           for (int row = (it.L - tok0) + lane; row < kKvTile; row += 32)
@@ -1437,7 +1485,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     }
   } else if (warp == kMmaWarp + 1) {
     // ------------------------------------------------------------ query loader
-    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
+    regs_dec<kOther>();
     if (lane == 0) tma_prefetch_desc(&tmQ);
     uint32_t n_units = 0, n_two = 0, k = 0;
     Unit it;
@@ -1471,15 +1519,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     // the other warps through the two-slot unit ring; -1 ends the walk.  Unit k is
     // claimed only once every warp has taken unit k - 1: one unit of lookahead, so
     // that at the end of the list no CTA holds small units that an idle CTA could run.
-    regs_dec<KV8 ? kRegsOther8 : kRegsMma>();
+    regs_dec<kOther>();
     uint32_t k = 0;
     [[maybe_unused]] int at = share.begin, group = share.group;
-    [[maybe_unused]] PfGroup now{};
-    if constexpr (SHARED) {
-      unsigned bad = 0;
-      bool decreases;
-      now = pf_group(p, group, &bad, &decreases);
-    }
+    [[maybe_unused]] PfGroup now = share.now;
     for (;;) {
       const int slot = k & 1;
       if (k >= 1 && !wait_all(&unit_empty[(k - 1) & 1], ((k - 1) >> 1) & 1)) break;
@@ -1540,9 +1583,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   } else if (WINDOW && warp > kMmaWarp) {
     // ------------------------------------------------------------ windows: V rows that not every query sees
     // Rows that none sees may hold anything: zeros, so that P = 0 stays 0 (also those behind the sequence's
-    // end, and pages that were not loaded).  Rows that some see become zeros when they hold an infinity or
+    // end).  Rows that some see become zeros when they hold an infinity or
     // NaN, and are noted.
-    regs_dec<kRegsMma>();
+    regs_dec<kOther>();
     uint32_t t = 0, k = 0;
     bool ok = true;
     Unit it;
@@ -1560,7 +1603,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
             ok = false;
             break;
           }
-          if (!pf_partial(p, it, tok0)) {
+          if (!pf_partial(it, j)) {
             if (lane == 0) mbar_arrive(&v_empty[st]);
             continue;
           }
@@ -1568,7 +1611,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           const int piece = lane % CPR;
           uint8_t* tile = sV + st * Sh::kKvBytes + (piece / 8) * Sh::kKvHalf + (piece % 8) * 16;
           // tokens [sinks, p_last - window] and those behind p_first, as rows of the tile
-          int a0 = max(p.sinks - tok0, 0), a1 = min(p_last - p.window + 1 - tok0, kKvTile);
+          int a0 = max(it.w.sinks - tok0, 0), a1 = min(p_last - p.window + 1 - tok0, kKvTile);
           if (a1 <= a0) a0 = a1 = 0;
           const int b0 = min(max(p_first + 1 - tok0, a1), kKvTile);
           for (int part = 0; part < 2; ++part) {
@@ -1578,7 +1621,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
               const int row = row0 + lane / CPR, tok = tok0 + row;
               const bool in = row < r1;
               uint4* at = reinterpret_cast<uint4*>(tile + (in ? row : r0) * 128);
-              const bool seen = tok <= p_last && (tok > p_first - p.window || tok < p.sinks);
+              const bool seen = tok <= p_last && (tok > p_first - p.window || tok < it.w.sinks);
               const bool odd = seen && any_nonfinite_bf16(*at);
               const uint32_t votes = __ballot_sync(0xffffffffu, in && odd);
               const bool row_odd = (votes >> (lane / CPR * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << CPR) - 1u);
@@ -1600,10 +1643,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       }
     }
   } else if (warp > kMmaWarp) {
-    regs_dec<kRegsMma>();  // idle: give the registers to the softmax groups
+    regs_dec<kOther>();  // idle: give the registers to the softmax groups
   } else {
     // ------------------------------------------------------------ softmax groups
-    regs_inc<KV8 ? kRegsSoftmax8 : kRegsSoftmax>();
+    regs_inc<KV8 ? kRegsSoftmax8 : WINDOW || SHARED ? kRegsSoftmaxU : kRegsSoftmax>();
     const int w = warp >> 2;                    // query tile of this group
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1679,7 +1722,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         // (windows: but for the keys [hole, hole + hole_len))
         [[maybe_unused]] int hole = 0, hole_len = 0;
         if constexpr (WINDOW) {
-          hole = min(max(p.sinks - tok0, 0), kKvTile);
+          hole = min(max(it.w.sinks - tok0, 0), kKvTile);
           hole_len = max(min(p_row - p.window + 1 - tok0, kKvTile) - hole, 0);
         }
         const bool lean = vis == kKvTile && sgn > 0.f && hole_len == 0;   // the common case: no mask, positive scale
