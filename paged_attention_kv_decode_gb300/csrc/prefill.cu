@@ -622,6 +622,41 @@ __device__ __forceinline__ bool any_nonfinite_bf16(const uint4& v) {
            ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
 }
 
+// Windows: rows [r0, r1) of a V tile become zeros, by one warp.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lane) {
+  constexpr int CPR = D / 8;  // 16-byte pieces of a row
+  for (int i = r0 * CPR + lane; i < r1 * CPR; i += 32) {
+    const int row = i / CPR, piece = i % CPR;
+    *reinterpret_cast<uint4*>(tile + (piece / 8) * (kKvTile * 128) + row * 128 + (piece % 8) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ... and of rows [r0, r1) those that hold an infinity or NaN do; note(row) for each.
+template <int D, typename Note>
+__device__ __forceinline__ void look_at_rows(uint8_t* tile, int r0, int r1, int lane, Note note) {
+  constexpr int CPR = D / 8, RPS = 32 / CPR;  // rows per step
+  constexpr int kSteps = 8;                   // loads in flight
+  const int piece = lane % CPR;
+  uint8_t* at = tile + (piece / 8) * (kKvTile * 128) + (piece % 8) * 16;
+#pragma unroll 1
+  for (int row0 = r0 + lane / CPR; row0 - lane / CPR < r1; row0 += kSteps * RPS) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (row0 + i * RPS < r1 && any_nonfinite_bf16(*reinterpret_cast<const uint4*>(at + (row0 + i * RPS) * 128))) odd |= 1u << i;
+    if (!__any_sync(0xffffffffu, odd != 0)) continue;
+#pragma unroll 1
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t votes = __ballot_sync(0xffffffffu, (odd >> i) & 1u);
+      if (!((votes >> (lane - piece)) & ((1u << CPR) - 1u))) continue;  // (CPR is 8 or 16)
+      *reinterpret_cast<uint4*>(at + (row0 + i * RPS) * 128) = make_uint4(0u, 0u, 0u, 0u);
+      if (piece == 0) note(row0 + i * RPS);
+    }
+  }
+}
+
 // Windows, the rare case: V rows with an infinity or NaN that were kept out of the unit's V tiles.
 // Every row of the warp that sees such a token adds weight * V to its O in TMEM (its sum of weights
 // has the weight already).  q: the thread's query row (NULL: none).
@@ -1607,32 +1642,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
             if (lane == 0) mbar_arrive(&v_empty[st]);
             continue;
           }
-          constexpr int CPR = D / 8, RPS = 32 / CPR;  // 16-byte pieces of a row, rows per step
-          const int piece = lane % CPR;
-          uint8_t* tile = sV + st * Sh::kKvBytes + (piece / 8) * Sh::kKvHalf + (piece % 8) * 16;
-          // tokens [sinks, p_last - window] and those behind p_first, as rows of the tile
-          int a0 = max(it.w.sinks - tok0, 0), a1 = min(p_last - p.window + 1 - tok0, kKvTile);
-          if (a1 <= a0) a0 = a1 = 0;
-          const int b0 = min(max(p_first + 1 - tok0, a1), kKvTile);
-          for (int part = 0; part < 2; ++part) {
-            const int r0 = part ? b0 : a0, r1 = part ? kKvTile : a1;
-#pragma unroll 4
-            for (int row0 = r0; row0 < r1; row0 += RPS) {
-              const int row = row0 + lane / CPR, tok = tok0 + row;
-              const bool in = row < r1;
-              uint4* at = reinterpret_cast<uint4*>(tile + (in ? row : r0) * 128);
-              const bool seen = tok <= p_last && (tok > p_first - p.window || tok < it.w.sinks);
-              const bool odd = seen && any_nonfinite_bf16(*at);
-              const uint32_t votes = __ballot_sync(0xffffffffu, in && odd);
-              const bool row_odd = (votes >> (lane / CPR * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << CPR) - 1u);
-              if (in && (!seen || row_odd)) *at = make_uint4(0u, 0u, 0u, 0u);
-              if (in && row_odd && piece == 0) {
-                const int i = tok > p_first ? 2 * p.Tq + tok - p_first - 1 : tok - (p_first - p.window + 1);
-                atomicOr(&xw.odd[slot][i / 32], 1u << (i % 32));
-                *reinterpret_cast<volatile int*>(&xw.any_odd[slot]) = 1;
-              }
-            }
-          }
+          uint8_t* tile = sV + st * Sh::kKvBytes;
+          auto in_tile = [&](int t) { return min(max(t - tok0, 0), kKvTile); };
+          // rows that none sees: between the first tokens and the first query's oldest key, and behind the last query
+          const int low = in_tile(it.w.sinks), old = max(in_tile(p_first - p.window + 1), low);
+          const int leave = max(in_tile(p_last - p.window + 1), old), end = in_tile(p_last + 1);
+          zero_rows<D>(tile, low, old, lane);
+          zero_rows<D>(tile, end, kKvTile, lane);
+          // rows that some see: those that leave the window of some queries, and those behind the first query
+          auto note = [&](int row) {
+            const int tok = tok0 + row, i = tok > p_first ? 2 * p.Tq + tok - p_first - 1 : tok - (p_first - p.window + 1);
+            atomicOr(&xw.odd[slot][i / 32], 1u << (i % 32));
+            *reinterpret_cast<volatile int*>(&xw.any_odd[slot]) = 1;
+          };
+          const int next = in_tile(p_first + 1);
+          look_at_rows<D>(tile, old, leave, lane, note);
+          look_at_rows<D>(tile, next, min(low, end), lane, note);  // (first tokens behind the first query)
+          look_at_rows<D>(tile, max(next, leave), end, lane, note);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -1657,6 +1683,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     const float sgn = sl2 < 0.f ? -1.f : sl2 > 0.f ? 1.f : 0.f;
     // > 0, so that a hidden key's -inf stays -inf (8-bit cache: the tile's factors are held above zero)
     const float asl2 = sl2 != 0.f ? fabsf(sl2) : KV8 ? 0.f : 1.f;
+    // windows: rows in 32-byte stores where out allows them (whole sectors: half the time of 16-byte ones)
+    [[maybe_unused]] const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     uint32_t ns = 0, npv = 0, k = 0;            // s_full phases consumed, PVs of this group, units read
     bool ok = true;
     Unit it;
@@ -1734,15 +1762,33 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         float mx[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-        if (!lean) {
+        if (WINDOW || SHARED) {
+          // the same (below) in pieces: of most tiles with hidden keys, one or two of the four need a look
+          if (!lean) {
+            if (sgn <= 0.f) {
+#pragma unroll
+              for (int c = 0; c < kKvTile; ++c) sv[c] = __float_as_uint(__uint_as_float(sv[c]) * sgn);
+            }
+#pragma unroll
+            for (int q = 0; q < kKvTile; q += 32) {
+              if (vis < q + 32) {
+#pragma unroll
+                for (int c = q; c < q + 32; ++c)
+                  if (c >= vis) sv[c] = 0xff800000u;
+              }
+              if (WINDOW && hole_len > 0 && hole < q + 32 && hole + hole_len > q) {
+#pragma unroll
+                for (int c = q; c < q + 32; ++c)
+                  if ((unsigned)(c - hole) < (unsigned)hole_len) sv[c] = 0xff800000u;
+              }
+            }
+          }
+        } else if (!lean) {
           // fold the mask (a select: NaN-safe) and a negative scale's sign into the
           // scores once, so that one code path serves every tile
 #pragma unroll
-          for (int c = 0; c < kKvTile; ++c) {
-            bool seen = c < vis;
-            if constexpr (WINDOW) seen = seen && (unsigned)(c - hole) >= (unsigned)hole_len;
-            sv[c] = seen ? __float_as_uint(__uint_as_float(sv[c]) * sgn) : 0xff800000u;
-          }
+          for (int c = 0; c < kKvTile; ++c)
+            sv[c] = c < vis ? __float_as_uint(__uint_as_float(sv[c]) * sgn) : 0xff800000u;
         }
         [[maybe_unused]] float fac[8];  // 8-bit cache: log2 units per unit of S, for each 16 tokens
         float m_new;
@@ -1879,6 +1925,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         tmem_ld32(o_tmem + c * 32, ov);
         tmem_ld_wait();
         if (row_valid) {
+          if (WINDOW && wide_out) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = pack_bf16x2(__uint_as_float(ov[i + 2 * e]) * inv, __uint_as_float(ov[i + 2 * e + 1]) * inv);
+              st_global_v8(orow + c * 32 + i, v);
+            }
+            continue;
+          }
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             uint4 v;
