@@ -95,66 +95,20 @@ __host__ __device__ __forceinline__ WindowSpan window_span(int L, int window, in
   return w;
 }
 
-// One work item of the bf16 decode: the tokens of `span` of KV head g of sequence s
-// (query row orow), run by NW warps (warp 0 .. NW - 1 of the caller's
-// group) over their NW x STAGES TMA ring at
-// smem with its barriers at bars.  kb: this warp's ring position before the item
-// (ring stages and barrier phases run on across the items of a persistent group),
-// advanced past the item's units.  status: the calling file's device status word.
-// sync(): a barrier over the group's threads.  store(cm, cl, co): takes the warps'
-// states (combine_and_store's) behind such a barrier.
-// The combine step reuses the ring: the caller syncs the group before the next
-// item's loads.  Returns false when a wait gave up.
-template <int D, int NW, int STAGES, typename Span, typename Sync, typename Store>
-__device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeParams& p,
-                                                 uint8_t* smem, uint64_t* bars, int g, int s, int orow,
-                                                 const Span& span, int warp, int lane, int& kb, unsigned int* status,
-                                                 Sync sync, Store store) {
-  using Shape = Bf16DecodeShape<D>;
-  constexpr int HALVES = Shape::kHalves;
-  constexpr int STAGE_BYTES = Shape::kStageBytes;
-  constexpr int KS = Shape::kSteps;
-
-  // this warp's units: warp + k * NW, k < n_my
-  const int n_units = span.units();
-  const int n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
-  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
-
-  // Lane l holds the TMA row coordinate (block * bs + slot) of unit k = 32 * batch + l;
-  // -kUnit (a box entirely outside the tensor, read as zeros) marks a bad block id.
-  auto row_coord = [&](int k) -> int {
-    if (k >= n_my) return -kUnit;
-    const int tok = span.token(warp + k * NW);
-    const int page = tok / p.bs;
-    const int b = checked_block(bt_row, page, p.num_blocks, status);
-    return b < 0 ? -kUnit : b * p.bs + (tok - page * p.bs);
-  };
-  int win_cur = row_coord(lane);
-  int win_next = row_coord(32 + lane);
-  const uint64_t policy = l2_policy_evict_first();
-
-  auto issue = [&](int k) {  // called by all lanes, in order k = 0, 1, 2, ...
-    if (k > 0 && (k & 31) == 0) {
-      win_cur = win_next;
-      win_next = row_coord(k + 32 + lane);
-    }
-    const int row = __shfl_sync(0xffffffffu, win_cur, k & 31);
-    const int st = (kb + k) % STAGES;
-    uint8_t* base = smem + (warp * STAGES + st) * STAGE_BYTES;
-    uint64_t* bar = &bars[warp * STAGES + st];
-    if (lane == 0) mbar_arrive_expect_tx(bar, STAGE_BYTES);
-    __syncwarp();
-    // one box per lane: a single thread issues TMA instructions far slower than several
-    if (lane < 2 * HALVES) {
-      const int h = lane % HALVES;
-      tma_load_3d(base + lane * kBoxBytes, lane < HALVES ? &tmK : &tmV, bar, h * 64, g, row, policy);
-    }
-  };
-
-  // q^T as the B operand of S^T = K q^T: lane holds head n = lane / 4, dims 2*(lane%4) (+1, +8, +9)
-  const int q4 = lane & 3, rA = lane >> 2;
+// A warp's running softmax over units of 16 tokens: the group's query rows (up to 8 heads) against one KV
+// head.  q^T is the B operand of S^T = K q^T: a lane holds head n = lane / 4, dims 2*(lane%4) (+1, +8, +9);
+// of O^T (D x 8 heads) the rows lane / 4 (+8) of each 16 and the heads 2*(lane%4) (+1), whose maxima (log2
+// units) and sums m, l are.
+template <int D>
+struct DecodeWarp {
+  static constexpr int KS = Bf16DecodeShape<D>::kSteps, HALVES = Bf16DecodeShape<D>::kHalves;
   uint32_t qf[KS][2];
-  {
+  float o[KS][4];
+  float m0, m1, l0, l1;
+
+  // Query row orow, KV head g: an empty state.
+  __device__ __forceinline__ void begin(const DecodeParams& p, int orow, int g, int lane) {
+    const int q4 = lane & 3, rA = lane >> 2;
     const bool live = rA < p.r;
     const __nv_bfloat16* qrow =
         reinterpret_cast<const __nv_bfloat16*>(p.q) + ((size_t)orow * p.H + g * p.r + (live ? rA : 0)) * D;
@@ -163,29 +117,17 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
       qf[kk][0] = live ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 2 * q4) : 0u;
       qf[kk][1] = live ? *reinterpret_cast<const uint32_t*>(qrow + kk * 16 + 8 + 2 * q4) : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
   }
 
-  float o[KS][4];
-#pragma unroll
-  for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2*q4 and 2*q4+1
-  const float sl2 = p.scale_log2;
-
-  const int prologue = n_my < STAGES ? n_my : STAGES;
-  for (int k = 0; k < prologue; ++k) issue(k);
-
-  int k = 0;
-  bool ok = true;
-  for (; k < n_my; ++k) {
-    const int st = (kb + k) % STAGES;
-    const bool landed = mbar_wait(&bars[warp * STAGES + st], ((kb + k) / STAGES) & 1, status);
-    if (!__all_sync(0xffffffffu, landed)) {  // leave the loop together
-      ok = false;
-      break;
-    }
-    const int tok0 = span.token(warp + k * NW);
+  // The unit whose K (and behind it V) boxes are at kbase and whose first token is tok0.
+  template <typename Span>
+  __device__ __forceinline__ void unit(uint32_t kbase, int tok0, const Span& span, float sl2, int lane) {
+    const int q4 = lane & 3, rA = lane >> 2;
     const int nv = min(kUnit, span.t1 - tok0);  // tokens in this unit before the span's end, >= 1
-    const uint32_t kbase = smem_u32(smem + (warp * STAGES + st) * STAGE_BYTES);
     const uint32_t vbase = kbase + HALVES * kBoxBytes;
 
     // S^T (16 tokens x 8 heads) = K (16 x D) . q^T (D x 8), in two independent
@@ -265,6 +207,82 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
         mma_bf16_16816(o[mt], a0 & mlo, a1 & mlo, a2 & mhi, a3 & mhi, pb0, pb1);
       }
     }
+  }
+};
+
+// One work item of the bf16 decode: the tokens of `span` of KV head g of sequence s
+// (query row orow), run by NW warps (warp 0 .. NW - 1 of the caller's
+// group) over their NW x STAGES TMA ring at
+// smem with its barriers at bars.  kb: this warp's ring position before the item
+// (ring stages and barrier phases run on across the items of a persistent group),
+// advanced past the item's units.  status: the calling file's device status word.
+// sync(): a barrier over the group's threads.  store(cm, cl, co): takes the warps'
+// states (combine_and_store's) behind such a barrier.
+// The combine step reuses the ring: the caller syncs the group before the next
+// item's loads.  Returns false when a wait gave up.
+template <int D, int NW, int STAGES, typename Span, typename Sync, typename Store>
+__device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeParams& p,
+                                                 uint8_t* smem, uint64_t* bars, int g, int s, int orow,
+                                                 const Span& span, int warp, int lane, int& kb, unsigned int* status,
+                                                 Sync sync, Store store) {
+  using Shape = Bf16DecodeShape<D>;
+  constexpr int HALVES = Shape::kHalves;
+  constexpr int STAGE_BYTES = Shape::kStageBytes;
+  constexpr int KS = Shape::kSteps;
+
+  // this warp's units: warp + k * NW, k < n_my
+  const int n_units = span.units();
+  const int n_my = warp < n_units ? (n_units - warp + NW - 1) / NW : 0;
+  const int32_t* bt_row = p.block_table + (size_t)s * p.max_blocks;
+
+  // Lane l holds the TMA row coordinate (block * bs + slot) of unit k = 32 * batch + l;
+  // -kUnit (a box entirely outside the tensor, read as zeros) marks a bad block id.
+  auto row_coord = [&](int k) -> int {
+    if (k >= n_my) return -kUnit;
+    const int tok = span.token(warp + k * NW);
+    const int page = tok / p.bs;
+    const int b = checked_block(bt_row, page, p.num_blocks, status);
+    return b < 0 ? -kUnit : b * p.bs + (tok - page * p.bs);
+  };
+  int win_cur = row_coord(lane);
+  int win_next = row_coord(32 + lane);
+  const uint64_t policy = l2_policy_evict_first();
+
+  auto issue = [&](int k) {  // called by all lanes, in order k = 0, 1, 2, ...
+    if (k > 0 && (k & 31) == 0) {
+      win_cur = win_next;
+      win_next = row_coord(k + 32 + lane);
+    }
+    const int row = __shfl_sync(0xffffffffu, win_cur, k & 31);
+    const int st = (kb + k) % STAGES;
+    uint8_t* base = smem + (warp * STAGES + st) * STAGE_BYTES;
+    uint64_t* bar = &bars[warp * STAGES + st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, STAGE_BYTES);
+    __syncwarp();
+    // one box per lane: a single thread issues TMA instructions far slower than several
+    if (lane < 2 * HALVES) {
+      const int h = lane % HALVES;
+      tma_load_3d(base + lane * kBoxBytes, lane < HALVES ? &tmK : &tmV, bar, h * 64, g, row, policy);
+    }
+  };
+
+  DecodeWarp<D> state;
+  state.begin(p, orow, g, lane);
+
+  const int prologue = n_my < STAGES ? n_my : STAGES;
+  for (int k = 0; k < prologue; ++k) issue(k);
+
+  int k = 0;
+  bool ok = true;
+  for (; k < n_my; ++k) {
+    const int st = (kb + k) % STAGES;
+    const bool landed = mbar_wait(&bars[warp * STAGES + st], ((kb + k) / STAGES) & 1, status);
+    if (!__all_sync(0xffffffffu, landed)) {  // leave the loop together
+      ok = false;
+      break;
+    }
+    const int tok0 = span.token(warp + k * NW);
+    state.unit(smem_u32(smem + (warp * STAGES + st) * STAGE_BYTES), tok0, span, p.scale_log2, lane);
     __syncwarp();
     if (k + STAGES < n_my) issue(k + STAGES);
   }
@@ -276,16 +294,16 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
     }
   }
 
-  l0 = warp_sum_xor(l0, 4);
-  l1 = warp_sum_xor(l1, 4);
+  const int q4 = lane & 3, rA = lane >> 2;
+  const float l0 = warp_sum_xor(state.l0, 4), l1 = warp_sum_xor(state.l1, 4);
   sync();  // every warp is done with its ring
 
   float* cm = reinterpret_cast<float*>(smem);
   float* cl = cm + NW * 8;
   float* co = cl + NW * 8;
   if (lane < 4) {
-    cm[warp * 8 + 2 * lane] = m0;
-    cm[warp * 8 + 2 * lane + 1] = m1;
+    cm[warp * 8 + 2 * lane] = state.m0;
+    cm[warp * 8 + 2 * lane + 1] = state.m1;
     cl[warp * 8 + 2 * lane] = l0;
     cl[warp * 8 + 2 * lane + 1] = l1;
   }
@@ -294,10 +312,10 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
     const int d0 = mt * 16 + rA;
     float* c0 = co + ((size_t)warp * D + d0) * 8 + 2 * q4;
     float* c1 = c0 + 8 * 8;
-    c0[0] = o[mt][0];
-    c0[1] = o[mt][1];
-    c1[0] = o[mt][2];
-    c1[1] = o[mt][3];
+    c0[0] = state.o[mt][0];
+    c0[1] = state.o[mt][1];
+    c1[0] = state.o[mt][2];
+    c1[1] = state.o[mt][3];
   }
   sync();
   store(cm, cl, co);
@@ -510,10 +528,6 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 // least kMinPartTokens each
 constexpr int kItemCtasPerSm = 2;
 constexpr int kMinPartTokens = 128;
-
-// Many items: a warp each, nine CTAs on an SM instead of two of four warps.  The bytes in flight are the
-// same, and an item's start (its lengths, block ids, first loads) hides behind eight others.
-inline bool one_warp_items(long long items, int sms) { return items >= 18ll * sms; }
 
 inline int item_parts(long long items, int tokens, int sms) {
   const long long fit = items > 0 ? kItemCtasPerSm * (long long)sms / items : 1;

@@ -144,15 +144,20 @@ struct SharedArgs {
   int S, num_groups, H, G, D, bs, max_blocks, num_blocks, cap;
   float scale;
 };
-// what the kernel over the shared prefixes leaves for the one over the sequences' own tokens,
+// what the kernel over the shared prefixes leaves for those behind it -- of the groups,
 struct SharedPlan {
-  int2 total;     // K/V tiles of all units, CTAs that share them
-  int2 unused;
-  int4 group[1];  // [num_groups]: tiles before the group, of a unit, units before the group, units per KV head
+  int2 total;           // K/V tiles of all units, CTAs that share them (0: none)
+  int own_shares;           // of the sequences' own tokens: shares, at least 1 (0: not counted yet),
+  unsigned int next_share;  // the next (share, KV head) to hand out
+  int2 group[1];            // [num_groups]: units before the group, units per KV head
 };
-// and the launch of the first (prefill.cu), `sms` CTAs: a part is [2][128] rows.
-int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, float* part_lse, float* part_out, int sms,
-                         cudaStream_t st);
+// of each sequence,
+struct SharedOwn {
+  int begin, group;  // its first token that is its own; its group (-1: every token is)
+};
+// and the launch of the first (prefill.cu), `sms` CTAs: a part is [2][128] rows; unit_parts: a unit's first and last.
+int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, SharedOwn* own, int2* unit_parts, float* part_lse,
+                         float* part_out, int sms, cudaStream_t st);
 
 // Per-translation-unit device status words.
 int decode_status(uint32_t* bits, int clear);

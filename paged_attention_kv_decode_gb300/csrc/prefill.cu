@@ -126,7 +126,6 @@ constexpr int kSortMax = 2048;    // schedule: heaviest-first sort up to this ma
 constexpr int kMaxSplits = 8;
 constexpr int kMinPartTiles = 4;
 constexpr int kMinSplitTiles = 13;
-constexpr int kMinShare = 4;      // shared prefixes: K/V tiles of a CTA at least
 
 struct PrefillParams {
   const int32_t* cu_q_lens;
@@ -166,6 +165,8 @@ struct PrefillParams {
   // kernel behind this one needs to find a row's parts.
   const int32_t* prefix_lens;
   SharedPlan* plan;
+  SharedOwn* own;
+  int2* unit_parts;
   int num_groups;
 };
 
@@ -856,14 +857,73 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, int tag, int 
   if (lse) *lse = (M + log2f(W)) * kLn2;
 }
 
-// Shared prefixes: this CTA's share [begin, end) of all units' K/V tiles in a row, the group in which it
-// begins, and the tiles and units of the groups before that one.  Called by the whole block; the first CTA
-// leaves the plan for the kernel behind.
+// Shared prefixes: a CTA's share [begin, end) of all units' K/V tiles in a row, the group in which it begins, and
+// the tiles and units of the groups before that one.
 struct PfShare {
   int begin, end, group, x, unit;
   PfGroup now;  // the group
 };
 
+// Shared prefixes, by one warp of every CTA, 32 sequences each at a time: where the sequences' own tokens begin.
+__device__ __forceinline__ void pf_own_tokens(const PrefillParams& p, int lane) {
+  for (long long s0 = (long long)blockIdx.x * 32; s0 < p.S; s0 += (long long)gridDim.x * 32) {
+    const int s = (int)min(s0 + lane, (long long)p.S - 1);
+    int lo = -1, hi = p.num_groups - 1;  // the last group that begins at or before s (-1: none)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.cu_q_lens[mid] <= s)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    SharedOwn v{0, -1};
+    int L = p.seq_lens[s];
+    if (L > p.cap) atomicOr(&g_status_prefill, METIS_STATUS_SEQ_TOO_LONG);
+    L = min(L, p.cap);
+    if (lo >= 0) {
+      const int a = p.cu_q_lens[lo], b = p.cu_q_lens[lo + 1], tokens = p.prefix_lens[lo];
+      if (a >= 0 && a <= s && s < b && b <= p.S && tokens > 0 && L >= tokens) v = SharedOwn{tokens, lo};
+    }
+    if (s0 + lane < p.S) p.own[s] = v;
+  }
+}
+
+// Shared prefixes: how many of the grid's CTAs (one per SM) share `total` K/V tiles, so that these and the
+// decodes of the sequences' own tokens, on the other SMs at the same time, end together.  A CTA takes 7 us to
+// start, 5 us for each unit (its queries, its parts) and 2 us a tile; decodes stream 40 GB/s on each of their
+// SMs, 6.1 TB/s together.  shared_tokens: of the caller's groups, over all threads the members' shared tokens.
+constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
+constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
+
+__device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total, int units, float shared_tokens) {
+  __shared__ float tokens;
+  __shared__ unsigned best;
+  const int tid = threadIdx.x, sms = gridDim.x;
+  if (tid == 0) {
+    tokens = 0.f;
+    best = 0xffffffffu;
+  }
+  float mine = -shared_tokens;
+  for (int s = tid; s < p.S; s += kPfThreads) mine += (float)min(max(p.seq_lens[s], 0), p.cap);
+  mine = warp_sum_xor(mine, 1);
+  __syncthreads();
+  if ((tid & 31) == 0) atomicAdd(&tokens, mine);
+  __syncthreads();
+  const float bytes = fmaxf(tokens, 0.f) * p.kv_token_bytes;
+  if (total == 0) return 0;
+  for (int n = tid + 1; n <= (bytes > 0.f && sms > 1 ? sms - 1 : sms); n += kPfThreads) {
+    const float prefix = kShareStartUs + kShareTileUs * (((unsigned)total + n - 1) / n) +
+                         kShareUnitUs * (((unsigned)units + n - 1) / n);
+    const float own = n < sms ? kShareStartUs + bytes / fminf(kOwnBytesPerUs * (sms - n), kOwnBytesPerUsAll) : 0.f;
+    const float t = fmaxf(prefix, own);
+    atomicMin(&best, (unsigned)fminf(t * 16.f, 4e6f) << 10 | (unsigned)n);  // (n: up to 1,023 SMs)
+  }
+  __syncthreads();
+  return min((int)(best & 1023u), total);
+}
+
+// Shared prefixes: this CTA's share.  Called by the whole block.  On the way the grid leaves the plan for the
+// kernels behind, the first of which may then start: every CTA has waited for the kernels in front.
 __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
   __shared__ int warp_sums[kPfThreads / 32];
   __shared__ PfShare mine;
@@ -871,7 +931,9 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
   int x = 0, unit = 0;  // of the groups before this round's
   PfGroup v{};
   int my_x = 0, my_unit = 0;
+  float shared_tokens = 0.f;  // of this thread's groups' members
   bool disorder = false;
+  if (tid >= kPfThreads - 32) pf_own_tokens(p, tid & 31);
   auto round = [&](int g0, bool first) {
     unsigned bad = 0;
     bool decreases = false;
@@ -884,16 +946,27 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
     my_x = x + block_exclusive_scan<kPfThreads>(v.units * v.tiles, warp_sums, &sum);
     x += sum;
     __syncthreads();
+    if (first && v.units) shared_tokens += (float)v.n * v.tokens;
     if (first && blockIdx.x == 0 && g0 + tid < p.num_groups) {
-      p.plan->group[g0 + tid] = make_int4(my_x, v.units ? v.tiles : 0, my_unit, v.units / p.G);
+      p.plan->group[g0 + tid] = make_int2(my_unit, v.units / p.G);
       if (bad) atomicOr(&g_status_prefill, bad);
     }
   };
   for (int g0 = 0; g0 < p.num_groups; g0 += kPfThreads) round(g0, true);
   // Groups that overlap (offsets that decrease somewhere) could have more units than there is room for
-  const int total = disorder ? 0 : x, ctas = min((int)gridDim.x, max(total / kMinShare, 1));
-  if (blockIdx.x == 0 && tid == 0) p.plan->total = make_int2(total, ctas);
+  const int total = disorder ? 0 : x, ctas = pf_shared_ctas(p, total, unit, shared_tokens);
+  if (tid >= kPfThreads - 32) {
+    if (blockIdx.x == 0 && tid == kPfThreads - 1) {
+      p.plan->total = make_int2(total, ctas);
+      p.plan->own_shares = 0;
+      p.plan->next_share = 0;
+    }
+    __threadfence();
+    __syncwarp();
+    if (tid == kPfThreads - 1) pdl_launch_dependents();
+  }
   PfShare s{};
+  if (total == 0) return s;
   s.begin = (int)((long long)min((int)blockIdx.x, ctas) * total / ctas);
   s.end = (int)((long long)min((int)blockIdx.x + 1, ctas) * total / ctas);
   if (s.begin == s.end) return s;
@@ -949,7 +1022,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
   // are complete: waited for here, or by every CTA of the decode grid in front before it let this
   // grid launch (the warps that read more than the items then fence, below).
   if (!p.wait_at_exit) pdl_wait();
-  if (SHARED) pdl_launch_dependents();  // every CTA has waited: the decodes may start on SMs that are free
   extern __shared__ uint8_t smem_raw[];
   const uint32_t slack = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + slack;
@@ -1528,7 +1600,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       // the previous unit's query tiles stay until its last QK has completed
       if (n_units > 0 && !wait_all(q_free, (n_units - 1) & 1)) break;
       const int ntiles = it.n1 > 0 ? 2 : 1;
-      if (lane == 0) {
+      if (WINDOW || SHARED) {  // a box per lane: one thread takes 0.1 us for each
+        if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(ntiles * Sh::kQBytes));
+        __syncwarp();
+        const uint64_t pol = l2_policy_evict_first();
+        for (int i = lane; i < ntiles * p.r * HALVES; i += 32) {
+          const int h = i % HALVES, hh = i / HALVES % p.r, w = i / HALVES / p.r;
+          tma_load_3d(sQ + w * Sh::kQBytes + h * Sh::kQHalf + hh * p.Tq * 128, &tmQ, q_full, h * 64, it.g * p.r + hh,
+                      it.q0 + (2 * it.pair + w) * p.Tq, pol);
+        }
+      } else if (lane == 0) {
         if (!KV8) mbar_arrive_expect_tx(q_full, (uint32_t)(ntiles * Sh::kQBytes));
         const uint64_t pol = l2_policy_evict_first();
         for (int w = 0; w < ntiles; ++w) {
@@ -1895,6 +1976,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         }
       }
       if constexpr (SHARED) {
+        if (threadIdx.x == 0) {
+          int2* unit = p.unit_parts + (it.part - blockIdx.x);
+          if (it.j0 == 0) unit->x = it.part;
+          if (it.j0 + it.n_kv == (it.L - 1) / kKvTile + 1) unit->y = it.part;
+        }
         const size_t at = ((size_t)it.part * 2 + w) * kRows + row;
         float* to = p.part_out + at * D;
 #pragma unroll 1
@@ -2217,8 +2303,8 @@ static int prefill_chunk(const void* q, const int32_t* cu_q_lens, const void* k_
 namespace metis {
 
 // The parts of the shared prefixes of a batch of decodes (shared_prefix.cu).
-int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, float* part_lse, float* part_out, int sms,
-                         cudaStream_t st) {
+int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, SharedOwn* own, int2* unit_parts, float* part_lse,
+                         float* part_out, int sms, cudaStream_t st) {
   PrefillParams p{};
   p.cu_q_lens = a.cu_group_seqs;
   p.prefix_lens = a.prefix_lens;
@@ -2236,6 +2322,9 @@ int launch_shared_prefix(const SharedArgs& a, SharedPlan* plan, float* part_lse,
   p.cap = a.cap;
   p.scale_log2 = a.scale * kLog2e;
   p.plan = plan;
+  p.own = own;
+  p.unit_parts = unit_parts;
+  p.kv_token_bytes = 4 * a.G * a.D;
   p.part_lse = part_lse;
   p.part_out = part_out;
   auto none = [](const PrefillParams&) { return METIS_OK; };

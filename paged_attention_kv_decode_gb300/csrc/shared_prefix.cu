@@ -7,139 +7,332 @@
 //
 //   1 the members' queries of a group become the rows of query tiles, and the chunk kernel (prefill.cu,
 //     SHARED) runs them over the prefix on the tensor cores: its K and V are read once per 256 rows.  All
-//     tiles of all groups are cut into equal shares, one per SM, so a unit may be several CTAs' parts.
-//   2 one CTA (or a cluster) per sequence and KV head decodes the sequence's own tokens (decode_items.cuh)
-//     and joins the prefix's parts in its epilogue.  It is a programmatic dependent of 1 that waits for it
-//     only there: its CTAs start on SMs that 1 has left, and its K/V stream under 1's tail.
+//     tiles of all groups are cut into equal shares, so a unit may be several CTAs' parts.
+//   2 the sequences' own tokens are decoded by warps that walk shares of them (decode_stream.cuh): the 16-token
+//     units of all sequences in a row, cut into equal shares that the warps claim for a KV head each.
+//   3 a kernel over the rows joins their parts.
 //
-// Bound by HBM for the own tokens, by the chunk kernel's tile loop (or HBM, few members) for the prefix.
+// 1 is bound by the tensor cores and the start and end of its units, 2 by HBM: they run side by side.  1
+// takes as many SMs as make the two end together (pf_shared_ctas: their rates are there), 2 the others.  2 is a
+// programmatic dependent of 1 that does not wait for it but at its very end; what 2 needs of 1 (the number of
+// SMs, where each sequence's own tokens begin) is written before 1 lets it start.
 #include <math.h>
 
 #include <algorithm>
 #include <type_traits>
 
 #include "../../include/metis_attn.h"
-#include "decode_items.cuh"
+#include "decode_stream.cuh"
 
 namespace metis {
 
 __device__ unsigned int g_status_shared = 0;
 
 constexpr int kSharedRows = 128;  // rows of a query tile
+constexpr int kMinUnits = 4;      // units (16 tokens of a KV head) of a share at least
+constexpr int kLargeShares = 2;   // shares for each warp: large ones of the first three quarters of the units,
+constexpr int kSmallShares = 4;   // small ones of the others, so that the warps end together
+constexpr int kRuns = 2048;       // (65,535 sequences: runs of 32)
 
 struct SharedParams {
   DecodeParams d;
   const int32_t* cu_group_seqs;
-  const int32_t* prefix_lens;
-  const SharedPlan* plan;
-  const float* part_lse;
-  const float* part_out;
-  int num_groups, Tq;
+  SharedPlan* plan;
+  const SharedOwn* own;     // [S]
+  const float* prefix_lse;  // [part][query tile][row], log2 units
+  const float* prefix_out;  // ... [head_dim], normalised
+  const int2* unit_parts;   // [unit]: its first and last part
+  int2* own_parts;          // [S]: the first and last share with units of the sequence
+  float* own_lse;           // [part][r], log2 units; part: (number of the sequence + of the share) * G + KV head
+  float* own_out;           // ... [head_dim], normalised
+  int Tq, prefix_slots, own_slots;  // slots: parts that there is memory for (own: for each KV head)
 };
 
-// The group of sequence s, the last that begins at or before it (-1: none), by a whole warp.
-__device__ __forceinline__ int group_of(const SharedParams& sp, int s, int lane) {
-  int lo = 0, n = sp.num_groups;
-  while (n > 0) {
-    const int step = (n + 31) / 32, at = lane * step;
-    const int before = __popc(__ballot_sync(0xffffffffu, at < n && sp.cu_group_seqs[lo + min(at, n - 1)] <= s));
-    if (before == 0) return -1;
-    lo += (before - 1) * step;
-    n = min(step, n - (before - 1) * step);
-    if (n == 1) return lo;
+// The shares of a KV head's units: the first `large` of them cut [0, first) evenly, the `small` others the rest.
+struct OwnShares {
+  long long units, first;
+  int large, small;
+  __device__ __forceinline__ OwnShares(long long units_, long long warps)  // warps: for each KV head, at least one
+      : units(units_), first(units_ - units_ / 4) {
+    large = (int)max(min(warps * kLargeShares, first / kMinUnits), first > 0 ? 1ll : 0ll);
+    small = (int)max(min(warps * kSmallShares, (units - first) / kMinUnits), units > first ? 1ll : 0ll);
   }
-  return -1;
+  __device__ __forceinline__ int count() const { return large + small; }
+  __device__ __forceinline__ long long edge(int i) const {
+    return i < large ? i * first / large : small ? first + (i - large) * (units - first) / small : units;
+  }
+};
+
+// Exclusive prefix over the kStreamWarps * 32 threads of a block; *total: of all.
+__device__ __forceinline__ long long stream_scan(long long v, long long* sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the last round's sums were read
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long front = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kStreamWarps; ++w) {
+    if (w < warp) front += sums[w];
+    all += sums[w];
+  }
+  *total = all;
+  return front + x - v;
 }
 
-// The prefix's parts of the rows of one (sequence, KV head): row h * Tq + qi of query tile `tile` of the
-// parts first .. first + count - 1.  grp < 0: the sequence shares nothing.
-struct PrefixParts {
-  const SharedParams& sp;
-  int grp, s, g;
-  const float *lse, *out;
-  int first, count, tile, qi, Tq, D;
-
-  __device__ __forceinline__ PrefixParts(const SharedParams& sp_, int grp_, int s_, int g_)
-      : sp(sp_), grp(grp_), s(s_), g(g_), lse(sp_.part_lse), out(sp_.part_out), first(0), count(0), tile(0), qi(0),
-        Tq(sp_.Tq), D(sp_.d.D) {}
-
-  // Waits for the kernel over the prefixes (every CTA does, so that this grid completes after it).
-  __device__ __forceinline__ void prepare() {
-    pdl_wait();
-    if (grp < 0) return;
-    const int4 v = __ldcg(sp.plan->group + grp);  // tiles before, tiles of a unit, units before, units per KV head
-    const int2 all = __ldcg(&sp.plan->total);
-    if (v.y <= 0 || all.x <= 0) return;
-    const int member = s - sp.cu_group_seqs[grp], pair = member / (2 * Tq), in = member - pair * 2 * Tq;
-    const int unit = g * v.w + pair;
-    // the CTAs whose shares hold the unit's first and last tile
-    const long long x0 = v.x + (long long)unit * v.y, x1 = x0 + v.y - 1;
-    const int c0 = (int)(((x0 + 1) * all.y - 1) / all.x), c1 = (int)(((x1 + 1) * all.y - 1) / all.x);
-    first = v.z + unit + c0;
-    count = c1 - c0 + 1;
-    tile = in / Tq;
-    qi = in - tile * Tq;
-  }
-
-  __device__ __forceinline__ void add(JoinedRow& row, int h, int d) const {
-    constexpr int kBatch = 8;  // loads in flight
-    for (int k = 0; k < count; k += kBatch) {
-      float x[kBatch];
-      float4 v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        x[j] = -INFINITY;
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k + j < count) {
-          const size_t at = ((size_t)(first + k + j) * 2 + tile) * kSharedRows + h * Tq + qi;
-          x[j] = __ldcg(lse + at);
-          v[j] = __ldcg(reinterpret_cast<const float4*>(out + at * D + d));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) row.add(x[j], v[j]);
-    }
-  }
-};
-
-template <int D, int NW>
-__global__ void __launch_bounds__(NW * 32) decode_shared_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                                        const __grid_constant__ CUtensorMap tmV,
-                                                                        const SharedParams sp) {
-  constexpr int STAGES = kBf16Stages, STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
+template <int D>
+__global__ void __launch_bounds__(kStreamWarps * 32, 1) decode_own_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                          const __grid_constant__ CUtensorMap tmV,
+                                                                          const SharedParams sp) {
+  constexpr int STAGES = stream_stages<D>(), STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
+  constexpr int KS = Bf16DecodeShape<D>::kSteps;
   const DecodeParams& p = sp.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NW * STAGES * STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStreamWarps * STAGES * STAGE_BYTES);
   // The kernel over the prefixes, in front of this one, let it start once all its CTAs had waited for
   // the kernels before: their outputs are there (lines that they left in this SM's L1 are dropped).
   __threadfence();
   pdl_launch_dependents();
+  // A CTA that starts behind the other kernel's, with nothing left to do.  One thread looks: others claim
+  // meanwhile, and a CTA whose threads saw different counts would run without its barriers.
+  bool late = false;
+  if (threadIdx.x == 0) {
+    const long long planned = __ldcg(&sp.plan->own_shares);  // (0: not counted yet)
+    late = planned > 0 && __ldcg(&sp.plan->next_share) >= planned * p.G;
+  }
+  if (__syncthreads_or(late)) {
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    for (int i = 0; i < NW * STAGES; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < kStreamWarps * STAGES; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
-  __shared__ int rank_lens[kMaxRankSeqs];
-  __shared__ int rank_found;
-  const int g = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
-  const int s = p.S <= kMaxRankSeqs && parts == 1 ? seq_of_rank(p, blockIdx.z, rank_lens, &rank_found) : (int)blockIdx.z;
-  int L = p.seq_lens[s];
-  if (L > p.cap) {
-    if (threadIdx.x == 0) atomicOr(&g_status_shared, METIS_STATUS_SEQ_TOO_LONG);
-    L = p.cap;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // Sequence s's units of one KV head
+  auto units_of = [&](int s, WindowSpan* span) {
+    const int L = min(max(p.seq_lens[s], 0), p.cap), begin = __ldcg(&sp.own[s].begin);
+    *span = window_span(L, L - begin, 0);
+    return L > begin ? span->n : 0;
+  };
+  // Every CTA adds them up, kPer sequences per thread and round, and keeps the sums in front of each run of
+  // `run` sequences.
+  constexpr int kPer = 4, kRound = kStreamWarps * 32 * kPer;
+  __shared__ long long sums[kStreamWarps];
+  __shared__ long long front[kRuns + 1];
+  const int run = (p.S + kRuns - 1) / kRuns;
+  long long total = 0;
+  for (int s0 = 0; s0 < p.S; s0 += kRound) {
+    int n[kPer];
+    long long sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = s0 + tid * kPer + i;
+      WindowSpan span;
+      n[i] = s < p.S ? units_of(s, &span) : 0;
+      sum += n[i];
+    }
+    long long at = total + stream_scan(sum, sums, &all);
+    total += all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = s0 + tid * kPer + i;
+      if (s < p.S && s % run == 0) front[s / run] = at;
+      at += n[i];
+    }
   }
-  L = max(L, 0);
-  int grp = group_of(sp, s, threadIdx.x & 31), shared = 0;
-  if (grp >= 0) {
-    const int a = sp.cu_group_seqs[grp], b = sp.cu_group_seqs[grp + 1], tokens = sp.prefix_lens[grp];
-    if (a >= 0 && a <= s && s < b && b <= p.S && tokens > 0 && L >= tokens) shared = tokens;
+  const int runs = (p.S + run - 1) / run;
+  // shares for the warps of the SMs that the other kernel leaves; what one has not claimed when another is done
+  // (on those that it leaves later, too) goes to that
+  const int warps = max(((int)gridDim.x - __ldcg(&sp.plan->total.y)) * kStreamWarps / p.G, 1);
+  const OwnShares shares(total, warps);
+  if (blockIdx.x == 0 && tid == 0) sp.plan->own_shares = max(shares.count(), 1);
+  __syncthreads();  // (the barriers are initialised, too)
+
+  // The walk over this warp's shares: the next unit `at` of the share, which ends at `end`, is unit u of `units` of
+  // sequence s, KV head g.  The KV heads of a share are claimed one after another, so that they run at about the same
+  // time: the rows of a token's heads lie side by side in memory.
+  long long at = 0, end = 0;
+  int s = 0, g = 0, u = 0, units = 0, share = 0;
+  WindowSpan span{};
+  auto next = [&](StreamItem& it) -> bool {
+    if (at >= end) {
+      unsigned id = 0;
+      if (lane == 0) id = atomicAdd(&sp.plan->next_share, 1u);
+      id = __shfl_sync(0xffffffffu, id, 0);
+      share = (int)(id / (unsigned)p.G);
+      g = (int)(id - (unsigned)share * p.G);
+      if (share >= shares.count()) return false;
+      at = shares.edge(share);
+      end = shares.edge(share + 1);
+      int lo = 0, hi = runs - 1;  // the last run that begins at or before the share
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (front[mid] <= at)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      // its sequences, one per lane
+      const int mine = lo * run + lane;
+      WindowSpan ignored;
+      const long long n = lane < run && mine < p.S ? units_of(mine, &ignored) : 0;
+      long long x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      x += front[lo];  // units up to the lane's sequence's end
+      const uint32_t behind = __ballot_sync(0xffffffffu, x > at);
+      const int k = behind ? __ffs(behind) - 1 : 0;
+      u = (int)(at - __shfl_sync(0xffffffffu, x - n, k));
+      s = lo * run + k;
+      units = units_of(s, &span);
+    }
+    while (u >= units) {
+      if (s + 1 >= p.S) return false;  // (not met: a share ends within the sequences' units)
+      units = units_of(++s, &span);
+      u = 0;
+    }
+    it.s = s;
+    it.g = g;
+    it.part = (s + share) * p.G + g;
+    it.span = span;
+    it.span.first = u;
+    it.span.n = (int)min((long long)(units - u), end - at);
+    if (g == 0 && lane == 0) {
+      if (u == 0) sp.own_parts[s].x = share;
+      if (u + it.span.n == units) sp.own_parts[s].y = share;
+    }
+    at += it.span.n;
+    u += it.span.n;
+    return true;
+  };
+  auto store = [&](const StreamItem& it, const DecodeWarp<D>& state) {
+    const int q4 = lane & 3, rA = lane >> 2, h = 2 * q4;
+    const float l0 = warp_sum_xor(state.l0, 4), l1 = warp_sum_xor(state.l1, 4);
+    const float i0 = 1.f / l0, i1 = 1.f / l1;
+    const size_t row = (size_t)it.part * p.r + h;
+    float* to = sp.own_out + row * D + rA;
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt) {
+      if (h < p.r) {
+        to[mt * 16] = state.o[mt][0] * i0;
+        to[mt * 16 + 8] = state.o[mt][2] * i0;
+      }
+      if (h + 1 < p.r) {
+        to[D + mt * 16] = state.o[mt][1] * i1;
+        to[D + mt * 16 + 8] = state.o[mt][3] * i1;
+      }
+    }
+    if (rA == 0 && h < p.r) sp.own_lse[row] = state.m0 + log2f(l0);
+    if (rA == 0 && h + 1 < p.r) sp.own_lse[row + 1] = state.m1 + log2f(l1);
+  };
+  decode_stream<D>(tmK, tmV, p, smem + warp * STAGES * STAGE_BYTES, bars + warp * STAGES, lane, &g_status_shared, next,
+                   store);
+  pdl_wait();  // this grid completes after the one over the prefixes
+}
+
+// A float4 column per lane (head_dim 64: two query heads at a time): the chunks of the sequence's own tokens,
+// then the parts of its prefix, kBatch of them for kHeads heads in flight.  A row's few parts: a warp per
+// (sequence, KV head), four heads at a time; many (MANY: units with a good share of the SMs each): one.
+constexpr int kJoinWarps = 4;
+template <int D>
+constexpr int join_heads(bool many) {  // query heads of a warp at a time
+  return many ? 128 / D : 4;
+}
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_shared_kernel(const SharedParams sp) {
+  constexpr int LANES = D / 4, ROWS = 32 / LANES, kBatch = MANY ? 8 : 2, kHeads = join_heads<D>(MANY) / ROWS;
+  const DecodeParams& p = sp.d;
+  // What the kernel over the prefixes wrote before it let the one in front of this start, and the call's inputs,
+  // are there (lines left in this SM's L1 are dropped); the rest behind the wait.
+  __threadfence();
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int blocks = (p.r + kHeads * ROWS - 1) / (kHeads * ROWS);  // of a KV head's query heads
+  if (item >= (long long)p.S * p.G * blocks) return;  // (the others' waits hold this grid back)
+  const int sg = (int)(item / blocks), h0 = (int)(item - (long long)sg * blocks) * kHeads * ROWS;
+  const int s = sg / p.G, g = sg - s * p.G, d = (lane % LANES) * 4;
+  const SharedOwn own{__ldcg(&sp.own[s].begin), __ldcg(&sp.own[s].group)};
+  int unit = -1;  // of the prefix
+  size_t at = 0;  // the first head's row in each of its parts
+  if (own.group >= 0) {
+    const int2 v = __ldcg(sp.plan->group + own.group);
+    if (v.y > 0 && __ldcg(&sp.plan->total.x) > 0) {
+      const int member = s - sp.cu_group_seqs[own.group], pair = member / (2 * sp.Tq), in = member - pair * 2 * sp.Tq;
+      unit = v.x + g * v.y + pair;
+      at = (size_t)(in / sp.Tq) * kSharedRows + in % sp.Tq;
+    }
   }
-  if (shared == 0) grp = -1;  // every token is the sequence's own
-  __syncthreads();            // the barriers are initialised
-  decode_joined_item<D, NW, STAGES>(tmK, tmV, p, smem, bars, g, s, part, parts, L > shared,
-                                    window_span(L, L - shared, 0), &g_status_shared, PrefixParts(sp, grp, s, g));
+  const int L = min(max(p.seq_lens[s], 0), p.cap);
+  const int units = L > own.begin ? window_span(L, L - own.begin, 0).n : 0;
+  pdl_wait();  // the kernels over the own tokens and, before it, over the prefixes are complete
+  // parts: first, first + 1, ..., and chunks of the own tokens
+  int first = 0, count = 0, chunks = 0;
+  size_t own_row = 0;
+  // (held to the workspace's, should a wait of the kernels in front have given up)
+  if (units > 0) {
+    const int2 v = __ldcg(sp.own_parts + s);
+    const int x = min(max(v.x, 0), sp.own_slots - 1 - s);
+    chunks = min(max(v.y - x + 1, 0), sp.own_slots - s - x);
+    own_row = ((size_t)(s + x) * p.G + g) * p.r;
+  }
+  if (unit >= 0) {
+    const int2 v = __ldcg(sp.unit_parts + unit);
+    first = min(max(v.x, 0), sp.prefix_slots - 1);
+    count = min(max(v.y - first + 1, 0), sp.prefix_slots - first);
+  }
+  {
+    JoinedRow sum[kHeads];
+    for (int k0 = 0; k0 < chunks + count; k0 += kBatch) {
+      float x[kHeads][kBatch];
+      float4 v[kHeads][kBatch];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int k = k0 + j, h = h0 + i * ROWS + lane / LANES;
+          x[i][j] = -INFINITY;
+          v[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (h >= p.r) continue;
+          if (k < chunks) {
+            const size_t r = own_row + (size_t)k * p.H + h;
+            x[i][j] = __ldcg(sp.own_lse + r);
+            v[i][j] = __ldcg(reinterpret_cast<const float4*>(sp.own_out + r * D + d));
+          } else if (k < chunks + count) {
+            const size_t r = (size_t)(first + k - chunks) * 2 * kSharedRows + at + h * sp.Tq;
+            x[i][j] = __ldcg(sp.prefix_lse + r);
+            v[i][j] = __ldcg(reinterpret_cast<const float4*>(sp.prefix_out + r * D + d));
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) sum[i].add(x[i][j], v[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i * ROWS + lane / LANES;
+      if (h >= p.r) continue;
+      const bool empty = sum[i].W == 0.f;  // no token
+      const float inv = empty ? 0.f : 1.f / sum[i].W;
+      const size_t row = (size_t)s * p.H + g * p.r + h;
+      store4<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + d, sum[i].a0 * inv, sum[i].a1 * inv,
+                            sum[i].a2 * inv, sum[i].a3 * inv);
+      if (d == 0 && p.lse_out) p.lse_out[row] = empty ? -INFINITY : (sum[i].M + log2f(sum[i].W)) * kLn2;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -164,9 +357,28 @@ static long long shared_units(int num_seqs, int num_groups, int r, int G) {
   return ((long long)(num_seqs + members - 1) / members + std::min(num_groups, num_seqs)) * G;
 }
 
-// Workspace: the plan, the parts' lse, their rows
-static size_t shared_plan_bytes(int num_groups) { return align_up(sizeof(SharedPlan) + (size_t)num_groups * sizeof(int4), 256); }
-static size_t shared_lse_bytes(size_t parts) { return parts * 2 * kSharedRows * sizeof(float); }
+// The workspace, in this order
+struct SharedSpace {
+  size_t own, unit_parts, own_parts, prefix_lse, prefix_out, own_lse, own_out, bytes;  // offsets behind the plan
+  int prefix_slots, own_slots;
+};
+static SharedSpace shared_space(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_groups, int sms) {
+  SharedSpace w;
+  const size_t r = num_heads / num_kv_heads, items = (size_t)num_seqs * num_kv_heads;
+  const size_t units = (size_t)shared_units(num_seqs, num_groups, (int)r, num_kv_heads), parts = units + sms;
+  const size_t rows = (items + ((size_t)sms * kStreamWarps + num_kv_heads) * (kLargeShares + kSmallShares)) * r;
+  w.prefix_slots = (int)parts;
+  w.own_slots = (int)(rows / r / num_kv_heads);
+  w.own = align_up(sizeof(SharedPlan) + (size_t)num_groups * sizeof(int2), 256);
+  w.unit_parts = align_up(w.own + (size_t)num_seqs * sizeof(SharedOwn), 256);
+  w.own_parts = align_up(w.unit_parts + units * sizeof(int2), 256);
+  w.prefix_lse = align_up(w.own_parts + (size_t)num_seqs * sizeof(int2), 256);
+  w.prefix_out = align_up(w.prefix_lse + parts * 2 * kSharedRows * sizeof(float), 256);
+  w.own_lse = align_up(w.prefix_out + parts * 2 * kSharedRows * head_dim * sizeof(float), 256);
+  w.own_out = align_up(w.own_lse + rows * sizeof(float), 256);
+  w.bytes = align_up(w.own_out + rows * head_dim * sizeof(float), 256);
+  return w;
+}
 
 static int current_sms(int* sms) {
   int dev = 0;
@@ -180,24 +392,25 @@ static int current_sms(int* sms) {
   return METIS_OK;
 }
 
-static size_t shared_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_groups, int sms) {
-  const size_t parts = (size_t)shared_units(num_seqs, num_groups, num_heads / num_kv_heads, num_kv_heads) + sms;
-  return shared_plan_bytes(num_groups) + shared_lse_bytes(parts) * (1 + (size_t)head_dim);
-}
-
-template <int D, int NW>
-static int launch_shared(const SharedParams& sp, const SharedArgs& a, int parts, cudaStream_t st) {
+template <int D>
+static int launch_own(const SharedParams& sp, const SharedArgs& a, long long units, int sms, cudaStream_t st) {
   CUtensorMap tmK, tmV;
   int rc = encode_kv_maps<D>(sp.d, a.k_cache, a.v_cache, &tmK, &tmV);
   if (rc) return rc;
-  constexpr int smem = bf16_decode_smem_bytes<D, NW, kBf16Stages>();
+  constexpr int smem = stream_smem_bytes<D>();
   static int done = 0;
-  auto kern = decode_shared_kernel<D, NW>;
+  auto kern = decode_own_kernel<D>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
   if (rc) return rc;
-  return launch_dependent_cluster(kern, dim3((unsigned)a.G, (unsigned)parts, (unsigned)a.S),
-                                  dim3(1, (unsigned)parts, 1), dim3(NW * 32), (size_t)smem, st,
-                                  "decode_shared_kernel launch", tmK, tmV, sp);
+  rc = launch_dependent(kern, dim3((unsigned)sms), dim3(kStreamWarps * 32), (size_t)smem, st,
+                        "decode_own_kernel launch", tmK, tmV, sp);
+  if (rc) return rc;
+  const bool many = 4 * units <= sms;  // a unit in four parts and more
+  const int heads = join_heads<D>(many);
+  const long long warps = (long long)a.S * a.G * ((sp.d.r + heads - 1) / heads);
+  const dim3 grid((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);
+  return many ? launch_dependent(join_shared_kernel<D, true>, grid, block, 0, st, "join_shared_kernel launch", sp)
+              : launch_dependent(join_shared_kernel<D, false>, grid, block, 0, st, "join_shared_kernel launch", sp);
 }
 
 }  // namespace metis
@@ -211,7 +424,7 @@ extern "C" size_t metis_shared_workspace_bytes(int num_seqs, int num_heads, int 
     return 0;
   int sms = 0;
   if (current_sms(&sms)) return 0;
-  return shared_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_groups, sms);
+  return shared_space(num_seqs, num_heads, num_kv_heads, head_dim, num_groups, sms).bytes;
 }
 
 extern "C" int metis_paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
@@ -261,14 +474,17 @@ extern "C" int metis_paged_attn_decode_shared(const void* q, const void* k_cache
   int sms = 0;
   rc = current_sms(&sms);
   if (rc) return rc;
-  const size_t need = shared_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_groups, sms);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
-    return fail(METIS_E_WORKSPACE, "workspace must hold %zu bytes (256-byte aligned)", need);
-  SharedPlan* plan = reinterpret_cast<SharedPlan*>(workspace);
-  float* part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + shared_plan_bytes(num_groups));
-  float* part_out = part_lse + (size_t)(units + sms) * 2 * kSharedRows;
+  const SharedSpace w = shared_space(num_seqs, num_heads, num_kv_heads, head_dim, num_groups, sms);
+  if (!workspace || workspace_bytes < w.bytes || !aligned(workspace, 256))
+    return fail(METIS_E_WORKSPACE, "workspace must hold %zu bytes (256-byte aligned)", w.bytes);
+  if ((long long)num_seqs * num_kv_heads > 0x70000000LL) return fail(METIS_E_SHAPE, "too many items");
+  char* base = reinterpret_cast<char*>(workspace);
+  SharedPlan* plan = reinterpret_cast<SharedPlan*>(base);
+  SharedOwn* own = reinterpret_cast<SharedOwn*>(base + w.own);
+  float* prefix_lse = reinterpret_cast<float*>(base + w.prefix_lse);
+  float* prefix_out = reinterpret_cast<float*>(base + w.prefix_out);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = launch_shared_prefix(a, plan, part_lse, part_out, sms, st);
+  rc = launch_shared_prefix(a, plan, own, reinterpret_cast<int2*>(base + w.unit_parts), prefix_lse, prefix_out, sms, st);
   if (rc) return rc;
   SharedParams sp{};
   DecodeParams& p = sp.d;
@@ -289,16 +505,16 @@ extern "C" int metis_paged_attn_decode_shared(const void* q, const void* k_cache
   p.max_parts = 1;
   p.cap = a.cap;
   sp.cu_group_seqs = cu_group_seqs;
-  sp.prefix_lens = prefix_lens;
   sp.plan = plan;
-  sp.part_lse = part_lse;
-  sp.part_out = part_out;
-  sp.num_groups = num_groups;
+  sp.own = own;
+  sp.prefix_lse = prefix_lse;
+  sp.prefix_out = prefix_out;
+  sp.own_lse = reinterpret_cast<float*>(base + w.own_lse);
+  sp.own_out = reinterpret_cast<float*>(base + w.own_out);
+  sp.unit_parts = reinterpret_cast<int2*>(base + w.unit_parts);
+  sp.own_parts = reinterpret_cast<int2*>(base + w.own_parts);
   sp.Tq = kSharedRows / r;
-  const long long items = (long long)num_kv_heads * num_seqs;
-  const int parts = item_parts(items, a.cap, sms);
-  if (one_warp_items(items, sms))
-    return head_dim == 64 ? launch_shared<64, 1>(sp, a, 1, st) : launch_shared<128, 1>(sp, a, 1, st);
-  return head_dim == 64 ? launch_shared<64, kBf16Warps>(sp, a, parts, st)
-                        : launch_shared<128, kBf16Warps>(sp, a, parts, st);
+  sp.prefix_slots = w.prefix_slots;
+  sp.own_slots = w.own_slots;
+  return head_dim == 64 ? launch_own<64>(sp, a, units, sms, st) : launch_own<128>(sp, a, units, sms, st);
 }
