@@ -17,6 +17,7 @@
 
 #include "../../include/metis_attn.h"
 #include "decode_items.cuh"
+#include "decode_stream.cuh"
 
 namespace metis {
 
@@ -73,6 +74,76 @@ __global__ void __launch_bounds__(kBf16Warps * 32) decode_window_bf16_kernel(con
   }
 }
 
+// Many items of few tokens: a warp walks items (decode_stream.cuh), every `warps`-th of the grid's.
+template <int D>
+__global__ void __launch_bounds__(kStreamWarps * 32, 1) decode_window_stream_kernel(
+    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const WindowParams wp) {
+  constexpr int STAGES = stream_stages<D>(), STAGE_BYTES = Bf16DecodeShape<D>::kStageBytes;
+  constexpr int KS = Bf16DecodeShape<D>::kSteps;
+  const DecodeParams& p = wp.d;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // 1024-aligned for the swizzle
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStreamWarps * STAGES * STAGE_BYTES);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int i = 0; i < kStreamWarps * STAGES; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+  }
+  pdl_wait();  // inputs are read after the previous grid in the stream has completed
+  pdl_launch_dependents();
+  __syncthreads();  // the barriers are initialised
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long items = (long long)p.S * p.G, warps = (long long)gridDim.x * kStreamWarps;
+  long long item = (long long)blockIdx.x * kStreamWarps + warp;  // KV heads side by side, as their rows are
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
+  auto next = [&](StreamItem& it) -> bool {
+    for (; item < items; item += warps) {
+      it.s = (int)(item / p.G);
+      it.g = (int)(item - (long long)it.s * p.G);
+      int L = p.seq_lens[it.s];
+      if (L > p.cap) {
+        if (lane == 0) atomicOr(&g_status_window, METIS_STATUS_SEQ_TOO_LONG);
+        L = p.cap;
+      }
+      if (L > 0) {
+        it.span = window_span(L, wp.window, wp.sinks);
+        item += warps;
+        return true;
+      }
+      const size_t row = (size_t)it.s * p.H + it.g * p.r;  // an empty sequence
+      for (int i = lane; i < p.r * D; i += 32) out[row * D + i] = __nv_bfloat16(0.0f);
+      if (p.lse_out && lane < p.r) p.lse_out[row + lane] = -INFINITY;
+    }
+    return false;
+  };
+  auto store = [&](const StreamItem& it, const DecodeWarp<D>& state) {
+    const int q4 = lane & 3, rA = lane >> 2, h = 2 * q4;
+    const float l0 = warp_sum_xor(state.l0, 4), l1 = warp_sum_xor(state.l1, 4);
+    const float i0 = 1.f / l0, i1 = 1.f / l1;
+    const size_t row = (size_t)it.s * p.H + it.g * p.r + h;
+    // lanes rA and rA ^ 1 hold neighbouring dims: the even one writes both for head h, the odd one for h + 1
+    const bool odd = rA & 1;
+    __nv_bfloat16* to = out + (row + odd) * D + (rA & ~1);
+    const bool live = h + odd < p.r;
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float a = state.o[mt][2 * half] * i0, b = state.o[mt][2 * half + 1] * i1;
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);  // (lane ^ 4: rA ^ 1)
+        const uint32_t v = odd ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
+        if (live) *reinterpret_cast<uint32_t*>(to + mt * 16 + half * 8) = v;
+      }
+    if (p.lse_out && rA == 0) {
+      if (h < p.r) p.lse_out[row] = (state.m0 + log2f(l0)) * kLn2;
+      if (h + 1 < p.r) p.lse_out[row + 1] = (state.m1 + log2f(l1)) * kLn2;
+    }
+  };
+  decode_stream<D>(tmK, tmV, p, smem + warp * STAGES * STAGE_BYTES, bars + warp * STAGES, lane, &g_status_window, next,
+                   store);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kF32Warps * 32) decode_window_f32_kernel(const float* k_cache, const float* v_cache,
                                                                            const WindowParams wp) {
@@ -119,6 +190,25 @@ static int launch_window(const WindowParams& wp, const void* k_cache, const void
   return launch_dependent(kern, dim3(G, S), dim3(kBf16Warps * 32), (size_t)smem, st, "decode_window_bf16_kernel launch",
                           tmK, tmV, wp);
 }
+
+template <int D>
+static int launch_window_stream(const WindowParams& wp, const void* k_cache, const void* v_cache, int sms,
+                                cudaStream_t st) {
+  CUtensorMap tmK, tmV;
+  int rc = encode_kv_maps<D>(wp.d, k_cache, v_cache, &tmK, &tmV);
+  if (rc) return rc;
+  constexpr int smem = stream_smem_bytes<D>();
+  static int done = 0;
+  auto kern = decode_window_stream_kernel<D>;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem, &done);
+  if (rc) return rc;
+  return launch_dependent(kern, dim3((unsigned)sms), dim3(kStreamWarps * 32), (size_t)smem, st,
+                          "decode_window_stream_kernel launch", tmK, tmV, wp);
+}
+
+// Items of at most this many tokens, at least kStreamItems for each of the stream's warps, are walked by those
+constexpr int kStreamTokens = 512;
+constexpr int kStreamItems = 2;
 
 }  // namespace metis
 
@@ -177,7 +267,11 @@ extern "C" int metis_paged_attn_decode_window(const void* q, const void* k_cache
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return fail(METIS_E_CUDA, "querying the SM count: %s", cudaGetErrorString(e));
   const int seen = (int)std::min<long long>((long long)window + sinks, p.cap);
-  const int parts = item_parts((long long)num_kv_heads * num_seqs, seen, sms);
+  const long long items = (long long)num_kv_heads * num_seqs;
+  if (seen <= kStreamTokens && items >= (long long)kStreamItems * kStreamWarps * sms)
+    return head_dim == 64 ? launch_window_stream<64>(wp, k_cache, v_cache, sms, st)
+                          : launch_window_stream<128>(wp, k_cache, v_cache, sms, st);
+  const int parts = item_parts(items, seen, sms);
   auto launch = [&](auto dim, auto join) {
     return launch_window<decltype(dim)::value, decltype(join)::value>(wp, k_cache, v_cache, parts, st);
   };

@@ -25,7 +25,8 @@ namespace metis {
 __device__ unsigned int g_status_rope = 0;
 
 constexpr int kRopeWarps = 4;
-constexpr int kRows = 4;  // rows a lane has in flight
+constexpr int kRows = 3;  // rows a lane has in flight
+constexpr int kRopeCtas = 7;   // CTAs of an SM
 constexpr int kRopeFill = 28;  // warps for each SM, below which tokens are shared by several
 
 struct RopeParams {
@@ -227,7 +228,7 @@ __device__ __forceinline__ void turn_rows(const RopeParams& p, const RopeLane& m
 // The rows of a token: 0 .. H - 1 are queries, then G keys, then (v given) G values.  `share` warps take
 // `chunk` of them each.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeParams p, const int interleaved,
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kernel(const RopeParams p, const int interleaved,
                                                                        const int num_tokens, const int share,
                                                                        const int chunk) {
   constexpr int N = RopeVec<T>::kN, LANES = D / N, STEP = 32 / LANES;  // STEP: rows of the warp at a time

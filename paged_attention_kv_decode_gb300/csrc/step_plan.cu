@@ -14,7 +14,7 @@
 // depth may be updated in place).
 //
 // Bound by latency: a step of 64 tokens moves 2 KB, 400,000 rows 5 MB.  Every CTA of a cluster scans all
-// lengths itself (four sequences per thread and round; two scans, tokens and then pages), the cluster's
+// lengths itself (a few sequences per thread and round; two scans, tokens and then pages), the cluster's
 // barrier separates the reads of those lengths from their update, and the CTAs share the pages and rows.  A
 // small step is one CTA of 256 threads: its barriers are the time.  Many rows would keep the cluster's eight
 // SMs busy with finding each row's sequence: a second kernel fills them, on every SM, from the offsets,
@@ -30,12 +30,15 @@ namespace metis {
 
 __device__ unsigned int g_status_plan = 0;
 
-constexpr int kPlanPer = 4;          // sequences per thread and round
 constexpr int kPlanTile = 128;       // rows a warp takes at a time
 constexpr int kMaxCluster = 8;
-constexpr int kPlanSmall = 256;      // threads of a small step's one CTA: up to kPlanSmall * kPlanPer sequences,
-constexpr int kPlanSmallRows = 2048; // and rows
-constexpr int kPlanWide = 1024;
+constexpr int kPlanSmall = 256;      // threads of a small step's one CTA, 4 sequences each in a round: one round,
+constexpr int kPlanSmallRows = 2048; // and up to so many rows
+constexpr int kPlanWide = 1024;      // otherwise: 8 sequences each
+template <int NT>
+constexpr int plan_per() {
+  return NT == kPlanSmall ? 4 : 8;
+}
 constexpr int kPlanOwnRows = 8192;   // more rows are left to the second kernel
 constexpr int kRowWarps = 4;
 
@@ -59,10 +62,11 @@ struct PlanParams {
 // What a CTA keeps of the sequences of the current round
 template <int NT>
 struct PlanSeqs {
-  int cu[NT * kPlanPer + 1];  // first row
-  int before[NT * kPlanPer];  // cached tokens
-  int held[NT * kPlanPer];    // pages in its table row
-  int page[NT * kPlanPer];    // its first new page, in the order of taking
+  static constexpr int N = NT * plan_per<NT>();
+  int cu[N + 1];  // first row
+  int before[N];  // cached tokens
+  int held[N];    // pages in its table row
+  int page[N];    // its first new page, in the order of taking
 };
 
 // Exclusive prefix of one value per thread, sums held at `top` (the sums of a batch may pass it:
@@ -106,7 +110,7 @@ __device__ __forceinline__ int plan_find(const int* v, int lo, int hi, int x) {
 
 template <int NT, bool ROWS>
 __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
-  constexpr int SEQS = NT * kPlanPer;
+  constexpr int PER = plan_per<NT>(), SEQS = NT * PER;
   extern __shared__ uint8_t plan_smem[];
   PlanSeqs<NT>& seqs = *reinterpret_cast<PlanSeqs<NT>*>(plan_smem);
   __shared__ int warp_sums[NT / 32];
@@ -118,12 +122,12 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
   int rows = 0, taken = 0;  // by the rounds before this one
   for (int base = 0; base < p.S; base += SEQS) {
     const int n_seqs = min(p.S - base, SEQS);
-    int n[kPlanPer], before[kPlanPer], held[kPlanPer];
+    int n[PER], before[PER], held[PER];
     int sum = 0;
     unsigned bad = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-      const int s = tid * kPlanPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = tid * PER + i;
       n[i] = before[i] = held[i] = 0;
       if (s < n_seqs) {
         n[i] = p.q_lens[base + s];
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       if (n[i] < 0 || before[i] < 0) bad |= METIS_STATUS_BAD_Q_LEN;
       n[i] = max(n[i], 0);
       before[i] = max(before[i], 0);
@@ -140,10 +144,10 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
     }
     int total;
     const int left = p.T - rows;  // rows that the call still has
-    int at = plan_scan<NT>(min(sum, left), left, warp_sums, &total), pages = 0, take[kPlanPer];
+    int at = plan_scan<NT>(min(sum, left), left, warp_sums, &total), pages = 0, take[PER];
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-      const int s = tid * kPlanPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = tid * PER + i;
       if (n[i] > left - at) {  // rows past the call's: those tokens are not planned
         n[i] = left - at;
         bad |= METIS_STATUS_BAD_OFFSETS;
@@ -165,8 +169,8 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
     int total_pages;
     int first = taken + plan_scan<NT>(pages, 0x7fffffff, warp_sums, &total_pages);
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-      const int s = tid * kPlanPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = tid * PER + i;
       if (s < n_seqs) seqs.page[s] = first;
       first += take[i];
     }
@@ -180,8 +184,8 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
 
     // per sequence
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-      const int s = tid * kPlanPer + i;
+    for (int i = 0; i < PER; ++i) {
+      const int s = tid * PER + i;
       if (s < n_seqs && s % ctas == cta) {
         p.seq_lens[base + s] = (int)min((unsigned)before[i] + (unsigned)n[i], 0x7fffffffu);
         if (p.held_out) p.held_out[base + s] = held[i] + take[i];
@@ -351,7 +355,7 @@ extern "C" int metis_plan_step(const int32_t* q_lens, const int32_t* cached_lens
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (num_seqs <= kPlanSmall * kPlanPer && num_tokens <= kPlanSmallRows)
+  if (num_seqs <= PlanSeqs<kPlanSmall>::N && num_tokens <= kPlanSmallRows)
     return launch_dependent(plan_step_kernel<kPlanSmall, true>, dim3(1), dim3(kPlanSmall), sizeof(PlanSeqs<kPlanSmall>), st,
                             "plan_step_kernel launch", p);
   // (positions within int32: the second kernel counts them back from the lengths)

@@ -112,12 +112,16 @@ def test_decode_parity(window, sinks, H, G, D, bs, dtype):
     (5, 28, 4, 128, 32, 513, 1),
     (40, 16, 8, 64, 16, 90, 33),     # one CTA an item
     (130, 8, 4, 128, 16, 40, 2),     # more than the ranked ones
+    (700, 16, 4, 128, 16, 40, 2),    # a warp walks items: short windows,
+    (700, 4, 4, 64, 32, 70, 20),
+    (2500, 7, 1, 128, 16, 33, 0),
 ])
 def test_decode_batches(S, H, G, D, bs, window, sinks):
     rng = np.random.default_rng(S)
     lens = rng.integers(1, 2000, S)
     lens[0] = 1999
-    Batch(S, [(int(n), 1) for n in lens], H, G, D, bs, window, sinks, decode=True, absent=10 ** 6).check()
+    lens[rng.integers(1, S, S // 50)] = 0
+    Batch(S, [(int(n), min(int(n), 1)) for n in lens], H, G, D, bs, window, sinks, decode=True, absent=10 ** 6).check()
 
 
 def test_decode_of_long_sequences_reads_only_the_window():
