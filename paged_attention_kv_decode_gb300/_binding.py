@@ -931,8 +931,11 @@ def metis_qk_norm_rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     nb, bs = k_cache.shape[:2]
     if q_out is None:
         q_out = _empty((T, H, D), q.dtype, q, stream)
+        o_at = q_out.data_ptr()
+    else:
+        o_at = _on(dev, "q_out", q_out, q.dtype, (T, H, D))
     rc = lib.metis_qk_norm_rope_and_cache(
-        q_at, k_at, v_at, qw, kw, table, pos, _on(dev, "q_out", q_out, q.dtype, (T, H, D)),
+        q_at, k_at, v_at, qw, kw, table, pos, o_at,
         _on(dev, "k_cache", k_cache, q.dtype, (nb, bs, G, D)), _on(dev, "v_cache", v_cache, q.dtype, (nb, bs, G, D)),
         _on(dev, "slot_mapping", slot_mapping, torch.int64, (T,)), T, H, G, D, q_stride, k_stride, v_stride, R, rows,
         int(bool(interleaved)), float(eps), bs, nb, code, _stream_of(dev, stream))

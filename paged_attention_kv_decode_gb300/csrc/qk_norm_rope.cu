@@ -87,6 +87,7 @@ __device__ __forceinline__ float row_sum(float v) {
 struct RopeLane {
   int at, sub, mate;   // sub: the lane's row among the warp's; mate: the lane that holds the partners
   bool turned, inter;  // the lane's elements are rotated; their partners are in the lane itself
+  bool known;          // the position has a row in the table (else: reads as zeros)
 };
 
 // The rows [lo, hi) of one kind (queries or keys) of a token: out = f (x a + x' b), x' the partner of x, with
@@ -116,10 +117,7 @@ __device__ __forceinline__ void turn_rows(const RopeParams& p, const RopeLane& m
       b[i] = 0.f;
     }
     if (me.turned) {
-      if (turn == nullptr) {  // a position outside the table: its row reads as zeros
-#pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = 0.f;
-      } else if (me.inter) {
+      if (me.inter) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           a[i] = turn[(e0 + i) / 2];
@@ -136,6 +134,10 @@ __device__ __forceinline__ void turn_rows(const RopeParams& p, const RopeLane& m
           b[i] = sign * s.x, b[i + 1] = sign * s.y, b[i + 2] = sign * s.z, b[i + 3] = sign * s.w;
         }
       }
+    }
+    if (!me.known && me.turned) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) a[i] = b[i] = 0.f;
     }
     if (weight != nullptr) {
       const uint4* w4 = reinterpret_cast<const uint4*>(weight);
@@ -240,23 +242,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
   const int lane = threadIdx.x & 31;
   const int lo = (int)(item - n * share) * chunk, hi = min(p.H + (p.v ? 2 : 1) * p.G, lo + chunk);
 
+  // (No branch on either before the first rows are on their way.)
   long long slot = n;
-  if (p.slots && hi > p.H) {
-    slot = p.slots[n];
-    if (slot >= p.total_slots) {
-      if (lane == 0) atomicOr(&g_status_rope, METIS_STATUS_BAD_BLOCK_ID);
-      slot = -1;
-    }
-  }
-  const float* turn = nullptr;
-  if (p.R > 0 && lo < p.H + p.G) {
-    const int pos = p.positions[n];
-    if (pos >= 0 && pos < p.max_position)
-      turn = p.cos_sin + (long long)pos * p.R;
-    else if (lane == 0)
-      atomicOr(&g_status_rope, METIS_STATUS_BAD_POSITION);
-  }
+  if (p.slots) slot = p.slots[n];
+  int pos = 0;
+  if (p.R > 0) pos = p.positions[n];
   RopeLane me;
+  me.known = p.R == 0 || (pos >= 0 && pos < p.max_position);
+  const float* turn = p.cos_sin + (long long)(me.known ? pos : 0) * p.R;
   me.at = lane % LANES;
   me.sub = lane / LANES;
   me.turned = me.at * N < p.R;
@@ -271,8 +264,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
                     [&](int row) { return reinterpret_cast<const uint4*>(from + row * D) + me.at; },
                     [&](int row, const uint4& v) { to[row * LANES] = v; });
   }
+  if (!me.known && lane == 0 && lo < p.H + p.G) atomicOr(&g_status_rope, METIS_STATUS_BAD_POSITION);
+  if (hi <= p.H) return;
+  if (p.slots && slot >= p.total_slots) {
+    if (lane == 0) atomicOr(&g_status_rope, METIS_STATUS_BAD_BLOCK_ID);
+    return;
+  }
   if (slot < 0) return;  // a padding row: neither its key nor its value is written
-  if (hi > p.H && lo < p.H + p.G) {
+  if (lo < p.H + p.G) {
     const T* from = reinterpret_cast<const T*>(p.k) + n * p.k_stride;
     uint4* to = reinterpret_cast<uint4*>(p.k_out) + slot * p.G * LANES + me.at;
     turn_rows<T, D>(p, me, turn, p.k_weight, max(lo - p.H, 0), min(hi - p.H, p.G),
