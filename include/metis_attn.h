@@ -238,7 +238,8 @@ size_t metis_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_heads
  * metis_paged_attn_prefill_chunk_window -- metis_paged_attn_prefill_chunk with a window:
  * each query row sees its own window, and single-token sequences are decoded as by the call
  * above.  Pages without a token that a query of the call sees are not read.  A value of a
- * token that a row does not see (NaN and infinities included) does not reach it.  Arguments,
+ * token that a row does not see (NaN and infinities included) does not reach it.  Weights of
+ * up to 2^8 meet V: sums of V values above 2^119 may overflow to infinity.  Arguments,
  * limits and workspace (metis_prefill_workspace_bytes) as there.
  */
 int metis_paged_attn_decode_window(const void* q, const void* k_cache, const void* v_cache,
@@ -260,7 +261,7 @@ int metis_paged_attn_prefill_chunk_window(const void* q, const int32_t* cu_q_len
  * prompt or document the same pages): each group's shared tokens are read and computed
  * once for all of its members, on the tensor cores, and joined with every sequence's
  * attention over its own tokens.  The result is that of metis_paged_attn_decode over all
- * of them.
+ * of them (shared V values above 2^119 may overflow, as in the call above).
  *
  *   cu_group_seqs  int32 [num_groups + 1], non-decreasing, within [0, num_seqs]: group g's
  *                  members are the sequences cu_group_seqs[g] .. cu_group_seqs[g + 1] - 1;
@@ -411,7 +412,8 @@ int metis_mla_reshape_and_cache(const void* kv_c, const void* k_pe, void* kv_cac
  *           call being free_stack[*free_count - 1 - k], as metis_prefix_lookup takes them;
  *           block_table gets the entry, refcount[page] = 1
  *   cu_q_lens[s + 1] = cu_q_lens[s] + n, cu_q_lens[0] = 0
- *   row cu_q_lens[s] + i, i < n:  positions = L0 + i,
+ *   row cu_q_lens[s] + i, i < n:  positions = L0 + i (lengths past 2^31 - 1 are held there,
+ *           the positions of such a sequence are not specified),
  *           slot_mapping = block_table[s][position / block_size] * block_size
  *                          + position % block_size
  *   seq_lens[s] = L0 + n;  held_blocks_out[s] = the pages its row names now

@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
       }
     }
     // per new page
-    for (int k = taken + cta * NT + tid; k < taken + total_pages; k += ctas * NT) {
-      const int s = plan_find(seqs.page, 0, n_seqs - 1, k);
+    for (long long next = (long long)taken + cta * NT + tid; next < (long long)taken + total_pages; next += ctas * NT) {
+      const int k = (int)next, s = plan_find(seqs.page, 0, n_seqs - 1, k);
       int block = -1;
       if (k < depth) block = checked_block(p.free_stack, depth - 1 - k, p.num_blocks, &g_status_plan);
       p.block_table[(size_t)(base + s) * p.max_blocks + seqs.held[s] + (k - seqs.page[s])] = block;
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
     // per row
     const int end = rows + total;
     if constexpr (ROWS) {
-      for (int row = rows + cta * NT + tid; row < end; row += ctas * NT) {
-        const int s = plan_find(seqs.cu, 0, n_seqs - 1, row);
+      for (long long next = (long long)rows + cta * NT + tid; next < end; next += ctas * NT) {
+        const int row = (int)next, s = plan_find(seqs.cu, 0, n_seqs - 1, row);
         const unsigned pos = (unsigned)seqs.before[s] + (unsigned)(row - seqs.cu[s]);
         const unsigned page = pos / (unsigned)p.bs, off = pos - page * (unsigned)p.bs;
         int block = -1;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(NT, 1) plan_step_kernel(const PlanParams p) {
     __syncthreads();  // the next round overwrites the sequences
   }
   if constexpr (ROWS) {  // rows behind the last sequence's: padding
-    for (int row = rows + cta * NT + tid; row < p.T; row += ctas * NT) {
+    for (long long row = (long long)rows + cta * NT + tid; row < p.T; row += ctas * NT) {
       p.slot_mapping[row] = -1;
       p.positions[row] = 0;
     }
