@@ -24,8 +24,8 @@
 //                into 3- and 2-stage rings, each tile's pages
 //                split between two warps (16-token pages make many small boxes,
 //                and one warp alone cannot issue them fast enough)
-//   warp 13      query loader; warp 14 hands out the units; warp 15 idle (the
-//                last warpgroup gives up registers to the softmax groups)
+//   warp 13      query loader; warp 14 hands out the units; warp 15 idle but with
+//                windows (the last warpgroup gives up registers to the softmax groups)
 //   warp 12      allocates TMEM (S0 | S1 | O0 | O1, 512 columns); one lane
 //                issues the UMMAs in the order
 //                  PV0_j, QK0_{j+1}, PV1_j, QK1_{j+1}
@@ -67,6 +67,18 @@
 // converted by three warps 528 us; the issuer's operands uniform over its warp, queries
 // split by the softmax threads and a fourth converter 431 us.  Few chunks: units are split
 // over their keys (SPLIT, at kMaxSplits).
+//
+// Windows (WINDOW).  A unit's keys are a row of whole pages, those of the first tokens and then those
+// from its first query's oldest key on (PfSpan); tiles, positions and masks count along it, so first tokens
+// cost a page and not a tile (16 chunks of 512 and 48 decodes, window of 1,024: 255 us, 224 so).  A hidden key's weight is
+// 0, but 0 times an infinity or NaN is not: warp 15 looks at the V rows that some query of the unit does
+// not see, once they have landed.  Hidden keys are masked in pieces of 32 columns, and only in those that the
+// edges cross; rows are written in 32-byte stores; the issuer is the uniform one of the 8-bit cache.  Measured there:
+// 224 us, uniform issuer 192, masks, V rows in batches and stores 165 (779 TFLOP/s of the visible keys: units of nine
+// tiles, whose queries, first products and epilogue cost as much as three); 2,048 queries, window of 4,096,
+// 175, 126, 120 us (1,162 TFLOP/s: 256 units on 152 SMs); 8,192 queries 556, 412, 383 us (1,436 TFLOP/s).
+//
+// Shared prefixes (SHARED): at PfGroup and pf_shared_ctas.
 #include <math.h>
 
 #include <algorithm>
@@ -891,7 +903,9 @@ __device__ __forceinline__ void pf_own_tokens(const PrefillParams& p, int lane) 
 // Shared prefixes: how many of the grid's CTAs (one per SM) share `total` K/V tiles, so that these and the
 // decodes of the sequences' own tokens, on the other SMs at the same time, end together.  A CTA takes 7 us to
 // start, 5 us for each unit (its queries, its parts) and 2 us a tile; decodes stream 40 GB/s on each of their
-// SMs, 6.1 TB/s together.  shared_tokens: of the caller's groups, over all threads the members' shared tokens.
+// SMs, 6.1 TB/s together.  (64 sequences behind 16,384 tokens: 64 CTAs, 51.7 us; 1,024 behind 16 prompts of about 600:
+// 26, 110 us; the own tokens behind the prefixes, each on all SMs: 58.9 and 129.)  shared_tokens: of the caller's
+// groups, over all threads the members' shared tokens.
 constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
 constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
 

@@ -13,7 +13,11 @@
 // tokens a share of a token's heads: a row of head_dim elements is 8 to 32 lanes with 16 bytes each, so the
 // token's angles and the weights stay in registers over all of the warp's rows, kRows loads of which are in
 // flight per lane.  The partner of a pair is in the same lane (interleaved) or half of rotary_dim away: a
-// shuffle.
+// shuffle.  With a = weight cos and b = +- weight sin formed once for a warp's token, an element costs two packed
+// fp32 operations and its conversions.
+//
+// Measured, 8,240 rows of 32 + 8 + 8 heads x 128 (207 MB): 42.6 us, 4.8 TB/s, 73 % of a copy (a CTA per token
+// with the factors per row took 72); 64 rows 2.8 us.
 #include <algorithm>
 
 #include "../../include/metis_attn.h"
@@ -25,6 +29,7 @@ namespace metis {
 __device__ unsigned int g_status_rope = 0;
 
 constexpr int kRopeWarps = 4;
+// (8,240 rows: 2 to 8 rows in flight on 5 to 16 CTAs are within 5 %; 2 x 8 took 45.1 us)
 constexpr int kRows = 3;  // rows a lane has in flight
 constexpr int kRopeCtas = 7;   // CTAs of an SM
 constexpr int kRopeFill = 28;  // warps for each SM, below which tokens are shared by several

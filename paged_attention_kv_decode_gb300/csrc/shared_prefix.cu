@@ -16,6 +16,10 @@
 // takes as many SMs as make the two end together (pf_shared_ctas: their rates are there), 2 the others.  2 is a
 // programmatic dependent of 1 that does not wait for it but at its very end; what 2 needs of 1 (the number of
 // SMs, where each sequence's own tokens begin) is written before 1 lets it start.
+//
+// Measured (32 / 8 heads x 128): 64 sequences behind a document of 16,384 tokens 51.7 us, of which 1 and 2 run until
+// 44 and 3 ends 5 later (2 behind 1, a CTA per item: 64); 1,024 sequences behind 16 system prompts 110 us, 2 on 126
+// SMs until 95, an SM taking in 40 GB/s, and 3 (50 MB of parts) 14 (2 behind 1: 132).
 #include <math.h>
 
 #include <algorithm>
@@ -31,7 +35,8 @@ __device__ unsigned int g_status_shared = 0;
 constexpr int kSharedRows = 128;  // rows of a query tile
 constexpr int kMinUnits = 4;      // units (16 tokens of a KV head) of a share at least
 constexpr int kLargeShares = 2;   // shares for each warp: large ones of the first three quarters of the units,
-constexpr int kSmallShares = 4;   // small ones of the others, so that the warps end together
+constexpr int kSmallShares = 4;   // small ones of the others, so that the warps end together (shares of one size: the
+                                  // document's 56.7 us for 51.7, the prompts' 112 for 110)
 constexpr int kRuns = 2048;       // (65,535 sequences: runs of 32)
 
 struct SharedParams {
@@ -405,7 +410,9 @@ static int launch_own(const SharedParams& sp, const SharedArgs& a, long long uni
   rc = launch_dependent(kern, dim3((unsigned)sms), dim3(kStreamWarps * 32), (size_t)smem, st,
                         "decode_own_kernel launch", tmK, tmV, sp);
   if (rc) return rc;
-  const bool many = 4 * units <= sms;  // a unit in four parts and more
+  // a unit in four parts and more (document, 8 units: 51.7 us, four heads at a time 59.6; prompts, 256 units: 120.1
+  // and 109.4)
+  const bool many = 4 * units <= sms;
   const int heads = join_heads<D>(many);
   const long long warps = (long long)a.S * a.G * ((sp.d.r + heads - 1) / heads);
   const dim3 grid((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);

@@ -19,6 +19,9 @@
 // small step is one CTA of 256 threads: its barriers are the time.  Many rows would keep the cluster's eight
 // SMs busy with finding each row's sequence: a second kernel fills them, on every SM, from the offsets,
 // lengths and table that the first one wrote.
+//
+// Measured: 64 sequences of one token 3.9 us (as one of the cluster's CTAs of 1,024 threads: 6.2); 4,096 prompts
+// with 393 K rows 16.9 us, 11 of them the first kernel.
 #include <algorithm>
 
 #include "../../include/metis_attn.h"
@@ -39,7 +42,9 @@ template <int NT>
 constexpr int plan_per() {
   return NT == kPlanSmall ? 4 : 8;
 }
-constexpr int kPlanOwnRows = 8192;   // more rows are left to the second kernel
+// More rows are left to the second kernel.  (7.7 K rows 8.5 us in the first, 10.7 in the second, 24 K even at 11.0,
+// 393 K 65.6 and 16.9.)
+constexpr int kPlanOwnRows = 8192;
 constexpr int kRowWarps = 4;
 
 struct PlanParams {
