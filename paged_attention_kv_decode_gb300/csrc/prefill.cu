@@ -1701,6 +1701,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       } else {
         u = -1;
       }
+      // Windows: nothing is noted of the unit yet.  Cleared here, in front of what every reader of the slot waits for:
+      // a unit without a partial tile, or a query tile whose own tiles have none, waits for nothing of warp 15.  Every
+      // softmax group has written out the unit before the last one, the slot's, as it has taken the last one.
+      if constexpr (WINDOW) {
+        if (lane < kOddWords) xw.odd[slot][lane] = 0u;
+        if (lane == 0) xw.any_odd[slot] = 0;
+        __syncwarp();
+      }
       if (lane == 0) {
         if (u >= 0) unit_info[slot] = it;
         unit_slot[slot] = u;
@@ -1721,10 +1729,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
     Unit it;
     if constexpr (WINDOW) {
       while (ok && next_unit(k, it) > 0) {
-        const int slot = (k - 1) & 1;  // every softmax group has written out the unit before the last one
-        if (lane < kOddWords) xw.odd[slot][lane] = 0u;
-        if (lane == 0) xw.any_odd[slot] = 0;
-        __syncwarp();
+        const int slot = (k - 1) & 1;  // (the fetcher has cleared its bits)
         const int p_first = pf_first_query(p, it), p_last = pf_last_query(p, it);
         for (int j = 0; j < it.n_kv; ++j, ++t) {
           const int tok0 = pf_tile(it, j) * kKvTile, st = t % kVStages;

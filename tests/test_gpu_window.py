@@ -182,6 +182,18 @@ def test_keys_of_unseen_tokens_do_not_reach_a_row():
     assert np.array_equal(got, ~sees) and np.array_equal(torch.isfinite(lse).all(1).cpu().numpy(), ~sees)
 
 
+def test_units_whose_queries_all_see_every_key():
+    """The last query of 65 that end at a tile's last key: a unit without a tile to look at, behind units
+    of the same SM in which infinities and NaN were noted."""
+    b = Batch(21, [(128, 65)] * 160 + [(256, 65)] * 8, 8, 2, 128, 16, 10 ** 6, 0)
+    rng = np.random.default_rng(4)
+    for s, (n, q) in enumerate(b.seqs):
+        if s % 4:
+            page, off = b.slot(s, int(rng.integers(n - q + 1, n)))
+            b.v[page, off, rng.integers(2), rng.integers(128)] = (float("nan"), float("inf"))[s % 2]
+    b.check()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-20, 4.0])
 def test_scales(scale):
     for decode in (True, False):

@@ -32,3 +32,16 @@ def test_the_guard_of_windows_waits_for_every_tile():
     assert loop.index("wait_all(&v_full[st]") < loop.index("if (!pf_partial(it, j))")
     skipped = loop[loop.index("if (!pf_partial(it, j))"):loop.index("continue;")]
     assert "mbar_arrive(&v_empty[st])" in skipped
+
+
+def test_the_notes_of_a_windows_unit_are_cleared_before_it_is_published():
+    """A unit without a partial tile waits for nothing that the warp which notes V rows does: bits that its
+    slot still held, or memory that nothing had written, would add tokens to its rows."""
+    text = source("prefill.cu")
+    fetcher = text[text.index("warp == kMmaWarp + 2"):text.index("WINDOW && warp > kMmaWarp")]
+    publish = fetcher.index("unit_info[slot] = it")
+    assert fetcher.index("wait_all(&unit_empty") < fetcher.index("xw.odd[slot][lane] = 0u") < publish
+    assert fetcher.index("xw.any_odd[slot] = 0") < publish
+    guard = text[text.index("WINDOW && warp > kMmaWarp"):]
+    guard = guard[:guard.index("softmax groups") if "softmax groups" in guard else guard.index("regs_inc")]
+    assert "any_odd[slot] = 0" not in guard and "odd[slot][lane]" not in guard
