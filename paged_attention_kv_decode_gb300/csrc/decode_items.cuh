@@ -296,6 +296,10 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
 
   const int q4 = lane & 3, rA = lane >> 2;
   const float l0 = warp_sum_xor(state.l0, 4), l1 = warp_sum_xor(state.l1, 4);
+  // scores of NaN have left the sum NaN, but not the maximum (no comparison with them holds):
+  // any finite one makes the state count
+  if (l0 != l0) state.m0 = 0.f;
+  if (l1 != l1) state.m1 = 0.f;
   sync();  // every warp is done with its ring
 
   float* cm = reinterpret_cast<float*>(smem);
@@ -494,7 +498,7 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
   if (lane == 0) {
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      cm[warp * 8 + h] = m[h];
+      cm[warp * 8 + h] = l[h] == l[h] ? m[h] : 0.f;  // (NaN: as in decode_bf16_item)
       cl[warp * 8 + h] = l[h];
     }
   }
