@@ -123,7 +123,9 @@ int metis_paged_attn_decode(const void* q, const void* k_cache, const void* v_ca
  *                                                       [num_seqs, num_heads, max_parts]
  *
  * with max_parts = ceil(max_seq_len / partition_size).  Partitions past a
- * sequence's end are not written (the merge does not read them).
+ * sequence's end are not written (the merge does not read them).  A partition
+ * with a score of NaN has an lse of +infinity, which the merge makes NaN (it
+ * passes a NaN over).
  */
 int metis_paged_attn_decode_partials(const void* q, const void* k_cache, const void* v_cache,
                                      const int32_t* block_table, const int32_t* seq_lens,

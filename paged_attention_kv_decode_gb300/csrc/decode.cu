@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(NW * 32) decode_bf16_kernel(const __grid_const
   decode_bf16_item<D, NW, STAGES>(tmK, tmV, p, smem, bars, g, s, orow, RangeSpan{t0, t1}, warp, lane, kb,
                                   &g_status_decode, [] { __syncthreads(); },
                                   [&](const float* cm, const float* cl, const float* co) {
-                                    combine_and_store<__nv_bfloat16, NW>(p, cm, cl, co, part, g, s, orow, threadIdx.x);
+                                    combine_and_store<__nv_bfloat16, NW, true>(p, cm, cl, co, part, g, s, orow,
+                                                                               threadIdx.x);
                                   });
 }
 

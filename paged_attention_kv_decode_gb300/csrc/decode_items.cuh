@@ -507,7 +507,7 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 #pragma unroll
     for (int i = 0; i < DPL; ++i) co[((size_t)warp * D + lane * DPL + i) * 8 + h] = o[h][i];
   __syncthreads();
-  combine_and_store<float, kF32Warps>(p, cm, cl, co, part, g, s, s, threadIdx.x);
+  combine_and_store<float, kF32Warps, true>(p, cm, cl, co, part, g, s, s, threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------

@@ -70,7 +70,7 @@ def test_windowed_decode(S, H, G, D, bs, window, sinks, dtype):
         same_nan(*b.run(), b.want())
 
 
-@pytest.mark.parametrize("partition", [0])
+@pytest.mark.parametrize("partition", [0, 64, 512])
 @pytest.mark.parametrize("H,G,D,dtype", [(8, 2, 128, BF16), (4, 1, 64, BF16), (7, 1, 64, F32)])
 def test_decode_of_all_tokens(partition, H, G, D, dtype):
     seqs = [(n, 1) for n in (900, 30, 5, 1300, 64, 129, 700)]
