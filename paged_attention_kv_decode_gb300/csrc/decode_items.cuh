@@ -161,9 +161,11 @@ struct DecodeWarp {
     }
     const float mn0 = fmaxf(m0, warp_max_xor(fmaxf(s0, s2), 4));
     const float mn1 = fmaxf(m1, warp_max_xor(fmaxf(s1, s3), 4));
-    const float al0 = exp2_approx(m0 - mn0), al1 = exp2_approx(m1 - mn1);
-    const float p0 = exp2_approx(s0 - mn0), p1 = exp2_approx(s1 - mn1);
-    const float p2 = exp2_approx(s2 - mn0), p3 = exp2_approx(s3 - mn1);
+    // (every score so far below fp32's range, -infinity: they weigh 0 and not NaN)
+    const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
+    const float al0 = exp2_approx(m0 - ref0), al1 = exp2_approx(m1 - ref1);
+    const float p0 = exp2_approx(s0 - ref0), p1 = exp2_approx(s1 - ref1);
+    const float p2 = exp2_approx(s2 - ref0), p3 = exp2_approx(s3 - ref1);
     l0 = l0 * al0 + (p0 + p2);
     l1 = l1 * al1 + (p1 + p3);
     m0 = mn0;
@@ -369,7 +371,7 @@ __device__ __forceinline__ void join_parts_of_item(const DecodeParams& p, const 
     }
 #pragma unroll
     for (int i = 0; i < kMaxParts; ++i) row.add(x[i], v[i]);
-    const bool empty = row.W == 0.f;  // no part, or none with a token
+    const bool empty = n == 0;  // no part with a token
     const float inv = empty ? 0.f : 1.f / row.W;
     const size_t at = (size_t)orow * p.H + g * p.r + h;
     store4<OutT>(reinterpret_cast<OutT*>(p.out) + at * D + d, row.a0 * inv, row.a1 * inv, row.a2 * inv, row.a3 * inv);
@@ -484,9 +486,9 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 #pragma unroll
           for (int i = 0; i < DPL; ++i) dot = fmaf(qv[h][i], kv[u][i], dot);
           dot = warp_sum_xor(dot, 1);
-          const float mn = fmaxf(m[h], dot);
-          const float al = exp2_approx(m[h] - mn);
-          const float pr = exp2_approx(dot - mn);
+          const float mn = fmaxf(m[h], dot), ref = mn == -INFINITY ? 0.f : mn;  // (as in DecodeWarp)
+          const float al = exp2_approx(m[h] - ref);
+          const float pr = exp2_approx(dot - ref);
           l[h] = l[h] * al + pr;
 #pragma unroll
           for (int i = 0; i < DPL; ++i) o[h][i] = fmaf(pr, vv[u][i], o[h][i] * al);

@@ -1942,7 +1942,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         l_run *= alpha;
         // P = exp2(s * |sl2| - m) as bf16 pairs (even token in the low half), packed in
         // place into sv[0, 64) and stored over the first 64 columns of S_w
-        const float neg_m = WINDOW && m_run == -INFINITY ? 0.f : -m_run;  // (windows: no key seen yet)
+        // (windows: no key seen yet; a part of a shared prefix: or none above fp32's range)
+        const float neg_m = (WINDOW || SHARED) && m_run == -INFINITY ? 0.f : -m_run;
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};   // row sums, as packed pairs
         const uint64_t asl2_2 = f2_pack(asl2, asl2), neg_m2 = f2_pack(neg_m, neg_m);
         // per pair: one packed FMA, two exponentials, one packed add, one bf16x2 convert
