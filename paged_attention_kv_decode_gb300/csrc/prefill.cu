@@ -1743,7 +1743,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
             continue;
           }
           uint8_t* tile = sV + st * Sh::kKvBytes;
-          auto in_tile = [&](int t) { return min(max(t - tok0, 0), kKvTile); };
+          auto in_tile = [&](int t) { return min(max(max(t, 0) - tok0, 0), kKvTile); };  // (t: to -2^31, of the largest windows)
           // rows that none sees: between the first tokens and the first query's oldest key, and behind the last query
           const int low = in_tile(it.w.sinks), old = max(in_tile(p_first - p.window + 1), low);
           const int leave = max(in_tile(p_last - p.window + 1), old), end = in_tile(p_last + 1);
@@ -1851,7 +1851,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         [[maybe_unused]] int hole = 0, hole_len = 0;
         if constexpr (WINDOW) {
           hole = min(max(it.w.sinks - tok0, 0), kKvTile);
-          hole_len = max(min(p_row - p.window + 1 - tok0, kKvTile) - hole, 0);
+          hole_len = max(min(max(p_row - p.window + 1, 0) - tok0, kKvTile) - hole, 0);
         }
         const bool lean = vis == kKvTile && sgn > 0.f && hole_len == 0;   // the common case: no mask, positive scale
         // the row's 128 scores, read once
