@@ -685,6 +685,12 @@ def _paged_cache(dev: int, q: torch.Tensor, k_cache, v_cache):
     return tuple(shape), (_on(dev, "k_cache", k_cache, q.dtype, shape), _on(dev, "v_cache", v_cache, q.dtype, shape))
 
 
+def _reach(tokens) -> int:
+    """A number of tokens that may exceed every length, held to what the library's int can say of it (ctypes
+    would drop the bits above); a negative one stays negative."""
+    return max(-1, min(int(tokens), 2 ** 31 - 1))
+
+
 def metis_paged_attn_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                    block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float, window: int,
                                    sinks: int = 0, *, out: Optional[torch.Tensor] = None,
@@ -704,7 +710,7 @@ def metis_paged_attn_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     if max_seq_len is None:
         max_seq_len = max(1, int(seq_lens.max().item())) if S else 1
     rc = lib.metis_paged_attn_decode_window(q_at, *cache, table, lens, o_at, l_at, S, H, G, D, bs, width, nb, code,
-                                            float(scale), int(window), int(sinks), int(max_seq_len),
+                                            float(scale), _reach(window), _reach(sinks), int(max_seq_len),
                                             _stream_of(dev, stream))
     if rc:
         _check(rc)
@@ -736,8 +742,8 @@ def metis_paged_attn_prefill_chunk_window(q: torch.Tensor, cu_q_lens: torch.Tens
     need = metis_prefill_workspace_bytes(S, T, H, G) if workspace is None else 0
     workspace, w_at, w_bytes = _workspace(dev, q, workspace, max(need, 256), stream)
     rc = lib.metis_paged_attn_prefill_chunk_window(q_at, cu, *cache, table, lens, o_at, l_at, S, T, H, G, D, bs, width,
-                                                   nb, code, float(scale), int(window), int(sinks), int(max_seq_len),
-                                                   w_at, w_bytes, _stream_of(dev, stream))
+                                                   nb, code, float(scale), _reach(window), _reach(sinks),
+                                                   int(max_seq_len), w_at, w_bytes, _stream_of(dev, stream))
     if rc:
         _check(rc)
     return out, lse_out

@@ -27,3 +27,18 @@ def test_chunks(window, sinks, H, G, D, bs, which):
     b.window, b.sinks = window, sinks
     out, lse = b.run(max_seq_len=1000)
     assert torch.equal(out, want) and torch.equal(lse, wl) and pa.metis_read_status() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 32 + 5, 0), (2 ** 40, 4), (5, 2 ** 32 + 3), (2 ** 31, 2 ** 63)])
+@pytest.mark.parametrize("decode", [False, True])
+def test_numbers_past_int32_are_beyond_every_length(window, sinks, decode):
+    seqs = [(n, min(n, 1 if decode else q)) for n, q in CHUNKS[0]]
+    b = Batch(3, seqs, 8, 2, 128, 16, 10 ** 6, 0, decode=decode)
+    want, wl = b.run()
+    b.window, b.sinks = window, sinks
+    out, lse = b.run()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    for window, sinks in ((-2 ** 32 + 5, 0), (5, -2 ** 32 + 3)):  # (their low 32 bits are positive)
+        b.window, b.sinks = window, sinks
+        with pytest.raises(pa.MetisError):
+            b.run()
