@@ -436,7 +436,8 @@ int metis_mla_reshape_and_cache(const void* kv_c, const void* k_pe, void* kv_cac
  * (METIS_STATUS_BAD_OFFSETS); tokens past the table row get slot -1
  * (METIS_STATUS_SEQ_TOO_LONG); with the stack empty a new page's entry and its slots are -1
  * (METIS_STATUS_OUT_OF_PAGES); so are those of an entry, held or from the stack, outside
- * [0, num_blocks) (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 is a successful no-op.
+ * [0, num_blocks) (METIS_STATUS_BAD_BLOCK_ID).  num_seqs == 0 is a successful no-op:
+ * no output is written, padding and *free_count_out neither.
  */
 int metis_plan_step(const int32_t* q_lens, const int32_t* cached_lens, const int32_t* held_blocks,
                     int32_t* block_table, const int32_t* free_stack, int free_capacity,

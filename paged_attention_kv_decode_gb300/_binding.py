@@ -447,14 +447,19 @@ def _stream_of(device: int, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(device: int, stream) -> Optional[torch.cuda.Stream]:
+    """The call's stream as torch's own (None: the current one)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream_of(device, stream))
+
+
 def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """Memory of a call on `stream`: torch's allocator reuses freed memory in the order of one stream,
     so the outputs and workspace of a call on another stream come from that one's pool."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_of(like.get_device(), stream))
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(like.get_device(), stream)):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -814,7 +819,8 @@ def metis_plan_step(q_lens: torch.Tensor, cached_lens: torch.Tensor, block_table
     ``block_table`` (int32 ``[S, max_blocks]``, in place) and ``refcount`` (int32 ``[num_blocks]``).
     ``num_tokens`` is the number of rows of the step's tensors: rows behind the new tokens' are padding.
     Outputs may be passed in; ``seq_lens``, ``held_blocks_out`` and ``free_count_out`` may be the inputs
-    they follow, which a captured step then advances.  Asynchronous."""
+    they follow, which a captured step then advances.  A step without sequences is ``num_tokens`` rows of
+    padding.  Asynchronous."""
     lib = _lib or load_library()
     dev = _device_of("q_lens", q_lens, 1)
     S = q_lens.shape[0]
@@ -849,6 +855,12 @@ def metis_plan_step(q_lens: torch.Tensor, cached_lens: torch.Tensor, block_table
         cu_at, slot_at, pos_at, S, T, int(block_size), width, int(num_blocks), _stream_of(dev, stream))
     if rc:
         _check(rc)
+    if S == 0:  # (the library writes nothing then)
+        with torch.cuda.stream(_torch_stream(dev, stream)):
+            slot_mapping.fill_(-1)
+            positions.zero_()
+            cu_q_lens.zero_()
+            torch.clamp(free_count, 0, capacity, out=free_count_out)
     return StepPlan(seq_lens, cu_q_lens, positions, slot_mapping, held_blocks_out, free_count_out)
 
 
