@@ -909,21 +909,22 @@ __device__ __forceinline__ void pf_own_tokens(const PrefillParams& p, int lane) 
 constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
 constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
 
-__device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total, int units, float shared_tokens) {
-  __shared__ float tokens;
+__device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total, int units, long long shared_tokens) {
+  __shared__ long long warp_tokens[kPfThreads / 32];
   __shared__ unsigned best;
   const int tid = threadIdx.x, sms = gridDim.x;
-  if (tid == 0) {
-    tokens = 0.f;
-    best = 0xffffffffu;
-  }
-  float mine = -shared_tokens;
-  for (int s = tid; s < p.S; s += kPfThreads) mine += (float)min(max(p.seq_lens[s], 0), p.cap);
-  mine = warp_sum_xor(mine, 1);
+  if (tid == 0) best = 0xffffffffu;
+  // Whole numbers: every CTA has to come to the same count, in whichever order its threads add up.
+  long long tokens = -shared_tokens;
+  for (int s = tid; s < p.S; s += kPfThreads) tokens += min(max(p.seq_lens[s], 0), p.cap);
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, m);
+  if ((tid & 31) == 0) warp_tokens[tid >> 5] = tokens;
   __syncthreads();
-  if ((tid & 31) == 0) atomicAdd(&tokens, mine);
-  __syncthreads();
-  const float bytes = fmaxf(tokens, 0.f) * p.kv_token_bytes;
+  tokens = 0;
+#pragma unroll
+  for (int w = 0; w < kPfThreads / 32; ++w) tokens += warp_tokens[w];
+  const float bytes = (float)max(tokens, 0ll) * p.kv_token_bytes;
   if (total == 0) return 0;
   for (int n = tid + 1; n <= (bytes > 0.f && sms > 1 ? sms - 1 : sms); n += kPfThreads) {
     const float prefix = kShareStartUs + kShareTileUs * (((unsigned)total + n - 1) / n) +
@@ -945,7 +946,7 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
   int x = 0, unit = 0;  // of the groups before this round's
   PfGroup v{};
   int my_x = 0, my_unit = 0;
-  float shared_tokens = 0.f;  // of this thread's groups' members
+  long long shared_tokens = 0;  // of this thread's groups' members
   bool disorder = false;
   if (tid >= kPfThreads - 32) pf_own_tokens(p, tid & 31);
   auto round = [&](int g0, bool first) {
@@ -960,7 +961,7 @@ __device__ __forceinline__ PfShare pf_share(const PrefillParams& p) {
     my_x = x + block_exclusive_scan<kPfThreads>(v.units * v.tiles, warp_sums, &sum);
     x += sum;
     __syncthreads();
-    if (first && v.units) shared_tokens += (float)v.n * v.tokens;
+    if (first && v.units) shared_tokens += (long long)v.n * v.tokens;
     if (first && blockIdx.x == 0 && g0 + tid < p.num_groups) {
       p.plan->group[g0 + tid] = make_int2(my_unit, v.units / p.G);
       if (bad) atomicOr(&g_status_prefill, bad);

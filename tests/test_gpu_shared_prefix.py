@@ -12,6 +12,7 @@ import torch
 
 import oracle
 import paged_attention_kv_decode_gb300 as pa
+from helpers import BF16_LSE_ATOL
 from test_gpu_window import compare, i32
 
 pytestmark = pytest.mark.gpu
@@ -136,6 +137,36 @@ def test_few_sequences_behind_a_long_prefix():
 
 def test_long_own_tokens():
     Batch(5, [(128, [5000, 130, 4000])], 8, 2, 128, 16).check()
+
+
+@pytest.mark.parametrize("shared,S", [(39000, 512), (17000, 1100)])
+def test_lengths_that_add_up_past_fp32s_whole_numbers(shared, S):
+    """More than 2^24 tokens over a few pages that every table row names again and again: the CTAs have to agree on
+    their shares whatever the lengths.  Against the decode that shares nothing: a tile left out or taken twice moves
+    lse by 0.003 and more."""
+    rng = np.random.default_rng(S)
+    H, G, D, bs, pages, hi = 4, 1, 64, 16, 64, shared + 3000
+    k, v = (torch.from_numpy(rng.standard_normal((pages, bs, G, D))).to(BF16).to(DEV) for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((S, H, D))).to(BF16).to(DEV)
+    table = i32(np.broadcast_to(np.arange(-(-hi // bs)) % pages, (S, -(-hi // bs))).copy())
+    ws = torch.empty(pa.metis_shared_workspace_bytes(S, H, G, D, 1), dtype=torch.uint8, device=DEV)
+    for _ in range(20):
+        p = int(rng.integers(shared, shared + 999))
+        lens = rng.integers(p, hi, S)
+        assert lens.sum() > 2 ** 24
+        kw = dict(max_seq_len=hi, want_lse=True)
+        call = lambda: pa.metis_paged_attn_decode_shared(q, k, v, table, i32(lens), i32([0, S]), i32([p]), 0.125, workspace=ws,
+                                                         **kw)
+        out, lse = call()
+        want, wl = pa.metis_paged_attn_decode(q, k, v, table, i32(lens), 0.125, **kw)
+        size, _ = pa.metis_paged_attn_decode(q, k, v.abs(), table, i32(lens), 0.125, **kw)
+        assert (lse - wl).abs().max() <= 2 * BF16_LSE_ATOL
+        # both are within the tolerance above of the exact values
+        tol = 2 * ((2.0 ** -8 + 2.0 ** -14) * size.double() * (1 + 2.0 ** -6) + 2.0 ** -8 * want.double().abs() * (1 + 2.0 ** -6))
+        assert ((out.double() - want.double()).abs() <= tol).all()
+        again = call()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    assert pa.metis_read_status() == 0
 
 
 def test_no_groups():

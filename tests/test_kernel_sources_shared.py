@@ -45,3 +45,12 @@ def test_the_notes_of_a_windows_unit_are_cleared_before_it_is_published():
     guard = text[text.index("WINDOW && warp > kMmaWarp"):]
     guard = guard[:guard.index("softmax groups") if "softmax groups" in guard else guard.index("regs_inc")]
     assert "any_odd[slot] = 0" not in guard and "odd[slot][lane]" not in guard
+
+
+def test_every_cta_counts_the_tokens_in_whole_numbers():
+    """Each CTA of the kernel over the prefixes works out for itself how many share them: a sum of fp32 that
+    threads add up in any order rounds differently from CTA to CTA beyond 2^24 tokens."""
+    text = source("prefill.cu")
+    body = text[text.index("int pf_shared_ctas("):text.index("PfShare pf_share(")]
+    assert "atomicAdd" not in body and "long long tokens = -shared_tokens" in body
+    assert not re.search(r"float\s+(shared_)?tokens", text[text.index("int pf_shared_ctas("):text.index("prefill_bf16_kernel(const")])
