@@ -89,6 +89,7 @@
 #include "decode.cuh"
 #include "fp8.cuh"
 #include "host.h"
+#include "shared_split.cuh"
 #include "tcgen05.cuh"
 
 namespace metis {
@@ -900,20 +901,12 @@ __device__ __forceinline__ void pf_own_tokens(const PrefillParams& p, int lane) 
   }
 }
 
-// Shared prefixes: how many of the grid's CTAs (one per SM) share `total` K/V tiles, so that these and the
-// decodes of the sequences' own tokens, on the other SMs at the same time, end together.  A CTA takes 7 us to
-// start, 5 us for each unit (its queries, its parts) and 2 us a tile; decodes stream 40 GB/s on each of their
-// SMs, 6.1 TB/s together.  (64 sequences behind 16,384 tokens: 64 CTAs, 51.7 us; 1,024 behind 16 prompts of about 600:
-// 26, 110 us; the own tokens behind the prefixes, each on all SMs: 58.9 and 129.)  shared_tokens: of the caller's
-// groups, over all threads the members' shared tokens.
-constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
-constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
-
+// Shared prefixes: how many of the grid's CTAs share the `total` K/V tiles of `units` units (shared_split.cuh).
+// shared_tokens: of the caller's groups, over all threads the members' shared tokens.
 __device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total, int units, long long shared_tokens) {
   __shared__ long long warp_tokens[kPfThreads / 32];
-  __shared__ unsigned best;
+  __shared__ unsigned long long warp_best[kPfThreads / 32];
   const int tid = threadIdx.x, sms = gridDim.x;
-  if (tid == 0) best = 0xffffffffu;
   // Whole numbers: every CTA has to come to the same count, in whichever order its threads add up.
   long long tokens = -shared_tokens;
   for (int s = tid; s < p.S; s += kPfThreads) tokens += min(max(p.seq_lens[s], 0), p.cap);
@@ -921,20 +914,21 @@ __device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total,
   for (int m = 1; m < 32; m <<= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, m);
   if ((tid & 31) == 0) warp_tokens[tid >> 5] = tokens;
   __syncthreads();
+  if (total == 0) return 0;
   tokens = 0;
 #pragma unroll
   for (int w = 0; w < kPfThreads / 32; ++w) tokens += warp_tokens[w];
   const float bytes = (float)max(tokens, 0ll) * p.kv_token_bytes;
-  if (total == 0) return 0;
-  for (int n = tid + 1; n <= (bytes > 0.f && sms > 1 ? sms - 1 : sms); n += kPfThreads) {
-    const float prefix = kShareStartUs + kShareTileUs * (((unsigned)total + n - 1) / n) +
-                         kShareUnitUs * (((unsigned)units + n - 1) / n);
-    const float own = n < sms ? kShareStartUs + bytes / fminf(kOwnBytesPerUs * (sms - n), kOwnBytesPerUsAll) : 0.f;
-    const float t = fmaxf(prefix, own);
-    atomicMin(&best, (unsigned)fminf(t * 16.f, 4e6f) << 10 | (unsigned)n);  // (n: up to 1,023 SMs)
-  }
+  unsigned long long best = ~0ull;
+  for (int n = tid + 1; n <= shared_split_most(bytes, sms); n += kPfThreads)
+    best = min(best, shared_split_key(total, units, bytes, n, sms));
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, m));
+  if ((tid & 31) == 0) warp_best[tid >> 5] = best;
   __syncthreads();
-  return min((int)(best & 1023u), total);
+#pragma unroll
+  for (int w = 0; w < kPfThreads / 32; ++w) best = min(best, warp_best[w]);
+  return min((int)(best & ((1u << kShareCountBits) - 1u)), total);
 }
 
 // Shared prefixes: this CTA's share.  Called by the whole block.  On the way the grid leaves the plan for the
