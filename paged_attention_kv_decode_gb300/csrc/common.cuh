@@ -19,6 +19,10 @@ namespace metis {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Where a running maximum of scores begins, if not at -infinity: finite, so that a state whose scores are all
+// -infinity (hidden keys; sums below fp32's range) has weights of 0 and not NaN, and one whose scores are all NaN,
+// which no comparison brings into its maximum, is told from no state (-infinity) when states are joined.
+constexpr float kNoScore = -3.402823466e38f;
 
 // ---------------------------------------------------------------------------
 // addresses, fences, timers

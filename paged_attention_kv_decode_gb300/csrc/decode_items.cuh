@@ -119,7 +119,7 @@ struct DecodeWarp {
     }
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    m0 = m1 = -INFINITY;
+    m0 = m1 = kNoScore;
     l0 = l1 = 0.f;
   }
 
@@ -161,11 +161,9 @@ struct DecodeWarp {
     }
     const float mn0 = fmaxf(m0, warp_max_xor(fmaxf(s0, s2), 4));
     const float mn1 = fmaxf(m1, warp_max_xor(fmaxf(s1, s3), 4));
-    // (every score so far below fp32's range, -infinity: they weigh 0 and not NaN)
-    const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
-    const float al0 = exp2_approx(m0 - ref0), al1 = exp2_approx(m1 - ref1);
-    const float p0 = exp2_approx(s0 - ref0), p1 = exp2_approx(s1 - ref1);
-    const float p2 = exp2_approx(s2 - ref0), p3 = exp2_approx(s3 - ref1);
+    const float al0 = exp2_approx(m0 - mn0), al1 = exp2_approx(m1 - mn1);
+    const float p0 = exp2_approx(s0 - mn0), p1 = exp2_approx(s1 - mn1);
+    const float p2 = exp2_approx(s2 - mn0), p3 = exp2_approx(s3 - mn1);
     l0 = l0 * al0 + (p0 + p2);
     l1 = l1 * al1 + (p1 + p3);
     m0 = mn0;
@@ -298,10 +296,6 @@ __device__ __forceinline__ bool decode_bf16_item(const CUtensorMap& tmK, const C
 
   const int q4 = lane & 3, rA = lane >> 2;
   const float l0 = warp_sum_xor(state.l0, 4), l1 = warp_sum_xor(state.l1, 4);
-  // scores of NaN have left the sum NaN, but not the maximum (no comparison with them holds):
-  // any finite one makes the state count
-  if (l0 != l0) state.m0 = 0.f;
-  if (l1 != l1) state.m1 = 0.f;
   sync();  // every warp is done with its ring
 
   float* cm = reinterpret_cast<float*>(smem);
@@ -441,7 +435,7 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
   float m[8], l[8], o[8][DPL];
 #pragma unroll
   for (int h = 0; h < 8; ++h) {
-    m[h] = -INFINITY;
+    m[h] = kNoScore;
     l[h] = 0.f;
 #pragma unroll
     for (int i = 0; i < DPL; ++i) o[h][i] = 0.f;
@@ -486,9 +480,9 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
 #pragma unroll
           for (int i = 0; i < DPL; ++i) dot = fmaf(qv[h][i], kv[u][i], dot);
           dot = warp_sum_xor(dot, 1);
-          const float mn = fmaxf(m[h], dot), ref = mn == -INFINITY ? 0.f : mn;  // (as in DecodeWarp)
-          const float al = exp2_approx(m[h] - ref);
-          const float pr = exp2_approx(dot - ref);
+          const float mn = fmaxf(m[h], dot);
+          const float al = exp2_approx(m[h] - mn);
+          const float pr = exp2_approx(dot - mn);
           l[h] = l[h] * al + pr;
 #pragma unroll
           for (int i = 0; i < DPL; ++i) o[h][i] = fmaf(pr, vv[u][i], o[h][i] * al);
@@ -500,7 +494,7 @@ __device__ __forceinline__ void decode_f32_item(const float* k_cache, const floa
   if (lane == 0) {
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      cm[warp * 8 + h] = l[h] == l[h] ? m[h] : 0.f;  // (NaN: as in decode_bf16_item)
+      cm[warp * 8 + h] = m[h];
       cl[warp * 8 + h] = l[h];
     }
   }

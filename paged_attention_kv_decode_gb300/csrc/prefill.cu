@@ -1831,7 +1831,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
       const int p_min = SHARED ? L - 1 : L - q_len + qi0;
       const int p_max = SHARED ? L - 1 : L - q_len + min(q_len - 1, qi0 + p.Tq - 1);
       const int p_row = row_valid && !SHARED ? (L - q_len + qi) : p_max;
-      float m_run = -INFINITY, l_run = 0.f;
+      // (windows: a row may see no key of its first tiles; a part of a shared prefix may hold none
+      // with a score within fp32's range)
+      float m_run = WINDOW || SHARED ? kNoScore : -INFINITY, l_run = 0.f;
       for (int j = 0; j < nkv; ++j) {
         if (!wait_all(&s_full[w], ns & 1)) {
           ok = false;
@@ -1937,8 +1939,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
         l_run *= alpha;
         // P = exp2(s * |sl2| - m) as bf16 pairs (even token in the low half), packed in
         // place into sv[0, 64) and stored over the first 64 columns of S_w
-        // (windows: no key seen yet; a part of a shared prefix: or none above fp32's range)
-        const float neg_m = (WINDOW || SHARED) && m_run == -INFINITY ? 0.f : -m_run;
+        const float neg_m = -m_run;
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};   // row sums, as packed pairs
         const uint64_t asl2_2 = f2_pack(asl2, asl2), neg_m2 = f2_pack(neg_m, neg_m);
         // per pair: one packed FMA, two exponentials, one packed add, one bf16x2 convert

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_shared_kernel(const Shar
     for (int i = 0; i < kHeads; ++i) {
       const int h = h0 + i * ROWS + lane / LANES;
       if (h >= p.r) continue;
-      const bool empty = chunks + count == 0;  // no token
+      const bool empty = sum[i].W == 0.f;  // no token
       const float inv = empty ? 0.f : 1.f / sum[i].W;
       const size_t row = (size_t)s * p.H + g * p.r + h;
       store4<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + d, sum[i].a0 * inv, sum[i].a1 * inv,
