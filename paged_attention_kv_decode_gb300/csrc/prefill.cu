@@ -910,9 +910,10 @@ __device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total,
   // Whole numbers: every CTA has to come to the same count, in whichever order its threads add up.
   long long tokens = -shared_tokens;
   for (int s = tid; s < p.S; s += kPfThreads) tokens += min(max(p.seq_lens[s], 0), p.cap);
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, m);
-  if ((tid & 31) == 0) warp_tokens[tid >> 5] = tokens;
+  // (a batch has at most 2^47 of either kind: in two parts that 32 bits hold)
+  const unsigned low = __reduce_add_sync(0xffffffffu, (unsigned)tokens & 0x3ffffffu);
+  const int high = __reduce_add_sync(0xffffffffu, (int)(tokens >> 26));
+  if ((tid & 31) == 0) warp_tokens[tid >> 5] = ((long long)high << 26) + low;
   __syncthreads();
   if (total == 0) return 0;
   tokens = 0;
@@ -922,13 +923,13 @@ __device__ __forceinline__ int pf_shared_ctas(const PrefillParams& p, int total,
   unsigned long long best = ~0ull;
   for (int n = tid + 1; n <= shared_split_most(bytes, sms); n += kPfThreads)
     best = min(best, shared_split_key(total, units, bytes, n, sms));
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, m));
-  if ((tid & 31) == 0) warp_best[tid >> 5] = best;
+  const unsigned time = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32));
+  const unsigned count = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32) == time ? (unsigned)best : 0xffffffffu);
+  if ((tid & 31) == 0) warp_best[tid >> 5] = (unsigned long long)time << 32 | count;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kPfThreads / 32; ++w) best = min(best, warp_best[w]);
-  return min((int)(best & ((1u << kShareCountBits) - 1u)), total);
+  return min((int)(unsigned)best, total);
 }
 
 // Shared prefixes: this CTA's share.  Called by the whole block.  On the way the grid leaves the plan for the

@@ -2,6 +2,9 @@
 // tokens beside it (prefill.cu, shared_prefix.cu).
 #pragma once
 
+#include <math.h>
+#include <string.h>
+
 namespace metis {
 
 // How many of the grid's CTAs (one per SM) share the prefixes' K/V tiles, so that these and the decodes of the
@@ -12,18 +15,18 @@ namespace metis {
 constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
 constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
 
-constexpr int kShareCountBits = 16;
-
-// What n of `sms` CTAs would take, in sixteenths of a microsecond, above n itself: the smallest key's n is the one to
-// take.  (2^31 tiles and units on one CTA come to 2.4e11 sixteenths, so that only decodes of a week are held there.)
+// What n of `sms` CTAs would take, in whole sixteenths of a microsecond (the bits of that fp32, which order as its
+// values do and do not saturate), above n itself: the smallest key's n is the one to take.
 __host__ __device__ __forceinline__ unsigned long long shared_split_key(int tiles, int units, float own_bytes, int n,
                                                                         int sms) {
   const float prefix = kShareStartUs + kShareTileUs * (((unsigned)tiles + n - 1) / n) +
                        kShareUnitUs * (((unsigned)units + n - 1) / n);
   const float rate = kOwnBytesPerUs * (sms - n) < kOwnBytesPerUsAll ? kOwnBytesPerUs * (sms - n) : kOwnBytesPerUsAll;
   const float own = n < sms ? kShareStartUs + own_bytes / rate : 0.f;
-  const float sixteenths = 16.f * (prefix > own ? prefix : own);
-  return (unsigned long long)(sixteenths < 1e13f ? sixteenths : 1e13f) << kShareCountBits | (unsigned)n;
+  const float sixteenths = floorf(16.f * (prefix > own ? prefix : own));
+  unsigned bits;
+  memcpy(&bits, &sixteenths, 4);
+  return (unsigned long long)bits << 32 | (unsigned)n;
 }
 
 // The counts to choose from: 1 .. this (an SM at least for own tokens)
