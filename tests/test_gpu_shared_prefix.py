@@ -124,6 +124,48 @@ def test_groups_of_all_kinds():
         Batch(seed, groups, H, G, D, bs, after=[50, 0, 7]).check()
 
 
+@pytest.mark.parametrize("H,G,D", [(8, 2, 128), (4, 1, 64)])
+def test_many_short_members_in_front(H, G, D):
+    """The first member with the whole prefix stands behind up to a few hundred padded or shorter ones, or there is none."""
+    groups = [(48, [3] * n + [50, 48]) for n in (7, 8, 9, 39, 40, 41, 135, 136, 137, 300)]
+    groups += [(130, [0] * n + [131]) for n in (8, 136, 264)] + [(16, [15] * 200), (16, []), (33, [0] * 9), (20, [21])]
+    Batch(15, groups, H, G, D, 16, after=[5]).check()
+    Batch(16, [(40, [0] * 30 + [60, 41])] * 520, 2, 1, 64, 16).check()  # more groups than threads
+
+
+def test_short_members_in_front_cost_no_load_each():
+    """20,000 padded rows in front of a group's members or behind them: the same work."""
+    S, live, p, bs = 20000, 64, 512, 16
+    b = Batch(17, [(p, [p + 20] * live)], 4, 1, 64, bs)
+    q = torch.randn(S, 4, 64, device=DEV).to(BF16)
+    ws = torch.empty(pa.metis_shared_workspace_bytes(S, 4, 1, 64, 1), dtype=torch.uint8, device=DEV)
+    times, outs = [], []
+    for at in (0, S - live):
+        lens, table = np.zeros(S, dtype=np.int64), np.full((S, b.table.shape[1]), -1)
+        lens[at:at + live], table[at:at + live] = b.lens, b.table
+        qa = q.clone()
+        qa[at:at + live] = b.q.to(DEV)
+        args = [qa, b.k.to(DEV), b.v.to(DEV), i32(table), i32(lens), i32([0, S]), i32([p]), b.scale]
+        call = lambda: pa.metis_paged_attn_decode_shared(*args, max_seq_len=600, workspace=ws)[0]
+        outs.append(call()[at:at + live].clone())
+        call()
+        took = []
+        for _ in range(9):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            call()
+            end.record()
+            end.synchronize()
+            took.append(start.elapsed_time(end))
+        times.append(sorted(took)[4])
+    assert pa.metis_read_status() == 0
+    o, _, size = b.want()
+    for out in outs:
+        d = np.abs(out.double().cpu().numpy() - o)
+        assert (d <= (2.0 ** -8 + 2.0 ** -14) * size + 2.0 ** -8 * np.abs(o)).all()
+    assert times[1] < 4 * times[0], times  # (16 times with a load in series for each, 2.5 by warps)
+
+
 def test_more_groups_than_threads():
     rng = np.random.default_rng(2)
     groups = [(int(p), members(rng, int(p), int(n), 20)) for p, n in zip(rng.integers(0, 200, 1100), rng.integers(0, 3, 1100))]
