@@ -1,7 +1,9 @@
 // Decode items one after another on a warp of its own, its loads running on across them: for many items of
 // few tokens each, where a CTA per item would spend its time on starting (lengths, block ids, the first
 // loads) and joining its warps.  512 windows of 128 tokens on 8 KV heads (268 MB): 54 us, 5.0 TB/s, where a
-// CTA per item takes 81.  A box of 16 rows costs an SM's TMA unit about 0.1 us, which holds an SM to some 40 GB/s.
+// CTA per item takes 81.  What is lost to the copy rate goes with the number of items, at equal boxes per byte (windows
+// of 64 tokens 4.5 TB/s, 128 5.0, 500 6.3): an item's length, table entries and query are loads in series, of which
+// only the first two run ahead of the item in hand.
 #pragma once
 
 #include "decode_items.cuh"

@@ -76,9 +76,9 @@
 // edges cross; rows are written in 32-byte stores; the issuer is the uniform one of the 8-bit cache.  Measured there:
 // 224 us, uniform issuer 192, masks, V rows in batches and stores 165 (779 TFLOP/s of the visible keys: units of nine
 // tiles, whose queries, first products and epilogue cost as much as three); 2,048 queries, window of 4,096,
-// 175, 126, 120 us (1,162 TFLOP/s: 256 units on 152 SMs); 8,192 queries 556, 412, 383 us (1,436 TFLOP/s).
+// 175, 126, 120 us (1,162 TFLOP/s: 256 units on 152 SMs); 8,192 queries 556, 412, 380 us (1,450 TFLOP/s).
 //
-// Shared prefixes (SHARED): at PfGroup and pf_shared_ctas.
+// Shared prefixes (SHARED): at PfGroup and in shared_split.cuh.
 #include <math.h>
 
 #include <algorithm>
@@ -1979,13 +1979,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_bf16_kernel(const __gri
           }
         }
         l_run *= alpha;
-        // P = exp2(s * |sl2| - m) as bf16 pairs (even token in the low half), packed in
+        // P = exp2(s * |sl2| - m) as bf16 pairs (2^-8 of each weight: V is bf16, and the two have one type in the
+        // instruction; the row sum is of the fp32 weights; even token in the low half), packed in
         // place into sv[0, 64) and stored over the first 64 columns of S_w
         const float neg_m = -m_run;
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};   // row sums, as packed pairs
         const uint64_t asl2_2 = f2_pack(asl2, asl2), neg_m2 = f2_pack(neg_m, neg_m);
         // per pair: one packed FMA, two exponentials, one packed add, one bf16x2 convert
-        // (a hidden key is -inf here and m_run is finite after tile 0, where every row sees
+        // (a hidden key is -inf here and m_run is finite: without windows after tile 0, where every row sees
         // key 0: its exponential is exactly 0)
 #pragma unroll
         for (int c = 0; c < kKvTile; c += 2) {

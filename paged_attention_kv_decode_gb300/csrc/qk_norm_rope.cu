@@ -9,7 +9,7 @@
 // kernels fed by the scheduler's block table", vllm-metal article, sections 3 and 4; the write is
 // the one of cache_write.cu).  Everything between load and store is fp32: one rounding.
 //
-// Bound by HBM: each row is read once and written once.  A warp takes a token, or where there are few
+// Each row is read once and written once.  A warp takes a token, or where there are few
 // tokens a share of a token's heads: a row of head_dim elements is 8 to 32 lanes with 16 bytes each, so the
 // token's angles and the weights stay in registers over all of the warp's rows, kRows loads of which are in
 // flight per lane.  The partner of a pair is in the same lane (interleaved) or half of rotary_dim away: a
@@ -17,7 +17,9 @@
 // fp32 operations and its conversions.
 //
 // Measured, 8,240 rows of 32 + 8 + 8 heads x 128 (207 MB): 42.6 us, 4.8 TB/s, 73 % of a copy (a CTA per token
-// with the factors per row took 72); 64 rows 2.8 us.
+// with the factors per row took 72); without the pages 37.5 (169 MB), fp32 60.2; 64 rows 2.8 us.  Neither HBM (47 % of
+// its nominal rate) nor the SMs (48 %) are busy then: it is the latency of a warp's start, its token's position and slot,
+// then angles and rows, one token and exit, with 28 warps an SM to cover it.  (The write alone: 81 % of a copy.)
 #include <algorithm>
 
 #include "../../include/metis_attn.h"

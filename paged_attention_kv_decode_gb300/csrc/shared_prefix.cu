@@ -13,11 +13,11 @@
 //   3 a kernel over the rows joins their parts.
 //
 // 1 is bound by the tensor cores and the start and end of its units, 2 by HBM: they run side by side.  1
-// takes as many SMs as make the two end together (pf_shared_ctas: their rates are there), 2 the others.  2 is a
+// takes as many SMs as make the two end together (shared_split.cuh), 2 the others.  2 is a
 // programmatic dependent of 1 that does not wait for it but at its very end; what 2 needs of 1 (the number of
 // SMs, where each sequence's own tokens begin) is written before 1 lets it start.
 //
-// Measured (32 / 8 heads x 128): 64 sequences behind a document of 16,384 tokens 51.7 us, of which 1 and 2 run until
+// Measured (32 / 8 heads x 128): 64 sequences behind a document of 16,384 tokens 52.3 us, of which 1 and 2 run until
 // 44 and 3 ends 5 later (2 behind 1, a CTA per item: 64); 1,024 sequences behind 16 system prompts 110 us, 2 on 126
 // SMs until 95, an SM taking in 40 GB/s, and 3 (50 MB of parts) 14 (2 behind 1: 132).
 #include <math.h>

@@ -9,9 +9,10 @@ namespace metis {
 
 // How many of the grid's CTAs (one per SM) share the prefixes' K/V tiles, so that these and the decodes of the
 // sequences' own tokens, on the other SMs at the same time, end together.  A CTA takes 7 us to
-// start, 5 us for each unit (its queries, its parts) and 2 us a tile; decodes stream 40 GB/s on each of their
-// SMs, 6.1 TB/s together.  (64 sequences behind 16,384 tokens: 64 CTAs, 51.7 us; 1,024 behind 16 prompts of about 600:
-// 26, 110 us; the own tokens behind the prefixes, each on all SMs: 58.9 and 129.)
+// start, 5 us for each unit (its queries, its parts) and 2 us a tile; decodes of own tokens stream 40 GB/s on each of
+// their SMs, 6.1 TB/s together.  These figures were fitted at two batches: 64 sequences behind 16,384 tokens (8 units)
+// take 64 CTAs, 52.3 us; 1,024 behind 16 prompts of about 600 (256 units) 26, 110 us (the own tokens behind the
+// prefixes, each on all SMs: 58.9 and 129).  Between them, 8 groups of 32 behind 2,048 tokens (64 units): 82.7 us.
 constexpr float kShareStartUs = 7.f, kShareUnitUs = 5.f, kShareTileUs = 2.f;
 constexpr float kOwnBytesPerUs = 40e3f, kOwnBytesPerUsAll = 6.1e6f;
 

@@ -20,8 +20,9 @@
 // SMs busy with finding each row's sequence: a second kernel fills them, on every SM, from the offsets,
 // lengths and table that the first one wrote.
 //
-// Measured: 64 sequences of one token 3.9 us (as one of the cluster's CTAs of 1,024 threads: 6.2); 4,096 prompts
-// with 393 K rows 16.9 us, 11 of them the first kernel.
+// Measured: 64 sequences of one token 3.9 us, 1,024 of them 7.3 (by the cluster 7.0 and 8.4; around 2,048 rows, of 256
+// sequences 8.8 and 8.9, of 1,024 sequences 11.6 and 9.6); 4,096 prompts with 393 K rows 16.9 us, 11 of them the first
+// kernel.
 #include <algorithm>
 
 #include "../../include/metis_attn.h"
